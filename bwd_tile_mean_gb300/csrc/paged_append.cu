@@ -1,0 +1,321 @@
+// paged_append.cu -- new tokens' keys and values into the paged cache, keys
+// and queries rotated by their positions on the way, and the mean key of
+// every page that fills up (vsa_paged_append).
+//
+// Work: a unit is one page of one sequence that receives tokens; a warp has
+// one 16-slot group of a unit and a chunk of HC key/value heads with their
+// query heads. Half a warp holds one token row (16 bytes = 8 dims per lane),
+// the two halves the even and the odd slots. The rotation's angles are
+// loaded once per token and chunk. Every key that a lane stores is also
+// added, as stored, to the lane's running sums; in a page that fills up the
+// slots written by earlier calls are read back from the cache in the same
+// order, and the groups' sums are joined through shared memory.
+//
+// Units are found without a scan of the lengths: sequence b with tokens
+// [cu[b], cu[b+1]) touches at most (cu[b+1] - cu[b]) / page + 2 pages, so
+// numbering its units from cu[b] / page + 2 b leaves room for them, and a
+// warp finds its b with a 32-way search of that ascending sequence.
+#include "paged.cuh"
+
+namespace vsa {
+namespace {
+
+struct AppendArgs {
+    Paged p;
+    int T;
+    const void *k, *v, *q;
+    long long ks, vs, qs;       // elements between tokens
+    void *q_out;
+    const int *cu, *pos;
+    const float *cos, *sin;
+    int rows, rot, inter;       // table rows, rotated dims, interleaved pairs
+    void *kc, *vc;
+    float *mean;
+    long long units;
+};
+
+constexpr int kGroup = 16;  // slots per warp
+
+// First token of sequence b, clamped into [0, T].
+__device__ __forceinline__ int cu_at(const AppendArgs &a, int b) { return clampi(__ldg(a.cu + b), 0, a.T); }
+
+// The sequence whose units hold unit u: the largest b with cu[b] / page +
+// 2 b <= u. Whole warp, same u.
+__device__ __forceinline__ int find_seq(const AppendArgs &a, long long u, int lane) {
+    int lo = 0, n = a.p.B;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) >> 5;
+        const int b = lo + lane * step;
+        const bool le = lane * step < n && (cu_at(a, b) >> a.p.page_log2) + 2LL * b <= u;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int last = m ? 31 - __clz(m) : 0;
+        const int end = lo + n;
+        lo += last * step;
+        n = min(step, end - lo);
+    }
+    return lo;
+}
+
+// cos / sin of the lane's 8 dims [8 i, 8 i + 8), by pair.
+struct Angles {
+    float c[8], s[8];  // half style: one per dim; interleaved: the first 4, one per pair
+};
+__device__ __forceinline__ void load4(float *dst, const float *src) {
+    const float4 x = __ldg(reinterpret_cast<const float4 *>(src));
+    dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
+}
+__device__ __forceinline__ void load_angles(const AppendArgs &a, int row, int i, Angles &w) {
+    const int half = a.rot >> 1;
+    const long long at = (long long)row * half;
+    if (a.inter) {
+        load4(w.c, a.cos + at + 4 * i);
+        load4(w.s, a.sin + at + 4 * i);
+    } else {
+        const int d = 8 * i < half ? 8 * i : 8 * i - half;
+        load4(w.c, a.cos + at + d);
+        load4(w.c + 4, a.cos + at + d + 4);
+        load4(w.s, a.sin + at + d);
+        load4(w.s + 4, a.sin + at + d + 4);
+    }
+}
+
+// Rotates the lane's 8 dims of a row held by 16 lanes. Each product and sum
+// is rounded to fp32 by itself (no contraction), so the stored bits follow
+// from the definition. All lanes of the warp take part.
+template <typename T>
+__device__ __forceinline__ uint4 rotate(const AppendArgs &a, uint4 x, const Angles &w, int i) {
+    uint32_t r[4] = {x.x, x.y, x.z, x.w};
+    if (a.inter) {
+        if (8 * i < a.rot) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 e = unpack2<T>(r[j]);
+                r[j] = pack2<T>(__fsub_rn(__fmul_rn(e.x, w.c[j]), __fmul_rn(e.y, w.s[j])),
+                                __fadd_rn(__fmul_rn(e.y, w.c[j]), __fmul_rn(e.x, w.s[j])));
+            }
+        }
+        return make_uint4(r[0], r[1], r[2], r[3]);
+    }
+    // the other element of each pair sits rot / 16 lanes away
+    const int hop = a.rot >> 4;
+    const bool on = 8 * i < a.rot, lower = i < hop;
+    const int peer = (threadIdx.x & 16) | (on ? (lower ? i + hop : i - hop) : i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t o = __shfl_sync(0xffffffffu, r[j], peer);
+        const float2 e = unpack2<T>(r[j]), f = unpack2<T>(o);
+        const float sx = lower ? -w.s[2 * j] : w.s[2 * j], sy = lower ? -w.s[2 * j + 1] : w.s[2 * j + 1];
+        // lower: x1 c - x2 s = x1 c + x2 (-s), the same bits; upper: x2 c + x1 s
+        const uint32_t y = pack2<T>(__fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx)),
+                                    __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy)));
+        r[j] = on ? y : r[j];
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+template <typename T> __device__ __forceinline__ void add8(float (&acc)[8], uint4 x) {
+    const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 e = unpack2<T>(r[j]);
+        acc[2 * j] = __fadd_rn(acc[2 * j], e.x);
+        acc[2 * j + 1] = __fadd_rn(acc[2 * j + 1], e.y);
+    }
+}
+
+template <typename T, int HC>
+__global__ void k_paged_append(AppendArgs a) {
+    extern __shared__ __align__(16) float ssum[];  // [warps][HC][128] group sums
+    const Paged &p = a.p;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
+    const int groups = p.page / kGroup;                     // warps per unit
+    const int per_cta = (int)(blockDim.x >> 5) / groups;    // units per CTA
+    const long long u = (long long)blockIdx.x * per_cta + wid / groups;
+    const int grp = wid % groups;
+    const int h0 = blockIdx.y * HC, hn = min(HC, p.Hkv - h0);
+    const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v), *q = static_cast<const T *>(a.q);
+    T *kc = static_cast<T *>(a.kc), *vc = static_cast<T *>(a.vc), *qo = static_cast<T *>(a.q_out);
+
+    // the unit: page `pg` of sequence b takes new tokens at slots [s0, s1)
+    int b = 0, t_of = 0, s0 = 0, s1 = 0, pg = 0;  // slot s holds token t_of + s
+    if (u < a.units) {
+        int t0, n;
+        if (a.cu) {
+            b = find_seq(a, u, lane);
+            t0 = cu_at(a, b);
+            n = max(cu_at(a, b + 1) - t0, 0);
+        } else {
+            b = (int)u;
+            t0 = b;
+            n = 1;
+        }
+        const long long len = __ldg(p.lens + b), first = len - n;  // unclamped: positions outside are dropped
+        const long long lo = max(first, 0LL), hi = min(len, (long long)p.max_len);
+        const long long base = a.cu ? (t0 >> p.page_log2) + 2LL * b : u;
+        const long long pl = (lo >> p.page_log2) + (u - base);
+        const long long at = pl << p.page_log2;
+        if (n > 0 && lo < hi && at < hi) {
+            pg = (int)pl;
+            s0 = (int)max(lo - at, 0LL);
+            s1 = (int)min(hi - at, (long long)p.page);
+            t_of = (int)(t0 + (at - first));
+        }
+    }
+    const bool work = s1 > s0;
+    const int id = work ? paged_id(p, b, pg) : -1;
+    const bool mean = a.mean && work && s1 == p.page && id >= 0;  // the page fills up in this call
+    const long long page_at = (long long)max(id, 0) * p.page_stride;
+    float acc[HC][8];
+#pragma unroll
+    for (int h = 0; h < HC; ++h)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
+
+    const int g0 = grp * kGroup;
+    if (work && (mean || (g0 < s1 && g0 + kGroup > s0))) {
+        for (int st = 0; st < kGroup; st += 2) {
+            const int s = g0 + st + half;
+            const bool fresh = s >= s0 && s < s1;
+            const bool old = mean && s < s0;
+            if (!__any_sync(0xffffffffu, fresh || old)) continue;
+            const long long tok = fresh ? t_of + s : 0;
+            Angles w;
+            if (a.rot && fresh && 8 * i < a.rot) {
+                const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                load_angles(a, clampi(row, 0, a.rows - 1), i, w);
+            }
+            const long long slot_at = page_at + s * p.tok_stride + 8 * i;
+            uint4 xk[HC], xv[HC];
+#pragma unroll
+            for (int h = 0; h < HC; ++h) {
+                xk[h] = xv[h] = make_uint4(0, 0, 0, 0);
+                if (h >= hn) continue;
+                if (fresh) {
+                    xk[h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
+                    xv[h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
+                } else if (old) {
+                    xk[h] = *reinterpret_cast<const uint4 *>(kc + slot_at + (h0 + h) * p.head_stride);
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < HC; ++h) {
+                if (h >= hn) continue;
+                if (a.rot) {
+                    const uint4 y = rotate<T>(a, xk[h], w, i);
+                    if (fresh) xk[h] = y;
+                }
+                if (fresh && id >= 0) {
+                    const long long at = slot_at + (h0 + h) * p.head_stride;
+                    *reinterpret_cast<uint4 *>(kc + at) = xk[h];
+                    *reinterpret_cast<uint4 *>(vc + at) = xv[h];
+                }
+                if (mean) add8<T>(acc[h], xk[h]);  // neither fresh nor old: cannot be, s1 == page
+            }
+            if (q) {
+                const int qn = hn * p.G, q0 = h0 * p.G;
+                for (int c = 0; c < qn; c += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = fresh && c + e < qn
+                                   ? __ldg(reinterpret_cast<const uint4 *>(q + tok * a.qs + (q0 + c + e) * kD + 8 * i))
+                                   : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (a.rot) x[e] = rotate<T>(a, x[e], w, i);
+                        if (fresh && c + e < qn)
+                            *reinterpret_cast<uint4 *>(qo + (tok * p.Hq + q0 + c + e) * kD + 8 * i) = x[e];
+                    }
+                }
+            }
+        }
+    }
+    if (!a.mean) return;
+    // even + odd slots of the group, then the unit's groups in order
+    if (mean) {
+#pragma unroll
+        for (int h = 0; h < HC; ++h)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float odd = __shfl_down_sync(0xffffffffu, acc[h][e], 16);
+                if (half == 0) ssum[(wid * HC + h) * kD + 8 * i + e] = __fadd_rn(acc[h][e], odd);
+            }
+    }
+    __syncthreads();
+    if (mean && grp == 0) {
+        const float inv = 1.f / (float)p.page;  // a power of two: exact
+        for (int h = 0; h < hn; ++h) {
+            float4 t = *reinterpret_cast<const float4 *>(&ssum[(wid * HC + h) * kD + 4 * lane]);
+            for (int g = 1; g < groups; ++g) {
+                const float4 x = *reinterpret_cast<const float4 *>(&ssum[((wid + g) * HC + h) * kD + 4 * lane]);
+                t.x = __fadd_rn(t.x, x.x);
+                t.y = __fadd_rn(t.y, x.y);
+                t.z = __fadd_rn(t.z, x.z);
+                t.w = __fadd_rn(t.w, x.w);
+            }
+            t.x *= inv, t.y *= inv, t.z *= inv, t.w *= inv;
+            *reinterpret_cast<float4 *>(a.mean + ((long long)id * p.Hkv + h0 + h) * kD + 4 * lane) = t;
+        }
+    }
+}
+
+template <typename T, int HC> cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
+    const int groups = a.p.page / kGroup;
+    const int warps = groups > 4 ? groups : 4, per_cta = warps / groups;
+    const dim3 grid((unsigned)((a.units + per_cta - 1) / per_cta), (unsigned)((a.p.Hkv + HC - 1) / HC));
+    const size_t smem = a.mean ? sizeof(float) * warps * HC * kD : 0;
+    k_paged_append<T, HC><<<grid, 32 * warps, smem, s>>>(a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+}  // namespace vsa
+
+extern "C" vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, int64_t k_stride,
+                                       const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                       const int32_t *cu_seqlens, const int32_t *positions, const float *cos,
+                                       const float *sin, int table_rows, int rot_dim, int interleaved, void *k_cache,
+                                       void *v_cache, float *k_mean, vsa_stream_t stream) {
+    using namespace vsa;
+    AppendArgs a{};
+    const vsa_status st = to_paged(desc, &a.p, true);
+    if (st != VSA_OK) return st;
+    if (T < 0 || (!cu_seqlens && T != a.p.B)) return VSA_ERR_SHAPE;
+    if (!token_stride(k_stride, a.p.Hkv, &a.ks) || !token_stride(v_stride, a.p.Hkv, &a.vs) ||
+        !token_stride(q_stride, a.p.Hq, &a.qs))
+        return VSA_ERR_SHAPE;
+    if (rot_dim < 0 || rot_dim > kD || rot_dim % 16 != 0) return VSA_ERR_UNSUPPORTED;
+    if (rot_dim > 0 && (!cos || !sin)) return VSA_ERR_NULL;
+    if (rot_dim > 0 && table_rows < 1) return VSA_ERR_SHAPE;
+    if (!q != !q_out || !k_cache || !v_cache) return VSA_ERR_NULL;
+    if (T == 0) return VSA_OK;
+    if (!k || !v) return VSA_ERR_NULL;
+    if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(k_cache) ||
+        !aligned16(v_cache) || !aligned16(k_mean))
+        return VSA_ERR_LAYOUT;
+    if (rot_dim > 0 && (!aligned16(cos) || !aligned16(sin))) return VSA_ERR_LAYOUT;
+    if ((uintptr_t)cu_seqlens & 3u || (uintptr_t)positions & 3u) return VSA_ERR_LAYOUT;
+    a.T = T;
+    a.k = k;
+    a.v = v;
+    a.q = q;
+    a.q_out = q_out;
+    a.cu = cu_seqlens;
+    a.pos = positions;
+    a.cos = cos;
+    a.sin = sin;
+    a.rows = table_rows;
+    a.rot = rot_dim;
+    a.inter = interleaved != 0;
+    a.kc = k_cache;
+    a.vc = v_cache;
+    a.mean = k_mean;
+    a.units = cu_seqlens ? (long long)T / a.p.page + 2LL * a.p.B : a.p.B;
+    if (a.p.Hkv > 65535 || a.units > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    prof_begin("paged_append", s);
+    const bool bf = a.p.dtype == T_BF16;
+    const cudaError_t e = bf ? launch_append<__nv_bfloat16, 1>(a, s) : launch_append<__half, 1>(a, s);
+    prof_end(s);
+    return status_from_cuda(e);
+}

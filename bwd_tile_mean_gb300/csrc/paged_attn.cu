@@ -1,0 +1,557 @@
+// paged_attn.cu -- attention of one token per sequence over a paged
+// key/value cache (vsa_paged_attn), all pages or the listed ones.
+//
+//   O = sum_u P_u v_u / sum_u P_u,  P_u = exp(scale q.k_u - max)
+//
+// A segment is one (sequence, key/value head, chunk of up to 16 MT query
+// heads of its group); its keys, in the order of the pages attended, are
+// cut into units of 64. The units of all segments, end to end, are dealt to
+// the CTAs in equal contiguous runs, whatever the lengths of the batch: a
+// CTA finds its run with one scan of the lengths and walks the segments it
+// covers. A segment inside one CTA's run is finished there; the pieces of a
+// segment that crosses runs go to the workspace (at most two per CTA) and
+// k_paged_join adds them in ascending order.
+//
+// In a run each of the CTA's four warps takes every fourth block of 16 keys
+// through its own ring of asynchronous copies (16 K rows and 16 V rows of
+// 256 bytes per stage, swizzled so that ldmatrix reads hit distinct banks;
+// rows past a page's valid slots are filled with zeros, so whatever the
+// cache holds there cannot reach the sums) and keeps its own running
+// maximum, sum and output in registers: no warp waits for another inside a
+// segment. The products run on m16n8k16 tensor instructions with the
+// group's query heads as rows. At one query token per sequence the kernel
+// reads 512 bytes per 512 G multiply-adds, far to the memory side of the
+// tensor cores' balance, so the instruction's rate does not bound it; the
+// memory pipe does, and its loads in flight.
+#include "paged.cuh"
+#include "sm103_ptx.cuh"
+
+namespace vsa {
+namespace {
+
+constexpr int kUnit = 64;       // keys per scheduling unit
+constexpr int kMinUnits = 2;    // fewest units a CTA takes when there is little work
+constexpr int kBlk = 16;        // keys per warp step
+constexpr int kWarps = 4;
+constexpr int kStages = 3;      // ring stages per warp
+constexpr int kCtas = 304;      // two per SM on 152 SMs
+constexpr int kStageBytes = 2 * kBlk * 256;
+constexpr int kPitch = 136;     // floats per row of the warps' outputs in shared memory
+constexpr int kSmem = kWarps * kStages * kStageBytes;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    Paged p;
+    const void *q;
+    long long qs;
+    const void *k, *v;
+    const int *idx, *cnt;  // page lists (NULL: all pages)
+    int cap;
+    void *out;
+    float *lse;
+    int rc, rows;          // chunks of a group's heads, rows per chunk
+    int2 *seg;             // [segments] first and last CTA
+    float2 *ml;            // [2 * kCtas, rows]
+    float *o;              // [2 * kCtas, rows, 128]
+};
+
+// Keys of segment list entry n ((b) without page lists, (b, h) with): the
+// positions it walks, valid or not.
+__device__ __forceinline__ int seg_keys(const AttnArgs &a, int n) {
+    if (!a.idx) return paged_len(a.p, n);
+    return clampi(__ldg(a.cnt + n), 0, a.cap) * a.p.page;
+}
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool fill) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// c += a b: a 16 x 16 (row), b 16 x 8 (col), fp32 accumulators.
+template <typename T>
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
+template <>
+__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                                        uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+template <>
+__device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Units of all list entries before this CTA's run, found by the whole CTA.
+struct Run {
+    long long x0, x1, per;  // this CTA's units and the units per CTA
+    int n;                  // list entry that holds x0
+    long long before;       // units of the entries before n
+};
+__device__ __forceinline__ Run find_run(const AttnArgs &a) {
+    __shared__ long long s_warp[kWarps];
+    __shared__ long long s_before;
+    __shared__ int s_n;
+    const int N = a.idx ? a.p.B * a.p.Hkv : a.p.B;
+    const int mult = a.idx ? a.rc : a.p.Hkv * a.rc;  // segments per entry
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    auto units_of = [&](int n) -> long long {
+        return n < N ? (long long)((seg_keys(a, n) + kUnit - 1) / kUnit) * mult : 0;
+    };
+    long long total = 0;
+    for (int n0 = 0; n0 < N; n0 += kWarps * 32) total += units_of(n0 + tid);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    if (lane == 0) s_warp[wid] = total;
+    __syncthreads();
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) total += s_warp[w];
+    Run r;
+    r.per = (total + kCtas - 1) / kCtas;
+    if (r.per < kMinUnits) r.per = kMinUnits;
+    r.x0 = (long long)blockIdx.x * r.per;
+    r.x1 = r.x0 + r.per < total ? r.x0 + r.per : total;
+    r.n = 0;
+    r.before = 0;
+    if (r.x0 >= r.x1) return r;  // no work: the whole CTA leaves
+    long long carry = 0;
+    for (int n0 = 0; n0 < N; n0 += kWarps * 32) {
+        const long long v = units_of(n0 + tid);
+        long long inc = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        __syncthreads();  // s_warp is free again
+        if (lane == 31) s_warp[wid] = inc;
+        __syncthreads();
+        long long base = carry, all = carry;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            base += w < wid ? s_warp[w] : 0;
+            all += s_warp[w];
+        }
+        inc += base;
+        if (inc - v <= r.x0 && r.x0 < inc) {  // one thread of the CTA
+            s_n = n0 + tid;
+            s_before = inc - v;
+        }
+        carry = all;
+        if (carry > r.x0) break;
+    }
+    __syncthreads();
+    r.n = s_n;
+    r.before = s_before;
+    return r;
+}
+
+template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    const Run run = find_run(a);
+    if (run.x0 >= run.x1) return;
+    const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v), *Q = static_cast<const T *>(a.q);
+    const uint32_t ring = ptx::smem_addr(smem) + wid * kStages * kStageBytes;
+    const float sl2 = p.scale * kLog2e;
+
+    const int N = a.idx ? p.B * p.Hkv : p.B;
+    int n = run.n;
+    long long before = run.before;
+    for (long long x = run.x0; x < run.x1 && n < N;) {
+        const int keys = seg_keys(a, n);
+        const int units = (keys + kUnit - 1) / kUnit;
+        const long long entry = (long long)units * (a.idx ? a.rc : p.Hkv * a.rc);
+        if (x >= before + entry) {  // also passes over entries without keys
+            before += entry;
+            ++n;
+            continue;
+        }
+        const int sub = (int)((x - before) / units), off = (int)((x - before) % units);
+        const int take = (int)min((long long)(units - off), run.x1 - x);
+        const bool first = off == 0, last = off + take == units;
+        const int r = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
+        const int b = bh / p.Hkv, h = bh % p.Hkv;
+        const int rows = min(a.rows, p.G - r * a.rows);
+        const int len = paged_len(p, b);
+        const int key0 = off * kUnit, key1 = min(keys, (off + take) * kUnit);
+        const int nblk = (key1 - key0 + kBlk - 1) / kBlk;
+        const long long hoff = (long long)h * p.head_stride;
+
+        // Q as A fragments: row g (and g + 8) of each 16-row tile, 8 k-steps
+        uint32_t qa[MT][8][4];
+        {
+            const T *qb = Q + (long long)b * a.qs + ((long long)h * p.G + r * a.rows) * kD;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = m * 16 + g + 8 * e;
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        qa[m][j][e] = row < rows ? __ldg(src + 8 * j + t) : 0u;
+                        qa[m][j][2 + e] = row < rows ? __ldg(src + 8 * j + 4 + t) : 0u;
+                    }
+                }
+        }
+
+        const int mine = nblk > wid ? (nblk - wid + kWarps - 1) / kWarps : 0;  // this warp's blocks
+
+        // Window of up to 32 of this warp's blocks, one per lane: the page
+        // (or -1) and the valid slots of the block.
+        int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
+        auto window = [&](int i0) {
+            w_base = i0;
+            w_id = -1;
+            w_valid = 0;
+            if (i0 + lane < mine) {
+                const int pos = key0 + ((i0 + lane) * kWarps + wid) * kBlk;
+                int j = pos >> p.page_log2;
+                w_slot = pos & (p.page - 1);
+                if (a.idx) j = __ldg(a.idx + (long long)bh * a.cap + j);
+                w_id = paged_id(p, b, j);
+                if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
+            }
+        };
+        int valid[kStages];
+        auto issue = [&](int i, int stage) {  // block i of this warp into a stage
+            if (i >= w_base + 32) window(i);
+            const int id = __shfl_sync(0xffffffffu, w_id, i - w_base);
+            const int slot = __shfl_sync(0xffffffffu, w_slot, i - w_base);
+            const int ok = __shfl_sync(0xffffffffu, w_valid, i - w_base);
+            const long long at = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + hoff;
+            const int c = lane & 15;
+            const uint32_t dst = ring + stage * kStageBytes;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int row = 2 * e + (lane >> 4);
+                const bool live = row < ok;
+                const long long src = live ? at + row * p.tok_stride + 8 * c : 0;
+                const uint32_t d = dst + row * 256 + ((c ^ (row & 7)) << 4);
+                cp16(d, K + src, live);
+                cp16(d + kBlk * 256, V + src, live);
+            }
+            return ok;
+        };
+#pragma unroll
+        for (int s = 0; s < kStages - 1; ++s) {
+            valid[s] = 0;
+            if (s < mine) valid[s] = issue(s, s);
+            cp_commit();
+        }
+        valid[kStages - 1] = 0;
+
+        float m_run[MT][2], l_run[MT][2], acc[MT][16][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            m_run[m][0] = m_run[m][1] = -INFINITY;
+            l_run[m][0] = l_run[m][1] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
+        }
+        for (int i0 = 0; i0 < mine; i0 += kStages) {
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) {
+                const int i = i0 + s;
+                if (i >= mine) break;
+                cp_wait<kStages - 2>();
+                __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
+                if (i + kStages - 1 < mine)
+                    valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
+                cp_commit();
+                const uint32_t st = ring + s * kStageBytes;
+                float sc[MT][2][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[m][0][e] = sc[m][1][e] = 0.f;
+                {
+                    const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t kb[4];
+                        ldsm4(kb, st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma16816<T>(sc[m][0], qa[m][j], kb[0], kb[1]);
+                            mma16816<T>(sc[m][1], qa[m][j], kb[2], kb[3]);
+                        }
+                    }
+                }
+                const int ok = valid[s];
+                uint32_t pa[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m) {
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = 8 * u + 2 * t + (e & 1);
+                            sc[m][u][e] = key < ok ? sc[m][u][e] * sl2 : -INFINITY;
+                        }
+                    float corr[2];
+                    bool moved = false;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {  // rows g and g + 8
+                        float mx = fmaxf(fmaxf(sc[m][0][2 * e], sc[m][0][2 * e + 1]),
+                                         fmaxf(sc[m][1][2 * e], sc[m][1][2 * e + 1]));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                        const float mn = fmaxf(m_run[m][e], mx);
+                        const float ref = mn == -INFINITY ? 0.f : mn;  // a row without keys so far
+                        corr[e] = ptx::ex2(m_run[m][e] - ref);
+                        moved = moved || mn != m_run[m][e];
+                        m_run[m][e] = mn;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                const float pr = ptx::ex2(sc[m][u][2 * e + c] - ref);
+                                sc[m][u][2 * e + c] = pr;
+                                sum += pr;
+                            }
+                        l_run[m][e] = l_run[m][e] * corr[e] + sum;  // this lane's keys; quads are joined at the end
+                    }
+                    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            acc[m][j][0] *= corr[0];
+                            acc[m][j][1] *= corr[0];
+                            acc[m][j][2] *= corr[1];
+                            acc[m][j][3] *= corr[1];
+                        }
+                    }
+                    // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps
+                    // the unrounded values): half a step of the output's own type
+                    pa[m][0] = pack2<T>(sc[m][0][0], sc[m][0][1]);
+                    pa[m][1] = pack2<T>(sc[m][0][2], sc[m][0][3]);
+                    pa[m][2] = pack2<T>(sc[m][1][0], sc[m][1][1]);
+                    pa[m][3] = pack2<T>(sc[m][1][2], sc[m][1][3]);
+                }
+                {
+                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, c0 = lane >> 4;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        uint32_t vb[4];
+                        ldsm4t(vb, st + kBlk * 256 + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int m = 0; m < MT; ++m) {
+                            mma16816<T>(acc[m][2 * j], pa[m], vb[0], vb[1]);
+                            mma16816<T>(acc[m][2 * j + 1], pa[m], vb[2], vb[3]);
+                        }
+                    }
+                }
+            }
+        }
+        cp_wait<0>();
+        __syncwarp();  // the warp's ring is free: it takes the warp's outputs
+        float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_run[m][e];
+                l += __shfl_xor_sync(0xffffffffu, l, 1);
+                l += __shfl_xor_sync(0xffffffffu, l, 2);
+                const int row = m * 16 + g + 8 * e;
+                if (t == 0) {
+                    s_m[wid][row] = m_run[m][e];
+                    s_l[wid][row] = l;
+                }
+                if (row < rows)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
+                            make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
+            }
+        __syncthreads();
+        const bool whole = first && last;
+        const int slot = 2 * (int)blockIdx.x + (first ? 1 : 0);
+        for (int row = 0; row < rows; ++row) {
+            float M = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
+            const float ref = M == -INFINITY ? 0.f : M;
+            float l = 0.f, o = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ptx::ex2(s_m[w][row] - ref);
+                l += f * s_l[w][row];
+                o += f * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
+            }
+            if (whole) {
+                const long long hq = (long long)b * p.Hq + h * p.G + r * a.rows + row;
+                static_cast<T *>(a.out)[hq * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
+                if (tid == 0) a.lse[hq] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+            } else {
+                a.o[((long long)slot * a.rows + row) * kD + tid] = o;
+                if (tid == 0) a.ml[(long long)slot * a.rows + row] = make_float2(M, l);
+            }
+        }
+        if (first && tid == 0)
+            a.seg[(long long)bh * a.rc + r] = make_int2((int)blockIdx.x, (int)((x - off + units - 1) / run.per));
+        __syncthreads();  // the ring is written again by the next segment
+        x += take;
+    }
+}
+
+// One CTA per (sequence, query head): writes the rows without keys and
+// joins the pieces of the segments that crossed CTAs, in ascending order of
+// their keys within each warp, then the warps in order.
+template <typename T> __global__ void __launch_bounds__(128) k_paged_join(AttnArgs a) {
+    __shared__ float s_m[4], s_l[4];
+    __shared__ __align__(16) float s_o[4][kD];
+    const Paged &p = a.p;
+    const int row = blockIdx.x, b = row / p.Hq, hq = row % p.Hq, h = hq / p.G, in = hq % p.G;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int bh = b * p.Hkv + h;
+    T *out = static_cast<T *>(a.out) + (long long)row * kD;
+    if (seg_keys(a, a.idx ? bh : b) == 0) {
+        out[tid] = from_f<T>(0.f);
+        if (tid == 0) a.lse[row] = -INFINITY;
+        return;
+    }
+    const int2 sg = a.seg[(long long)bh * a.rc + in / a.rows];
+    if (sg.x == sg.y) return;  // finished by its CTA
+    const int r = in % a.rows, pieces = sg.y - sg.x + 1;
+    float M = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = wid; i < pieces; i += 4) {
+        const long long at = (long long)(2 * (sg.x + i) + (i == 0 ? 1 : 0)) * a.rows + r;
+        const float2 ml = a.ml[at];
+        const float4 x = *reinterpret_cast<const float4 *>(a.o + at * kD + 4 * lane);
+        const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn;
+        const float f = ptx::ex2(M - ref), e = ptx::ex2(ml.x - ref);
+        M = mn;
+        l = l * f + ml.y * e;
+        o.x = o.x * f + x.x * e;
+        o.y = o.y * f + x.y * e;
+        o.z = o.z * f + x.z * e;
+        o.w = o.w * f + x.w * e;
+    }
+    *reinterpret_cast<float4 *>(&s_o[wid][4 * lane]) = o;
+    if (lane == 0) {
+        s_m[wid] = M;
+        s_l[wid] = l;
+    }
+    __syncthreads();
+    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float sum = 0.f, val = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const float e = ptx::ex2(s_m[w] - ref);
+        sum += e * s_l[w];
+        val += e * s_o[w][tid];
+    }
+    out[tid] = from_f<T>(sum == 0.f ? 0.f : val / sum);
+    if (tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (M + log2f(sum));
+}
+
+// Query heads of a group are taken 16 at a time, 32 when there are more.
+int rows_of(int G) { return G <= 16 ? G : (G <= 32 ? G : 32); }
+
+template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
+    const bool one = a.rows <= 16;
+    const void *fn = one ? (const void *)k_paged_attn<T, 1> : (const void *)k_paged_attn<T, 2>;
+    const cudaError_t ae = ensure_smem_limit(fn, kSmem);
+    if (ae != cudaSuccess) return status_from_cuda(ae);
+    prof_begin("paged_attn", s);
+    if (one)
+        k_paged_attn<T, 1><<<kCtas, kWarps * 32, kSmem, s>>>(a);
+    else
+        k_paged_attn<T, 2><<<kCtas, kWarps * 32, kSmem, s>>>(a);
+    prof_end(s);
+    const vsa_status st = status_from_cuda(cudaGetLastError());
+    if (st != VSA_OK) return st;
+    prof_begin("paged_join", s);
+    k_paged_join<T><<<(unsigned)(a.p.B * a.p.Hq), 128, 0, s>>>(a);
+    prof_end(s);
+    return status_from_cuda(cudaGetLastError());
+}
+
+}  // namespace
+
+PagedWs paged_ws(const Paged &p) {
+    PagedWs w{};
+    size_t at = 0;
+    auto take = [&](size_t bytes) {
+        const size_t o = at;
+        at += (bytes + 255) & ~size_t(255);
+        return o;
+    };
+    const size_t rows = rows_of(p.G), rc = (p.G + rows - 1) / rows;
+    w.keys = take(sizeof(uint32_t) * p.B * (size_t)p.Hkv * p.max_pages);
+    w.seg = take(sizeof(int2) * p.B * (size_t)p.Hkv * rc);
+    w.ml = take(sizeof(float2) * 2 * kCtas * rows);
+    w.o = take(sizeof(float) * 2 * kCtas * rows * kD);
+    w.total = at;
+    return w;
+}
+
+}  // namespace vsa
+
+extern "C" size_t vsa_paged_workspace_size(const vsa_paged_desc *desc) {
+    vsa::Paged p;
+    if (vsa::to_paged(desc, &p, false) != VSA_OK) return 0;
+    return vsa::paged_ws(p).total;
+}
+
+extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride,
+                                     const void *k_cache, const void *v_cache, const int32_t *page_idx,
+                                     const int32_t *page_cnt, int idx_cap, void *out, float *lse, void *workspace,
+                                     size_t workspace_bytes, vsa_stream_t stream) {
+    using namespace vsa;
+    AttnArgs a{};
+    const vsa_status st = to_paged(desc, &a.p, true);
+    if (st != VSA_OK) return st;
+    if (!token_stride(q_stride, a.p.Hq, &a.qs)) return VSA_ERR_SHAPE;
+    if (!q || !k_cache || !v_cache || !out || !lse || !page_idx != !page_cnt) return VSA_ERR_NULL;
+    if (page_idx && idx_cap < 1) return VSA_ERR_SHAPE;
+    if (page_idx && (long long)idx_cap * a.p.page > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return VSA_ERR_LAYOUT;
+    if (((uintptr_t)page_idx | (uintptr_t)page_cnt | (uintptr_t)lse) & 3u) return VSA_ERR_LAYOUT;
+    const PagedWs ws = paged_ws(a.p);
+    if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < ws.total) return VSA_ERR_WORKSPACE;
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.idx = page_idx;
+    a.cnt = page_cnt;
+    a.cap = idx_cap;
+    a.out = out;
+    a.lse = lse;
+    a.rows = rows_of(a.p.G);
+    a.rc = (a.p.G + a.rows - 1) / a.rows;
+    char *w = static_cast<char *>(workspace);
+    a.seg = reinterpret_cast<int2 *>(w + ws.seg);
+    a.ml = reinterpret_cast<float2 *>(w + ws.ml);
+    a.o = reinterpret_cast<float *>(w + ws.o);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16>(a, s) : launch_attn<__half>(a, s);
+}

@@ -34,7 +34,8 @@ EXPORTS = ("vsa_workspace_size", "vsa_build_block_map", "vsa_build_block_map_sta
            "vsa_tile_3d_count", "vsa_tile_3d", "vsa_untile_3d", "vsa_gate_grad",
            "vsa_mask_to_index_blocks", "vsa_fwd_blocks", "vsa_bwd_blocks", "vsa_check_wait_timeout",
            "vsa_train_step_host_size", "vsa_train_step_host", "vsa_fwd_step_host", "vsa_step_host_status",
-           "vsa_check_inputs", "vsa_head_slice", "vsa_fwd_reuse", "vsa_bwd_reuse")
+           "vsa_check_inputs", "vsa_head_slice", "vsa_fwd_reuse", "vsa_bwd_reuse",
+           "vsa_paged_workspace_size", "vsa_paged_append", "vsa_page_select", "vsa_paged_attn")
 
 REUSE_QK_MEANS, REUSE_V_MEANS = 1, 2  # vsa_fwd_reuse / vsa_bwd_reuse mask bits
 
@@ -53,6 +54,13 @@ class VsaDesc(C.Structure):
                 ("Hkv", C.c_int32), ("D", C.c_int32), ("Sq", C.c_int32), ("Skv", C.c_int32),
                 ("tile_q", C.c_int32), ("tile_kv", C.c_int32), ("nQ", C.c_int32), ("nKV", C.c_int32),
                 ("cu_seqlens_q", C.c_void_p), ("cu_seqlens_kv", C.c_void_p), ("scale", C.c_float)]
+
+
+class PagedDesc(C.Structure):
+    _fields_ = [("layout", C.c_int32), ("dtype", C.c_int32), ("B", C.c_int32), ("Hq", C.c_int32),
+                ("Hkv", C.c_int32), ("D", C.c_int32), ("page", C.c_int32), ("num_pages", C.c_int32),
+                ("max_pages", C.c_int32), ("page_stride", C.c_int64), ("page_table", C.c_void_p),
+                ("seq_lens", C.c_void_p), ("scale", C.c_float)]
 
 
 _lib = None
@@ -139,6 +147,17 @@ def lib():
         L.vsa_fwd_step_host.restype = C.c_int
         L.vsa_fwd_step_host.argtypes = [C.POINTER(VsaDesc), C.c_int, P, P, P, P, P, P, C.c_int, P, P, P, C.c_size_t,
                                         P]
+        i64 = C.c_int64
+        L.vsa_paged_workspace_size.restype = C.c_size_t
+        L.vsa_paged_workspace_size.argtypes = [C.POINTER(PagedDesc)]
+        L.vsa_paged_append.restype = C.c_int
+        L.vsa_paged_append.argtypes = [C.POINTER(PagedDesc), C.c_int, P, i64, P, i64, P, i64, P, P, P, P, P, C.c_int,
+                                       C.c_int, C.c_int, P, P, P, P]
+        L.vsa_page_select.restype = C.c_int
+        L.vsa_page_select.argtypes = [C.POINTER(PagedDesc), P, i64, P, C.c_int, C.c_int, C.c_int, P, P, P, C.c_size_t,
+                                      P]
+        L.vsa_paged_attn.restype = C.c_int
+        L.vsa_paged_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
         _lib = L
     return _lib
 
@@ -550,3 +569,233 @@ def check_wait_timeout(workspace: torch.Tensor, limit_ns: int = 50_000_000, stre
     _check("vsa_check_wait_timeout", lib().vsa_check_wait_timeout(_p(workspace), int(limit_ns), _p(done),
                                                                     _stream(stream)))
     return int(done.item())
+
+
+# ---------------------------------------------------------------- paged cache
+
+def _row_stride(name, x, heads, D):
+    """Elements from one token of x [T, heads, D] to the next (heads and
+    dims dense; 0 where there is only one token)."""
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D:
+        raise ValueError(f"{name}: expected [tokens, {heads}, {D}], got {list(x.shape)}")
+    if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != D)):
+        raise ValueError(f"{name}: heads and dims must be dense")
+    return x.stride(0) if x.shape[0] > 1 else 0
+
+
+class PagedCache:
+    """One layer's paged key/value cache (the conventions of the paged calls
+    in include/vsa.h): appending, page selection, one-token attention.
+
+    layout: "bshd" (pages [page, Hkv, D]) | "bhsd" (pages [Hkv, page, D]).
+    k, v: [num_pages, ...page] tensors of dtype, dense inside a page (halves
+    of one buffer are fine); k_mean: fp32 [num_pages, Hkv, D], or False for a
+    cache whose pages are never selected. Those not given are allocated
+    unless allocate is False (a cache that only selects needs no k and v).
+    page_table: int32 [B, max_pages]; seq_lens: int32 [B], the tokens in the
+    cache with those of the current step counted in. Both belong to the
+    caller, are read by every call when it runs on the device and may be
+    shared by all layers (allocated as zeros if not given). workspace: at
+    least ``vsa_paged_workspace_size`` bytes, 256-byte aligned, may be shared by
+    caches whose calls run one after another on a stream.
+    """
+
+    def __init__(self, layout, dtype, B, Hq, Hkv, D, page, num_pages, max_pages, k=None, v=None, k_mean=None,
+                 page_table=None, seq_lens=None, scale=0.0, workspace=None, allocate=True, device="cuda"):
+        if layout not in ("bshd", "bhsd"):
+            raise ValueError(f"a page's layout is bshd or bhsd, not {layout}")
+        if dtype not in DTYPES:
+            raise ValueError("the cache holds bf16 or fp16")
+        given = [t for t in (k, v, k_mean, page_table, seq_lens, workspace) if torch.is_tensor(t)]
+        self.device = given[0].device if given else torch.device(device)
+        if self.device.type == "cuda" and self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.layout, self.dtype = layout, dtype
+        self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
+        self.page, self.num_pages, self.max_pages = page, num_pages, max_pages
+        shape = (num_pages, page, Hkv, D) if layout == "bshd" else (num_pages, Hkv, page, D)
+        if k is None and v is None and allocate:
+            k, v = (torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
+        if k_mean is None and allocate:
+            k_mean = torch.zeros((num_pages, Hkv, D), dtype=torch.float32, device=self.device)
+        elif k_mean is False:
+            k_mean = None
+        i32 = dict(dtype=torch.int32, device=self.device)
+        page_table = torch.zeros((B, max_pages), **i32) if page_table is None else page_table
+        seq_lens = torch.zeros(B, **i32) if seq_lens is None else seq_lens
+        inner = (Hkv * D, D, 1) if layout == "bshd" else (page * D, D, 1)
+        stride = 0
+        for name, t in (("k", k), ("v", v)):
+            if t is None:
+                continue
+            self._is(name, t, shape, dtype)
+            if any(n > 1 and a != b for n, a, b in zip(shape[1:], t.stride()[1:], inner)):
+                raise ValueError(f"{name}: a page must be dense")
+            if num_pages > 1 and stride not in (0, t.stride(0)):
+                raise ValueError("k and v must have the same page stride")
+            stride = t.stride(0) if num_pages > 1 else 0
+        if (k is None) != (v is None):
+            raise ValueError("give both k and v, or neither")
+        for name, t, shp, dt in (("k_mean", k_mean, (num_pages, Hkv, D), torch.float32),
+                                 ("page_table", page_table, (B, max_pages), torch.int32),
+                                 ("seq_lens", seq_lens, (B,), torch.int32)):
+            if t is not None:
+                self._is(name, t, shp, dt)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}: must be contiguous")
+        self.k, self.v, self.k_mean, self.page_table, self.seq_lens = k, v, k_mean, page_table, seq_lens
+        self.desc = PagedDesc(LAYOUTS[layout], DTYPES[dtype], B, Hq, Hkv, D, page, num_pages, max_pages, stride,
+                              page_table.data_ptr(), seq_lens.data_ptr(), float(scale))
+        need = int(lib().vsa_paged_workspace_size(C.byref(self.desc)))
+        if need == 0:
+            raise ValueError("invalid paged-cache description")
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        elif workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace: at least {need} bytes on {self.device} are needed")
+        self.workspace = workspace
+        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+
+    def _is(self, name, t, shape, dtype):
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: expected {dtype} {list(shape)} on {self.device}, "
+                             f"got {t.dtype} {list(t.shape)} on {t.device}")
+
+    def _on(self, name, t, dtype):
+        if t.dtype != dtype or t.device != self.device:
+            raise ValueError(f"{name}: expected {dtype} on {self.device}, got {t.dtype} on {t.device}")
+
+    def _empty(self, shape, dtype, stream):
+        """An output that belongs to the stream the call runs on."""
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+    def _run(self, name, stream, *args):
+        """The call on this cache's device and the given (or current) stream."""
+        if self.device.type != "cuda":
+            raise ValueError(f"the cache is on {self.device}: the calls run on a GPU only")
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        elif stream.device != self.device:
+            raise ValueError(f"stream: expected one of {self.device}, got {stream.device}")
+        fn = getattr(lib(), name)
+        if torch.cuda.current_device() == self.device.index:
+            code = fn(C.byref(self.desc), *args, stream.cuda_stream)
+        else:
+            with torch.cuda.device(self.device):
+                code = fn(C.byref(self.desc), *args, stream.cuda_stream)
+        _check(name, code)
+
+    def _need(self, *names):
+        for n in names:
+            if getattr(self, n) is None:
+                raise ValueError(f"this cache has no {n}")
+
+    def append(self, k, v, q=None, cu_seqlens=None, cos=None, sin=None, positions=None, interleaved=False, q_out=None,
+               stream=None):
+        """vsa_paged_append: k, v [T, Hkv, D] (and q [T, Hq, D]) of the new
+        tokens, which seq_lens already counts; cu_seqlens int32 [B+1], None
+        for one token per sequence. cos, sin: fp32 [rows, rot_dim / 2], None
+        for no rotation. Returns the rotated q (None without q)."""
+        self._need("k", "v")
+        T = k.shape[0]
+        self._on("k", k, self.dtype)
+        self._on("v", v, self.dtype)
+        ks, vs = _row_stride("k", k, self.Hkv, self.D), _row_stride("v", v, self.Hkv, self.D)
+        qs = 0
+        if v.shape[0] != T or (q is not None and q.shape[0] != T):
+            raise ValueError("k, v and q must have the same number of tokens")
+        if q is not None:
+            self._on("q", q, self.dtype)
+            qs = _row_stride("q", q, self.Hq, self.D)
+            if q_out is None:
+                q_out = self._empty((T, self.Hq, self.D), self.dtype, stream)
+            else:
+                self._is("q_out", q_out, (T, self.Hq, self.D), self.dtype)
+                if not q_out.is_contiguous():
+                    raise ValueError("q_out: must be contiguous")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        if cu_seqlens is not None:
+            self._is("cu_seqlens", cu_seqlens, (self.B + 1,), torch.int32)
+            if not cu_seqlens.is_contiguous():
+                raise ValueError("cu_seqlens: must be contiguous")
+        elif T != self.B:
+            raise ValueError("without cu_seqlens there is one token per sequence")
+        rows = rot = 0
+        if (cos is None) != (sin is None):
+            raise ValueError("give both cos and sin, or neither")
+        if cos is not None:
+            if cos.dim() != 2 or cos.shape != sin.shape or not (cos.is_contiguous() and sin.is_contiguous()):
+                raise ValueError("cos and sin: expected contiguous [rows, rot_dim / 2]")
+            self._on("cos", cos, torch.float32)
+            self._on("sin", sin, torch.float32)
+            rows, rot = cos.shape[0], 2 * cos.shape[1]
+        if positions is not None:
+            self._is("positions", positions, (T,), torch.int32)
+            if not positions.is_contiguous():
+                raise ValueError("positions: must be contiguous")
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._run("vsa_paged_append", stream, T, k.data_ptr(), ks, v.data_ptr(), vs, ptr(q), qs, ptr(q_out),
+                  ptr(cu_seqlens), ptr(positions), ptr(cos), ptr(sin), rows, rot, int(bool(interleaved)),
+                  self.k.data_ptr(), self.v.data_ptr(), ptr(self.k_mean))
+        return q_out
+
+    def select(self, q, topk, keep_first=0, keep_last=1, page_idx=None, page_cnt=None, stream=None):
+        """vsa_page_select: the pages that q [B, Hq, D] attends to, as
+        (page_idx int32 [B, Hkv, topk], page_cnt int32 [B, Hkv])."""
+        self._need("k_mean")
+        self._on("q", q, self.dtype)
+        qs = self._rows(q)
+        if page_idx is None:
+            page_idx = self._empty((self.B, self.Hkv, topk), torch.int32, stream)
+        if page_cnt is None:
+            page_cnt = self._empty((self.B, self.Hkv), torch.int32, stream)
+        self._lists(page_idx, page_cnt)
+        if page_idx.shape[2] != topk:
+            raise ValueError(f"page_idx: expected topk = {topk} entries per row")
+        self._run("vsa_page_select", stream, q.data_ptr(), qs, self.k_mean.data_ptr(), int(topk), int(keep_first),
+                  int(keep_last), page_idx.data_ptr(), page_cnt.data_ptr(), *self._ws)
+        return page_idx, page_cnt
+
+    def attend(self, q, pages=None, out=None, lse=None, stream=None):
+        """vsa_paged_attn: q [B, Hq, D] over the whole cache, or over the
+        pages = (page_idx, page_cnt) that select returned. Returns (out
+        [B, Hq, D], lse fp32 [B, Hq])."""
+        self._need("k", "v")
+        self._on("q", q, self.dtype)
+        qs = self._rows(q)
+        idx = cnt = None
+        cap = 0
+        if pages is not None:
+            self._lists(*pages)
+            idx, cnt, cap = pages[0].data_ptr(), pages[1].data_ptr(), pages[0].shape[2]
+        if out is None:
+            out = self._empty((self.B, self.Hq, self.D), self.dtype, stream)
+        else:
+            self._is("out", out, (self.B, self.Hq, self.D), self.dtype)
+            if not out.is_contiguous():
+                raise ValueError("out: must be contiguous")
+        if lse is None:
+            lse = self._empty((self.B, self.Hq), torch.float32, stream)
+        else:
+            self._is("lse", lse, (self.B, self.Hq), torch.float32)
+            if not lse.is_contiguous():
+                raise ValueError("lse: must be contiguous")
+        self._run("vsa_paged_attn", stream, q.data_ptr(), qs, self.k.data_ptr(), self.v.data_ptr(), idx, cnt, cap,
+                  out.data_ptr(), lse.data_ptr(), *self._ws)
+        return out, lse
+
+    def _rows(self, q):
+        qs = _row_stride("q", q, self.Hq, self.D)
+        if q.shape[0] != self.B:
+            raise ValueError(f"q: expected one token for each of {self.B} sequences")
+        return qs
+
+    def _lists(self, idx, cnt):
+        if idx.dim() != 3 or not (idx.is_contiguous() and cnt.is_contiguous()):
+            raise ValueError("page lists: expected contiguous page_idx [B, Hkv, cap] and page_cnt [B, Hkv]")
+        self._is("page_idx", idx, (self.B, self.Hkv, idx.shape[2]), torch.int32)
+        self._is("page_cnt", cnt, (self.B, self.Hkv), torch.int32)

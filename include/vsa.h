@@ -447,6 +447,130 @@ vsa_status vsa_check_inputs(const vsa_desc *desc, const int32_t *q_var, const in
                             const int32_t *kv_qidx, void *workspace, size_t workspace_bytes, vsa_stream_t stream,
                             int32_t *code);
 
+/* ------------------------------------------------------------ paged cache
+ * Serving: one new token per sequence attends to a key/value cache kept in
+ * pages, the single-token form of the calls above. A page holds `page`
+ * consecutive tokens of one sequence and plays the part of a key/value
+ * tile: its mean key is the coarse key that vsa_page_select scores. The
+ * pages of the sources have no such call; the conventions at the top of
+ * this file apply (device pointers, caller-owned buffers, nothing
+ * allocated, no synchronisation), and:
+ *   cache     k_cache, v_cache: num_pages pages of page x Hkv x D elements,
+ *             VSA_LAYOUT_BSHD pages [page, Hkv, D] or VSA_LAYOUT_BHSD pages
+ *             [Hkv, page, D], dense inside a page, page_stride elements
+ *             from one page to the next (so that keys and values may be
+ *             halves of one buffer).
+ *   table     page_table [B, max_pages] int32: the page that holds tokens
+ *             [j * page, (j + 1) * page) of sequence b. Several sequences
+ *             may read one page (a shared prefix); pages that a call writes
+ *             belong to one sequence only. Entries past a sequence's end
+ *             are not read as pages.
+ *   lengths   seq_lens [B] int32: tokens of each sequence in the cache,
+ *             those of the current step included, at most
+ *             max_pages * page; 0 marks an unused row of a padded batch.
+ *   means     k_mean [num_pages, Hkv, D] fp32: the mean of the page's stored
+ *             keys, defined for full pages.
+ * Device-resident values out of range never move an access outside a
+ * buffer: lengths are clamped, a token whose page id is outside
+ * [0, num_pages) is not stored, and a listed page that does not exist
+ * (its index outside [0, max_pages) or its id outside the pool) holds no
+ * key. Every length, id and offset is 64-bit where it is multiplied. */
+typedef struct {
+    int32_t layout;       /* VSA_LAYOUT_BSHD or VSA_LAYOUT_BHSD: the order inside a page */
+    int32_t dtype;        /* vsa_dtype of q, k, v, the cache and out */
+    int32_t B;            /* sequences */
+    int32_t Hq, Hkv;      /* query heads, key/value heads; Hq % Hkv == 0 */
+    int32_t D;            /* head dim; must be 128 */
+    int32_t page;         /* tokens per page: 16, 32, 64, 128 or 256 */
+    int32_t num_pages;    /* pages in the pool */
+    int32_t max_pages;    /* entries of page_table per sequence; max_pages * page < 2^31 */
+    int64_t page_stride;  /* elements between pages, a multiple of 8; 0: dense (page * Hkv * D) */
+    const int32_t *page_table; /* device [B, max_pages] */
+    const int32_t *seq_lens;   /* device [B] */
+    float scale;          /* softmax scale on q.k; 0 means 1/sqrt(D) */
+} vsa_paged_desc;
+
+/* Bytes of workspace for vsa_page_select and vsa_paged_attn on this
+ * problem (256-byte aligned; 0 for an invalid descriptor). It holds nothing
+ * between calls and needs no clearing; calls that share it must not run
+ * concurrently. The page_table and seq_lens pointers are not looked at. */
+size_t vsa_paged_workspace_size(const vsa_paged_desc *desc);
+
+/* Appends the new tokens' keys and values to the cache, rotating keys (and
+ * queries) by their positions on the way, and writes the means of the
+ * pages that fill up.
+ *   T            new tokens in all, packed: token t of k [T, Hkv, D], v
+ *                [T, Hkv, D] and q [T, Hq, D] starts at t * k_stride,
+ *                t * v_stride, t * q_stride elements (multiples of 8, heads
+ *                and dims dense; 0: dense), so the three may be parts of
+ *                one projection's output.
+ *   cu_seqlens   device [B+1] int32, ascending: sequence b's tokens are
+ *                [cu_seqlens[b], cu_seqlens[b+1]); NULL: one token per
+ *                sequence (T == B). Tokens behind cu_seqlens[B] are ignored.
+ *   Token i of sequence b's n goes to position seq_lens[b] - n + i; a token
+ *   whose position is outside [0, max_pages * page) is ignored (nothing of
+ *   it is written, q_out included): an unused row has seq_lens[b] == 0.
+ *   cos, sin     device fp32 [table_rows, rot_dim / 2] (both or neither;
+ *                16-byte aligned), rot_dim a multiple of 16 up to D: row r
+ *                holds the angles of position r. The first rot_dim dims are
+ *                rotated in pairs (d, d + rot_dim/2), or (2d, 2d + 1) when
+ *                interleaved != 0: y1 = x1 c - x2 s, y2 = x2 c + x1 s, each
+ *                product and each sum rounded once to fp32, the result once
+ *                to dtype. The row is the token's position, or
+ *                positions[t] (device [T] int32, may be NULL: video tokens
+ *                number theirs by frame, row and column), clamped into the
+ *                table. rot_dim == 0: no rotation.
+ *   q, q_out     rotated queries, q_out [T, Hq, D] dense; both NULL: none.
+ *   k_mean       NULL: no means. A page gets its mean when its last slot is
+ *                written: the fp32 sum of its stored (16-bit) keys, slots
+ *                in groups of 16 (the even and the odd slots of a group in
+ *                ascending order, then the two sums), groups in ascending
+ *                order, divided by page. It is a function of the stored keys
+ *                alone, so it does not depend on how the tokens were cut
+ *                into calls, and a call made again gives the same result.
+ * k, v, q and q_out must not overlap each other's or the cache's memory.
+ * Errors: VSA_ERR_NULL, VSA_ERR_SHAPE (sizes, strides, T < 0, T != B
+ * without cu_seqlens), VSA_ERR_DTYPE, VSA_ERR_LAYOUT (also misaligned
+ * pointers), VSA_ERR_UNSUPPORTED (D, page, rot_dim, sizes past a limit),
+ * VSA_ERR_CUDA. T == 0 enqueues nothing. */
+vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, int64_t k_stride, const void *v,
+                            int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                            const int32_t *cu_seqlens, const int32_t *positions, const float *cos,
+                            const float *sin, int table_rows, int rot_dim, int interleaved, void *k_cache,
+                            void *v_cache, float *k_mean, vsa_stream_t stream);
+
+/* Chooses the pages each key/value head's queries attend to. q [B, Hq, D]
+ * (q_stride elements between sequences, 0: dense) is summed over the query
+ * heads of each group (in fp64, rounded once to fp32: g); full page j of
+ * sequence b scores r_j = sum_d g_d m_jd with the page's mean m_j, the
+ * products and sums rounded to fp32 in this order: x_d = g_d m_d; x_d +
+ * x_(d+64) for d < 64; of those x_d + x_(d+32) for d < 32; then neighbours
+ * (2i, 2i + 1) until one is left. NaN counts as -inf. The first keep_first
+ * (>= 0) and the last keep_last (>= 1) of the ceil(len / page) pages are
+ * always chosen (a partial last page has no mean and is always among
+ * them); the rest of min(topk, pages) by (r desc, j asc).
+ * Writes page_idx [B, Hkv, topk] int32, ascending, unused entries -1, and
+ * page_cnt [B, Hkv]. topk >= keep_first + keep_last. The result is the
+ * same bit for bit on every run. Errors as for vsa_paged_append, and
+ * VSA_ERR_WORKSPACE. */
+vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const float *k_mean,
+                           int topk, int keep_first, int keep_last, int32_t *page_idx, int32_t *page_cnt,
+                           void *workspace, size_t workspace_bytes, vsa_stream_t stream);
+
+/* Attention of one token per sequence over the cache: q [B, Hq, D]
+ * (q_stride as above), out [B, Hq, D] dense, lse fp32 [B, Hq] (natural
+ * log). With page_idx == NULL every token of the sequence is attended;
+ * otherwise the tokens of the pages page_idx [B, Hkv, idx_cap] lists for
+ * the query head's key/value head, page_cnt [B, Hkv] of them (a page listed
+ * twice counts twice). A row without keys gets O = 0, LSE = -inf. The work
+ * of the batch is cut into equal pieces whatever its lengths, and pieces
+ * of one row are joined in ascending order: the result is the same bit for
+ * bit on every run with the same batch. Errors as for vsa_page_select;
+ * VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1. */
+vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
+                          const void *v_cache, const int32_t *page_idx, const int32_t *page_cnt, int idx_cap,
+                          void *out, float *lse, void *workspace, size_t workspace_bytes, vsa_stream_t stream);
+
 /* Message of the last CUDA error behind a VSA_ERR_CUDA return, with the
  * name of the last kernel the library launched ("no error" if there was
  * none). The string is owned by the library (per calling thread). */

@@ -1,0 +1,182 @@
+"""Paged-cache calls on a machine without a GPU: every bad argument is
+refused on the host, before any CUDA call, and the references' own logic."""
+import ctypes as C
+
+import pytest
+import torch
+
+from bwd_tile_mean_gb300 import build as libbuild
+from bwd_tile_mean_gb300 import vsa
+from tests import paged_ref as ref
+
+# aligned and never dereferenced: every call fails host validation
+FAKE = C.c_void_p(1 << 20)
+ODD = C.c_void_p((1 << 20) + 2)
+
+
+@pytest.fixture(scope="module")
+def L():
+    libbuild.build()
+    return vsa.lib()
+
+
+def desc(**kw):
+    d = dict(layout=1, dtype=0, B=2, Hq=8, Hkv=2, D=128, page=64, num_pages=10, max_pages=4, page_stride=0,
+             page_table=1 << 20, seq_lens=1 << 20, scale=0.0)
+    d.update(kw)
+    return vsa.PagedDesc(*[d[f] for f, _ in vsa.PagedDesc._fields_])
+
+
+BAD_DESC = [(dict(layout=2), 4), (dict(layout=-1), 4), (dict(dtype=2), 3), (dict(B=0), 2), (dict(Hq=7), 2),
+            (dict(Hkv=0), 2), (dict(D=64), 5), (dict(page=48), 5), (dict(page=8), 5), (dict(page=512), 5),
+            (dict(num_pages=0), 2), (dict(max_pages=0), 2), (dict(max_pages=1 << 25), 5),
+            (dict(page_stride=64 * 2 * 128 - 8), 2), (dict(page_stride=64 * 2 * 128 + 4), 2),
+            (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2)]
+BAD_ARRAYS = [(dict(page_table=None), 1), (dict(seq_lens=None), 1), (dict(seq_lens=(1 << 20) + 2), 4)]
+
+
+def append(L, d=None, **kw):
+    a = dict(T=2, k=FAKE, ks=0, v=FAKE, vs=0, q=FAKE, qs=0, q_out=FAKE, cu=None, pos=None, cos=FAKE, sin=FAKE,
+             rows=9, rot=128, inter=0, kc=FAKE, vc=FAKE, mean=FAKE)
+    a.update(kw)
+    return L.vsa_paged_append(C.byref(d or desc()), *a.values(), None)
+
+
+def select(L, d=None, **kw):
+    a = dict(q=FAKE, qs=0, mean=FAKE, topk=2, first=0, last=1, idx=FAKE, cnt=FAKE, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.vsa_page_select(C.byref(d or desc()), *a.values(), None)
+
+
+def attn(L, d=None, **kw):
+    a = dict(q=FAKE, qs=0, kc=FAKE, vc=FAKE, idx=None, cnt=None, cap=0, out=FAKE, lse=FAKE, ws=FAKE, wsb=1 << 40)
+    a.update(kw)
+    return L.vsa_paged_attn(C.byref(d or desc()), *a.values(), None)
+
+
+@pytest.mark.parametrize("bad,code", BAD_DESC + BAD_ARRAYS, ids=lambda x: str(x))
+def test_descriptor_errors(L, bad, code):
+    assert append(L, desc(**bad)) == code
+    assert select(L, desc(**bad)) == code
+    assert attn(L, desc(**bad)) == code
+    size = L.vsa_paged_workspace_size(C.byref(desc(**bad)))
+    assert (size > 0) == ((bad, code) in BAD_ARRAYS)  # the size needs no arrays
+    assert L.vsa_paged_attn(None, FAKE, 0, FAKE, FAKE, None, None, 0, FAKE, FAKE, FAKE, 1 << 40, None) == 1
+
+
+def test_append_errors(L):
+    for name in ("k", "v", "kc", "vc", "q", "q_out", "cos", "sin"):
+        assert append(L, **{name: None}) == 1, name
+    for name in ("k", "v", "q", "q_out", "kc", "vc", "mean", "cos", "sin", "cu", "pos"):
+        assert append(L, **{name: ODD}) == 4, name
+    assert append(L, T=-1) == 2
+    assert append(L, T=3) == 2                       # T != B without offsets
+    assert append(L, ks=2 * 128 - 8) == 2            # tokens that overlap
+    assert append(L, vs=2 * 128 + 4) == 2            # not a multiple of 8
+    assert append(L, qs=-1024) == 2
+    assert append(L, rot=120) == 5
+    assert append(L, rot=144) == 5
+    assert append(L, rot=-16) == 5
+    assert append(L, rows=0) == 2
+    assert append(L, T=0, cu=FAKE) == 0              # nothing to do, nothing launched
+
+
+def test_select_errors(L):
+    for name in ("q", "mean", "idx", "cnt"):
+        assert select(L, **{name: None}) == 1, name
+        assert select(L, **{name: ODD}) == 4, name
+    assert select(L, topk=0) == 2
+    assert select(L, first=-1) == 2
+    assert select(L, last=0) == 2
+    assert select(L, topk=2, first=2) == 2
+    assert select(L, topk=3, first=2, last=2) == 2
+    assert select(L, first=2 ** 31 - 1, last=2 ** 31 - 1) == 2
+    assert select(L, qs=8) == 2
+    need = L.vsa_paged_workspace_size(C.byref(desc()))
+    assert select(L, wsb=need - 1) == 7 and select(L, ws=None) == 7 and select(L, ws=C.c_void_p((1 << 20) + 128)) == 7
+
+
+def test_attend_errors(L):
+    for name in ("q", "kc", "vc", "out", "lse"):
+        assert attn(L, **{name: None}) == 1, name
+        assert attn(L, **{name: ODD}) == 4, name
+    assert attn(L, idx=FAKE, cap=3) == 1 and attn(L, cnt=FAKE, cap=3) == 1
+    assert attn(L, idx=FAKE, cnt=FAKE, cap=0) == 2
+    assert attn(L, idx=FAKE, cnt=FAKE, cap=1 << 26) == 5
+    assert attn(L, idx=ODD, cnt=FAKE, cap=3) == 4
+    assert attn(L, qs=12) == 2
+    need = L.vsa_paged_workspace_size(C.byref(desc()))
+    assert attn(L, wsb=need - 1) == 7 and attn(L, ws=None) == 7
+
+
+def test_workspace_grows_with_the_problem(L):
+    size = lambda **kw: L.vsa_paged_workspace_size(C.byref(desc(**kw)))  # noqa: E731
+    assert size(max_pages=4000) > size()
+    assert size(Hq=32) > size()
+    assert size(B=300) > size()
+
+
+def cache(**kw):
+    a = dict(layout="bshd", dtype=torch.bfloat16, B=2, Hq=4, Hkv=2, D=128, page=16, num_pages=5, max_pages=3,
+             device="cpu")
+    a.update(kw)
+    return vsa.PagedCache(**a)
+
+
+def test_cache_refuses_bad_tensors(L):
+    good = torch.zeros(5, 16, 2, 128, dtype=torch.bfloat16)
+    cache(k=good, v=good)
+    for kw in (dict(layout="tnd"), dict(dtype=torch.float32), dict(D=64), dict(page=48), dict(Hq=3),
+               dict(k=good), dict(v=good), dict(k=good.half(), v=good), dict(k=good[:4], v=good),
+               dict(k=good.transpose(1, 2), v=good), dict(k=torch.zeros(5, 16, 4, 128, dtype=good.dtype)[:, :, ::2], v=good),
+               dict(k=torch.zeros(5, 2, 16, 2, 128, dtype=good.dtype)[:, 0], v=good),  # strides differ
+               dict(seq_lens=torch.zeros(2)), dict(seq_lens=torch.zeros(3, dtype=torch.int32)),
+               dict(page_table=torch.zeros(2, 4, dtype=torch.int32)),
+               dict(page_table=torch.zeros(2, 6, dtype=torch.int32)[:, ::2]),
+               dict(k_mean=torch.zeros(5, 2, 128, dtype=torch.bfloat16)), dict(workspace=torch.zeros(16))):
+        with pytest.raises(ValueError):
+            cache(**kw)
+
+
+def test_calls_refuse_bad_tensors(L):
+    c = cache()
+    bf = dict(dtype=torch.bfloat16)
+    k, q = torch.zeros(2, 2, 128, **bf), torch.zeros(2, 4, 128, **bf)
+    t = torch.zeros(9, 64)
+    i32 = dict(dtype=torch.int32)
+    for args, kw in (((k, k[:1]), {}), ((k, k, q[:1]), {}), ((k.half(), k), {}), ((k, k[:, :1]), {}),
+                     ((k, k.transpose(1, 2)), {}), ((torch.zeros(3, 2, 128, **bf),) * 2, {}),
+                     ((k, k), dict(cos=t)), ((k, k), dict(cos=t, sin=t[:8])), ((k, k), dict(cos=t.double(), sin=t)),
+                     ((k, k), dict(cos=t.t(), sin=t.t())), ((k, k), dict(q_out=q)), ((k, k, q), dict(q_out=q[:1])),
+                     ((k, k), dict(cu_seqlens=torch.zeros(2, **i32))), ((k, k), dict(cu_seqlens=torch.zeros(3))),
+                     ((k, k), dict(positions=torch.zeros(2))), ((k, k), dict(positions=torch.zeros(3, **i32)))):
+        with pytest.raises(ValueError):
+            c.append(*args, **kw)
+    idx, cnt = torch.zeros(2, 2, 2, **i32), torch.zeros(2, 2, **i32)
+    for call in (lambda: c.select(q[:1], 2), lambda: c.select(q.half(), 2), lambda: c.select(q, 3, page_idx=idx),
+                 lambda: c.attend(k), lambda: c.attend(q, (idx, cnt[:1])), lambda: c.attend(q, (idx.long(), cnt)),
+                 lambda: c.attend(q, (idx[:, :, ::2], cnt)), lambda: c.attend(q, out=q.half()),
+                 lambda: c.attend(q, lse=torch.zeros(2, 3)), lambda: cache(k_mean=False).select(q, 2),
+                 lambda: cache(allocate=False).attend(q), lambda: cache(allocate=False).append(k, k)):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: c.append(k, k), lambda: c.select(q, 2), lambda: c.attend(q)):
+        with pytest.raises(ValueError, match="GPU only"):
+            call()
+
+
+def test_reference_select_and_attend_on_a_case_by_hand():
+    pool = ref.Pool("bshd", torch.bfloat16, 1, 1, 16, 6, 6, [16 * 4 + 3], seed=1)
+    q = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
+    q[0, 0, 0] = 1.0
+    for j, value in enumerate((1.0, 3.0, 2.0, 3.0)):
+        pool.mean[pool.table[0][j]] = value
+    idx, cnt = ref.select(pool, q, 3, 0, 1)
+    assert idx.tolist() == [[[1, 3, 4]]] and cnt.tolist() == [[3]]
+    idx, cnt = ref.select(pool, q, 2, 0, 1)
+    assert idx.tolist() == [[[1, 4]]]                # of equal scores the lower page
+    q.zero_()
+    out, lse, _, _ = ref.attend(pool, q, (idx, cnt))
+    keys = [pool.v[pool.table[0][1]][:, 0].double(), pool.v[pool.table[0][4]][:3, 0].double()]
+    assert torch.allclose(out[0, 0], torch.cat(keys).mean(0))
+    assert abs(float(lse[0, 0]) - torch.log(torch.tensor(19.0)).item()) < 1e-6
