@@ -80,10 +80,34 @@ inline bool token_stride(int64_t given, int heads, long long *out) {
     return given == 0 || (given >= dense && given % 8 == 0);
 }
 
-// Workspace of vsa_page_select and vsa_paged_attn (either uses its own part).
+// Kernels of the paged calls are launched so that the next one on the stream
+// may start while this one drains: every CTA waits for the work before it
+// with grid_wait() before it touches memory, and lets the launch after it
+// go ahead with grid_go().
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+template <typename A>
+inline cudaError_t launch_paged(void (*kernel)(A), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                                const A &args, cudaStream_t s) {
+    cudaLaunchAttribute at[2];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    at[1].id = cudaLaunchAttributeClusterDimension;
+    at[1].val.clusterDim.x = cluster;
+    at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t c{};
+    c.gridDim = grid;
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = smem;
+    c.stream = s;
+    c.attrs = at;
+    c.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&c, kernel, args);
+}
+
+// Workspace of vsa_paged_attn.
 struct PagedWs {
-    size_t keys;        // [B * Hkv, max_pages] uint32 ordered score keys
-    size_t seg;         // [segments] int2: first and last CTA of a segment
+    size_t seg;         // [segments] int4: where a segment's pieces are
     size_t ml;          // [slots, rows] float2: running maximum (log2 units) and sum
     size_t o;           // [slots, rows, 128] fp32 unnormalised partial outputs
     size_t total;

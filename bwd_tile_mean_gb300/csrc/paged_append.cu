@@ -3,13 +3,14 @@
 // every page that fills up (vsa_paged_append).
 //
 // Work: a unit is one page of one sequence that receives tokens; a warp has
-// one 16-slot group of a unit and a chunk of HC key/value heads with their
-// query heads. Half a warp holds one token row (16 bytes = 8 dims per lane),
-// the two halves the even and the odd slots. The rotation's angles are
-// loaded once per token and chunk. Every key that a lane stores is also
-// added, as stored, to the lane's running sums; in a page that fills up the
-// slots written by earlier calls are read back from the cache in the same
-// order, and the groups' sums are joined through shared memory.
+// one 16-slot group of a unit and a chunk of rows per token: HC keys and
+// values, or 2 HC queries. Half a warp holds one token row (16 bytes = 8
+// dims per lane), the two halves the even and the odd slots; PB pairs of
+// slots are loaded together. The rotation's angles are loaded once per token
+// and chunk. Every key that a lane stores is also added, as stored, to the
+// lane's running sums; in a page that fills up the slots written by earlier
+// calls are read back from the cache in the same order, and the groups' sums
+// are joined through shared memory.
 //
 // Units are found without a scan of the lengths: sequence b with tokens
 // [cu[b], cu[b+1]) touches at most (cu[b+1] - cu[b]) / page + 2 pages, so
@@ -32,9 +33,11 @@ struct AppendArgs {
     void *kc, *vc;
     float *mean;
     long long units;
+    int kv_chunks, chunks;  // chunks of key/value heads, and with the queries'
 };
 
 constexpr int kGroup = 16;  // slots per warp
+constexpr long long kWideRows = 65536;  // token x key head rows from which a warp takes four heads
 
 // First token of sequence b, clamped into [0, T].
 __device__ __forceinline__ int cu_at(const AppendArgs &a, int b) { return clampi(__ldg(a.cu + b), 0, a.T); }
@@ -123,18 +126,21 @@ template <typename T> __device__ __forceinline__ void add8(float (&acc)[8], uint
     }
 }
 
-template <typename T, int HC>
-__global__ void k_paged_append(AppendArgs a) {
+template <typename T, int HC, int PB>
+__global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
     extern __shared__ __align__(16) float ssum[];  // [warps][HC][128] group sums
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
     const int groups = p.page / kGroup;                     // warps per unit
     const int per_cta = (int)(blockDim.x >> 5) / groups;    // units per CTA
-    const long long u = (long long)blockIdx.x * per_cta + wid / groups;
+    const int chunk = (int)(blockIdx.x % a.chunks);         // neighbouring CTAs: the rows of the same tokens
+    const long long u = (long long)(blockIdx.x / a.chunks) * per_cta + wid / groups;
     const int grp = wid % groups;
-    const int h0 = blockIdx.y * HC, hn = min(HC, p.Hkv - h0);
+    const bool kv = chunk < a.kv_chunks;
     const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v), *q = static_cast<const T *>(a.q);
     T *kc = static_cast<T *>(a.kc), *vc = static_cast<T *>(a.vc), *qo = static_cast<T *>(a.q_out);
+    grid_wait();
+    grid_go();
 
     // the unit: page `pg` of sequence b takes new tokens at slots [s0, s1)
     int b = 0, t_of = 0, s0 = 0, s1 = 0, pg = 0;  // slot s holds token t_of + s
@@ -162,70 +168,99 @@ __global__ void k_paged_append(AppendArgs a) {
         }
     }
     const bool work = s1 > s0;
-    const int id = work ? paged_id(p, b, pg) : -1;
-    const bool mean = a.mean && work && s1 == p.page && id >= 0;  // the page fills up in this call
+    const int id = work && kv ? paged_id(p, b, pg) : -1;
+    const bool mean = kv && a.mean && work && s1 == p.page && id >= 0;  // the page fills up in this call
     const long long page_at = (long long)max(id, 0) * p.page_stride;
+    const int g0 = grp * kGroup;
+    const bool mine = work && g0 < s1 && g0 + kGroup > s0;  // the group takes new tokens
+
+    if (!kv) {
+        if (!mine) return;
+        const int h0 = (chunk - a.kv_chunks) * 2 * HC, hn = min(2 * HC, p.Hq - h0);
+        for (int st = 0; st < kGroup; st += 2 * PB) {
+            if (g0 + st >= s1 || g0 + st + 2 * PB <= s0) continue;
+            uint4 x[PB][2 * HC];
+            Angles w[PB];
+#pragma unroll
+            for (int c = 0; c < PB; ++c) {
+                const int s = g0 + st + 2 * c + half;
+                const bool fresh = s >= s0 && s < s1;
+                const long long tok = fresh ? t_of + s : 0;
+#pragma unroll
+                for (int h = 0; h < 2 * HC; ++h)
+                    x[c][h] = fresh && h < hn
+                                  ? __ldg(reinterpret_cast<const uint4 *>(q + tok * a.qs + (h0 + h) * kD + 8 * i))
+                                  : make_uint4(0, 0, 0, 0);
+                if (fresh && 8 * i < a.rot) {
+                    const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                    load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < PB; ++c) {
+                const int s = g0 + st + 2 * c + half;
+                const bool fresh = s >= s0 && s < s1;
+                const long long tok = fresh ? t_of + s : 0;
+#pragma unroll
+                for (int h = 0; h < 2 * HC; ++h) {
+                    if (a.rot) x[c][h] = rotate<T>(a, x[c][h], w[c], i);
+                    if (fresh && h < hn)
+                        *reinterpret_cast<uint4 *>(qo + (tok * p.Hq + h0 + h) * kD + 8 * i) = x[c][h];
+                }
+            }
+        }
+        return;
+    }
+
+    const int h0 = chunk * HC, hn = min(HC, p.Hkv - h0);
     float acc[HC][8];
 #pragma unroll
     for (int h = 0; h < HC; ++h)
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
-
-    const int g0 = grp * kGroup;
-    if (work && (mean || (g0 < s1 && g0 + kGroup > s0))) {
-        for (int st = 0; st < kGroup; st += 2) {
-            const int s = g0 + st + half;
-            const bool fresh = s >= s0 && s < s1;
-            const bool old = mean && s < s0;
-            if (!__any_sync(0xffffffffu, fresh || old)) continue;
-            const long long tok = fresh ? t_of + s : 0;
-            Angles w;
-            if (a.rot && fresh && 8 * i < a.rot) {
-                const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
-                load_angles(a, clampi(row, 0, a.rows - 1), i, w);
-            }
-            const long long slot_at = page_at + s * p.tok_stride + 8 * i;
-            uint4 xk[HC], xv[HC];
+    if (mean || mine) {
+        for (int st = 0; st < kGroup; st += 2 * PB) {
+            if (!mean && (g0 + st >= s1 || g0 + st + 2 * PB <= s0)) continue;
+            uint4 xk[PB][HC], xv[PB][HC];
+            Angles w[PB];
 #pragma unroll
-            for (int h = 0; h < HC; ++h) {
-                xk[h] = xv[h] = make_uint4(0, 0, 0, 0);
-                if (h >= hn) continue;
-                if (fresh) {
-                    xk[h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
-                    xv[h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
-                } else if (old) {
-                    xk[h] = *reinterpret_cast<const uint4 *>(kc + slot_at + (h0 + h) * p.head_stride);
-                }
-            }
+            for (int c = 0; c < PB; ++c) {
+                const int s = g0 + st + 2 * c + half;
+                const bool fresh = s >= s0 && s < s1;
+                const long long tok = fresh ? t_of + s : 0;
+                const long long slot_at = page_at + s * p.tok_stride + 8 * i;
 #pragma unroll
-            for (int h = 0; h < HC; ++h) {
-                if (h >= hn) continue;
-                if (a.rot) {
-                    const uint4 y = rotate<T>(a, xk[h], w, i);
-                    if (fresh) xk[h] = y;
-                }
-                if (fresh && id >= 0) {
-                    const long long at = slot_at + (h0 + h) * p.head_stride;
-                    *reinterpret_cast<uint4 *>(kc + at) = xk[h];
-                    *reinterpret_cast<uint4 *>(vc + at) = xv[h];
-                }
-                if (mean) add8<T>(acc[h], xk[h]);  // neither fresh nor old: cannot be, s1 == page
-            }
-            if (q) {
-                const int qn = hn * p.G, q0 = h0 * p.G;
-                for (int c = 0; c < qn; c += 4) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        x[e] = fresh && c + e < qn
-                                   ? __ldg(reinterpret_cast<const uint4 *>(q + tok * a.qs + (q0 + c + e) * kD + 8 * i))
-                                   : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (a.rot) x[e] = rotate<T>(a, x[e], w, i);
-                        if (fresh && c + e < qn)
-                            *reinterpret_cast<uint4 *>(qo + (tok * p.Hq + q0 + c + e) * kD + 8 * i) = x[e];
+                for (int h = 0; h < HC; ++h) {
+                    xk[c][h] = xv[c][h] = make_uint4(0, 0, 0, 0);
+                    if (fresh && h < hn) {
+                        xk[c][h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
+                        xv[c][h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
+                    } else if (mean && s < s0 && h < hn) {  // written by an earlier call
+                        xk[c][h] = *reinterpret_cast<const uint4 *>(kc + slot_at + (h0 + h) * p.head_stride);
                     }
+                }
+                if (fresh && 8 * i < a.rot) {
+                    const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                    load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < PB; ++c) {
+                const int s = g0 + st + 2 * c + half;
+                const bool fresh = s >= s0 && s < s1;
+                const long long slot_at = page_at + s * p.tok_stride + 8 * i;
+#pragma unroll
+                for (int h = 0; h < HC; ++h) {
+                    if (a.rot) {
+                        const uint4 y = rotate<T>(a, xk[c][h], w[c], i);
+                        if (fresh) xk[c][h] = y;
+                    }
+                    if (fresh && id >= 0 && h < hn) {
+                        const long long at = slot_at + (h0 + h) * p.head_stride;
+                        *reinterpret_cast<uint4 *>(kc + at) = xk[c][h];
+                        *reinterpret_cast<uint4 *>(vc + at) = xv[c][h];
+                    }
+                    if (mean) add8<T>(acc[h], xk[c][h]);  // every slot below s1 == page is new or old
                 }
             }
         }
@@ -259,13 +294,15 @@ __global__ void k_paged_append(AppendArgs a) {
     }
 }
 
-template <typename T, int HC> cudaError_t launch_append(const AppendArgs &a, cudaStream_t s) {
+template <typename T, int HC, int PB> cudaError_t launch_append(AppendArgs &a, cudaStream_t s) {
     const int groups = a.p.page / kGroup;
     const int warps = groups > 4 ? groups : 4, per_cta = warps / groups;
-    const dim3 grid((unsigned)((a.units + per_cta - 1) / per_cta), (unsigned)((a.p.Hkv + HC - 1) / HC));
+    a.kv_chunks = (a.p.Hkv + HC - 1) / HC;
+    a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
+    const long long ctas = (a.units + per_cta - 1) / per_cta * a.chunks;
+    if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const size_t smem = a.mean ? sizeof(float) * warps * HC * kD : 0;
-    k_paged_append<T, HC><<<grid, 32 * warps, smem, s>>>(a);
-    return cudaGetLastError();
+    return launch_paged(k_paged_append<T, HC, PB>, dim3((unsigned)ctas), 32 * warps, smem, 1, a, s);
 }
 
 }  // namespace
@@ -311,11 +348,15 @@ extern "C" vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const 
     a.vc = v_cache;
     a.mean = k_mean;
     a.units = cu_seqlens ? (long long)T / a.p.page + 2LL * a.p.B : a.p.B;
-    if (a.p.Hkv > 65535 || a.units > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
+    if (a.units * (a.p.Hkv + a.p.Hq) > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;  // more CTAs than a grid holds
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("paged_append", s);
     const bool bf = a.p.dtype == T_BF16;
-    const cudaError_t e = bf ? launch_append<__nv_bfloat16, 1>(a, s) : launch_append<__half, 1>(a, s);
+    // Many tokens: four heads per warp, so that a token's angles serve 8 rows. Few: one head per warp and
+    // four pairs of slots at once, for the shortest chain of loads.
+    const bool wide = (long long)T * a.p.Hkv >= kWideRows;
+    const cudaError_t e = wide ? (bf ? launch_append<__nv_bfloat16, 4, 1>(a, s) : launch_append<__half, 4, 1>(a, s))
+                               : (bf ? launch_append<__nv_bfloat16, 1, 4>(a, s) : launch_append<__half, 1, 4>(a, s));
     prof_end(s);
     return status_from_cuda(e);
 }

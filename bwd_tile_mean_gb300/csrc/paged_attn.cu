@@ -5,33 +5,39 @@
 //
 // A segment is one (sequence, key/value head, chunk of up to 16 MT query
 // heads of its group); its keys, in the order of the pages attended, are
-// cut into units of 64. The units of all segments, end to end, are dealt to
-// the CTAs in equal contiguous runs, whatever the lengths of the batch: a
-// CTA finds its run with one scan of the lengths and walks the segments it
-// covers. A segment inside one CTA's run is finished there; the pieces of a
-// segment that crosses runs go to the workspace (at most two per CTA) and
-// k_paged_join adds them in ascending order.
+// cut into blocks of 16. The blocks of all segments, end to end, are dealt
+// to the grid's warps in equal contiguous runs, whatever the lengths of the
+// batch: a CTA finds its run with one scan of the lengths, and each warp
+// walks the segments of its own part of it. A segment inside one warp's run
+// is finished there. Where a CTA's whole run lies in one segment its warps'
+// results are joined in shared memory first; the remaining pieces of
+// segments that cross runs go to the workspace (at most two per warp) and
+// k_paged_join adds them in ascending order. When the table allows only
+// short sequences (kAlignedKeys) each segment gets a CTA of its own and
+// there is nothing left to join: one launch.
 //
-// In a run each of the CTA's four warps takes every fourth block of 16 keys
-// through its own ring of asynchronous copies (16 K rows and 16 V rows of
-// 256 bytes per stage, swizzled so that ldmatrix reads hit distinct banks;
-// rows past a page's valid slots are filled with zeros, so whatever the
-// cache holds there cannot reach the sums) and keeps its own running
-// maximum, sum and output in registers: no warp waits for another inside a
-// segment. The products run on m16n8k16 tensor instructions with the
-// group's query heads as rows. At one query token per sequence the kernel
-// reads 512 bytes per 512 G multiply-adds, far to the memory side of the
-// tensor cores' balance, so the instruction's rate does not bound it; the
-// memory pipe does, and its loads in flight.
+// A warp takes its blocks through its own ring of asynchronous copies (16 K
+// rows and 16 V rows of 256 bytes per stage, swizzled so that ldmatrix reads
+// hit distinct banks; rows past a page's valid slots are filled with zeros,
+// so whatever the cache holds there cannot reach the sums) and keeps its own
+// running maximum, sum and output in registers: no warp waits for another
+// while it streams. The products run on m16n8k16 tensor instructions with
+// the group's query heads as rows. At one query token per sequence the
+// kernel reads 512 bytes per 256 G multiply-adds, far to the memory side of
+// the tensor cores' balance, so the instruction's rate does not bound it;
+// the memory pipe does, and the loads in flight on it.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
 
 namespace vsa {
 namespace {
 
-constexpr int kUnit = 64;       // keys per scheduling unit
-constexpr int kMinUnits = 2;    // fewest units a CTA takes when there is little work
 constexpr int kBlk = 16;        // keys per warp step
+constexpr int kLead = 1;        // blocks a segment counts for beyond its own (its start-up time)
+constexpr int kMinBlocks = 4;   // fewest blocks a warp's run has when there is little work
+constexpr int kAlignedKeys = 1024;  // up to this many keys a segment is one CTA's
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // ring stages per warp
 constexpr int kCtas = 304;      // two per SM on 152 SMs
@@ -50,9 +56,11 @@ struct AttnArgs {
     void *out;
     float *lse;
     int rc, rows;          // chunks of a group's heads, rows per chunk
-    int2 *seg;             // [segments] first and last CTA
-    float2 *ml;            // [2 * kCtas, rows]
-    float *o;              // [2 * kCtas, rows, 128]
+    int aligned;           // one CTA per segment, nothing to join
+    int lead;              // kLead, 0 when aligned
+    int4 *seg;             // [segments] its pieces: first warp, warps before / CTAs joined / pieces in all
+    float2 *ml;            // [2 * kCtas * kWarps, rows]
+    float *o;              // [2 * kCtas * kWarps, rows, 128]
 };
 
 // Keys of segment list entry n ((b) without page lists, (b, h) with): the
@@ -100,11 +108,17 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Units of all list entries before this CTA's run, found by the whole CTA.
+// Blocks of a segment, its lead in front of its own counted in.
+__device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) {
+    const int nb = (seg_keys(a, n) + kBlk - 1) / kBlk;
+    return nb > 0 ? nb + a.lead : 0;
+}
+
+// A CTA's run of blocks, and the list entry where it begins.
 struct Run {
-    long long x0, x1, per;  // this CTA's units and the units per CTA
-    int n;                  // list entry that holds x0
-    long long before;       // units of the entries before n
+    long long x0, x1, total, per;  // this CTA's blocks, all blocks, blocks per warp
+    int n;                         // list entry that holds x0
+    long long before;              // blocks of the entries before n
 };
 __device__ __forceinline__ Run find_run(const AttnArgs &a) {
     __shared__ long long s_warp[kWarps];
@@ -113,11 +127,9 @@ __device__ __forceinline__ Run find_run(const AttnArgs &a) {
     const int N = a.idx ? a.p.B * a.p.Hkv : a.p.B;
     const int mult = a.idx ? a.rc : a.p.Hkv * a.rc;  // segments per entry
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    auto units_of = [&](int n) -> long long {
-        return n < N ? (long long)((seg_keys(a, n) + kUnit - 1) / kUnit) * mult : 0;
-    };
+    auto blocks_of = [&](int n) -> long long { return n < N ? (long long)seg_blocks(a, n) * mult : 0; };
     long long total = 0;
-    for (int n0 = 0; n0 < N; n0 += kWarps * 32) total += units_of(n0 + tid);
+    for (int n0 = 0; n0 < N; n0 += kWarps * 32) total += blocks_of(n0 + tid);
 #pragma unroll
     for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
     if (lane == 0) s_warp[wid] = total;
@@ -126,16 +138,17 @@ __device__ __forceinline__ Run find_run(const AttnArgs &a) {
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) total += s_warp[w];
     Run r;
-    r.per = (total + kCtas - 1) / kCtas;
-    if (r.per < kMinUnits) r.per = kMinUnits;
-    r.x0 = (long long)blockIdx.x * r.per;
-    r.x1 = r.x0 + r.per < total ? r.x0 + r.per : total;
+    r.total = total;
+    r.per = (total + kCtas * kWarps - 1) / (kCtas * kWarps);
+    if (r.per < kMinBlocks) r.per = kMinBlocks;
+    r.x0 = (long long)blockIdx.x * r.per * kWarps;
+    r.x1 = r.x0 + r.per * kWarps < total ? r.x0 + r.per * kWarps : total;
     r.n = 0;
     r.before = 0;
     if (r.x0 >= r.x1) return r;  // no work: the whole CTA leaves
     long long carry = 0;
     for (int n0 = 0; n0 < N; n0 += kWarps * 32) {
-        const long long v = units_of(n0 + tid);
+        const long long v = blocks_of(n0 + tid);
         long long inc = v;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -170,33 +183,71 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
-    const Run run = find_run(a);
-    if (run.x0 >= run.x1) return;
+    grid_wait();
+    grid_go();
+    const int N = a.idx ? p.B * p.Hkv : p.B;             // list entries
+    const int mult = a.idx ? a.rc : p.Hkv * a.rc;        // segments per entry
     const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v), *Q = static_cast<const T *>(a.q);
     const uint32_t ring = ptx::smem_addr(smem) + wid * kStages * kStageBytes;
     const float sl2 = p.scale * kLog2e;
 
-    const int N = a.idx ? p.B * p.Hkv : p.B;
+    Run run;
+    if (a.aligned) {
+        run.n = (int)blockIdx.x / mult;
+        const int nb = seg_blocks(a, run.n);
+        run.per = (nb + kWarps - 1) / kWarps;
+        run.before = 0;
+        run.x0 = (long long)(blockIdx.x % mult) * nb;
+        run.x1 = run.x0 + nb;
+        run.total = 0;
+    } else {
+        run = find_run(a);
+        if (run.x0 >= run.x1) return;
+    }
+    // the CTA's run lies in one segment: its warps' results are joined
+    bool joined = a.aligned;
+    if (!a.aligned) {
+        const int nb = seg_blocks(a, run.n);
+        joined = (run.x0 - run.before) / nb == (run.x1 - 1 - run.before) / nb && run.x1 <= run.before + (long long)nb * mult;
+    }
+    long long x = min(run.x0 + wid * run.per, run.x1);
+    const long long x_end = min(x + run.per, run.x1);
     int n = run.n;
     long long before = run.before;
-    for (long long x = run.x0; x < run.x1 && n < N;) {
-        const int keys = seg_keys(a, n);
-        const int units = (keys + kUnit - 1) / kUnit;
-        const long long entry = (long long)units * (a.idx ? a.rc : p.Hkv * a.rc);
-        if (x >= before + entry) {  // also passes over entries without keys
-            before += entry;
-            ++n;
+    bool more = joined || x < x_end;  // a joined CTA's warp without blocks still brings its empty part
+    while (more) {
+        int nb = n < N ? seg_blocks(a, n) : 0;
+        if (!joined && x >= before + (long long)nb * mult) {  // also passes over entries without keys
+            before += (long long)nb * mult;
+            if (++n >= N) break;
             continue;
         }
-        const int sub = (int)((x - before) / units), off = (int)((x - before) % units);
-        const int take = (int)min((long long)(units - off), run.x1 - x);
-        const bool first = off == 0, last = off + take == units;
+        long long seg0;   // first block of the segment
+        int sub, off, take;
+        if (joined) {     // the segment is the run's, also for a warp without blocks
+            sub = a.aligned ? (int)blockIdx.x % mult : (int)((run.x0 - before) / nb);
+            seg0 = before + (long long)sub * nb;
+            off = (int)(x - seg0);
+            take = (int)(x_end - x);
+        } else {
+            sub = (int)((x - before) / nb);
+            seg0 = before + (long long)sub * nb;
+            off = (int)(x - seg0);
+            take = (int)min((long long)(nb - off), x_end - x);
+        }
+        const bool first = joined ? run.x0 == seg0 : off == 0;
+        const bool last = joined ? run.x1 == seg0 + nb : off + take == nb;
+        x += take;
+        {   // the piece's own blocks: those behind the lead
+            const int skip = clampi(a.lead - off, 0, take);
+            off += skip - a.lead;
+            take -= skip;
+        }
         const int r = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
         const int b = bh / p.Hkv, h = bh % p.Hkv;
         const int rows = min(a.rows, p.G - r * a.rows);
         const int len = paged_len(p, b);
-        const int key0 = off * kUnit, key1 = min(keys, (off + take) * kUnit);
-        const int nblk = (key1 - key0 + kBlk - 1) / kBlk;
+        const int key0 = off * kBlk;
         const long long hoff = (long long)h * p.head_stride;
 
         // Q as A fragments: row g (and g + 8) of each 16-row tile, 8 k-steps
@@ -217,17 +268,15 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
                 }
         }
 
-        const int mine = nblk > wid ? (nblk - wid + kWarps - 1) / kWarps : 0;  // this warp's blocks
-
-        // Window of up to 32 of this warp's blocks, one per lane: the page
-        // (or -1) and the valid slots of the block.
+        // Window of up to 32 blocks, one per lane: the page (or -1), the
+        // slot in it and the valid slots of the block.
         int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
         auto window = [&](int i0) {
             w_base = i0;
             w_id = -1;
             w_valid = 0;
-            if (i0 + lane < mine) {
-                const int pos = key0 + ((i0 + lane) * kWarps + wid) * kBlk;
+            if (i0 + lane < take) {
+                const int pos = key0 + (i0 + lane) * kBlk;
                 int j = pos >> p.page_log2;
                 w_slot = pos & (p.page - 1);
                 if (a.idx) j = __ldg(a.idx + (long long)bh * a.cap + j);
@@ -236,7 +285,7 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
             }
         };
         int valid[kStages];
-        auto issue = [&](int i, int stage) {  // block i of this warp into a stage
+        auto issue = [&](int i, int stage) {  // block i of this piece into a stage
             if (i >= w_base + 32) window(i);
             const int id = __shfl_sync(0xffffffffu, w_id, i - w_base);
             const int slot = __shfl_sync(0xffffffffu, w_slot, i - w_base);
@@ -258,7 +307,7 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
 #pragma unroll
         for (int s = 0; s < kStages - 1; ++s) {
             valid[s] = 0;
-            if (s < mine) valid[s] = issue(s, s);
+            if (s < take) valid[s] = issue(s, s);
             cp_commit();
         }
         valid[kStages - 1] = 0;
@@ -273,14 +322,14 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
         }
-        for (int i0 = 0; i0 < mine; i0 += kStages) {
+        for (int i0 = 0; i0 < take; i0 += kStages) {
 #pragma unroll
             for (int s = 0; s < kStages; ++s) {
                 const int i = i0 + s;
-                if (i >= mine) break;
+                if (i >= take) break;
                 cp_wait<kStages - 2>();
                 __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
-                if (i + kStages - 1 < mine)
+                if (i + kStages - 1 < take)
                     valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
                 cp_commit();
                 const uint32_t st = ring + s * kStageBytes;
@@ -369,59 +418,103 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
             }
         }
         cp_wait<0>();
-        __syncwarp();  // the warp's ring is free: it takes the warp's outputs
-        float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
+        __syncwarp();  // the warp's ring is free
 #pragma unroll
         for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float l = l_run[m][e];
-                l += __shfl_xor_sync(0xffffffffu, l, 1);
-                l += __shfl_xor_sync(0xffffffffu, l, 2);
-                const int row = m * 16 + g + 8 * e;
-                if (t == 0) {
-                    s_m[wid][row] = m_run[m][e];
-                    s_l[wid][row] = l;
+                l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 1);
+                l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 2);
+            }
+        const long long hq0 = (long long)b * p.Hq + h * p.G + r * a.rows;  // first output row of the segment
+
+        // A piece of the segment that begins it describes all of its pieces.
+        const int gw = (int)blockIdx.x * kWarps + (joined ? 0 : wid);
+        const long long slot = 2LL * gw + (first ? 1 : 0);
+        if (!a.aligned && first && lane == 0 && (!joined || wid == 0)) {
+            const long long s1 = seg0 + nb, cta = run.per * kWarps;
+            const int w_last = (int)((s1 - 1) / run.per);
+            const int ca = (int)((seg0 + cta - 1) / cta);
+            const int cb = (int)(s1 == run.total ? (s1 + cta - 1) / cta : s1 / cta);
+            const int w0 = (int)(seg0 / run.per);
+            int4 d = make_int4(w0, w_last + 1 - w0, 0, w_last + 1 - w0);
+            if (cb > ca) {
+                d.y = ca * kWarps - w0;
+                d.z = cb - ca;
+                d.w = d.y + d.z + max(0, w_last + 1 - cb * kWarps);
+            }
+            a.seg[(long long)bh * a.rc + r] = d;
+        }
+
+        if (joined) {  // the warps' outputs in shared memory, one thread per dim
+            float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int row = m * 16 + g + 8 * e;
+                    if (t == 0) {
+                        s_m[wid][row] = m_run[m][e];
+                        s_l[wid][row] = l_run[m][e];
+                    }
+                    if (row < rows)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
+                                make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
                 }
-                if (row < rows)
+            __syncthreads();
+            for (int row = 0; row < rows; ++row) {
+                float M = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
+                const float ref = M == -INFINITY ? 0.f : M;
+                float l = 0.f, o = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = ptx::ex2(s_m[w][row] - ref);
+                    l += f * s_l[w][row];
+                    o += f * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
+                }
+                if (first && last) {
+                    static_cast<T *>(a.out)[(hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
+                    if (tid == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+                } else {
+                    a.o[(slot * a.rows + row) * kD + tid] = o;
+                    if (tid == 0) a.ml[slot * a.rows + row] = make_float2(M, l);
+                }
+            }
+            return;
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int row = m * 16 + g + 8 * e;
+                if (row >= rows) continue;
+                const float l = l_run[m][e];
+                if (first && last) {
+                    const float inv = l == 0.f ? 0.f : 1.f / l;
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (hq0 + row) * kD);
 #pragma unroll
                     for (int j = 0; j < 16; ++j)
-                        *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
+                        dst[4 * j + t] = pack2<T>(acc[m][j][2 * e] * inv, acc[m][j][2 * e + 1] * inv);
+                    if (t == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (m_run[m][e] + log2f(l));
+                } else {
+                    float *dst = a.o + (slot * a.rows + row) * kD;
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t) =
                             make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
+                    if (t == 0) a.ml[slot * a.rows + row] = make_float2(m_run[m][e], l);
+                }
             }
-        __syncthreads();
-        const bool whole = first && last;
-        const int slot = 2 * (int)blockIdx.x + (first ? 1 : 0);
-        for (int row = 0; row < rows; ++row) {
-            float M = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
-            const float ref = M == -INFINITY ? 0.f : M;
-            float l = 0.f, o = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ptx::ex2(s_m[w][row] - ref);
-                l += f * s_l[w][row];
-                o += f * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
-            }
-            if (whole) {
-                const long long hq = (long long)b * p.Hq + h * p.G + r * a.rows + row;
-                static_cast<T *>(a.out)[hq * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
-                if (tid == 0) a.lse[hq] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
-            } else {
-                a.o[((long long)slot * a.rows + row) * kD + tid] = o;
-                if (tid == 0) a.ml[(long long)slot * a.rows + row] = make_float2(M, l);
-            }
-        }
-        if (first && tid == 0)
-            a.seg[(long long)bh * a.rc + r] = make_int2((int)blockIdx.x, (int)((x - off + units - 1) / run.per));
-        __syncthreads();  // the ring is written again by the next segment
-        x += take;
+        more = x < x_end;
     }
 }
 
 // One CTA per (sequence, query head): writes the rows without keys and
-// joins the pieces of the segments that crossed CTAs, in ascending order of
+// joins the pieces of the segments that crossed runs, in ascending order of
 // their keys within each warp, then the warps in order.
 template <typename T> __global__ void __launch_bounds__(128) k_paged_join(AttnArgs a) {
     __shared__ float s_m[4], s_l[4];
@@ -431,18 +524,23 @@ template <typename T> __global__ void __launch_bounds__(128) k_paged_join(AttnAr
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int bh = b * p.Hkv + h;
     T *out = static_cast<T *>(a.out) + (long long)row * kD;
+    grid_wait();
+    grid_go();
     if (seg_keys(a, a.idx ? bh : b) == 0) {
         out[tid] = from_f<T>(0.f);
         if (tid == 0) a.lse[row] = -INFINITY;
         return;
     }
-    const int2 sg = a.seg[(long long)bh * a.rc + in / a.rows];
-    if (sg.x == sg.y) return;  // finished by its CTA
-    const int r = in % a.rows, pieces = sg.y - sg.x + 1;
+    const int4 sg = a.seg[(long long)bh * a.rc + in / a.rows];
+    if (sg.w == 1) return;  // finished where it was computed
+    const int r = in % a.rows;
     float M = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = wid; i < pieces; i += 4) {
-        const long long at = (long long)(2 * (sg.x + i) + (i == 0 ? 1 : 0)) * a.rows + r;
+    for (int i = wid; i < sg.w; i += 4) {
+        // warps before the first joined CTA, joined CTAs (at their first warp's place), warps after
+        const int w = i < sg.y ? sg.x + i : (i < sg.y + sg.z ? sg.x + sg.y + (i - sg.y) * kWarps
+                                                            : sg.x + i + sg.z * (kWarps - 1));
+        const long long at = (2LL * w + (i == 0 ? 1 : 0)) * a.rows + r;
         const float2 ml = a.ml[at];
         const float4 x = *reinterpret_cast<const float4 *>(a.o + at * kD + 4 * lane);
         const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn;
@@ -481,18 +579,16 @@ template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) 
     const void *fn = one ? (const void *)k_paged_attn<T, 1> : (const void *)k_paged_attn<T, 2>;
     const cudaError_t ae = ensure_smem_limit(fn, kSmem);
     if (ae != cudaSuccess) return status_from_cuda(ae);
+    const unsigned grid = a.aligned ? (unsigned)(a.p.B * a.p.Hkv * a.rc) : kCtas;
     prof_begin("paged_attn", s);
-    if (one)
-        k_paged_attn<T, 1><<<kCtas, kWarps * 32, kSmem, s>>>(a);
-    else
-        k_paged_attn<T, 2><<<kCtas, kWarps * 32, kSmem, s>>>(a);
+    cudaError_t e = one ? launch_paged(k_paged_attn<T, 1>, grid, kWarps * 32, kSmem, 1, a, s)
+                        : launch_paged(k_paged_attn<T, 2>, grid, kWarps * 32, kSmem, 1, a, s);
     prof_end(s);
-    const vsa_status st = status_from_cuda(cudaGetLastError());
-    if (st != VSA_OK) return st;
+    if (e != cudaSuccess || a.aligned) return status_from_cuda(e);
     prof_begin("paged_join", s);
-    k_paged_join<T><<<(unsigned)(a.p.B * a.p.Hq), 128, 0, s>>>(a);
+    e = launch_paged(k_paged_join<T>, dim3((unsigned)(a.p.B * a.p.Hq)), 128, 0, 1, a, s);
     prof_end(s);
-    return status_from_cuda(cudaGetLastError());
+    return status_from_cuda(e);
 }
 
 }  // namespace
@@ -506,10 +602,9 @@ PagedWs paged_ws(const Paged &p) {
         return o;
     };
     const size_t rows = rows_of(p.G), rc = (p.G + rows - 1) / rows;
-    w.keys = take(sizeof(uint32_t) * p.B * (size_t)p.Hkv * p.max_pages);
-    w.seg = take(sizeof(int2) * p.B * (size_t)p.Hkv * rc);
-    w.ml = take(sizeof(float2) * 2 * kCtas * rows);
-    w.o = take(sizeof(float) * 2 * kCtas * rows * kD);
+    w.seg = take(sizeof(int4) * p.B * (size_t)p.Hkv * rc);
+    w.ml = take(sizeof(float2) * 2 * kCtas * kWarps * rows);
+    w.o = take(sizeof(float) * 2 * kCtas * kWarps * rows * kD);
     w.total = at;
     return w;
 }
@@ -548,8 +643,11 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.lse = lse;
     a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
+    const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
+    a.aligned = most <= kAlignedKeys;
+    a.lead = a.aligned ? 0 : kLead;
     char *w = static_cast<char *>(workspace);
-    a.seg = reinterpret_cast<int2 *>(w + ws.seg);
+    a.seg = reinterpret_cast<int4 *>(w + ws.seg);
     a.ml = reinterpret_cast<float2 *>(w + ws.ml);
     a.o = reinterpret_cast<float *>(w + ws.o);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

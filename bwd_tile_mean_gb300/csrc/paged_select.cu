@@ -1,14 +1,21 @@
 // paged_select.cu -- the pages each key/value head attends to, by the score
 // of their mean key against the group's query (vsa_page_select).
 //
-// Two launches: k_page_scores reads each full page's fp32 mean once (8 lanes
-// per page, 16 bytes per load) and writes an order-preserving 32-bit key per
-// page; k_page_topk finds, per row, the topk-th largest key 8 bits at a time
-// (a 256-bin histogram per digit) and lists every key above it plus the
-// lowest-indexed ties, ascending.
+// One launch. A cluster of 8 CTAs has one sequence and up to 8 key/value
+// heads; the pages that compete (all but the first keep_first and the last
+// keep_last) are cut into 8 runs, one per CTA. A CTA reads the fp32 means of
+// its run once (8 lanes per page, 16 bytes per load; the heads of a page are
+// neighbours in memory) and leaves an order-preserving 32-bit key per page
+// and head in its shared memory. Then each CTA finishes one head: it reads
+// the 8 CTAs' keys through the cluster's distributed shared memory and finds
+// the last page to take under (key desc, page asc), 11 bits of (key, page)
+// at a time from the top (a 2,048-bin histogram), until the bin that holds
+// it is small enough to rank outright; then lists the taken pages in order.
+// The scores never leave the SMs.
 #include <algorithm>
 
 #include "paged.cuh"
+#include "sm103_ptx.cuh"
 
 namespace vsa {
 namespace {
@@ -20,13 +27,19 @@ struct SelectArgs {
     const float *mean;
     int topk, first, last;
     int *idx, *cnt;
-    uint32_t *keys;  // [B * Hkv, max_pages]
+    int hg, hgroups;  // heads per cluster, clusters per sequence
+    int cap;          // pages per CTA at most
 };
 
-constexpr int kChunk = 128;  // pages per CTA of the scoring pass
+constexpr int kCluster = 8;
+constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
+constexpr int kItems = 4;    // groups of four pages a warp has in flight
+constexpr int kBins = 2048;
+constexpr int kRank = 256;   // a bin of up to this many pages is ranked outright
+constexpr int kIndexBits = 22;
+constexpr int kMaxSmem = 200 * 1024;  // dynamic, beside the bins and the list
 
-// Larger score, larger key; -0 folded into +0, NaN counted as -inf. No key
-// reaches 0xFFFFFFFF, which marks the pages that are always chosen.
+// Larger score, larger key; -0 folded into +0, NaN counted as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) x = -INFINITY;
     if (x == 0.f) x = 0.f;
@@ -34,143 +47,210 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-template <typename T> __global__ void __launch_bounds__(256) k_page_scores(SelectArgs a) {
-    const Paged &p = a.p;
-    const int row = blockIdx.x, b = row / p.Hkv, h = row % p.Hkv;
-    const int len = paged_len(p, b), full = len >> p.page_log2, pages = (len + p.page - 1) >> p.page_log2;
-    if (pages <= a.topk) return;  // every page is chosen
-    const int lane = threadIdx.x & 31, sub = lane >> 3, j = lane & 7;
-    // lane j of 8 holds dims 32 i + 4 j + c of the group's summed query
-    float g[4][4];
-    const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h * p.G * kD;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) g[i][c] = 0.f;
-    if (p.G == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) g[i][c] = to_f<T>(q[32 * i + 4 * j + c]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                double sum = 0.0;  // exact for any group of 16-bit values of like size: the order does not matter
-                for (int m = 0; m < p.G; ++m) sum += (double)to_f<T>(q[(long long)m * kD + 32 * i + 4 * j + c]);
-                g[i][c] = (float)sum;
-            }
+__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// Sum of the group's 16-bit queries at one dim: the fp32 running sum with
+// its rounding errors kept aside (each found exactly), added at the end.
+template <typename T> __device__ __forceinline__ float group_sum(const T *q, int G) {
+    float s = to_f<T>(q[0]), err = 0.f;
+    for (int m = 1; m < G; ++m) {
+        const float x = to_f<T>(q[(long long)m * kD]);
+        const float t = __fadd_rn(s, x), y = __fsub_rn(t, s);
+        err = __fadd_rn(err, __fadd_rn(__fsub_rn(s, __fsub_rn(t, y)), __fsub_rn(x, y)));
+        s = t;
     }
-    uint32_t *keys = a.keys + (long long)row * p.max_pages;
-    for (int c0 = blockIdx.y * kChunk; c0 < pages; c0 += gridDim.y * kChunk) {
-        const int end = min(pages, c0 + kChunk);
-        for (int n = c0 + (int)(threadIdx.x >> 5) * 4; n < end; n += 32) {
-            const int pg = n + sub;
-            const bool kept = pg < a.first || pg >= pages - a.last || pg >= full;
-            const int id = pg < end && !kept ? paged_id(p, b, pg) : -1;
+    return isfinite(s) ? __fadd_rn(s, err) : s;
+}
+
+// (key, page) as one number, the larger the better: 32 key bits, then the
+// page counted from the end.
+__device__ __forceinline__ uint64_t rank_of(uint32_t key, int c) {
+    return ((uint64_t)key << kIndexBits) | (uint32_t)((1 << kIndexBits) - 1 - c);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(SelectArgs a) {
+    extern __shared__ __align__(16) unsigned char sm[];
+    __shared__ int hist[kBins];
+    __shared__ int wsum[kWarpsSel];
+    __shared__ int s_bin, s_above, s_in, s_fill;
+    __shared__ uint64_t s_cut;
+    __shared__ uint64_t list[kRank];
+    float *sq = reinterpret_cast<float *>(sm);                       // [hg][128] summed queries
+    uint32_t *keys = reinterpret_cast<uint32_t *>(sq + a.hg * kD);   // [hg][cap] keys of this CTA's run
+    int *ids = reinterpret_cast<int *>(keys + (size_t)a.hg * a.cap); // [cap] page ids of the run
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int rank = (int)ptx::cluster_rank(), cl = (int)blockIdx.x / kCluster;
+    const int b = cl / a.hgroups, h0 = (cl % a.hgroups) * a.hg, hn = min(a.hg, p.Hkv - h0);
+    grid_wait();
+    grid_go();
+    const int len = paged_len(p, b), pages = (len + p.page - 1) >> p.page_log2;
+    if (pages <= a.topk) {  // all of them: the same for every CTA of the cluster
+        for (int hh = rank; hh < hn; hh += kCluster) {
+            const long long row = (long long)b * p.Hkv + h0 + hh;
+            for (int n = tid; n < a.topk; n += kThreads) a.idx[row * a.topk + n] = n < pages ? n : -1;
+            if (tid == 0) a.cnt[row] = pages;
+        }
+        return;
+    }
+    // Competing pages c = j - first, 0 <= c < comp: every one is full, since the partial page is the last.
+    const int comp = pages - a.first - a.last, take = a.topk - a.first - a.last;
+    const int run = (comp + kCluster - 1) / kCluster;
+    const int c0 = min(rank * run, comp), nc = min(run, comp - c0);
+
+    for (int c = tid; c < nc; c += kThreads) ids[c] = paged_id(p, b, a.first + c0 + c);
+    const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h0 * p.G * kD;
+    for (int e = tid; e < hn * kD; e += kThreads)
+        sq[e] = group_sum<T>(q + (long long)(e / kD) * p.G * kD + e % kD, p.G);
+    __syncthreads();
+
+    // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
+    const int sub = lane >> 3, j = lane & 7, items = (nc + 3) / 4 * hn;
+    for (int it0 = wid; it0 < items; it0 += kWarpsSel * kItems) {
+        float4 m[kItems][4];
+#pragma unroll
+        for (int e = 0; e < kItems; ++e) {
+            const int it = it0 + e * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
+            const int id = it < items && c < nc ? ids[c] : -1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                m[e][i] = id >= 0 ? __ldg(reinterpret_cast<const float4 *>(
+                                        a.mean + ((long long)id * p.Hkv + h0 + hh) * kD + 32 * i + 4 * j))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int e = 0; e < kItems; ++e) {
+            const int it = it0 + e * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
             float x[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float4 m = id >= 0 ? __ldg(reinterpret_cast<const float4 *>(
-                                               a.mean + ((long long)id * p.Hkv + h) * kD + 32 * i + 4 * j))
-                                         : make_float4(0.f, 0.f, 0.f, 0.f);
-                x[i][0] = __fmul_rn(g[i][0], m.x);
-                x[i][1] = __fmul_rn(g[i][1], m.y);
-                x[i][2] = __fmul_rn(g[i][2], m.z);
-                x[i][3] = __fmul_rn(g[i][3], m.w);
+                const float4 g = *reinterpret_cast<const float4 *>(sq + hh * kD + 32 * i + 4 * j);
+                x[i][0] = __fmul_rn(g.x, m[e][i].x);
+                x[i][1] = __fmul_rn(g.y, m[e][i].y);
+                x[i][2] = __fmul_rn(g.z, m[e][i].z);
+                x[i][3] = __fmul_rn(g.w, m[e][i].w);
             }
             // 128 -> 64 -> 32: dims 64 and 32 apart; then neighbours
             float y[4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                y[c] = __fadd_rn(__fadd_rn(x[0][c], x[2][c]), __fadd_rn(x[1][c], x[3][c]));
+            for (int d = 0; d < 4; ++d)
+                y[d] = __fadd_rn(__fadd_rn(x[0][d], x[2][d]), __fadd_rn(x[1][d], x[3][d]));
             float r = __fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3]));
             r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
             r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 2));
             r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 4));
-            if (j == 0 && pg < end)
-                keys[pg] = kept ? 0xFFFFFFFFu : (id >= 0 ? order_key(r) : order_key(-INFINITY));
+            if (j == 0 && it < items && c < nc) keys[hh * a.cap + c] = order_key(ids[c] >= 0 ? r : -INFINITY);
         }
     }
-}
+    ptx::cluster_sync();  // every run's keys are there
 
-__global__ void __launch_bounds__(256) k_page_topk(SelectArgs a) {
-    const Paged &p = a.p;
-    const int row = blockIdx.x, b = row / p.Hkv, tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int len = paged_len(p, b), pages = (len + p.page - 1) >> p.page_log2;
-    int *idx = a.idx + (long long)row * a.topk;
-    const int take = min(a.topk, pages);
-    if (tid == 0) a.cnt[row] = take;
-    for (int n = take + tid; n < a.topk; n += 256) idx[n] = -1;
-    if (pages <= a.topk) {
-        for (int n = tid; n < pages; n += 256) idx[n] = n;
-        return;
-    }
-    __shared__ int hist[256];
-    __shared__ int s_digit, s_above;
-    __shared__ int wtot[8], wtie[8];
-    const uint32_t *keys = a.keys + (long long)row * p.max_pages;
-    uint32_t prefix = 0u, known = 0u;
-    int rem = take;
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        hist[tid] = 0;
-        __syncthreads();
-        for (int n = tid; n < pages; n += 256) {
-            const uint32_t key = keys[n];
-            if ((key & known) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1);
-        }
-        __syncthreads();
-        if (wid == 0) {  // lane l: digits 255 - 8 l down to 248 - 8 l
-            int c[8], sum = 0;
+    for (int hh = rank; hh < hn; hh += kCluster) {
+        const long long row = (long long)b * p.Hkv + h0 + hh;
+        int *idx = a.idx + row * a.topk;
+        const uint32_t base = ptx::smem_addr(keys + (size_t)hh * a.cap);
+        // f(c, rank_of(key, c)) over this thread's share of the competing pages
+        auto each = [&](auto f) {
+            for (int r = 0; r < kCluster; ++r) {
+                const uint32_t at = ptx::cluster_addr(base, r);
+                const int n = min(run, comp - r * run);
+#pragma unroll 4
+                for (int c = tid; c < n; c += kThreads) f(r * run + c, rank_of(ld_cluster(at + 4 * c), r * run + c));
+            }
+        };
+        // cut: the `take`-th largest rank (ranks are distinct); 2^54 when none is taken
+        uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
+        int rem = take, top = 32 + kIndexBits;  // bits [top, 54) of the cut are `prefix`
+        while (rem > 0) {
+            const int shift = max(top - 11, 0), bits = top - shift;
+            for (int e = tid; e < kBins; e += kThreads) hist[e] = 0;
+            __syncthreads();
+            each([&](int, uint64_t k) {
+                if (k >> top == prefix) atomicAdd(&hist[(int)((k >> shift) & ((1u << bits) - 1u))], 1);
+            });
+            __syncthreads();
+            // thread t: bins 2047 - 8 t down to 2040 - 8 t
+            int cnt[kBins / kThreads], sum = 0;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) sum += c[u] = hist[255 - 8 * lane - u];
+            for (int e = 0; e < kBins / kThreads; ++e) sum += cnt[e] = hist[kBins - 1 - tid * (kBins / kThreads) - e];
             int inc = sum;
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1) {
                 const int y = __shfl_up_sync(0xffffffffu, inc, off);
                 if (lane >= off) inc += y;
             }
-            int above = inc - sum;  // keys with a larger digit
+            if (lane == 31) wsum[wid] = inc;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kWarpsSel; ++w) inc += w < wid ? wsum[w] : 0;
+            int above = inc - sum;  // pages in larger bins
             if (above < rem && inc >= rem) {
-                int u = 0;
-                while (above + c[u] < rem) above += c[u++];
-                s_digit = 255 - 8 * lane - u;
-                s_above = above;
+#pragma unroll
+                for (int e = 0; e < kBins / kThreads; ++e)
+                    if (above < rem) {
+                        s_bin = kBins - 1 - tid * (kBins / kThreads) - e;
+                        s_above = above;
+                        s_in = cnt[e];
+                        above += cnt[e];
+                    }
             }
+            if (tid == 0) s_fill = 0;
+            __syncthreads();
+            prefix = (prefix << bits) | (uint32_t)s_bin;
+            top = shift;
+            rem -= s_above;
+            const int in = s_in;
+            if (in == rem) {  // the whole bin
+                cut = prefix << top;
+                break;
+            }
+            if (in <= kRank) {
+                each([&](int, uint64_t k) {
+                    if (k >> top == prefix) list[atomicAdd(&s_fill, 1)] = k;
+                });
+                __syncthreads();
+                if (tid < in) {
+                    const uint64_t k = list[tid];
+                    int larger = 0;
+                    for (int e = 0; e < in; ++e) larger += list[e] > k ? 1 : 0;
+                    if (larger == rem - 1) s_cut = k;
+                }
+                __syncthreads();
+                cut = s_cut;
+                break;
+            }
+            __syncthreads();  // s_bin and the bins are read before the next digit
         }
+        // pages at or above the cut, in order: each warp has a contiguous share
+        const int share = ((comp + kWarpsSel - 1) / kWarpsSel + 31) & ~31;
+        const int lo = min(wid * share, comp), hi = min(lo + share, comp);
+        auto chosen = [&](int c) {
+            const int r = c / run;
+            return rank_of(ld_cluster(ptx::cluster_addr(base, r) + 4 * (c - r * run)), c) >= cut;
+        };
+        int n = 0;
+        for (int c = lo + lane; c - lane < hi; c += 32) n += __popc(__ballot_sync(0xffffffffu, c < hi && chosen(c)));
+        __syncthreads();  // wsum was read
+        if (lane == 0) wsum[wid] = n;
         __syncthreads();
-        rem -= s_above;
-        prefix |= (uint32_t)s_digit << shift;
-        known |= 255u << shift;
+        int at = a.first;
+#pragma unroll
+        for (int w = 0; w < kWarpsSel; ++w) at += w < wid ? wsum[w] : 0;
+        for (int c = lo + lane; c - lane < hi; c += 32) {
+            const bool on = c < hi && chosen(c);
+            const unsigned m = __ballot_sync(0xffffffffu, on);
+            if (on) idx[at + __popc(m & ((1u << lane) - 1u))] = a.first + c;
+            at += __popc(m);
+        }
+        for (int e = tid; e < a.first; e += kThreads) idx[e] = e;
+        for (int e = tid; e < a.last; e += kThreads) idx[a.topk - a.last + e] = pages - a.last + e;
+        if (tid == 0) a.cnt[row] = a.topk;
+        __syncthreads();  // the bins and sums serve the next head
     }
-    // every key above prefix, and the first `rem` keys equal to it, in order
-    int done = 0, ties = 0;
-    for (int n0 = 0; n0 < pages; n0 += 256) {
-        const int n = n0 + tid;
-        const uint32_t key = n < pages ? keys[n] : 0u;
-        const bool tie = n < pages && key == prefix, over = n < pages && key > prefix;
-        const unsigned mt = __ballot_sync(0xffffffffu, tie), lt = (1u << lane) - 1u;
-        if (lane == 0) wtie[wid] = __popc(mt);
-        __syncthreads();
-        int before = ties, all = ties;
-        for (int w = 0; w < 8; ++w) {
-            before += w < wid ? wtie[w] : 0;
-            all += wtie[w];
-        }
-        const bool on = over || (tie && before + __popc(mt & lt) < rem);
-        const unsigned mo = __ballot_sync(0xffffffffu, on);
-        if (lane == 0) wtot[wid] = __popc(mo);
-        __syncthreads();
-        int at = done, sum = done;
-        for (int w = 0; w < 8; ++w) {
-            at += w < wid ? wtot[w] : 0;
-            sum += wtot[w];
-        }
-        if (on) idx[at + __popc(mo & lt)] = n;
-        done = sum;
-        ties = all;
-    }
+    ptx::cluster_sync();  // no CTA leaves while another reads its keys
 }
 
 }  // namespace
@@ -178,8 +258,7 @@ __global__ void __launch_bounds__(256) k_page_topk(SelectArgs a) {
 
 extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride,
                                       const float *k_mean, int topk, int keep_first, int keep_last,
-                                      int32_t *page_idx, int32_t *page_cnt, void *workspace, size_t workspace_bytes,
-                                      vsa_stream_t stream) {
+                                      int32_t *page_idx, int32_t *page_cnt, vsa_stream_t stream) {
     using namespace vsa;
     SelectArgs a{};
     const vsa_status st = to_paged(desc, &a.p, true);
@@ -188,8 +267,6 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     if (keep_first < 0 || keep_last < 1 || topk < 1 || (long long)keep_first + keep_last > topk) return VSA_ERR_SHAPE;
     if (!q || !k_mean || !page_idx || !page_cnt) return VSA_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_mean) || ((uintptr_t)page_idx | (uintptr_t)page_cnt) & 3u) return VSA_ERR_LAYOUT;
-    const PagedWs ws = paged_ws(a.p);
-    if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < ws.total) return VSA_ERR_WORKSPACE;
     a.q = q;
     a.mean = k_mean;
     a.topk = topk;
@@ -197,22 +274,25 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     a.last = keep_last;
     a.idx = page_idx;
     a.cnt = page_cnt;
-    a.keys = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + ws.keys);
+    // Heads per cluster: as many as still leave a CTA for every SM.
+    a.hg = 8;
+    while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
+        a.hg /= 2;
+    a.cap = (std::min(a.p.max_pages, 1 << kIndexBits) + kCluster - 1) / kCluster;
+    auto bytes = [&] { return sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (a.hg + 1); };
+    while (a.hg > 1 && bytes() > kMaxSmem) a.hg /= 2;
+    if (a.p.max_pages > (1 << kIndexBits) || bytes() > kMaxSmem) return VSA_ERR_UNSUPPORTED;
+    a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
+    const long long ctas = (long long)a.p.B * a.hgroups * kCluster;
+    if (ctas > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const unsigned rows = (unsigned)(a.p.B * a.p.Hkv);
-    if (a.p.max_pages > topk) {  // otherwise no row has anything to choose
-        const unsigned chunks = (unsigned)std::min((a.p.max_pages + kChunk - 1) / kChunk, 65535);
-        prof_begin("page_scores", s);
-        if (a.p.dtype == T_BF16)
-            k_page_scores<__nv_bfloat16><<<dim3(rows, chunks), 256, 0, s>>>(a);
-        else
-            k_page_scores<__half><<<dim3(rows, chunks), 256, 0, s>>>(a);
-        prof_end(s);
-        const vsa_status se = status_from_cuda(cudaGetLastError());
-        if (se != VSA_OK) return se;
-    }
-    prof_begin("page_topk", s);
-    k_page_topk<<<rows, 256, 0, s>>>(a);
+    const bool bf = a.p.dtype == T_BF16;
+    const void *fn = bf ? (const void *)k_page_select<__nv_bfloat16> : (const void *)k_page_select<__half>;
+    const cudaError_t ae = ensure_smem_limit(fn, kMaxSmem);
+    if (ae != cudaSuccess) return status_from_cuda(ae);
+    prof_begin("page_select", s);
+    const cudaError_t e = launch_paged(bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
+                                       kThreads, bytes(), kCluster, a, s);
     prof_end(s);
-    return status_from_cuda(cudaGetLastError());
+    return status_from_cuda(e);
 }

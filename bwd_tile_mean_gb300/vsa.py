@@ -154,8 +154,7 @@ def lib():
         L.vsa_paged_append.argtypes = [C.POINTER(PagedDesc), C.c_int, P, i64, P, i64, P, i64, P, P, P, P, P, C.c_int,
                                        C.c_int, C.c_int, P, P, P, P]
         L.vsa_page_select.restype = C.c_int
-        L.vsa_page_select.argtypes = [C.POINTER(PagedDesc), P, i64, P, C.c_int, C.c_int, C.c_int, P, P, P, C.c_size_t,
-                                      P]
+        L.vsa_page_select.argtypes = [C.POINTER(PagedDesc), P, i64, P, C.c_int, C.c_int, C.c_int, P, P, P]
         L.vsa_paged_attn.restype = C.c_int
         L.vsa_paged_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
         _lib = L
@@ -757,7 +756,7 @@ class PagedCache:
         if page_idx.shape[2] != topk:
             raise ValueError(f"page_idx: expected topk = {topk} entries per row")
         self._run("vsa_page_select", stream, q.data_ptr(), qs, self.k_mean.data_ptr(), int(topk), int(keep_first),
-                  int(keep_last), page_idx.data_ptr(), page_cnt.data_ptr(), *self._ws)
+                  int(keep_last), page_idx.data_ptr(), page_cnt.data_ptr())
         return page_idx, page_cnt
 
     def attend(self, q, pages=None, out=None, lse=None, stream=None):

@@ -468,4 +468,4 @@ def test_profile_names_and_launch_count():
         cache.attend(dq, pages)
         torch.cuda.synchronize()
     assert vsa.vsa_launch_count() - n == len(pr.records)
-    assert {name for name, _ in pr.records} >= {"page_topk", "paged_attn"}
+    assert {name for name, _ in pr.records} >= {"page_select", "paged_attn"}
