@@ -12,9 +12,10 @@
 // is finished there. Where a CTA's whole run lies in one segment its warps'
 // results are joined in shared memory first; the remaining pieces of
 // segments that cross runs go to the workspace (at most two per warp) and
-// k_paged_join adds them in ascending order. When the table allows only
-// short sequences (kAlignedKeys) each segment gets a CTA of its own and
-// there is nothing left to join: one launch.
+// k_paged_join adds them in ascending order. When the table or the page
+// lists allow only short segments (up to kAlignedKeys keys per CTA) each
+// segment gets a CTA, or a cluster of CTAs that join through distributed
+// shared memory, and one launch does it all.
 //
 // A warp takes its blocks through its own ring of asynchronous copies (16 K
 // rows and 16 V rows of 256 bytes per stage, swizzled so that ldmatrix reads
@@ -37,7 +38,8 @@ namespace {
 constexpr int kBlk = 16;        // keys per warp step
 constexpr int kLead = 1;        // blocks a segment counts for beyond its own (its start-up time)
 constexpr int kMinBlocks = 4;   // fewest blocks a warp's run has when there is little work
-constexpr int kAlignedKeys = 1024;  // up to this many keys a segment is one CTA's
+constexpr int kAlignedKeys = 1024;  // keys per CTA up to which a segment is one CTA's or one cluster's
+constexpr int kMaxCluster = 8;
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // ring stages per warp
 constexpr int kCtas = 304;      // two per SM on 152 SMs
@@ -56,7 +58,7 @@ struct AttnArgs {
     void *out;
     float *lse;
     int rc, rows;          // chunks of a group's heads, rows per chunk
-    int aligned;           // one CTA per segment, nothing to join
+    int aligned;           // CTAs per segment, one cluster; 0: equal runs of all segments' blocks
     int lead;              // kLead, 0 when aligned
     int4 *seg;             // [segments] its pieces: first warp, warps before / CTAs joined / pieces in all
     float2 *ml;            // [2 * kCtas * kWarps, rows]
@@ -76,6 +78,16 @@ __device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool fill) {
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -128,15 +140,33 @@ __device__ __forceinline__ Run find_run(const AttnArgs &a) {
     const int mult = a.idx ? a.rc : a.p.Hkv * a.rc;  // segments per entry
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     auto blocks_of = [&](int n) -> long long { return n < N ? (long long)seg_blocks(a, n) * mult : 0; };
-    long long total = 0;
-    for (int n0 = 0; n0 < N; n0 += kWarps * 32) total += blocks_of(n0 + tid);
+    // inclusive scan of one value per thread over the CTA; *all gets the sum
+    auto scan = [&](long long v, long long *all) {
+        long long inc = v;
 #pragma unroll
-    for (int off = 16; off; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
-    if (lane == 0) s_warp[wid] = total;
-    __syncthreads();
-    total = 0;
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) s_warp[wid] = inc;
+        __syncthreads();
+        *all = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_warp[w];
+        for (int w = 0; w < kWarps; ++w) {
+            if (w == wid) inc += *all;
+            *all += s_warp[w];
+        }
+        return inc;
+    };
+    const long long v0 = blocks_of(tid);
+    long long total, inc = scan(v0, &total);
+    const long long inc0 = inc, all0 = total;
+    for (int n0 = kWarps * 32; n0 < N; n0 += kWarps * 32) {
+        long long all;
+        __syncthreads();  // s_warp was read
+        scan(blocks_of(n0 + tid), &all);
+        total += all;
+    }
     Run r;
     r.total = total;
     r.per = (total + kCtas * kWarps - 1) / (kCtas * kWarps);
@@ -146,31 +176,20 @@ __device__ __forceinline__ Run find_run(const AttnArgs &a) {
     r.n = 0;
     r.before = 0;
     if (r.x0 >= r.x1) return r;  // no work: the whole CTA leaves
-    long long carry = 0;
-    for (int n0 = 0; n0 < N; n0 += kWarps * 32) {
-        const long long v = blocks_of(n0 + tid);
-        long long inc = v;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
-        }
-        __syncthreads();  // s_warp is free again
-        if (lane == 31) s_warp[wid] = inc;
-        __syncthreads();
-        long long base = carry, all = carry;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            base += w < wid ? s_warp[w] : 0;
-            all += s_warp[w];
-        }
-        inc += base;
+    long long carry = 0, v = v0, all = all0;
+    inc = inc0;
+    for (int n0 = 0; n0 < N;) {
+        inc += carry;
         if (inc - v <= r.x0 && r.x0 < inc) {  // one thread of the CTA
             s_n = n0 + tid;
             s_before = inc - v;
         }
-        carry = all;
-        if (carry > r.x0) break;
+        carry += all;
+        n0 += kWarps * 32;
+        if (carry > r.x0 || n0 >= N) break;
+        __syncthreads();  // s_warp was read
+        v = blocks_of(n0 + tid);
+        inc = scan(v, &all);
     }
     __syncthreads();
     r.n = s_n;
@@ -181,6 +200,7 @@ __device__ __forceinline__ Run find_run(const AttnArgs &a) {
 template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
+    __shared__ float2 s_cta[16 * MT];  // the CTA's own maximum and sum, for its cluster
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     grid_wait();
@@ -192,13 +212,14 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
     const float sl2 = p.scale * kLog2e;
 
     Run run;
+    const int segment = a.aligned ? (int)(blockIdx.x / a.aligned) : 0;
     if (a.aligned) {
-        run.n = (int)blockIdx.x / mult;
-        const int nb = seg_blocks(a, run.n);
-        run.per = (nb + kWarps - 1) / kWarps;
+        run.n = segment / mult;
+        const int nb = seg_blocks(a, run.n), at = (int)(blockIdx.x % a.aligned) * kWarps;
+        run.per = (nb + a.aligned * kWarps - 1) / (a.aligned * kWarps);
         run.before = 0;
-        run.x0 = (long long)(blockIdx.x % mult) * nb;
-        run.x1 = run.x0 + nb;
+        run.x0 = (long long)(segment % mult) * nb + min((long long)at * run.per, (long long)nb);
+        run.x1 = (long long)(segment % mult) * nb + min((long long)(at + kWarps) * run.per, (long long)nb);
         run.total = 0;
     } else {
         run = find_run(a);
@@ -225,7 +246,7 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         long long seg0;   // first block of the segment
         int sub, off, take;
         if (joined) {     // the segment is the run's, also for a warp without blocks
-            sub = a.aligned ? (int)blockIdx.x % mult : (int)((run.x0 - before) / nb);
+            sub = a.aligned ? segment % mult : (int)((run.x0 - before) / nb);
             seg0 = before + (long long)sub * nb;
             off = (int)(x - seg0);
             take = (int)(x_end - x);
@@ -476,13 +497,45 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
                     l += f * s_l[w][row];
                     o += f * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
                 }
-                if (first && last) {
+                if (a.aligned > 1) {  // in place: this thread alone reads and writes the element
+                    reinterpret_cast<float *>(smem)[row * kPitch + tid] = o;
+                    if (tid == 0) s_cta[row] = make_float2(M, l);
+                } else if (a.aligned || (first && last)) {
                     static_cast<T *>(a.out)[(hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
                     if (tid == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
                 } else {
                     a.o[(slot * a.rows + row) * kD + tid] = o;
                     if (tid == 0) a.ml[slot * a.rows + row] = make_float2(M, l);
                 }
+            }
+            if (a.aligned > 1) {  // the cluster's CTAs, each for its share of the rows
+                ptx::cluster_sync();
+                const uint32_t at_o = ptx::smem_addr(smem) + tid * 4, at_ml = ptx::smem_addr(s_cta);
+                for (int row = (int)ptx::cluster_rank(); row < rows; row += a.aligned) {
+                    float2 ml[kMaxCluster];
+                    float o[kMaxCluster], M = -INFINITY, l = 0.f, sum = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c) {
+                        ml[c] = make_float2(-INFINITY, 0.f);
+                        o[c] = 0.f;
+                        if (c < a.aligned) {
+                            ml[c] = ld_cluster2(ptx::cluster_addr(at_ml + row * 8, c));
+                            o[c] = ld_cluster(ptx::cluster_addr(at_o + row * kPitch * 4, c));
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ml[c].x);
+                    const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                    for (int c = 0; c < kMaxCluster; ++c) {
+                        const float f = ptx::ex2(ml[c].x - ref);
+                        l += f * ml[c].y;
+                        sum += f * o[c];
+                    }
+                    static_cast<T *>(a.out)[(hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : sum / l);
+                    if (tid == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+                }
+                ptx::cluster_sync();  // no CTA leaves while another reads its part
             }
             return;
         }
@@ -579,10 +632,11 @@ template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) 
     const void *fn = one ? (const void *)k_paged_attn<T, 1> : (const void *)k_paged_attn<T, 2>;
     const cudaError_t ae = ensure_smem_limit(fn, kSmem);
     if (ae != cudaSuccess) return status_from_cuda(ae);
-    const unsigned grid = a.aligned ? (unsigned)(a.p.B * a.p.Hkv * a.rc) : kCtas;
+    const unsigned grid = a.aligned ? (unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.aligned) : kCtas;
+    const unsigned cluster = a.aligned > 1 ? a.aligned : 1;
     prof_begin("paged_attn", s);
-    cudaError_t e = one ? launch_paged(k_paged_attn<T, 1>, grid, kWarps * 32, kSmem, 1, a, s)
-                        : launch_paged(k_paged_attn<T, 2>, grid, kWarps * 32, kSmem, 1, a, s);
+    cudaError_t e = one ? launch_paged(k_paged_attn<T, 1>, grid, kWarps * 32, kSmem, cluster, a, s)
+                        : launch_paged(k_paged_attn<T, 2>, grid, kWarps * 32, kSmem, cluster, a, s);
     prof_end(s);
     if (e != cudaSuccess || a.aligned) return status_from_cuda(e);
     prof_begin("paged_join", s);
@@ -644,7 +698,11 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
-    a.aligned = most <= kAlignedKeys;
+    // The largest cluster that leaves every CTA of the grid resident at once.
+    const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
+    int cluster = kMaxCluster;
+    while (cluster > 1 && segments * cluster > kCtas) cluster /= 2;
+    a.aligned = most <= (long long)kAlignedKeys * cluster ? cluster : 0;
     a.lead = a.aligned ? 0 : kLead;
     char *w = static_cast<char *>(workspace);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);

@@ -11,7 +11,8 @@
 // the last page to take under (key desc, page asc), 11 bits of (key, page)
 // at a time from the top (a 2,048-bin histogram), until the bin that holds
 // it is small enough to rank outright; then lists the taken pages in order.
-// The scores never leave the SMs.
+// The scores never leave the SMs. The means stream through a ring of
+// asynchronous copies per warp; a lane reads back what it copied itself.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -33,11 +34,18 @@ struct SelectArgs {
 
 constexpr int kCluster = 8;
 constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
-constexpr int kItems = 4;    // groups of four pages a warp has in flight
+constexpr int kRing = 4;     // ring stages per warp, each four pages' means of one head (2 KB)
 constexpr int kBins = 2048;
 constexpr int kRank = 256;   // a bin of up to this many pages is ranked outright
 constexpr int kIndexBits = 22;
+constexpr int kRingBytes = kRing * 2048;
 constexpr int kMaxSmem = 200 * 1024;  // dynamic, beside the bins and the list
+
+// Shared memory of the rings, and later of one head's keys.
+__host__ __device__ __forceinline__ int front_bytes(int cap) {
+    const int ring = kWarpsSel * kRingBytes, keys = kCluster * cap * 4;
+    return ring > keys ? ring : (keys + 15) & ~15;
+}
 
 // Larger score, larger key; -0 folded into +0, NaN counted as -inf.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -79,9 +87,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     __shared__ int s_bin, s_above, s_in, s_fill;
     __shared__ uint64_t s_cut;
     __shared__ uint64_t list[kRank];
-    float *sq = reinterpret_cast<float *>(sm);                       // [hg][128] summed queries
-    uint32_t *keys = reinterpret_cast<uint32_t *>(sq + a.hg * kD);   // [hg][cap] keys of this CTA's run
-    int *ids = reinterpret_cast<int *>(keys + (size_t)a.hg * a.cap); // [cap] page ids of the run
+    uint32_t *mine = reinterpret_cast<uint32_t *>(sm);                   // [kCluster * cap] all keys of one head,
+                                                                         // where the rings were
+    float *sq = reinterpret_cast<float *>(sm + front_bytes(a.cap));      // [hg][128] summed queries
+    uint32_t *keys = reinterpret_cast<uint32_t *>(sq + a.hg * kD);       // [hg][cap] keys of this CTA's run
+    int *ids = reinterpret_cast<int *>(keys + (size_t)a.hg * a.cap);     // [cap] page ids of the run
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = (int)ptx::cluster_rank(), cl = (int)blockIdx.x / kCluster;
@@ -110,41 +120,48 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
 
     // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
     const int sub = lane >> 3, j = lane & 7, items = (nc + 3) / 4 * hn;
-    for (int it0 = wid; it0 < items; it0 += kWarpsSel * kItems) {
-        float4 m[kItems][4];
+    const uint32_t ring = ptx::smem_addr(sm) + wid * kRingBytes + lane * 16;
+    auto copy = [&](int it, int stage) {
+        const int hh = it % hn, c = it / hn * 4 + sub;
+        const int id = c < nc ? ids[c] : -1;
+        const float *src = a.mean + ((long long)max(id, 0) * p.Hkv + h0 + hh) * kD + 4 * j;
 #pragma unroll
-        for (int e = 0; e < kItems; ++e) {
-            const int it = it0 + e * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
-            const int id = it < items && c < nc ? ids[c] : -1;
+        for (int i = 0; i < 4; ++i)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + stage * 2048 + i * 512),
+                         "l"(src + 32 * i), "r"(id >= 0 ? 16 : 0)
+                         : "memory");
+    };
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                m[e][i] = id >= 0 ? __ldg(reinterpret_cast<const float4 *>(
-                                        a.mean + ((long long)id * p.Hkv + h0 + hh) * kD + 32 * i + 4 * j))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = 0; s < kRing - 1; ++s) {
+        if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int n = 0; wid + n * kWarpsSel < items; ++n) {
+        const int it = wid + n * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
+        const int ahead = it + (kRing - 1) * kWarpsSel;
+        if (ahead < items) copy(ahead, (n + kRing - 1) % kRing);  // the stage this lane read last
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+        float x[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 g = *reinterpret_cast<const float4 *>(sq + hh * kD + 32 * i + 4 * j);
+            const float4 m = *reinterpret_cast<const float4 *>(sm + wid * kRingBytes + (n % kRing) * 2048 + i * 512 +
+                                                               lane * 16);
+            x[i][0] = __fmul_rn(g.x, m.x);
+            x[i][1] = __fmul_rn(g.y, m.y);
+            x[i][2] = __fmul_rn(g.z, m.z);
+            x[i][3] = __fmul_rn(g.w, m.w);
         }
+        // 128 -> 64 -> 32: dims 64 and 32 apart; then neighbours
+        float y[4];
 #pragma unroll
-        for (int e = 0; e < kItems; ++e) {
-            const int it = it0 + e * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
-            float x[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 g = *reinterpret_cast<const float4 *>(sq + hh * kD + 32 * i + 4 * j);
-                x[i][0] = __fmul_rn(g.x, m[e][i].x);
-                x[i][1] = __fmul_rn(g.y, m[e][i].y);
-                x[i][2] = __fmul_rn(g.z, m[e][i].z);
-                x[i][3] = __fmul_rn(g.w, m[e][i].w);
-            }
-            // 128 -> 64 -> 32: dims 64 and 32 apart; then neighbours
-            float y[4];
-#pragma unroll
-            for (int d = 0; d < 4; ++d)
-                y[d] = __fadd_rn(__fadd_rn(x[0][d], x[2][d]), __fadd_rn(x[1][d], x[3][d]));
-            float r = __fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3]));
-            r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
-            r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 2));
-            r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 4));
-            if (j == 0 && it < items && c < nc) keys[hh * a.cap + c] = order_key(ids[c] >= 0 ? r : -INFINITY);
-        }
+        for (int d = 0; d < 4; ++d) y[d] = __fadd_rn(__fadd_rn(x[0][d], x[2][d]), __fadd_rn(x[1][d], x[3][d]));
+        float r = __fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3]));
+        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
+        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 2));
+        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 4));
+        if (j == 0 && c < nc) keys[hh * a.cap + c] = order_key(ids[c] >= 0 ? r : -INFINITY);
     }
     ptx::cluster_sync();  // every run's keys are there
 
@@ -152,14 +169,16 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
         const long long row = (long long)b * p.Hkv + h0 + hh;
         int *idx = a.idx + row * a.topk;
         const uint32_t base = ptx::smem_addr(keys + (size_t)hh * a.cap);
-        // f(c, rank_of(key, c)) over this thread's share of the competing pages
+        // the head's keys from all runs, in page order
+#pragma unroll
+        for (int r = 0; r < kCluster; ++r) {
+            const uint32_t at = ptx::cluster_addr(base, r);
+            const int n = min(run, comp - r * run);
+            for (int c = tid; c < n; c += kThreads) mine[r * run + c] = ld_cluster(at + 4 * c);
+        }
+        __syncthreads();
         auto each = [&](auto f) {
-            for (int r = 0; r < kCluster; ++r) {
-                const uint32_t at = ptx::cluster_addr(base, r);
-                const int n = min(run, comp - r * run);
-#pragma unroll 4
-                for (int c = tid; c < n; c += kThreads) f(r * run + c, rank_of(ld_cluster(at + 4 * c), r * run + c));
-            }
+            for (int c = tid; c < comp; c += kThreads) f(rank_of(mine[c], c));
         };
         // cut: the `take`-th largest rank (ranks are distinct); 2^54 when none is taken
         uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
@@ -168,7 +187,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
             const int shift = max(top - 11, 0), bits = top - shift;
             for (int e = tid; e < kBins; e += kThreads) hist[e] = 0;
             __syncthreads();
-            each([&](int, uint64_t k) {
+            each([&](uint64_t k) {
                 if (k >> top == prefix) atomicAdd(&hist[(int)((k >> shift) & ((1u << bits) - 1u))], 1);
             });
             __syncthreads();
@@ -208,7 +227,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
                 break;
             }
             if (in <= kRank) {
-                each([&](int, uint64_t k) {
+                each([&](uint64_t k) {
                     if (k >> top == prefix) list[atomicAdd(&s_fill, 1)] = k;
                 });
                 __syncthreads();
@@ -227,10 +246,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
         // pages at or above the cut, in order: each warp has a contiguous share
         const int share = ((comp + kWarpsSel - 1) / kWarpsSel + 31) & ~31;
         const int lo = min(wid * share, comp), hi = min(lo + share, comp);
-        auto chosen = [&](int c) {
-            const int r = c / run;
-            return rank_of(ld_cluster(ptx::cluster_addr(base, r) + 4 * (c - r * run)), c) >= cut;
-        };
+        auto chosen = [&](int c) { return rank_of(mine[c], c) >= cut; };
         int n = 0;
         for (int c = lo + lane; c - lane < hi; c += 32) n += __popc(__ballot_sync(0xffffffffu, c < hi && chosen(c)));
         __syncthreads();  // wsum was read
@@ -279,7 +295,9 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
         a.hg /= 2;
     a.cap = (std::min(a.p.max_pages, 1 << kIndexBits) + kCluster - 1) / kCluster;
-    auto bytes = [&] { return sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (a.hg + 1); };
+    auto bytes = [&] {
+        return front_bytes(a.cap) + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (a.hg + 1);
+    };
     while (a.hg > 1 && bytes() > kMaxSmem) a.hg /= 2;
     if (a.p.max_pages > (1 << kIndexBits) || bytes() > kMaxSmem) return VSA_ERR_UNSUPPORTED;
     a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;

@@ -575,11 +575,17 @@ def check_wait_timeout(workspace: torch.Tensor, limit_ns: int = 50_000_000, stre
 def _row_stride(name, x, heads, D):
     """Elements from one token of x [T, heads, D] to the next (heads and
     dims dense; 0 where there is only one token)."""
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != D:
-        raise ValueError(f"{name}: expected [tokens, {heads}, {D}], got {list(x.shape)}")
-    if x.numel() and (x.stride(2) != 1 or (heads > 1 and x.stride(1) != D)):
+    shape, stride = x.shape, x.stride()
+    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
+        raise ValueError(f"{name}: expected [tokens, {heads}, {D}], got {list(shape)}")
+    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
         raise ValueError(f"{name}: heads and dims must be dense")
-    return x.stride(0) if x.shape[0] > 1 else 0
+    return stride[0] if shape[0] > 1 else 0
+
+
+# The current stream's handle by device index: what torch.cuda.current_stream
+# wraps in a Stream object, at a twentieth of its time (2 us of a call of 10).
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 class PagedCache:
@@ -653,16 +659,27 @@ class PagedCache:
         elif workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace: at least {need} bytes on {self.device} are needed")
         self.workspace = workspace
-        self._ws = (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        # what every call passes on: the tensors above are not to be replaced, only written
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self._k, self._v, self._mean = ptr(k), ptr(v), ptr(k_mean)
+        self._ws, self._ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        self._desc, self._index = C.byref(self.desc), self.device.index
+        self._out_shape, self._lse_shape = (B, Hq, D), (B, Hq)
+        self._out_dense = (Hq * D, D, 1)
 
     def _is(self, name, t, shape, dtype):
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != tuple(shape):
+        if t.dtype != dtype or t.device != self.device or t.shape != shape:
             raise ValueError(f"{name}: expected {dtype} {list(shape)} on {self.device}, "
                              f"got {t.dtype} {list(t.shape)} on {t.device}")
 
     def _on(self, name, t, dtype):
         if t.dtype != dtype or t.device != self.device:
             raise ValueError(f"{name}: expected {dtype} on {self.device}, got {t.dtype} on {t.device}")
+
+    def _dense(self, name, t, shape, dtype):
+        self._is(name, t, shape, dtype)
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
 
     def _empty(self, shape, dtype, stream):
         """An output that belongs to the stream the call runs on."""
@@ -673,24 +690,39 @@ class PagedCache:
 
     def _run(self, name, stream, *args):
         """The call on this cache's device and the given (or current) stream."""
-        if self.device.type != "cuda":
+        if self._index is None:
             raise ValueError(f"the cache is on {self.device}: the calls run on a GPU only")
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            handle = _raw_stream(self._index)
         elif stream.device != self.device:
             raise ValueError(f"stream: expected one of {self.device}, got {stream.device}")
-        fn = getattr(lib(), name)
-        if torch.cuda.current_device() == self.device.index:
-            code = fn(C.byref(self.desc), *args, stream.cuda_stream)
+        else:
+            handle = stream.cuda_stream
+        fn = getattr(_lib, name)
+        if torch.cuda.current_device() == self._index:
+            code = fn(self._desc, *args, handle)
         else:
             with torch.cuda.device(self.device):
-                code = fn(C.byref(self.desc), *args, stream.cuda_stream)
-        _check(name, code)
+                code = fn(self._desc, *args, handle)
+        if code:
+            raise VsaError(name, code)
 
-    def _need(self, *names):
-        for n in names:
-            if getattr(self, n) is None:
-                raise ValueError(f"this cache has no {n}")
+    def _rows(self, q):
+        """Checks the queries of one token per sequence; their row stride."""
+        if q.dtype != self.dtype or q.device != self.device:
+            self._on("q", q, self.dtype)
+        if q.shape == self._out_shape and q.stride() == self._out_dense:
+            return 0
+        qs = _row_stride("q", q, self.Hq, self.D)
+        if q.shape[0] != self.B:
+            raise ValueError(f"q: expected one token for each of {self.B} sequences")
+        return qs
+
+    def _lists(self, idx, cnt):
+        if idx.dim() != 3:
+            raise ValueError("page lists: expected page_idx [B, Hkv, cap] and page_cnt [B, Hkv]")
+        self._dense("page_idx", idx, (self.B, self.Hkv, idx.shape[2]), torch.int32)
+        self._dense("page_cnt", cnt, (self.B, self.Hkv), torch.int32)
 
     def append(self, k, v, q=None, cu_seqlens=None, cos=None, sin=None, positions=None, interleaved=False, q_out=None,
                stream=None):
@@ -698,12 +730,14 @@ class PagedCache:
         tokens, which seq_lens already counts; cu_seqlens int32 [B+1], None
         for one token per sequence. cos, sin: fp32 [rows, rot_dim / 2], None
         for no rotation. Returns the rotated q (None without q)."""
-        self._need("k", "v")
+        if self._k is None:
+            raise ValueError("this cache has no k and v")
         T = k.shape[0]
         self._on("k", k, self.dtype)
         self._on("v", v, self.dtype)
         ks, vs = _row_stride("k", k, self.Hkv, self.D), _row_stride("v", v, self.Hkv, self.D)
-        qs = 0
+        qp = qop = cu = pos = cp = sp = None
+        qs = rows = rot = 0
         if v.shape[0] != T or (q is not None and q.shape[0] != T):
             raise ValueError("k, v and q must have the same number of tokens")
         if q is not None:
@@ -712,59 +746,56 @@ class PagedCache:
             if q_out is None:
                 q_out = self._empty((T, self.Hq, self.D), self.dtype, stream)
             else:
-                self._is("q_out", q_out, (T, self.Hq, self.D), self.dtype)
-                if not q_out.is_contiguous():
-                    raise ValueError("q_out: must be contiguous")
+                self._dense("q_out", q_out, (T, self.Hq, self.D), self.dtype)
+            qp, qop = q.data_ptr(), q_out.data_ptr()
         elif q_out is not None:
             raise ValueError("q_out without q")
         if cu_seqlens is not None:
-            self._is("cu_seqlens", cu_seqlens, (self.B + 1,), torch.int32)
-            if not cu_seqlens.is_contiguous():
-                raise ValueError("cu_seqlens: must be contiguous")
+            self._dense("cu_seqlens", cu_seqlens, (self.B + 1,), torch.int32)
+            cu = cu_seqlens.data_ptr()
         elif T != self.B:
             raise ValueError("without cu_seqlens there is one token per sequence")
-        rows = rot = 0
-        if (cos is None) != (sin is None):
-            raise ValueError("give both cos and sin, or neither")
-        if cos is not None:
-            if cos.dim() != 2 or cos.shape != sin.shape or not (cos.is_contiguous() and sin.is_contiguous()):
+        if cos is not None and sin is not None:
+            shape = cos.shape
+            if len(shape) != 2 or not cos.is_contiguous():
                 raise ValueError("cos and sin: expected contiguous [rows, rot_dim / 2]")
             self._on("cos", cos, torch.float32)
-            self._on("sin", sin, torch.float32)
-            rows, rot = cos.shape[0], 2 * cos.shape[1]
+            self._dense("sin", sin, shape, torch.float32)
+            rows, rot, cp, sp = shape[0], 2 * shape[1], cos.data_ptr(), sin.data_ptr()
+        elif cos is not sin:
+            raise ValueError("give both cos and sin, or neither")
         if positions is not None:
-            self._is("positions", positions, (T,), torch.int32)
-            if not positions.is_contiguous():
-                raise ValueError("positions: must be contiguous")
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._run("vsa_paged_append", stream, T, k.data_ptr(), ks, v.data_ptr(), vs, ptr(q), qs, ptr(q_out),
-                  ptr(cu_seqlens), ptr(positions), ptr(cos), ptr(sin), rows, rot, int(bool(interleaved)),
-                  self.k.data_ptr(), self.v.data_ptr(), ptr(self.k_mean))
+            self._dense("positions", positions, (T,), torch.int32)
+            pos = positions.data_ptr()
+        self._run("vsa_paged_append", stream, T, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qop, cu, pos, cp, sp,
+                  rows, rot, 1 if interleaved else 0, self._k, self._v, self._mean)
         return q_out
 
     def select(self, q, topk, keep_first=0, keep_last=1, page_idx=None, page_cnt=None, stream=None):
         """vsa_page_select: the pages that q [B, Hq, D] attends to, as
         (page_idx int32 [B, Hkv, topk], page_cnt int32 [B, Hkv])."""
-        self._need("k_mean")
-        self._on("q", q, self.dtype)
+        if self._mean is None:
+            raise ValueError("this cache has no k_mean")
         qs = self._rows(q)
+        given = page_idx is not None or page_cnt is not None
         if page_idx is None:
             page_idx = self._empty((self.B, self.Hkv, topk), torch.int32, stream)
         if page_cnt is None:
             page_cnt = self._empty((self.B, self.Hkv), torch.int32, stream)
-        self._lists(page_idx, page_cnt)
-        if page_idx.shape[2] != topk:
-            raise ValueError(f"page_idx: expected topk = {topk} entries per row")
-        self._run("vsa_page_select", stream, q.data_ptr(), qs, self.k_mean.data_ptr(), int(topk), int(keep_first),
-                  int(keep_last), page_idx.data_ptr(), page_cnt.data_ptr())
+        if given:
+            self._lists(page_idx, page_cnt)
+            if page_idx.shape[2] != topk:
+                raise ValueError(f"page_idx: expected topk = {topk} entries per row")
+        self._run("vsa_page_select", stream, q.data_ptr(), qs, self._mean, topk, keep_first, keep_last,
+                  page_idx.data_ptr(), page_cnt.data_ptr())
         return page_idx, page_cnt
 
     def attend(self, q, pages=None, out=None, lse=None, stream=None):
         """vsa_paged_attn: q [B, Hq, D] over the whole cache, or over the
         pages = (page_idx, page_cnt) that select returned. Returns (out
         [B, Hq, D], lse fp32 [B, Hq])."""
-        self._need("k", "v")
-        self._on("q", q, self.dtype)
+        if self._k is None:
+            raise ValueError("this cache has no k and v")
         qs = self._rows(q)
         idx = cnt = None
         cap = 0
@@ -772,29 +803,13 @@ class PagedCache:
             self._lists(*pages)
             idx, cnt, cap = pages[0].data_ptr(), pages[1].data_ptr(), pages[0].shape[2]
         if out is None:
-            out = self._empty((self.B, self.Hq, self.D), self.dtype, stream)
+            out = self._empty(self._out_shape, self.dtype, stream)
         else:
-            self._is("out", out, (self.B, self.Hq, self.D), self.dtype)
-            if not out.is_contiguous():
-                raise ValueError("out: must be contiguous")
+            self._dense("out", out, self._out_shape, self.dtype)
         if lse is None:
-            lse = self._empty((self.B, self.Hq), torch.float32, stream)
+            lse = self._empty(self._lse_shape, torch.float32, stream)
         else:
-            self._is("lse", lse, (self.B, self.Hq), torch.float32)
-            if not lse.is_contiguous():
-                raise ValueError("lse: must be contiguous")
-        self._run("vsa_paged_attn", stream, q.data_ptr(), qs, self.k.data_ptr(), self.v.data_ptr(), idx, cnt, cap,
-                  out.data_ptr(), lse.data_ptr(), *self._ws)
+            self._dense("lse", lse, self._lse_shape, torch.float32)
+        self._run("vsa_paged_attn", stream, q.data_ptr(), qs, self._k, self._v, idx, cnt, cap, out.data_ptr(),
+                  lse.data_ptr(), self._ws, self._ws_bytes)
         return out, lse
-
-    def _rows(self, q):
-        qs = _row_stride("q", q, self.Hq, self.D)
-        if q.shape[0] != self.B:
-            raise ValueError(f"q: expected one token for each of {self.B} sequences")
-        return qs
-
-    def _lists(self, idx, cnt):
-        if idx.dim() != 3 or not (idx.is_contiguous() and cnt.is_contiguous()):
-            raise ValueError("page lists: expected contiguous page_idx [B, Hkv, cap] and page_cnt [B, Hkv]")
-        self._is("page_idx", idx, (self.B, self.Hkv, idx.shape[2]), torch.int32)
-        self._is("page_cnt", cnt, (self.B, self.Hkv), torch.int32)

@@ -552,7 +552,7 @@ vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, in
  * Writes page_idx [B, Hkv, topk] int32, ascending, unused entries -1, and
  * page_cnt [B, Hkv]. topk >= keep_first + keep_last. The result is the
  * same bit for bit on every run. Errors as for vsa_paged_append;
- * VSA_ERR_UNSUPPORTED when max_pages is over 204,288. */
+ * VSA_ERR_UNSUPPORTED when max_pages is over 40,856. */
 vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const float *k_mean,
                            int topk, int keep_first, int keep_last, int32_t *page_idx, int32_t *page_cnt,
                            vsa_stream_t stream);

@@ -92,7 +92,7 @@ def test_select_errors(L):
     assert select(L, topk=3, first=2, last=2) == 2
     assert select(L, first=2 ** 31 - 1, last=2 ** 31 - 1) == 2
     assert select(L, qs=8) == 2
-    assert select(L, desc(max_pages=204289)) == 5    # more pages than the cluster's shared memory holds keys for
+    assert select(L, desc(max_pages=40857)) == 5    # more pages than the cluster's shared memory holds keys for
 
 
 def test_attend_errors(L):
