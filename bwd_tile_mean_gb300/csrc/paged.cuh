@@ -80,6 +80,80 @@ inline bool token_stride(int64_t given, int heads, long long *out) {
     return given == 0 || (given >= dense && given % 8 == 0);
 }
 
+// Equal contiguous runs of the work of a list of entries, whatever their
+// sizes: entry n has size_of(n) units (n < N), the units of all entries end
+// to end are dealt to `workers` workers (at least min_per units each), and a
+// CTA has `per_cta` neighbouring workers. Called by the whole CTA (W warps);
+// every thread gets the CTA's run and the entry that holds its first unit.
+struct Run {
+    long long x0, x1, total, per;  // this CTA's units, all units, units per worker
+    int n;                         // entry that holds x0 (x0 < x1)
+    long long before;              // units of the entries before n
+};
+template <int W, typename F>
+__device__ __forceinline__ Run find_run(int N, F size_of, int workers, int min_per, int per_cta) {
+    __shared__ long long s_warp[W];
+    __shared__ long long s_before;
+    __shared__ int s_n;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    auto size = [&](int n) -> long long { return n < N ? size_of(n) : 0; };
+    // inclusive scan of one value per thread over the CTA; *all gets the sum
+    auto scan = [&](long long v, long long *all) {
+        long long inc = v;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) s_warp[wid] = inc;
+        __syncthreads();
+        *all = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            if (w == wid) inc += *all;
+            *all += s_warp[w];
+        }
+        return inc;
+    };
+    const long long v0 = size(tid);
+    long long total, inc = scan(v0, &total);
+    const long long inc0 = inc, all0 = total;
+    for (int n0 = W * 32; n0 < N; n0 += W * 32) {
+        long long all;
+        __syncthreads();  // s_warp was read
+        scan(size(n0 + tid), &all);
+        total += all;
+    }
+    Run r;
+    r.total = total;
+    r.per = (total + workers - 1) / workers;
+    if (r.per < min_per) r.per = min_per;
+    r.x0 = (long long)blockIdx.x * r.per * per_cta;
+    r.x1 = r.x0 + r.per * per_cta < total ? r.x0 + r.per * per_cta : total;
+    r.n = 0;
+    r.before = 0;
+    if (r.x0 >= r.x1) return r;  // no work, for the whole CTA
+    long long carry = 0, v = v0, all = all0;
+    inc = inc0;
+    for (int n0 = 0; n0 < N;) {
+        inc += carry;
+        if (inc - v <= r.x0 && r.x0 < inc) {  // one thread of the CTA
+            s_n = n0 + tid;
+            s_before = inc - v;
+        }
+        carry += all;
+        n0 += W * 32;
+        if (carry > r.x0 || n0 >= N) break;
+        __syncthreads();  // s_warp was read
+        v = size(n0 + tid);
+        inc = scan(v, &all);
+    }
+    __syncthreads();
+    r.n = s_n;
+    r.before = s_before;
+    return r;
+}
+
 // Kernels of the paged calls are launched so that the next one on the stream
 // may start while this one drains: every CTA waits for the work before it
 // with grid_wait() before it touches memory, and lets the launch after it
@@ -105,8 +179,9 @@ inline cudaError_t launch_paged(void (*kernel)(A), dim3 grid, unsigned threads, 
     return cudaLaunchKernelEx(&c, kernel, args);
 }
 
-// Workspace of vsa_paged_attn.
+// Workspace of vsa_page_select and vsa_paged_attn (each uses its own part).
 struct PagedWs {
+    size_t keys;        // [B * Hkv, max_pages] uint32 score keys
     size_t seg;         // [segments] int4: where a segment's pieces are
     size_t ml;          // [slots, rows] float2: running maximum (log2 units) and sum
     size_t o;           // [slots, rows, 128] fp32 unnormalised partial outputs

@@ -126,77 +126,6 @@ __device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) {
     return nb > 0 ? nb + a.lead : 0;
 }
 
-// A CTA's run of blocks, and the list entry where it begins.
-struct Run {
-    long long x0, x1, total, per;  // this CTA's blocks, all blocks, blocks per warp
-    int n;                         // list entry that holds x0
-    long long before;              // blocks of the entries before n
-};
-__device__ __forceinline__ Run find_run(const AttnArgs &a) {
-    __shared__ long long s_warp[kWarps];
-    __shared__ long long s_before;
-    __shared__ int s_n;
-    const int N = a.idx ? a.p.B * a.p.Hkv : a.p.B;
-    const int mult = a.idx ? a.rc : a.p.Hkv * a.rc;  // segments per entry
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    auto blocks_of = [&](int n) -> long long { return n < N ? (long long)seg_blocks(a, n) * mult : 0; };
-    // inclusive scan of one value per thread over the CTA; *all gets the sum
-    auto scan = [&](long long v, long long *all) {
-        long long inc = v;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const long long y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
-        }
-        if (lane == 31) s_warp[wid] = inc;
-        __syncthreads();
-        *all = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w == wid) inc += *all;
-            *all += s_warp[w];
-        }
-        return inc;
-    };
-    const long long v0 = blocks_of(tid);
-    long long total, inc = scan(v0, &total);
-    const long long inc0 = inc, all0 = total;
-    for (int n0 = kWarps * 32; n0 < N; n0 += kWarps * 32) {
-        long long all;
-        __syncthreads();  // s_warp was read
-        scan(blocks_of(n0 + tid), &all);
-        total += all;
-    }
-    Run r;
-    r.total = total;
-    r.per = (total + kCtas * kWarps - 1) / (kCtas * kWarps);
-    if (r.per < kMinBlocks) r.per = kMinBlocks;
-    r.x0 = (long long)blockIdx.x * r.per * kWarps;
-    r.x1 = r.x0 + r.per * kWarps < total ? r.x0 + r.per * kWarps : total;
-    r.n = 0;
-    r.before = 0;
-    if (r.x0 >= r.x1) return r;  // no work: the whole CTA leaves
-    long long carry = 0, v = v0, all = all0;
-    inc = inc0;
-    for (int n0 = 0; n0 < N;) {
-        inc += carry;
-        if (inc - v <= r.x0 && r.x0 < inc) {  // one thread of the CTA
-            s_n = n0 + tid;
-            s_before = inc - v;
-        }
-        carry += all;
-        n0 += kWarps * 32;
-        if (carry > r.x0 || n0 >= N) break;
-        __syncthreads();  // s_warp was read
-        v = blocks_of(n0 + tid);
-        inc = scan(v, &all);
-    }
-    __syncthreads();
-    r.n = s_n;
-    r.before = s_before;
-    return r;
-}
-
 template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
@@ -222,7 +151,9 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         run.x1 = (long long)(segment % mult) * nb + min((long long)(at + kWarps) * run.per, (long long)nb);
         run.total = 0;
     } else {
-        run = find_run(a);
+        run = find_run<kWarps>(
+            N, [&](int n) -> long long { return (long long)seg_blocks(a, n) * mult; }, kCtas * kWarps, kMinBlocks,
+            kWarps);
         if (run.x0 >= run.x1) return;
     }
     // the CTA's run lies in one segment: its warps' results are joined
@@ -656,6 +587,7 @@ PagedWs paged_ws(const Paged &p) {
         return o;
     };
     const size_t rows = rows_of(p.G), rc = (p.G + rows - 1) / rows;
+    w.keys = take(sizeof(uint32_t) * p.B * (size_t)p.Hkv * p.max_pages);
     w.seg = take(sizeof(int4) * p.B * (size_t)p.Hkv * rc);
     w.ml = take(sizeof(float2) * 2 * kCtas * kWarps * rows);
     w.o = take(sizeof(float) * 2 * kCtas * kWarps * rows * kD);

@@ -1,21 +1,27 @@
 // paged_select.cu -- the pages each key/value head attends to, by the score
 // of their mean key against the group's query (vsa_page_select).
 //
-// One launch. A cluster of 8 CTAs has one sequence and up to 8 key/value
-// heads; the pages that compete (all but the first keep_first and the last
-// keep_last) are cut into 8 runs, one per CTA. A CTA reads the fp32 means of
-// its run once (8 lanes per page, 16 bytes per load; the heads of a page are
-// neighbours in memory) and leaves an order-preserving 32-bit key per page
-// and head in its shared memory. Then each CTA finishes one head: it reads
-// the 8 CTAs' keys through the cluster's distributed shared memory and finds
-// the last page to take under (key desc, page asc), 11 bits of (key, page)
-// at a time from the top (a 2,048-bin histogram), until the bin that holds
-// it is small enough to rank outright; then lists the taken pages in order.
-// The scores never leave the SMs. The means stream through a ring of
-// asynchronous copies per warp; a lane reads back what it copied itself.
+// A page competes unless it is among the first keep_first or the last
+// keep_last. Its fp32 mean is read once (8 lanes per page, 16 bytes per load,
+// through a ring of asynchronous copies per warp; the heads of a page are
+// neighbours in memory; a lane reads back what it copied itself) and becomes
+// one order-preserving 32-bit key per head. Then a CTA per row finds the last
+// page to take under (key desc, page asc), 11 bits of (key, page) at a time
+// from the top (a 2,048-bin histogram), until the bin that holds it is small
+// enough to rank outright, and lists the taken pages in order.
+//
+// Few pages (kClusterPages): k_page_select, one launch. A cluster of 8 CTAs
+// has one sequence and up to 8 heads, cuts the pages into 8 runs and stores
+// the keys straight into the shared memory of the CTA that finishes the head;
+// the scores never leave the SMs.
+// Many: k_page_scores deals the pages of the whole batch, four at a time with
+// up to 16 heads of each, to the CTAs in equal contiguous runs whatever the
+// lengths, with the keys in the workspace, and k_page_topk finishes the rows.
+// The longest sequence then does not wait for the 8 CTAs of its cluster.
 #include <algorithm>
 
 #include "paged.cuh"
+#include "sm103_ptx.cuh"
 #include "sm103_ptx.cuh"
 
 namespace vsa {
@@ -28,23 +34,29 @@ struct SelectArgs {
     const float *mean;
     int topk, first, last;
     int *idx, *cnt;
-    int hg, hgroups;  // heads per cluster, clusters per sequence
+    uint32_t *keys;   // [B * Hkv, max_pages] of the competing pages, from keep_first on
+    int hg, hgroups;  // k_page_select: heads per cluster, clusters per sequence
     int cap;          // pages per CTA at most
 };
 
-constexpr int kCluster = 8;
 constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
-constexpr int kRing = 4;     // ring stages per warp, each four pages' means of one head (2 KB)
-constexpr int kBins = 2048;
-constexpr int kRank = 256;   // a bin of up to this many pages is ranked outright
-constexpr int kIndexBits = 22;
+constexpr int kCtasSel = 304;  // two per SM on 152 SMs
+constexpr int kHeads = 16;     // heads of a page taken together
+constexpr int kRing = 5;       // ring stages per warp, each four pages' means of one head (2 KB)
 constexpr int kRingBytes = kRing * 2048;
-constexpr int kMaxSmem = 200 * 1024;  // dynamic, beside the bins and the list
+constexpr int kSmemSel = kWarpsSel * kRingBytes + kHeads * kD * 4;
+constexpr int kCluster = 8;
+constexpr int kClusterStages = 4, kClusterRing = kClusterStages * 2048;
+constexpr int kClusterPages = 2048;  // pages x heads a cluster has at most
+constexpr int kBins = 2048;
+constexpr int kRank = 256;     // a bin of up to this many pages is ranked outright
+constexpr int kIndexBits = 27; // of a page index
 
-// Shared memory of the rings, and later of one head's keys.
-__host__ __device__ __forceinline__ int front_bytes(int cap) {
-    const int ring = kWarpsSel * kRingBytes, keys = kCluster * cap * 4;
-    return ring > keys ? ring : (keys + 15) & ~15;
+// Competing pages of sequence b (all of them full: the partial page is the
+// last); 0 when every page is taken.
+__device__ __forceinline__ int competing(const SelectArgs &a, int b) {
+    const int pages = (paged_len(a.p, b) + a.p.page - 1) >> a.p.page_log2;
+    return pages > a.topk ? pages - a.first - a.last : 0;
 }
 
 // Larger score, larger key; -0 folded into +0, NaN counted as -inf.
@@ -55,23 +67,33 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t ld_cluster(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Sum of the group's 16-bit queries at one dim: the fp32 running sum with
-// its rounding errors kept aside (each found exactly), added at the end.
-template <typename T> __device__ __forceinline__ float group_sum(const T *q, int G) {
-    float s = to_f<T>(q[0]), err = 0.f;
-    for (int m = 1; m < G; ++m) {
-        const float x = to_f<T>(q[(long long)m * kD]);
-        const float t = __fadd_rn(s, x), y = __fsub_rn(t, s);
-        err = __fadd_rn(err, __fadd_rn(__fsub_rn(s, __fsub_rn(t, y)), __fsub_rn(x, y)));
-        s = t;
+// Sums of the group's 16-bit queries at eight dims: fp32 running sums with
+// their rounding errors kept aside (each found exactly), added at the end.
+template <typename T> __device__ __forceinline__ void group_sum(const T *q, int G, float *out) {
+    float s[8], err[8];
+    for (int m = 0; m < G; ++m) {
+        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(q + (long long)m * kD));
+        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float2 f = unpack2<T>(r[e / 2]);
+            const float x = e & 1 ? f.y : f.x;
+            if (m == 0) {
+                s[e] = x;
+                err[e] = 0.f;
+            } else {
+                const float t = __fadd_rn(s[e], x), y = __fsub_rn(t, s[e]);
+                err[e] = __fadd_rn(err[e], __fadd_rn(__fsub_rn(s[e], __fsub_rn(t, y)), __fsub_rn(x, y)));
+                s[e] = t;
+            }
+        }
     }
-    return isfinite(s) ? __fadd_rn(s, err) : s;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) out[e] = isfinite(s[e]) ? __fadd_rn(s[e], err[e]) : s[e];
 }
 
 // (key, page) as one number, the larger the better: 32 key bits, then the
@@ -80,193 +102,284 @@ __device__ __forceinline__ uint64_t rank_of(uint32_t key, int c) {
     return ((uint64_t)key << kIndexBits) | (uint32_t)((1 << kIndexBits) - 1 - c);
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(SelectArgs a) {
+// Score of a page: lane j of eight holds dims 32 i + 4 j + c of its mean, at
+// m + 512 i bytes; g: the head's summed query. Every lane gets the score.
+__device__ __forceinline__ float page_score(const float *g, const unsigned char *m, int j) {
+    float x[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 u = *reinterpret_cast<const float4 *>(g + 32 * i + 4 * j);
+        const float4 v = *reinterpret_cast<const float4 *>(m + i * 512);
+        x[i][0] = __fmul_rn(u.x, v.x);
+        x[i][1] = __fmul_rn(u.y, v.y);
+        x[i][2] = __fmul_rn(u.z, v.z);
+        x[i][3] = __fmul_rn(u.w, v.w);
+    }
+    // 128 -> 64 -> 32: dims 64 and 32 apart; then neighbours
+    float y[4];
+#pragma unroll
+    for (int d = 0; d < 4; ++d) y[d] = __fadd_rn(__fadd_rn(x[0][d], x[2][d]), __fadd_rn(x[1][d], x[3][d]));
+    float r = __fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3]));
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
+    r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 2));
+    return __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 4));
+}
+// Four pages' means of one head into a ring stage; page: this lane's, -1: zeros.
+__device__ __forceinline__ void copy_means(uint32_t dst, const SelectArgs &a, int page, int head, int j) {
+    const float *src = a.mean + ((long long)max(page, 0) * a.p.Hkv + head) * kD + 4 * j;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + i * 512), "l"(src + 32 * i),
+                     "r"(page >= 0 ? 16 : 0)
+                     : "memory");
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(SelectArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
-    __shared__ int hist[kBins];
+    float *sq = reinterpret_cast<float *>(sm + kWarpsSel * kRingBytes);  // [kHeads][128] summed queries
+    const Paged &p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int hgroups = (p.Hkv + kHeads - 1) / kHeads;
+    grid_wait();
+    grid_go();
+    // a unit: four pages, the heads of one group
+    const Run run = find_run<kWarpsSel>(
+        p.B, [&](int b) -> long long { return (long long)((competing(a, b) + 3) / 4) * hgroups; }, kCtasSel, 1, 1);
+    long long before = run.before;
+    int b = run.n;
+    for (long long x = run.x0; x < run.x1 && b < p.B;) {
+        const int comp = competing(a, b), quads = (comp + 3) / 4;
+        if (x >= before + (long long)quads * hgroups) {
+            before += (long long)quads * hgroups;
+            ++b;
+            continue;
+        }
+        const int grp = (int)((x - before) / quads), q0 = (int)((x - before) % quads);
+        const int nq = (int)min((long long)(quads - q0), run.x1 - x);
+        const int h0 = grp * kHeads, hn = min(kHeads, p.Hkv - h0);
+        x += nq;
+        const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h0 * p.G * kD;
+        __syncthreads();  // the sums of the piece before were read
+        if (tid < hn * (kD / 8)) group_sum<T>(q + (long long)(tid >> 4) * p.G * kD + 8 * (tid & 15), p.G, sq + 8 * tid);
+
+        // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
+        const int sub = lane >> 3, j = lane & 7, items = nq * hn;
+        const uint32_t ring = ptx::smem_addr(sm) + wid * kRingBytes + lane * 16;
+        auto id_of = [&](int it) {
+            const int c = (q0 + it / hn) * 4 + sub;
+            return it < items && c < comp ? paged_id(p, b, a.first + c) : -1;
+        };
+        int id[kRing];  // page ids of the items in flight, by stage
+        auto copy = [&](int it, int stage, int page) { copy_means(ring + stage * 2048, a, page, h0 + it % hn, j); };
+#pragma unroll
+        for (int s = 0; s < kRing; ++s) id[s] = id_of(wid + s * kWarpsSel);
+#pragma unroll
+        for (int s = 0; s < kRing - 1; ++s) {
+            if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s, id[s]);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        }
+        __syncthreads();  // the sums are there
+        uint32_t *keys = a.keys + ((long long)b * p.Hkv + h0) * p.max_pages;
+        for (int n0 = 0; wid + n0 * kWarpsSel < items; n0 += kRing) {
+#pragma unroll
+            for (int s = 0; s < kRing; ++s) {
+                const int it = wid + (n0 + s) * kWarpsSel;
+                if (it >= items) break;
+                const int ahead = it + (kRing - 1) * kWarpsSel, sa = (s + kRing - 1) % kRing;
+                if (ahead < items) copy(ahead, sa, id[sa]);  // into the stage this lane read last
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+                const int hh = it % hn, c = (q0 + it / hn) * 4 + sub, page = id[s];
+                id[s] = id_of(it + kRing * kWarpsSel);
+                const float r = page_score(sq + hh * kD, sm + wid * kRingBytes + s * 2048 + lane * 16, j);
+                if (j == 0 && c < comp) keys[(long long)hh * p.max_pages + c] = order_key(page >= 0 ? r : -INFINITY);
+            }
+        }
+    }
+}
+
+// Rows with nothing to choose: every page.
+__device__ __forceinline__ void list_all(const SelectArgs &a, long long row, int pages) {
+    for (int n = threadIdx.x; n < a.topk; n += kThreads) a.idx[row * a.topk + n] = n < pages ? n : -1;
+    if (threadIdx.x == 0) a.cnt[row] = pages;
+}
+__device__ __forceinline__ void clear_bins(int (&hist)[kBins]) {
+    for (int e = threadIdx.x; e < kBins / 4; e += kThreads) reinterpret_cast<int4 *>(hist)[e] = make_int4(0, 0, 0, 0);
+}
+
+// Lists the pages of a row: the first and last ones that are always taken,
+// and the `take` best of the competing ones, whose keys are keys[0, comp).
+// Whole CTA; `hist` is clear.
+__device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, int pages, int comp, int (&hist)[kBins],
+                                           const uint32_t *keys) {
     __shared__ int wsum[kWarpsSel];
     __shared__ int s_bin, s_above, s_in, s_fill;
     __shared__ uint64_t s_cut;
     __shared__ uint64_t list[kRank];
-    uint32_t *mine = reinterpret_cast<uint32_t *>(sm);                   // [kCluster * cap] all keys of one head,
-                                                                         // where the rings were
-    float *sq = reinterpret_cast<float *>(sm + front_bytes(a.cap));      // [hg][128] summed queries
-    uint32_t *keys = reinterpret_cast<uint32_t *>(sq + a.hg * kD);       // [hg][cap] keys of this CTA's run
-    int *ids = reinterpret_cast<int *>(keys + (size_t)a.hg * a.cap);     // [cap] page ids of the run
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+    const int take = a.topk - a.first - a.last;
+    int *idx = a.idx + row * a.topk;
+    auto each = [&](auto f) {
+#pragma unroll 8
+        for (int c = tid; c < comp; c += kThreads) f(rank_of(keys[c], c));
+    };
+    // cut: the `take`-th largest rank (ranks are distinct); 2^59 when none is taken
+    uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
+    int rem = take, top = 32 + kIndexBits;  // bits [top, 59) of the cut are `prefix`
+    while (rem > 0) {
+        const int shift = max(top - 11, 0), bits = top - shift;
+        __syncthreads();  // the bins are clear (and the keys there)
+        each([&](uint64_t k) {
+            if (k >> top == prefix) atomicAdd(&hist[(int)((k >> shift) & ((1u << bits) - 1u))], 1);
+        });
+        __syncthreads();
+        // thread t: bins 2047 - 8 t down to 2040 - 8 t
+        int cnt[kBins / kThreads], sum = 0;
+#pragma unroll
+        for (int e = 0; e < kBins / kThreads; e += 4) {
+            const int4 n = *reinterpret_cast<const int4 *>(&hist[kBins - 4 - tid * (kBins / kThreads) - e]);
+            cnt[e] = n.w, cnt[e + 1] = n.z, cnt[e + 2] = n.y, cnt[e + 3] = n.x;
+            sum += n.x + n.y + n.z + n.w;
+        }
+        int inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) wsum[wid] = inc;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWarpsSel; ++w) inc += w < wid ? wsum[w] : 0;
+        int above = inc - sum;  // pages in larger bins
+        if (above < rem && inc >= rem) {
+#pragma unroll
+            for (int e = 0; e < kBins / kThreads; ++e)
+                if (above < rem) {
+                    s_bin = kBins - 1 - tid * (kBins / kThreads) - e;
+                    s_above = above;
+                    s_in = cnt[e];
+                    above += cnt[e];
+                }
+        }
+        if (tid == 0) s_fill = 0;
+        __syncthreads();
+        prefix = (prefix << bits) | (uint32_t)s_bin;
+        top = shift;
+        rem -= s_above;
+        const int in = s_in;
+        if (in == rem) {  // the whole bin
+            cut = prefix << top;
+            break;
+        }
+        if (in <= kRank) {
+            each([&](uint64_t k) {
+                if (k >> top == prefix) list[atomicAdd(&s_fill, 1)] = k;
+            });
+            __syncthreads();
+            if (tid < in) {
+                const uint64_t k = list[tid];
+                int larger = 0;
+                for (int e = 0; e < in; ++e) larger += list[e] > k ? 1 : 0;
+                if (larger == rem - 1) s_cut = k;
+            }
+            __syncthreads();
+            cut = s_cut;
+            break;
+        }
+        clear_bins(hist);
+    }
+    // pages at or above the cut, in order: each warp has a contiguous share
+    const int share = ((comp + kWarpsSel - 1) / kWarpsSel + 31) & ~31;
+    const int lo = min(wid * share, comp), hi = min(lo + share, comp);
+    auto chosen = [&](int c) { return rank_of(keys[c], c) >= cut; };
+    int n = 0;
+    for (int c = lo + lane; c - lane < hi; c += 32) n += __popc(__ballot_sync(0xffffffffu, c < hi && chosen(c)));
+    __syncthreads();  // wsum was read
+    if (lane == 0) wsum[wid] = n;
+    __syncthreads();
+    int at = a.first;
+#pragma unroll
+    for (int w = 0; w < kWarpsSel; ++w) at += w < wid ? wsum[w] : 0;
+    for (int c = lo + lane; c - lane < hi; c += 32) {
+        const bool on = c < hi && chosen(c);
+        const unsigned m = __ballot_sync(0xffffffffu, on);
+        if (on) idx[at + __popc(m & ((1u << lane) - 1u))] = a.first + c;
+        at += __popc(m);
+    }
+    for (int e = tid; e < a.first; e += kThreads) idx[e] = e;
+    for (int e = tid; e < a.last; e += kThreads) idx[a.topk - a.last + e] = pages - a.last + e;
+    if (tid == 0) a.cnt[row] = a.topk;
+}
+
+__global__ void __launch_bounds__(kThreads) k_page_topk(SelectArgs a) {
+    __shared__ __align__(16) int hist[kBins];
+    const Paged &p = a.p;
+    const long long row = blockIdx.x;
+    const int b = (int)(row / p.Hkv);
+    clear_bins(hist);
+    grid_wait();
+    grid_go();
+    const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2, comp = competing(a, b);
+    if (comp == 0)
+        list_all(a, row, pages);
+    else
+        list_pages(a, row, pages, comp, hist, a.keys + row * p.max_pages);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(SelectArgs a) {
+    extern __shared__ __align__(16) unsigned char sm[];
+    __shared__ __align__(16) int hist[kBins];
+    float *sq = reinterpret_cast<float *>(sm + kWarpsSel * kClusterRing);  // [hg][128] summed queries
+    uint32_t *mine = reinterpret_cast<uint32_t *>(sq + a.hg * kD);       // [kCluster * cap] keys of this CTA's head
+    int *ids = reinterpret_cast<int *>(mine + kCluster * a.cap);         // [cap] page ids of this CTA's run
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = (int)ptx::cluster_rank(), cl = (int)blockIdx.x / kCluster;
     const int b = cl / a.hgroups, h0 = (cl % a.hgroups) * a.hg, hn = min(a.hg, p.Hkv - h0);
+    clear_bins(hist);
     grid_wait();
     grid_go();
-    const int len = paged_len(p, b), pages = (len + p.page - 1) >> p.page_log2;
-    if (pages <= a.topk) {  // all of them: the same for every CTA of the cluster
-        for (int hh = rank; hh < hn; hh += kCluster) {
-            const long long row = (long long)b * p.Hkv + h0 + hh;
-            for (int n = tid; n < a.topk; n += kThreads) a.idx[row * a.topk + n] = n < pages ? n : -1;
-            if (tid == 0) a.cnt[row] = pages;
-        }
+    const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2;
+    const int comp = competing(a, b);
+    if (comp == 0) {  // the same for every CTA of the cluster
+        if (rank < hn) list_all(a, (long long)b * p.Hkv + h0 + rank, pages);
         return;
     }
-    // Competing pages c = j - first, 0 <= c < comp: every one is full, since the partial page is the last.
-    const int comp = pages - a.first - a.last, take = a.topk - a.first - a.last;
     const int run = (comp + kCluster - 1) / kCluster;
     const int c0 = min(rank * run, comp), nc = min(run, comp - c0);
 
     for (int c = tid; c < nc; c += kThreads) ids[c] = paged_id(p, b, a.first + c0 + c);
     const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h0 * p.G * kD;
-    for (int e = tid; e < hn * kD; e += kThreads)
-        sq[e] = group_sum<T>(q + (long long)(e / kD) * p.G * kD + e % kD, p.G);
-    __syncthreads();
+    if (tid < hn * (kD / 8)) group_sum<T>(q + (long long)(tid >> 4) * p.G * kD + 8 * (tid & 15), p.G, sq + 8 * tid);
+    ptx::cluster_sync();  // every CTA of the cluster runs: their shared memory may be written
 
     // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
     const int sub = lane >> 3, j = lane & 7, items = (nc + 3) / 4 * hn;
-    const uint32_t ring = ptx::smem_addr(sm) + wid * kRingBytes + lane * 16;
+    const uint32_t ring = ptx::smem_addr(sm) + wid * kClusterRing + lane * 16;
     auto copy = [&](int it, int stage) {
-        const int hh = it % hn, c = it / hn * 4 + sub;
-        const int id = c < nc ? ids[c] : -1;
-        const float *src = a.mean + ((long long)max(id, 0) * p.Hkv + h0 + hh) * kD + 4 * j;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(ring + stage * 2048 + i * 512),
-                         "l"(src + 32 * i), "r"(id >= 0 ? 16 : 0)
-                         : "memory");
+        const int c = it / hn * 4 + sub;
+        copy_means(ring + stage * 2048, a, c < nc ? ids[c] : -1, h0 + it % hn, j);
     };
 #pragma unroll
-    for (int s = 0; s < kRing - 1; ++s) {
+    for (int s = 0; s < kClusterStages - 1; ++s) {
         if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
     for (int n = 0; wid + n * kWarpsSel < items; ++n) {
         const int it = wid + n * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
-        const int ahead = it + (kRing - 1) * kWarpsSel;
-        if (ahead < items) copy(ahead, (n + kRing - 1) % kRing);  // the stage this lane read last
+        const int ahead = it + (kClusterStages - 1) * kWarpsSel;
+        if (ahead < items) copy(ahead, (n + kClusterStages - 1) % kClusterStages);  // the stage this lane read last
         asm volatile("cp.async.commit_group;" ::: "memory");
-        asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-        float x[4][4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float4 g = *reinterpret_cast<const float4 *>(sq + hh * kD + 32 * i + 4 * j);
-            const float4 m = *reinterpret_cast<const float4 *>(sm + wid * kRingBytes + (n % kRing) * 2048 + i * 512 +
-                                                               lane * 16);
-            x[i][0] = __fmul_rn(g.x, m.x);
-            x[i][1] = __fmul_rn(g.y, m.y);
-            x[i][2] = __fmul_rn(g.z, m.z);
-            x[i][3] = __fmul_rn(g.w, m.w);
-        }
-        // 128 -> 64 -> 32: dims 64 and 32 apart; then neighbours
-        float y[4];
-#pragma unroll
-        for (int d = 0; d < 4; ++d) y[d] = __fadd_rn(__fadd_rn(x[0][d], x[2][d]), __fadd_rn(x[1][d], x[3][d]));
-        float r = __fadd_rn(__fadd_rn(y[0], y[1]), __fadd_rn(y[2], y[3]));
-        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 1));
-        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 2));
-        r = __fadd_rn(r, __shfl_xor_sync(0xffffffffu, r, 4));
-        if (j == 0 && c < nc) keys[hh * a.cap + c] = order_key(ids[c] >= 0 ? r : -INFINITY);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kClusterStages - 1) : "memory");
+        const float r = page_score(sq + hh * kD, sm + wid * kClusterRing + (n % kClusterStages) * 2048 + lane * 16, j);
+        if (j == 0 && c < nc)
+            st_cluster(ptx::cluster_addr(ptx::smem_addr(mine + c0 + c), hh), order_key(ids[c] >= 0 ? r : -INFINITY));
     }
     ptx::cluster_sync();  // every run's keys are there
+    if (rank >= hn) return;
 
-    for (int hh = rank; hh < hn; hh += kCluster) {
-        const long long row = (long long)b * p.Hkv + h0 + hh;
-        int *idx = a.idx + row * a.topk;
-        const uint32_t base = ptx::smem_addr(keys + (size_t)hh * a.cap);
-        // the head's keys from all runs, in page order
-#pragma unroll
-        for (int r = 0; r < kCluster; ++r) {
-            const uint32_t at = ptx::cluster_addr(base, r);
-            const int n = min(run, comp - r * run);
-            for (int c = tid; c < n; c += kThreads) mine[r * run + c] = ld_cluster(at + 4 * c);
-        }
-        __syncthreads();
-        auto each = [&](auto f) {
-            for (int c = tid; c < comp; c += kThreads) f(rank_of(mine[c], c));
-        };
-        // cut: the `take`-th largest rank (ranks are distinct); 2^54 when none is taken
-        uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
-        int rem = take, top = 32 + kIndexBits;  // bits [top, 54) of the cut are `prefix`
-        while (rem > 0) {
-            const int shift = max(top - 11, 0), bits = top - shift;
-            for (int e = tid; e < kBins; e += kThreads) hist[e] = 0;
-            __syncthreads();
-            each([&](uint64_t k) {
-                if (k >> top == prefix) atomicAdd(&hist[(int)((k >> shift) & ((1u << bits) - 1u))], 1);
-            });
-            __syncthreads();
-            // thread t: bins 2047 - 8 t down to 2040 - 8 t
-            int cnt[kBins / kThreads], sum = 0;
-#pragma unroll
-            for (int e = 0; e < kBins / kThreads; ++e) sum += cnt[e] = hist[kBins - 1 - tid * (kBins / kThreads) - e];
-            int inc = sum;
-#pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int y = __shfl_up_sync(0xffffffffu, inc, off);
-                if (lane >= off) inc += y;
-            }
-            if (lane == 31) wsum[wid] = inc;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < kWarpsSel; ++w) inc += w < wid ? wsum[w] : 0;
-            int above = inc - sum;  // pages in larger bins
-            if (above < rem && inc >= rem) {
-#pragma unroll
-                for (int e = 0; e < kBins / kThreads; ++e)
-                    if (above < rem) {
-                        s_bin = kBins - 1 - tid * (kBins / kThreads) - e;
-                        s_above = above;
-                        s_in = cnt[e];
-                        above += cnt[e];
-                    }
-            }
-            if (tid == 0) s_fill = 0;
-            __syncthreads();
-            prefix = (prefix << bits) | (uint32_t)s_bin;
-            top = shift;
-            rem -= s_above;
-            const int in = s_in;
-            if (in == rem) {  // the whole bin
-                cut = prefix << top;
-                break;
-            }
-            if (in <= kRank) {
-                each([&](uint64_t k) {
-                    if (k >> top == prefix) list[atomicAdd(&s_fill, 1)] = k;
-                });
-                __syncthreads();
-                if (tid < in) {
-                    const uint64_t k = list[tid];
-                    int larger = 0;
-                    for (int e = 0; e < in; ++e) larger += list[e] > k ? 1 : 0;
-                    if (larger == rem - 1) s_cut = k;
-                }
-                __syncthreads();
-                cut = s_cut;
-                break;
-            }
-            __syncthreads();  // s_bin and the bins are read before the next digit
-        }
-        // pages at or above the cut, in order: each warp has a contiguous share
-        const int share = ((comp + kWarpsSel - 1) / kWarpsSel + 31) & ~31;
-        const int lo = min(wid * share, comp), hi = min(lo + share, comp);
-        auto chosen = [&](int c) { return rank_of(mine[c], c) >= cut; };
-        int n = 0;
-        for (int c = lo + lane; c - lane < hi; c += 32) n += __popc(__ballot_sync(0xffffffffu, c < hi && chosen(c)));
-        __syncthreads();  // wsum was read
-        if (lane == 0) wsum[wid] = n;
-        __syncthreads();
-        int at = a.first;
-#pragma unroll
-        for (int w = 0; w < kWarpsSel; ++w) at += w < wid ? wsum[w] : 0;
-        for (int c = lo + lane; c - lane < hi; c += 32) {
-            const bool on = c < hi && chosen(c);
-            const unsigned m = __ballot_sync(0xffffffffu, on);
-            if (on) idx[at + __popc(m & ((1u << lane) - 1u))] = a.first + c;
-            at += __popc(m);
-        }
-        for (int e = tid; e < a.first; e += kThreads) idx[e] = e;
-        for (int e = tid; e < a.last; e += kThreads) idx[a.topk - a.last + e] = pages - a.last + e;
-        if (tid == 0) a.cnt[row] = a.topk;
-        __syncthreads();  // the bins and sums serve the next head
-    }
-    ptx::cluster_sync();  // no CTA leaves while another reads its keys
+    list_pages(a, (long long)b * p.Hkv + h0 + rank, pages, comp, hist, mine);
 }
 
 }  // namespace
@@ -274,7 +387,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
 
 extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride,
                                       const float *k_mean, int topk, int keep_first, int keep_last,
-                                      int32_t *page_idx, int32_t *page_cnt, vsa_stream_t stream) {
+                                      int32_t *page_idx, int32_t *page_cnt, void *workspace, size_t workspace_bytes,
+                                      vsa_stream_t stream) {
     using namespace vsa;
     SelectArgs a{};
     const vsa_status st = to_paged(desc, &a.p, true);
@@ -283,6 +397,8 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     if (keep_first < 0 || keep_last < 1 || topk < 1 || (long long)keep_first + keep_last > topk) return VSA_ERR_SHAPE;
     if (!q || !k_mean || !page_idx || !page_cnt) return VSA_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_mean) || ((uintptr_t)page_idx | (uintptr_t)page_cnt) & 3u) return VSA_ERR_LAYOUT;
+    const PagedWs ws = paged_ws(a.p);
+    if (!workspace || ((uintptr_t)workspace & 255u) || workspace_bytes < ws.total) return VSA_ERR_WORKSPACE;
     a.q = q;
     a.mean = k_mean;
     a.topk = topk;
@@ -290,27 +406,33 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     a.last = keep_last;
     a.idx = page_idx;
     a.cnt = page_cnt;
+    a.keys = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + ws.keys);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool bf = a.p.dtype == T_BF16;
+    auto run = [&](const char *name, auto kernel, dim3 grid, size_t smem, unsigned cluster) {
+        cudaError_t e = ensure_smem_limit((const void *)kernel, (int)smem);
+        if (e != cudaSuccess) return status_from_cuda(e);
+        prof_begin(name, s);
+        e = launch_paged(kernel, grid, kThreads, smem, cluster, a, s);
+        prof_end(s);
+        return status_from_cuda(e);
+    };
     // Heads per cluster: as many as still leave a CTA for every SM.
     a.hg = 8;
     while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
         a.hg /= 2;
-    a.cap = (std::min(a.p.max_pages, 1 << kIndexBits) + kCluster - 1) / kCluster;
-    auto bytes = [&] {
-        return front_bytes(a.cap) + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (a.hg + 1);
-    };
-    while (a.hg > 1 && bytes() > kMaxSmem) a.hg /= 2;
-    if (a.p.max_pages > (1 << kIndexBits) || bytes() > kMaxSmem) return VSA_ERR_UNSUPPORTED;
     a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
     const long long ctas = (long long)a.p.B * a.hgroups * kCluster;
-    if (ctas > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool bf = a.p.dtype == T_BF16;
-    const void *fn = bf ? (const void *)k_page_select<__nv_bfloat16> : (const void *)k_page_select<__half>;
-    const cudaError_t ae = ensure_smem_limit(fn, kMaxSmem);
-    if (ae != cudaSuccess) return status_from_cuda(ae);
-    prof_begin("page_select", s);
-    const cudaError_t e = launch_paged(bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
-                                       kThreads, bytes(), kCluster, a, s);
-    prof_end(s);
-    return status_from_cuda(e);
+    if ((long long)a.p.max_pages * a.hg <= kClusterPages && ctas <= kCtasSel) {
+        a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
+        const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
+        return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas), smem,
+                   kCluster);
+    }
+    if (a.p.max_pages > topk) {  // otherwise no row has anything to choose
+        const vsa_status e = run("page_scores", bf ? k_page_scores<__nv_bfloat16> : k_page_scores<__half>,
+                                 dim3(kCtasSel), kSmemSel, 1);
+        if (e != VSA_OK) return e;
+    }
+    return run("page_topk", k_page_topk, dim3((unsigned)(a.p.B * a.p.Hkv)), 0, 1);
 }

@@ -154,7 +154,8 @@ def lib():
         L.vsa_paged_append.argtypes = [C.POINTER(PagedDesc), C.c_int, P, i64, P, i64, P, i64, P, P, P, P, P, C.c_int,
                                        C.c_int, C.c_int, P, P, P, P]
         L.vsa_page_select.restype = C.c_int
-        L.vsa_page_select.argtypes = [C.POINTER(PagedDesc), P, i64, P, C.c_int, C.c_int, C.c_int, P, P, P]
+        L.vsa_page_select.argtypes = [C.POINTER(PagedDesc), P, i64, P, C.c_int, C.c_int, C.c_int, P, P, P, C.c_size_t,
+                                      P]
         L.vsa_paged_attn.restype = C.c_int
         L.vsa_paged_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
         _lib = L
@@ -787,7 +788,7 @@ class PagedCache:
             if page_idx.shape[2] != topk:
                 raise ValueError(f"page_idx: expected topk = {topk} entries per row")
         self._run("vsa_page_select", stream, q.data_ptr(), qs, self._mean, topk, keep_first, keep_last,
-                  page_idx.data_ptr(), page_cnt.data_ptr())
+                  page_idx.data_ptr(), page_cnt.data_ptr(), self._ws, self._ws_bytes)
         return page_idx, page_cnt
 
     def attend(self, q, pages=None, out=None, lse=None, stream=None):

@@ -490,8 +490,8 @@ typedef struct {
     float scale;          /* softmax scale on q.k; 0 means 1/sqrt(D) */
 } vsa_paged_desc;
 
-/* Bytes of workspace for vsa_paged_attn on this problem (256-byte aligned;
- * 0 for an invalid descriptor). It holds nothing between calls and needs no
+/* Bytes of workspace for vsa_page_select and vsa_paged_attn on this problem
+ * (256-byte aligned; 0 for an invalid descriptor). It holds nothing between calls and needs no
  * clearing; calls that share it must not run concurrently. The page_table
  * and seq_lens pointers are not looked at. */
 size_t vsa_paged_workspace_size(const vsa_paged_desc *desc);
@@ -551,11 +551,11 @@ vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, in
  * them); the rest of min(topk, pages) by (r desc, j asc).
  * Writes page_idx [B, Hkv, topk] int32, ascending, unused entries -1, and
  * page_cnt [B, Hkv]. topk >= keep_first + keep_last. The result is the
- * same bit for bit on every run. Errors as for vsa_paged_append;
- * VSA_ERR_UNSUPPORTED when max_pages is over 40,856. */
+ * same bit for bit on every run. Errors as for vsa_paged_append, and
+ * VSA_ERR_WORKSPACE. */
 vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const float *k_mean,
                            int topk, int keep_first, int keep_last, int32_t *page_idx, int32_t *page_cnt,
-                           vsa_stream_t stream);
+                           void *workspace, size_t workspace_bytes, vsa_stream_t stream);
 
 /* Attention of one token per sequence over the cache: q [B, Hq, D]
  * (q_stride as above), out [B, Hq, D] dense, lse fp32 [B, Hq] (natural
@@ -565,8 +565,8 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
  * twice counts twice). A row without keys gets O = 0, LSE = -inf. The work
  * of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
- * bit on every run with the same batch. Errors as for vsa_page_select, and
- * VSA_ERR_WORKSPACE; VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1. */
+ * bit on every run with the same batch. Errors as for vsa_page_select;
+ * VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1. */
 vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
                           const void *v_cache, const int32_t *page_idx, const int32_t *page_cnt, int idx_cap,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, vsa_stream_t stream);

@@ -43,7 +43,7 @@ def append(L, d=None, **kw):
 
 
 def select(L, d=None, **kw):
-    a = dict(q=FAKE, qs=0, mean=FAKE, topk=2, first=0, last=1, idx=FAKE, cnt=FAKE)
+    a = dict(q=FAKE, qs=0, mean=FAKE, topk=2, first=0, last=1, idx=FAKE, cnt=FAKE, ws=FAKE, wsb=1 << 40)
     a.update(kw)
     return L.vsa_page_select(C.byref(d or desc()), *a.values(), None)
 
@@ -92,7 +92,8 @@ def test_select_errors(L):
     assert select(L, topk=3, first=2, last=2) == 2
     assert select(L, first=2 ** 31 - 1, last=2 ** 31 - 1) == 2
     assert select(L, qs=8) == 2
-    assert select(L, desc(max_pages=40857)) == 5    # more pages than the cluster's shared memory holds keys for
+    need = L.vsa_paged_workspace_size(C.byref(desc()))
+    assert select(L, wsb=need - 1) == 7 and select(L, ws=None) == 7 and select(L, ws=C.c_void_p((1 << 20) + 128)) == 7
 
 
 def test_attend_errors(L):
@@ -110,6 +111,7 @@ def test_attend_errors(L):
 
 def test_workspace_grows_with_the_problem(L):
     size = lambda **kw: L.vsa_paged_workspace_size(C.byref(desc(**kw)))  # noqa: E731
+    assert size(max_pages=4000) > size()
     assert size(Hq=32) > size()
     assert size(B=300) > size()
 
