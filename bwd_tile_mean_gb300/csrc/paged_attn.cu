@@ -3,8 +3,9 @@
 //
 //   O = sum_u P_u v_u / sum_u P_u,  P_u = exp(scale q.k_u - max)
 //
-// A segment is one (sequence, key/value head, chunk of up to 16 MT query
-// heads of its group); its keys, in the order of the pages attended, are
+// A segment is one (sequence, key/value head, chunk of up to 16 query heads
+// of its group: one tile of the tensor instructions; a wider group's chunks
+// read the same keys, from L2 but for the first); its keys, in the order of the pages attended, are
 // cut into blocks of 16. The blocks of all segments, end to end, are dealt
 // to the grid's warps in equal contiguous runs, whatever the lengths of the
 // batch: a CTA finds its run with one scan of the lengths, and each warp
@@ -36,9 +37,11 @@ namespace vsa {
 namespace {
 
 constexpr int kBlk = 16;        // keys per warp step
-constexpr int kLead = 1;        // blocks a segment counts for beyond its own (its start-up time)
+constexpr int kRows = 16;       // query heads per segment at most
+constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time)
 constexpr int kMinBlocks = 4;   // fewest blocks a warp's run has when there is little work
-constexpr int kAlignedKeys = 1024;  // keys per CTA up to which a segment is one CTA's or one cluster's
+constexpr int kAlignedKeys = 2048;  // keys per CTA up to which a segment is one CTA's or one cluster's
+constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
 constexpr int kMaxCluster = 8;
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // ring stages per warp
@@ -126,10 +129,10 @@ __device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) {
     return nb > 0 ? nb + a.lead : 0;
 }
 
-template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
+template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_m[kWarps][16 * MT], s_l[kWarps][16 * MT];
-    __shared__ float2 s_cta[16 * MT];  // the CTA's own maximum and sum, for its cluster
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
+    __shared__ float2 s_cta[kRows];  // the CTA's own maximum and sum, for its cluster
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     grid_wait();
@@ -203,21 +206,19 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         const long long hoff = (long long)h * p.head_stride;
 
         // Q as A fragments: row g (and g + 8) of each 16-row tile, 8 k-steps
-        uint32_t qa[MT][8][4];
+        uint32_t qa[8][4];
         {
             const T *qb = Q + (long long)b * a.qs + ((long long)h * p.G + r * a.rows) * kD;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
+            for (int e = 0; e < 2; ++e) {
+                const int row = g + 8 * e;
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = m * 16 + g + 8 * e;
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        qa[m][j][e] = row < rows ? __ldg(src + 8 * j + t) : 0u;
-                        qa[m][j][2 + e] = row < rows ? __ldg(src + 8 * j + 4 + t) : 0u;
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    qa[j][e] = row < rows ? __ldg(src + 8 * j + t) : 0u;
+                    qa[j][2 + e] = row < rows ? __ldg(src + 8 * j + 4 + t) : 0u;
                 }
+            }
         }
 
         // Window of up to 32 blocks, one per lane: the page (or -1), the
@@ -264,16 +265,11 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         }
         valid[kStages - 1] = 0;
 
-        float m_run[MT][2], l_run[MT][2], acc[MT][16][4];
+        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, acc[16][4];  // rows g and g + 8
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            m_run[m][0] = m_run[m][1] = -INFINITY;
-            l_run[m][0] = l_run[m][1] = 0.f;
+        for (int j = 0; j < 16; ++j)
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[m][j][e] = 0.f;
-        }
+            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
         for (int i0 = 0; i0 < take; i0 += kStages) {
 #pragma unroll
             for (int s = 0; s < kStages; ++s) {
@@ -285,86 +281,71 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
                     valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
                 cp_commit();
                 const uint32_t st = ring + s * kStageBytes;
-                float sc[MT][2][4];
+                float sc[2][4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[m][0][e] = sc[m][1][e] = 0.f;
+                for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
                 {
                     const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         uint32_t kb[4];
                         ldsm4(kb, st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            mma16816<T>(sc[m][0], qa[m][j], kb[0], kb[1]);
-                            mma16816<T>(sc[m][1], qa[m][j], kb[2], kb[3]);
-                        }
+                        mma16816<T>(sc[0], qa[j], kb[0], kb[1]);
+                        mma16816<T>(sc[1], qa[j], kb[2], kb[3]);
                     }
                 }
                 const int ok = valid[s];
-                uint32_t pa[MT][4];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = 8 * u + 2 * t + (e & 1);
+                        sc[u][e] = key < ok ? sc[u][e] * sl2 : -INFINITY;
+                    }
+                float corr[2];
+                bool moved = false;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(fmaxf(sc[0][2 * e], sc[0][2 * e + 1]), fmaxf(sc[1][2 * e], sc[1][2 * e + 1]));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                    const float mn = fmaxf(m_run[e], mx);
+                    const float ref = mn == -INFINITY ? 0.f : mn;  // a row without keys so far
+                    corr[e] = ptx::ex2(m_run[e] - ref);
+                    moved = moved || mn != m_run[e];
+                    m_run[e] = mn;
+                    float sum = 0.f;
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const int key = 8 * u + 2 * t + (e & 1);
-                            sc[m][u][e] = key < ok ? sc[m][u][e] * sl2 : -INFINITY;
+                        for (int c = 0; c < 2; ++c) {
+                            const float pr = ptx::ex2(sc[u][2 * e + c] - ref);
+                            sc[u][2 * e + c] = pr;
+                            sum += pr;
                         }
-                    float corr[2];
-                    bool moved = false;
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {  // rows g and g + 8
-                        float mx = fmaxf(fmaxf(sc[m][0][2 * e], sc[m][0][2 * e + 1]),
-                                         fmaxf(sc[m][1][2 * e], sc[m][1][2 * e + 1]));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                        const float mn = fmaxf(m_run[m][e], mx);
-                        const float ref = mn == -INFINITY ? 0.f : mn;  // a row without keys so far
-                        corr[e] = ptx::ex2(m_run[m][e] - ref);
-                        moved = moved || mn != m_run[m][e];
-                        m_run[m][e] = mn;
-                        float sum = 0.f;
-#pragma unroll
-                        for (int u = 0; u < 2; ++u)
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                const float pr = ptx::ex2(sc[m][u][2 * e + c] - ref);
-                                sc[m][u][2 * e + c] = pr;
-                                sum += pr;
-                            }
-                        l_run[m][e] = l_run[m][e] * corr[e] + sum;  // this lane's keys; quads are joined at the end
-                    }
-                    if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            acc[m][j][0] *= corr[0];
-                            acc[m][j][1] *= corr[0];
-                            acc[m][j][2] *= corr[1];
-                            acc[m][j][3] *= corr[1];
-                        }
-                    }
-                    // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps
-                    // the unrounded values): half a step of the output's own type
-                    pa[m][0] = pack2<T>(sc[m][0][0], sc[m][0][1]);
-                    pa[m][1] = pack2<T>(sc[m][0][2], sc[m][0][3]);
-                    pa[m][2] = pack2<T>(sc[m][1][0], sc[m][1][1]);
-                    pa[m][3] = pack2<T>(sc[m][1][2], sc[m][1][3]);
+                    l_run[e] = l_run[e] * corr[e] + sum;  // this lane's keys; quads are joined at the end
                 }
+                if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        acc[j][0] *= corr[0];
+                        acc[j][1] *= corr[0];
+                        acc[j][2] *= corr[1];
+                        acc[j][3] *= corr[1];
+                    }
+                }
+                // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the
+                // unrounded values): half a step of the output's own type
+                const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
+                                        pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
                 {
                     const int row = (lane & 7) + ((lane >> 3) & 1) * 8, c0 = lane >> 4;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         uint32_t vb[4];
                         ldsm4t(vb, st + kBlk * 256 + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-#pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            mma16816<T>(acc[m][2 * j], pa[m], vb[0], vb[1]);
-                            mma16816<T>(acc[m][2 * j + 1], pa[m], vb[2], vb[3]);
-                        }
+                        mma16816<T>(acc[2 * j], pa, vb[0], vb[1]);
+                        mma16816<T>(acc[2 * j + 1], pa, vb[2], vb[3]);
                     }
                 }
             }
@@ -372,12 +353,10 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         cp_wait<0>();
         __syncwarp();  // the warp's ring is free
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 1);
-                l_run[m][e] += __shfl_xor_sync(0xffffffffu, l_run[m][e], 2);
-            }
+        for (int e = 0; e < 2; ++e) {
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
+            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
+        }
         const long long hq0 = (long long)b * p.Hq + h * p.G + r * a.rows;  // first output row of the segment
 
         // A piece of the segment that begins it describes all of its pieces.
@@ -401,20 +380,18 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
         if (joined) {  // the warps' outputs in shared memory, one thread per dim
             float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const int row = m * 16 + g + 8 * e;
-                    if (t == 0) {
-                        s_m[wid][row] = m_run[m][e];
-                        s_l[wid][row] = l_run[m][e];
-                    }
-                    if (row < rows)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
-                                make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
+            for (int e = 0; e < 2; ++e) {
+                const int row = g + 8 * e;
+                if (t == 0) {
+                    s_m[wid][row] = m_run[e];
+                    s_l[wid][row] = l_run[e];
                 }
+                if (row < rows)
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
+                            make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+            }
             __syncthreads();
             for (int row = 0; row < rows; ++row) {
                 float M = -INFINITY;
@@ -471,107 +448,147 @@ template <typename T, int MT> __global__ void __launch_bounds__(kWarps * 32) k_p
             return;
         }
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
+        for (int e = 0; e < 2; ++e) {
+            const int row = g + 8 * e;
+            if (row >= rows) continue;
+            const float l = l_run[e];
+            if (first && last) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (hq0 + row) * kD);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = m * 16 + g + 8 * e;
-                if (row >= rows) continue;
-                const float l = l_run[m][e];
-                if (first && last) {
-                    const float inv = l == 0.f ? 0.f : 1.f / l;
-                    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (hq0 + row) * kD);
+                for (int j = 0; j < 16; ++j) dst[4 * j + t] = pack2<T>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
+                if (t == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (m_run[e] + log2f(l));
+            } else {
+                float *dst = a.o + (slot * a.rows + row) * kD;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        dst[4 * j + t] = pack2<T>(acc[m][j][2 * e] * inv, acc[m][j][2 * e + 1] * inv);
-                    if (t == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (m_run[m][e] + log2f(l));
-                } else {
-                    float *dst = a.o + (slot * a.rows + row) * kD;
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t) =
-                            make_float2(acc[m][j][2 * e], acc[m][j][2 * e + 1]);
-                    if (t == 0) a.ml[slot * a.rows + row] = make_float2(m_run[m][e], l);
-                }
+                for (int j = 0; j < 16; ++j)
+                    *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+                if (t == 0) a.ml[slot * a.rows + row] = make_float2(m_run[e], l);
             }
+        }
         more = x < x_end;
     }
 }
 
-// One CTA per (sequence, query head): writes the rows without keys and
-// joins the pieces of the segments that crossed runs, in ascending order of
-// their keys within each warp, then the warps in order.
-template <typename T> __global__ void __launch_bounds__(128) k_paged_join(AttnArgs a) {
-    __shared__ float s_m[4], s_l[4];
-    __shared__ __align__(16) float s_o[4][kD];
+// Writes the rows (sequence, query head) without keys and joins the pieces
+// of the segments that crossed runs: W warps per row, R rows per CTA. The
+// pieces' weights come first, all at once; then the warps take turns on the
+// pieces, each with kJoinDeep loads in flight, and their sums are added in
+// order. Many rows have few pieces each, few rows many: kJoinFew rows and
+// fewer get 16 warps each, kJoinMany and more one.
+constexpr int kJoinDeep = 8, kJoinFew = 152, kJoinMany = 1024;
+template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32) k_paged_join(AttnArgs a) {
+    static_assert(W == 1 || R == 1, "a row's warps meet at the CTA's barrier");
+    __shared__ float s_wt[R][kCtas * kWarps], s_red[W], s_sum[W];
+    __shared__ __align__(16) float s_o[W][kD];
     const Paged &p = a.p;
-    const int row = blockIdx.x, b = row / p.Hq, hq = row % p.Hq, h = hq / p.G, in = hq % p.G;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int bh = b * p.Hkv + h;
-    T *out = static_cast<T *>(a.out) + (long long)row * kD;
+    const int lane = threadIdx.x & 31, wid = R > 1 ? 0 : (int)threadIdx.x >> 5;  // warp of the row
+    const int team = R > 1 ? (int)threadIdx.x >> 5 : 0, tid = wid * 32 + lane;
+    const int row = blockIdx.x * R + team;
     grid_wait();
     grid_go();
+    if (row >= p.B * p.Hq) return;
+    const int b = row / p.Hq, hq = row % p.Hq, h = hq / p.G, in = hq % p.G;
+    const int bh = b * p.Hkv + h;
+    float *s_w = s_wt[team];
+    T *out = static_cast<T *>(a.out) + (long long)row * kD;
+    const int4 sg = a.seg[(long long)bh * a.rc + in / a.rows];  // not written for a segment without keys
     if (seg_keys(a, a.idx ? bh : b) == 0) {
-        out[tid] = from_f<T>(0.f);
+        for (int d = tid; d < kD; d += W * 32) out[d] = from_f<T>(0.f);
         if (tid == 0) a.lse[row] = -INFINITY;
         return;
     }
-    const int4 sg = a.seg[(long long)bh * a.rc + in / a.rows];
     if (sg.w == 1) return;  // finished where it was computed
-    const int r = in % a.rows;
-    float M = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i = wid; i < sg.w; i += 4) {
-        // warps before the first joined CTA, joined CTAs (at their first warp's place), warps after
+    const int r = in % a.rows, pieces = min(sg.w, kCtas * kWarps);
+    // warps before the first joined CTA, joined CTAs (at their first warp's place), warps after
+    auto place = [&](int i) {
         const int w = i < sg.y ? sg.x + i : (i < sg.y + sg.z ? sg.x + sg.y + (i - sg.y) * kWarps
                                                             : sg.x + i + sg.z * (kWarps - 1));
-        const long long at = (2LL * w + (i == 0 ? 1 : 0)) * a.rows + r;
-        const float2 ml = a.ml[at];
-        const float4 x = *reinterpret_cast<const float4 *>(a.o + at * kD + 4 * lane);
-        const float mn = fmaxf(M, ml.x), ref = mn == -INFINITY ? 0.f : mn;
-        const float f = ptx::ex2(M - ref), e = ptx::ex2(ml.x - ref);
-        M = mn;
-        l = l * f + ml.y * e;
-        o.x = o.x * f + x.x * e;
-        o.y = o.y * f + x.y * e;
-        o.z = o.z * f + x.z * e;
-        o.w = o.w * f + x.w * e;
+        return (2LL * w + (i == 0 ? 1 : 0)) * a.rows + r;
+    };
+    float M = -INFINITY;
+    for (int i = tid; i < pieces; i += W * 32) {
+        s_w[i] = a.ml[place(i)].x;
+        M = fmaxf(M, s_w[i]);
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    if (W > 1) {
+        if (lane == 0) s_red[wid] = M;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) M = fmaxf(M, s_red[w]);
+    }
+    const float ref = M == -INFINITY ? 0.f : M;
+    float l = 0.f;
+    for (int i = tid; i < pieces; i += W * 32) {  // the thread's own entries again
+        const float e = ptx::ex2(s_w[i] - ref);
+        s_w[i] = e;
+        l += e * a.ml[place(i)].y;
+    }
+#pragma unroll
+    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    if (W > 1) {
+        if (lane == 0) s_sum[wid] = l;
+        __syncthreads();
+    } else {
+        __syncwarp();
+    }
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = wid; i0 < pieces; i0 += W * kJoinDeep) {
+        float4 x[kJoinDeep];
+#pragma unroll
+        for (int e = 0; e < kJoinDeep; ++e)
+            x[e] = i0 + e * W < pieces ? *reinterpret_cast<const float4 *>(a.o + place(i0 + e * W) * kD + 4 * lane)
+                                       : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < kJoinDeep; ++e) {
+            const float f = i0 + e * W < pieces ? s_w[i0 + e * W] : 0.f;
+            o.x += f * x[e].x;
+            o.y += f * x[e].y;
+            o.z += f * x[e].z;
+            o.w += f * x[e].w;
+        }
+    }
+    if (W == 1) {
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+        return;
     }
     *reinterpret_cast<float4 *>(&s_o[wid][4 * lane]) = o;
-    if (lane == 0) {
-        s_m[wid] = M;
-        s_l[wid] = l;
-    }
     __syncthreads();
-    M = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
-    const float ref = M == -INFINITY ? 0.f : M;
+    if (tid >= kD) return;
     float sum = 0.f, val = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        const float e = ptx::ex2(s_m[w] - ref);
-        sum += e * s_l[w];
-        val += e * s_o[w][tid];
+    for (int w = 0; w < W; ++w) {
+        sum += s_sum[w];
+        val += s_o[w][tid];
     }
     out[tid] = from_f<T>(sum == 0.f ? 0.f : val / sum);
     if (tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (M + log2f(sum));
 }
 
-// Query heads of a group are taken 16 at a time, 32 when there are more.
-int rows_of(int G) { return G <= 16 ? G : (G <= 32 ? G : 32); }
+// Rows per chunk of a group of G query heads: equal chunks of up to 16.
+int rows_of(int G) {
+    const int chunks = (G + kRows - 1) / kRows;
+    return (G + chunks - 1) / chunks;
+}
 
 template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
-    const bool one = a.rows <= 16;
-    const void *fn = one ? (const void *)k_paged_attn<T, 1> : (const void *)k_paged_attn<T, 2>;
-    const cudaError_t ae = ensure_smem_limit(fn, kSmem);
+    const cudaError_t ae = ensure_smem_limit((const void *)k_paged_attn<T>, kSmem);
     if (ae != cudaSuccess) return status_from_cuda(ae);
     const unsigned grid = a.aligned ? (unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.aligned) : kCtas;
     const unsigned cluster = a.aligned > 1 ? a.aligned : 1;
     prof_begin("paged_attn", s);
-    cudaError_t e = one ? launch_paged(k_paged_attn<T, 1>, grid, kWarps * 32, kSmem, cluster, a, s)
-                        : launch_paged(k_paged_attn<T, 2>, grid, kWarps * 32, kSmem, cluster, a, s);
+    cudaError_t e = launch_paged(k_paged_attn<T>, grid, kWarps * 32, kSmem, cluster, a, s);
     prof_end(s);
     if (e != cudaSuccess || a.aligned) return status_from_cuda(e);
     prof_begin("paged_join", s);
-    e = launch_paged(k_paged_join<T>, dim3((unsigned)(a.p.B * a.p.Hq)), 128, 0, 1, a, s);
+    const unsigned out_rows = (unsigned)(a.p.B * a.p.Hq);
+    e = out_rows <= kJoinFew    ? launch_paged(k_paged_join<T, 16, 1>, dim3(out_rows), 512, 0, 1, a, s)
+        : out_rows < kJoinMany ? launch_paged(k_paged_join<T, 4, 1>, dim3(out_rows), 128, 0, 1, a, s)
+                               : launch_paged(k_paged_join<T, 1, 4>, dim3((out_rows + 3) / 4), 128, 0, 1, a, s);
     prof_end(s);
     return status_from_cuda(e);
 }
@@ -630,11 +647,14 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
-    // The largest cluster that leaves every CTA of the grid resident at once.
+    // One cluster per segment, the smallest that gives every SM a CTA. Segments of one length (one sequence, or
+    // page lists) are then balanced by themselves; of unknown lengths only while the longest stays short.
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
-    int cluster = kMaxCluster;
-    while (cluster > 1 && segments * cluster > kCtas) cluster /= 2;
-    a.aligned = most <= (long long)kAlignedKeys * cluster ? cluster : 0;
+    int cluster = 1;
+    while (cluster < kMaxCluster && segments * cluster < 152) cluster *= 2;
+    const bool even = page_idx || a.p.B == 1;
+    const bool few = most <= (long long)kAlignedKeys * cluster && segments * cluster <= kCtas;
+    a.aligned = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
     a.lead = a.aligned ? 0 : kLead;
     char *w = static_cast<char *>(workspace);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);

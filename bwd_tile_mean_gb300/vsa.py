@@ -584,9 +584,10 @@ def _row_stride(name, x, heads, D):
     return stride[0] if shape[0] > 1 else 0
 
 
-# The current stream's handle by device index: what torch.cuda.current_stream
-# wraps in a Stream object, at a twentieth of its time (2 us of a call of 10).
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# The current stream's handle by device index, and the current device: what
+# torch.cuda.current_stream and current_device return, without the objects and
+# checks around them (2 us of a call of 8).
+_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
 class PagedCache:
@@ -666,7 +667,9 @@ class PagedCache:
         self._ws, self._ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
         self._desc, self._index = C.byref(self.desc), self.device.index
         self._out_shape, self._lse_shape = (B, Hq, D), (B, Hq)
-        self._out_dense = (Hq * D, D, 1)
+        self._out_dense, self._new = (Hq * D, D, 1), dict(dtype=dtype, device=self.device)
+        self._f32, self._i32 = dict(dtype=torch.float32, device=self.device), i32
+        self._fn = {n: getattr(lib(), n) for n in ("vsa_paged_append", "vsa_page_select", "vsa_paged_attn")}
 
     def _is(self, name, t, shape, dtype):
         if t.dtype != dtype or t.device != self.device or t.shape != shape:
@@ -682,29 +685,29 @@ class PagedCache:
         if not t.is_contiguous():
             raise ValueError(f"{name}: must be contiguous")
 
-    def _empty(self, shape, dtype, stream):
+    def _empty(self, stream, shape, like):
         """An output that belongs to the stream the call runs on."""
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, **like)
         with torch.cuda.stream(stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+            return torch.empty(shape, **like)
 
     def _run(self, name, stream, *args):
         """The call on this cache's device and the given (or current) stream."""
-        if self._index is None:
+        index = self._index
+        if index is None:
             raise ValueError(f"the cache is on {self.device}: the calls run on a GPU only")
         if stream is None:
-            handle = _raw_stream(self._index)
+            stream = _raw_stream(index)
         elif stream.device != self.device:
             raise ValueError(f"stream: expected one of {self.device}, got {stream.device}")
         else:
-            handle = stream.cuda_stream
-        fn = getattr(_lib, name)
-        if torch.cuda.current_device() == self._index:
-            code = fn(self._desc, *args, handle)
+            stream = stream.cuda_stream
+        if _device() == index:
+            code = self._fn[name](self._desc, *args, stream)
         else:
             with torch.cuda.device(self.device):
-                code = fn(self._desc, *args, handle)
+                code = self._fn[name](self._desc, *args, stream)
         if code:
             raise VsaError(name, code)
 
@@ -745,7 +748,7 @@ class PagedCache:
             self._on("q", q, self.dtype)
             qs = _row_stride("q", q, self.Hq, self.D)
             if q_out is None:
-                q_out = self._empty((T, self.Hq, self.D), self.dtype, stream)
+                q_out = self._empty(stream, (T, self.Hq, self.D), self._new)
             else:
                 self._dense("q_out", q_out, (T, self.Hq, self.D), self.dtype)
             qp, qop = q.data_ptr(), q_out.data_ptr()
@@ -780,9 +783,9 @@ class PagedCache:
         qs = self._rows(q)
         given = page_idx is not None or page_cnt is not None
         if page_idx is None:
-            page_idx = self._empty((self.B, self.Hkv, topk), torch.int32, stream)
+            page_idx = self._empty(stream, (self.B, self.Hkv, topk), self._i32)
         if page_cnt is None:
-            page_cnt = self._empty((self.B, self.Hkv), torch.int32, stream)
+            page_cnt = self._empty(stream, (self.B, self.Hkv), self._i32)
         if given:
             self._lists(page_idx, page_cnt)
             if page_idx.shape[2] != topk:
@@ -804,11 +807,11 @@ class PagedCache:
             self._lists(*pages)
             idx, cnt, cap = pages[0].data_ptr(), pages[1].data_ptr(), pages[0].shape[2]
         if out is None:
-            out = self._empty(self._out_shape, self.dtype, stream)
+            out = self._empty(stream, self._out_shape, self._new)
         else:
             self._dense("out", out, self._out_shape, self.dtype)
         if lse is None:
-            lse = self._empty(self._lse_shape, torch.float32, stream)
+            lse = self._empty(stream, self._lse_shape, self._f32)
         else:
             self._dense("lse", lse, self._lse_shape, torch.float32)
         self._run("vsa_paged_attn", stream, q.data_ptr(), qs, self._k, self._v, idx, cnt, cap, out.data_ptr(),
