@@ -3,7 +3,7 @@
 // every page that fills up (vsa_paged_append).
 //
 // Work: a unit is one page of one sequence that receives tokens; a warp has
-// one 16-slot group of a unit and a chunk of rows per token: HC keys and
+// a 16-slot group of a unit (or some, in turns) and a chunk of rows per token: HC keys and
 // values, or 2 HC queries. Half a warp holds one token row (16 bytes = 8
 // dims per lane), the two halves the even and the odd slots; PB pairs of
 // slots are loaded together. The rotation's angles are loaded once per token
@@ -16,7 +16,10 @@
 // [cu[b], cu[b+1]) touches at most (cu[b+1] - cu[b]) / page + 2 pages, so
 // numbering its units from cu[b] / page + 2 b leaves room for them, and a
 // warp finds its b with a 32-way search of that ascending sequence.
+#include <algorithm>
+
 #include "paged.cuh"
+#include "sm103_ptx.cuh"
 
 namespace vsa {
 namespace {
@@ -34,6 +37,7 @@ struct AppendArgs {
     float *mean;
     long long units;
     int kv_chunks, chunks;  // chunks of key/value heads, and with the queries'
+    int team;               // warps per unit
 };
 
 constexpr int kGroup = 16;  // slots per warp
@@ -128,14 +132,13 @@ template <typename T> __device__ __forceinline__ void add8(float (&acc)[8], uint
 
 template <typename T, int HC, int PB>
 __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
-    extern __shared__ __align__(16) float ssum[];  // [warps][HC][128] group sums
+    extern __shared__ __align__(16) float ssum[];  // [units of the CTA][groups][HC][128] group sums
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
-    const int groups = p.page / kGroup;                     // warps per unit
-    const int per_cta = (int)(blockDim.x >> 5) / groups;    // units per CTA
+    const int groups = p.page / kGroup, per_cta = (int)(blockDim.x >> 5) / a.team;  // units per CTA
     const int chunk = (int)(blockIdx.x % a.chunks);         // neighbouring CTAs: the rows of the same tokens
-    const long long u = (long long)(blockIdx.x / a.chunks) * per_cta + wid / groups;
-    const int grp = wid % groups;
+    const int unit = wid / a.team, first_grp = wid % a.team;
+    const long long u = (long long)(blockIdx.x / a.chunks) * per_cta + unit;
     const bool kv = chunk < a.kv_chunks;
     const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v), *q = static_cast<const T *>(a.q);
     T *kc = static_cast<T *>(a.kc), *vc = static_cast<T *>(a.vc), *qo = static_cast<T *>(a.q_out);
@@ -171,19 +174,16 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
     const int id = work && kv ? paged_id(p, b, pg) : -1;
     const bool mean = kv && a.mean && work && s1 == p.page && id >= 0;  // the page fills up in this call
     const long long page_at = (long long)max(id, 0) * p.page_stride;
-    const int g0 = grp * kGroup;
-    const bool mine = work && g0 < s1 && g0 + kGroup > s0;  // the group takes new tokens
-
     if (!kv) {
-        if (!mine) return;
         const int h0 = (chunk - a.kv_chunks) * 2 * HC, hn = min(2 * HC, p.Hq - h0);
-        for (int st = 0; st < kGroup; st += 2 * PB) {
-            if (g0 + st >= s1 || g0 + st + 2 * PB <= s0) continue;
+        for (int st = first_grp * kGroup; st < s1; st += 2 * PB) {
+            if (st % kGroup == 0 && st != first_grp * kGroup) st += (a.team - 1) * kGroup;  // the warp's next group
+            if (st >= s1 || st + 2 * PB <= s0) continue;
             uint4 x[PB][2 * HC];
             Angles w[PB];
 #pragma unroll
             for (int c = 0; c < PB; ++c) {
-                const int s = g0 + st + 2 * c + half;
+                const int s = st + 2 * c + half;
                 const bool fresh = s >= s0 && s < s1;
                 const long long tok = fresh ? t_of + s : 0;
 #pragma unroll
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
             }
 #pragma unroll
             for (int c = 0; c < PB; ++c) {
-                const int s = g0 + st + 2 * c + half;
+                const int s = st + 2 * c + half;
                 const bool fresh = s >= s0 && s < s1;
                 const long long tok = fresh ? t_of + s : 0;
 #pragma unroll
@@ -213,76 +213,90 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
     }
 
     const int h0 = chunk * HC, hn = min(HC, p.Hkv - h0);
-    float acc[HC][8];
-#pragma unroll
-    for (int h = 0; h < HC; ++h)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
-    if (mean || mine) {
-        for (int st = 0; st < kGroup; st += 2 * PB) {
-            if (!mean && (g0 + st >= s1 || g0 + st + 2 * PB <= s0)) continue;
-            uint4 xk[PB][HC], xv[PB][HC];
-            Angles w[PB];
-#pragma unroll
-            for (int c = 0; c < PB; ++c) {
-                const int s = g0 + st + 2 * c + half;
-                const bool fresh = s >= s0 && s < s1;
-                const long long tok = fresh ? t_of + s : 0;
-                const long long slot_at = page_at + s * p.tok_stride + 8 * i;
-#pragma unroll
-                for (int h = 0; h < HC; ++h) {
-                    xk[c][h] = xv[c][h] = make_uint4(0, 0, 0, 0);
-                    if (fresh && h < hn) {
-                        xk[c][h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
-                        xv[c][h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
-                    } else if (mean && s < s0 && h < hn) {  // written by an earlier call
-                        xk[c][h] = *reinterpret_cast<const uint4 *>(kc + slot_at + (h0 + h) * p.head_stride);
-                    }
-                }
-                if (fresh && 8 * i < a.rot) {
-                    const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
-                    load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
-                }
-            }
-#pragma unroll
-            for (int c = 0; c < PB; ++c) {
-                const int s = g0 + st + 2 * c + half;
-                const bool fresh = s >= s0 && s < s1;
-                const long long slot_at = page_at + s * p.tok_stride + 8 * i;
-#pragma unroll
-                for (int h = 0; h < HC; ++h) {
-                    if (a.rot) {
-                        const uint4 y = rotate<T>(a, xk[c][h], w[c], i);
-                        if (fresh) xk[c][h] = y;
-                    }
-                    if (fresh && id >= 0 && h < hn) {
-                        const long long at = slot_at + (h0 + h) * p.head_stride;
-                        *reinterpret_cast<uint4 *>(kc + at) = xk[c][h];
-                        *reinterpret_cast<uint4 *>(vc + at) = xv[c][h];
-                    }
-                    if (mean) add8<T>(acc[h], xk[c][h]);  // every slot below s1 == page is new or old
-                }
-            }
-        }
-    }
-    if (!a.mean) return;
-    // even + odd slots of the group, then the unit's groups in order
-    if (mean) {
+    for (int grp = first_grp; grp < groups; grp += a.team) {
+        const int g0 = grp * kGroup;
+        float acc[HC][8];
 #pragma unroll
         for (int h = 0; h < HC; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float odd = __shfl_down_sync(0xffffffffu, acc[h][e], 16);
-                if (half == 0) ssum[(wid * HC + h) * kD + 8 * i + e] = __fadd_rn(acc[h][e], odd);
+            for (int e = 0; e < 8; ++e) acc[h][e] = 0.f;
+        if (mean && g0 < s0) {  // the page's earlier keys, written by earlier calls
+            constexpr int OB = HC <= 2 ? 8 / HC : 2;  // pairs of slots loaded together
+            for (int st = 0; st < kGroup && g0 + st < s0; st += 2 * OB) {
+                uint4 x[OB][HC];
+#pragma unroll
+                for (int c = 0; c < OB; ++c)
+#pragma unroll
+                    for (int h = 0; h < HC; ++h) {
+                        const int s = g0 + st + 2 * c + half;
+                        x[c][h] = s < s0 && h < hn ? *reinterpret_cast<const uint4 *>(kc + page_at + s * p.tok_stride +
+                                                                                      (h0 + h) * p.head_stride + 8 * i)
+                                                   : make_uint4(0, 0, 0, 0);  // adds nothing
+                    }
+#pragma unroll
+                for (int c = 0; c < OB; ++c)
+#pragma unroll
+                    for (int h = 0; h < HC; ++h) add8<T>(acc[h], x[c][h]);
             }
+        }
+        if (g0 < s1 && g0 + kGroup > s0) {  // new tokens
+            for (int st = 0; st < kGroup; st += 2 * PB) {
+                if (g0 + st >= s1 || g0 + st + 2 * PB <= s0) continue;
+                uint4 xk[PB][HC], xv[PB][HC];
+                Angles w[PB];
+#pragma unroll
+                for (int c = 0; c < PB; ++c) {
+                    const int s = g0 + st + 2 * c + half;
+                    const bool fresh = s >= s0 && s < s1;
+                    const long long tok = fresh ? t_of + s : 0;
+#pragma unroll
+                    for (int h = 0; h < HC; ++h) {
+                        xk[c][h] = xv[c][h] = make_uint4(0, 0, 0, 0);
+                        if (fresh && h < hn) {
+                            xk[c][h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
+                            xv[c][h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
+                        }
+                    }
+                    if (fresh && 8 * i < a.rot) {
+                        const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                        load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < PB; ++c) {
+                    const int s = g0 + st + 2 * c + half;
+                    const bool fresh = s >= s0 && s < s1;
+                    const long long slot_at = page_at + s * p.tok_stride + 8 * i;
+#pragma unroll
+                    for (int h = 0; h < HC; ++h) {
+                        if (a.rot) xk[c][h] = rotate<T>(a, xk[c][h], w[c], i);
+                        if (fresh && id >= 0 && h < hn) {
+                            const long long at = slot_at + (h0 + h) * p.head_stride;
+                            *reinterpret_cast<uint4 *>(kc + at) = xk[c][h];
+                            *reinterpret_cast<uint4 *>(vc + at) = xv[c][h];
+                        }
+                        if (mean && fresh) add8<T>(acc[h], xk[c][h]);
+                    }
+                }
+            }
+        }
+        if (mean)  // even + odd slots of the group
+#pragma unroll
+            for (int h = 0; h < HC; ++h)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float odd = __shfl_down_sync(0xffffffffu, acc[h][e], 16);
+                    if (half == 0) ssum[((unit * groups + grp) * HC + h) * kD + 8 * i + e] = __fadd_rn(acc[h][e], odd);
+                }
     }
-    __syncthreads();
-    if (mean && grp == 0) {
+    if (!mean) return;
+    ptx::named_sync(1 + unit, 32 * a.team);  // the unit's warps alone: others may have left
+    if (first_grp == 0) {  // the groups in order
         const float inv = 1.f / (float)p.page;  // a power of two: exact
         for (int h = 0; h < hn; ++h) {
-            float4 t = *reinterpret_cast<const float4 *>(&ssum[(wid * HC + h) * kD + 4 * lane]);
+            float4 t = *reinterpret_cast<const float4 *>(&ssum[(unit * groups * HC + h) * kD + 4 * lane]);
             for (int g = 1; g < groups; ++g) {
-                const float4 x = *reinterpret_cast<const float4 *>(&ssum[((wid + g) * HC + h) * kD + 4 * lane]);
+                const float4 x = *reinterpret_cast<const float4 *>(&ssum[((unit * groups + g) * HC + h) * kD + 4 * lane]);
                 t.x = __fadd_rn(t.x, x.x);
                 t.y = __fadd_rn(t.y, x.y);
                 t.z = __fadd_rn(t.z, x.z);
@@ -296,12 +310,14 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
 
 template <typename T, int HC, int PB> cudaError_t launch_append(AppendArgs &a, cudaStream_t s) {
     const int groups = a.p.page / kGroup;
-    const int warps = groups > 4 ? groups : 4, per_cta = warps / groups;
+    // A prompt fills most groups of its units; one token leaves all but one warp idle, and few are enough.
+    a.team = a.cu ? groups : std::min(groups, 4);
+    const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
     a.kv_chunks = (a.p.Hkv + HC - 1) / HC;
     a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
     const long long ctas = (a.units + per_cta - 1) / per_cta * a.chunks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t smem = a.mean ? sizeof(float) * warps * HC * kD : 0;
+    const size_t smem = a.mean ? sizeof(float) * per_cta * groups * HC * kD : 0;
     return launch_paged(k_paged_append<T, HC, PB>, dim3((unsigned)ctas), 32 * warps, smem, 1, a, s);
 }
 
@@ -352,11 +368,11 @@ extern "C" vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("paged_append", s);
     const bool bf = a.p.dtype == T_BF16;
-    // Many tokens: four heads per warp, so that a token's angles serve 8 rows. Few: one head per warp and
-    // four pairs of slots at once, for the shortest chain of loads.
+    // Many tokens: four heads per warp, so that a token's angles serve 8 rows. Few: two heads per warp and
+    // two pairs of slots at once, for a short chain of loads.
     const bool wide = (long long)T * a.p.Hkv >= kWideRows;
     const cudaError_t e = wide ? (bf ? launch_append<__nv_bfloat16, 4, 1>(a, s) : launch_append<__half, 4, 1>(a, s))
-                               : (bf ? launch_append<__nv_bfloat16, 1, 4>(a, s) : launch_append<__half, 1, 4>(a, s));
+                               : (bf ? launch_append<__nv_bfloat16, 2, 2>(a, s) : launch_append<__half, 2, 2>(a, s));
     prof_end(s);
     return status_from_cuda(e);
 }
