@@ -1,7 +1,8 @@
-"""Builds libvsa.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Builds libvsa.so (the C-ABI library) in-tree with nvcc for sm_103a, and
+the paged cache's Python binding beside it with the host compiler.
 
-Each translation unit compiles in its own nvcc process (in parallel) and
-the objects link into bwd_tile_mean_gb300/_build/libvsa.so. Objects are
+Each translation unit compiles in its own process (in parallel) and the
+CUDA objects link into bwd_tile_mean_gb300/_build/libvsa.so. Objects are
 rebuilt when their source or any header is newer.
 """
 from __future__ import annotations
@@ -10,6 +11,7 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,10 +20,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libvsa.so")
+BINDING = os.path.join(OUT, "paged_binding.so")
 SOURCES = ["vsa_api.cu", "index_kernels.cu", "fwd_kernel.cu", "bwd_kernels.cu", "noalloc.cu", "tile3d.cu", "waitcheck.cu",
            "host_step.cu", "check_inputs.cu", "compress_kernels.cu", "paged_append.cu", "paged_select.cu",
            "paged_attn.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 
@@ -52,13 +56,37 @@ def _compile(src, verbose):
     return obj
 
 
+def _bind(verbose):
+    """paged_binding.so: a Python extension against the installed torch."""
+    import torch
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if not _stale(BINDING, [src, torch.__file__] + _headers()):
+        return
+    at = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + f".{os.getpid()}.tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(at, "include"),
+           "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
+           src, "-o", tmp, "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+           "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+    if r.returncode != 0:
+        raise RuntimeError("the host compiler failed on paged_binding.cpp")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     if force:
-        for o in glob.glob(os.path.join(OUT, "*.o")):
+        for o in glob.glob(os.path.join(OUT, "*.o")) + glob.glob(BINDING):
             os.remove(o)
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_bind, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), SOURCES))
+        binding.result()
     if _stale(LIB, objs):
         tmp = LIB + f".{os.getpid()}.tmp"
         cmd = [NVCC] + ARCH + ["-shared", "-o", tmp] + objs

@@ -11,6 +11,7 @@ missing library raises.
 from __future__ import annotations
 
 import ctypes as C
+import importlib.util
 import math
 import os
 import weakref
@@ -573,21 +574,20 @@ def check_wait_timeout(workspace: torch.Tensor, limit_ns: int = 50_000_000, stre
 
 # ---------------------------------------------------------------- paged cache
 
-def _row_stride(name, x, heads, D):
-    """Elements from one token of x [T, heads, D] to the next (heads and
-    dims dense; 0 where there is only one token)."""
-    shape, stride = x.shape, x.stride()
-    if len(shape) != 3 or shape[1] != heads or shape[2] != D:
-        raise ValueError(f"{name}: expected [tokens, {heads}, {D}], got {list(shape)}")
-    if shape[0] and (stride[2] != 1 or (heads > 1 and stride[1] != D)):
-        raise ValueError(f"{name}: heads and dims must be dense")
-    return stride[0] if shape[0] > 1 else 0
+_binding = None
 
 
-# The current stream's handle by device index, and the current device: what
-# torch.cuda.current_stream and current_device return, without the objects and
-# checks around them (2 us of a call of 8).
-_raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+def _paged_binding():
+    """The extension module behind PagedCache's calls; raise if absent."""
+    global _binding
+    if _binding is None:
+        path = _build.BINDING
+        if not os.path.exists(path):
+            raise RuntimeError(f"paged_binding.so is not built ({path}); run __graft_entry__.build()")
+        spec = importlib.util.spec_from_file_location("paged_binding", path)
+        _binding = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_binding)
+    return _binding
 
 
 class PagedCache:
@@ -661,72 +661,25 @@ class PagedCache:
         elif workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace: at least {need} bytes on {self.device} are needed")
         self.workspace = workspace
-        # what every call passes on: the tensors above are not to be replaced, only written
-        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        self._k, self._v, self._mean = ptr(k), ptr(v), ptr(k_mean)
-        self._ws, self._ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-        self._desc, self._index = C.byref(self.desc), self.device.index
-        self._out_shape, self._lse_shape = (B, Hq, D), (B, Hq)
-        self._out_dense, self._new = (Hq * D, D, 1), dict(dtype=dtype, device=self.device)
-        self._f32, self._i32 = dict(dtype=torch.float32, device=self.device), i32
-        self._fn = {n: getattr(lib(), n) for n in ("vsa_paged_append", "vsa_page_select", "vsa_paged_attn")}
+        # every call passes these on: the tensors above are not to be replaced, only written
+        at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+        entry = lambda f: C.cast(f, C.c_void_p).value  # noqa: E731
+        L = lib()
+        self._calls = _paged_binding().Calls(
+            C.addressof(self.desc), self.device.index if self.device.type == "cuda" else -1, at(k), at(v), at(k_mean),
+            at(workspace), workspace.numel() * workspace.element_size(), entry(L.vsa_paged_append),
+            entry(L.vsa_page_select), entry(L.vsa_paged_attn), _check)
 
     def _is(self, name, t, shape, dtype):
         if t.dtype != dtype or t.device != self.device or t.shape != shape:
             raise ValueError(f"{name}: expected {dtype} {list(shape)} on {self.device}, "
                              f"got {t.dtype} {list(t.shape)} on {t.device}")
 
-    def _on(self, name, t, dtype):
-        if t.dtype != dtype or t.device != self.device:
-            raise ValueError(f"{name}: expected {dtype} on {self.device}, got {t.dtype} on {t.device}")
-
-    def _dense(self, name, t, shape, dtype):
-        self._is(name, t, shape, dtype)
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
-
-    def _empty(self, stream, shape, like):
-        """An output that belongs to the stream the call runs on."""
-        if stream is None:
-            return torch.empty(shape, **like)
-        with torch.cuda.stream(stream):
-            return torch.empty(shape, **like)
-
-    def _run(self, name, stream, *args):
-        """The call on this cache's device and the given (or current) stream."""
-        index = self._index
-        if index is None:
-            raise ValueError(f"the cache is on {self.device}: the calls run on a GPU only")
-        if stream is None:
-            stream = _raw_stream(index)
-        elif stream.device != self.device:
+    def _on(self, stream):
+        """Makes `stream` current, for a call and the outputs it allocates."""
+        if stream.device != self.device:
             raise ValueError(f"stream: expected one of {self.device}, got {stream.device}")
-        else:
-            stream = stream.cuda_stream
-        if _device() == index:
-            code = self._fn[name](self._desc, *args, stream)
-        else:
-            with torch.cuda.device(self.device):
-                code = self._fn[name](self._desc, *args, stream)
-        if code:
-            raise VsaError(name, code)
-
-    def _rows(self, q):
-        """Checks the queries of one token per sequence; their row stride."""
-        if q.dtype != self.dtype or q.device != self.device:
-            self._on("q", q, self.dtype)
-        if q.shape == self._out_shape and q.stride() == self._out_dense:
-            return 0
-        qs = _row_stride("q", q, self.Hq, self.D)
-        if q.shape[0] != self.B:
-            raise ValueError(f"q: expected one token for each of {self.B} sequences")
-        return qs
-
-    def _lists(self, idx, cnt):
-        if idx.dim() != 3:
-            raise ValueError("page lists: expected page_idx [B, Hkv, cap] and page_cnt [B, Hkv]")
-        self._dense("page_idx", idx, (self.B, self.Hkv, idx.shape[2]), torch.int32)
-        self._dense("page_cnt", cnt, (self.B, self.Hkv), torch.int32)
+        return torch.cuda.stream(stream)
 
     def append(self, k, v, q=None, cu_seqlens=None, cos=None, sin=None, positions=None, interleaved=False, q_out=None,
                stream=None):
@@ -734,86 +687,24 @@ class PagedCache:
         tokens, which seq_lens already counts; cu_seqlens int32 [B+1], None
         for one token per sequence. cos, sin: fp32 [rows, rot_dim / 2], None
         for no rotation. Returns the rotated q (None without q)."""
-        if self._k is None:
-            raise ValueError("this cache has no k and v")
-        T = k.shape[0]
-        self._on("k", k, self.dtype)
-        self._on("v", v, self.dtype)
-        ks, vs = _row_stride("k", k, self.Hkv, self.D), _row_stride("v", v, self.Hkv, self.D)
-        qp = qop = cu = pos = cp = sp = None
-        qs = rows = rot = 0
-        if v.shape[0] != T or (q is not None and q.shape[0] != T):
-            raise ValueError("k, v and q must have the same number of tokens")
-        if q is not None:
-            self._on("q", q, self.dtype)
-            qs = _row_stride("q", q, self.Hq, self.D)
-            if q_out is None:
-                q_out = self._empty(stream, (T, self.Hq, self.D), self._new)
-            else:
-                self._dense("q_out", q_out, (T, self.Hq, self.D), self.dtype)
-            qp, qop = q.data_ptr(), q_out.data_ptr()
-        elif q_out is not None:
-            raise ValueError("q_out without q")
-        if cu_seqlens is not None:
-            self._dense("cu_seqlens", cu_seqlens, (self.B + 1,), torch.int32)
-            cu = cu_seqlens.data_ptr()
-        elif T != self.B:
-            raise ValueError("without cu_seqlens there is one token per sequence")
-        if cos is not None and sin is not None:
-            shape = cos.shape
-            if len(shape) != 2 or not cos.is_contiguous():
-                raise ValueError("cos and sin: expected contiguous [rows, rot_dim / 2]")
-            self._on("cos", cos, torch.float32)
-            self._dense("sin", sin, shape, torch.float32)
-            rows, rot, cp, sp = shape[0], 2 * shape[1], cos.data_ptr(), sin.data_ptr()
-        elif cos is not sin:
-            raise ValueError("give both cos and sin, or neither")
-        if positions is not None:
-            self._dense("positions", positions, (T,), torch.int32)
-            pos = positions.data_ptr()
-        self._run("vsa_paged_append", stream, T, k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, qop, cu, pos, cp, sp,
-                  rows, rot, 1 if interleaved else 0, self._k, self._v, self._mean)
-        return q_out
+        if stream is not None:
+            with self._on(stream):
+                return self._calls.append(k, v, q, cu_seqlens, cos, sin, positions, interleaved, q_out)
+        return self._calls.append(k, v, q, cu_seqlens, cos, sin, positions, interleaved, q_out)
 
     def select(self, q, topk, keep_first=0, keep_last=1, page_idx=None, page_cnt=None, stream=None):
         """vsa_page_select: the pages that q [B, Hq, D] attends to, as
         (page_idx int32 [B, Hkv, topk], page_cnt int32 [B, Hkv])."""
-        if self._mean is None:
-            raise ValueError("this cache has no k_mean")
-        qs = self._rows(q)
-        given = page_idx is not None or page_cnt is not None
-        if page_idx is None:
-            page_idx = self._empty(stream, (self.B, self.Hkv, topk), self._i32)
-        if page_cnt is None:
-            page_cnt = self._empty(stream, (self.B, self.Hkv), self._i32)
-        if given:
-            self._lists(page_idx, page_cnt)
-            if page_idx.shape[2] != topk:
-                raise ValueError(f"page_idx: expected topk = {topk} entries per row")
-        self._run("vsa_page_select", stream, q.data_ptr(), qs, self._mean, topk, keep_first, keep_last,
-                  page_idx.data_ptr(), page_cnt.data_ptr(), self._ws, self._ws_bytes)
-        return page_idx, page_cnt
+        if stream is not None:
+            with self._on(stream):
+                return self._calls.select(q, topk, keep_first, keep_last, page_idx, page_cnt)
+        return self._calls.select(q, topk, keep_first, keep_last, page_idx, page_cnt)
 
     def attend(self, q, pages=None, out=None, lse=None, stream=None):
         """vsa_paged_attn: q [B, Hq, D] over the whole cache, or over the
         pages = (page_idx, page_cnt) that select returned. Returns (out
         [B, Hq, D], lse fp32 [B, Hq])."""
-        if self._k is None:
-            raise ValueError("this cache has no k and v")
-        qs = self._rows(q)
-        idx = cnt = None
-        cap = 0
-        if pages is not None:
-            self._lists(*pages)
-            idx, cnt, cap = pages[0].data_ptr(), pages[1].data_ptr(), pages[0].shape[2]
-        if out is None:
-            out = self._empty(stream, self._out_shape, self._new)
-        else:
-            self._dense("out", out, self._out_shape, self.dtype)
-        if lse is None:
-            lse = self._empty(stream, self._lse_shape, self._f32)
-        else:
-            self._dense("lse", lse, self._lse_shape, torch.float32)
-        self._run("vsa_paged_attn", stream, q.data_ptr(), qs, self._k, self._v, idx, cnt, cap, out.data_ptr(),
-                  lse.data_ptr(), self._ws, self._ws_bytes)
-        return out, lse
+        if stream is not None:
+            with self._on(stream):
+                return self._calls.attend(q, pages, out, lse)
+        return self._calls.attend(q, pages, out, lse)
