@@ -277,23 +277,33 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
                 if (i >= take) break;
                 cp_wait<kStages - 2>();
                 __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
-                if (i + kStages - 1 < take)
-                    valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
-                cp_commit();
                 const uint32_t st = ring + s * kStageBytes;
-                float sc[2][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
+                // All K fragments before the products that use them: the loads' latency is paid once a block.
+                uint32_t kb[8][4];
                 {
                     const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t kb[4];
-                        ldsm4(kb, st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-                        mma16816<T>(sc[0], qa[j], kb[0], kb[1]);
-                        mma16816<T>(sc[1], qa[j], kb[2], kb[3]);
-                    }
+                    for (int j = 0; j < 8; ++j) ldsm4(kb[j], st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
                 }
+                if (i + kStages - 1 < take)
+                    valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
+                cp_commit();
+                float sc[2][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    mma16816<T>(sc[0], qa[j], kb[j][0], kb[j][1]);
+                    mma16816<T>(sc[1], qa[j], kb[j][2], kb[j][3]);
+                }
+                // half of V's fragments, to arrive while the softmax runs
+                const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc0 = lane >> 4;
+                auto ld_v = [&](uint32_t (&r)[4], int j) {
+                    ldsm4t(r, st + kBlk * 256 + vrow * 256 + (((2 * j + vc0) ^ (vrow & 7)) << 4));
+                };
+                uint32_t vb[4][4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) ld_v(vb[j], j);
                 const int ok = valid[s];
 #pragma unroll
                 for (int u = 0; u < 2; ++u)
@@ -338,15 +348,11 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
                 // unrounded values): half a step of the output's own type
                 const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
                                         pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
-                {
-                    const int row = (lane & 7) + ((lane >> 3) & 1) * 8, c0 = lane >> 4;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        uint32_t vb[4];
-                        ldsm4t(vb, st + kBlk * 256 + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-                        mma16816<T>(acc[2 * j], pa, vb[0], vb[1]);
-                        mma16816<T>(acc[2 * j + 1], pa, vb[2], vb[3]);
-                    }
+                for (int j = 0; j < 8; ++j) {
+                    mma16816<T>(acc[2 * j], pa, vb[j & 3][0], vb[j & 3][1]);
+                    mma16816<T>(acc[2 * j + 1], pa, vb[j & 3][2], vb[j & 3][3]);
+                    if (j < 4) ld_v(vb[j], j + 4);
                 }
             }
         }
@@ -576,12 +582,12 @@ int rows_of(int G) {
 }
 
 template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
-    const cudaError_t ae = ensure_smem_limit((const void *)k_paged_attn<T>, kSmem);
-    if (ae != cudaSuccess) return status_from_cuda(ae);
     const unsigned grid = a.aligned ? (unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.aligned) : kCtas;
     const unsigned cluster = a.aligned > 1 ? a.aligned : 1;
+    cudaError_t e = ensure_smem_limit((const void *)k_paged_attn<T>, kSmem);
+    if (e != cudaSuccess) return status_from_cuda(e);
     prof_begin("paged_attn", s);
-    cudaError_t e = launch_paged(k_paged_attn<T>, grid, kWarps * 32, kSmem, cluster, a, s);
+    e = launch_paged(k_paged_attn<T>, grid, kWarps * 32, kSmem, cluster, a, s);
     prof_end(s);
     if (e != cudaSuccess || a.aligned) return status_from_cuda(e);
     prof_begin("paged_join", s);

@@ -40,8 +40,10 @@ struct SelectArgs {
 };
 
 constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
+constexpr int kTopkThreads = 512;
 constexpr int kCtasSel = 304;  // two per SM on 152 SMs
 constexpr int kHeads = 16;     // heads of a page taken together
+constexpr int kLeadSel = 6;    // units a sequence counts for beyond its own (its start-up time)
 constexpr int kRing = 5;       // ring stages per warp, each four pages' means of one head (2 KB)
 constexpr int kRingBytes = kRing * 2048;
 constexpr int kSmemSel = kWarpsSel * kRingBytes + kHeads * kD * 4;
@@ -142,25 +144,25 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
     const int hgroups = (p.Hkv + kHeads - 1) / kHeads;
     grid_wait();
     grid_go();
-    // a unit: four pages, the heads of one group
+    // a unit: four pages, the heads of one group; a group's lead goes before its own units
+    auto units_of = [&](int n) { const int q = (competing(a, n) + 3) / 4; return q > 0 ? q + kLeadSel : 0; };
     const Run run = find_run<kWarpsSel>(
-        p.B, [&](int b) -> long long { return (long long)((competing(a, b) + 3) / 4) * hgroups; }, kCtasSel, 1, 1);
+        p.B, [&](int n) -> long long { return (long long)units_of(n) * hgroups; }, kCtasSel, 1, 1);
     long long before = run.before;
     int b = run.n;
     for (long long x = run.x0; x < run.x1 && b < p.B;) {
-        const int comp = competing(a, b), quads = (comp + 3) / 4;
-        if (x >= before + (long long)quads * hgroups) {
-            before += (long long)quads * hgroups;
+        const int comp = competing(a, b), units = units_of(b);
+        if (x >= before + (long long)units * hgroups) {
+            before += (long long)units * hgroups;
             ++b;
             continue;
         }
-        const int grp = (int)((x - before) / quads), q0 = (int)((x - before) % quads);
-        const int nq = (int)min((long long)(quads - q0), run.x1 - x);
+        const int grp = (int)((x - before) / units), off = (int)((x - before) % units);
+        const int take = (int)min((long long)(units - off), run.x1 - x);
+        const int q0 = max(off - kLeadSel, 0), nq = max(off + take - kLeadSel, 0) - q0;  // its own units
         const int h0 = grp * kHeads, hn = min(kHeads, p.Hkv - h0);
-        x += nq;
-        const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h0 * p.G * kD;
-        __syncthreads();  // the sums of the piece before were read
-        if (tid < hn * (kD / 8)) group_sum<T>(q + (long long)(tid >> 4) * p.G * kD + 8 * (tid & 15), p.G, sq + 8 * tid);
+        x += take;
+        if (nq == 0) continue;
 
         // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
         const int sub = lane >> 3, j = lane & 7, items = nq * hn;
@@ -178,7 +180,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
             if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s, id[s]);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        __syncthreads();  // the sums are there
+        __syncthreads();  // the sums of the piece before were read
+        const T *q = static_cast<const T *>(a.q) + b * a.qs + (long long)h0 * p.G * kD;
+        if (tid < hn * (kD / 8)) group_sum<T>(q + (long long)(tid >> 4) * p.G * kD + 8 * (tid & 15), p.G, sq + 8 * tid);
+        __syncthreads();
         uint32_t *keys = a.keys + ((long long)b * p.Hkv + h0) * p.max_pages;
         for (int n0 = 0; wid + n0 * kWarpsSel < items; n0 += kRing) {
 #pragma unroll
@@ -199,20 +204,21 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
 }
 
 // Rows with nothing to choose: every page.
-__device__ __forceinline__ void list_all(const SelectArgs &a, long long row, int pages) {
-    for (int n = threadIdx.x; n < a.topk; n += kThreads) a.idx[row * a.topk + n] = n < pages ? n : -1;
+template <int N> __device__ __forceinline__ void list_all(const SelectArgs &a, long long row, int pages) {
+    for (int n = threadIdx.x; n < a.topk; n += N) a.idx[row * a.topk + n] = n < pages ? n : -1;
     if (threadIdx.x == 0) a.cnt[row] = pages;
 }
-__device__ __forceinline__ void clear_bins(int (&hist)[kBins]) {
-    for (int e = threadIdx.x; e < kBins / 4; e += kThreads) reinterpret_cast<int4 *>(hist)[e] = make_int4(0, 0, 0, 0);
+template <int N> __device__ __forceinline__ void clear_bins(int (&hist)[kBins]) {
+    for (int e = threadIdx.x; e < kBins / 4; e += N) reinterpret_cast<int4 *>(hist)[e] = make_int4(0, 0, 0, 0);
 }
 
 // Lists the pages of a row: the first and last ones that are always taken,
 // and the `take` best of the competing ones, whose keys are keys[0, comp).
 // Whole CTA; `hist` is clear.
-__device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, int pages, int comp, int (&hist)[kBins],
+template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, int pages, int comp, int (&hist)[kBins],
                                            const uint32_t *keys) {
-    __shared__ int wsum[kWarpsSel];
+    constexpr int W = N / 32;
+    __shared__ int wsum[W];
     __shared__ int s_bin, s_above, s_in, s_fill;
     __shared__ uint64_t s_cut;
     __shared__ uint64_t list[kRank];
@@ -221,7 +227,7 @@ __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, i
     int *idx = a.idx + row * a.topk;
     auto each = [&](auto f) {
 #pragma unroll 8
-        for (int c = tid; c < comp; c += kThreads) f(rank_of(keys[c], c));
+        for (int c = tid; c < comp; c += N) f(rank_of(keys[c], c));
     };
     // cut: the `take`-th largest rank (ranks are distinct); 2^59 when none is taken
     uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
@@ -233,13 +239,14 @@ __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, i
             if (k >> top == prefix) atomicAdd(&hist[(int)((k >> shift) & ((1u << bits) - 1u))], 1);
         });
         __syncthreads();
-        // thread t: bins 2047 - 8 t down to 2040 - 8 t
-        int cnt[kBins / kThreads], sum = 0;
+        // thread t: the bins 2047 - kPer t and down
+        constexpr int kPer = kBins / N;
+        int cnt[kPer], sum = 0;
 #pragma unroll
-        for (int e = 0; e < kBins / kThreads; e += 4) {
-            const int4 n = *reinterpret_cast<const int4 *>(&hist[kBins - 4 - tid * (kBins / kThreads) - e]);
-            cnt[e] = n.w, cnt[e + 1] = n.z, cnt[e + 2] = n.y, cnt[e + 3] = n.x;
-            sum += n.x + n.y + n.z + n.w;
+        for (int e = 0; e < kPer; e += 2) {
+            const int2 n = *reinterpret_cast<const int2 *>(&hist[kBins - 2 - tid * kPer - e]);
+            cnt[e] = n.y, cnt[e + 1] = n.x;
+            sum += n.x + n.y;
         }
         int inc = sum;
 #pragma unroll
@@ -250,13 +257,13 @@ __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, i
         if (lane == 31) wsum[wid] = inc;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarpsSel; ++w) inc += w < wid ? wsum[w] : 0;
+        for (int w = 0; w < W; ++w) inc += w < wid ? wsum[w] : 0;
         int above = inc - sum;  // pages in larger bins
         if (above < rem && inc >= rem) {
 #pragma unroll
-            for (int e = 0; e < kBins / kThreads; ++e)
+            for (int e = 0; e < kPer; ++e)
                 if (above < rem) {
-                    s_bin = kBins - 1 - tid * (kBins / kThreads) - e;
+                    s_bin = kBins - 1 - tid * kPer - e;
                     s_above = above;
                     s_in = cnt[e];
                     above += cnt[e];
@@ -287,10 +294,10 @@ __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, i
             cut = s_cut;
             break;
         }
-        clear_bins(hist);
+        clear_bins<N>(hist);
     }
     // pages at or above the cut, in order: each warp has a contiguous share
-    const int share = ((comp + kWarpsSel - 1) / kWarpsSel + 31) & ~31;
+    const int share = ((comp + W - 1) / W + 31) & ~31;
     const int lo = min(wid * share, comp), hi = min(lo + share, comp);
     auto chosen = [&](int c) { return rank_of(keys[c], c) >= cut; };
     int n = 0;
@@ -300,31 +307,31 @@ __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, i
     __syncthreads();
     int at = a.first;
 #pragma unroll
-    for (int w = 0; w < kWarpsSel; ++w) at += w < wid ? wsum[w] : 0;
+    for (int w = 0; w < W; ++w) at += w < wid ? wsum[w] : 0;
     for (int c = lo + lane; c - lane < hi; c += 32) {
         const bool on = c < hi && chosen(c);
         const unsigned m = __ballot_sync(0xffffffffu, on);
         if (on) idx[at + __popc(m & ((1u << lane) - 1u))] = a.first + c;
         at += __popc(m);
     }
-    for (int e = tid; e < a.first; e += kThreads) idx[e] = e;
-    for (int e = tid; e < a.last; e += kThreads) idx[a.topk - a.last + e] = pages - a.last + e;
+    for (int e = tid; e < a.first; e += N) idx[e] = e;
+    for (int e = tid; e < a.last; e += N) idx[a.topk - a.last + e] = pages - a.last + e;
     if (tid == 0) a.cnt[row] = a.topk;
 }
 
-__global__ void __launch_bounds__(kThreads) k_page_topk(SelectArgs a) {
+__global__ void __launch_bounds__(kTopkThreads) k_page_topk(SelectArgs a) {
     __shared__ __align__(16) int hist[kBins];
     const Paged &p = a.p;
     const long long row = blockIdx.x;
     const int b = (int)(row / p.Hkv);
-    clear_bins(hist);
+    clear_bins<kTopkThreads>(hist);
     grid_wait();
     grid_go();
     const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2, comp = competing(a, b);
     if (comp == 0)
-        list_all(a, row, pages);
+        list_all<kTopkThreads>(a, row, pages);
     else
-        list_pages(a, row, pages, comp, hist, a.keys + row * p.max_pages);
+        list_pages<kTopkThreads>(a, row, pages, comp, hist, a.keys + row * p.max_pages);
 }
 
 template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(SelectArgs a) {
@@ -337,13 +344,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int rank = (int)ptx::cluster_rank(), cl = (int)blockIdx.x / kCluster;
     const int b = cl / a.hgroups, h0 = (cl % a.hgroups) * a.hg, hn = min(a.hg, p.Hkv - h0);
-    clear_bins(hist);
+    clear_bins<kThreads>(hist);
     grid_wait();
     grid_go();
     const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2;
     const int comp = competing(a, b);
     if (comp == 0) {  // the same for every CTA of the cluster
-        if (rank < hn) list_all(a, (long long)b * p.Hkv + h0 + rank, pages);
+        if (rank < hn) list_all<kThreads>(a, (long long)b * p.Hkv + h0 + rank, pages);
         return;
     }
     const int run = (comp + kCluster - 1) / kCluster;
@@ -379,7 +386,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     ptx::cluster_sync();  // every run's keys are there
     if (rank >= hn) return;
 
-    list_pages(a, (long long)b * p.Hkv + h0 + rank, pages, comp, hist, mine);
+    list_pages<kThreads>(a, (long long)b * p.Hkv + h0 + rank, pages, comp, hist, mine);
 }
 
 }  // namespace
@@ -409,11 +416,11 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     a.keys = reinterpret_cast<uint32_t *>(static_cast<char *>(workspace) + ws.keys);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = a.p.dtype == T_BF16;
-    auto run = [&](const char *name, auto kernel, dim3 grid, size_t smem, unsigned cluster) {
+    auto run = [&](const char *name, auto kernel, dim3 grid, int threads, size_t smem, unsigned cluster) {
         cudaError_t e = ensure_smem_limit((const void *)kernel, (int)smem);
         if (e != cudaSuccess) return status_from_cuda(e);
         prof_begin(name, s);
-        e = launch_paged(kernel, grid, kThreads, smem, cluster, a, s);
+        e = launch_paged(kernel, grid, threads, smem, cluster, a, s);
         prof_end(s);
         return status_from_cuda(e);
     };
@@ -426,13 +433,13 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     if ((long long)a.p.max_pages * a.hg <= kClusterPages && ctas <= kCtasSel) {
         a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
         const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
-        return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas), smem,
-                   kCluster);
+        return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
+                   kThreads, smem, kCluster);
     }
     if (a.p.max_pages > topk) {  // otherwise no row has anything to choose
         const vsa_status e = run("page_scores", bf ? k_page_scores<__nv_bfloat16> : k_page_scores<__half>,
-                                 dim3(kCtasSel), kSmemSel, 1);
+                                 dim3(kCtasSel), kThreads, kSmemSel, 1);
         if (e != VSA_OK) return e;
     }
-    return run("page_topk", k_page_topk, dim3((unsigned)(a.p.B * a.p.Hkv)), 0, 1);
+    return run("page_topk", k_page_topk, dim3((unsigned)(a.p.B * a.p.Hkv)), kTopkThreads, 0, 1);
 }
