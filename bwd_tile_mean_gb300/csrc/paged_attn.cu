@@ -5,29 +5,30 @@
 //
 // A segment is one (sequence, key/value head, chunk of up to 16 query heads
 // of its group: one tile of the tensor instructions; a wider group's chunks
-// read the same keys, from L2 but for the first); its keys, in the order of the pages attended, are
-// cut into blocks of 16. The blocks of all segments, end to end, are dealt
-// to the grid's warps in equal contiguous runs, whatever the lengths of the
-// batch: a CTA finds its run with one scan of the lengths, and each warp
-// walks the segments of its own part of it. A segment inside one warp's run
-// is finished there. Where a CTA's whole run lies in one segment its warps'
-// results are joined in shared memory first; the remaining pieces of
-// segments that cross runs go to the workspace (at most two per warp) and
-// k_paged_join adds them in ascending order. When the table or the page
-// lists allow only short segments (up to kAlignedKeys keys per CTA) each
-// segment gets a CTA, or a cluster of CTAs that join through distributed
-// shared memory, and one launch does it all.
+// read the same keys, from L2 but for the first); its keys, in the order of
+// the pages attended, are cut into blocks of 16. A warp streams a run of
+// blocks through its own ring of asynchronous copies (16 K rows and 16 V rows
+// of 256 bytes per stage, swizzled so that ldmatrix reads hit distinct banks;
+// rows past a page's valid slots are filled with zeros, so whatever the cache
+// holds there cannot reach the sums) and keeps its own running maximum, sum
+// and output in registers: no warp waits for another while it streams. The
+// products run on m16n8k16 tensor instructions with the group's query heads
+// as rows. At one query token per sequence the kernel reads 512 bytes per
+// 256 G multiply-adds, far to the memory side of the tensor cores' balance, so
+// the instruction's rate does not bound it; the memory pipe does, and for
+// short segments the chain of dependent loads before the first product.
 //
-// A warp takes its blocks through its own ring of asynchronous copies (16 K
-// rows and 16 V rows of 256 bytes per stage, swizzled so that ldmatrix reads
-// hit distinct banks; rows past a page's valid slots are filled with zeros,
-// so whatever the cache holds there cannot reach the sums) and keeps its own
-// running maximum, sum and output in registers: no warp waits for another
-// while it streams. The products run on m16n8k16 tensor instructions with
-// the group's query heads as rows. At one query token per sequence the
-// kernel reads 512 bytes per 256 G multiply-adds, far to the memory side of
-// the tensor cores' balance, so the instruction's rate does not bound it;
-// the memory pipe does, and the loads in flight on it.
+// Short or equal segments: k_paged_attn_cluster, one launch. A segment is one
+// cluster's (of 1 to 16 CTAs); the CTAs join their four warps' results in
+// shared memory and send each row to the CTA that finishes it.
+// Any lengths: k_paged_attn_runs. The blocks of all segments, end to end, are
+// dealt to the grid's warps in equal contiguous runs, whatever the lengths of
+// the batch: a CTA finds its run with one scan of the lengths, and each warp
+// walks the segments of its own part of it. A segment inside one warp's run
+// is finished there; where a CTA's whole run lies in one segment its warps'
+// results are joined first; the remaining pieces of segments that cross runs
+// go to the workspace (at most two per warp), and k_paged_join adds them in
+// ascending order.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -41,8 +42,9 @@ constexpr int kRows = 16;       // query heads per segment at most
 constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time)
 constexpr int kMinBlocks = 4;   // fewest blocks a warp's run has when there is little work
 constexpr int kAlignedKeys = 2048;  // keys per CTA up to which a segment is one CTA's or one cluster's
+constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does not grow
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kWarps = 4;
 constexpr int kStages = 3;      // ring stages per warp
 constexpr int kCtas = 304;      // two per SM on 152 SMs
@@ -61,8 +63,7 @@ struct AttnArgs {
     void *out;
     float *lse;
     int rc, rows;          // chunks of a group's heads, rows per chunk
-    int aligned;           // CTAs per segment, one cluster; 0: equal runs of all segments' blocks
-    int lead;              // kLead, 0 when aligned
+    int cluster;           // CTAs per segment, one cluster; 0: equal runs of all segments' blocks
     int4 *seg;             // [segments] its pieces: first warp, warps before / CTAs joined / pieces in all
     float2 *ml;            // [2 * kCtas * kWarps, rows]
     float *o;              // [2 * kCtas * kWarps, rows, 128]
@@ -75,22 +76,22 @@ __device__ __forceinline__ int seg_keys(const AttnArgs &a, int n) {
     return clampi(__ldg(a.cnt + n), 0, a.cap) * a.p.page;
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void *src, bool fill) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(fill ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// Copies the first `bytes` (0 or 16) and fills the rest with zeros.
+__device__ __forceinline__ void cp16z(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
-    float2 v;
-    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
-    return v;
+__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -123,257 +124,371 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Blocks of a segment, its lead in front of its own counted in.
-__device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) {
-    const int nb = (seg_keys(a, n) + kBlk - 1) / kBlk;
-    return nb > 0 ? nb + a.lead : 0;
+__device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) { return (seg_keys(a, n) + kBlk - 1) / kBlk; }
+// x / d for 0 <= x: in 32 bits where they hold it.
+__device__ __forceinline__ int div_small(long long x, int d) {
+    return x <= 0x7fffffffLL ? (int)((unsigned)x / (unsigned)d) : (int)(x / d);
 }
 
-template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn(AttnArgs a) {
+// Where a segment's queries, keys and outputs are.
+struct Segment {
+    int bh, b, h;        // list row, sequence, key/value head
+    int rows;            // query heads
+    long long hq0;       // first (sequence, query head)
+};
+__device__ __forceinline__ Segment segment_of(const AttnArgs &a, int bh, int r) {
+    const Paged &p = a.p;
+    Segment s;
+    s.bh = bh;
+    s.b = bh / p.Hkv;
+    s.h = bh % p.Hkv;
+    s.rows = min(a.rows, p.G - r * a.rows);
+    s.hq0 = (long long)s.b * p.Hq + s.h * p.G + r * a.rows;
+    return s;
+}
+
+// Q as A fragments: row g (and g + 8), 8 k-steps; rows past the segment's are zero.
+template <typename T> __device__ __forceinline__ void load_q(const AttnArgs &a, const Segment &sg, uint32_t (&qa)[8][4]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const T *qb = static_cast<const T *>(a.q) + (long long)sg.b * a.qs + (sg.hq0 - (long long)sg.b * a.p.Hq) * kD;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int row = g + 8 * e;
+        const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            qa[j][e] = row < sg.rows ? __ldg(src + 8 * j + t) : 0u;
+            qa[j][2 + e] = row < sg.rows ? __ldg(src + 8 * j + 4 + t) : 0u;
+        }
+    }
+}
+
+// One warp streams blocks [blk0, blk0 + nblk) of a segment: the running
+// maximum (log2 units) and sum of rows g and g + 8, and their unnormalised
+// outputs at dims 8 j + 2 t, + 1. The warp's ring is free again afterwards.
+template <typename T>
+__device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &sg, const uint32_t (&qa)[8][4], int len,
+                                              int blk0, int nblk, uint32_t ring, float (&m_run)[2], float (&l_run)[2],
+                                              float (&acc)[16][4]) {
+    const Paged &p = a.p;
+    const int lane = threadIdx.x & 31, t = lane & 3, b = sg.b, bh = sg.bh;
+    const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v);
+    const float sl2 = p.scale * kLog2e;
+    const int key0 = blk0 * kBlk;
+    const long long hoff = (long long)sg.h * p.head_stride;
+    // Window of up to 32 blocks, one per lane: the page (or -1), the
+    // slot in it and the valid slots of the block.
+    int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
+    auto window = [&](int i0) {
+        w_base = i0;
+        w_id = -1;
+        w_valid = 0;
+        if (i0 + lane < nblk) {
+            const int pos = key0 + (i0 + lane) * kBlk;
+            int j = pos >> p.page_log2;
+            w_slot = pos & (p.page - 1);
+            if (a.idx) j = __ldg(a.idx + (long long)bh * a.cap + j);
+            w_id = paged_id(p, b, j);
+            if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
+        }
+    };
+    int valid[kStages];
+    // Copy e of a lane: rows 2 e (lanes 0-15) and 2 e + 1 (16-31), 16-byte chunk lane % 16, stored at chunk
+    // (lane % 16) ^ (row % 8).
+    const long long lane_at = hoff + (lane >> 4) * p.tok_stride + 8 * (lane & 15);
+    const uint32_t lane_dst = (lane >> 4) * 256 + (((lane & 15) ^ (lane >> 4)) << 4);
+    const uint32_t step = (uint32_t)p.tok_stride * 4;  // bytes of two rows
+    auto issue = [&](int i, int stage) {  // block i of this piece into a stage
+        if (i >= w_base + 32) window(i);
+        const int id = __shfl_sync(0xffffffffu, w_id, i - w_base);
+        const int slot = __shfl_sync(0xffffffffu, w_slot, i - w_base);
+        const int ok = __shfl_sync(0xffffffffu, w_valid, i - w_base);
+        // A block lies inside its page, so the address of a row without a token is the page's own too.
+        const long long at = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + lane_at;
+        const char *kp = reinterpret_cast<const char *>(K + at), *vp = reinterpret_cast<const char *>(V + at);
+        const uint32_t dst = ring + stage * kStageBytes + lane_dst;
+        if (ok == kBlk) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                cp16((dst + e * 512) ^ ((2 * e & 7) << 4), kp + (uint64_t)e * step);
+                cp16((dst + kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), vp + (uint64_t)e * step);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int bytes = 2 * e + (lane >> 4) < ok ? 16 : 0;
+                cp16z((dst + e * 512) ^ ((2 * e & 7) << 4), kp + (uint64_t)e * step, bytes);
+                cp16z((dst + kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), vp + (uint64_t)e * step, bytes);
+            }
+        }
+        return ok;
+    };
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        valid[s] = 0;
+        if (s < nblk) valid[s] = issue(s, s);
+        cp_commit();
+    }
+    valid[kStages - 1] = 0;
+
+    m_run[0] = m_run[1] = -INFINITY;
+    l_run[0] = l_run[1] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+    for (int i0 = 0; i0 < nblk; i0 += kStages) {
+#pragma unroll
+        for (int s = 0; s < kStages; ++s) {
+            const int i = i0 + s;
+            if (i >= nblk) break;
+            cp_wait<kStages - 2>();
+            __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
+            const uint32_t st = ring + s * kStageBytes;
+            // All K fragments before the products that use them: the loads' latency is paid once a block.
+            uint32_t kb[8][4];
+            {
+                const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) ldsm4(kb[j], st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
+            }
+            if (i + kStages - 1 < nblk)
+                valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
+            cp_commit();
+            float sc[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                mma16816<T>(sc[0], qa[j], kb[j][0], kb[j][1]);
+                mma16816<T>(sc[1], qa[j], kb[j][2], kb[j][3]);
+            }
+            // half of V's fragments, to arrive while the softmax runs
+            const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc0 = lane >> 4;
+            auto ld_v = [&](uint32_t (&r)[4], int j) {
+                ldsm4t(r, st + kBlk * 256 + vrow * 256 + (((2 * j + vc0) ^ (vrow & 7)) << 4));
+            };
+            uint32_t vb[4][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) ld_v(vb[j], j);
+            if (valid[s] < kBlk) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (8 * u + 2 * t + (e & 1) >= valid[s]) sc[u][e] = -INFINITY;
+            }
+            // running maximum m of the unscaled scores; P = 2^(scale log2(e) (s - m))
+            float corr[2];
+            bool moved = false;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float mx = fmaxf(ptx::fmax3(sc[0][2 * e], sc[0][2 * e + 1], sc[1][2 * e]), sc[1][2 * e + 1]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = ptx::fmax3(m_run[e], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                moved = moved || mx != m_run[e];
+                const float ref = mx == -INFINITY ? 0.f : mx * sl2;  // a row without keys so far
+                corr[e] = ptx::ex2(fmaf(m_run[e], sl2, -ref));
+                m_run[e] = mx;
+                float sum = 0.f;
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float pr = ptx::ex2(fmaf(sc[u][2 * e + c], sl2, -ref));
+                        sc[u][2 * e + c] = pr;
+                        sum += pr;
+                    }
+                l_run[e] = fmaf(l_run[e], corr[e], sum);  // this lane's keys; quads are joined at the end
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    acc[j][0] *= corr[0];
+                    acc[j][1] *= corr[0];
+                    acc[j][2] *= corr[1];
+                    acc[j][3] *= corr[1];
+                }
+            }
+            // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the
+            // unrounded values): half a step of the output's own type
+            const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
+                                    pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                mma16816<T>(acc[2 * j], pa, vb[j & 3][0], vb[j & 3][1]);
+                mma16816<T>(acc[2 * j + 1], pa, vb[j & 3][2], vb[j & 3][3]);
+                if (j < 4) ld_v(vb[j], j + 4);
+            }
+        }
+    }
+    cp_wait<0>();
+    __syncwarp();  // the warp's ring is free
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
+        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
+        m_run[e] *= sl2;  // log2 units from here on
+    }
+}
+
+// Joins the CTA's four warps: f(row, o, M, l) per row, in the thread of its
+// dim, with the unnormalised output o, the maximum M (log2 units) and the sum
+// l. The warps' rings hold the outputs meanwhile.
+template <typename F>
+__device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const float (&m_run)[2], const float (&l_run)[2],
+                                           const float (&acc)[16][4], F f) {
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
+    __shared__ float2 s_ml[kRows];
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int row = g + 8 * e;
+        if (t == 0) {
+            s_m[wid][row] = m_run[e];
+            s_l[wid][row] = l_run[e];
+        }
+        if (row < rows)
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+    }
+    __syncthreads();
+    if (tid < kWarps * kRows) {  // the warps' weights
+        const int w = tid / kRows, row = tid % kRows;
+        float M = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) M = fmaxf(M, s_m[v][row]);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll
+        for (int v = 0; v < kWarps; ++v) l += ptx::ex2(s_m[v][row] - ref) * s_l[v][row];
+        s_f[w][row] = ptx::ex2(s_m[w][row] - ref);
+        if (w == 0) s_ml[row] = make_float2(M, l);
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (int row = 0; row < rows; ++row) {
+        float o = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w)
+            o += s_f[w][row] * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
+        f(row, o, s_ml[row].x, s_ml[row].y);
+    }
+}
+__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : kLn2 * (M + log2f(l)); }
+
+// A cluster per segment (a.cluster CTAs of four warps, equal runs of its
+// blocks). Row r is finished by CTA r % cluster, which has a place for every
+// CTA's part of it.
+template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
-    __shared__ float2 s_cta[kRows];  // the CTA's own maximum and sum, for its cluster
+    __shared__ float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
+    __shared__ float2 s_pml[kRows];
+    const int tid = threadIdx.x, wid = tid >> 5, CS = a.cluster;
+    const int rank = (int)(blockIdx.x % CS), segment = (int)(blockIdx.x / CS);
+    grid_wait();
+    grid_go();
+    if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+    const int bh = segment / a.rc;
+    const Segment sg = segment_of(a, bh, segment % a.rc);
+    const int len = paged_len(a.p, sg.b), nb = seg_blocks(a, a.idx ? bh : sg.b);
+    uint32_t qa[8][4];
+    load_q<T>(a, sg, qa);
+    const int per = (nb + CS * kWarps - 1) / (CS * kWarps);
+    const int blk0 = min((rank * kWarps + wid) * per, nb), nblk = min(per, nb - blk0);
+    float m_run[2], l_run[2], acc[16][4];
+    stream_blocks<T>(a, sg, qa, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
+    T *out = static_cast<T *>(a.out);
+    if (CS == 1) {
+        join_warps(smem, sg.rows, m_run, l_run, acc, [&](int row, float o, float M, float l) {
+            out[(sg.hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
+            if (tid == 0) a.lse[sg.hq0 + row] = lse_of(M, l);
+        });
+        return;
+    }
+    const int own = (sg.rows + CS - 1) / CS;  // rows a CTA finishes at most
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
+    join_warps(smem, sg.rows, m_run, l_run, acc, [&](int row, float o, float M, float l) {
+        const uint32_t at = rank * own + row / CS;
+        st_cluster(ptx::cluster_addr(ptx::smem_addr(&s_part[at][tid]), row % CS), o);
+        if (tid == 0) st_cluster2(ptx::cluster_addr(ptx::smem_addr(&s_pml[at]), row % CS), make_float2(M, l));
+    });
+    ptx::cluster_sync();  // the parts are there
+    for (int row = rank; row < sg.rows; row += CS) {
+        const int at = row / CS;
+        float M = -INFINITY, l = 0.f, o = 0.f;
+        for (int c = 0; c < CS; ++c) M = fmaxf(M, s_pml[c * own + at].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+#pragma unroll 4
+        for (int c = 0; c < CS; ++c) {
+            const float f = ptx::ex2(s_pml[c * own + at].x - ref);
+            l += f * s_pml[c * own + at].y;
+            o += f * s_part[c * own + at][tid];
+        }
+        out[(sg.hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
+        if (tid == 0) a.lse[sg.hq0 + row] = lse_of(M, l);
+    }
+}
+
+// Equal runs of all segments' blocks. A segment counts kLead blocks more than
+// it has, in front of its own.
+template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
+    extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     grid_wait();
     grid_go();
-    const int N = a.idx ? p.B * p.Hkv : p.B;             // list entries
-    const int mult = a.idx ? a.rc : p.Hkv * a.rc;        // segments per entry
-    const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v), *Q = static_cast<const T *>(a.q);
-    const uint32_t ring = ptx::smem_addr(smem) + wid * kStages * kStageBytes;
-    const float sl2 = p.scale * kLog2e;
-
-    Run run;
-    const int segment = a.aligned ? (int)(blockIdx.x / a.aligned) : 0;
-    if (a.aligned) {
-        run.n = segment / mult;
-        const int nb = seg_blocks(a, run.n), at = (int)(blockIdx.x % a.aligned) * kWarps;
-        run.per = (nb + a.aligned * kWarps - 1) / (a.aligned * kWarps);
-        run.before = 0;
-        run.x0 = (long long)(segment % mult) * nb + min((long long)at * run.per, (long long)nb);
-        run.x1 = (long long)(segment % mult) * nb + min((long long)(at + kWarps) * run.per, (long long)nb);
-        run.total = 0;
-    } else {
-        run = find_run<kWarps>(
-            N, [&](int n) -> long long { return (long long)seg_blocks(a, n) * mult; }, kCtas * kWarps, kMinBlocks,
-            kWarps);
-        if (run.x0 >= run.x1) return;
-    }
+    const int N = a.idx ? p.B * p.Hkv : p.B;       // list entries
+    const int mult = a.idx ? a.rc : p.Hkv * a.rc;  // segments per entry
+    auto weight = [&](int n) {
+        const int nb = seg_blocks(a, n);
+        return nb > 0 ? nb + kLead : 0;
+    };
+    const Run run = find_run<kWarps>(
+        N, [&](int n) -> long long { return (long long)weight(n) * mult; }, kCtas * kWarps, kMinBlocks, kWarps);
+    if (run.x0 >= run.x1) return;
+    int n = run.n, nb = weight(n);
+    long long before = run.before;
     // the CTA's run lies in one segment: its warps' results are joined
-    bool joined = a.aligned;
-    if (!a.aligned) {
-        const int nb = seg_blocks(a, run.n);
-        joined = (run.x0 - run.before) / nb == (run.x1 - 1 - run.before) / nb && run.x1 <= run.before + (long long)nb * mult;
-    }
+    const int sub0 = div_small(run.x0 - before, nb);
+    const bool joined = run.x1 <= before + (long long)(sub0 + 1) * nb;
     long long x = min(run.x0 + wid * run.per, run.x1);
     const long long x_end = min(x + run.per, run.x1);
-    int n = run.n;
-    long long before = run.before;
-    bool more = joined || x < x_end;  // a joined CTA's warp without blocks still brings its empty part
-    while (more) {
-        int nb = n < N ? seg_blocks(a, n) : 0;
+    T *out = static_cast<T *>(a.out);
+    while (joined || x < x_end) {  // a joined CTA's warp without blocks still brings its empty part
         if (!joined && x >= before + (long long)nb * mult) {  // also passes over entries without keys
             before += (long long)nb * mult;
-            if (++n >= N) break;
+            if (++n >= N) return;
+            nb = weight(n);
             continue;
         }
-        long long seg0;   // first block of the segment
-        int sub, off, take;
-        if (joined) {     // the segment is the run's, also for a warp without blocks
-            sub = a.aligned ? segment % mult : (int)((run.x0 - before) / nb);
-            seg0 = before + (long long)sub * nb;
-            off = (int)(x - seg0);
-            take = (int)(x_end - x);
-        } else {
-            sub = (int)((x - before) / nb);
-            seg0 = before + (long long)sub * nb;
-            off = (int)(x - seg0);
-            take = (int)min((long long)(nb - off), x_end - x);
-        }
+        const int sub = joined ? sub0 : div_small(x - before, nb);
+        const long long seg0 = before + (long long)sub * nb;  // the segment's first block
+        int off = (int)(x - seg0), take = (int)min((long long)(nb - off), x_end - x);
         const bool first = joined ? run.x0 == seg0 : off == 0;
         const bool last = joined ? run.x1 == seg0 + nb : off + take == nb;
         x += take;
         {   // the piece's own blocks: those behind the lead
-            const int skip = clampi(a.lead - off, 0, take);
-            off += skip - a.lead;
+            const int skip = clampi(kLead - off, 0, take);
+            off += skip - kLead;
             take -= skip;
         }
         const int r = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
-        const int b = bh / p.Hkv, h = bh % p.Hkv;
-        const int rows = min(a.rows, p.G - r * a.rows);
-        const int len = paged_len(p, b);
-        const int key0 = off * kBlk;
-        const long long hoff = (long long)h * p.head_stride;
-
-        // Q as A fragments: row g (and g + 8) of each 16-row tile, 8 k-steps
+        const Segment sg = segment_of(a, bh, r);
+        const int len = paged_len(p, sg.b);
         uint32_t qa[8][4];
-        {
-            const T *qb = Q + (long long)b * a.qs + ((long long)h * p.G + r * a.rows) * kD;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = g + 8 * e;
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    qa[j][e] = row < rows ? __ldg(src + 8 * j + t) : 0u;
-                    qa[j][2 + e] = row < rows ? __ldg(src + 8 * j + 4 + t) : 0u;
-                }
-            }
-        }
-
-        // Window of up to 32 blocks, one per lane: the page (or -1), the
-        // slot in it and the valid slots of the block.
-        int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
-        auto window = [&](int i0) {
-            w_base = i0;
-            w_id = -1;
-            w_valid = 0;
-            if (i0 + lane < take) {
-                const int pos = key0 + (i0 + lane) * kBlk;
-                int j = pos >> p.page_log2;
-                w_slot = pos & (p.page - 1);
-                if (a.idx) j = __ldg(a.idx + (long long)bh * a.cap + j);
-                w_id = paged_id(p, b, j);
-                if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
-            }
-        };
-        int valid[kStages];
-        auto issue = [&](int i, int stage) {  // block i of this piece into a stage
-            if (i >= w_base + 32) window(i);
-            const int id = __shfl_sync(0xffffffffu, w_id, i - w_base);
-            const int slot = __shfl_sync(0xffffffffu, w_slot, i - w_base);
-            const int ok = __shfl_sync(0xffffffffu, w_valid, i - w_base);
-            const long long at = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + hoff;
-            const int c = lane & 15;
-            const uint32_t dst = ring + stage * kStageBytes;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 2 * e + (lane >> 4);
-                const bool live = row < ok;
-                const long long src = live ? at + row * p.tok_stride + 8 * c : 0;
-                const uint32_t d = dst + row * 256 + ((c ^ (row & 7)) << 4);
-                cp16(d, K + src, live);
-                cp16(d + kBlk * 256, V + src, live);
-            }
-            return ok;
-        };
-#pragma unroll
-        for (int s = 0; s < kStages - 1; ++s) {
-            valid[s] = 0;
-            if (s < take) valid[s] = issue(s, s);
-            cp_commit();
-        }
-        valid[kStages - 1] = 0;
-
-        float m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f}, acc[16][4];  // rows g and g + 8
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-        for (int i0 = 0; i0 < take; i0 += kStages) {
-#pragma unroll
-            for (int s = 0; s < kStages; ++s) {
-                const int i = i0 + s;
-                if (i >= take) break;
-                cp_wait<kStages - 2>();
-                __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
-                const uint32_t st = ring + s * kStageBytes;
-                // All K fragments before the products that use them: the loads' latency is paid once a block.
-                uint32_t kb[8][4];
-                {
-                    const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) ldsm4(kb[j], st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-                }
-                if (i + kStages - 1 < take)
-                    valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
-                cp_commit();
-                float sc[2][4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    mma16816<T>(sc[0], qa[j], kb[j][0], kb[j][1]);
-                    mma16816<T>(sc[1], qa[j], kb[j][2], kb[j][3]);
-                }
-                // half of V's fragments, to arrive while the softmax runs
-                const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc0 = lane >> 4;
-                auto ld_v = [&](uint32_t (&r)[4], int j) {
-                    ldsm4t(r, st + kBlk * 256 + vrow * 256 + (((2 * j + vc0) ^ (vrow & 7)) << 4));
-                };
-                uint32_t vb[4][4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) ld_v(vb[j], j);
-                const int ok = valid[s];
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = 8 * u + 2 * t + (e & 1);
-                        sc[u][e] = key < ok ? sc[u][e] * sl2 : -INFINITY;
-                    }
-                float corr[2];
-                bool moved = false;
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float mx = fmaxf(fmaxf(sc[0][2 * e], sc[0][2 * e + 1]), fmaxf(sc[1][2 * e], sc[1][2 * e + 1]));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                    const float mn = fmaxf(m_run[e], mx);
-                    const float ref = mn == -INFINITY ? 0.f : mn;  // a row without keys so far
-                    corr[e] = ptx::ex2(m_run[e] - ref);
-                    moved = moved || mn != m_run[e];
-                    m_run[e] = mn;
-                    float sum = 0.f;
-#pragma unroll
-                    for (int u = 0; u < 2; ++u)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const float pr = ptx::ex2(sc[u][2 * e + c] - ref);
-                            sc[u][2 * e + c] = pr;
-                            sum += pr;
-                        }
-                    l_run[e] = l_run[e] * corr[e] + sum;  // this lane's keys; quads are joined at the end
-                }
-                if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                        acc[j][0] *= corr[0];
-                        acc[j][1] *= corr[0];
-                        acc[j][2] *= corr[1];
-                        acc[j][3] *= corr[1];
-                    }
-                }
-                // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the
-                // unrounded values): half a step of the output's own type
-                const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
-                                        pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    mma16816<T>(acc[2 * j], pa, vb[j & 3][0], vb[j & 3][1]);
-                    mma16816<T>(acc[2 * j + 1], pa, vb[j & 3][2], vb[j & 3][3]);
-                    if (j < 4) ld_v(vb[j], j + 4);
-                }
-            }
-        }
-        cp_wait<0>();
-        __syncwarp();  // the warp's ring is free
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
-            l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
-        }
-        const long long hq0 = (long long)b * p.Hq + h * p.G + r * a.rows;  // first output row of the segment
+        load_q<T>(a, sg, qa);
+        float m_run[2], l_run[2], acc[16][4];
+        stream_blocks<T>(a, sg, qa, len, off, take, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
 
         // A piece of the segment that begins it describes all of its pieces.
-        const int gw = (int)blockIdx.x * kWarps + (joined ? 0 : wid);
-        const long long slot = 2LL * gw + (first ? 1 : 0);
-        if (!a.aligned && first && lane == 0 && (!joined || wid == 0)) {
+        const long long slot = 2LL * ((int)blockIdx.x * kWarps + (joined ? 0 : wid)) + (first ? 1 : 0);
+        if (first && lane == 0 && (!joined || wid == 0)) {
             const long long s1 = seg0 + nb, cta = run.per * kWarps;
-            const int w_last = (int)((s1 - 1) / run.per);
+            const int w0 = (int)(seg0 / run.per), w_last = (int)((s1 - 1) / run.per);
             const int ca = (int)((seg0 + cta - 1) / cta);
             const int cb = (int)(s1 == run.total ? (s1 + cta - 1) / cta : s1 / cta);
-            const int w0 = (int)(seg0 / run.per);
             int4 d = make_int4(w0, w_last + 1 - w0, 0, w_last + 1 - w0);
             if (cb > ca) {
                 d.y = ca * kWarps - w0;
@@ -382,88 +497,29 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
             }
             a.seg[(long long)bh * a.rc + r] = d;
         }
-
-        if (joined) {  // the warps' outputs in shared memory, one thread per dim
-            float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int row = g + 8 * e;
-                if (t == 0) {
-                    s_m[wid][row] = m_run[e];
-                    s_l[wid][row] = l_run[e];
-                }
-                if (row < rows)
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
-                            make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
-            }
-            __syncthreads();
-            for (int row = 0; row < rows; ++row) {
-                float M = -INFINITY;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w][row]);
-                const float ref = M == -INFINITY ? 0.f : M;
-                float l = 0.f, o = 0.f;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
-                    const float f = ptx::ex2(s_m[w][row] - ref);
-                    l += f * s_l[w][row];
-                    o += f * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
-                }
-                if (a.aligned > 1) {  // in place: this thread alone reads and writes the element
-                    reinterpret_cast<float *>(smem)[row * kPitch + tid] = o;
-                    if (tid == 0) s_cta[row] = make_float2(M, l);
-                } else if (a.aligned || (first && last)) {
-                    static_cast<T *>(a.out)[(hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
-                    if (tid == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+        if (joined) {
+            join_warps(smem, sg.rows, m_run, l_run, acc, [&](int row, float o, float M, float l) {
+                if (first && last) {
+                    out[(sg.hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : o / l);
+                    if (tid == 0) a.lse[sg.hq0 + row] = lse_of(M, l);
                 } else {
                     a.o[(slot * a.rows + row) * kD + tid] = o;
                     if (tid == 0) a.ml[slot * a.rows + row] = make_float2(M, l);
                 }
-            }
-            if (a.aligned > 1) {  // the cluster's CTAs, each for its share of the rows
-                ptx::cluster_sync();
-                const uint32_t at_o = ptx::smem_addr(smem) + tid * 4, at_ml = ptx::smem_addr(s_cta);
-                for (int row = (int)ptx::cluster_rank(); row < rows; row += a.aligned) {
-                    float2 ml[kMaxCluster];
-                    float o[kMaxCluster], M = -INFINITY, l = 0.f, sum = 0.f;
-#pragma unroll
-                    for (int c = 0; c < kMaxCluster; ++c) {
-                        ml[c] = make_float2(-INFINITY, 0.f);
-                        o[c] = 0.f;
-                        if (c < a.aligned) {
-                            ml[c] = ld_cluster2(ptx::cluster_addr(at_ml + row * 8, c));
-                            o[c] = ld_cluster(ptx::cluster_addr(at_o + row * kPitch * 4, c));
-                        }
-                    }
-#pragma unroll
-                    for (int c = 0; c < kMaxCluster; ++c) M = fmaxf(M, ml[c].x);
-                    const float ref = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                    for (int c = 0; c < kMaxCluster; ++c) {
-                        const float f = ptx::ex2(ml[c].x - ref);
-                        l += f * ml[c].y;
-                        sum += f * o[c];
-                    }
-                    static_cast<T *>(a.out)[(hq0 + row) * kD + tid] = from_f<T>(l == 0.f ? 0.f : sum / l);
-                    if (tid == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
-                }
-                ptx::cluster_sync();  // no CTA leaves while another reads its part
-            }
+            });
             return;
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int row = g + 8 * e;
-            if (row >= rows) continue;
+            if (row >= sg.rows) continue;
             const float l = l_run[e];
             if (first && last) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
-                uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + (hq0 + row) * kD);
+                uint32_t *dst = reinterpret_cast<uint32_t *>(out + (sg.hq0 + row) * kD);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) dst[4 * j + t] = pack2<T>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
-                if (t == 0) a.lse[hq0 + row] = l == 0.f ? -INFINITY : kLn2 * (m_run[e] + log2f(l));
+                if (t == 0) a.lse[sg.hq0 + row] = lse_of(m_run[e], l);
             } else {
                 float *dst = a.o + (slot * a.rows + row) * kD;
 #pragma unroll
@@ -472,7 +528,6 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
                 if (t == 0) a.ml[slot * a.rows + row] = make_float2(m_run[e], l);
             }
         }
-        more = x < x_end;
     }
 }
 
@@ -582,14 +637,24 @@ int rows_of(int G) {
 }
 
 template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
-    const unsigned grid = a.aligned ? (unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.aligned) : kCtas;
-    const unsigned cluster = a.aligned > 1 ? a.aligned : 1;
-    cudaError_t e = ensure_smem_limit((const void *)k_paged_attn<T>, kSmem);
+    if (a.cluster) {
+        const auto kernel = k_paged_attn_cluster<T>;
+        cudaError_t e = ensure_smem_limit((const void *)kernel, kSmem);
+        if (e == cudaSuccess && a.cluster > 8)
+            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return status_from_cuda(e);
+        prof_begin("paged_attn", s);
+        e = launch_paged(kernel, dim3((unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.cluster)), kWarps * 32, kSmem,
+                         a.cluster, a, s);
+        prof_end(s);
+        return status_from_cuda(e);
+    }
+    cudaError_t e = ensure_smem_limit((const void *)k_paged_attn_runs<T>, kSmem);
     if (e != cudaSuccess) return status_from_cuda(e);
     prof_begin("paged_attn", s);
-    e = launch_paged(k_paged_attn<T>, grid, kWarps * 32, kSmem, cluster, a, s);
+    e = launch_paged(k_paged_attn_runs<T>, dim3(kCtas), kWarps * 32, kSmem, 1, a, s);
     prof_end(s);
-    if (e != cudaSuccess || a.aligned) return status_from_cuda(e);
+    if (e != cudaSuccess) return status_from_cuda(e);
     prof_begin("paged_join", s);
     const unsigned out_rows = (unsigned)(a.p.B * a.p.Hq);
     e = out_rows <= kJoinFew    ? launch_paged(k_paged_join<T, 16, 1>, dim3(out_rows), 512, 0, 1, a, s)
@@ -653,15 +718,15 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
-    // One cluster per segment, the smallest that gives every SM a CTA. Segments of one length (one sequence, or
-    // page lists) are then balanced by themselves; of unknown lengths only while the longest stays short.
+    // One cluster per segment: twice the CTAs while that leaves an SM without one and every CTA with kClusterKeys
+    // keys. Segments of one length (one sequence, or page lists) are then balanced by themselves; of unknown lengths
+    // only while the longest stays short.
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
     int cluster = 1;
-    while (cluster < kMaxCluster && segments * cluster < 152) cluster *= 2;
+    while (cluster < kMaxCluster && segments * cluster < 152 && most > (long long)kClusterKeys * cluster) cluster *= 2;
     const bool even = page_idx || a.p.B == 1;
     const bool few = most <= (long long)kAlignedKeys * cluster && segments * cluster <= kCtas;
-    a.aligned = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
-    a.lead = a.aligned ? 0 : kLead;
+    a.cluster = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
     char *w = static_cast<char *>(workspace);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);
     a.ml = reinterpret_cast<float2 *>(w + ws.ml);
