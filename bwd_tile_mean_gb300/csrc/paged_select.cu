@@ -287,6 +287,7 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
             if (tid < in) {
                 const uint64_t k = list[tid];
                 int larger = 0;
+#pragma unroll 8
                 for (int e = 0; e < in; ++e) larger += list[e] > k ? 1 : 0;
                 if (larger == rem - 1) s_cut = k;
             }
