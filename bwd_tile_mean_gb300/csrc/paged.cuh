@@ -23,6 +23,7 @@ struct Paged {
 };
 
 constexpr int kD = 128;
+constexpr int kMaxHeads = 65536;  // key/value heads: a token's bytes stay within 32 bits
 
 // Sequence length, clamped into what the page table can hold.
 __device__ __forceinline__ int paged_len(const Paged &p, int b) { return clampi(__ldg(p.lens + b), 0, p.max_len); }
@@ -40,7 +41,7 @@ inline vsa_status to_paged(const vsa_paged_desc *d, Paged *p, bool need_arrays) 
     if (d->layout != VSA_LAYOUT_BSHD && d->layout != VSA_LAYOUT_BHSD) return VSA_ERR_LAYOUT;
     if (d->dtype != VSA_DTYPE_BF16 && d->dtype != VSA_DTYPE_FP16) return VSA_ERR_DTYPE;
     if (d->B < 1 || d->Hq < 1 || d->Hkv < 1 || d->Hq % d->Hkv != 0) return VSA_ERR_SHAPE;
-    if (d->D != kD) return VSA_ERR_UNSUPPORTED;
+    if (d->D != kD || d->Hkv > kMaxHeads) return VSA_ERR_UNSUPPORTED;
     int lg = 0;
     while ((1 << lg) < d->page && lg < 9) ++lg;
     if (d->page < 16 || d->page > 256 || (1 << lg) != d->page) return VSA_ERR_UNSUPPORTED;
@@ -97,6 +98,7 @@ __device__ __forceinline__ Run find_run(int N, F size_of, int workers, int min_p
     __shared__ int s_n;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     auto size = [&](int n) -> long long { return n < N ? size_of(n) : 0; };
+    if (tid == 0) s_n = 0, s_before = 0;
     // inclusive scan of one value per thread over the CTA; *all gets the sum
     auto scan = [&](long long v, long long *all) {
         long long inc = v;
@@ -176,7 +178,9 @@ inline cudaError_t launch_paged(void (*kernel)(A), dim3 grid, unsigned threads, 
     c.stream = s;
     c.attrs = at;
     c.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&c, kernel, args);
+    const cudaError_t e = cudaLaunchKernelEx(&c, kernel, args);
+    if (e != cudaSuccess) cudaGetLastError();  // returned to the caller, not left for the next launch
+    return e;
 }
 
 // Workspace of vsa_page_select and vsa_paged_attn (each uses its own part).

@@ -187,7 +187,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
             const int pos = key0 + (i0 + lane) * kBlk;
             int j = pos >> p.page_log2;
             w_slot = pos & (p.page - 1);
-            if (a.idx) j = __ldg(a.idx + (long long)bh * a.cap + j);
+            if (a.idx) j = (unsigned)j < (unsigned)a.cap ? __ldg(a.idx + (long long)bh * a.cap + j) : -1;
             w_id = paged_id(p, b, j);
             if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
         }
@@ -448,10 +448,10 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     const Run run = find_run<kWarps>(
         N, [&](int n) -> long long { return (long long)weight(n) * mult; }, kCtas * kWarps, kMinBlocks, kWarps);
     if (run.x0 >= run.x1) return;
-    int n = run.n, nb = weight(n);
+    int n = min(run.n, N - 1), nb = weight(n);
     long long before = run.before;
     // the CTA's run lies in one segment: its warps' results are joined
-    const int sub0 = div_small(run.x0 - before, nb);
+    const int sub0 = clampi(div_small(run.x0 - before, max(nb, 1)), 0, mult - 1);
     const bool joined = run.x1 <= before + (long long)(sub0 + 1) * nb;
     long long x = min(run.x0 + wid * run.per, run.x1);
     const long long x_end = min(x + run.per, run.x1);
@@ -463,7 +463,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
             nb = weight(n);
             continue;
         }
-        const int sub = joined ? sub0 : div_small(x - before, nb);
+        const int sub = joined ? sub0 : clampi(div_small(x - before, max(nb, 1)), 0, mult - 1);
         const long long seg0 = before + (long long)sub * nb;  // the segment's first block
         int off = (int)(x - seg0), take = (int)min((long long)(nb - off), x_end - x);
         const bool first = joined ? run.x0 == seg0 : off == 0;
@@ -565,7 +565,7 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
     auto place = [&](int i) {
         const int w = i < sg.y ? sg.x + i : (i < sg.y + sg.z ? sg.x + sg.y + (i - sg.y) * kWarps
                                                             : sg.x + i + sg.z * (kWarps - 1));
-        return (2LL * w + (i == 0 ? 1 : 0)) * a.rows + r;
+        return (2LL * clampi(w, 0, kCtas * kWarps - 1) + (i == 0 ? 1 : 0)) * a.rows + r;
     };
     float M = -INFINITY;
     for (int i = tid; i < pieces; i += W * 32) {

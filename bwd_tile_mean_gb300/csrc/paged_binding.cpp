@@ -166,6 +166,7 @@ PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (given) {
             if (!q) refuse("q_out without q");
             check_dense(c, "q_out", *given, c.dtype(), {T, c.d.Hq, c.d.D});
+            if (T > 0 && given->data_ptr() == q->data_ptr()) refuse("q_out: must not be q");
             q_out = *given;
         } else if (q) {
             q_out = output(c, {T, c.d.Hq, c.d.D}, c.dtype());

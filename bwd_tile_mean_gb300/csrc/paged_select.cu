@@ -229,10 +229,11 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
 #pragma unroll 8
         for (int c = tid; c < comp; c += N) f(rank_of(keys[c], c));
     };
-    // cut: the `take`-th largest rank (ranks are distinct); 2^59 when none is taken
+    // cut: the `take`-th largest rank (ranks are distinct); 2^59 when none is taken. Every pass fixes more bits, so
+    // the loop ends whatever the keys are.
     uint64_t cut = 1ull << (32 + kIndexBits), prefix = 0;
-    int rem = take, top = 32 + kIndexBits;  // bits [top, 59) of the cut are `prefix`
-    while (rem > 0) {
+    int rem = take;
+    for (int top = 32 + kIndexBits; rem > 0 && top > 0;) {  // bits [top, 59) of the cut are `prefix`
         const int shift = max(top - 11, 0), bits = top - shift;
         __syncthreads();  // the bins are clear (and the keys there)
         each([&](uint64_t k) {
@@ -281,7 +282,9 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
         }
         if (in <= kRank) {
             each([&](uint64_t k) {
-                if (k >> top == prefix) list[atomicAdd(&s_fill, 1)] = k;
+                if (k >> top != prefix) return;
+                const int at = atomicAdd(&s_fill, 1);
+                if (at < kRank) list[at] = k;
             });
             __syncthreads();
             if (tid < in) {
@@ -312,7 +315,8 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
     for (int c = lo + lane; c - lane < hi; c += 32) {
         const bool on = c < hi && chosen(c);
         const unsigned m = __ballot_sync(0xffffffffu, on);
-        if (on) idx[at + __popc(m & ((1u << lane) - 1u))] = a.first + c;
+        const int to = at + __popc(m & ((1u << lane) - 1u));
+        if (on && to < a.topk - a.last) idx[to] = a.first + c;
         at += __popc(m);
     }
     for (int e = tid; e < a.first; e += N) idx[e] = e;

@@ -650,7 +650,7 @@ class PagedCache:
                 self._is(name, t, shp, dt)
                 if not t.is_contiguous():
                     raise ValueError(f"{name}: must be contiguous")
-        self.k, self.v, self.k_mean, self.page_table, self.seq_lens = k, v, k_mean, page_table, seq_lens
+        self._tensors = (k, v, k_mean, page_table, seq_lens)
         self.desc = PagedDesc(LAYOUTS[layout], DTYPES[dtype], B, Hq, Hkv, D, page, num_pages, max_pages, stride,
                               page_table.data_ptr(), seq_lens.data_ptr(), float(scale))
         need = int(lib().vsa_paged_workspace_size(C.byref(self.desc)))
@@ -660,8 +660,8 @@ class PagedCache:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         elif workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace: at least {need} bytes on {self.device} are needed")
-        self.workspace = workspace
-        # every call passes these on: the tensors above are not to be replaced, only written
+        self._workspace = workspace
+        # every call passes these addresses on: the tensors behind them are read-only attributes
         at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
         entry = lambda f: C.cast(f, C.c_void_p).value  # noqa: E731
         L = lib()
@@ -669,6 +669,13 @@ class PagedCache:
             C.addressof(self.desc), self.device.index if self.device.type == "cuda" else -1, at(k), at(v), at(k_mean),
             at(workspace), workspace.numel() * workspace.element_size(), entry(L.vsa_paged_append),
             entry(L.vsa_page_select), entry(L.vsa_paged_attn), _check)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_mean = property(lambda self: self._tensors[2])
+    page_table = property(lambda self: self._tensors[3])
+    seq_lens = property(lambda self: self._tensors[4])
+    workspace = property(lambda self: self._workspace)
 
     def _is(self, name, t, shape, dtype):
         if t.dtype != dtype or t.device != self.device or t.shape != shape:

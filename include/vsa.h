@@ -470,8 +470,9 @@ vsa_status vsa_check_inputs(const vsa_desc *desc, const int32_t *q_var, const in
  *             max_pages * page; 0 marks an unused row of a padded batch.
  *   means     k_mean [num_pages, Hkv, D] fp32: the mean of the page's stored
  *             keys, defined for full pages.
- * Device-resident values out of range never move an access outside a
- * buffer: lengths are clamped, a token whose page id is outside
+ * Tables, lengths and lists are read when the kernels run and must not
+ * change while a call that reads them is under way. Device-resident values
+ * out of range never move an access outside a buffer: lengths are clamped, a token whose page id is outside
  * [0, num_pages) is not stored, and a listed page that does not exist
  * (its index outside [0, max_pages) or its id outside the pool) holds no
  * key. Every length, id and offset is 64-bit where it is multiplied. */
@@ -479,7 +480,7 @@ typedef struct {
     int32_t layout;       /* VSA_LAYOUT_BSHD or VSA_LAYOUT_BHSD: the order inside a page */
     int32_t dtype;        /* vsa_dtype of q, k, v, the cache and out */
     int32_t B;            /* sequences */
-    int32_t Hq, Hkv;      /* query heads, key/value heads; Hq % Hkv == 0 */
+    int32_t Hq, Hkv;      /* query heads, key/value heads (at most 65536); Hq % Hkv == 0 */
     int32_t D;            /* head dim; must be 128 */
     int32_t page;         /* tokens per page: 16, 32, 64, 128 or 256 */
     int32_t num_pages;    /* pages in the pool */
@@ -558,8 +559,8 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
                            void *workspace, size_t workspace_bytes, vsa_stream_t stream);
 
 /* Attention of one token per sequence over the cache: q [B, Hq, D]
- * (q_stride as above), out [B, Hq, D] dense, lse fp32 [B, Hq] (natural
- * log). With page_idx == NULL every token of the sequence is attended;
+ * (q_stride as above), out [B, Hq, D] dense (not q's memory), lse fp32
+ * [B, Hq] (natural log). With page_idx == NULL every token of the sequence is attended;
  * otherwise the tokens of the pages page_idx [B, Hkv, idx_cap] lists for
  * the query head's key/value head, page_cnt [B, Hkv] of them (a page listed
  * twice counts twice). A row without keys gets O = 0, LSE = -inf. The work

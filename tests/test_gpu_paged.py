@@ -117,6 +117,21 @@ def test_append_in_pieces_gives_the_same_bits(page):
         assert same(a, b)
 
 
+def test_append_to_many_sequences():
+    """More sequences than two steps of the search hold, some without tokens."""
+    new = [b % 3 if b % 11 else 0 for b in range(1100)]
+    lens = [n + (b % 29 if n else 0) for b, n in enumerate(new)]
+    pool = Pool("bshd", BF, 2, 1, 16, sum(-(-n // 16) for n in lens), 2, lens, seed=17)
+    cu = [0] + list(itertools.accumulate(new))
+    qkv, q, k, v = new_tokens(pool, cu[-1])
+    cos, sin = angles(32, 128)
+    cache = pool.cache()
+    got = cache.append(k.cuda(), v.cuda(), q.cuda(), cu_seqlens=torch.tensor(cu, dtype=torch.int32).cuda(),
+                       cos=cos.cuda(), sin=sin.cuda())
+    want = ref.append(pool, k, v, q, cu, cos, sin)
+    assert same(cache.k, pool.k) and same(cache.v, pool.v) and same(cache.k_mean, pool.mean) and same(got, want)
+
+
 def test_append_ignores_what_has_no_place():
     # lengths past the table, more new tokens than the length, page ids outside the pool, no tokens
     pool = Pool("bshd", HF, 4, 2, 16, 8, 3, [48, 20, 7, 5], seed=3)
@@ -216,6 +231,13 @@ def test_select_ties_and_special_scores():
         check_select(pool, q, k, 0, 1)
 
 
+def test_select_batch_of_many_sequences():
+    """More sequences than one scan of a CTA holds, most without a choice."""
+    lens = [16 * 40 + 3 if b % 37 == 5 else b % 90 for b in range(300)]
+    pool, q = select_pool(("bhsd", HF, 2, 2, 16, lens, 0, 0, 0))
+    check_select(pool, q, 7, 1, 2)
+
+
 def test_select_strided_queries():
     pool, q = select_pool(SELECT[2])
     wide = torch.randn((pool.B, pool.Hq + 7, D), device="cuda").to(BF)
@@ -262,15 +284,50 @@ def spoil(pool):
         x[~held] = value
 
 
+def widened(pool, entries):
+    """The pool's cache with a page table that much wider: the call takes
+    another variant for tables that allow long sequences."""
+    table = torch.nn.functional.pad(torch.tensor(pool.table, dtype=torch.int32), (0, entries), value=-9)
+    return vsa.PagedCache(pool.layout, pool.dtype, pool.B, pool.Hq, pool.Hkv, D, pool.page, pool.num_pages,
+                          pool.max_pages + entries, k=pool.view(pool.k).cuda(), v=pool.view(pool.v).cuda(),
+                          k_mean=pool.mean.cuda(), page_table=table.cuda(),
+                          seq_lens=torch.tensor(pool.lens, dtype=torch.int32).cuda())
+
+
 @pytest.mark.parametrize("case", ATTEND, ids=lambda c: f"{c[0]}-{c[2]}x{c[3]}-p{c[4]}-b{len(c[5])}")
 def test_attend(case):
     pool, q = attend_pool(case)
     spoil(pool)
-    cache = pool.cache()
-    got = cache.attend(q.cuda())
-    ref.check_attend(got, ref.attend(pool, q), "all pages")
-    again = cache.attend(q.cuda())
-    assert same(got[0], again[0]) and same(got[1], again[1])
+    want = ref.attend(pool, q)
+    for cache in (pool.cache(), widened(pool, 70000 // pool.page)):
+        got = cache.attend(q.cuda())
+        ref.check_attend(got, want, "all pages")
+        again = cache.attend(q.cuda())
+        assert same(got[0], again[0]) and same(got[1], again[1])
+
+
+RAGGED = [9000, 1, 0, 300, 5003, 17, 0, 0, 64, 2048, 1, 777, 4096, 33, 15, 6001]
+
+
+@pytest.mark.parametrize("Hq,Hkv,page", [(16, 1, 16), (3, 3, 64), (20, 1, 32), (8, 2, 128)])
+def test_attend_ragged_batch_in_equal_runs(Hq, Hkv, page):
+    """Segments that end inside a warp's run, a CTA's run, and span many."""
+    pool, q = attend_pool(("bhsd", BF, Hq, Hkv, page, RAGGED), seed=33)
+    spoil(pool)
+    got = widened(pool, 70000 // page).attend(q.cuda())
+    ref.check_attend(got, ref.attend(pool, q), "ragged")
+
+
+def test_attend_long_list_in_equal_runs():
+    pool, q = attend_pool(("bhsd", HF, 16, 1, 16, [20011, 300]), seed=34)
+    g = torch.Generator().manual_seed(8)
+    idx = torch.full((2, 1, 2200), -1, dtype=torch.int32)
+    cnt = torch.tensor([[1251], [7]], dtype=torch.int32)
+    for b in range(2):
+        n = int(cnt[b, 0])
+        idx[b, 0, :n] = torch.randperm(-(-pool.lens[b] // 16), generator=g)[:n].int()
+    got = widened(pool, 3000).attend(q.cuda(), (idx.cuda(), cnt.cuda()))
+    ref.check_attend(got, ref.attend(pool, q, (idx, cnt)), "long list")
 
 
 @pytest.mark.parametrize("case", ATTEND, ids=lambda c: f"{c[0]}-{c[2]}x{c[3]}-p{c[4]}-b{len(c[5])}")
@@ -455,6 +512,52 @@ def test_layers_share_table_lengths_and_workspace_on_another_stream():
     for x, p in zip(got, (pool, other, pool)):
         ref.check_attend(x, ref.attend(p, q))
     ref.check_attend(listed, ref.attend(pool, q, [x.cpu() for x in picked]))
+
+
+def test_graphs_that_share_a_workspace_and_streams_that_do_not():
+    """Captured calls of two caches with one workspace, replayed in turns;
+    then the two caches on two streams at once, each with its own."""
+    case = ("bshd", BF, 8, 2, 32, RAGGED)
+    pools = [attend_pool(case, seed=80 + i) for i in range(2)]
+    first = widened(pools[0][0], 3000)
+    shared = [first, widened(pools[1][0], 3000)]
+    shared[1] = vsa.PagedCache("bshd", BF, len(RAGGED), 8, 2, D, 32, shared[1].num_pages, shared[1].max_pages,
+                               k=shared[1].k, v=shared[1].v, k_mean=shared[1].k_mean, page_table=shared[1].page_table,
+                               seq_lens=shared[1].seq_lens, workspace=first.workspace)
+    qs = [q.cuda() for _, q in pools]
+    want = [ref.attend(p, q) for p, q in pools]
+
+    def run(c, q):
+        pages = c.select(q, 20, keep_first=1)
+        return (*pages, *c.attend(q, pages), *c.attend(q))
+
+    eager = [run(c, q) for c, q in zip(shared, qs)]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c, q in zip(shared, qs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(run(c, q))
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        graphs[i].replay()
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(same(a, b) for a, b in zip(eager[i], outs[i]))
+        ref.check_attend(outs[i][4:], want[i], f"graph {i}")
+    apart = [widened(p, 3000) for p, _ in pools]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        got.append([])
+        for c, q, s in zip(apart, qs, streams):
+            with torch.cuda.stream(s):
+                got[-1].append(run(c, q))
+    torch.cuda.synchronize()
+    for round_ in got:
+        for i in range(2):
+            assert all(same(a, b) for a, b in zip(eager[i], round_[i]))
 
 
 def test_pages_of_a_shared_prefix():
