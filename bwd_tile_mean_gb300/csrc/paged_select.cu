@@ -225,9 +225,17 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int take = a.topk - a.first - a.last;
     int *idx = a.idx + row * a.topk;
+    // f(rank) of this thread's share of the pages, kDeep loads at a time
+    constexpr int kDeep = 8;
     auto each = [&](auto f) {
-#pragma unroll 8
-        for (int c = tid; c < comp; c += N) f(rank_of(keys[c], c));
+        for (int c0 = tid; c0 < comp; c0 += N * kDeep) {
+            uint32_t key[kDeep];
+#pragma unroll
+            for (int e = 0; e < kDeep; ++e) key[e] = c0 + e * N < comp ? keys[c0 + e * N] : 0u;
+#pragma unroll
+            for (int e = 0; e < kDeep; ++e)
+                if (c0 + e * N < comp) f(rank_of(key[e], c0 + e * N));
+        }
     };
     // cut: the `take`-th largest rank (ranks are distinct); 2^59 when none is taken. Every pass fixes more bits, so
     // the loop ends whatever the keys are.
@@ -303,22 +311,33 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
     // pages at or above the cut, in order: each warp has a contiguous share
     const int share = ((comp + W - 1) / W + 31) & ~31;
     const int lo = min(wid * share, comp), hi = min(lo + share, comp);
-    auto chosen = [&](int c) { return rank_of(keys[c], c) >= cut; };
+    // chosen(c, ballot) of 32 pages at a time, in order, four loads at a time
+    auto each32 = [&](auto f) {
+        for (int c0 = lo; c0 < hi; c0 += 128) {
+            uint32_t key[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[e] = c0 + 32 * e + lane < hi ? keys[c0 + 32 * e + lane] : 0u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int c = c0 + 32 * e + lane;
+                const bool on = c < hi && rank_of(key[e], c) >= cut;
+                f(c, on, __ballot_sync(0xffffffffu, on));
+            }
+        }
+    };
     int n = 0;
-    for (int c = lo + lane; c - lane < hi; c += 32) n += __popc(__ballot_sync(0xffffffffu, c < hi && chosen(c)));
+    each32([&](int, bool, unsigned m) { n += __popc(m); });
     __syncthreads();  // wsum was read
     if (lane == 0) wsum[wid] = n;
     __syncthreads();
     int at = a.first;
 #pragma unroll
     for (int w = 0; w < W; ++w) at += w < wid ? wsum[w] : 0;
-    for (int c = lo + lane; c - lane < hi; c += 32) {
-        const bool on = c < hi && chosen(c);
-        const unsigned m = __ballot_sync(0xffffffffu, on);
+    each32([&](int c, bool on, unsigned m) {
         const int to = at + __popc(m & ((1u << lane) - 1u));
         if (on && to < a.topk - a.last) idx[to] = a.first + c;
         at += __popc(m);
-    }
+    });
     for (int e = tid; e < a.first; e += N) idx[e] = e;
     for (int e = tid; e < a.last; e += N) idx[a.topk - a.last + e] = pages - a.last + e;
     if (tid == 0) a.cnt[row] = a.topk;
