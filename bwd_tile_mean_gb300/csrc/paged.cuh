@@ -81,6 +81,11 @@ inline bool token_stride(int64_t given, int heads, long long *out) {
     return given == 0 || (given >= dense && given % 8 == 0);
 }
 
+// x / d for 0 <= x: in 32 bits where they hold it.
+__device__ __forceinline__ int div_small(long long x, int d) {
+    return x <= 0x7fffffffLL ? (int)((unsigned)x / (unsigned)d) : (int)(x / d);
+}
+
 // Equal contiguous runs of the work of a list of entries, whatever their
 // sizes: entry n has size_of(n) units (n < N), the units of all entries end
 // to end are dealt to `workers` workers (at least min_per units each), and a

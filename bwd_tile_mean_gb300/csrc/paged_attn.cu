@@ -125,10 +125,6 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
 }
 
 __device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) { return (seg_keys(a, n) + kBlk - 1) / kBlk; }
-// x / d for 0 <= x: in 32 bits where they hold it.
-__device__ __forceinline__ int div_small(long long x, int d) {
-    return x <= 0x7fffffffLL ? (int)((unsigned)x / (unsigned)d) : (int)(x / d);
-}
 
 // Where a segment's queries, keys and outputs are.
 struct Segment {

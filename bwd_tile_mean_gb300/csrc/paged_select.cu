@@ -77,17 +77,20 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, uint32_t v) {
 // their rounding errors kept aside (each found exactly), added at the end.
 template <typename T> __device__ __forceinline__ void group_sum(const T *q, int G, float *out) {
     float s[8], err[8];
-    for (int m = 0; m < G; ++m) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(q + (long long)m * kD));
-        const uint32_t r[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = unpack2<T>(r[e / 2]);
-            const float x = e & 1 ? f.y : f.x;
-            if (m == 0) {
-                s[e] = x;
-                err[e] = 0.f;
-            } else {
+    for (int e = 0; e < 8; ++e) s[e] = err[e] = 0.f;
+    for (int m0 = 0; m0 < G; m0 += 4) {  // four rows' loads at a time
+        uint4 w[4];
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+            w[m] = m0 + m < G ? __ldg(reinterpret_cast<const uint4 *>(q + (long long)(m0 + m) * kD)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            const uint32_t r[4] = {w[m].x, w[m].y, w[m].z, w[m].w};
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float2 f = unpack2<T>(r[e / 2]);
+                const float x = e & 1 ? f.y : f.x;
                 const float t = __fadd_rn(s[e], x), y = __fsub_rn(t, s[e]);
                 err[e] = __fadd_rn(err[e], __fadd_rn(__fsub_rn(s[e], __fsub_rn(t, y)), __fsub_rn(x, y)));
                 s[e] = t;
@@ -136,6 +139,22 @@ __device__ __forceinline__ void copy_means(uint32_t dst, const SelectArgs &a, in
                      : "memory");
 }
 
+// A warp's items: four pages of one of hn heads each, every kWarpsSel-th item
+// from its own number on, without a division per item.
+struct Walk {
+    int head, quad, dh, dq, hn;
+    __device__ __forceinline__ Walk(int first, int heads)
+        : head(first % heads), quad(first / heads), dh(kWarpsSel % heads), dq(kWarpsSel / heads), hn(heads) {}
+    __device__ __forceinline__ void next() {
+        head += dh;
+        quad += dq;
+        if (head >= hn) {
+            head -= hn;
+            ++quad;
+        }
+    }
+};
+
 template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(SelectArgs a) {
     extern __shared__ __align__(16) unsigned char sm[];
     float *sq = reinterpret_cast<float *>(sm + kWarpsSel * kRingBytes);  // [kHeads][128] summed queries
@@ -157,7 +176,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
             ++b;
             continue;
         }
-        const int grp = (int)((x - before) / units), off = (int)((x - before) % units);
+        const int grp = div_small(x - before, units), off = (int)(x - before - (long long)grp * units);
         const int take = (int)min((long long)(units - off), run.x1 - x);
         const int q0 = max(off - kLeadSel, 0), nq = max(off + take - kLeadSel, 0) - q0;  // its own units
         const int h0 = grp * kHeads, hn = min(kHeads, p.Hkv - h0);
@@ -167,17 +186,20 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
         // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
         const int sub = lane >> 3, j = lane & 7, items = nq * hn;
         const uint32_t ring = ptx::smem_addr(sm) + wid * kRingBytes + lane * 16;
-        auto id_of = [&](int it) {
-            const int c = (q0 + it / hn) * 4 + sub;
-            return it < items && c < comp ? paged_id(p, b, a.first + c) : -1;
+        int id[kRing], at[kRing], head[kRing];  // of the items in flight, by stage: page id, competing page, head
+        Walk w(wid, hn);
+        auto plan = [&](int stage) {  // the next item
+            at[stage] = (q0 + w.quad) * 4 + sub;
+            head[stage] = w.head;
+            id[stage] = w.quad < nq && at[stage] < comp ? paged_id(p, b, a.first + at[stage]) : -1;
+            w.next();
         };
-        int id[kRing];  // page ids of the items in flight, by stage
-        auto copy = [&](int it, int stage, int page) { copy_means(ring + stage * 2048, a, page, h0 + it % hn, j); };
+        auto copy = [&](int stage) { copy_means(ring + stage * 2048, a, id[stage], h0 + head[stage], j); };
 #pragma unroll
-        for (int s = 0; s < kRing; ++s) id[s] = id_of(wid + s * kWarpsSel);
+        for (int s = 0; s < kRing; ++s) plan(s);
 #pragma unroll
         for (int s = 0; s < kRing - 1; ++s) {
-            if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s, id[s]);
+            if (wid + s * kWarpsSel < items) copy(s);
             asm volatile("cp.async.commit_group;" ::: "memory");
         }
         __syncthreads();  // the sums of the piece before were read
@@ -190,12 +212,12 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
             for (int s = 0; s < kRing; ++s) {
                 const int it = wid + (n0 + s) * kWarpsSel;
                 if (it >= items) break;
-                const int ahead = it + (kRing - 1) * kWarpsSel, sa = (s + kRing - 1) % kRing;
-                if (ahead < items) copy(ahead, sa, id[sa]);  // into the stage this lane read last
+                const int sa = (s + kRing - 1) % kRing;
+                if (it + (kRing - 1) * kWarpsSel < items) copy(sa);  // into the stage this lane read last
                 asm volatile("cp.async.commit_group;" ::: "memory");
                 asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
-                const int hh = it % hn, c = (q0 + it / hn) * 4 + sub, page = id[s];
-                id[s] = id_of(it + kRing * kWarpsSel);
+                const int hh = head[s], c = at[s], page = id[s];
+                plan(s);
                 const float r = page_score(sq + hh * kD, sm + wid * kRingBytes + s * 2048 + lane * 16, j);
                 if (j == 0 && c < comp) keys[(long long)hh * p.max_pages + c] = order_key(page >= 0 ? r : -INFINITY);
             }
@@ -388,21 +410,23 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     // An item is four pages of one head; lane j of eight holds dims 32 i + 4 j + c of a page.
     const int sub = lane >> 3, j = lane & 7, items = (nc + 3) / 4 * hn;
     const uint32_t ring = ptx::smem_addr(sm) + wid * kClusterRing + lane * 16;
-    auto copy = [&](int it, int stage) {
-        const int c = it / hn * 4 + sub;
-        copy_means(ring + stage * 2048, a, c < nc ? ids[c] : -1, h0 + it % hn, j);
+    Walk w(wid, hn), ahead(wid, hn);  // the item being scored, and the next to copy
+    auto copy = [&](int stage) {
+        const int c = ahead.quad * 4 + sub;
+        copy_means(ring + stage * 2048, a, c < nc ? ids[c] : -1, h0 + ahead.head, j);
+        ahead.next();
     };
 #pragma unroll
     for (int s = 0; s < kClusterStages - 1; ++s) {
-        if (wid + s * kWarpsSel < items) copy(wid + s * kWarpsSel, s);
+        if (wid + s * kWarpsSel < items) copy(s);
         asm volatile("cp.async.commit_group;" ::: "memory");
     }
-    for (int n = 0; wid + n * kWarpsSel < items; ++n) {
-        const int it = wid + n * kWarpsSel, hh = it % hn, c = it / hn * 4 + sub;
-        const int ahead = it + (kClusterStages - 1) * kWarpsSel;
-        if (ahead < items) copy(ahead, (n + kClusterStages - 1) % kClusterStages);  // the stage this lane read last
+    for (int n = 0; wid + n * kWarpsSel < items; ++n, w.next()) {
+        if (wid + (n + kClusterStages - 1) * kWarpsSel < items)
+            copy((n + kClusterStages - 1) % kClusterStages);  // the stage this lane read last
         asm volatile("cp.async.commit_group;" ::: "memory");
         asm volatile("cp.async.wait_group %0;" ::"n"(kClusterStages - 1) : "memory");
+        const int hh = w.head, c = w.quad * 4 + sub;
         const float r = page_score(sq + hh * kD, sm + wid * kClusterRing + (n % kClusterStages) * 2048 + lane * 16, j);
         if (j == 0 && c < nc)
             st_cluster(ptx::cluster_addr(ptx::smem_addr(mine + c0 + c), hh), order_key(ids[c] >= 0 ? r : -INFINITY));
