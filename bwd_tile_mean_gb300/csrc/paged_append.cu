@@ -310,8 +310,10 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
 
 template <typename T, int HC, int PB> cudaError_t launch_append(AppendArgs &a, cudaStream_t s) {
     const int groups = a.p.page / kGroup;
-    // A prompt fills most groups of its units; one token leaves all but one warp idle, and few are enough.
-    a.team = a.cu ? groups : std::min(groups, 4);
+    // Warps per unit: as many as a sequence's tokens fill groups on average (idle warps hold registers), and up to
+    // four for the earlier keys of a page that fills up.
+    a.team = std::min(groups, 4);
+    while (a.team < groups && (long long)a.T > (long long)a.team * kGroup * a.p.B) a.team *= 2;
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
     a.kv_chunks = (a.p.Hkv + HC - 1) / HC;
     a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
@@ -368,9 +370,10 @@ extern "C" vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("paged_append", s);
     const bool bf = a.p.dtype == T_BF16;
-    // Many tokens: four heads per warp, so that a token's angles serve 8 rows. Few: two heads per warp and
-    // two pairs of slots at once, for a short chain of loads.
-    const bool wide = (long long)T * a.p.Hkv >= kWideRows;
+    // Four key heads per warp let a token's angles serve 8 rows, two heads and two pairs of slots at once give more
+    // and shorter warps. Measured (us, four heads / two): 30,000 tokens of 24 key heads 191 / 201, 4,000 of them 27.9
+    // / 29.8, 2,000 21.7 / 15.4; 8,000 tokens of 8 key heads with 4 queries each 44.7 / 40.7, 16,000 67 / 64.
+    const bool wide = (long long)T * a.p.Hkv >= kWideRows && a.p.G <= 2;
     const cudaError_t e = wide ? (bf ? launch_append<__nv_bfloat16, 4, 1>(a, s) : launch_append<__half, 4, 1>(a, s))
                                : (bf ? launch_append<__nv_bfloat16, 2, 2>(a, s) : launch_append<__half, 2, 2>(a, s));
     prof_end(s);
