@@ -49,6 +49,8 @@ APPEND = [  # layout, dtype, Hq, Hkv, page, rot, interleaved, lengths, new token
     ("bhsd", BF, 24, 24, 64, 0, False, [70, 130], [33, 130]),
     ("bshd", HF, 40, 2, 16, 128, True, [17] * 40, [1] * 40),
     ("bhsd", BF, 10, 5, 32, 32, False, [96, 97, 33], [32, 96, 2]),
+    ("bshd", BF, 48, 24, 64, 96, True, [1500, 900, 450], [1450, 900, 400]),   # many rows: four key heads per warp
+    ("bhsd", HF, 23, 23, 256, 128, False, [2100, 800], [2100, 777]),
 ]
 
 
