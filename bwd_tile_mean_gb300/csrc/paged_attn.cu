@@ -384,7 +384,6 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     const int tid = threadIdx.x, wid = tid >> 5, CS = a.cluster;
     const int rank = (int)(blockIdx.x % CS), segment = (int)(blockIdx.x / CS);
     grid_wait();
-    grid_go();
     if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int bh = segment / a.rc;
     const Segment sg = segment_of(a, bh, segment % a.rc);
@@ -395,6 +394,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     const int blk0 = min((rank * kWarps + wid) * per, nb), nblk = min(per, nb - blk0);
     float m_run[2], l_run[2], acc[16][4];
     stream_blocks<T>(a, sg, qa, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
+    grid_go();
     T *out = static_cast<T *>(a.out);
     if (CS == 1) {
         join_warps(smem, sg.rows, m_run, l_run, acc, [&](int row, float o, float M, float l) {
@@ -434,7 +434,6 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     grid_wait();
-    grid_go();
     const int N = a.idx ? p.B * p.Hkv : p.B;       // list entries
     const int mult = a.idx ? a.rc : p.Hkv * a.rc;  // segments per entry
     auto weight = [&](int n) {
@@ -477,6 +476,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         load_q<T>(a, sg, qa);
         float m_run[2], l_run[2], acc[16][4];
         stream_blocks<T>(a, sg, qa, len, off, take, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
+        if (x >= x_end) grid_go();
 
         // A piece of the segment that begins it describes all of its pieces.
         const long long slot = 2LL * ((int)blockIdx.x * kWarps + (joined ? 0 : wid)) + (first ? 1 : 0);
