@@ -162,7 +162,6 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const int hgroups = (p.Hkv + kHeads - 1) / kHeads;
     grid_wait();
-    grid_go();
     // a unit: four pages, the heads of one group; a group's lead goes before its own units
     auto units_of = [&](int n) { const int q = (competing(a, n) + 3) / 4; return q > 0 ? q + kLeadSel : 0; };
     const Run run = find_run<kWarpsSel>(
@@ -223,6 +222,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
             }
         }
     }
+    grid_go();
 }
 
 // Rows with nothing to choose: every page.
@@ -392,7 +392,6 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     const int b = cl / a.hgroups, h0 = (cl % a.hgroups) * a.hg, hn = min(a.hg, p.Hkv - h0);
     clear_bins<kThreads>(hist);
     grid_wait();
-    grid_go();
     const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2;
     const int comp = competing(a, b);
     if (comp == 0) {  // the same for every CTA of the cluster
@@ -432,6 +431,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
             st_cluster(ptx::cluster_addr(ptx::smem_addr(mine + c0 + c), hh), order_key(ids[c] >= 0 ? r : -INFINITY));
     }
     ptx::cluster_sync();  // every run's keys are there
+    grid_go();
     if (rank >= hn) return;
 
     list_pages<kThreads>(a, (long long)b * p.Hkv + h0 + rank, pages, comp, hist, mine);
