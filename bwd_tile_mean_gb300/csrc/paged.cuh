@@ -163,8 +163,12 @@ __device__ __forceinline__ Run find_run(int N, F size_of, int workers, int min_p
 
 // Kernels of the paged calls are launched so that the next one on the stream
 // may start while this one drains: every CTA waits for the work before it
-// with grid_wait() before it touches memory, and lets the launch after it
-// go ahead with grid_go().
+// with grid_wait() before it touches memory, and lets the launch after it go
+// ahead with grid_go() when its streaming is over. Measured (us, such launches
+// / plain ones): one-token append 2.7 / 2.9, attention of 101 keys 3.7 / 4.1,
+// select and attend 24.0 / 25.1. Letting the next launch in at the kernel's
+// start instead takes slots from its own CTAs: 4 sequences of 8,000 pages
+// 39 us for a selection against 32.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename A>
