@@ -39,14 +39,15 @@ namespace {
 
 constexpr int kBlk = 16;        // keys per warp step
 constexpr int kRows = 16;       // query heads per segment at most
-constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time)
-constexpr int kMinBlocks = 4;   // fewest blocks a warp's run has when there is little work
-constexpr int kAlignedKeys = 2048;  // keys per CTA up to which a segment is one CTA's or one cluster's
-constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does not grow
+constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time): 0, 1, 2, 3, 4
+                                // measured 102, 92, 87, 85.1, 84.8 us on 64 sequences of 37 to 16,000 keys
+constexpr int kAlignedKeys = 1280;  // keys per CTA up to which segments of unknown lengths get a cluster each
+constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does not grow: 64, 128, 256 measured 4.6, 3.9,
+                                    // 3.8 us at 101 keys x 3 heads and 4.1, 4.6, 5.5 at 300 x 8
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
-constexpr int kMaxCluster = 16;
+constexpr int kMaxCluster = 16;     // 16,000 keys x 8 heads: 15.6 us, 22 with clusters of 8
 constexpr int kWarps = 4;
-constexpr int kStages = 3;      // ring stages per warp; six (one CTA per SM) measured no faster anywhere
+constexpr int kStages = 3;      // ring stages per warp, for two CTAs per SM; six and one CTA measured slower
 constexpr int kCtas = 304;      // two per SM on 152 SMs
 constexpr int kStageBytes = 2 * kBlk * 256;
 constexpr int kPitch = 136;     // floats per row of the warps' outputs in shared memory
@@ -376,7 +377,12 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 
 // A cluster per segment (a.cluster CTAs of four warps, equal runs of its
 // blocks). Row r is finished by CTA r % cluster, which has a place for every
-// CTA's part of it.
+// CTA's part of it. 122,880 keys x 24 heads (1.51 GB): 213 to 226 us, 6.7 to
+// 7.1 TB/s, the measured copy rate; 6,144 listed keys x 24 heads 16 us with 11
+// of them the bytes; 101 keys x 3 heads 3.7 us, of which 2 are the launch and
+// the rest length -> page id -> keys -> join, one after another. A warp alone
+// on its scheduler takes about 1,000 cycles per block (230 instructions, most
+// waiting on the one before), so few segments want many CTAs.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
@@ -428,7 +434,10 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
 }
 
 // Equal runs of all segments' blocks. A segment counts kLead blocks more than
-// it has, in front of its own.
+// it has, in front of its own. 64 sequences of 37 to 16,000 keys x 8 heads
+// (504 MB): 84 us with the join, 88% of the measured copy rate; of the rest
+// 3.5 us are the start of a CTA (scan, length, page id, first keys) and 4 the
+// join.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;
@@ -441,7 +450,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         return nb > 0 ? nb + kLead : 0;
     };
     const Run run = find_run<kWarps>(
-        N, [&](int n) -> long long { return (long long)weight(n) * mult; }, kCtas * kWarps, kMinBlocks, kWarps);
+        N, [&](int n) -> long long { return (long long)weight(n) * mult; }, kCtas * kWarps, 1, kWarps);
     if (run.x0 >= run.x1) return;
     int n = min(run.n, N - 1), nb = weight(n);
     long long before = run.before;
@@ -531,8 +540,10 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
 // of the segments that crossed runs: W warps per row, R rows per CTA. The
 // pieces' weights come first, all at once; then the warps take turns on the
 // pieces, each with kJoinDeep loads in flight, and their sums are added in
-// order. Many rows have few pieces each, few rows many: kJoinFew rows and
-// fewer get 16 warps each, kJoinMany and more one.
+// order (one head of 122,880 keys, 304 pieces: 20 us with its streaming; a
+// running maximum over one piece after another took 48). Many rows have few
+// pieces each, few rows many: kJoinFew rows and fewer get 16 warps each,
+// kJoinMany and more one (8,192 rows: 43 -> 37 us with their streaming).
 constexpr int kJoinDeep = 8, kJoinFew = 152, kJoinMany = 1024;
 template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32) k_paged_join(AttnArgs a) {
     static_assert(W == 1 || R == 1, "a row's warps meet at the CTA's barrier");
@@ -716,7 +727,9 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
     // One cluster per segment: twice the CTAs while that leaves an SM without one and every CTA with kClusterKeys
     // keys. Segments of one length (one sequence, or page lists) are then balanced by themselves; of unknown lengths
-    // only while the longest stays short.
+    // only while the longest stays short. Measured (us, clusters / runs): 300 keys x 8 heads 4.6 / 8.8, 4,000 x 8
+    // 6.9 / 9.6, 64,000 x 8 46.1 / 46.2, 64,000 x 1 34 / 13.6; 16 sequences of 1,000 to 9,000 keys x 2 heads 19.6 /
+    // 21.1, 64 of 37 to 16,000 x 8 151 / 84; lists of 4,096 keys x 256 rows, with their choice, 107 / 114.
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
     int cluster = 1;
     while (cluster < kMaxCluster && segments * cluster < 152 && most > (long long)kClusterKeys * cluster) cluster *= 2;
