@@ -21,10 +21,9 @@
 //
 // Measured (us, cluster / runs): 960 pages x 24 heads of one sequence 7.7 /
 // 11.3, 32 sequences of 312 to 2,047 pages x 8 heads 44 / 30.5. The latter
-// reads 105 MB, 15.5 us at the measured copy rate: the means stream in 13 us
-// (8 TB/s), before them 4 us go by from the launch (scan of the lengths, page
-// ids, first means) and after them 6 to 7 (keys out, the second launch, the
-// top-k). One sequence is a chain of loads and barriers: 1.2 us length and
+// reads 105 MB, 15.5 us at the measured copy rate: the means stream in about
+// 16 us, before them 4 us go by from the launch (scan of the lengths, page
+// ids) and after them 7 to 8 (keys out, the second launch, the top-k). One sequence is a chain of loads and barriers: 1.2 us length and
 // page ids, 2.4 the means, 3 the top-k.
 #include <algorithm>
 
