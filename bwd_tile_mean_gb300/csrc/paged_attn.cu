@@ -37,7 +37,7 @@
 namespace vsa {
 namespace {
 
-constexpr int kBlk = 16;        // keys per warp step
+constexpr int kBlk = 16;        // keys per block; a warp takes two per step
 constexpr int kRows = 16;       // query heads per segment at most
 constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time): 0, 1, 2, 3, 4
                                 // measured 102, 92, 87, 85.1, 84.8 us on 64 sequences of 37 to 16,000 keys
@@ -47,9 +47,9 @@ constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does n
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
 constexpr int kMaxCluster = 16;     // 16,000 keys x 8 heads: 15.6 us, 22 with clusters of 8
 constexpr int kWarps = 4;
-constexpr int kStages = 3;      // ring stages per warp, for two CTAs per SM; six and one CTA measured slower
+constexpr int kStages = 3;      // ring slots per warp, for two CTAs per SM
 constexpr int kCtas = 304;      // two per SM on 152 SMs
-constexpr int kStageBytes = 2 * kBlk * 256;
+constexpr int kStageBytes = 2 * kBlk * 256;  // the K or the V rows of a step
 constexpr int kPitch = 136;     // floats per row of the warps' outputs in shared memory
 constexpr int kSmem = kWarps * kStages * kStageBytes;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -160,9 +160,12 @@ template <typename T> __device__ __forceinline__ void load_q(const AttnArgs &a, 
     }
 }
 
-// One warp streams blocks [blk0, blk0 + nblk) of a segment: the running
-// maximum (log2 units) and sum of rows g and g + 8, and their unnormalised
-// outputs at dims 8 j + 2 t, + 1. The warp's ring is free again afterwards.
+// One warp streams blocks [blk0, blk0 + nblk) of a segment, two at a time
+// (32 keys: two independent chains of products, one maximum and one rescaling
+// for both): the running maximum (log2 units) and sum of rows g and g + 8, and
+// their unnormalised outputs at dims 8 j + 2 t, + 1. The ring's slots take the
+// K rows of a step, its V rows, the K rows of the next step and so on; two are
+// in flight while one is used. The ring is free again afterwards.
 template <typename T>
 __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &sg, const uint32_t (&qa)[8][4], int len,
                                               int blk0, int nblk, uint32_t ring, float (&m_run)[2], float (&l_run)[2],
@@ -172,9 +175,8 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v);
     const float sl2 = p.scale * kLog2e;
     const int key0 = blk0 * kBlk;
-    const long long hoff = (long long)sg.h * p.head_stride;
-    // Window of up to 32 blocks, one per lane: the page (or -1), the
-    // slot in it and the valid slots of the block.
+    // Window of up to 32 blocks, one per lane: the page (or -1), the slot in
+    // it and the valid slots of the block.
     int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
     auto window = [&](int i0) {
         w_base = i0;
@@ -189,44 +191,51 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
             if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
         }
     };
-    int valid[kStages];
-    // Copy e of a lane: rows 2 e (lanes 0-15) and 2 e + 1 (16-31), 16-byte chunk lane % 16, stored at chunk
-    // (lane % 16) ^ (row % 8).
-    const long long lane_at = hoff + (lane >> 4) * p.tok_stride + 8 * (lane & 15);
+    // A lane copies the 16-byte chunk lane % 16 of rows 2 e (lanes 0-15) and 2 e + 1 (16-31) of each block, stored at
+    // chunk (lane % 16) ^ (row % 8).
+    const long long lane_at = (long long)sg.h * p.head_stride + (lane >> 4) * p.tok_stride + 8 * (lane & 15);
     const uint32_t lane_dst = (lane >> 4) * 256 + (((lane & 15) ^ (lane >> 4)) << 4);
-    const uint32_t step = (uint32_t)p.tok_stride * 4;  // bytes of two rows
-    auto issue = [&](int i, int stage) {  // block i of this piece into a stage
-        if (i >= w_base + 32) window(i);
-        const int id = __shfl_sync(0xffffffffu, w_id, i - w_base);
-        const int slot = __shfl_sync(0xffffffffu, w_slot, i - w_base);
-        const int ok = __shfl_sync(0xffffffffu, w_valid, i - w_base);
-        // A block lies inside its page, so the address of a row without a token is the page's own too.
-        const long long at = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + lane_at;
-        const char *kp = reinterpret_cast<const char *>(K + at), *vp = reinterpret_cast<const char *>(V + at);
-        const uint32_t dst = ring + stage * kStageBytes + lane_dst;
-        if (ok == kBlk) {
+    const uint32_t two_rows = (uint32_t)p.tok_stride * 4;  // bytes
+    long long at[2];  // of the step being copied: its blocks' elements in the cache, and their valid slots
+    int ok[2];
+    auto locate = [&](int step) {
+        if (2 * step >= w_base + 32) window(2 * step);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                cp16((dst + e * 512) ^ ((2 * e & 7) << 4), kp + (uint64_t)e * step);
-                cp16((dst + kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), vp + (uint64_t)e * step);
-            }
-        } else {
+        for (int h = 0; h < 2; ++h) {
+            const int from = 2 * step + h - w_base;
+            const int id = __shfl_sync(0xffffffffu, w_id, from);
+            const int slot = __shfl_sync(0xffffffffu, w_slot, from);
+            ok[h] = __shfl_sync(0xffffffffu, w_valid, from);
+            // A block lies inside its page, so the address of a row without a token is the page's own too.
+            at[h] = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + lane_at;
+        }
+    };
+    auto copy = [&](const T *from, uint32_t slot) {
+        const uint32_t dst = slot + lane_dst;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int bytes = 2 * e + (lane >> 4) < ok ? 16 : 0;
-                cp16z((dst + e * 512) ^ ((2 * e & 7) << 4), kp + (uint64_t)e * step, bytes);
-                cp16z((dst + kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), vp + (uint64_t)e * step, bytes);
+        for (int h = 0; h < 2; ++h) {
+            const char *src = reinterpret_cast<const char *>(from + at[h]);
+            if (ok[h] == kBlk) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    cp16((dst + h * kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), src + (uint64_t)e * two_rows);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    cp16z((dst + h * kBlk * 256 + e * 512) ^ ((2 * e & 7) << 4), src + (uint64_t)e * two_rows,
+                          2 * e + (lane >> 4) < ok[h] ? 16 : 0);
             }
         }
-        return ok;
     };
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-        valid[s] = 0;
-        if (s < nblk) valid[s] = issue(s, s);
+    const int steps = (nblk + 1) / 2;
+    uint32_t k_slot = ring, v_slot = ring + kStageBytes, free_slot = ring + 2 * kStageBytes;
+    if (steps > 0) {
+        locate(0);
+        copy(K, k_slot);
+        cp_commit();
+        copy(V, v_slot);
         cp_commit();
     }
-    valid[kStages - 1] = 0;
 
     m_run[0] = m_run[1] = -INFINITY;
     l_run[0] = l_run[1] = 0.f;
@@ -234,90 +243,111 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     for (int j = 0; j < 16; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    for (int i0 = 0; i0 < nblk; i0 += kStages) {
+    for (int i = 0; i < steps; ++i) {
+        const int live[2] = {ok[0], ok[1]};
+        cp_wait<1>();
+        __syncwarp();  // every lane's K copies have landed, and V of the step before was read
+        if (i + 1 < steps) {
+            locate(i + 1);
+            copy(K, free_slot);
+        }
+        cp_commit();
+        float sc[4][4];  // keys 8 u + 2 t, + 1 of rows g, g + 8
 #pragma unroll
-        for (int s = 0; s < kStages; ++s) {
-            const int i = i0 + s;
-            if (i >= nblk) break;
-            cp_wait<kStages - 2>();
-            __syncwarp();  // every lane's copies of this block have landed, and the stage ahead is free
-            const uint32_t st = ring + s * kStageBytes;
-            // All K fragments before the products that use them: the loads' latency is paid once a block.
-            uint32_t kb[8][4];
-            {
-                const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) ldsm4(kb[j], st + row * 256 + (((2 * j + c0) ^ (row & 7)) << 4));
-            }
-            if (i + kStages - 1 < nblk)
-                valid[(s + kStages - 1) % kStages] = issue(i + kStages - 1, (s + kStages - 1) % kStages);
-            cp_commit();
-            float sc[2][4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mma16816<T>(sc[0], qa[j], kb[j][0], kb[j][1]);
-                mma16816<T>(sc[1], qa[j], kb[j][2], kb[j][3]);
-            }
-            // half of V's fragments, to arrive while the softmax runs
-            const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc0 = lane >> 4;
-            auto ld_v = [&](uint32_t (&r)[4], int j) {
-                ldsm4t(r, st + kBlk * 256 + vrow * 256 + (((2 * j + vc0) ^ (vrow & 7)) << 4));
+            for (int e = 0; e < 4; ++e) sc[u][e] = 0.f;
+        {
+            // fragments a few products ahead of their use: f = 2 j + h is k-step j of block h
+            constexpr int kAhead = 6;
+            const int row = (lane & 7) + ((lane >> 4) << 3), c0 = (lane >> 3) & 1;
+            uint32_t kb[kAhead][4];
+            auto ld_k = [&](uint32_t (&r)[4], int f) {
+                ldsm4(r, k_slot + ((f & 1) * kBlk + row) * 256 + (((f & ~1) + c0) ^ (row & 7)) * 16);
             };
-            uint32_t vb[4][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) ld_v(vb[j], j);
-            if (valid[s] < kBlk) {
+            for (int f = 0; f < kAhead; ++f) ld_k(kb[f], f);
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (8 * u + 2 * t + (e & 1) >= valid[s]) sc[u][e] = -INFINITY;
-            }
-            // running maximum m of the unscaled scores; P = 2^(scale log2(e) (s - m))
-            float corr[2];
-            bool moved = false;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(ptx::fmax3(sc[0][2 * e], sc[0][2 * e + 1], sc[1][2 * e]), sc[1][2 * e + 1]);
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = ptx::fmax3(m_run[e], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                moved = moved || mx != m_run[e];
-                const float ref = mx == -INFINITY ? 0.f : mx * sl2;  // a row without keys so far
-                corr[e] = ptx::ex2(fmaf(m_run[e], sl2, -ref));
-                m_run[e] = mx;
-                float sum = 0.f;
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const float pr = ptx::ex2(fmaf(sc[u][2 * e + c], sl2, -ref));
-                        sc[u][2 * e + c] = pr;
-                        sum += pr;
-                    }
-                l_run[e] = fmaf(l_run[e], corr[e], sum);  // this lane's keys; quads are joined at the end
-            }
-            if (__any_sync(0xffffffffu, moved)) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    acc[j][0] *= corr[0];
-                    acc[j][1] *= corr[0];
-                    acc[j][2] *= corr[1];
-                    acc[j][3] *= corr[1];
-                }
-            }
-            // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the
-            // unrounded values): half a step of the output's own type
-            const uint32_t pa[4] = {pack2<T>(sc[0][0], sc[0][1]), pack2<T>(sc[0][2], sc[0][3]),
-                                    pack2<T>(sc[1][0], sc[1][1]), pack2<T>(sc[1][2], sc[1][3])};
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                mma16816<T>(acc[2 * j], pa, vb[j & 3][0], vb[j & 3][1]);
-                mma16816<T>(acc[2 * j + 1], pa, vb[j & 3][2], vb[j & 3][3]);
-                if (j < 4) ld_v(vb[j], j + 4);
+            for (int f = 0; f < 16; ++f) {
+                mma16816<T>(sc[2 * (f & 1)], qa[f >> 1], kb[f % kAhead][0], kb[f % kAhead][1]);
+                mma16816<T>(sc[2 * (f & 1) + 1], qa[f >> 1], kb[f % kAhead][2], kb[f % kAhead][3]);
+                if (f + kAhead < 16) ld_k(kb[f % kAhead], f + kAhead);
             }
         }
+        cp_wait<1>();
+        __syncwarp();  // every lane's V copies have landed, and K of this step was read
+        if (i + 1 < steps) copy(V, k_slot);
+        cp_commit();
+        constexpr int kAheadV = 6;
+        const int vrow = (lane & 7) + ((lane >> 3) & 1) * 8, vc0 = lane >> 4;
+        uint32_t vb[kAheadV][4];
+        auto ld_v = [&](uint32_t (&r)[4], int f) {  // f = 8 h + j: dims 16 j.. of block h
+            ldsm4t(r, v_slot + ((f >> 3) * kBlk + vrow) * 256 + (((2 * (f & 7) + vc0) ^ (vrow & 7)) << 4));
+        };
+#pragma unroll
+        for (int f = 0; f < kAheadV; ++f) ld_v(vb[f], f);  // to arrive while the softmax runs
+        if (live[0] + live[1] < 2 * kBlk) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (8 * (u & 1) + 2 * t + (e & 1) >= live[u >> 1]) sc[u][e] = -INFINITY;
+        }
+        // running maximum m of the unscaled scores; P = 2^(scale log2(e) (s - m))
+        float corr[2];
+        bool moved = false;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float mx = ptx::fmax3(sc[0][2 * e], sc[0][2 * e + 1], sc[1][2 * e]);
+            mx = ptx::fmax3(mx, sc[1][2 * e + 1], sc[2][2 * e]);
+            mx = ptx::fmax3(mx, sc[2][2 * e + 1], sc[3][2 * e]);
+            mx = fmaxf(mx, sc[3][2 * e + 1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = ptx::fmax3(m_run[e], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            moved = moved || mx != m_run[e];
+            const float ref = mx == -INFINITY ? 0.f : mx * sl2;  // a row without keys so far
+            corr[e] = ptx::ex2(fmaf(m_run[e], sl2, -ref));
+            m_run[e] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float pr = ptx::ex2(fmaf(sc[u][2 * e + c], sl2, -ref));
+                    sc[u][2 * e + c] = pr;
+                    sum += pr;
+                }
+            l_run[e] = fmaf(l_run[e], corr[e], sum);  // this lane's keys; quads are joined at the end
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                acc[j][0] *= corr[0];
+                acc[j][1] *= corr[0];
+                acc[j][2] *= corr[1];
+                acc[j][3] *= corr[1];
+            }
+        }
+        // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the unrounded
+        // values): half a step of the output's own type
+        uint32_t pa[2][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                pa[h][2 * u] = pack2<T>(sc[2 * h + u][0], sc[2 * h + u][1]);
+                pa[h][2 * u + 1] = pack2<T>(sc[2 * h + u][2], sc[2 * h + u][3]);
+            }
+#pragma unroll
+        for (int f = 0; f < 16; ++f) {
+            mma16816<T>(acc[2 * (f & 7)], pa[f >> 3], vb[f % kAheadV][0], vb[f % kAheadV][1]);
+            mma16816<T>(acc[2 * (f & 7) + 1], pa[f >> 3], vb[f % kAheadV][2], vb[f % kAheadV][3]);
+            if (f + kAheadV < 16) ld_v(vb[f % kAheadV], f + kAheadV);
+        }
+        const uint32_t was_k = k_slot;
+        k_slot = free_slot;
+        free_slot = v_slot;
+        v_slot = was_k;
     }
     cp_wait<0>();
     __syncwarp();  // the warp's ring is free
