@@ -47,7 +47,8 @@ constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does n
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
 constexpr int kMaxCluster = 16;     // 16,000 keys x 8 heads: 15.6 us, 22 with clusters of 8
 constexpr int kWarps = 4;
-constexpr int kStages = 3;      // ring slots per warp, for two CTAs per SM
+constexpr int kStages = 3;      // ring slots per warp, for two CTAs per SM; five, where there are no more CTAs than SMs,
+                                // left clusters of 16 without a place: 8 x 16,000 keys 15.7 -> 23 us
 constexpr int kCtas = 304;      // two per SM on 152 SMs
 constexpr int kStageBytes = 2 * kBlk * 256;  // the K or the V rows of a step
 constexpr int kPitch = 136;     // floats per row of the warps' outputs in shared memory
@@ -411,8 +412,10 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // 7.1 TB/s, the measured copy rate; 6,144 listed keys x 24 heads 16 us with 11
 // of them the bytes; 101 keys x 3 heads 3.7 us, of which 2 are the launch and
 // the rest length -> page id -> keys -> join, one after another. A warp alone
-// on its scheduler takes about 1,000 cycles per block (230 instructions, most
-// waiting on the one before), so few segments want many CTAs.
+// on its scheduler takes about 1,500 cycles per step of 32 keys, whatever the
+// depth of its ring: 400 instructions, most of them waiting on the one before
+// (of single blocks, 16 keys, it took 1,000 each). So few segments want many
+// CTAs.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
@@ -677,8 +680,7 @@ template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) 
     if (a.cluster) {
         const auto kernel = k_paged_attn_cluster<T>;
         cudaError_t e = ensure_smem_limit((const void *)kernel, kSmem);
-        if (e == cudaSuccess && a.cluster > 8)
-            e = cudaFuncSetAttribute((const void *)kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess && a.cluster > 8) e = ensure_wide_clusters((const void *)kernel);
         if (e != cudaSuccess) return status_from_cuda(e);
         prof_begin("paged_attn", s);
         e = launch_paged(kernel, dim3((unsigned)((long long)a.p.B * a.p.Hkv * a.rc * a.cluster)), kWarps * 32, kSmem,

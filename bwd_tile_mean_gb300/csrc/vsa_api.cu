@@ -162,6 +162,17 @@ cudaError_t ensure_smem_limit(const void *kernel, int bytes) {
     return cudaSuccess;
 }
 
+cudaError_t ensure_wide_clusters(const void *kernel) {
+    static std::vector<std::pair<unsigned long long, const void *>> done;  // (context id, kernel), under g_attr_mu
+    std::lock_guard<std::mutex> lock(g_attr_mu);
+    const unsigned long long ctx = current_context_id();
+    for (const auto &e : done)
+        if (ctx && e.first == ctx && e.second == kernel) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e == cudaSuccess && ctx) done.push_back({ctx, kernel});
+    return e;
+}
+
 // -------------------------------------------------------------- validation
 bool aligned16(const void *ptr) { return (reinterpret_cast<uintptr_t>(ptr) & 15u) == 0; }
 

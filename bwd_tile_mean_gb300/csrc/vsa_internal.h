@@ -35,6 +35,9 @@ unsigned long long current_context_id();
 // GPU and every context after a reset gets its own call); a later call with
 // a larger size raises it again. Thread-safe.
 cudaError_t ensure_smem_limit(const void *kernel, int bytes);
+// Allows a kernel clusters of more than 8 CTAs in the current context, once
+// per context. Thread-safe.
+cudaError_t ensure_wide_clusters(const void *kernel);
 
 // Host-side validation shared by the entry points: descriptor -> Prob
 // (VSA_OK or the status to return; scale 0 becomes 1/sqrt(D)); the tile
