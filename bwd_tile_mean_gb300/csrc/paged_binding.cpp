@@ -89,7 +89,9 @@ int64_t row_stride(const Calls &c, const char *name, const at::Tensor &t, int64_
         refuse(name, ": expected [tokens, ", heads, ", ", c.d.D, "], got ", t.sizes());
     if (t.size(0) > 0 && (t.stride(2) != 1 || (heads > 1 && t.stride(1) != c.d.D)))
         refuse(name, ": heads and dims must be dense");
-    return t.size(0) > 1 ? t.stride(0) : 0;
+    if (t.size(0) < 2) return 0;
+    if (t.stride(0) < heads * c.d.D) refuse(name, ": tokens must not share memory");  // 0 means dense further on
+    return t.stride(0);
 }
 at::Tensor output(const Calls &c, at::IntArrayRef shape, at::ScalarType dtype) {
     const at::Device device = c.device < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c.device);
@@ -228,6 +230,7 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         }
         const at::Tensor *go = optional(a[2], "out"), *gl = optional(a[3], "lse");
         if (go) check_dense(c, "out", *go, c.dtype(), {c.d.B, c.d.Hq, c.d.D});
+        if (go && go->data_ptr() == q.data_ptr()) refuse("out: must not be q");
         if (gl) check_dense(c, "lse", *gl, at::kFloat, {c.d.B, c.d.Hq});
         at::Tensor out = go ? *go : output(c, {c.d.B, c.d.Hq, c.d.D}, c.dtype());
         at::Tensor lse = gl ? *gl : output(c, {c.d.B, c.d.Hq}, at::kFloat);

@@ -638,6 +638,8 @@ class PagedCache:
             self._is(name, t, shape, dtype)
             if any(n > 1 and a != b for n, a, b in zip(shape[1:], t.stride()[1:], inner)):
                 raise ValueError(f"{name}: a page must be dense")
+            if num_pages > 1 and t.stride(0) < page * Hkv * D:
+                raise ValueError(f"{name}: pages must not share memory")
             if num_pages > 1 and stride not in (0, t.stride(0)):
                 raise ValueError("k and v must have the same page stride")
             stride = t.stride(0) if num_pages > 1 else 0
@@ -658,8 +660,9 @@ class PagedCache:
             raise ValueError("invalid paged-cache description")
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
-        elif workspace.device != self.device or workspace.numel() * workspace.element_size() < need:
-            raise ValueError(f"workspace: at least {need} bytes on {self.device} are needed")
+        elif (workspace.device != self.device or not workspace.is_contiguous()
+              or workspace.numel() * workspace.element_size() < need):
+            raise ValueError(f"workspace: at least {need} contiguous bytes on {self.device} are needed")
         self._workspace = workspace
         # every call passes these addresses on: the tensors behind them are read-only attributes
         at = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731

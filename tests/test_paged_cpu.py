@@ -167,6 +167,27 @@ def test_calls_refuse_bad_tensors(L):
             call()
 
 
+def test_broadcast_tensors_are_refused(L):
+    """An expanded tensor has the stride 0, which the C calls take for dense:
+    its storage ends before the rows they would then read."""
+    bf = dict(dtype=torch.bfloat16)
+    one, pages = torch.zeros(1, 16, 2, 128, **bf).expand(5, -1, -1, -1), torch.zeros(5, 16, 2, 128, **bf)
+    for kw in (dict(k=one, v=one), dict(k=one, v=pages), dict(k=pages, v=one),
+               dict(k=pages.as_strided(pages.shape, (8, 256, 128, 1)), v=pages),
+               dict(workspace=torch.zeros(1, dtype=torch.uint8).expand(1 << 28))):
+        with pytest.raises(ValueError):
+            cache(**kw)
+    c = cache()
+    k, q = torch.zeros(2, 2, 128, **bf), torch.zeros(2, 4, 128, **bf)
+    k1, q1 = k[:1].expand(2, -1, -1), q[:1].expand(2, -1, -1)
+    for call in (lambda: c.append(k1, k), lambda: c.append(k, k1), lambda: c.append(k, k, q1), lambda: c.select(q1, 2),
+                 lambda: c.attend(q1), lambda: c.append(k.as_strided(k.shape, (128, 128, 1)), k)):
+        with pytest.raises(ValueError, match="share memory"):
+            call()
+    with pytest.raises(ValueError, match="must not be q"):
+        c.attend(q, out=q)
+
+
 def test_reference_select_and_attend_on_a_case_by_hand():
     pool = ref.Pool("bshd", torch.bfloat16, 1, 1, 16, 6, 6, [16 * 4 + 3], seed=1)
     q = torch.zeros(1, 1, 128, dtype=torch.bfloat16)
