@@ -30,6 +30,7 @@
 // go to the workspace (at most two per warp), and k_paged_join adds them in
 // ascending order.
 #include <algorithm>
+#include <type_traits>
 
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
@@ -175,6 +176,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     const int lane = threadIdx.x & 31, t = lane & 3, b = sg.b, bh = sg.bh;
     const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v);
     const float sl2 = p.scale * kLog2e;
+    constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f, kDrop = kLift != 0.f ? 0x1p-15f : 1.f;
     const int key0 = blk0 * kBlk;
     // Window of up to 32 blocks, one per lane: the page (or -1), the slot in
     // it and the valid slots of the block.
@@ -294,7 +296,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
                 for (int e = 0; e < 4; ++e)
                     if (8 * (u & 1) + 2 * t + (e & 1) >= live[u >> 1]) sc[u][e] = -INFINITY;
         }
-        // running maximum m of the unscaled scores; P = 2^(scale log2(e) (s - m))
+        // running maximum m of the unscaled scores; P = 2^(scale log2(e) (s - m) + lift)
         float corr[2];
         bool moved = false;
 #pragma unroll
@@ -306,15 +308,16 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = ptx::fmax3(m_run[e], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             moved = moved || mx != m_run[e];
-            const float ref = mx == -INFINITY ? 0.f : mx * sl2;  // a row without keys so far
-            corr[e] = ptx::ex2(fmaf(m_run[e], sl2, -ref));
+            const float ref = mx == -INFINITY ? 0.f : mx;  // a row without keys so far
+            corr[e] = ptx::ex2((m_run[e] - ref) * sl2);
             m_run[e] = mx;
             float sum = 0.f;
 #pragma unroll
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float pr = ptx::ex2(fmaf(sc[u][2 * e + c], sl2, -ref));
+                    // the difference first: scale * s by itself loses what lies below its own last bit
+                    const float pr = ptx::ex2(fmaf(sc[u][2 * e + c] - ref, sl2, kLift));
                     sc[u][2 * e + c] = pr;
                     sum += pr;
                 }
@@ -329,8 +332,9 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
                 acc[j][3] *= corr[1];
             }
         }
-        // P <= 1 is rounded to the cache's 16-bit type for the product with V (the sum l keeps the unrounded
-        // values): half a step of the output's own type
+        // P is rounded to the cache's 16-bit type for the product with V (the sum l keeps the unrounded values):
+        // half a step of the output's own type. fp16 has no full steps below 2^-14, and a long row's keys may all lie
+        // below that next to one large score: there P is lifted into [0, 2^15], full steps down to 2^-29.
         uint32_t pa[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -356,8 +360,14 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     for (int e = 0; e < 2; ++e) {
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
+        l_run[e] *= kDrop;
         m_run[e] *= sl2;  // log2 units from here on
     }
+    if (kLift != 0.f)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][e] *= kDrop;
 }
 
 // Joins the CTA's four warps: f(row, o, M, l) per row, in the thread of its

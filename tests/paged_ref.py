@@ -185,15 +185,16 @@ def attend(pool, q, pages=None, scale=None):
             # A score is a sum of 128 products in fp32, scaled twice: off by at most
             # 132 * 2^-24 of the products' magnitudes (and 2^-22 of itself in log2 units), so a
             # weight by e^(2 ds) - 1 with its sum; exp2 adds 2^-22, the weight's rounding to
-            # 16 bits u (fp16: 2^-25 absolute below its normal range), sums over n keys n * 2^-24
-            # (tree-like: n / 16 steps of a warp), and the output's own rounding u.
+            # 16 bits u (fp16, lifted by 2^15: 2^-40 absolute below its normal range), sums over
+            # n keys n * 2^-24 (tree-like: n / 16 steps of a warp), and the output's own rounding
+            # u (fp16: 2^-25 absolute below its normal range).
             ds = 132 * 2.0 ** -24 * scale * (qq.abs() @ kk.abs().T).amax(1) + 2.0 ** -22 * s.abs().amax(1)
             rel = u + 2 * ds + (8 + kk.shape[0] / 16) * 2.0 ** -23
             mag = p @ vv.abs()
             tol[b, rows] = u * out[b, rows].abs() + rel[:, None] * mag * 1.01
             if pool.dtype == torch.float16:
                 top = torch.exp(s.amax(1) - torch.logsumexp(s, 1))  # 1 / sum of weights relative to the largest
-                tol[b, rows] += 2.0 ** -25 * (top[:, None] * vv.abs().sum(0)[None] + 1)
+                tol[b, rows] += 2.0 ** -40 * top[:, None] * vv.abs().sum(0)[None] + 2.0 ** -25
             ltol[b, rows] = ds + (8 + kk.shape[0] / 16) * 2.0 ** -23 + 2.0 ** -23 * lse[b, rows].abs()
     return out, lse, tol, ltol
 

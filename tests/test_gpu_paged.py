@@ -399,6 +399,44 @@ def test_attend_special_values():
         assert abs(float(l[3, h] - torch.logsumexp(s, 0))) < 1e-4
 
 
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("lens", [[9001], [9001, 33, 5000]])
+def test_attend_one_large_score_before_a_long_tail(dtype, lens):
+    """The first key's weight is e^16 times every other's, and its value 0:
+    the output is the sum of thousands of weights of 1e-7 each."""
+    pool, q = attend_pool(("bshd", dtype, 4, 2, 64, lens), seed=44)
+    q.fill_(1.0)
+    pool.k.zero_()
+    pool.v.copy_(pool.v.abs())
+    for b in range(pool.B):
+        first = pool.table[b][0]
+        pool.k[first, 0] = 16.0 / (D * D ** -0.5)
+        pool.v[first, 0] = 0.0
+    want = ref.attend(pool, q)
+    assert float(want[0][0].amax()) < 2e-3
+    for cache in (pool.cache(), widened(pool, 70000 // pool.page)):
+        ref.check_attend(cache.attend(q.cuda()), want, "long tail")
+
+
+@pytest.mark.parametrize("lens", [[40], [9001], [9001, 33, 5000]])
+def test_attend_scores_past_the_exponents_last_bit(lens):
+    """Scores of 1e13, whose last bit is worth thousands: the largest one's
+    weight is 1 all the same and the output its value."""
+    pool, q = attend_pool(("bhsd", BF, 4, 2, 64, lens), seed=45)
+    q = (q.float().abs() + 1).to(BF) * 1e6
+    pool.k.copy_((pool.k.float().abs() * 1e5).to(BF))
+    best = [n // 3 for n in lens]
+    for b, pos in enumerate(best):
+        pool.k[pool.table[b][pos // 64], pos % 64] = 3e6
+    for cache in (pool.cache(), widened(pool, 70000 // pool.page)):
+        out, lse = cache.attend(q.cuda())
+        for b, pos in enumerate(best):
+            v = pool.v[pool.table[b][pos // 64], pos % 64]
+            assert torch.equal(out[b].cpu(), v.repeat_interleave(2, 0))
+            s = q[b].double().sum(1) * 3e6 * D ** -0.5  # 3e6 in bf16 is off by less than 2^-8
+            assert ((lse[b].cpu().double() / s - 1).abs() < 2.0 ** -8).all()
+
+
 def test_attend_offsets_past_32_bits():
     """A pool of more than 2^32 bytes and 2^31 elements, pages at both ends."""
     page, Hkv = 256, 8
