@@ -26,11 +26,11 @@ constexpr int kD = 128;
 constexpr int kMaxHeads = 65536;  // key/value heads: a token's bytes stay within 32 bits
 
 // Sequence length, clamped into what the page table can hold.
-__device__ __forceinline__ int paged_len(const Paged &p, int b) { return clampi(__ldg(p.lens + b), 0, p.max_len); }
+__device__ __forceinline__ int paged_len(const Paged &p, int b) { return clampi(p.lens[b], 0, p.max_len); }
 // Page id of logical page j of sequence b, -1 when there is no such page.
 __device__ __forceinline__ int paged_id(const Paged &p, int b, int j) {
     if (j < 0 || j >= p.max_pages) return -1;
-    const int id = __ldg(p.table + (long long)b * p.max_pages + j);
+    const int id = p.table[(long long)b * p.max_pages + j];
     return id >= 0 && id < p.num_pages ? id : -1;
 }
 
@@ -164,7 +164,10 @@ __device__ __forceinline__ Run find_run(int N, F size_of, int workers, int min_p
 // Kernels of the paged calls are launched so that the next one on the stream
 // may start while this one drains: every CTA waits for the work before it
 // with grid_wait() before it touches memory, and lets the launch after it go
-// ahead with grid_go() when its streaming is over. Measured (us, such launches
+// ahead with grid_go() when its streaming is over. What the work before may
+// have written is read with ordinary loads: __ldg promises memory that no one
+// writes while the kernel runs, its wait included, and could be moved before
+// the wait. Measured (us, such launches
 // / plain ones): one-token append 2.7 / 2.9, attention of 101 keys 3.7 / 4.1,
 // select and attend 24.0 / 25.1. Letting the next launch in at the kernel's
 // start instead takes slots from its own CTAs: 4 sequences of 8,000 pages

@@ -51,7 +51,7 @@ constexpr int kGroup = 16;  // slots per warp
 constexpr long long kWideRows = 65536;  // token x key head rows from which a warp takes four heads
 
 // First token of sequence b, clamped into [0, T].
-__device__ __forceinline__ int cu_at(const AppendArgs &a, int b) { return clampi(__ldg(a.cu + b), 0, a.T); }
+__device__ __forceinline__ int cu_at(const AppendArgs &a, int b) { return clampi(a.cu[b], 0, a.T); }
 
 // The sequence whose units hold unit u: the largest b with cu[b] / page +
 // 2 b <= u. Whole warp, same u.
@@ -75,7 +75,7 @@ struct Angles {
     float c[8], s[8];  // half style: one per dim; interleaved: the first 4, one per pair
 };
 __device__ __forceinline__ void load4(float *dst, const float *src) {
-    const float4 x = __ldg(reinterpret_cast<const float4 *>(src));
+    const float4 x = *reinterpret_cast<const float4 *>(src);
     dst[0] = x.x, dst[1] = x.y, dst[2] = x.z, dst[3] = x.w;
 }
 __device__ __forceinline__ void load_angles(const AppendArgs &a, int row, int i, Angles &w) {
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
             t0 = b;
             n = 1;
         }
-        const long long len = __ldg(p.lens + b), first = len - n;  // unclamped: positions outside are dropped
+        const long long len = p.lens[b], first = len - n;  // unclamped: positions outside are dropped
         const long long lo = max(first, 0LL), hi = min(len, (long long)p.max_len);
         const long long base = a.cu ? (t0 >> p.page_log2) + 2LL * b : u;
         const long long pl = (lo >> p.page_log2) + (u - base);
@@ -195,10 +195,10 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
 #pragma unroll
                 for (int h = 0; h < 2 * HC; ++h)
                     x[c][h] = fresh && h < hn
-                                  ? __ldg(reinterpret_cast<const uint4 *>(q + tok * a.qs + (h0 + h) * kD + 8 * i))
+                                  ? *reinterpret_cast<const uint4 *>(q + tok * a.qs + (h0 + h) * kD + 8 * i)
                                   : make_uint4(0, 0, 0, 0);
                 if (fresh && 8 * i < a.rot) {
-                    const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                    const int row = a.pos ? a.pos[tok] : (pg << p.page_log2) + s;
                     load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
                 }
             }
@@ -260,12 +260,12 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
                     for (int h = 0; h < HC; ++h) {
                         xk[c][h] = xv[c][h] = make_uint4(0, 0, 0, 0);
                         if (fresh && h < hn) {
-                            xk[c][h] = __ldg(reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i));
-                            xv[c][h] = __ldg(reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i));
+                            xk[c][h] = *reinterpret_cast<const uint4 *>(k + tok * a.ks + (h0 + h) * kD + 8 * i);
+                            xv[c][h] = *reinterpret_cast<const uint4 *>(v + tok * a.vs + (h0 + h) * kD + 8 * i);
                         }
                     }
                     if (fresh && 8 * i < a.rot) {
-                        const int row = a.pos ? __ldg(a.pos + tok) : (pg << p.page_log2) + s;
+                        const int row = a.pos ? a.pos[tok] : (pg << p.page_log2) + s;
                         load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
                     }
                 }

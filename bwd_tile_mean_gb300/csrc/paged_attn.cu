@@ -76,7 +76,7 @@ struct AttnArgs {
 // positions it walks, valid or not.
 __device__ __forceinline__ int seg_keys(const AttnArgs &a, int n) {
     if (!a.idx) return paged_len(a.p, n);
-    return clampi(__ldg(a.cnt + n), 0, a.cap) * a.p.page;
+    return clampi(a.cnt[n], 0, a.cap) * a.p.page;
 }
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src) {
@@ -156,8 +156,8 @@ template <typename T> __device__ __forceinline__ void load_q(const AttnArgs &a, 
         const uint32_t *src = reinterpret_cast<const uint32_t *>(qb + (long long)row * kD);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            qa[j][e] = row < sg.rows ? __ldg(src + 8 * j + t) : 0u;
-            qa[j][2 + e] = row < sg.rows ? __ldg(src + 8 * j + 4 + t) : 0u;
+            qa[j][e] = row < sg.rows ? src[8 * j + t] : 0u;
+            qa[j][2 + e] = row < sg.rows ? src[8 * j + 4 + t] : 0u;
         }
     }
 }
@@ -189,7 +189,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
             const int pos = key0 + (i0 + lane) * kBlk;
             int j = pos >> p.page_log2;
             w_slot = pos & (p.page - 1);
-            if (a.idx) j = (unsigned)j < (unsigned)a.cap ? __ldg(a.idx + (long long)bh * a.cap + j) : -1;
+            if (a.idx) j = (unsigned)j < (unsigned)a.cap ? a.idx[(long long)bh * a.cap + j] : -1;
             w_id = paged_id(p, b, j);
             if (w_id >= 0) w_valid = clampi(len - (j << p.page_log2) - w_slot, 0, kBlk);
         }

@@ -23,12 +23,12 @@
 // 11.3, 32 sequences of 312 to 2,047 pages x 8 heads 44 / 30.5. The latter
 // reads 105 MB, 15.5 us at the measured copy rate: the means stream in about
 // 16 us, before them 4 us go by from the launch (scan of the lengths, page
-// ids) and after them 7 to 8 (keys out, the second launch, the top-k). One sequence is a chain of loads and barriers: 1.2 us length and
-// page ids, 2.4 the means, 3 the top-k.
+// ids) and after them 7 to 8 (keys out, the second launch, the top-k). One
+// sequence is a chain of loads and barriers: 1.2 us length and page ids, 2.4
+// the means, 3 the top-k.
 #include <algorithm>
 
 #include "paged.cuh"
-#include "sm103_ptx.cuh"
 #include "sm103_ptx.cuh"
 
 namespace vsa {
@@ -91,7 +91,7 @@ template <typename T> __device__ __forceinline__ void group_sum(const T *q, int 
         uint4 w[4];
 #pragma unroll
         for (int m = 0; m < 4; ++m)
-            w[m] = m0 + m < G ? __ldg(reinterpret_cast<const uint4 *>(q + (long long)(m0 + m) * kD)) : make_uint4(0, 0, 0, 0);
+            w[m] = m0 + m < G ? *reinterpret_cast<const uint4 *>(q + (long long)(m0 + m) * kD) : make_uint4(0, 0, 0, 0);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             const uint32_t r[4] = {w[m].x, w[m].y, w[m].z, w[m].w};
