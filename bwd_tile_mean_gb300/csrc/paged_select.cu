@@ -402,8 +402,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     grid_wait();
     const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2;
     const int comp = competing(a, b);
-    if (comp == 0) {  // the same for every CTA of the cluster
+    if (comp == 0) {
         if (rank < hn) list_all<kThreads>(a, (long long)b * p.Hkv + h0 + rank, pages);
+        ptx::cluster_sync();  // with the others, so that a CTA's shared memory is there whatever length they read
+        ptx::cluster_sync();
         return;
     }
     const int run = (comp + kCluster - 1) / kCluster;
