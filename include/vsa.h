@@ -472,10 +472,10 @@ vsa_status vsa_check_inputs(const vsa_desc *desc, const int32_t *q_var, const in
  *             keys, defined for full pages.
  * Tables, lengths and lists are read when the kernels run and must not
  * change while a call that reads them is under way. Device-resident values
- * out of range never move an access outside a buffer: lengths are clamped, a token whose page id is outside
- * [0, num_pages) is not stored, and a listed page that does not exist
- * (its index outside [0, max_pages) or its id outside the pool) holds no
- * key. Every length, id and offset is 64-bit where it is multiplied. */
+ * out of range never move an access outside a buffer: lengths are clamped,
+ * a token whose page id is outside [0, num_pages) is not stored, and a
+ * listed page that does not exist (its index outside [0, max_pages) or its
+ * id outside the pool) holds no key. Every length, id and offset is 64-bit where it is multiplied. */
 typedef struct {
     int32_t layout;       /* VSA_LAYOUT_BSHD or VSA_LAYOUT_BHSD: the order inside a page */
     int32_t dtype;        /* vsa_dtype of q, k, v, the cache and out */
@@ -492,9 +492,9 @@ typedef struct {
 } vsa_paged_desc;
 
 /* Bytes of workspace for vsa_page_select and vsa_paged_attn on this problem
- * (256-byte aligned; 0 for an invalid descriptor). It holds nothing between calls and needs no
- * clearing; calls that share it must not run concurrently. The page_table
- * and seq_lens pointers are not looked at. */
+ * (256-byte aligned; 0 for an invalid descriptor). It holds nothing between
+ * calls and needs no clearing; calls that share it must not run concurrently.
+ * The page_table and seq_lens pointers are not looked at. */
 size_t vsa_paged_workspace_size(const vsa_paged_desc *desc);
 
 /* Appends the new tokens' keys and values to the cache, rotating keys (and
@@ -542,8 +542,10 @@ vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, in
 
 /* Chooses the pages each key/value head's queries attend to. q [B, Hq, D]
  * (q_stride elements between sequences, 0: dense) is summed over the query
- * heads of each group (the exact sum, rounded once to fp32: g); full page j of
- * sequence b scores r_j = sum_d g_d m_jd with the page's mean m_j, the
+ * heads of each group in ascending order in fp32, the error of each rounding
+ * summed beside it and added last (the exact sum rounded once, but for ties
+ * and for sums that cancel by 2^20 and more): g. Full page j of sequence b
+ * scores r_j = sum_d g_d m_jd with the page's mean m_j, the
  * products and sums rounded to fp32 in this order: x_d = g_d m_d; x_d +
  * x_(d+64) for d < 64; of those x_d + x_(d+32) for d < 32; then neighbours
  * (2i, 2i + 1) until one is left. NaN counts as -inf. The first keep_first
@@ -560,10 +562,10 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
 
 /* Attention of one token per sequence over the cache: q [B, Hq, D]
  * (q_stride as above), out [B, Hq, D] dense (not q's memory), lse fp32
- * [B, Hq] (natural log). With page_idx == NULL every token of the sequence is attended;
- * otherwise the tokens of the pages page_idx [B, Hkv, idx_cap] lists for
- * the query head's key/value head, page_cnt [B, Hkv] of them (a page listed
- * twice counts twice). A row without keys gets O = 0, LSE = -inf. The work
+ * [B, Hq] (natural log). With page_idx == NULL every token of the sequence
+ * is attended; otherwise the tokens of the pages page_idx [B, Hkv, idx_cap]
+ * lists for the query head's key/value head, page_cnt [B, Hkv] of them (a
+ * page listed twice counts twice). A row without keys gets O = 0, LSE = -inf. The work
  * of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
  * bit on every run with the same batch. Errors as for vsa_page_select;
