@@ -21,8 +21,8 @@
 // 191 us = 6.1 TB/s, 90% of the measured copy rate (97% without a rotation:
 // the rest is the angles, read once per chunk); 31,000 tokens of 8 key heads
 // in 16-token pages 120 us, 97%. By the chain of dependent loads (offsets,
-// length, page id, rows) for a few tokens: 2.7 us for one, 4.9 us for 64
-// sequences' next tokens.
+// length, page id, rows) for a few tokens: 2.6 us for one, 4.2 us for 64
+// sequences' next tokens, 6.5 us for 13 prompts of up to 360.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -48,7 +48,19 @@ struct AppendArgs {
 };
 
 constexpr int kGroup = 16;  // slots per warp
-constexpr long long kWideRows = 65536;  // token x key head rows from which a warp takes four heads
+// A warp's share of a token, by the warps that the call would have with four
+// key heads each (of which 16 fit on an SM, 2,432 on 152): four heads, so that
+// a token's angles serve eight rows, once that fills half of the places with
+// whole groups of tokens (kWideFull) or all of them twice (kWideWarps, of which
+// many have little to do); one head and two pairs of slots at once, more and
+// shorter warps, while whole groups fill a quarter (kThinFull) and the other
+// warps no more (kThinRest); two heads between. Measured (us, four / two / one):
+// 20,400 tokens of 8 key heads with 4 queries each 91.9 / 102.5 / 134.7, 5,100
+// of them 24.6 / 29.3 / 38.4, 2,500 17.4 / 14.7 / 20.0, 1,270 10.9 / 8.7 / 8.2;
+// 1,480 tokens of 3 key heads 11.3 / 8.6 / 7.0; one token for each of 256
+// sequences, 24 key heads, 13.9 / 16.0 / 27.5, of 64, 8 key heads, 6.9 / 4.5 /
+// 6.0, of 8 6.3 / 3.9 / 3.4.
+constexpr long long kWideFull = 1216, kWideWarps = 4864, kThinFull = 608, kThinRest = 700;
 
 // First token of sequence b, clamped into [0, T].
 __device__ __forceinline__ int cu_at(const AppendArgs &a, int b) { return clampi(a.cu[b], 0, a.T); }
@@ -316,12 +328,19 @@ __global__ void __launch_bounds__(512) k_paged_append(AppendArgs a) {
     }
 }
 
+// Warps per unit: as many as a sequence's tokens fill groups on average (idle
+// warps hold registers), and up to four for the earlier keys of a page that
+// fills up.
+int team_of(const AppendArgs &a) {
+    const int groups = a.p.page / kGroup;
+    int team = std::min(groups, 4);
+    while (team < groups && (long long)a.T > (long long)team * kGroup * a.p.B) team *= 2;
+    return team;
+}
+
 template <typename T, int HC, int PB> cudaError_t launch_append(AppendArgs &a, cudaStream_t s) {
     const int groups = a.p.page / kGroup;
-    // Warps per unit: as many as a sequence's tokens fill groups on average (idle warps hold registers), and up to
-    // four for the earlier keys of a page that fills up.
-    a.team = std::min(groups, 4);
-    while (a.team < groups && (long long)a.T > (long long)a.team * kGroup * a.p.B) a.team *= 2;
+    a.team = team_of(a);
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
     a.kv_chunks = (a.p.Hkv + HC - 1) / HC;
     a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
@@ -378,12 +397,12 @@ extern "C" vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const 
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("paged_append", s);
     const bool bf = a.p.dtype == T_BF16;
-    // Four key heads per warp let a token's angles serve 8 rows, two heads and two pairs of slots at once give more
-    // and shorter warps. Measured (us, four heads / two): 30,000 tokens of 24 key heads 191 / 201, 4,000 of them 27.9
-    // / 29.8, 2,000 21.7 / 15.4; 8,000 tokens of 8 key heads with 4 queries each 44.7 / 40.7, 16,000 67 / 64.
-    const bool wide = (long long)T * a.p.Hkv >= kWideRows && a.p.G <= 2;
-    const cudaError_t e = wide ? (bf ? launch_append<__nv_bfloat16, 4, 1>(a, s) : launch_append<__half, 4, 1>(a, s))
-                               : (bf ? launch_append<__nv_bfloat16, 2, 2>(a, s) : launch_append<__half, 2, 2>(a, s));
+    const long long chunks = (a.p.Hkv + 3) / 4 + (q ? (a.p.Hq + 7) / 8 : 0), warps = a.units * team_of(a) * chunks;
+    const long long full = T / kGroup * chunks;
+    const bool wide = full > kWideFull || warps > kWideWarps, thin = full <= kThinFull && warps - full <= kThinRest;
+    const cudaError_t e = wide   ? (bf ? launch_append<__nv_bfloat16, 4, 1>(a, s) : launch_append<__half, 4, 1>(a, s))
+                          : thin ? (bf ? launch_append<__nv_bfloat16, 1, 2>(a, s) : launch_append<__half, 1, 2>(a, s))
+                                 : (bf ? launch_append<__nv_bfloat16, 2, 1>(a, s) : launch_append<__half, 2, 1>(a, s));
     prof_end(s);
     return status_from_cuda(e);
 }

@@ -51,6 +51,7 @@ APPEND = [  # layout, dtype, Hq, Hkv, page, rot, interleaved, lengths, new token
     ("bhsd", BF, 10, 5, 32, 32, False, [96, 97, 33], [32, 96, 2]),
     ("bshd", BF, 48, 24, 64, 96, True, [1500, 900, 450], [1450, 900, 400]),   # many rows: four key heads per warp
     ("bhsd", HF, 23, 23, 256, 128, False, [2100, 800], [2100, 777]),
+    ("bhsd", HF, 15, 5, 64, 96, False, [130, 64, 128, 71, 70] * 6, [70, 64, 70, 71, 3] * 6),  # two key heads per warp
 ]
 
 
@@ -117,6 +118,23 @@ def test_append_in_pieces_gives_the_same_bits(page):
     assert done == final
     for a, b in ((whole.k, pieces.k), (whole.v, pieces.v), (whole.k_mean, pieces.k_mean)):
         assert same(a, b)
+
+
+@pytest.mark.parametrize("B", [3, 200, 1300])
+def test_append_one_token_each(B):
+    """Without offsets; one, two and four key heads per warp."""
+    lens = [0 if b % 13 == 7 else (b % 3 + 1) * 32 if b % 4 == 0 else 1 + b % 70 for b in range(B)]
+    pool = Pool("bshd", BF, 6, 3, 32, sum(-(-n // 32) for n in lens), 4, lens, seed=18)
+    qkv, q, k, v = new_tokens(pool, B, seed=19)
+    cos, sin = angles(100, 128)
+    cache = pool.cache()
+    dq, dk, dv = split(pool, qkv.cuda())
+    q_out = torch.full((B, 6, D), math.nan, dtype=BF, device="cuda")
+    cache.append(dk, dv, dq, cos=cos.cuda(), sin=sin.cuda(), q_out=q_out)
+    want = ref.append(pool, k, v, q, list(range(B + 1)), cos, sin)
+    assert same(cache.k, pool.k) and same(cache.v, pool.v) and same(cache.k_mean, pool.mean)
+    fine = ~torch.isnan(want)
+    assert torch.equal(torch.isnan(q_out).cpu(), ~fine) and torch.equal(q_out.cpu()[fine], want[fine])
 
 
 def test_append_to_many_sequences():
