@@ -90,11 +90,12 @@ __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_grou
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
-}
 __device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v) {
     asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -371,8 +372,9 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 }
 
 // Joins the CTA's four warps: stat(row, M, l) once per row, with the maximum M
-// (log2 units) and the sum l, then out(row, o) per row, in the thread of its
-// dim: the unnormalised output, or the finished one (divided by l) where `done`.
+// (log2 units) and the sum l, then out(row, o) per row, in one warp, with a
+// lane's dims 4 lane..: the unnormalised output, or where `done` the finished
+// one (divided by l).
 // The rows' weights come first, side by side: one after another, with the
 // division and the logarithm of each, 16 rows took 2.4 us more than 5.
 // The warps' rings hold the outputs meanwhile.
@@ -408,14 +410,20 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
         if (w == 0 && row < rows) stat(row, M, l);
     }
     __syncthreads();
-#pragma unroll 4
-    for (int row = 0; row < rows; ++row) {
-        float o = 0.f;
+#pragma unroll 2
+    for (int row = wid; row < rows; row += kWarps) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w)
-            o += s_f[w][row] * reinterpret_cast<const float *>(smem + w * kStages * kStageBytes)[row * kPitch + tid];
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = s_f[w][row];
+            const float4 x = *reinterpret_cast<const float4 *>(smem + w * kStages * kStageBytes + (row * kPitch + 4 * lane) * 4);
+            o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
+        }
         out(row, o);
     }
+}
+template <typename T> __device__ __forceinline__ uint2 pack4(float4 o) {
+    return make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
 }
 __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : kLn2 * (M + log2f(l)); }
 
@@ -431,11 +439,12 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // CTAs.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
+    __shared__ __align__(16) float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
     __shared__ float2 s_pml[kRows];
     __shared__ float s_w[kRows];
-    const int tid = threadIdx.x, wid = tid >> 5, CS = a.cluster;
-    const int rank = (int)(blockIdx.x % CS), segment = (int)(blockIdx.x / CS);
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, CS = a.cluster;
+    const int lg = __ffs(CS) - 1;  // CS is a power of two
+    const int rank = (int)(blockIdx.x & (CS - 1)), segment = (int)(blockIdx.x >> lg);
     grid_wait();
     if (CS > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
     const int bh = segment / a.rc;
@@ -452,11 +461,12 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     if (CS == 1) {
         join_warps(
             smem, sg.rows, m_run, l_run, acc, true, [&](int row, float M, float l) { a.lse[sg.hq0 + row] = lse_of(M, l); },
-            [&](int row, float o) { out[(sg.hq0 + row) * kD + tid] = from_f<T>(o); });
+            [&](int row, float4 o) {
+                *reinterpret_cast<uint2 *>(out + (sg.hq0 + row) * kD + 4 * lane) = pack4<T>(o);
+            });
         return;
     }
-    const int lg = __ffs(CS) - 1;                // CS is a power of two
-    const int own = (sg.rows + CS - 1) >> lg;    // rows a CTA finishes at most
+    const int own = (sg.rows + CS - 1) >> lg;  // rows a CTA finishes at most
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     const auto part = [&](int row) { return rank * own + (row >> lg); };
     const auto to = [&](int row) { return (uint32_t)(row & (CS - 1)); };
@@ -465,7 +475,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         [&](int row, float M, float l) {
             st_cluster2(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), make_float2(M, l));
         },
-        [&](int row, float o) { st_cluster(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][tid]), to(row)), o); });
+        [&](int row, float4 o) { st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][4 * lane]), to(row)), o); });
     ptx::cluster_sync();  // the parts are there
     if (tid < CS * own) {  // their weights, side by side
         const int at = tid % own, row = (at << lg) + rank;
@@ -565,11 +575,11 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
                     else
                         a.ml[slot * a.rows + row] = make_float2(M, l);
                 },
-                [&](int row, float o) {
+                [&](int row, float4 o) {
                     if (whole)
-                        out[(sg.hq0 + row) * kD + tid] = from_f<T>(o);
+                        *reinterpret_cast<uint2 *>(out + (sg.hq0 + row) * kD + 4 * lane) = pack4<T>(o);
                     else
-                        a.o[(slot * a.rows + row) * kD + tid] = o;
+                        *reinterpret_cast<float4 *>(a.o + (slot * a.rows + row) * kD + 4 * lane) = o;
                 });
             return;
         }
@@ -679,7 +689,7 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
     }
     if (W == 1) {
         const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2 *>(out + 4 * lane) = make_uint2(pack2<T>(o.x * inv, o.y * inv), pack2<T>(o.z * inv, o.w * inv));
+        *reinterpret_cast<uint2 *>(out + 4 * lane) = pack4<T>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
         if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
         return;
     }
