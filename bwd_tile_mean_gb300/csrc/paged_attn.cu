@@ -43,8 +43,8 @@ constexpr int kRows = 16;       // query heads per segment at most
 constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time): 0, 1, 2, 3, 4
                                 // measured 102, 92, 87, 85.1, 84.8 us on 64 sequences of 37 to 16,000 keys
 constexpr int kAlignedKeys = 1280;  // keys per CTA up to which segments of unknown lengths get a cluster each
-constexpr int kClusterKeys = 128;   // keys per CTA below which a cluster does not grow: 64, 128, 256 measured 4.6, 3.9,
-                                    // 3.8 us at 101 keys x 3 heads and 4.1, 4.6, 5.5 at 300 x 8
+constexpr int kFewCtas = 912;       // and CTAs in all, three at each place: 1,192 segments of 17 keys 11.6 us, 7.6 in runs;
+                                    // 800 of 64 11.9, 14.2
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
 constexpr int kMaxCluster = 16;     // 16,000 keys x 8 heads: 15.6 us, 22 with clusters of 8
 constexpr int kWarps = 4;
@@ -712,6 +712,21 @@ int rows_of(int G) {
     return (G + chunks - 1) / chunks;
 }
 
+// Whether clusters of 2 c CTAs take segments of up to `keys` keys better than
+// clusters of c. The GPU has places for 152, 74, 36 and 14 clusters of 2, 4, 8
+// and 16 CTAs; one more than that starts when another ends (15 segments of
+// 16,000 keys in clusters of 8 / 16: 25.0 / 31.5 us, 14: 24.2 / 21.3), and a few
+// less leave the SMs' loads more even (36 of 4,000, 4 / 8: 15.9 / 18.1). A
+// cluster's barriers and join cost 1 to 2 us against 0.7 per 128 keys of a CTA:
+// clusters of 1 / 2 / 4 took 4.1 / 4.5 / 4.4 for 200 keys x 14 heads, 5.7 / 5.4 /
+// 4.4 for 400, 6.1 / 6.5 / - for 400 x 80, 12.0 / 11.1 / - for 1,000; of 4 / 8 / 16
+// 5.5 / 4.8 / 5.7 for 1,000 x 14, 7.2 / 6.2 / 5.6 for 2,000.
+bool grows(int c, long long segments, long long keys) {
+    if (c == 1) return segments <= 72 ? keys > 320 : segments <= 152 && keys > 1024;
+    if (c == 2) return segments <= 72;
+    return c == 4 ? segments <= 32 && keys > 768 : segments <= 14 && keys > 1024;
+}
+
 template <typename T> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
     if (a.cluster) {
         const auto kernel = k_paged_attn_cluster<T>;
@@ -793,16 +808,16 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
-    // One cluster per segment: twice the CTAs while that leaves an SM without one and every CTA with kClusterKeys
-    // keys. Segments of one length (one sequence, or page lists) are then balanced by themselves; of unknown lengths
-    // only while the longest stays short. Measured (us, clusters / runs): 300 keys x 8 heads 4.6 / 8.8, 4,000 x 8
-    // 6.9 / 9.6, 64,000 x 8 46.1 / 46.2, 64,000 x 1 34 / 13.6; 16 sequences of 1,000 to 9,000 keys x 2 heads 19.6 /
-    // 21.1, 64 of 37 to 16,000 x 8 151 / 84; lists of 4,096 keys x 256 rows, with their choice, 107 / 114.
+    // One cluster per segment, its CTAs doubled while all of the clusters find a place at once and the keys are many
+    // enough (grows()). Segments of one length (one sequence, or page lists) are then balanced by themselves; of
+    // unknown lengths only while the longest stays short. Measured (us, clusters / runs): 400 keys x 14 heads 4.4 /
+    // 8.2, x 400 19.5 / 21.8, x 1,600 61.6 / 60.9; 4,000 x 8 6.9 / 9.6, 64,000 x 24 116 / 124, 64,000 x 1 34 / 13.6; 16
+    // sequences of 1,000 to 9,000 keys x 2 heads 18.8 / 21.1, 64 of 37 to 16,000 x 8 151 / 84.
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
     int cluster = 1;
-    while (cluster < kMaxCluster && segments * cluster < 152 && most > (long long)kClusterKeys * cluster) cluster *= 2;
+    while (cluster < kMaxCluster && grows(cluster, segments, most)) cluster *= 2;
     const bool even = page_idx || a.p.B == 1;
-    const bool few = most <= (long long)kAlignedKeys * cluster && segments * cluster <= kCtas;
+    const bool few = most <= (long long)kAlignedKeys * cluster && segments * cluster <= kFewCtas;
     a.cluster = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
     char *w = static_cast<char *>(workspace);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);

@@ -283,6 +283,10 @@ ATTEND = [  # layout, dtype, Hq, Hkv, page, lengths
     ("bshd", BF, 2, 2, 64, [6000, 1, 0, 3001]),
     ("bhsd", HF, 16, 1, 16, [20011]),
     ("bshd", BF, 10, 2, 32, [7] * 200),
+    ("bhsd", BF, 80, 80, 64, [1100]),                # clusters of two CTAs
+    ("bshd", HF, 60, 20, 32, [700, 321, 0]),         # of four
+    ("bshd", BF, 64, 4, 64, [1000, 999]),            # of eight
+    ("bhsd", HF, 40, 2, 16, [3000]),                 # of sixteen, two chunks of a group's heads
 ]
 
 
