@@ -42,14 +42,14 @@ struct SelectArgs {
     int topk, first, last;
     int *idx, *cnt;
     uint32_t *keys;   // [B * Hkv, max_pages] of the competing pages, from keep_first on
-    int hg, hgroups;  // k_page_select: heads per cluster, clusters per sequence
+    int hg, hgroups;  // heads taken together, and their groups per sequence
     int cap;          // pages per CTA at most
 };
 
 constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
 constexpr int kTopkThreads = 512;  // 256, 512, 1,024 measured 36.4, 34.9, 34.9 us on 32 sequences of up to 2,047 pages
 constexpr int kCtasSel = 304;  // two per SM on 152 SMs
-constexpr int kHeads = 16;     // heads of a page taken together
+constexpr int kHeads = 16;     // heads of a page taken together at most, in equal groups
 constexpr int kLeadSel = 6;    // units a sequence counts for beyond its own (its start-up time): 1, 2, 4, 6 measured
                                // 36.4, 35.6, 34.9, 34.1 us on the same
 constexpr int kRing = 5;       // ring stages per warp, each four pages' means of one head (2 KB)
@@ -87,13 +87,15 @@ template <typename T> __device__ __forceinline__ void group_sum(const T *q, int 
     float s[8], err[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) s[e] = err[e] = 0.f;
-    for (int m0 = 0; m0 < G; m0 += 4) {  // four rows' loads at a time
-        uint4 w[4];
+    constexpr int kDeep = 8;  // rows' loads at a time
+    for (int m0 = 0; m0 < G; m0 += kDeep) {
+        uint4 w[kDeep];
 #pragma unroll
-        for (int m = 0; m < 4; ++m)
+        for (int m = 0; m < kDeep; ++m)
             w[m] = m0 + m < G ? *reinterpret_cast<const uint4 *>(q + (long long)(m0 + m) * kD) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-        for (int m = 0; m < 4; ++m) {
+        for (int m = 0; m < kDeep; ++m) {
+            if (m0 + m >= G) break;
             const uint32_t r[4] = {w[m].x, w[m].y, w[m].z, w[m].w};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -168,25 +170,24 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_scores(
     float *sq = reinterpret_cast<float *>(sm + kWarpsSel * kRingBytes);  // [kHeads][128] summed queries
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-    const int hgroups = (p.Hkv + kHeads - 1) / kHeads;
     grid_wait();
     // a unit: four pages, the heads of one group; a group's lead goes before its own units
     auto units_of = [&](int n) { const int q = (competing(a, n) + 3) / 4; return q > 0 ? q + kLeadSel : 0; };
     const Run run = find_run<kWarpsSel>(
-        p.B, [&](int n) -> long long { return (long long)units_of(n) * hgroups; }, kCtasSel, 1, 1);
+        p.B, [&](int n) -> long long { return (long long)units_of(n) * a.hgroups; }, kCtasSel, 1, 1);
     long long before = run.before;
     int b = run.n;
     for (long long x = run.x0; x < run.x1 && b < p.B;) {
         const int comp = competing(a, b), units = units_of(b);
-        if (x >= before + (long long)units * hgroups) {
-            before += (long long)units * hgroups;
+        if (x >= before + (long long)units * a.hgroups) {
+            before += (long long)units * a.hgroups;
             ++b;
             continue;
         }
         const int grp = div_small(x - before, units), off = (int)(x - before - (long long)grp * units);
         const int take = (int)min((long long)(units - off), run.x1 - x);
         const int q0 = max(off - kLeadSel, 0), nq = max(off + take - kLeadSel, 0) - q0;  // its own units
-        const int h0 = grp * kHeads, hn = min(kHeads, p.Hkv - h0);
+        const int h0 = grp * a.hg, hn = min(a.hg, p.Hkv - h0);
         x += take;
         if (nq == 0) continue;
 
@@ -482,19 +483,21 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
         prof_end(s);
         return status_from_cuda(e);
     };
-    // Heads per cluster: as many as still leave a CTA for every SM.
-    a.hg = 8;
-    while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
-        a.hg /= 2;
-    a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
-    const long long ctas = (long long)a.p.B * a.hgroups * kCluster;
-    if ((long long)a.p.max_pages * a.hg <= kClusterPages && ctas <= kCtasSel) {
-        a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
-        const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
-        return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
-                   kThreads, smem, kCluster);
-    }
     if (a.p.max_pages > topk) {  // otherwise no row has anything to choose
+        // Heads per cluster: as many as still leave a CTA for every SM.
+        a.hg = 8;
+        while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
+            a.hg /= 2;
+        a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
+        const long long ctas = (long long)a.p.B * a.hgroups * kCluster;
+        if ((long long)a.p.max_pages * a.hg <= kClusterPages && ctas <= kCtasSel) {
+            a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
+            const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
+            return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
+                       kThreads, smem, kCluster);
+        }
+        a.hgroups = (a.p.Hkv + kHeads - 1) / kHeads;
+        a.hg = (a.p.Hkv + a.hgroups - 1) / a.hgroups;
         const vsa_status e = run("page_scores", bf ? k_page_scores<__nv_bfloat16> : k_page_scores<__half>,
                                  dim3(kCtasSel), kThreads, kSmemSel, 1);
         if (e != VSA_OK) return e;
