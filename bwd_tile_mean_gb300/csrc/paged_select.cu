@@ -10,11 +10,11 @@
 // from the top (a 2,048-bin histogram), until the bin that holds it is small
 // enough to rank outright, and lists the taken pages in order.
 //
-// Few pages (kClusterPages): k_page_select, one launch. A cluster of 8 CTAs
-// has one sequence and up to 8 heads, cuts the pages into 8 runs and stores
+// Few pages, or very many (by_clusters): k_page_select, one launch. A cluster of
+// 8 CTAs has one sequence and up to 8 heads, cuts the pages into 8 runs and stores
 // the keys straight into the shared memory of the CTA that finishes the head;
 // the scores never leave the SMs.
-// Many: k_page_scores deals the pages of the whole batch, four at a time with
+// Others: k_page_scores deals the pages of the whole batch, four at a time with
 // up to 16 heads of each, to the CTAs in equal contiguous runs whatever the
 // lengths, with the keys in the workspace, and k_page_topk finishes the rows.
 // The longest sequence then does not wait for the 8 CTAs of its cluster.
@@ -57,7 +57,9 @@ constexpr int kRingBytes = kRing * 2048;
 constexpr int kSmemSel = kWarpsSel * kRingBytes + kHeads * kD * 4;
 constexpr int kCluster = 8;
 constexpr int kClusterStages = 4, kClusterRing = kClusterStages * 2048;
-constexpr int kClusterPages = 2048;  // pages x heads a cluster has at most
+constexpr int kClusterPages = 2048, kFullClusterPages = 2700;  // pages x heads a cluster has at most, the latter where
+                                                               // its CTAs fill the GPU
+constexpr long long kBatchPages = 560000;  // pages x heads of a batch (290 MB)
 constexpr int kBins = 2048;
 constexpr int kRank = 256;     // a bin of up to this many pages is ranked outright
 constexpr int kIndexBits = 27; // of a page index
@@ -448,6 +450,36 @@ template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(
     list_pages<kThreads>(a, (long long)b * p.Hkv + h0 + rank, pages, comp, hist, mine);
 }
 
+// CTAs of k_page_select with a.hg heads per cluster.
+long long cluster_ctas(const SelectArgs &a) { return (long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster; }
+
+// Whether k_page_select takes the call, and a.hg, a.hgroups for it. Measured
+// (us, clusters / equal runs): 960 pages x 24 heads of one sequence 7.7 / 11.3,
+// 3 sequences of 580 pages x 40 heads 10.4 / 12.4, 4,984 pages x 3 heads of one
+// 11.8 / 10.2, 32 sequences of 312 to 2,047 pages x 8 heads 44 / 30.5. With
+// work for many waves of clusters (kBatchPages) those start as others end,
+// which evens out the SMs' different shares of the memory (equal runs end
+// between 119,000 and 164,000 cycles): 89 sequences of 62 to 1,257 pages x 40
+// heads 230 / 282, 20 of 414 to 3,397 x 24 97 / 116, 77 of 162 to 3,025 x 8
+// 100.8 / 116.8; with short sequences their own start-up is too much, 89 of 14
+// to 195 x 40 82.6 / 68.2.
+bool by_clusters(SelectArgs &a) {
+    const int pages = a.p.max_pages;
+    auto heads = [&](long long ctas, int least) {  // as many per cluster as leave that many CTAs
+        for (a.hg = 8; a.hg > least && (cluster_ctas(a) < ctas || a.hg / 2 >= a.p.Hkv);) a.hg /= 2;
+        a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
+        return cluster_ctas(a);
+    };
+    if (pages >= 400 && pages <= 8192 && (long long)a.p.B * a.p.Hkv * pages > kBatchPages && a.p.Hkv > 1 &&
+        heads(700, 2) >= 700)
+        return cluster_ctas(a) <= 0x7fffffffLL;
+    heads(120, 1);
+    auto fits = [&] { return (long long)pages * a.hg <= (cluster_ctas(a) >= 144 ? kFullClusterPages : kClusterPages); };
+    while (a.hg > 1 && !fits()) a.hg /= 2;  // fewer heads for each, as far as places last
+    a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
+    return fits() && cluster_ctas(a) <= 320;
+}
+
 }  // namespace
 }  // namespace vsa
 
@@ -484,16 +516,10 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
         return status_from_cuda(e);
     };
     if (a.p.max_pages > topk) {  // otherwise no row has anything to choose
-        // Heads per cluster: as many as still leave a CTA for every SM.
-        a.hg = 8;
-        while (a.hg > 1 && ((long long)a.p.B * ((a.p.Hkv + a.hg - 1) / a.hg) * kCluster < 152 || a.hg / 2 >= a.p.Hkv))
-            a.hg /= 2;
-        a.hgroups = (a.p.Hkv + a.hg - 1) / a.hg;
-        const long long ctas = (long long)a.p.B * a.hgroups * kCluster;
-        if ((long long)a.p.max_pages * a.hg <= kClusterPages && ctas <= kCtasSel) {
+        if (by_clusters(a)) {
             a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
             const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
-            return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)ctas),
+            return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)cluster_ctas(a)),
                        kThreads, smem, kCluster);
         }
         a.hgroups = (a.p.Hkv + kHeads - 1) / kHeads;

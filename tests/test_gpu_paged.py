@@ -200,6 +200,9 @@ SELECT = [  # layout, dtype, Hq, Hkv, page, lengths, topk, keep_first, keep_last
     ("bshd", HF, 1, 1, 256, [256 * 40], 39, 0, 1),
     ("bhsd", BF, 6, 2, 32, [32 * 50, 32 * 49 + 7], 1, 0, 1),
     ("bhsd", BF, 16, 1, 16, [16 * 5000 + 3, 16 * 700], 300, 4, 4),
+    ("bshd", BF, 4, 2, 16, [100, 16, 0, 333], 64, 0, 1),                          # fewer pages than are asked for
+    ("bhsd", HF, 24, 24, 16, [b * 71 % 1400 for b in range(20)], 20, 1, 1),       # many heads: two groups, many clusters
+    ("bshd", BF, 96, 3, 64, [64 * 900, 64 * 350 + 9, 64 * 41], 33, 0, 2),         # 32 query heads each
 ]
 
 
