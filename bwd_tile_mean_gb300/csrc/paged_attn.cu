@@ -7,10 +7,10 @@
 // of its group: one tile of the tensor instructions; a wider group's chunks
 // read the same keys, from L2 but for the first); its keys, in the order of
 // the pages attended, are cut into blocks of 16. A warp streams a run of
-// blocks through its own ring of asynchronous copies (16 K rows and 16 V rows
-// of 256 bytes per stage, swizzled so that ldmatrix reads hit distinct banks;
-// rows past a page's valid slots are filled with zeros, so whatever the cache
-// holds there cannot reach the sums) and keeps its own running maximum, sum
+// blocks, two per step, through its own ring of asynchronous copies (a slot
+// takes the 32 K rows of a step or its V rows, 256 bytes each, swizzled so that
+// ldmatrix reads hit distinct banks; rows past a page's valid slots are filled
+// with zeros, so whatever the cache holds there cannot reach the sums) and keeps its own running maximum, sum
 // and output in registers: no warp waits for another while it streams. The
 // products run on m16n8k16 tensor instructions with the group's query heads
 // as rows. At one query token per sequence the kernel reads 512 bytes per
@@ -431,12 +431,13 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // blocks). Row r is finished by CTA r % cluster, which has a place for every
 // CTA's part of it. 122,880 keys x 24 heads (1.51 GB): 213 to 226 us, 6.7 to
 // 7.1 TB/s, the measured copy rate; 6,144 listed keys x 24 heads 16 us with 11
-// of them the bytes; 101 keys x 3 heads 3.7 us, of which 2 are the launch and
+// of them the bytes; 101 keys x 3 heads 3.6 us, of which 2 are the launch and
 // the rest length -> page id -> keys -> join, one after another. A warp alone
-// on its scheduler takes about 1,500 cycles per step of 32 keys, whatever the
-// depth of its ring: 400 instructions, most of them waiting on the one before
-// (of single blocks, 16 keys, it took 1,000 each). So few segments want many
-// CTAs.
+// on its scheduler takes about 1,500 cycles per step of 32 keys (of single
+// blocks, 16 keys, it took 1,000 each), whatever the depth of its ring and with
+// half the products too: the four warps' copies and fragment loads are 128 KB
+// a step through the SM's shared memory, 1,000 cycles. So few segments want
+// many CTAs.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ __align__(16) float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
@@ -498,9 +499,9 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
 
 // Equal runs of all segments' blocks. A segment counts kLead blocks more than
 // it has, in front of its own. 64 sequences of 37 to 16,000 keys x 8 heads
-// (504 MB): 84 us with the join, 88% of the measured copy rate; of the rest
-// 3.5 us are the start of a CTA (scan, length, page id, first keys) and 4 the
-// join.
+// (504 MB): 82 to 84 us with the join, 88 to 90% of the measured copy rate (99% at
+// four times the bytes); of the rest 3.5 us are the start of a CTA (scan, length,
+// page id, first keys) and 4 the join.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;
