@@ -48,6 +48,8 @@ struct SelectArgs {
 
 constexpr int kThreads = 256, kWarpsSel = kThreads / 32;
 constexpr int kTopkThreads = 512;  // 256, 512, 1,024 measured 36.4, 34.9, 34.9 us on 32 sequences of up to 2,047 pages
+constexpr int kLongRow = 20480;    // pages from which a row has twice the threads: 512, 1,024 measured 13.5, 14.7 us on one
+                                   // of 10,000 pages, 20.0, 20.1 of 20,000, 41.9, 35.0 of 40,000
 constexpr int kCtasSel = 304;  // two per SM on 152 SMs
 constexpr int kHeads = 16;     // heads of a page taken together at most, in equal groups
 constexpr int kLeadSel = 6;    // units a sequence counts for beyond its own (its start-up time): 1, 2, 4, 6 measured
@@ -376,19 +378,19 @@ template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a,
     if (tid == 0) a.cnt[row] = a.topk;
 }
 
-__global__ void __launch_bounds__(kTopkThreads) k_page_topk(SelectArgs a) {
+template <int N> __global__ void __launch_bounds__(N) k_page_topk(SelectArgs a) {
     __shared__ __align__(16) int hist[kBins];
     const Paged &p = a.p;
     const long long row = blockIdx.x;
     const int b = (int)(row / p.Hkv);
-    clear_bins<kTopkThreads>(hist);
+    clear_bins<N>(hist);
     grid_wait();
     grid_go();
     const int pages = (paged_len(p, b) + p.page - 1) >> p.page_log2, comp = competing(a, b);
     if (comp == 0)
-        list_all<kTopkThreads>(a, row, pages);
+        list_all<N>(a, row, pages);
     else
-        list_pages<kTopkThreads>(a, row, pages, comp, hist, a.keys + row * p.max_pages);
+        list_pages<N>(a, row, pages, comp, hist, a.keys + row * p.max_pages);
 }
 
 template <typename T> __global__ void __launch_bounds__(kThreads) k_page_select(SelectArgs a) {
@@ -528,5 +530,7 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
                                  dim3(kCtasSel), kThreads, kSmemSel, 1);
         if (e != VSA_OK) return e;
     }
-    return run("page_topk", k_page_topk, dim3((unsigned)(a.p.B * a.p.Hkv)), kTopkThreads, 0, 1);
+    const dim3 rows((unsigned)(a.p.B * a.p.Hkv));
+    return a.p.max_pages > kLongRow ? run("page_topk", k_page_topk<2 * kTopkThreads>, rows, 2 * kTopkThreads, 0, 1)
+                                    : run("page_topk", k_page_topk<kTopkThreads>, rows, kTopkThreads, 0, 1);
 }

@@ -203,6 +203,7 @@ SELECT = [  # layout, dtype, Hq, Hkv, page, lengths, topk, keep_first, keep_last
     ("bshd", BF, 4, 2, 16, [100, 16, 0, 333], 64, 0, 1),                          # fewer pages than are asked for
     ("bhsd", HF, 24, 24, 16, [b * 71 % 1400 for b in range(20)], 20, 1, 1),       # many heads: two groups, many clusters
     ("bshd", BF, 96, 3, 64, [64 * 900, 64 * 350 + 9, 64 * 41], 33, 0, 2),         # 32 query heads each
+    ("bhsd", HF, 4, 1, 16, [16 * 30000 + 5, 16 * 21], 900, 2, 2),
 ]
 
 
@@ -215,10 +216,10 @@ def select_pool(case, seed=21):
 
 
 def check_select(pool, q, topk, first, last):
-    """With the table as it is and with a much wider one: the call takes
-    another variant for tables of many pages."""
+    """With the table as it is and with much wider ones: the call takes
+    other variants for tables of many pages."""
     want = ref.select(pool, q, topk, first, last)
-    for wide in (0, 4000):
+    for wide in (0, 4000, 25000):
         table = torch.nn.functional.pad(torch.tensor(pool.table, dtype=torch.int32), (0, wide), value=-9)
         cache = vsa.PagedCache(pool.layout, pool.dtype, pool.B, pool.Hq, pool.Hkv, D, pool.page, pool.num_pages,
                                pool.max_pages + wide, k_mean=pool.mean.cuda(), page_table=table.cuda(),
