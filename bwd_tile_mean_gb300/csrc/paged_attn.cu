@@ -394,7 +394,8 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
         if (row < rows)
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-                *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
+                *reinterpret_cast<float2 *>(so + row * kPitch + 8 * j + 2 * t) =
+                    make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
     }
     __syncthreads();
     if (tid < kWarps * kRows) {  // the warps' weights
@@ -416,7 +417,8 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             const float f = s_f[w][row];
-            const float4 x = *reinterpret_cast<const float4 *>(smem + w * kStages * kStageBytes + (row * kPitch + 4 * lane) * 4);
+            const float *from = reinterpret_cast<const float *>(smem + w * kStages * kStageBytes);
+            const float4 x = *reinterpret_cast<const float4 *>(from + row * kPitch + 4 * lane);
             o.x += f * x.x, o.y += f * x.y, o.z += f * x.z, o.w += f * x.w;
         }
         out(row, o);
@@ -440,7 +442,8 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // many CTAs.
 template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ __align__(16) float s_part[kRows][kD];  // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
+    // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
+    __shared__ __align__(16) float s_part[kRows][kD];
     __shared__ float2 s_pml[kRows];
     __shared__ float s_w[kRows];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, CS = a.cluster;
@@ -476,7 +479,9 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         [&](int row, float M, float l) {
             st_cluster2(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), make_float2(M, l));
         },
-        [&](int row, float4 o) { st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][4 * lane]), to(row)), o); });
+        [&](int row, float4 o) {
+            st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][4 * lane]), to(row)), o);
+        });
     ptx::cluster_sync();  // the parts are there
     if (tid < CS * own) {  // their weights, side by side
         const int at = tid % own, row = (at << lg) + rank;

@@ -250,7 +250,8 @@ template <int N> __device__ __forceinline__ void clear_bins(int (&hist)[kBins]) 
 // Lists the pages of a row: the first and last ones that are always taken,
 // and the `take` best of the competing ones, whose keys are keys[0, comp).
 // Whole CTA; `hist` is clear.
-template <int N> __device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, int pages, int comp, int (&hist)[kBins],
+template <int N>
+__device__ __forceinline__ void list_pages(const SelectArgs &a, long long row, int pages, int comp, int (&hist)[kBins],
                                            const uint32_t *keys) {
     constexpr int W = N / 32;
     __shared__ int wsum[W];
@@ -521,8 +522,8 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
         if (by_clusters(a)) {
             a.cap = (a.p.max_pages + kCluster - 1) / kCluster;
             const size_t smem = kWarpsSel * kClusterRing + sizeof(float) * a.hg * kD + (size_t)a.cap * 4 * (kCluster + 1);
-            return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>, dim3((unsigned)cluster_ctas(a)),
-                       kThreads, smem, kCluster);
+            return run("page_select", bf ? k_page_select<__nv_bfloat16> : k_page_select<__half>,
+                       dim3((unsigned)cluster_ctas(a)), kThreads, smem, kCluster);
         }
         a.hgroups = (a.p.Hkv + kHeads - 1) / kHeads;
         a.hg = (a.p.Hkv + a.hgroups - 1) / a.hgroups;

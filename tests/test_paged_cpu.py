@@ -28,7 +28,8 @@ def desc(**kw):
 
 
 BAD_DESC = [(dict(layout=2), 4), (dict(layout=-1), 4), (dict(dtype=2), 3), (dict(B=0), 2), (dict(Hq=7), 2),
-            (dict(Hkv=0), 2), (dict(Hq=65537, Hkv=65537), 5), (dict(D=64), 5), (dict(page=48), 5), (dict(page=8), 5), (dict(page=512), 5),
+            (dict(Hkv=0), 2), (dict(Hq=65537, Hkv=65537), 5), (dict(D=64), 5), (dict(page=48), 5),
+            (dict(page=8), 5), (dict(page=512), 5),
             (dict(num_pages=0), 2), (dict(max_pages=0), 2), (dict(max_pages=1 << 25), 5),
             (dict(page_stride=64 * 2 * 128 - 8), 2), (dict(page_stride=64 * 2 * 128 + 4), 2),
             (dict(scale=-1.0), 2), (dict(scale=float("nan")), 2), (dict(scale=float("inf")), 2)]
@@ -149,7 +150,8 @@ def test_calls_refuse_bad_tensors(L):
     for args, kw in (((k, k[:1]), {}), ((k, k, q[:1]), {}), ((k.half(), k), {}), ((k, k[:, :1]), {}),
                      ((k, k.transpose(1, 2)), {}), ((torch.zeros(3, 2, 128, **bf),) * 2, {}),
                      ((k, k), dict(cos=t)), ((k, k), dict(cos=t, sin=t[:8])), ((k, k), dict(cos=t.double(), sin=t)),
-                     ((k, k), dict(cos=t.t(), sin=t.t())), ((k, k), dict(q_out=q)), ((k, k, q), dict(q_out=q[:1])), ((k, k, q), dict(q_out=q)),
+                     ((k, k), dict(cos=t.t(), sin=t.t())), ((k, k), dict(q_out=q)),
+                     ((k, k, q), dict(q_out=q[:1])), ((k, k, q), dict(q_out=q)),
                      ((k, k), dict(cu_seqlens=torch.zeros(2, **i32))), ((k, k), dict(cu_seqlens=torch.zeros(3))),
                      ((k, k), dict(positions=torch.zeros(2))), ((k, k), dict(positions=torch.zeros(3, **i32)))):
         with pytest.raises(ValueError):
