@@ -199,7 +199,7 @@ inline cudaError_t launch_paged(void (*kernel)(A), dim3 grid, unsigned threads, 
 struct PagedWs {
     size_t keys;        // [B * Hkv, max_pages] uint32 score keys
     size_t seg;         // [segments] int4: where a segment's pieces are
-    size_t ml;          // [slots, rows] float2: running maximum (log2 units) and sum
+    size_t ml;          // [slots, rows] float4: maximum (log2 units), sum of weights, of rounded weights, 0
     size_t o;           // [slots, rows, 128] fp32 unnormalised partial outputs
     size_t total;
 };

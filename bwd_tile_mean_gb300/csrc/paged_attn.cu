@@ -1,7 +1,16 @@
 // paged_attn.cu -- attention of one token per sequence over a paged
 // key/value cache (vsa_paged_attn), all pages or the listed ones.
 //
-//   O = sum_u P_u v_u / sum_u P_u,  P_u = exp(scale q.k_u - max)
+//   O = sum_u W_u v_u / sum_u W_u,  LSE = max + log sum_u P_u,
+//   P_u = exp(scale q.k_u - max), W_u = P_u rounded to the cache's 16 bits
+//
+// The products with V take 16-bit weights; O is divided by the sum of the
+// weights it was made with, so these sum to one whatever the roundings did:
+// keys of one score all round the same way, and the sum of the P_u left their
+// common error in O (9,001 keys, scores 0 and -0.69, V = 1: 0.996 in bf16, and
+// +inf in fp16 for V = 65504). What remains is u sum_u p_u |v_u - O|, u half a
+// step of the type. The sum of the W_u comes from the same instruction, as the
+// product with a column of ones: two more of a step's 64.
 //
 // A segment is one (sequence, key/value head, chunk of up to 16 query heads
 // of its group: one tile of the tensor instructions; a wider group's chunks
@@ -68,7 +77,7 @@ struct AttnArgs {
     int rc, rows;          // chunks of a group's heads, rows per chunk
     int cluster;           // CTAs per segment, one cluster; 0: equal runs of all segments' blocks
     int4 *seg;             // [segments] its pieces: first warp, warps before / CTAs joined / pieces in all
-    float2 *ml;            // [2 * kCtas * kWarps, rows]
+    float4 *ml;            // [2 * kCtas * kWarps, rows] maximum (log2 units), sum of P, sum of W, 0
     float *o;              // [2 * kCtas * kWarps, rows, 128]
 };
 
@@ -89,9 +98,6 @@ __device__ __forceinline__ void cp16z(uint32_t dst, const void *src, int bytes) 
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-__device__ __forceinline__ void st_cluster2(uint32_t addr, float2 v) {
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(addr), "f"(v.x), "f"(v.y) : "memory");
 }
 __device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
@@ -165,19 +171,20 @@ template <typename T> __device__ __forceinline__ void load_q(const AttnArgs &a, 
 
 // One warp streams blocks [blk0, blk0 + nblk) of a segment, two at a time
 // (32 keys: two independent chains of products, one maximum and one rescaling
-// for both): the running maximum (log2 units) and sum of rows g and g + 8, and
-// their unnormalised outputs at dims 8 j + 2 t, + 1. The ring's slots take the
+// for both): the running maximum (log2 units), the sums of P and of W of rows
+// g and g + 8, and their unnormalised outputs at dims 8 j + 2 t, + 1. The ring's slots take the
 // K rows of a step, its V rows, the K rows of the next step and so on; two are
 // in flight while one is used. The ring is free again afterwards.
 template <typename T>
 __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &sg, const uint32_t (&qa)[8][4], int len,
                                               int blk0, int nblk, uint32_t ring, float (&m_run)[2], float (&l_run)[2],
-                                              float (&acc)[16][4]) {
+                                              float (&w_run)[2], float (&acc)[16][4]) {
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, t = lane & 3, b = sg.b, bh = sg.bh;
     const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v);
     const float sl2 = p.scale * kLog2e;
     constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f, kDrop = kLift != 0.f ? 0x1p-15f : 1.f;
+    constexpr uint32_t kOnes = std::is_same<T, __half>::value ? 0x3C003C00u : 0x3F803F80u;
     const int key0 = blk0 * kBlk;
     // Window of up to 32 blocks, one per lane: the page (or -1), the slot in
     // it and the valid slots of the block.
@@ -243,6 +250,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 
     m_run[0] = m_run[1] = -INFINITY;
     l_run[0] = l_run[1] = 0.f;
+    float wsum[4] = {0.f, 0.f, 0.f, 0.f};  // rows g, g, g + 8, g + 8
 #pragma unroll
     for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -325,6 +333,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
             l_run[e] = fmaf(l_run[e], corr[e], sum);  // this lane's keys; quads are joined at the end
         }
         if (__any_sync(0xffffffffu, moved)) {
+            wsum[0] *= corr[0], wsum[1] *= corr[0], wsum[2] *= corr[1], wsum[3] *= corr[1];
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
                 acc[j][0] *= corr[0];
@@ -333,9 +342,9 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
                 acc[j][3] *= corr[1];
             }
         }
-        // P is rounded to the cache's 16-bit type for the product with V (the sum l keeps the unrounded values):
-        // half a step of the output's own type. fp16 has no full steps below 2^-14, and a long row's keys may all lie
-        // below that next to one large score: there P is lifted into [0, 2^15], full steps down to 2^-29.
+        // W: P rounded to the cache's 16-bit type for the product with V; the sum of P, for the LSE, keeps the
+        // unrounded values. fp16 has no full steps below 2^-14, and a long row's keys may all lie below that next to
+        // one large score: there P is lifted into [0, 2^15], full steps down to 2^-29.
         uint32_t pa[2][4];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -344,6 +353,8 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
                 pa[h][2 * u] = pack2<T>(sc[2 * h + u][0], sc[2 * h + u][1]);
                 pa[h][2 * u + 1] = pack2<T>(sc[2 * h + u][2], sc[2 * h + u][3]);
             }
+        mma16816<T>(wsum, pa[0], kOnes, kOnes);
+        mma16816<T>(wsum, pa[1], kOnes, kOnes);
 #pragma unroll
         for (int f = 0; f < 16; ++f) {
             mma16816<T>(acc[2 * (f & 7)], pa[f >> 3], vb[f % kAheadV][0], vb[f % kAheadV][1]);
@@ -361,27 +372,23 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     for (int e = 0; e < 2; ++e) {
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
-        l_run[e] *= kDrop;
-        m_run[e] *= sl2;  // log2 units from here on
+        l_run[e] *= kDrop;  // the outputs and the sum of W they are divided by stay lifted
+        m_run[e] *= sl2;    // log2 units from here on
+        w_run[e] = wsum[2 * e];
     }
-    if (kLift != 0.f)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[j][e] *= kDrop;
 }
 
-// Joins the CTA's four warps: stat(row, M, l) once per row, with the maximum M
-// (log2 units) and the sum l, then out(row, o) per row, in one warp, with a
-// lane's dims 4 lane..: the unnormalised output, or where `done` the finished
-// one (divided by l).
+// Joins the CTA's four warps: stat(row, {M, l, w, 0}) once per row, with the
+// maximum M (log2 units) and the sums l of P and w of W, then out(row, o) per
+// row, in one warp, with a lane's dims 4 lane..: the unnormalised output, or
+// where `done` the finished one (divided by w).
 // The rows' weights come first, side by side: one after another, with the
 // division and the logarithm of each, 16 rows took 2.4 us more than 5.
 // The warps' rings hold the outputs meanwhile.
 template <typename S, typename F>
 __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const float (&m_run)[2], const float (&l_run)[2],
-                                           const float (&acc)[16][4], bool done, S stat, F out) {
-    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_f[kWarps][kRows];
+                                           const float (&w_run)[2], const float (&acc)[16][4], bool done, S stat, F out) {
+    __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_w[kWarps][kRows], s_f[kWarps][kRows];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
     float *so = reinterpret_cast<float *>(smem + wid * kStages * kStageBytes);
 #pragma unroll
@@ -390,6 +397,7 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
         if (t == 0) {
             s_m[wid][row] = m_run[e];
             s_l[wid][row] = l_run[e];
+            s_w[wid][row] = w_run[e];
         }
         if (row < rows)
 #pragma unroll
@@ -399,16 +407,20 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
     }
     __syncthreads();
     if (tid < kWarps * kRows) {  // the warps' weights
-        const int w = tid / kRows, row = tid % kRows;
-        float M = -INFINITY, l = 0.f;
+        const int mine = tid / kRows, row = tid % kRows;
+        float M = -INFINITY, l = 0.f, w = 0.f;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) M = fmaxf(M, s_m[v][row]);
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
-        for (int v = 0; v < kWarps; ++v) l += ptx::ex2(s_m[v][row] - ref) * s_l[v][row];
-        const float f = ptx::ex2(s_m[w][row] - ref);
-        s_f[w][row] = !done ? f : l == 0.f ? 0.f : f / l;
-        if (w == 0 && row < rows) stat(row, M, l);
+        for (int v = 0; v < kWarps; ++v) {
+            const float f = ptx::ex2(s_m[v][row] - ref);
+            l += f * s_l[v][row];
+            w += f * s_w[v][row];
+        }
+        const float f = ptx::ex2(s_m[mine][row] - ref);
+        s_f[mine][row] = !done ? f : w == 0.f ? 0.f : f / w;
+        if (mine == 0 && row < rows) stat(row, make_float4(M, l, w, 0.f));
     }
     __syncthreads();
 #pragma unroll 2
@@ -444,8 +456,8 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     extern __shared__ __align__(128) unsigned char smem[];
     // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
     __shared__ __align__(16) float s_part[kRows][kD];
-    __shared__ float2 s_pml[kRows];
-    __shared__ float s_w[kRows];
+    __shared__ __align__(16) float4 s_pml[kRows];
+    __shared__ float s_f[kRows];
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, CS = a.cluster;
     const int lg = __ffs(CS) - 1;  // CS is a power of two
     const int rank = (int)(blockIdx.x & (CS - 1)), segment = (int)(blockIdx.x >> lg);
@@ -458,13 +470,15 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     load_q<T>(a, sg, qa);
     const int per = (nb + CS * kWarps - 1) / (CS * kWarps);
     const int blk0 = min((rank * kWarps + wid) * per, nb), nblk = min(per, nb - blk0);
-    float m_run[2], l_run[2], acc[16][4];
-    stream_blocks<T>(a, sg, qa, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
+    float m_run[2], l_run[2], w_run[2], acc[16][4];
+    stream_blocks<T>(a, sg, qa, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, w_run,
+                     acc);
     grid_go();
     T *out = static_cast<T *>(a.out);
     if (CS == 1) {
         join_warps(
-            smem, sg.rows, m_run, l_run, acc, true, [&](int row, float M, float l) { a.lse[sg.hq0 + row] = lse_of(M, l); },
+            smem, sg.rows, m_run, l_run, w_run, acc, true,
+            [&](int row, float4 s) { a.lse[sg.hq0 + row] = lse_of(s.x, s.y); },
             [&](int row, float4 o) {
                 *reinterpret_cast<uint2 *>(out + (sg.hq0 + row) * kD + 4 * lane) = pack4<T>(o);
             });
@@ -475,29 +489,32 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
     const auto part = [&](int row) { return rank * own + (row >> lg); };
     const auto to = [&](int row) { return (uint32_t)(row & (CS - 1)); };
     join_warps(
-        smem, sg.rows, m_run, l_run, acc, false,
-        [&](int row, float M, float l) {
-            st_cluster2(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), make_float2(M, l));
-        },
+        smem, sg.rows, m_run, l_run, w_run, acc, false,
+        [&](int row, float4 s) { st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), s); },
         [&](int row, float4 o) {
             st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][4 * lane]), to(row)), o);
         });
     ptx::cluster_sync();  // the parts are there
     if (tid < CS * own) {  // their weights, side by side
         const int at = tid % own, row = (at << lg) + rank;
-        float M = -INFINITY, l = 0.f;
+        float M = -INFINITY, l = 0.f, w = 0.f;
         for (int c = 0; c < CS; ++c) M = fmaxf(M, s_pml[c * own + at].x);
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll 4
-        for (int c = 0; c < CS; ++c) l += ptx::ex2(s_pml[c * own + at].x - ref) * s_pml[c * own + at].y;
-        s_w[tid] = l == 0.f ? 0.f : ptx::ex2(s_pml[tid].x - ref) / l;
+        for (int c = 0; c < CS; ++c) {
+            const float4 s = s_pml[c * own + at];
+            const float f = ptx::ex2(s.x - ref);
+            l += f * s.y;
+            w += f * s.z;
+        }
+        s_f[tid] = w == 0.f ? 0.f : ptx::ex2(s_pml[tid].x - ref) / w;
         if (tid < own && row < sg.rows) a.lse[sg.hq0 + row] = lse_of(M, l);
     }
     __syncthreads();
     for (int at = 0, row = rank; row < sg.rows; ++at, row += CS) {
         float o = 0.f;
 #pragma unroll 4
-        for (int c = 0; c < CS; ++c) o += s_w[c * own + at] * s_part[c * own + at][tid];
+        for (int c = 0; c < CS; ++c) o += s_f[c * own + at] * s_part[c * own + at][tid];
         out[(sg.hq0 + row) * kD + tid] = from_f<T>(o);
     }
 }
@@ -552,8 +569,9 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         const int len = paged_len(p, sg.b);
         uint32_t qa[8][4];
         load_q<T>(a, sg, qa);
-        float m_run[2], l_run[2], acc[16][4];
-        stream_blocks<T>(a, sg, qa, len, off, take, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, acc);
+        float m_run[2], l_run[2], w_run[2], acc[16][4];
+        stream_blocks<T>(a, sg, qa, len, off, take, ptx::smem_addr(smem) + wid * kStages * kStageBytes, m_run, l_run, w_run,
+                         acc);
         if (x >= x_end) grid_go();
 
         // A piece of the segment that begins it describes all of its pieces.
@@ -574,12 +592,12 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         if (joined) {
             const bool whole = first && last;
             join_warps(
-                smem, sg.rows, m_run, l_run, acc, whole,
-                [&](int row, float M, float l) {
+                smem, sg.rows, m_run, l_run, w_run, acc, whole,
+                [&](int row, float4 s) {
                     if (whole)
-                        a.lse[sg.hq0 + row] = lse_of(M, l);
+                        a.lse[sg.hq0 + row] = lse_of(s.x, s.y);
                     else
-                        a.ml[slot * a.rows + row] = make_float2(M, l);
+                        a.ml[slot * a.rows + row] = s;
                 },
                 [&](int row, float4 o) {
                     if (whole)
@@ -593,19 +611,18 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
         for (int e = 0; e < 2; ++e) {
             const int row = g + 8 * e;
             if (row >= sg.rows) continue;
-            const float l = l_run[e];
             if (first && last) {
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = w_run[e] == 0.f ? 0.f : 1.f / w_run[e];
                 uint32_t *dst = reinterpret_cast<uint32_t *>(out + (sg.hq0 + row) * kD);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) dst[4 * j + t] = pack2<T>(acc[j][2 * e] * inv, acc[j][2 * e + 1] * inv);
-                if (t == 0) a.lse[sg.hq0 + row] = lse_of(m_run[e], l);
+                if (t == 0) a.lse[sg.hq0 + row] = lse_of(m_run[e], l_run[e]);
             } else {
                 float *dst = a.o + (slot * a.rows + row) * kD;
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
                     *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t) = make_float2(acc[j][2 * e], acc[j][2 * e + 1]);
-                if (t == 0) a.ml[slot * a.rows + row] = make_float2(m_run[e], l);
+                if (t == 0) a.ml[slot * a.rows + row] = make_float4(m_run[e], l_run[e], w_run[e], 0.f);
             }
         }
     }
@@ -622,7 +639,7 @@ template <typename T> __global__ void __launch_bounds__(kWarps * 32) k_paged_att
 constexpr int kJoinDeep = 8, kJoinFew = 152, kJoinMany = 1024;
 template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32) k_paged_join(AttnArgs a) {
     static_assert(W == 1 || R == 1, "a row's warps meet at the CTA's barrier");
-    __shared__ float s_wt[R][kCtas * kWarps], s_red[W], s_sum[W];
+    __shared__ float s_ft[R][kCtas * kWarps], s_red[W], s_l[W], s_w[W];
     __shared__ __align__(16) float s_o[W][kD];
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, wid = R > 1 ? 0 : (int)threadIdx.x >> 5;  // warp of the row
@@ -633,7 +650,7 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
     if (row >= p.B * p.Hq) return;
     const int b = row / p.Hq, hq = row % p.Hq, h = hq / p.G, in = hq % p.G;
     const int bh = b * p.Hkv + h;
-    float *s_w = s_wt[team];
+    float *s_f = s_ft[team];
     T *out = static_cast<T *>(a.out) + (long long)row * kD;
     const int4 sg = a.seg[(long long)bh * a.rc + in / a.rows];  // not written for a segment without keys
     if (seg_keys(a, a.idx ? bh : b) == 0) {
@@ -651,8 +668,8 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
     };
     float M = -INFINITY;
     for (int i = tid; i < pieces; i += W * 32) {
-        s_w[i] = a.ml[place(i)].x;
-        M = fmaxf(M, s_w[i]);
+        s_f[i] = a.ml[place(i)].x;
+        M = fmaxf(M, s_f[i]);
     }
 #pragma unroll
     for (int off = 16; off; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
@@ -663,16 +680,21 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
         for (int w = 0; w < W; ++w) M = fmaxf(M, s_red[w]);
     }
     const float ref = M == -INFINITY ? 0.f : M;
-    float l = 0.f;
+    float l = 0.f, w = 0.f;
     for (int i = tid; i < pieces; i += W * 32) {  // the thread's own entries again
-        const float e = ptx::ex2(s_w[i] - ref);
-        s_w[i] = e;
-        l += e * a.ml[place(i)].y;
+        const float e = ptx::ex2(s_f[i] - ref);
+        const float4 s = a.ml[place(i)];
+        s_f[i] = e;
+        l += e * s.y;
+        w += e * s.z;
     }
 #pragma unroll
-    for (int off = 16; off; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    for (int off = 16; off; off >>= 1) {
+        l += __shfl_xor_sync(0xffffffffu, l, off);
+        w += __shfl_xor_sync(0xffffffffu, w, off);
+    }
     if (W > 1) {
-        if (lane == 0) s_sum[wid] = l;
+        if (lane == 0) s_l[wid] = l, s_w[wid] = w;
         __syncthreads();
     } else {
         __syncwarp();
@@ -686,7 +708,7 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
                                        : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < kJoinDeep; ++e) {
-            const float f = i0 + e * W < pieces ? s_w[i0 + e * W] : 0.f;
+            const float f = i0 + e * W < pieces ? s_f[i0 + e * W] : 0.f;
             o.x += f * x[e].x;
             o.y += f * x[e].y;
             o.z += f * x[e].z;
@@ -694,22 +716,24 @@ template <typename T, int W, int R> __global__ void __launch_bounds__(W * R * 32
         }
     }
     if (W == 1) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = w == 0.f ? 0.f : 1.f / w;
         *reinterpret_cast<uint2 *>(out + 4 * lane) = pack4<T>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (lane == 0) a.lse[row] = l == 0.f ? -INFINITY : kLn2 * (M + log2f(l));
+        if (lane == 0) a.lse[row] = lse_of(M, l);
         return;
     }
     *reinterpret_cast<float4 *>(&s_o[wid][4 * lane]) = o;
     __syncthreads();
     if (tid >= kD) return;
-    float sum = 0.f, val = 0.f;
+    float val = 0.f;
+    l = w = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        sum += s_sum[w];
-        val += s_o[w][tid];
+    for (int c = 0; c < W; ++c) {
+        l += s_l[c];
+        w += s_w[c];
+        val += s_o[c][tid];
     }
-    out[tid] = from_f<T>(sum == 0.f ? 0.f : val / sum);
-    if (tid == 0) a.lse[row] = sum == 0.f ? -INFINITY : kLn2 * (M + log2f(sum));
+    out[tid] = from_f<T>(w == 0.f ? 0.f : val / w);
+    if (tid == 0) a.lse[row] = lse_of(M, l);
 }
 
 // Rows per chunk of a group of G query heads: equal chunks of up to 16.
@@ -773,7 +797,7 @@ PagedWs paged_ws(const Paged &p) {
     const size_t rows = rows_of(p.G), rc = (p.G + rows - 1) / rows;
     w.keys = take(sizeof(uint32_t) * p.B * (size_t)p.Hkv * p.max_pages);
     w.seg = take(sizeof(int4) * p.B * (size_t)p.Hkv * rc);
-    w.ml = take(sizeof(float2) * 2 * kCtas * kWarps * rows);
+    w.ml = take(sizeof(float4) * 2 * kCtas * kWarps * rows);
     w.o = take(sizeof(float) * 2 * kCtas * kWarps * rows * kD);
     w.total = at;
     return w;
@@ -827,7 +851,7 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     a.cluster = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
     char *w = static_cast<char *>(workspace);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);
-    a.ml = reinterpret_cast<float2 *>(w + ws.ml);
+    a.ml = reinterpret_cast<float4 *>(w + ws.ml);
     a.o = reinterpret_cast<float *>(w + ws.o);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16>(a, s) : launch_attn<__half>(a, s);

@@ -565,7 +565,10 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
  * [B, Hq] (natural log). With page_idx == NULL every token of the sequence
  * is attended; otherwise the tokens of the pages page_idx [B, Hkv, idx_cap]
  * lists for the query head's key/value head, page_cnt [B, Hkv] of them (a
- * page listed twice counts twice). A row without keys gets O = 0, LSE = -inf. The work
+ * page listed twice counts twice). A row without keys, or whose scores are all -inf,
+ * gets O = 0, LSE = -inf. The softmax and its sums are fp32; the weights are
+ * rounded to dtype for the product with V, and O is divided by their sum as
+ * rounded, so O stays within the values it averages. The work
  * of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
  * bit on every run with the same batch. Errors as for vsa_page_select;

@@ -444,6 +444,68 @@ def test_attend_one_large_score_before_a_long_tail(dtype, lens):
         ref.check_attend(cache.attend(q.cuda()), want, "long tail")
 
 
+@pytest.mark.parametrize("dtype,value", [(BF, 1.0), (BF, -2.984375), (HF, 1.0), (HF, 65504.0)])
+@pytest.mark.parametrize("lens", [[300], [9001], [9001, 33, 5000]])
+def test_attend_gives_a_constant_value_back(dtype, value, lens):
+    """Every 16th score 0 (one for each block of a warp's run), the others
+    between -0.69 and -0.77, the same within a head, so that all weights of a
+    head round the same way (by up to half a step: the heads differ), and
+    every value the same: so is the output, from clusters, equal runs and page
+    lists. The 16-bit weights' sum is taken as their products with V are, so
+    their roundings cancel; what is left is that of fp32 sums of at most
+    9,001 / 16 steps: 563 * 2^-23 = 6.7e-5, below half a step of either type
+    (fp16 at 65504: 2.4e-4)."""
+    pool, q = attend_pool(("bshd", dtype, 16, 2, 64, lens), seed=46)
+    q.copy_((1 + torch.arange(16) / 128)[None, :, None].expand_as(q))
+    pool.k.fill_(-0.69 / D ** 0.5)
+    pool.v.fill_(value)
+    pool.k[:, ::16] = 0.0
+    want = ref.attend(pool, q)
+    every = torch.full((pool.B, 2, pool.max_pages), -1, dtype=torch.int32)
+    cnt = torch.zeros((pool.B, 2), dtype=torch.int32)
+    for b, n in enumerate(lens):
+        cnt[b] = -(-n // 64)
+        every[b, :, :cnt[b, 0]] = torch.arange(int(cnt[b, 0]), dtype=torch.int32)
+    for cache, pages in itertools.product((pool.cache(), widened(pool, 70000 // 64)), (None, (every.cuda(), cnt.cuda()))):
+        out, lse = cache.attend(q.cuda(), pages)
+        assert (out == value).all(), float(out[0, 0, 0])
+        assert ((lse.double().cpu() - want[1]).abs() <= want[3]).all()
+
+
+@pytest.mark.parametrize("Hq,Hkv,page", [(16, 1, 16), (3, 3, 64), (20, 1, 32), (8, 2, 128)])
+@pytest.mark.parametrize("classes", [128, 127, 101])
+def test_attend_counts_every_block_once(Hq, Hkv, page, classes):
+    """Equal scores, and dim d of V set in the 16-key blocks d, d + classes,
+    ... only: dim d of the output is the share of those keys, so a block that
+    is lost, doubled or taken for its neighbour shows. All weights are alike
+    and counts are exact, so a share is off by its own rounding and a few of
+    fp32's (2^-20)."""
+    pool, q = attend_pool(("bhsd", BF, Hq, Hkv, page, RAGGED), seed=47)
+    q.zero_()
+    pool.v.zero_()
+    spoil(pool)
+    counts = torch.zeros((pool.B, D), dtype=torch.float64)
+    for b, n in enumerate(pool.lens):
+        for pos in range(n):
+            pool.v[pool.table[b][pos // page], pos % page, :, pos // 16 % classes] = 1.0
+            counts[b, pos // 16 % classes] += 1
+    lens = torch.tensor(pool.lens, dtype=torch.float64)
+    share = (counts / lens.clamp(min=1)[:, None])[:, None].expand(-1, Hq, -1)
+    logs = lens.log()[:, None].expand(-1, Hq)
+    idx = torch.full((pool.B, Hkv, pool.max_pages + 2), -1, dtype=torch.int32)
+    cnt = torch.zeros((pool.B, Hkv), dtype=torch.int32)
+    for b, n in enumerate(pool.lens):
+        order = torch.randperm(-(-n // page), generator=pool.gen).int()
+        cnt[b] = len(order)
+        idx[b, :, :len(order)] = order
+    for cache, pages in itertools.product((pool.cache(), widened(pool, 70000 // page)), (None, (idx.cuda(), cnt.cuda()))):
+        out, lse = (x.double().cpu() for x in cache.attend(q.cuda(), pages))
+        assert ((out - share).abs() <= (ref.U[BF] + 2.0 ** -20) * share).all()
+        assert torch.equal(lse == -math.inf, logs == -math.inf)
+        held = logs > -math.inf
+        assert ((lse - logs).abs()[held] <= 2.0 ** -20 * (1 + logs[held])).all()
+
+
 @pytest.mark.parametrize("lens", [[40], [9001], [9001, 33, 5000]])
 def test_attend_scores_past_the_exponents_last_bit(lens):
     """Scores of 1e13, whose last bit is worth thousands: the largest one's
