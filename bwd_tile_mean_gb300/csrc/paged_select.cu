@@ -496,6 +496,8 @@ extern "C" vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q,
     if (st != VSA_OK) return st;
     if (!token_stride(q_stride, a.p.Hq, &a.qs)) return VSA_ERR_SHAPE;
     if (keep_first < 0 || keep_last < 1 || topk < 1 || (long long)keep_first + keep_last > topk) return VSA_ERR_SHAPE;
+    // as vsa_paged_attn's lists; the kernels count a list's entries, past its end by a CTA's threads, in 32 bits
+    if ((long long)topk * a.p.page > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
     if (!q || !k_mean || !page_idx || !page_cnt) return VSA_ERR_NULL;
     if (!aligned16(q) || !aligned16(k_mean) || ((uintptr_t)page_idx | (uintptr_t)page_cnt) & 3u) return VSA_ERR_LAYOUT;
     const PagedWs ws = paged_ws(a.p);

@@ -553,8 +553,8 @@ vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, in
  * always chosen (a partial last page has no mean and is always among
  * them); the rest of min(topk, pages) by (r desc, j asc).
  * Writes page_idx [B, Hkv, topk] int32, ascending, unused entries -1, and
- * page_cnt [B, Hkv]. topk >= keep_first + keep_last. The result is the
- * same bit for bit on every run. Errors as for vsa_paged_append, and
+ * page_cnt [B, Hkv]. topk >= keep_first + keep_last, topk * page < 2^31. The
+ * result is the same bit for bit on every run. Errors as for vsa_paged_append, and
  * VSA_ERR_WORKSPACE. */
 vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const float *k_mean,
                            int topk, int keep_first, int keep_last, int32_t *page_idx, int32_t *page_cnt,
@@ -572,7 +572,8 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
  * of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
  * bit on every run with the same batch. Errors as for vsa_page_select;
- * VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1. */
+ * VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1,
+ * VSA_ERR_UNSUPPORTED for idx_cap * page >= 2^31. */
 vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
                           const void *v_cache, const int32_t *page_idx, const int32_t *page_cnt, int idx_cap,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, vsa_stream_t stream);

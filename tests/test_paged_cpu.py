@@ -205,3 +205,16 @@ def test_reference_select_and_attend_on_a_case_by_hand():
     keys = [pool.v[pool.table[0][1]][:, 0].double(), pool.v[pool.table[0][4]][:3, 0].double()]
     assert torch.allclose(out[0, 0], torch.cat(keys).mean(0))
     assert abs(float(lse[0, 0]) - torch.log(torch.tensor(19.0)).item()) < 1e-6
+
+
+def test_select_refuses_more_entries_than_a_list_can_have(L):
+    """topk entries are written in steps of a CTA's threads, counted in 32
+    bits; vsa_paged_attn takes lists of the same lengths."""
+    for page in (16, 256):
+        most = (2 ** 31 - 1) // page
+        need = L.vsa_paged_workspace_size(C.byref(desc(page=page)))
+        assert select(L, desc(page=page), topk=most + 1) == 5
+        assert select(L, desc(page=page), topk=2 ** 31 - 1) == 5
+        assert select(L, desc(page=page), topk=most, wsb=need - 1) == 7  # gets as far as the workspace
+        assert attn(L, desc(page=page), idx=FAKE, cnt=FAKE, cap=most + 1) == 5
+        assert attn(L, desc(page=page), idx=FAKE, cnt=FAKE, cap=most, wsb=need - 1) == 7
