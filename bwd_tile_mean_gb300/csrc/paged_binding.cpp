@@ -5,7 +5,7 @@
 // vsa_paged_attn on a GB300's CPU; here 4.7 us, most of it the launch.
 //
 // Module paged_binding, type Calls(desc, k, v, k_mean, workspace,
-// workspace_bytes, functions, fail): desc is the address of a vsa_paged_desc
+// workspace_bytes, functions, fail), the cache's tensors apart: desc is the address of a vsa_paged_desc
 // (copied), k .. workspace device addresses (0: none), functions the
 // addresses of vsa_paged_append, vsa_page_select and vsa_paged_attn, fail a
 // callable (name, status) that raises. The tensors behind the addresses are
@@ -20,8 +20,10 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
 #include <sstream>
 #include <stdexcept>
+#include <utility>
 
 #include "vsa.h"
 
@@ -37,6 +39,7 @@ struct Calls {
     decltype(&vsa_paged_attn) attn;
     PyObject *fail;
     int device;  // CUDA device index, -1: the cache is not on a GPU
+    bool shared;  // k and v share memory: attended to, but not appended to
     at::ScalarType dtype() const { return d.dtype == VSA_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
 };
 
@@ -104,6 +107,53 @@ PyObject *pair(at::Tensor a, at::Tensor b) {
     PyTuple_SET_ITEM(t, 1, THPVariable_Wrap(std::move(b)));
     return t;
 }
+// Equal pieces of memory, `pitch` bytes from one to the next: the rows of a
+// part of a projection's output, the pages of one half of a buffer.
+struct Pieces {
+    const char *name;
+    uintptr_t at;
+    int64_t count, bytes, pitch;
+};
+// t, whose entries along its first dimension are dense.
+Pieces pieces(const char *name, const at::Tensor &t) {
+    const int64_t n = t.numel() > 0 ? t.size(0) : 0, size = t.element_size();
+    return {name, (uintptr_t)t.data_ptr(), n, n ? t.numel() / n * size : 0, n ? t.stride(0) * size : 0};
+}
+Pieces whole(const char *name, const void *at, int64_t bytes) { return {name, (uintptr_t)at, at ? 1 : 0, bytes, 0}; }
+bool meet(Pieces a, Pieces b) {
+    if (a.count > b.count) std::swap(a, b);
+    if (a.count == 0 || a.bytes == 0 || b.bytes == 0) return false;
+    auto end = [](const Pieces &p) { return p.at + (p.count - 1) * p.pitch + p.bytes; };
+    if (end(a) <= b.at || end(b) <= a.at) return false;
+    for (int64_t i = 0; i < a.count; ++i) {
+        const int64_t from = (int64_t)(a.at - b.at) + i * a.pitch;  // of this piece, behind b's first
+        // b's first piece that ends behind it
+        const int64_t j = from < b.bytes ? 0 : b.count == 1 ? 1 : (from - b.bytes) / b.pitch + 1;
+        if (j < b.count && j * b.pitch < from + a.bytes) return true;
+    }
+    return false;
+}
+// Refuses memory that a call writes and that others of its tensors share:
+// some CTAs still read the one while others write the other.
+void apart(const Pieces &one, std::initializer_list<Pieces> others) {
+    for (const Pieces &o : others)
+        if (meet(one, o)) refuse(one.name, ": shares memory with ", o.name);
+}
+Pieces opt(const char *name, const at::Tensor *t) { return t ? pieces(name, *t) : Pieces{name, 0, 0, 0, 0}; }
+// The cache's own memory.
+Pieces cache_pages(const Calls &c, const char *name, const void *at) {
+    const int64_t dense = (int64_t)c.d.page * c.d.Hkv * c.d.D * 2;
+    return {name, (uintptr_t)at, at ? c.d.num_pages : 0, dense, c.d.page_stride ? c.d.page_stride * 2 : dense};
+}
+Pieces cache_k(const Calls &c) { return cache_pages(c, "the cache's k", c.k); }
+Pieces cache_v(const Calls &c) { return cache_pages(c, "the cache's v", c.v); }
+Pieces cache_mean(const Calls &c) {
+    return whole("the cache's k_mean", c.mean, (int64_t)c.d.num_pages * c.d.Hkv * c.d.D * 4);
+}
+Pieces cache_table(const Calls &c) { return whole("page_table", c.d.page_table, (int64_t)c.d.B * c.d.max_pages * 4); }
+Pieces cache_lens(const Calls &c) { return whole("seq_lens", c.d.seq_lens, (int64_t)c.d.B * 4); }
+Pieces cache_ws(const Calls &c) { return whole("the workspace", c.ws, (int64_t)c.ws_bytes); }
+
 template <typename T> T *ptr(const at::Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 
 // The call itself: f(stream) with the cache's device current.
@@ -142,6 +192,7 @@ template <typename F> PyObject *guarded(PyObject *self, Py_ssize_t given, Py_ssi
 PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     return guarded(self, n, 9, [&](Calls &c) -> PyObject * {
         if (!c.k) refuse("this cache has no k and v");
+        if (c.shared) refuse("the cache's k and v share memory");
         const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
         const at::Tensor *q = optional(a[2], "q"), *cu = optional(a[3], "cu_seqlens"), *cos = optional(a[4], "cos"),
                          *sin = optional(a[5], "sin"), *pos = optional(a[6], "positions"),
@@ -169,10 +220,17 @@ PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             if (!q) refuse("q_out without q");
             check_dense(c, "q_out", *given, c.dtype(), {T, c.d.Hq, c.d.D});
             if (T > 0 && given->data_ptr() == q->data_ptr()) refuse("q_out: must not be q");
+            apart(pieces("q_out", *given),
+                  {pieces("k", k), pieces("v", v), pieces("q", *q), opt("cu_seqlens", cu), opt("cos", cos),
+                   opt("sin", sin), opt("positions", pos), cache_k(c), cache_v(c), cache_mean(c), cache_table(c),
+                   cache_lens(c)});
             q_out = *given;
         } else if (q) {
             q_out = output(c, {T, c.d.Hq, c.d.D}, c.dtype());
         }
+        for (const Pieces &written : {cache_k(c), cache_v(c), cache_mean(c)})
+            apart(written, {pieces("k", k), pieces("v", v), opt("q", q), opt("cu_seqlens", cu), opt("cos", cos),
+                            opt("sin", sin), opt("positions", pos)});
         if (T > 0 || c.device < 0)
             run(c, "vsa_paged_append", [&](vsa_stream_t s) {
                 return c.append(&c.d, (int)T, k.data_ptr(), ks, v.data_ptr(), vs, ptr<void>(q), qs,
@@ -203,6 +261,10 @@ PyObject *calls_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (topk < 1) refuse("topk: at least one page");
         if (gi) check_dense(c, "page_idx", *gi, at::kInt, {c.d.B, c.d.Hkv, topk});
         if (gc) check_dense(c, "page_cnt", *gc, at::kInt, {c.d.B, c.d.Hkv});
+        const Pieces pi = opt("page_idx", gi), pc = opt("page_cnt", gc);
+        for (const Pieces &written : {pi, pc})
+            apart(written, {pieces("q", q), cache_mean(c), cache_table(c), cache_lens(c), cache_ws(c)});
+        apart(pi, {pc});
         at::Tensor idx = gi ? *gi : output(c, {c.d.B, c.d.Hkv, topk}, at::kInt);
         at::Tensor cnt = gc ? *gc : output(c, {c.d.B, c.d.Hkv}, at::kInt);
         run(c, "vsa_page_select", [&](vsa_stream_t s) {
@@ -232,6 +294,11 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (go) check_dense(c, "out", *go, c.dtype(), {c.d.B, c.d.Hq, c.d.D});
         if (go && go->data_ptr() == q.data_ptr()) refuse("out: must not be q");
         if (gl) check_dense(c, "lse", *gl, at::kFloat, {c.d.B, c.d.Hq});
+        const Pieces po = opt("out", go), pl = opt("lse", gl);
+        for (const Pieces &written : {po, pl})
+            apart(written, {pieces("q", q), opt("page_idx", idx), opt("page_cnt", cnt), cache_k(c), cache_v(c),
+                            cache_table(c), cache_lens(c), cache_ws(c)});
+        apart(po, {pl});
         at::Tensor out = go ? *go : output(c, {c.d.B, c.d.Hq, c.d.D}, c.dtype());
         at::Tensor lse = gl ? *gl : output(c, {c.d.B, c.d.Hq}, at::kFloat);
         run(c, "vsa_paged_attn", [&](vsa_stream_t s) {
@@ -265,6 +332,17 @@ PyObject *calls_new(PyTypeObject *type, PyObject *args, PyObject *) {
     c->attn = reinterpret_cast<decltype(c->attn)>(attn);
     Py_INCREF(fail);
     c->fail = fail;
+    c->shared = meet(cache_k(*c), cache_v(*c));
+    try {
+        apart(cache_mean(*c), {cache_k(*c), cache_v(*c)});
+        apart(cache_ws(*c), {cache_k(*c), cache_v(*c), cache_mean(*c)});
+        for (const Pieces &read : {cache_table(*c), cache_lens(*c)})
+            apart(read, {cache_k(*c), cache_v(*c), cache_mean(*c), cache_ws(*c)});
+    } catch (const Refused &e) {
+        PyErr_SetString(PyExc_ValueError, e.what());
+        Py_DECREF(self);
+        return nullptr;
+    }
     return self;
 }
 void calls_dealloc(PyObject *self) {

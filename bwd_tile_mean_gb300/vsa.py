@@ -602,7 +602,8 @@ class PagedCache:
     page_table: int32 [B, max_pages]; seq_lens: int32 [B], the tokens in the
     cache with those of the current step counted in. Both belong to the
     caller, are read by every call when it runs on the device and may be
-    shared by all layers (allocated as zeros if not given). workspace: at
+    shared by all layers (allocated as zeros if not given). Tensors that a
+    call writes may not overlap its others. workspace: at
     least ``vsa_paged_workspace_size`` bytes, 256-byte aligned, may be shared by
     caches whose calls run one after another on a stream.
     """
@@ -670,7 +671,7 @@ class PagedCache:
         L = lib()
         self._calls = _paged_binding().Calls(
             C.addressof(self.desc), self.device.index if self.device.type == "cuda" else -1, at(k), at(v), at(k_mean),
-            at(workspace), workspace.numel() * workspace.element_size(), entry(L.vsa_paged_append),
+            at(workspace), need, entry(L.vsa_paged_append),
             entry(L.vsa_page_select), entry(L.vsa_paged_attn), _check)
 
     k = property(lambda self: self._tensors[0])

@@ -529,7 +529,7 @@ size_t vsa_paged_workspace_size(const vsa_paged_desc *desc);
  *                order, divided by page. It is a function of the stored keys
  *                alone, so it does not depend on how the tokens were cut
  *                into calls, and a call made again gives the same result.
- * k, v, q and q_out must not overlap each other's or the cache's memory.
+ * q_out must not overlap k, v or q, and none of the four the cache's memory.
  * Errors: VSA_ERR_NULL, VSA_ERR_SHAPE (sizes, strides, T < 0, T != B
  * without cu_seqlens), VSA_ERR_DTYPE, VSA_ERR_LAYOUT (also misaligned
  * pointers), VSA_ERR_UNSUPPORTED (D, page, rot_dim, sizes past a limit),

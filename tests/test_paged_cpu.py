@@ -218,3 +218,68 @@ def test_select_refuses_more_entries_than_a_list_can_have(L):
         assert select(L, desc(page=page), topk=most, wsb=need - 1) == 7  # gets as far as the workspace
         assert attn(L, desc(page=page), idx=FAKE, cnt=FAKE, cap=most + 1) == 5
         assert attn(L, desc(page=page), idx=FAKE, cnt=FAKE, cap=most, wsb=need - 1) == 7
+
+
+def test_outputs_that_share_memory_are_refused(L):
+    """What a call writes may be no memory that it reads: the kernel's CTAs
+    read and write in no set order."""
+    bf, i32 = dict(dtype=torch.bfloat16), dict(dtype=torch.int32)
+    good = torch.zeros(5, 16, 2, 128, **bf)
+    ahead = torch.zeros(6, 16, 2, 128, **bf)
+    arena = torch.zeros(1 << 23, dtype=torch.uint8)
+    kk = torch.zeros(2, 2, 128, **bf)
+    for kv in (dict(k=good, v=good), dict(k=ahead[:5], v=ahead[1:]),
+               dict(k=ahead.view(-1)[:20480].view(good.shape), v=ahead.view(-1)[8:20488].view(good.shape))):
+        with pytest.raises(ValueError, match="k and v share memory"):  # good to attend to
+            cache(**kv).append(kk, kk)
+    for kw in (dict(k=good, v=good.clone(), k_mean=good.view(torch.float32).view(-1)[:1280].view(5, 2, 128)),
+               dict(k_mean=arena[:5120].view(torch.float32).view(5, 2, 128), workspace=arena),
+               dict(seq_lens=arena[4096:4104].view(torch.int32), workspace=arena)):
+        with pytest.raises(ValueError, match="shares memory"):
+            cache(**kw)
+    both = torch.zeros(5, 2, 16, 2, 128, **bf)       # halves of one buffer lie apart
+    three = torch.zeros(5, 3, 16, 2, 128, **bf)
+    for pair in ((both[:, 0], both[:, 1]), (both[:, 1], both[:, 0]), (three[:, 2], three[:, 0]), (three[:, 1], three[:, 2]),
+                 (both.view(10, 16, 2, 128)[:5], both.view(10, 16, 2, 128)[5:])):
+        c = cache(k=pair[0], v=pair[1])
+        with pytest.raises(ValueError, match="GPU only"):
+            c.append(kk, kk)
+    need = L.vsa_paged_workspace_size(C.byref(c.desc))  # an arena's first bytes, whatever lies behind them
+    big = torch.zeros(need + 64, dtype=torch.uint8)
+    cache(workspace=big, seq_lens=big[need:need + 8].view(torch.int32))
+
+    c = cache(k=both[:, 0], v=both[:, 1])
+    qkv = torch.zeros(2 * 8 + 4, 128, **bf)           # room for two tokens and a shifted view
+    rows = qkv[:16].view(2, 8, 128)
+    q, k, v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+    dense = torch.zeros(13, 128, **bf)
+    dq = dense[:8].view(2, 4, 128)
+    idx, cnt = torch.zeros(2, 2, 3, **i32), torch.zeros(2, 2, **i32)
+    lists = torch.zeros(16, **i32)
+    words = lambda t: t.view(-1).view(torch.int32)  # noqa: E731
+    for call, why in ((lambda: c.append(k, v, q, q_out=qkv[4:12].view(2, 4, 128)), "shares memory with"),
+                      (lambda: c.append(k, v, q, q_out=qkv[9:17].view(2, 4, 128)), "shares memory with"),
+                      (lambda: c.append(kk, kk, dq, q_out=dense[4:12].view(2, 4, 128)), "with q"),
+                      (lambda: c.append(kk, kk, dq, q_out=both[4, 1, 12:].view(2, 4, 128)), "with the cache's v"),
+                      (lambda: c.append(both[3, 0, :2], kk), "with k"),
+                      (lambda: c.append(kk, both[3, 1, 4:6]), "with v"),
+                      (lambda: c.select(dq, 3, page_idx=lists[:12].view(2, 2, 3), page_cnt=lists[11:15].view(2, 2)),
+                       "with page_cnt"),
+                      (lambda: c.select(dq, 3, page_idx=words(dense)[:12].view(2, 2, 3)), "with q"),
+                      (lambda: c.select(dq, 3, page_cnt=c.page_table.view(-1)[:4].view(2, 2)), "with page_table"),
+                      (lambda: c.attend(dq, out=dense[1:9].view(2, 4, 128)), "with q"),
+                      (lambda: c.attend(dq, out=both[0, 0, :4].view(2, 4, 128)), "with the cache's k"),
+                      (lambda: c.attend(dq, (idx, cnt), lse=idx.view(-1)[2:10].view(torch.float32).view(2, 4)), "page_idx"),
+                      (lambda: c.attend(dq, lse=c.workspace[64:96].view(torch.float32).view(2, 4)), "workspace"),
+                      (lambda: c.attend(dq, lse=words(dense)[480:488].view(torch.float32).view(2, 4)), "with q")):
+        with pytest.raises(ValueError, match=why):
+            call()
+    # apart: parts of one projection's output, neighbouring memory, a gap between rows
+    wide = torch.zeros(2, 24, 128, **bf)
+    for call in (lambda: c.append(k, v, q, q_out=torch.zeros(2, 4, 128, **bf)),
+                 lambda: c.append(kk, kk, wide[:, :4], q_out=wide[0, 4:12].view(2, 4, 128)),
+                 lambda: c.append(kk, kk, wide[:, 20:], q_out=wide[1, 12:20].view(2, 4, 128)),
+                 lambda: c.attend(wide[:, 2:6], out=wide[0, 6:14].view(2, 4, 128)),
+                 lambda: c.attend(dense[5:].view(2, 4, 128), lse=words(dense)[312:320].view(torch.float32).view(2, 4))):
+        with pytest.raises(ValueError, match="GPU only"):
+            call()
