@@ -14,6 +14,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -78,6 +79,8 @@ void check_kind(const Calls &c, const char *name, const at::Tensor &t, at::Scala
         refuse(name, ": expected ", dtype, " on the cache's device (", c.device < 0 ? "cpu" : "cuda:",
                c.device < 0 ? std::string() : std::to_string(c.device), "), got ", t.scalar_type(), " on ",
                t.device());
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse(name, ": the paged calls give no gradient; detach it, or call them under torch.no_grad()");
 }
 void check_dense(const Calls &c, const char *name, const at::Tensor &t, at::ScalarType dtype, at::IntArrayRef shape) {
     check_kind(c, name, t, dtype);

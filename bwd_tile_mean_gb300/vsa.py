@@ -592,7 +592,9 @@ def _paged_binding():
 
 class PagedCache:
     """One layer's paged key/value cache (the conventions of the paged calls
-    in include/vsa.h): appending, page selection, one-token attention.
+    in include/vsa.h): appending, page selection, one-token attention. The
+    calls give no gradients; tensors that require one are refused while
+    gradients are recorded.
 
     layout: "bshd" (pages [page, Hkv, D]) | "bhsd" (pages [Hkv, page, D]).
     k, v: [num_pages, ...page] tensors of dtype, dense inside a page (halves
@@ -685,6 +687,9 @@ class PagedCache:
         if t.dtype != dtype or t.device != self.device or t.shape != shape:
             raise ValueError(f"{name}: expected {dtype} {list(shape)} on {self.device}, "
                              f"got {t.dtype} {list(t.shape)} on {t.device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name}: the paged calls give no gradient; detach it, or make the cache under "
+                             "torch.no_grad()")
 
     def _on(self, stream):
         """Makes `stream` current, for a call and the outputs it allocates."""

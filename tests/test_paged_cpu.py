@@ -283,3 +283,30 @@ def test_outputs_that_share_memory_are_refused(L):
                  lambda: c.attend(dense[5:].view(2, 4, 128), lse=words(dense)[312:320].view(torch.float32).view(2, 4))):
         with pytest.raises(ValueError, match="GPU only"):
             call()
+
+
+def test_inputs_that_want_a_gradient_are_refused(L):
+    """The calls give none: outputs without a history would look trained."""
+    c = cache()
+    bf = dict(dtype=torch.bfloat16)
+    k, q = torch.zeros(2, 2, 128, **bf), torch.zeros(2, 4, 128, **bf)
+    gk, gq = (torch.zeros_like(t, requires_grad=True) for t in (k, q))
+    calls = (lambda: c.append(gk, k), lambda: c.append(k, gk), lambda: c.append(k, k, gq), lambda: c.select(gq, 2),
+             lambda: c.attend(gq))
+    for call in calls:
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+        for off in (torch.no_grad, torch.inference_mode):
+            with off(), pytest.raises(ValueError, match="GPU only"):
+                call()
+    with pytest.raises(ValueError, match="no gradient"):
+        c.append(k, k, cos=torch.zeros(9, 64, requires_grad=True), sin=torch.zeros(9, 64))
+    with pytest.raises(ValueError, match="no gradient"):
+        c.attend(q, out=torch.zeros_like(q, requires_grad=True))
+    with pytest.raises(ValueError, match="GPU only"):
+        c.attend(gq.detach())
+    pages = [torch.zeros(5, 16, 2, 128, **bf, requires_grad=True) for _ in range(2)]
+    with pytest.raises(ValueError, match="no gradient"):
+        cache(k=pages[0], v=pages[1])
+    with torch.no_grad():
+        cache(k=pages[0], v=pages[1])
