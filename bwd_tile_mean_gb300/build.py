@@ -3,7 +3,8 @@ the paged cache's Python binding beside it with the host compiler.
 
 Each translation unit compiles in its own process (in parallel) and the
 CUDA objects link into bwd_tile_mean_gb300/_build/libvsa.so. Objects are
-rebuilt when their source or any header is newer.
+rebuilt when their source or any header is newer; the binding also belongs
+to one torch and one Python.
 """
 from __future__ import annotations
 
@@ -20,7 +21,6 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libvsa.so")
-BINDING = os.path.join(OUT, "paged_binding.so")
 SOURCES = ["vsa_api.cu", "index_kernels.cu", "fwd_kernel.cu", "bwd_kernels.cu", "noalloc.cu", "tile3d.cu", "waitcheck.cu",
            "host_step.cu", "check_inputs.cu", "compress_kernels.cu", "paged_append.cu", "paged_select.cu",
            "paged_attn.cu"]
@@ -56,15 +56,23 @@ def _compile(src, verbose):
     return obj
 
 
-def _bind(verbose):
-    """paged_binding.so: a Python extension against the installed torch."""
+def binding():
+    """The paged cache's Python extension for the running Python and the
+    installed torch, whose objects it unpacks (dates alone would let the
+    binary of an earlier torch pass after a downgrade, or another Python's)."""
     import torch
-    src = os.path.join(CSRC, "paged_binding.cpp")
-    if not _stale(BINDING, [src, torch.__file__] + _headers()):
+    abi = int(torch._C._GLIBCXX_USE_CXX11_ABI)
+    return os.path.join(OUT, f"paged_binding.torch-{torch.__version__}-abi{abi}.{sysconfig.get_config_var('SOABI')}.so")
+
+
+def _bind(verbose):
+    import torch
+    src, target = os.path.join(CSRC, "paged_binding.cpp"), binding()
+    if not _stale(target, [src, torch.__file__, os.path.abspath(__file__)] + _headers()):
         return
     at = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
-    tmp = BINDING + f".{os.getpid()}.tmp"
+    tmp = target + f".{os.getpid()}.tmp"
     cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I" + INCLUDE, "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(at, "include"),
            "-I" + os.path.join(at, "include", "torch", "csrc", "api", "include"), "-I" + os.path.join(cuda, "include"),
@@ -75,13 +83,13 @@ def _bind(verbose):
         sys.stderr.write(r.stdout + r.stderr)
     if r.returncode != 0:
         raise RuntimeError("the host compiler failed on paged_binding.cpp")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, target)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     os.makedirs(OUT, exist_ok=True)
     if force:
-        for o in glob.glob(os.path.join(OUT, "*.o")) + glob.glob(BINDING):
+        for o in glob.glob(os.path.join(OUT, "*.o")) + glob.glob(os.path.join(OUT, "paged_binding.*.so")):
             os.remove(o)
     with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
         binding = ex.submit(_bind, verbose)

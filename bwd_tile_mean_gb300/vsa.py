@@ -581,9 +581,9 @@ def _paged_binding():
     """The extension module behind PagedCache's calls; raise if absent."""
     global _binding
     if _binding is None:
-        path = _build.BINDING
+        path = _build.binding()
         if not os.path.exists(path):
-            raise RuntimeError(f"paged_binding.so is not built ({path}); run __graft_entry__.build()")
+            raise RuntimeError(f"the paged cache's binding is not built ({path}); run __graft_entry__.build()")
         spec = importlib.util.spec_from_file_location("paged_binding", path)
         _binding = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(_binding)

@@ -310,3 +310,23 @@ def test_inputs_that_want_a_gradient_are_refused(L):
         cache(k=pages[0], v=pages[1])
     with torch.no_grad():
         cache(k=pages[0], v=pages[1])
+
+
+def test_binding_belongs_to_this_python_and_torch(L, monkeypatch):
+    """The binding unpacks torch's own C++ objects: another torch or another
+    Python on the same tree has one of its own, whatever the files' dates."""
+    import os
+    here = libbuild.binding()
+    assert os.path.exists(here) and os.path.samefile(vsa._paged_binding().__file__, here)
+    monkeypatch.setattr(torch, "__version__", "0.0.1+other")
+    other = libbuild.binding()
+    assert other != here
+    monkeypatch.setattr(vsa, "_binding", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        vsa._paged_binding()
+    monkeypatch.undo()
+    assert libbuild.binding() == here
+    import sysconfig
+    get = sysconfig.get_config_var
+    monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-0" if n == "SOABI" else get(n))
+    assert libbuild.binding() not in (here, other)
