@@ -616,6 +616,9 @@ class PagedCache:
             raise ValueError(f"a page's layout is bshd or bhsd, not {layout}")
         if dtype not in DTYPES:
             raise ValueError("the cache holds bf16 or fp16")
+        for name, n in dict(B=B, Hq=Hq, Hkv=Hkv, D=D, page=page, num_pages=num_pages, max_pages=max_pages).items():
+            if not 0 < n < 1 << 31:  # ctypes keeps the low 32 bits of others
+                raise ValueError(f"{name}: {n} is out of range")
         given = [t for t in (k, v, k_mean, page_table, seq_lens, workspace) if torch.is_tensor(t)]
         self.device = given[0].device if given else torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:

@@ -330,3 +330,15 @@ def test_binding_belongs_to_this_python_and_torch(L, monkeypatch):
     get = sysconfig.get_config_var
     monkeypatch.setattr(sysconfig, "get_config_var", lambda n: "cpython-0" if n == "SOABI" else get(n))
     assert libbuild.binding() not in (here, other)
+
+
+def test_cache_refuses_sizes_past_32_bits(L):
+    """The C descriptor holds 32-bit sizes; ctypes would keep the low bits."""
+    for name in ("B", "Hq", "Hkv", "D", "page", "num_pages", "max_pages"):
+        for past in (2 ** 32, -2 ** 32):
+            good = dict(B=2, Hq=4, Hkv=2, D=128, page=16, num_pages=5, max_pages=3)
+            tables = dict(page_table=torch.zeros(2, 3, dtype=torch.int32), seq_lens=torch.zeros(2, dtype=torch.int32))
+            with pytest.raises(ValueError, match=name):
+                cache(allocate=False, **tables, **{**good, name: good[name] + past})
+    with pytest.raises(ValueError, match="num_pages"):
+        cache(allocate=False, num_pages=2 ** 32 + 5)
