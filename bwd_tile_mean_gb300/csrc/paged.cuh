@@ -23,6 +23,7 @@ struct Paged {
 };
 
 constexpr int kD = 128;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr int kMaxHeads = 65536;  // key/value heads: a token's bytes stay within 32 bits
 
 // Sequence length, clamped into what the page table can hold.
@@ -50,7 +51,7 @@ inline vsa_status to_paged(const vsa_paged_desc *d, Paged *p, bool need_arrays) 
     if ((long long)d->B * d->Hq > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
     const long long dense = (long long)d->page * d->Hkv * kD;
     if (d->page_stride != 0 && (d->page_stride < dense || d->page_stride % 8 != 0)) return VSA_ERR_SHAPE;
-    if (!(d->scale >= 0.f) || std::isinf(d->scale)) return VSA_ERR_SHAPE;
+    if (!(d->scale >= 0.f) || std::isinf(d->scale * kLog2e)) return VSA_ERR_SHAPE;
     if (need_arrays) {
         if (!d->page_table || !d->seq_lens) return VSA_ERR_NULL;
         if (((uintptr_t)d->page_table | (uintptr_t)d->seq_lens) & 3u) return VSA_ERR_LAYOUT;

@@ -63,7 +63,6 @@ constexpr int kCtas = 304;      // two per SM on 152 SMs
 constexpr int kStageBytes = 2 * kBlk * 256;  // the K or the V rows of a step
 constexpr int kPitch = 136;     // floats per row of the warps' outputs in shared memory
 constexpr int kSmem = kWarps * kStages * kStageBytes;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct AttnArgs {
     Paged p;

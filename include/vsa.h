@@ -488,7 +488,7 @@ typedef struct {
     int64_t page_stride;  /* elements between pages, a multiple of 8; 0: dense (page * Hkv * D) */
     const int32_t *page_table; /* device [B, max_pages] */
     const int32_t *seq_lens;   /* device [B] */
-    float scale;          /* softmax scale on q.k; 0 means 1/sqrt(D) */
+    float scale;          /* softmax scale on q.k, below 2.3e38; 0 means 1/sqrt(D) */
 } vsa_paged_desc;
 
 /* Bytes of workspace for vsa_page_select and vsa_paged_attn on this problem

@@ -342,3 +342,12 @@ def test_cache_refuses_sizes_past_32_bits(L):
                 cache(allocate=False, **tables, **{**good, name: good[name] + past})
     with pytest.raises(ValueError, match="num_pages"):
         cache(allocate=False, num_pages=2 ** 32 + 5)
+
+
+@pytest.mark.parametrize("scale,fine", [(2.3e38, True), (2.4e38, False), (3.4e38, False)])
+def test_scale_whose_log2_multiple_overflows_is_refused(L, scale, fine):
+    """Weights are powers of two: scale * log2(e) infinite times the largest
+    score's distance 0 from itself would be NaN."""
+    need = L.vsa_paged_workspace_size(C.byref(desc(scale=scale)))
+    assert (need > 0) == fine
+    assert attn(L, desc(scale=scale), wsb=0) == (7 if fine else 2)
