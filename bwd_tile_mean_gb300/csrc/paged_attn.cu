@@ -10,7 +10,12 @@
 // common error in O (9,001 keys, scores 0 and -0.69, V = 1: 0.996 in bf16, and
 // +inf in fp16 for V = 65504). What remains is u sum_u p_u |v_u - O|, u half a
 // step of the type. The sum of the W_u comes from the same instruction, as the
-// product with a column of ones: two more of a step's 64.
+// product with a column of ones: two more of a step's 64 (no time measured).
+// The product of what the rounding leaves, P - W, would take 32 more: the error
+// of random outputs falls from 1.1 to 1.2 times that of rounding them once to
+// 1.0, and 16 sequences of up to 9,000 keys with 16 heads each go from 18.6 to
+// 20.5 us, 64 of up to 16,000 from 83.7 to 84.9, 24 heads of 122,880 keys stay at
+// 217; and 0 * inf would be NaN where an infinite value is attended. Not done.
 //
 // A segment is one (sequence, key/value head, chunk of up to 16 query heads
 // of its group: one tile of the tensor instructions; a wider group's chunks
@@ -839,9 +844,11 @@ extern "C" vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, 
     const long long most = page_idx ? std::min((long long)idx_cap * a.p.page, (long long)a.p.max_len) : a.p.max_len;
     // One cluster per segment, its CTAs doubled while all of the clusters find a place at once and the keys are many
     // enough (grows()). Segments of one length (one sequence, or page lists) are then balanced by themselves; of
-    // unknown lengths only while the longest stays short. Measured (us, clusters / runs): 400 keys x 14 heads 4.4 /
-    // 8.2, x 400 19.5 / 21.8, x 1,600 61.6 / 60.9; 4,000 x 8 6.9 / 9.6, 64,000 x 24 116 / 124, 64,000 x 1 34 / 13.6; 16
-    // sequences of 1,000 to 9,000 keys x 2 heads 18.8 / 21.1, 64 of 37 to 16,000 x 8 151 / 84.
+    // unknown lengths only while the longest stays short: the table's width stands for it, so that short sequences in a
+    // wide table go to runs too (101 keys x 3 heads 3.2 us, in a table for 131,072 keys 7.2). Measured (us, clusters /
+    // runs): 400 keys x 14 heads 4.4 / 8.2, x 400 19.5 / 21.8, x 1,600 61.6 / 60.9; 4,000 x 8 6.9 / 9.6, 64,000 x 24
+    // 116 / 124, 64,000 x 1 34 / 13.6; 16 sequences of 1,000 to 9,000 keys x 2 heads 18.8 / 21.1, 64 of 37 to 16,000 x
+    // 8 151 / 84.
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
     int cluster = 1;
     while (cluster < kMaxCluster && grows(cluster, segments, most)) cluster *= 2;

@@ -607,7 +607,9 @@ class PagedCache:
     shared by all layers (allocated as zeros if not given). Tensors that a
     call writes may not overlap its others. workspace: at
     least ``vsa_paged_workspace_size`` bytes, 256-byte aligned, may be shared by
-    caches whose calls run one after another on a stream.
+    caches whose calls run one after another on a stream: the layers of a
+    model pass on the first one's, of up to 21 MB and the scores, instead of
+    allocating one each.
     """
 
     def __init__(self, layout, dtype, B, Hq, Hkv, D, page, num_pages, max_pages, k=None, v=None, k_mean=None,
@@ -705,7 +707,9 @@ class PagedCache:
         """vsa_paged_append: k, v [T, Hkv, D] (and q [T, Hq, D]) of the new
         tokens, which seq_lens already counts; cu_seqlens int32 [B+1], None
         for one token per sequence. cos, sin: fp32 [rows, rot_dim / 2], None
-        for no rotation. Returns the rotated q (None without q)."""
+        for no rotation. Returns the rotated q (None without q); the rows of
+        tokens without a place (of an unused sequence, or behind the last one)
+        are not written: zeros only where the q_out given held them."""
         if stream is not None:
             with self._on(stream):
                 return self._calls.append(k, v, q, cu_seqlens, cos, sin, positions, interleaved, q_out)
@@ -713,7 +717,8 @@ class PagedCache:
 
     def select(self, q, topk, keep_first=0, keep_last=1, page_idx=None, page_cnt=None, stream=None):
         """vsa_page_select: the pages that q [B, Hq, D] attends to, as
-        (page_idx int32 [B, Hkv, topk], page_cnt int32 [B, Hkv])."""
+        (page_idx int32 [B, Hkv, topk], page_cnt int32 [B, Hkv]): one list for
+        the query heads of a group, by the sum of their queries."""
         if stream is not None:
             with self._on(stream):
                 return self._calls.select(q, topk, keep_first, keep_last, page_idx, page_cnt)

@@ -551,7 +551,9 @@ vsa_status vsa_paged_append(const vsa_paged_desc *desc, int T, const void *k, in
  * (2i, 2i + 1) until one is left. NaN counts as -inf. The first keep_first
  * (>= 0) and the last keep_last (>= 1) of the ceil(len / page) pages are
  * always chosen (a partial last page has no mean and is always among
- * them); the rest of min(topk, pages) by (r desc, j asc).
+ * them); the rest of min(topk, pages) by (r desc, j asc). The query heads of
+ * a group share their key/value head's list; vsa_build_block_map scores and
+ * lists for each query head, so the two choose alike where Hq == Hkv.
  * Writes page_idx [B, Hkv, topk] int32, ascending, unused entries -1, and
  * page_cnt [B, Hkv]. topk >= keep_first + keep_last, topk * page < 2^31. The
  * result is the same bit for bit on every run. Errors as for vsa_paged_append, and
@@ -561,14 +563,14 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
                            void *workspace, size_t workspace_bytes, vsa_stream_t stream);
 
 /* Attention of one token per sequence over the cache: q [B, Hq, D]
- * (q_stride as above), out [B, Hq, D] dense (not q's memory), lse fp32
- * [B, Hq] (natural log). With page_idx == NULL every token of the sequence
+ * (q_stride as above), out [B, Hq, D] dense, lse fp32 [B, Hq]
+ * (natural log), neither in memory that the call reads. With page_idx == NULL every token of the sequence
  * is attended; otherwise the tokens of the pages page_idx [B, Hkv, idx_cap]
  * lists for the query head's key/value head, page_cnt [B, Hkv] of them (a
  * page listed twice counts twice). A row without keys, or whose scores are all -inf,
  * gets O = 0, LSE = -inf. The softmax and its sums are fp32; the weights are
  * rounded to dtype for the product with V, and O is divided by their sum as
- * rounded, so O stays within the values it averages. The work
+ * rounded: the weights that O is made with sum to one. The work
  * of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
  * bit on every run with the same batch. Errors as for vsa_page_select;
