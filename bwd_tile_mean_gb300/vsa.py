@@ -609,7 +609,9 @@ class PagedCache:
     least ``vsa_paged_workspace_size`` bytes, 256-byte aligned, may be shared by
     caches whose calls run one after another on a stream: the layers of a
     model pass on the first one's, of up to 21 MB and the scores, instead of
-    allocating one each.
+    allocating one each. As in the rest of this module, tensors used on a
+    stream other than the one they were allocated on, a cache's own among
+    them, are kept alive by the caller until that stream is done with them.
     """
 
     def __init__(self, layout, dtype, B, Hq, Hkv, D, page, num_pages, max_pages, k=None, v=None, k_mean=None,
