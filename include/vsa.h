@@ -564,14 +564,15 @@ vsa_status vsa_page_select(const vsa_paged_desc *desc, const void *q, int64_t q_
 
 /* Attention of one token per sequence over the cache: q [B, Hq, D]
  * (q_stride as above), out [B, Hq, D] dense, lse fp32 [B, Hq]
- * (natural log), neither in memory that the call reads. With page_idx == NULL every token of the sequence
- * is attended; otherwise the tokens of the pages page_idx [B, Hkv, idx_cap]
+ * (natural log), neither in memory that the call reads. With page_idx ==
+ * NULL every token of the sequence is attended; otherwise the tokens of the pages page_idx [B, Hkv, idx_cap]
  * lists for the query head's key/value head, page_cnt [B, Hkv] of them (a
  * page listed twice counts twice). A row without keys, or whose scores are all -inf,
  * gets O = 0, LSE = -inf. The softmax and its sums are fp32; the weights are
  * rounded to dtype for the product with V, and O is divided by their sum as
- * rounded: the weights that O is made with sum to one. The work
- * of the batch is cut into equal pieces whatever its lengths, and pieces
+ * rounded: the weights that O is made with sum to one (fp16 keeps weights
+ * down to 2^-40 of the largest; an infinite value with a smaller one gives
+ * NaN). The work of the batch is cut into equal pieces whatever its lengths, and pieces
  * of one row are joined in ascending order: the result is the same bit for
  * bit on every run with the same batch. Errors as for vsa_page_select;
  * VSA_ERR_NULL for half a page list, VSA_ERR_SHAPE for idx_cap < 1,
