@@ -1,4 +1,4 @@
-// paged_binding.cpp -- the hot side of vsa.PagedCache: checks the tensors of
+// paged_binding.cpp -- the hot side of vsa.PagedCache and vsa.AxialRope: checks the tensors of
 // a call, allocates its outputs and passes their pointers on to the C entry
 // points, for the decode step whose kernels take a few microseconds. The same
 // in Python (checks, two torch.empty, a ctypes call) took 12.7 us for
@@ -10,7 +10,9 @@
 // addresses of vsa_paged_append, vsa_page_select and vsa_paged_attn, fail a
 // callable (name, status) that raises. The tensors behind the addresses are
 // kept alive by the owner. Calls run on the current stream of the cache's
-// device, with that device current.
+// device, with that device current. Type Rope(rope, functions, fail): rope is
+// the address of a vsa_rope (copied), functions those of vsa_rope_apply and
+// vsa_rope_table; calls run on the device of their tensors.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
@@ -174,14 +176,14 @@ template <typename F> void run(const Calls &c, const char *name, F f) {
 
 // Runs a method body; refused arguments become ValueError, torch's errors
 // what torch makes of them. No exception leaves.
-template <typename F> PyObject *guarded(PyObject *self, Py_ssize_t given, Py_ssize_t wanted, F f) {
+template <typename C = Calls, typename F> PyObject *guarded(PyObject *self, Py_ssize_t given, Py_ssize_t wanted, F f) {
     HANDLE_TH_ERRORS
     if (given != wanted) {
         PyErr_Format(PyExc_TypeError, "expected %zd arguments, got %zd", wanted, given);
         return nullptr;
     }
     try {
-        return f(*reinterpret_cast<Calls *>(self));
+        return f(*reinterpret_cast<C *>(self));
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
         return nullptr;
@@ -348,9 +350,236 @@ PyObject *calls_new(PyTypeObject *type, PyObject *args, PyObject *) {
     }
     return self;
 }
-void calls_dealloc(PyObject *self) {
+struct Rope {
+    PyObject_HEAD;
+    vsa_rope r;
+    decltype(&vsa_rope_apply) apply;
+    decltype(&vsa_rope_table) table;
+    PyObject *fail;
+};
+
+// A tensor of tokens as vsa_rope_apply takes it: sizes and strides of batch
+// entries, tokens and heads (strides of dimensions of one entry are 0).
+struct Tokens {
+    const char *name;
+    char *at;
+    int64_t size, n[3], stride[3];  // element size; batch, tokens, heads
+    int64_t last() const {          // bytes from the first element to behind the last
+        int64_t e = 128;
+        for (int i = 0; i < 3; ++i) e += (n[i] - 1) * stride[i];
+        return e * size;
+    }
+};
+enum { kBhsd = 0, kBshd = 1, kTnd = 2 };
+Tokens tokens(const char *name, const at::Tensor &t, int layout) {
+    const int64_t dims = layout == kTnd ? 3 : 4;
+    if (t.dim() != dims || t.size(dims - 1) != 128)
+        refuse(name, ": expected ", layout == kTnd ? "[T, H, 128]" : layout == kBshd ? "[B, S, H, 128]" : "[B, H, S, 128]",
+               ", got ", t.sizes());
+    const int64_t order[3][3] = {{0, 2, 1}, {0, 1, 2}, {-1, 0, 1}};
+    Tokens k{name, static_cast<char *>(t.data_ptr()), (int64_t)t.element_size(), {}, {}};
+    if (t.numel() > 0 && t.stride(dims - 1) != 1) refuse(name, ": the last dimension must be dense");
+    for (int i = 0; i < 3; ++i) {
+        const int64_t d = order[layout][i];
+        k.n[i] = d < 0 ? 1 : t.size(d);
+        k.stride[i] = k.n[i] > 1 ? t.stride(d) : 0;
+        if (k.stride[i] % 8 != 0) refuse(name, ": strides must be multiples of 8 elements");
+    }
+    return k;
+}
+bool empty(const Tokens &t) { return t.n[0] == 0 || t.n[1] == 0 || t.n[2] == 0; }
+bool same_place(const Tokens &a, const Tokens &b) {
+    bool same = a.at == b.at;
+    for (int i = 0; i < 3; ++i) same = same && a.n[i] == b.n[i] && a.stride[i] == b.stride[i];
+    return same;
+}
+// Whether the rows of `t` are known to be apart from each other.
+bool rows_apart(const Tokens &t) {
+    int at[3] = {0, 1, 2};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 3; ++j)
+            if (t.stride[at[j]] < t.stride[at[i]]) std::swap(at[i], at[j]);
+    int64_t reach = 128;  // elements of the dimensions so far
+    for (int i : at) {
+        if (t.n[i] < 2) continue;
+        if (t.stride[i] < reach) return false;
+        reach = (t.n[i] - 1) * t.stride[i] + reach;
+    }
+    return true;
+}
+// Whether a and b are known to share no memory: apart as a whole, or heads
+// side by side in the same rows of one buffer, as the parts of a projection's
+// output are.
+bool are_apart(const Tokens &a, const Tokens &b) {
+    if (empty(a) || empty(b) || a.at + a.last() <= b.at || b.at + b.last() <= a.at) return true;
+    auto dense = [](const Tokens &t) { return t.n[2] < 2 || t.stride[2] == 128; };
+    const int64_t row = a.n[1] > 1 ? a.stride[1] : a.stride[0];
+    if (!dense(a) || !dense(b) || row <= 0 || a.n[0] != b.n[0] || a.n[1] != b.n[1] || a.stride[0] != b.stride[0] ||
+        a.stride[1] != b.stride[1] || a.stride[0] % row != 0)
+        return false;
+    const int64_t pitch = row * a.size;
+    int64_t rel = (b.at - a.at) % pitch;
+    if (rel < 0) rel += pitch;
+    return rel >= a.n[2] * 128 * a.size && rel + b.n[2] * 128 * b.size <= pitch;
+}
+void same_device(const at::Tensor &first, const char *name, const at::Tensor &t, at::ScalarType dtype) {
+    if (t.scalar_type() != dtype || t.device() != first.device() || t.layout() != at::kStrided)
+        refuse(name, ": expected ", dtype, " on ", first.device(), ", got ", t.scalar_type(), " on ", t.device());
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        refuse(name, ": the call records no gradient; use backward() for it, and call both under torch.no_grad()");
+}
+// The call itself, with the tensors' device current.
+template <typename F> void run_at(const Rope &r, const at::Tensor &first, const char *name, F f) {
+    if (!first.is_cuda()) refuse("the tensors are on ", first.device(), ": the calls run on a GPU only");
+    const c10::cuda::CUDAGuard guard(first.device());
+    const vsa_status st = f(static_cast<vsa_stream_t>(c10::cuda::getCurrentCUDAStream(first.get_device()).stream()));
+    if (st != VSA_OK) {
+        PyObject *x = PyObject_CallFunction(r.fail, "si", name, (int)st);
+        Py_XDECREF(x);
+        if (!PyErr_Occurred()) PyErr_Format(PyExc_RuntimeError, "%s failed: %d", name, (int)st);
+        throw Raised();
+    }
+}
+// Positions [S, axes] or [B, S, axes]: strides between batch entries and tokens.
+struct Positions {
+    const int32_t *at;
+    int64_t batch, token;
+};
+Positions positions_of(const Rope &r, const at::Tensor &t, int64_t B, int64_t S, bool batched) {
+    const int64_t d = t.dim();
+    if (!(d == 2 || (batched && d == 3)) || t.size(d - 1) != r.r.n_axes || t.size(d - 2) != S || (d == 3 && t.size(0) != B))
+        refuse("positions: expected ", batched ? "[S, axes] or [B, S, axes]" : "[T, axes]", " of ", B, " x ", S,
+               " tokens and ", r.r.n_axes, " axes, got ", t.sizes());
+    if (t.numel() > 0 && r.r.n_axes > 1 && t.stride(d - 1) != 1) refuse("positions: a token's must be dense");
+    return {static_cast<int32_t *>(t.data_ptr()), d == 3 && B > 1 ? t.stride(0) : 0, S > 1 ? t.stride(d - 2) : 0};
+}
+Tokens as_tokens(const at::Tensor &t, const char *name) {  // a dense or strided small tensor as one piece of memory
+    int64_t last = t.numel() > 0 ? 1 : 0;
+    for (int64_t i = 0; i < t.dim() && last; ++i) last += (t.size(i) - 1) * t.stride(i);
+    Tokens k{name, static_cast<char *>(t.data_ptr()), 1, {last ? 1 : 0, 1, 1}, {}};
+    k.n[1] = last * (int64_t)t.element_size();  // bytes as tokens one byte apart
+    k.stride[1] = 1;
+    return k;
+}
+
+// apply(q, k, positions, layout, q_out, k_out, inverse)
+PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return guarded<Rope>(self, n, 7, [&](Rope &r) -> PyObject * {
+        const at::Tensor &q = tensor(a[0], "q"), &pos = tensor(a[2], "positions");
+        const at::Tensor *k = optional(a[1], "k"), *qo = optional(a[4], "q_out"), *ko = optional(a[5], "k_out");
+        const long layout = integer(a[3], "layout");
+        const int inverse = PyObject_IsTrue(a[6]);
+        if (inverse < 0) throw Raised();
+        if (layout < 0 || layout > 2) refuse("layout: bshd, bhsd or tnd");
+        if (ko && !k) refuse("k_out without k");
+        if (q.scalar_type() != at::kBFloat16 && q.scalar_type() != at::kHalf)
+            refuse("q: expected bfloat16 or float16, got ", q.scalar_type());
+        const at::ScalarType dtype = q.scalar_type();
+        same_device(q, "q", q, dtype);
+        same_device(q, "positions", pos, at::kInt);
+        Tokens x[2] = {tokens("q", q, layout)};
+        const int64_t B = x[0].n[0], S = x[0].n[1];
+        if (k) {
+            same_device(q, "k", *k, dtype);
+            x[1] = tokens("k", *k, layout);
+            if (x[1].n[0] != B || x[1].n[1] != S) refuse("k: expected as many tokens as q, got ", k->sizes());
+        }
+        for (int i = 0; i < (k ? 2 : 1); ++i)
+            if (B > INT32_MAX || S > INT32_MAX || x[i].n[2] > INT32_MAX) refuse(x[i].name, ": too large");
+        const Positions p = positions_of(r, pos, B, S, layout != kTnd);
+        const int count = k ? 2 : 1;
+        at::Tensor out[2];
+        Tokens y[2];
+        const at::Tensor *in[2] = {&q, k}, *given[2] = {qo, ko};
+        for (int i = 0; i < count; ++i) {
+            const char *name = i ? "k_out" : "q_out";
+            if (given[i]) {
+                same_device(q, name, *given[i], dtype);
+                if (given[i]->sizes() != in[i]->sizes()) refuse(name, ": expected ", in[i]->sizes(), ", got ", given[i]->sizes());
+                out[i] = *given[i];
+            } else {
+                out[i] = at::empty(in[i]->sizes(), in[i]->options().memory_format(c10::nullopt));
+            }
+            y[i] = tokens(name, out[i], layout);
+            if (!given[i]) continue;
+            if (!empty(y[i]) && !rows_apart(y[i])) refuse(name, ": its rows share memory");
+            for (int j = 0; j < count; ++j)
+                if (!(i == j && same_place(y[i], x[j])) && !are_apart(y[i], x[j])) refuse(name, ": shares memory with ", x[j].name);
+            const char *first = y[i].at, *end = first + (empty(y[i]) ? 0 : y[i].last());
+            const Tokens m = as_tokens(pos, "positions");
+            if (!empty(m) && !empty(y[i]) && m.at < end && first < m.at + m.n[1]) refuse(name, ": shares memory with positions");
+        }
+        if (count == 2 && !are_apart(y[0], y[1])) refuse("q_out: shares memory with k_out");
+        // a tensor without heads has no part in the call
+        vsa_rope_tensor t[2];
+        int used = 0;
+        for (int i = 0; i < count; ++i)
+            if (!empty(x[i]))
+                t[used++] = {x[i].at,        y[i].at,        (int32_t)x[i].n[2], x[i].stride[0], x[i].stride[1],
+                             x[i].stride[2], y[i].stride[0], y[i].stride[1],     y[i].stride[2]};
+        if (used)
+            run_at(r, q, "vsa_rope_apply", [&](vsa_stream_t s) {
+                return r.apply(&r.r, dtype == at::kBFloat16 ? VSA_DTYPE_BF16 : VSA_DTYPE_FP16, (int)B, (int)S, 128, t, used,
+                               p.at, p.batch, p.token, inverse, s);
+            });
+        if (!k) return THPVariable_Wrap(std::move(out[0]));
+        return pair(std::move(out[0]), std::move(out[1]));
+    });
+}
+
+// table(positions, cos, sin)
+PyObject *rope_table(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return guarded<Rope>(self, n, 3, [&](Rope &r) -> PyObject * {
+        const at::Tensor &pos = tensor(a[0], "positions");
+        const at::Tensor *gc = optional(a[1], "cos"), *gs = optional(a[2], "sin");
+        same_device(pos, "positions", pos, at::kInt);
+        const int64_t T = pos.dim() == 2 ? pos.size(0) : 0, pairs = r.r.rot_dim / 2;
+        const Positions p = positions_of(r, pos, 1, T, false);
+        if (T > INT32_MAX) refuse("positions: too many tokens");
+        at::Tensor out[2];
+        const at::Tensor *given[2] = {gc, gs};
+        for (int i = 0; i < 2; ++i) {
+            const char *name = i ? "sin" : "cos";
+            if (given[i]) {
+                same_device(pos, name, *given[i], at::kFloat);
+                if (given[i]->sizes() != at::IntArrayRef({T, pairs}) || !given[i]->is_contiguous())
+                    refuse(name, ": expected a contiguous [", T, ", ", pairs, "], got ", given[i]->sizes());
+                out[i] = *given[i];
+            } else {
+                out[i] = at::empty({T, pairs}, pos.options().dtype(at::kFloat));
+            }
+        }
+        const Tokens m = as_tokens(pos, "positions");
+        const Pieces mine = whole("positions", m.at, m.n[0] ? m.n[1] : 0);
+        apart(pieces("cos", out[0]), {mine, pieces("sin", out[1])});
+        apart(pieces("sin", out[1]), {mine});
+        if (T > 0)
+            run_at(r, pos, "vsa_rope_table", [&](vsa_stream_t s) {
+                return r.table(&r.r, (int)T, p.at, p.token, static_cast<float *>(out[0].data_ptr()),
+                               static_cast<float *>(out[1].data_ptr()), s);
+            });
+        return pair(std::move(out[0]), std::move(out[1]));
+    });
+}
+
+// Rope(rope, apply, table, fail)
+PyObject *rope_new(PyTypeObject *type, PyObject *args, PyObject *) {
+    unsigned long long rope, apply, table;
+    PyObject *fail;
+    if (!PyArg_ParseTuple(args, "KKKO", &rope, &apply, &table, &fail)) return nullptr;
+    PyObject *self = type->tp_alloc(type, 0);
+    if (!self) return nullptr;
+    Rope *r = reinterpret_cast<Rope *>(self);
+    r->r = *reinterpret_cast<const vsa_rope *>(rope);
+    r->apply = reinterpret_cast<decltype(r->apply)>(apply);
+    r->table = reinterpret_cast<decltype(r->table)>(table);
+    Py_INCREF(fail);
+    r->fail = fail;
+    return self;
+}
+template <typename C> void drop(PyObject *self) {
     PyTypeObject *type = Py_TYPE(self);
-    Py_XDECREF(reinterpret_cast<Calls *>(self)->fail);
+    Py_XDECREF(reinterpret_cast<C *>(self)->fail);
     type->tp_free(self);
     Py_DECREF(type);
 }
@@ -366,11 +595,23 @@ PyMethodDef methods[] = {
 };
 PyType_Slot slots[] = {
     {Py_tp_new, reinterpret_cast<void *>(calls_new)},
-    {Py_tp_dealloc, reinterpret_cast<void *>(calls_dealloc)},
+    {Py_tp_dealloc, reinterpret_cast<void *>(drop<Calls>)},
     {Py_tp_methods, methods},
     {0, nullptr},
 };
 PyType_Spec spec = {"paged_binding.Calls", sizeof(Calls), 0, Py_TPFLAGS_DEFAULT, slots};
+PyMethodDef rope_methods[] = {
+    {"apply", fast(rope_apply), METH_FASTCALL, "vsa_rope_apply"},
+    {"table", fast(rope_table), METH_FASTCALL, "vsa_rope_table"},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyType_Slot rope_slots[] = {
+    {Py_tp_new, reinterpret_cast<void *>(rope_new)},
+    {Py_tp_dealloc, reinterpret_cast<void *>(drop<Rope>)},
+    {Py_tp_methods, rope_methods},
+    {0, nullptr},
+};
+PyType_Spec rope_spec = {"paged_binding.Rope", sizeof(Rope), 0, Py_TPFLAGS_DEFAULT, rope_slots};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "paged_binding", nullptr, -1, nullptr, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
@@ -378,11 +619,13 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "paged_binding", nullptr, -1, nullp
 PyMODINIT_FUNC PyInit_paged_binding() {
     PyObject *m = PyModule_Create(&module);
     if (!m) return nullptr;
-    PyObject *t = PyType_FromSpec(&spec);
-    if (!t || PyModule_AddObject(m, "Calls", t) < 0) {
-        Py_XDECREF(t);
-        Py_DECREF(m);
-        return nullptr;
+    for (auto [name, from] : {std::pair{"Calls", &spec}, std::pair{"Rope", &rope_spec}}) {
+        PyObject *t = PyType_FromSpec(from);
+        if (!t || PyModule_AddObject(m, name, t) < 0) {
+            Py_XDECREF(t);
+            Py_DECREF(m);
+            return nullptr;
+        }
     }
     return m;
 }

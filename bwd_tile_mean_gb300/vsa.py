@@ -36,7 +36,8 @@ EXPORTS = ("vsa_workspace_size", "vsa_build_block_map", "vsa_build_block_map_sta
            "vsa_mask_to_index_blocks", "vsa_fwd_blocks", "vsa_bwd_blocks", "vsa_check_wait_timeout",
            "vsa_train_step_host_size", "vsa_train_step_host", "vsa_fwd_step_host", "vsa_step_host_status",
            "vsa_check_inputs", "vsa_head_slice", "vsa_fwd_reuse", "vsa_bwd_reuse",
-           "vsa_paged_workspace_size", "vsa_paged_append", "vsa_page_select", "vsa_paged_attn")
+           "vsa_paged_workspace_size", "vsa_paged_append", "vsa_page_select", "vsa_paged_attn",
+           "vsa_rope_init", "vsa_rope_apply", "vsa_rope_table")
 
 REUSE_QK_MEANS, REUSE_V_MEANS = 1, 2  # vsa_fwd_reuse / vsa_bwd_reuse mask bits
 
@@ -62,6 +63,17 @@ class PagedDesc(C.Structure):
                 ("Hkv", C.c_int32), ("D", C.c_int32), ("page", C.c_int32), ("num_pages", C.c_int32),
                 ("max_pages", C.c_int32), ("page_stride", C.c_int64), ("page_table", C.c_void_p),
                 ("seq_lens", C.c_void_p), ("scale", C.c_float)]
+
+
+class RopeDesc(C.Structure):
+    _fields_ = [("n_axes", C.c_int32), ("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("axis", C.c_uint8 * 64),
+                ("turn", C.c_uint64 * 64)]
+
+
+class RopeTensor(C.Structure):
+    _fields_ = [("x", C.c_void_p), ("y", C.c_void_p), ("heads", C.c_int32), ("x_batch", C.c_int64),
+                ("x_token", C.c_int64), ("x_head", C.c_int64), ("y_batch", C.c_int64), ("y_token", C.c_int64),
+                ("y_head", C.c_int64)]
 
 
 _lib = None
@@ -159,6 +171,13 @@ def lib():
                                       P]
         L.vsa_paged_attn.restype = C.c_int
         L.vsa_paged_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
+        L.vsa_rope_init.restype = C.c_int
+        L.vsa_rope_init.argtypes = [C.POINTER(RopeDesc), C.c_int, C.c_int, C.c_int, P, P]
+        L.vsa_rope_apply.restype = C.c_int
+        L.vsa_rope_apply.argtypes = [C.POINTER(RopeDesc), C.c_int, C.c_int, C.c_int, C.c_int, C.POINTER(RopeTensor),
+                                     C.c_int, P, i64, i64, C.c_int, P]
+        L.vsa_rope_table.restype = C.c_int
+        L.vsa_rope_table.argtypes = [C.POINTER(RopeDesc), C.c_int, P, i64, P, P, P]
         _lib = L
     return _lib
 
@@ -561,6 +580,105 @@ def untile_3d(tiled: torch.Tensor, grid, tile=(4, 8, 8), out=None, stream=None):
     _check("vsa_untile_3d", lib().vsa_untile_3d(B, T, H, W, row_bytes, *tile, _p(tiled), _p(out),
                                                 _stream(stream)))
     return out
+
+
+# ---------------------------------------------- rotary positions, several axes
+
+class AxialRope:
+    """Rotary positions with several axes (include/vsa.h): queries and keys of
+    image and video tokens, turned by their frame, row and column.
+
+    dims: rotated dims of each axis (even; together a multiple of 16, up to
+    128). The head's pairs, (2i, 2i + 1) when interleaved, else (i, i +
+    rot_dim / 2), go to the axes in this order; pair j of an axis of n dims
+    turns by base ** (-2 j / n) * scale radians per step of the axis (scale: a
+    number, or one per axis, e.g. the ratio of two frame rates). freqs: the
+    radians per step of every pair instead, at most 1024 each; axes: the axis
+    of every pair, instead of the order of dims.
+
+    The calls run on the device of their tensors, with the rules for streams of
+    the rest of this module. They record no gradient (tensors that require one
+    are refused while gradients are recorded): backward() gives it.
+    """
+
+    def __init__(self, dims, base=10000.0, scale=1.0, interleaved=False, freqs=None, axes=None):
+        dims = [int(n) for n in dims]
+        if not 1 <= len(dims) <= 4 or any(n < 0 or n % 2 for n in dims):
+            raise ValueError(f"dims: even numbers for 1 to 4 axes, not {dims}")
+        self.dims, self.rot_dim, self.interleaved = tuple(dims), sum(dims), bool(interleaved)
+        pairs = self.rot_dim // 2
+        if self.rot_dim % 16 or not 0 < self.rot_dim <= 128:
+            raise ValueError(f"dims: their sum must be a multiple of 16 up to 128, not {self.rot_dim}")
+        scales = [float(scale)] * len(dims) if isinstance(scale, (int, float)) else [float(x) for x in scale]
+        if len(scales) != len(dims):
+            raise ValueError("scale: a number, or one for each axis")
+        if freqs is None:
+            if not base > 0:
+                raise ValueError(f"base: must be positive, not {base}")
+            freqs = [float(base) ** (-2.0 * j / n) * x for n, x in zip(dims, scales) for j in range(n // 2)]
+        elif any(x != 1.0 for x in scales):
+            raise ValueError("scale: freqs hold it already")
+        if axes is None:
+            axes = [a for a, n in enumerate(dims) for _ in range(n // 2)]
+        freqs, axes = [float(f) for f in freqs], [int(a) for a in axes]
+        if len(freqs) != pairs or len(axes) != pairs:
+            raise ValueError(f"freqs, axes: one for each of the {pairs} pairs")
+        if not all(abs(f) <= 1024 for f in freqs) or not all(0 <= a < len(dims) for a in axes):
+            raise ValueError("freqs: at most 1024 radians per step; axes: those of dims")
+        self.freqs, self.axes = tuple(freqs), tuple(axes)
+        self.desc = RopeDesc()
+        L = lib()
+        _check("vsa_rope_init", L.vsa_rope_init(C.byref(self.desc), len(dims), self.rot_dim, int(self.interleaved),
+                                                (C.c_int32 * pairs)(*axes), (C.c_double * pairs)(*freqs)))
+        entry = lambda f: C.cast(f, C.c_void_p).value  # noqa: E731
+        self._calls = _paged_binding().Rope(C.addressof(self.desc), entry(L.vsa_rope_apply), entry(L.vsa_rope_table),
+                                            _check)
+
+    def _apply(self, q, k, positions, layout, q_out, k_out, stream, inverse):
+        if layout not in LAYOUTS:
+            raise ValueError(f"layout: bshd, bhsd or tnd, not {layout}")
+        if stream is not None:
+            if torch.is_tensor(q) and stream.device != q.device:
+                raise ValueError(f"stream: expected one of {q.device}, got {stream.device}")
+            with torch.cuda.stream(stream):
+                return self._calls.apply(q, k, positions, LAYOUTS[layout], q_out, k_out, inverse)
+        return self._calls.apply(q, k, positions, LAYOUTS[layout], q_out, k_out, inverse)
+
+    def forward(self, q, k=None, positions=None, layout="bshd", q_out=None, k_out=None, stream=None):
+        """vsa_rope_apply: q and k (or q alone) of one set of tokens, "bshd"
+        [B, S, H, 128], "bhsd" [B, H, S, 128] or "tnd" [T, H, 128], rotated by
+        positions int32 [S, axes] or [B, S, axes] ([T, axes]). Any strides
+        that are multiples of 8 with dense last dimensions, so that q and k may
+        be parts of a projection's output. q_out, k_out may be q and k; those
+        not given are dense. Returns (q, k), or q without k."""
+        return self._apply(q, k, positions, layout, q_out, k_out, stream, False)
+
+    def backward(self, dq, dk=None, positions=None, layout="bshd", q_out=None, k_out=None, stream=None):
+        """The gradients with respect to forward's inputs from those with
+        respect to its outputs: the rotation by the opposite angles."""
+        return self._apply(dq, dk, positions, layout, q_out, k_out, stream, True)
+
+    def table(self, positions, cos=None, sin=None, stream=None):
+        """vsa_rope_table: (cos, sin), fp32 [T, rot_dim / 2], of positions int32
+        [T, axes]: what PagedCache.append takes, with the row of each token in
+        its own positions argument (torch.arange(T) where each has its own)."""
+        if stream is not None:
+            if torch.is_tensor(positions) and stream.device != positions.device:
+                raise ValueError(f"stream: expected one of {positions.device}, got {stream.device}")
+            with torch.cuda.stream(stream):
+                return self._calls.table(positions, cos, sin)
+        return self._calls.table(positions, cos, sin)
+
+
+def tile_positions(T, H, W, tile=(4, 8, 8), device="cuda"):
+    """Positions int32 [slots, 3] (frame, row, column) of the tokens that
+    tile_3d lays out from a T x H x W latent; zeros in padding slots."""
+    at = torch.zeros((1, T, H, W, 4), dtype=torch.int32)
+    for axis, n in enumerate((T, H, W)):
+        at[..., axis] = torch.arange(n, dtype=torch.int32).view([-1 if a == axis else 1 for a in range(3)])
+    at = at.to(device)
+    with torch.cuda.device(at.device):
+        return tile_3d(at, tile)[0][0, :, :3]
 
 
 def check_wait_timeout(workspace: torch.Tensor, limit_ns: int = 50_000_000, stream=None) -> int:

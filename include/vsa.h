@@ -581,6 +581,61 @@ vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_s
                           const void *v_cache, const int32_t *page_idx, const int32_t *page_cnt, int idx_cap,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, vsa_stream_t stream);
 
+/* --------------------------------------------- rotary positions, several axes
+ * Queries and keys of image and video tokens, rotated by the token's position
+ * along several axes (frame, row, column) before the attention calls above, the
+ * gradients rotated back behind them, and tables of the same angles for
+ * vsa_paged_append. The pages of the sources have no such call. The first
+ * rot_dim dims of a head are rot_dim / 2 pairs: (2i, 2i + 1) when interleaved,
+ * else (i, i + rot_dim / 2). Pair i of a token at positions p turns by the angle
+ * p[axis[i]] * freq[i]:
+ *     y1 = x1 c - x2 s,  y2 = x2 c + x1 s,
+ * each product and each sum rounded once to fp32, the result once to dtype;
+ * the other dims are copied. Angles are products modulo one turn in 64-bit
+ * fixed point: c and s are off by at most 2^-22 at any int32 position. */
+#define VSA_ROPE_AXES 4
+typedef struct {
+    int32_t n_axes;       /* 1 to VSA_ROPE_AXES */
+    int32_t rot_dim;      /* a multiple of 16, up to 128 */
+    int32_t interleaved;
+    uint8_t axis[64];     /* of each pair */
+    uint64_t turn[64];    /* a pair's step, as a fraction of a turn: freq / (2 pi) modulo 1, times 2^64 */
+} vsa_rope;
+
+/* Fills *rope (host memory, no device call): axis[rot_dim / 2] in [0, n_axes),
+ * freq[rot_dim / 2] in radians per step, |freq| <= 1024. Errors: VSA_ERR_NULL,
+ * VSA_ERR_SHAPE, VSA_ERR_UNSUPPORTED (rot_dim); *rope is then unchanged. */
+vsa_status vsa_rope_init(vsa_rope *rope, int n_axes, int rot_dim, int interleaved, const int32_t *axis,
+                         const double *freq);
+
+/* One tensor of a call: x and y [B, S, heads, D] with these strides in elements
+ * between batch entries, tokens and heads (taken as they are, 0 included in
+ * x_*; multiples of 8; D dense), 16-byte aligned. y may be x with x's strides;
+ * otherwise y must not overlap any x of the call. y's rows must not overlap. */
+typedef struct {
+    const void *x;
+    void *y;
+    int32_t heads;
+    int64_t x_batch, x_token, x_head, y_batch, y_token, y_head;
+} vsa_rope_tensor;
+
+/* Rotates n (1 or 2: queries and keys) tensors of the same B x S tokens in one
+ * launch. positions: device int32, the n_axes positions of token s of batch
+ * entry b start at b * pos_batch + s * pos_token (0: shared). inverse != 0
+ * rotates by -angle: the gradients with respect to x from those with respect
+ * to y. D must be 128; B * S < 2^31. Errors: VSA_ERR_NULL, VSA_ERR_SHAPE,
+ * VSA_ERR_DTYPE, VSA_ERR_LAYOUT (alignment), VSA_ERR_UNSUPPORTED,
+ * VSA_ERR_CUDA. B * S == 0 enqueues nothing. */
+vsa_status vsa_rope_apply(const vsa_rope *rope, int dtype, int B, int S, int D, const vsa_rope_tensor *t, int n,
+                          const int32_t *positions, int64_t pos_batch, int64_t pos_token, int inverse,
+                          vsa_stream_t stream);
+
+/* The angles of T tokens (positions as above, pos_token elements apart) for
+ * vsa_paged_append: cos, sin fp32 [T, rot_dim / 2], 16-byte aligned; rotating
+ * by them gives vsa_rope_apply's bits. */
+vsa_status vsa_rope_table(const vsa_rope *rope, int T, const int32_t *positions, int64_t pos_token, float *cos, float *sin,
+                          vsa_stream_t stream);
+
 /* Message of the last CUDA error behind a VSA_ERR_CUDA return, with the
  * name of the last kernel the library launched ("no error" if there was
  * none). The string is owned by the library (per calling thread). */
