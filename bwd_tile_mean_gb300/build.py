@@ -23,7 +23,7 @@ OUT = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT, "libvsa.so")
 SOURCES = ["vsa_api.cu", "index_kernels.cu", "fwd_kernel.cu", "bwd_kernels.cu", "noalloc.cu", "tile3d.cu", "waitcheck.cu",
            "host_step.cu", "check_inputs.cu", "compress_kernels.cu", "paged_append.cu", "paged_select.cu",
-           "paged_attn.cu", "rope.cu"]
+           "paged_attn.cu", "paged_attn8.cu", "paged_append8.cu", "paged_weigh.cu", "rope.cu"]
 NVCC = os.environ.get("NVCC", "nvcc")
 CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -205,5 +205,33 @@ struct PagedWs {
     size_t total;
 };
 PagedWs paged_ws(const Paged &p);
+// Workspace of vsa_paged_attn_weigh: that of vsa_paged_attn, then the blocks'
+// sums of weights, float2 [segments, max_len / 16, rows].
+size_t weigh_bytes(const Paged &p);
+// Query heads per chunk of a group of G: equal chunks of up to 16.
+inline int rows_of(int G) {
+    const int chunks = (G + 15) / 16;
+    return (G + chunks - 1) / chunks;
+}
+
+// A call of the attention; ks, vs: the scales of an 8-bit cache.
+struct AttnCall {
+    const vsa_paged_desc *desc;
+    const void *q;
+    int64_t q_stride;
+    const void *k, *v;
+    const float *ks, *vs;
+    const int32_t *idx, *cnt;
+    int cap;
+    void *out;
+    float *lse;
+    void *ws;
+    size_t ws_bytes;
+    bool weigh;  // also the blocks' sums of weights
+};
+// What the lifted P of the blocks' sums are multiplied by: fp16 weights are lifted by 2^15, of an 8-bit cache by 2^14.
+inline float attn_drop(bool eight, int dtype) { return eight ? 0x1p-14f : dtype == T_FP16 ? 0x1p-15f : 1.f; }
+vsa_status attn16(const AttnCall &c, cudaStream_t s);
+vsa_status attn8(const AttnCall &c, cudaStream_t s);
 
 }  // namespace vsa

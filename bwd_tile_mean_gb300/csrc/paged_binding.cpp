@@ -4,10 +4,11 @@
 // in Python (checks, two torch.empty, a ctypes call) took 12.7 us for
 // vsa_paged_attn on a GB300's CPU; here 4.7 us, most of it the launch.
 //
-// Module paged_binding, type Calls(desc, k, v, k_mean, workspace,
-// workspace_bytes, functions, fail), the cache's tensors apart: desc is the address of a vsa_paged_desc
-// (copied), k .. workspace device addresses (0: none), functions the
-// addresses of vsa_paged_append, vsa_page_select and vsa_paged_attn, fail a
+// Module paged_binding, type Calls(desc, device, eight, k, v, k_scale, v_scale, k_mean, workspace,
+// workspace_bytes, weigh_bytes, functions, fail), the cache's tensors apart: desc is the address of a vsa_paged_desc
+// (copied), eight whether the cache is in 8 bits, k .. workspace device addresses (0: none), weigh_bytes the workspace's
+// for page weights (0: too small), functions the
+// addresses of the paged entry points in the order of their members below, fail a
 // callable (name, status) that raises. The tensors behind the addresses are
 // kept alive by the owner. Calls run on the current stream of the cache's
 // device, with that device current. Type Rope(rope, functions, fail): rope is
@@ -36,12 +37,19 @@ struct Calls {
     PyObject_HEAD;
     vsa_paged_desc d;
     void *k, *v, *mean, *ws;
-    size_t ws_bytes;
+    float *kscale, *vscale;
+    size_t ws_bytes, weigh_bytes;
     decltype(&vsa_paged_append) append;
     decltype(&vsa_page_select) select;
     decltype(&vsa_paged_attn) attn;
+    decltype(&vsa_paged8_append) append8;
+    decltype(&vsa_paged8_attn) attn8;
+    decltype(&vsa_paged_read) read;
+    decltype(&vsa_paged_attn_weigh) weigh;
+    decltype(&vsa_page_evict) evict;
     PyObject *fail;
     int device;  // CUDA device index, -1: the cache is not on a GPU
+    bool eight;   // the cache is in 8 bits
     bool shared;  // k and v share memory: attended to, but not appended to
     at::ScalarType dtype() const { return d.dtype == VSA_DTYPE_BF16 ? at::kBFloat16 : at::kHalf; }
 };
@@ -147,17 +155,24 @@ void apart(const Pieces &one, std::initializer_list<Pieces> others) {
 Pieces opt(const char *name, const at::Tensor *t) { return t ? pieces(name, *t) : Pieces{name, 0, 0, 0, 0}; }
 // The cache's own memory.
 Pieces cache_pages(const Calls &c, const char *name, const void *at) {
-    const int64_t dense = (int64_t)c.d.page * c.d.Hkv * c.d.D * 2;
-    return {name, (uintptr_t)at, at ? c.d.num_pages : 0, dense, c.d.page_stride ? c.d.page_stride * 2 : dense};
+    const int64_t size = c.eight ? 1 : 2, dense = (int64_t)c.d.page * c.d.Hkv * c.d.D * size;
+    return {name, (uintptr_t)at, at ? c.d.num_pages : 0, dense, c.d.page_stride ? c.d.page_stride * size : dense};
 }
 Pieces cache_k(const Calls &c) { return cache_pages(c, "the cache's k", c.k); }
 Pieces cache_v(const Calls &c) { return cache_pages(c, "the cache's v", c.v); }
 Pieces cache_mean(const Calls &c) {
     return whole("the cache's k_mean", c.mean, (int64_t)c.d.num_pages * c.d.Hkv * c.d.D * 4);
 }
+Pieces cache_scale(const Calls &c, const char *name, const float *at) {
+    return whole(name, at, (int64_t)c.d.num_pages * c.d.Hkv * (c.d.page / 16) * 4);
+}
+Pieces cache_ks(const Calls &c) { return cache_scale(c, "the cache's k_scale", c.kscale); }
+Pieces cache_vs(const Calls &c) { return cache_scale(c, "the cache's v_scale", c.vscale); }
 Pieces cache_table(const Calls &c) { return whole("page_table", c.d.page_table, (int64_t)c.d.B * c.d.max_pages * 4); }
 Pieces cache_lens(const Calls &c) { return whole("seq_lens", c.d.seq_lens, (int64_t)c.d.B * 4); }
-Pieces cache_ws(const Calls &c) { return whole("the workspace", c.ws, (int64_t)c.ws_bytes); }
+Pieces cache_ws(const Calls &c, bool weigh = false) {
+    return whole("the workspace", c.ws, (int64_t)(weigh ? c.weigh_bytes : c.ws_bytes));
+}
 
 template <typename T> T *ptr(const at::Tensor *t) { return t ? static_cast<T *>(t->data_ptr()) : nullptr; }
 
@@ -227,17 +242,22 @@ PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             if (T > 0 && given->data_ptr() == q->data_ptr()) refuse("q_out: must not be q");
             apart(pieces("q_out", *given),
                   {pieces("k", k), pieces("v", v), pieces("q", *q), opt("cu_seqlens", cu), opt("cos", cos),
-                   opt("sin", sin), opt("positions", pos), cache_k(c), cache_v(c), cache_mean(c), cache_table(c),
-                   cache_lens(c)});
+                   opt("sin", sin), opt("positions", pos), cache_k(c), cache_v(c), cache_ks(c), cache_vs(c),
+                   cache_mean(c), cache_table(c), cache_lens(c)});
             q_out = *given;
         } else if (q) {
             q_out = output(c, {T, c.d.Hq, c.d.D}, c.dtype());
         }
-        for (const Pieces &written : {cache_k(c), cache_v(c), cache_mean(c)})
+        for (const Pieces &written : {cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_mean(c)})
             apart(written, {pieces("k", k), pieces("v", v), opt("q", q), opt("cu_seqlens", cu), opt("cos", cos),
                             opt("sin", sin), opt("positions", pos)});
         if (T > 0 || c.device < 0)
-            run(c, "vsa_paged_append", [&](vsa_stream_t s) {
+            run(c, c.eight ? "vsa_paged8_append" : "vsa_paged_append", [&](vsa_stream_t s) {
+                if (c.eight)
+                    return c.append8(&c.d, (int)T, k.data_ptr(), ks, v.data_ptr(), vs, ptr<void>(q), qs,
+                                     q ? q_out.data_ptr() : nullptr, ptr<int32_t>(cu), ptr<int32_t>(pos), ptr<float>(cos),
+                                     ptr<float>(sin), cos ? (int)cos->size(0) : 0, cos ? 2 * (int)cos->size(1) : 0, inter,
+                                     c.k, c.v, c.kscale, c.vscale, static_cast<float *>(c.mean), s);
                 return c.append(&c.d, (int)T, k.data_ptr(), ks, v.data_ptr(), vs, ptr<void>(q), qs,
                                 q ? q_out.data_ptr() : nullptr, ptr<int32_t>(cu), ptr<int32_t>(pos), ptr<float>(cos),
                                 ptr<float>(sin), cos ? (int)cos->size(0) : 0, cos ? 2 * (int)cos->size(1) : 0, inter,
@@ -280,9 +300,15 @@ PyObject *calls_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     });
 }
 
-// attend(q, pages, out, lse)
+double number(PyObject *o) {
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw Raised();
+    return v;
+}
+
+// attend(q, pages, out, lse, page_weight, weight_out, decay)
 PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
-    return guarded(self, n, 4, [&](Calls &c) -> PyObject * {
+    return guarded(self, n, 7, [&](Calls &c) -> PyObject * {
         if (!c.k) refuse("this cache has no k and v");
         const at::Tensor &q = tensor(a[0], "q");
         const int64_t qs = query_rows(c, q);
@@ -296,53 +322,163 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             check_dense(c, "page_cnt", *cnt, at::kInt, {c.d.B, c.d.Hkv});
         }
         const at::Tensor *go = optional(a[2], "out"), *gl = optional(a[3], "lse");
+        const at::Tensor *pw = optional(a[4], "page_weight"), *wo = optional(a[5], "weight_out");
+        const double decay = number(a[6]);
         if (go) check_dense(c, "out", *go, c.dtype(), {c.d.B, c.d.Hq, c.d.D});
         if (go && go->data_ptr() == q.data_ptr()) refuse("out: must not be q");
         if (gl) check_dense(c, "lse", *gl, at::kFloat, {c.d.B, c.d.Hq});
-        const Pieces po = opt("out", go), pl = opt("lse", gl);
-        for (const Pieces &written : {po, pl})
-            apart(written, {pieces("q", q), opt("page_idx", idx), opt("page_cnt", cnt), cache_k(c), cache_v(c),
-                            cache_table(c), cache_lens(c), cache_ws(c)});
-        apart(po, {pl});
+        if (!pw && (wo || decay != 1.0)) refuse("weight_out and decay belong to page_weight");
+        if (pw) {
+            check_dense(c, "page_weight", *pw, at::kFloat, {c.d.B, c.d.Hkv, c.d.max_pages});
+            if (wo) check_dense(c, "weight_out", *wo, at::kFloat, pw->sizes());
+            if (!(decay >= 0.0 && decay <= 1.0)) refuse("decay: from 0 to 1, not ", decay);
+            if (idx && idx->size(2) > c.d.max_pages) refuse("page_idx: no longer than the table where pages are weighed");
+            if (!c.weigh_bytes) refuse("the workspace is too small for page weights: make the cache with weigh=True");
+        }
+        const at::Tensor *to = pw && !wo ? pw : wo;
+        const Pieces po = opt("out", go), pl = opt("lse", gl), pt = opt("weight_out", to), pp = opt("page_weight", pw);
+        for (const Pieces &written : {po, pl, pt})
+            apart(written, {pieces("q", q), opt("page_idx", idx), opt("page_cnt", cnt), cache_k(c), cache_v(c), cache_ks(c),
+                            cache_vs(c), cache_table(c), cache_lens(c), cache_ws(c, pw != nullptr)});
+        apart(po, {pl, pt, pp});
+        apart(pl, {pt, pp});
+        if (pw && pt.at != pp.at) apart(pt, {pp});
         at::Tensor out = go ? *go : output(c, {c.d.B, c.d.Hq, c.d.D}, c.dtype());
         at::Tensor lse = gl ? *gl : output(c, {c.d.B, c.d.Hq}, at::kFloat);
-        run(c, "vsa_paged_attn", [&](vsa_stream_t s) {
-            return c.attn(&c.d, q.data_ptr(), qs, c.k, c.v, ptr<int32_t>(idx), ptr<int32_t>(cnt),
-                          idx ? (int)idx->size(2) : 0, out.data_ptr(), ptr<float>(&lse), c.ws, c.ws_bytes, s);
+        const int cap = idx ? (int)idx->size(2) : 0;
+        run(c, pw ? "vsa_paged_attn_weigh" : c.eight ? "vsa_paged8_attn" : "vsa_paged_attn", [&](vsa_stream_t s) {
+            if (pw)
+                return c.weigh(&c.d, q.data_ptr(), qs, c.k, c.v, c.kscale, c.vscale, ptr<int32_t>(idx), ptr<int32_t>(cnt), cap,
+                               out.data_ptr(), ptr<float>(&lse), ptr<float>(pw), ptr<float>(to), (float)decay, c.ws,
+                               c.weigh_bytes, s);
+            if (c.eight)
+                return c.attn8(&c.d, q.data_ptr(), qs, c.k, c.v, c.kscale, c.vscale, ptr<int32_t>(idx), ptr<int32_t>(cnt), cap,
+                               out.data_ptr(), ptr<float>(&lse), c.ws, c.ws_bytes, s);
+            return c.attn(&c.d, q.data_ptr(), qs, c.k, c.v, ptr<int32_t>(idx), ptr<int32_t>(cnt), cap, out.data_ptr(),
+                          ptr<float>(&lse), c.ws, c.ws_bytes, s);
         });
         return pair(std::move(out), std::move(lse));
     });
 }
 
-// Calls(desc, device, k, v, k_mean, workspace, workspace_bytes, append, select, attn, fail)
+// read(tokens, cu_seqlens, k_out, v_out)
+PyObject *calls_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return guarded(self, n, 4, [&](Calls &c) -> PyObject * {
+        if (!c.k) refuse("this cache has no k and v");
+        const long T = integer(a[0], "tokens");
+        const at::Tensor *cu = optional(a[1], "cu_seqlens"), *gk = optional(a[2], "k_out"), *gv = optional(a[3], "v_out");
+        if (T < 0) refuse("tokens: out of range");
+        if (cu)
+            check_dense(c, "cu_seqlens", *cu, at::kInt, {c.d.B + 1});
+        else if (T != c.d.B)
+            refuse("without cu_seqlens there is one token per sequence");
+        if (gk) check_dense(c, "k_out", *gk, c.dtype(), {T, c.d.Hkv, c.d.D});
+        if (gv) check_dense(c, "v_out", *gv, c.dtype(), {T, c.d.Hkv, c.d.D});
+        const Pieces pk = opt("k_out", gk), pv = opt("v_out", gv);
+        for (const Pieces &written : {pk, pv})
+            apart(written, {opt("cu_seqlens", cu), cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_table(c),
+                            cache_lens(c)});
+        apart(pk, {pv});
+        at::Tensor k = gk ? *gk : output(c, {T, c.d.Hkv, c.d.D}, c.dtype());
+        at::Tensor v = gv ? *gv : output(c, {T, c.d.Hkv, c.d.D}, c.dtype());
+        if (T > 0 || c.device < 0)
+            run(c, "vsa_paged_read", [&](vsa_stream_t s) {
+                return c.read(&c.d, (int)T, ptr<int32_t>(cu), c.k, c.v, c.kscale, c.vscale, k.data_ptr(), v.data_ptr(), s);
+            });
+        return pair(std::move(k), std::move(v));
+    });
+}
+
+// evict(page_weight, keep, keep_first, keep_last, freed, freed_cnt, out)
+PyObject *calls_evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    return guarded(self, n, 7, [&](Calls &c) -> PyObject * {
+        const at::Tensor &w = tensor(a[0], "page_weight");
+        const long keep = integer(a[1], "keep"), first = integer(a[2], "keep_first"), last = integer(a[3], "keep_last");
+        const at::Tensor *gf = optional(a[4], "freed"), *gc = optional(a[5], "freed_cnt");
+        check_dense(c, "page_weight", w, at::kFloat, {c.d.B, c.d.Hkv, c.d.max_pages});
+        if (first < 0 || last < 1 || keep < first + last)
+            refuse("keep: at least keep_first (0 or more) and keep_last (1 or more), not ", keep, " of ", first, " and ", last);
+        const int64_t cap = keep < c.d.max_pages ? c.d.max_pages - keep : 1;
+        if (gf) check_dense(c, "freed", *gf, at::kInt, {c.d.B, cap});
+        if (gc) check_dense(c, "freed_cnt", *gc, at::kInt, {c.d.B});
+        // in place, or into the three tensors of `out`
+        void *table = const_cast<int32_t *>(c.d.page_table), *lens = const_cast<int32_t *>(c.d.seq_lens), *to = w.data_ptr();
+        if (a[6] != Py_None) {
+            if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 3)
+                refuse("out: expected (page_table, seq_lens, page_weight)");
+            const at::Tensor &t = tensor(PyTuple_GET_ITEM(a[6], 0), "out: page_table"),
+                             &l = tensor(PyTuple_GET_ITEM(a[6], 1), "out: seq_lens"),
+                             &o = tensor(PyTuple_GET_ITEM(a[6], 2), "out: page_weight");
+            check_dense(c, "out: page_table", t, at::kInt, {c.d.B, c.d.max_pages});
+            check_dense(c, "out: seq_lens", l, at::kInt, {c.d.B});
+            check_dense(c, "out: page_weight", o, at::kFloat, w.sizes());
+            table = t.data_ptr();
+            lens = l.data_ptr();
+            to = o.data_ptr();
+        }
+        const Pieces in[3] = {cache_table(c), cache_lens(c), pieces("page_weight", w)};
+        Pieces outs[5] = {in[0], in[1], in[2], opt("freed", gf), opt("freed_cnt", gc)};
+        const void *at[3] = {table, lens, to};
+        const char *names[3] = {"the evicted page_table", "the evicted seq_lens", "the evicted page_weight"};
+        for (int i = 0; i < 3; ++i) outs[i].at = (uintptr_t)at[i], outs[i].name = names[i];
+        for (int i = 0; i < 5; ++i) {
+            apart(outs[i], {cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_mean(c), cache_ws(c)});
+            for (int j = 0; j < 3; ++j)
+                if (i != j || outs[i].at != in[j].at) apart(outs[i], {in[j]});
+            for (int j = 0; j < i; ++j) apart(outs[i], {outs[j]});
+        }
+        at::Tensor freed = gf ? *gf : output(c, {c.d.B, cap}, at::kInt);
+        at::Tensor count = gc ? *gc : output(c, {c.d.B}, at::kInt);
+        run(c, "vsa_page_evict", [&](vsa_stream_t s) {
+            return c.evict(&c.d, ptr<float>(&w), (int)keep, (int)first, (int)last, static_cast<int32_t *>(table),
+                           static_cast<int32_t *>(lens), static_cast<float *>(to), ptr<int32_t>(&freed), ptr<int32_t>(&count),
+                           c.ws, c.ws_bytes, s);
+        });
+        return pair(std::move(freed), std::move(count));
+    });
+}
+
+// Calls(desc, device, eight, k, v, k_scale, v_scale, k_mean, workspace, workspace_bytes, weigh_bytes, functions, fail)
 PyObject *calls_new(PyTypeObject *type, PyObject *args, PyObject *) {
-    unsigned long long desc, k, v, mean, ws, bytes, append, select, attn;
-    int device;
+    unsigned long long desc, k, v, ks, vs, mean, ws, bytes, weigh_bytes, f[8];
+    int device, eight;
     PyObject *fail;
-    if (!PyArg_ParseTuple(args, "KiKKKKKKKKO", &desc, &device, &k, &v, &mean, &ws, &bytes, &append, &select, &attn,
-                          &fail))
+    if (!PyArg_ParseTuple(args, "KipKKKKKKKK(KKKKKKKK)O", &desc, &device, &eight, &k, &v, &ks, &vs, &mean, &ws, &bytes,
+                          &weigh_bytes, &f[0], &f[1], &f[2], &f[3], &f[4], &f[5], &f[6], &f[7], &fail))
         return nullptr;
     PyObject *self = type->tp_alloc(type, 0);
     if (!self) return nullptr;
     Calls *c = reinterpret_cast<Calls *>(self);
     c->d = *reinterpret_cast<const vsa_paged_desc *>(desc);
     c->device = device;
+    c->eight = eight != 0;
     c->k = reinterpret_cast<void *>(k);
     c->v = reinterpret_cast<void *>(v);
+    c->kscale = reinterpret_cast<float *>(ks);
+    c->vscale = reinterpret_cast<float *>(vs);
     c->mean = reinterpret_cast<void *>(mean);
     c->ws = reinterpret_cast<void *>(ws);
     c->ws_bytes = (size_t)bytes;
-    c->append = reinterpret_cast<decltype(c->append)>(append);
-    c->select = reinterpret_cast<decltype(c->select)>(select);
-    c->attn = reinterpret_cast<decltype(c->attn)>(attn);
+    c->weigh_bytes = (size_t)weigh_bytes;
+    c->append = reinterpret_cast<decltype(c->append)>(f[0]);
+    c->select = reinterpret_cast<decltype(c->select)>(f[1]);
+    c->attn = reinterpret_cast<decltype(c->attn)>(f[2]);
+    c->append8 = reinterpret_cast<decltype(c->append8)>(f[3]);
+    c->attn8 = reinterpret_cast<decltype(c->attn8)>(f[4]);
+    c->read = reinterpret_cast<decltype(c->read)>(f[5]);
+    c->weigh = reinterpret_cast<decltype(c->weigh)>(f[6]);
+    c->evict = reinterpret_cast<decltype(c->evict)>(f[7]);
     Py_INCREF(fail);
     c->fail = fail;
     c->shared = meet(cache_k(*c), cache_v(*c));
     try {
         apart(cache_mean(*c), {cache_k(*c), cache_v(*c)});
         apart(cache_ws(*c), {cache_k(*c), cache_v(*c), cache_mean(*c)});
+        apart(cache_ks(*c), {cache_vs(*c)});
+        for (const Pieces &scale : {cache_ks(*c), cache_vs(*c)})
+            apart(scale, {cache_k(*c), cache_v(*c), cache_mean(*c), cache_ws(*c)});
         for (const Pieces &read : {cache_table(*c), cache_lens(*c)})
-            apart(read, {cache_k(*c), cache_v(*c), cache_mean(*c), cache_ws(*c)});
+            apart(read, {cache_k(*c), cache_v(*c), cache_ks(*c), cache_vs(*c), cache_mean(*c), cache_ws(*c)});
     } catch (const Refused &e) {
         PyErr_SetString(PyExc_ValueError, e.what());
         Py_DECREF(self);
@@ -588,9 +724,11 @@ PyCFunction fast(PyObject *(*f)(PyObject *, PyObject *const *, Py_ssize_t)) {
     return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f));
 }
 PyMethodDef methods[] = {
-    {"append", fast(calls_append), METH_FASTCALL, "vsa_paged_append"},
+    {"append", fast(calls_append), METH_FASTCALL, "vsa_paged_append, vsa_paged8_append"},
     {"select", fast(calls_select), METH_FASTCALL, "vsa_page_select"},
-    {"attend", fast(calls_attend), METH_FASTCALL, "vsa_paged_attn"},
+    {"attend", fast(calls_attend), METH_FASTCALL, "vsa_paged_attn, vsa_paged8_attn, vsa_paged_attn_weigh"},
+    {"read", fast(calls_read), METH_FASTCALL, "vsa_paged_read"},
+    {"evict", fast(calls_evict), METH_FASTCALL, "vsa_page_evict"},
     {nullptr, nullptr, 0, nullptr},
 };
 PyType_Slot slots[] = {

@@ -37,7 +37,8 @@ EXPORTS = ("vsa_workspace_size", "vsa_build_block_map", "vsa_build_block_map_sta
            "vsa_train_step_host_size", "vsa_train_step_host", "vsa_fwd_step_host", "vsa_step_host_status",
            "vsa_check_inputs", "vsa_head_slice", "vsa_fwd_reuse", "vsa_bwd_reuse",
            "vsa_paged_workspace_size", "vsa_paged_append", "vsa_page_select", "vsa_paged_attn",
-           "vsa_rope_init", "vsa_rope_apply", "vsa_rope_table")
+           "vsa_paged8_append", "vsa_paged8_attn", "vsa_paged_read", "vsa_paged_weigh_workspace_size",
+           "vsa_paged_attn_weigh", "vsa_page_evict", "vsa_rope_init", "vsa_rope_apply", "vsa_rope_table")
 
 REUSE_QK_MEANS, REUSE_V_MEANS = 1, 2  # vsa_fwd_reuse / vsa_bwd_reuse mask bits
 
@@ -171,6 +172,20 @@ def lib():
                                       P]
         L.vsa_paged_attn.restype = C.c_int
         L.vsa_paged_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
+        L.vsa_paged8_append.restype = C.c_int
+        L.vsa_paged8_append.argtypes = [C.POINTER(PagedDesc), C.c_int, P, i64, P, i64, P, i64, P, P, P, P, P, C.c_int,
+                                        C.c_int, C.c_int, P, P, P, P, P, P]
+        L.vsa_paged8_attn.restype = C.c_int
+        L.vsa_paged8_attn.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, P, P, C.c_int, P, P, P, C.c_size_t, P]
+        L.vsa_paged_read.restype = C.c_int
+        L.vsa_paged_read.argtypes = [C.POINTER(PagedDesc), C.c_int, P, P, P, P, P, P, P, P]
+        L.vsa_paged_weigh_workspace_size.restype = C.c_size_t
+        L.vsa_paged_weigh_workspace_size.argtypes = [C.POINTER(PagedDesc)]
+        L.vsa_paged_attn_weigh.restype = C.c_int
+        L.vsa_paged_attn_weigh.argtypes = [C.POINTER(PagedDesc), P, i64, P, P, P, P, P, P, C.c_int, P, P, P, P, C.c_float,
+                                           P, C.c_size_t, P]
+        L.vsa_page_evict.restype = C.c_int
+        L.vsa_page_evict.argtypes = [C.POINTER(PagedDesc), P, C.c_int, C.c_int, C.c_int, P, P, P, P, P, P, C.c_size_t, P]
         L.vsa_rope_init.restype = C.c_int
         L.vsa_rope_init.argtypes = [C.POINTER(RopeDesc), C.c_int, C.c_int, C.c_int, P, P]
         L.vsa_rope_apply.restype = C.c_int
@@ -710,15 +725,21 @@ def _paged_binding():
 
 class PagedCache:
     """One layer's paged key/value cache (the conventions of the paged calls
-    in include/vsa.h): appending, page selection, one-token attention. The
-    calls give no gradients; tensors that require one are refused while
-    gradients are recorded.
+    in include/vsa.h): appending, page selection, one-token attention, reading
+    back, page weights and eviction. The calls give no gradients; tensors that
+    require one are refused while gradients are recorded.
 
     layout: "bshd" (pages [page, Hkv, D]) | "bhsd" (pages [Hkv, page, D]).
     k, v: [num_pages, ...page] tensors of dtype, dense inside a page (halves
     of one buffer are fine); k_mean: fp32 [num_pages, Hkv, D], or False for a
     cache whose pages are never selected. Those not given are allocated
-    unless allocate is False (a cache that only selects needs no k and v).
+    unless allocate is False (a cache that only selects or evicts needs no k and v).
+    kv_dtype: torch.float8_e4m3fn for a cache in 8 bits, whose k and v are of that
+    type and have a scale per block of 16 tokens and head, k_scale and v_scale:
+    fp32 [num_pages, Hkv, page / 16]; None: dtype.
+    weigh: whether the workspace allocated here is large enough for attend with
+    page weights (``vsa_paged_weigh_workspace_size`` bytes; one passed in decides by
+    its size).
     page_table: int32 [B, max_pages]; seq_lens: int32 [B], the tokens in the
     cache with those of the current step counted in. Both belong to the
     caller, are read by every call when it runs on the device and may be
@@ -733,24 +754,41 @@ class PagedCache:
     """
 
     def __init__(self, layout, dtype, B, Hq, Hkv, D, page, num_pages, max_pages, k=None, v=None, k_mean=None,
-                 page_table=None, seq_lens=None, scale=0.0, workspace=None, allocate=True, device="cuda"):
+                 page_table=None, seq_lens=None, scale=0.0, workspace=None, allocate=True, device="cuda",
+                 kv_dtype=None, k_scale=None, v_scale=None, weigh=False):
         if layout not in ("bshd", "bhsd"):
             raise ValueError(f"a page's layout is bshd or bhsd, not {layout}")
         if dtype not in DTYPES:
             raise ValueError("the cache holds bf16 or fp16")
+        kv_dtype = dtype if kv_dtype is None else kv_dtype
+        if kv_dtype not in (dtype, torch.float8_e4m3fn):
+            raise ValueError(f"kv_dtype: {dtype} or torch.float8_e4m3fn, not {kv_dtype}")
+        eight = kv_dtype == torch.float8_e4m3fn
         for name, n in dict(B=B, Hq=Hq, Hkv=Hkv, D=D, page=page, num_pages=num_pages, max_pages=max_pages).items():
             if not 0 < n < 1 << 31:  # ctypes keeps the low 32 bits of others
                 raise ValueError(f"{name}: {n} is out of range")
-        given = [t for t in (k, v, k_mean, page_table, seq_lens, workspace) if torch.is_tensor(t)]
+        given = [t for t in (k, v, k_mean, page_table, seq_lens, workspace, k_scale, v_scale) if torch.is_tensor(t)]
         self.device = given[0].device if given else torch.device(device)
         if self.device.type == "cuda" and self.device.index is None:
             self.device = torch.device("cuda", torch.cuda.current_device())
-        self.layout, self.dtype = layout, dtype
+        self.layout, self.dtype, self.kv_dtype = layout, dtype, kv_dtype
         self.B, self.Hq, self.Hkv, self.D = B, Hq, Hkv, D
         self.page, self.num_pages, self.max_pages = page, num_pages, max_pages
         shape = (num_pages, page, Hkv, D) if layout == "bshd" else (num_pages, Hkv, page, D)
         if k is None and v is None and allocate:
-            k, v = (torch.zeros(shape, dtype=dtype, device=self.device) for _ in range(2))
+            k, v = (torch.zeros(shape, dtype=kv_dtype, device=self.device) for _ in range(2))
+        blocks = (num_pages, Hkv, max(1, page // 16))
+        if not eight and (k_scale is not None or v_scale is not None):
+            raise ValueError("k_scale and v_scale belong to a cache of 8 bits")
+        if eight and k is not None:
+            if k_scale is None and v_scale is None:
+                if any(t is k for t in given):  # its bytes stand for nothing without them
+                    raise ValueError("give k_scale and v_scale with k and v")
+                k_scale, v_scale = (torch.ones(blocks, device=self.device) for _ in range(2))
+            if k_scale is None or v_scale is None:
+                raise ValueError("give both k_scale and v_scale, or neither")
+        elif eight and (k_scale is not None or v_scale is not None):
+            raise ValueError("k_scale and v_scale without k and v")
         if k_mean is None and allocate:
             k_mean = torch.zeros((num_pages, Hkv, D), dtype=torch.float32, device=self.device)
         elif k_mean is False:
@@ -763,7 +801,7 @@ class PagedCache:
         for name, t in (("k", k), ("v", v)):
             if t is None:
                 continue
-            self._is(name, t, shape, dtype)
+            self._is(name, t, shape, kv_dtype)
             if any(n > 1 and a != b for n, a, b in zip(shape[1:], t.stride()[1:], inner)):
                 raise ValueError(f"{name}: a page must be dense")
             if num_pages > 1 and t.stride(0) < page * Hkv * D:
@@ -775,17 +813,22 @@ class PagedCache:
             raise ValueError("give both k and v, or neither")
         for name, t, shp, dt in (("k_mean", k_mean, (num_pages, Hkv, D), torch.float32),
                                  ("page_table", page_table, (B, max_pages), torch.int32),
-                                 ("seq_lens", seq_lens, (B,), torch.int32)):
+                                 ("seq_lens", seq_lens, (B,), torch.int32),
+                                 ("k_scale", k_scale, blocks, torch.float32),
+                                 ("v_scale", v_scale, blocks, torch.float32)):
             if t is not None:
                 self._is(name, t, shp, dt)
                 if not t.is_contiguous():
                     raise ValueError(f"{name}: must be contiguous")
-        self._tensors = (k, v, k_mean, page_table, seq_lens)
+        self._tensors = (k, v, k_mean, page_table, seq_lens, k_scale, v_scale)
         self.desc = PagedDesc(LAYOUTS[layout], DTYPES[dtype], B, Hq, Hkv, D, page, num_pages, max_pages, stride,
                               page_table.data_ptr(), seq_lens.data_ptr(), float(scale))
         need = int(lib().vsa_paged_workspace_size(C.byref(self.desc)))
-        if need == 0:
+        if need == 0 or (eight and stride % 16):
             raise ValueError("invalid paged-cache description")
+        weigh_need = int(lib().vsa_paged_weigh_workspace_size(C.byref(self.desc)))
+        if weigh:
+            need = weigh_need
         if workspace is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
         elif (workspace.device != self.device or not workspace.is_contiguous()
@@ -797,15 +840,20 @@ class PagedCache:
         entry = lambda f: C.cast(f, C.c_void_p).value  # noqa: E731
         L = lib()
         self._calls = _paged_binding().Calls(
-            C.addressof(self.desc), self.device.index if self.device.type == "cuda" else -1, at(k), at(v), at(k_mean),
-            at(workspace), need, entry(L.vsa_paged_append),
-            entry(L.vsa_page_select), entry(L.vsa_paged_attn), _check)
+            C.addressof(self.desc), self.device.index if self.device.type == "cuda" else -1, eight, at(k), at(v),
+            at(k_scale), at(v_scale), at(k_mean), at(workspace), int(lib().vsa_paged_workspace_size(C.byref(self.desc))),
+            weigh_need if workspace.numel() * workspace.element_size() >= weigh_need else 0,
+            tuple(entry(f) for f in (L.vsa_paged_append, L.vsa_page_select, L.vsa_paged_attn, L.vsa_paged8_append,
+                                     L.vsa_paged8_attn, L.vsa_paged_read, L.vsa_paged_attn_weigh, L.vsa_page_evict)),
+            _check)
 
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
     k_mean = property(lambda self: self._tensors[2])
     page_table = property(lambda self: self._tensors[3])
     seq_lens = property(lambda self: self._tensors[4])
+    k_scale = property(lambda self: self._tensors[5])
+    v_scale = property(lambda self: self._tensors[6])
     workspace = property(lambda self: self._workspace)
 
     def _is(self, name, t, shape, dtype):
@@ -844,11 +892,35 @@ class PagedCache:
                 return self._calls.select(q, topk, keep_first, keep_last, page_idx, page_cnt)
         return self._calls.select(q, topk, keep_first, keep_last, page_idx, page_cnt)
 
-    def attend(self, q, pages=None, out=None, lse=None, stream=None):
-        """vsa_paged_attn: q [B, Hq, D] over the whole cache, or over the
-        pages = (page_idx, page_cnt) that select returned. Returns (out
-        [B, Hq, D], lse fp32 [B, Hq])."""
+    def attend(self, q, pages=None, out=None, lse=None, stream=None, page_weight=None, weight_out=None, decay=1.0):
+        """vsa_paged_attn (vsa_paged8_attn): q [B, Hq, D] over the whole cache, or
+        over the pages = (page_idx, page_cnt) that select returned. Returns (out
+        [B, Hq, D], lse fp32 [B, Hq]). With page_weight fp32 [B, Hkv, max_pages]
+        (vsa_paged_attn_weigh) the attention weight that each page receives is
+        added to it, in place or into weight_out, what it held multiplied by
+        decay: what evict goes by."""
         if stream is not None:
             with self._on(stream):
-                return self._calls.attend(q, pages, out, lse)
-        return self._calls.attend(q, pages, out, lse)
+                return self._calls.attend(q, pages, out, lse, page_weight, weight_out, decay)
+        return self._calls.attend(q, pages, out, lse, page_weight, weight_out, decay)
+
+    def read(self, tokens, cu_seqlens=None, k_out=None, v_out=None, stream=None):
+        """vsa_paged_read: (k, v), each [tokens, Hkv, D] in dtype, of the newest
+        tokens of each sequence: cu_seqlens [B+1] as in append, one each without
+        it. A cache in 8 bits gives the values it stands for."""
+        if stream is not None:
+            with self._on(stream):
+                return self._calls.read(tokens, cu_seqlens, k_out, v_out)
+        return self._calls.read(tokens, cu_seqlens, k_out, v_out)
+
+    def evict(self, page_weight, keep, keep_first=0, keep_last=1, freed=None, freed_cnt=None, out=None, stream=None):
+        """vsa_page_evict: cuts sequences of more than keep pages to those with the
+        largest page_weight fp32 [B, Hkv, max_pages] and the first keep_first and
+        last keep_last. The table, the lengths and page_weight change in place, or
+        are left and written to out = (page_table, seq_lens, page_weight).
+        Returns (freed int32 [B, max(1, max_pages - keep)], freed_cnt int32 [B]):
+        the pages that went."""
+        if stream is not None:
+            with self._on(stream):
+                return self._calls.evict(page_weight, keep, keep_first, keep_last, freed, freed_cnt, out)
+        return self._calls.evict(page_weight, keep, keep_first, keep_last, freed, freed_cnt, out)

@@ -581,6 +581,100 @@ vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_s
                           const void *v_cache, const int32_t *page_idx, const int32_t *page_cnt, int idx_cap,
                           void *out, float *lse, void *workspace, size_t workspace_bytes, vsa_stream_t stream);
 
+/* ---------------------------------------------------- paged cache in 8 bits
+ * The paged cache with keys and values of 8 bits (e4m3: 4 exponent and 3
+ * fraction bits, 448 at most, no infinities) and a scale for each block of 16
+ * tokens of a page and key/value head. Descriptor and conventions as above, but:
+ *   cache     k_cache, v_cache: bytes, in the page layouts above; page_stride in
+ *             bytes, a multiple of 16. desc->dtype is the type of q, k, v and out.
+ *   scales    k_scale, v_scale [num_pages, Hkv, page / 16] fp32, positive
+ *             powers of two: a byte of block i of a page stands for its e4m3
+ *             value times the block's scale. (Others are used as they are by
+ *             reading calls, v_scale to 11 bits relative to the largest
+ *             power of two met.)
+ * vsa_page_select works on such a cache as it is: it reads means, the table and
+ * lengths only. */
+
+/* vsa_paged_append for 8 bits: the same arguments and errors, and the scales
+ * (VSA_ERR_NULL, VSA_ERR_LAYOUT). Keys are rotated in fp32 (each product and
+ * each sum rounded once) and rounded once, to e4m3. A block's scale becomes the
+ * least power of two, 2^-126 or more, that brings the largest magnitude of its
+ * new entries within 448, or stays where it is larger and the block's first
+ * slot is not written by the call. Where it grows, the block's earlier bytes are
+ * divided by the growth and rounded again, which only changes what falls below
+ * 2^-6 of the scale. So scales do not depend on how the tokens were cut
+ * into calls, bytes only there, and a call made again gives the same result.
+ * Infinities become NaN and, like NaN, do not count for the scale; fp16 entries
+ * never round beyond 65504. k_mean: of the stored values, in the order of
+ * vsa_paged_append. */
+vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const void *k, int64_t k_stride, const void *v,
+                             int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                             const int32_t *cu_seqlens, const int32_t *positions, const float *cos,
+                             const float *sin, int table_rows, int rot_dim, int interleaved, void *k_cache,
+                             void *v_cache, float *k_scale, float *v_scale, float *k_mean, vsa_stream_t stream);
+
+/* vsa_paged_attn over an 8-bit cache: the same arguments, results and errors,
+ * and the scales. The products run in fp16 with fp32 sums: q is brought there by
+ * a power of two per row (bf16 entries keep their 8 bits down to 2^-29 of the
+ * row's largest), e4m3 exactly, the weights are rounded to fp16. A value
+ * counts down to 2^-38 of the largest (scale of the cache times weight). */
+vsa_status vsa_paged8_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
+                           const void *v_cache, const float *k_scale, const float *v_scale, const int32_t *page_idx,
+                           const int32_t *page_cnt, int idx_cap, void *out, float *lse, void *workspace,
+                           size_t workspace_bytes, vsa_stream_t stream);
+
+/* The stored keys and values of T tokens as dtype, k_out, v_out [T, Hkv, D]
+ * dense (k rotated, as it was appended): the tokens that an append of the same
+ * T and cu_seqlens would write, the newest of each sequence. k_scale and v_scale
+ * NULL: a 16-bit cache. A token without a place in the cache, or whose page does
+ * not exist, reads as zeros; rows behind cu_seqlens[B] are not written. The
+ * outputs must not overlap the cache, nor each other. Errors as for
+ * vsa_paged_append. */
+vsa_status vsa_paged_read(const vsa_paged_desc *desc, int T, const int32_t *cu_seqlens, const void *k_cache,
+                          const void *v_cache, const float *k_scale, const float *v_scale, void *k_out, void *v_out,
+                          vsa_stream_t stream);
+
+/* ------------------------------------------------------------ page eviction
+ * A cache within a budget of pages: the attention adds up what weight each page
+ * receives, and the pages that received least are given up. */
+
+/* vsa_paged_attn (k_scale and v_scale NULL) or vsa_paged8_attn that also adds up
+ * the attention weight of pages: for every page j of sequence b that holds a token,
+ *   weight_out[b, h, j] = decay * page_weight[b, h, j] + sum P
+ * over the page's tokens and the query heads of key/value head h, P = exp(scale
+ * q.k - LSE); a listed page that is listed twice counts twice, one that is not listed
+ * adds 0. The other entries are copied. page_weight, weight_out [B, Hkv,
+ * max_pages] fp32, one buffer or two that do not overlap; decay in [0, 1] (0: page_weight's
+ * entries of the sequence's pages are not read). out and lse are those of the plain call bit for bit, and the
+ * sums are the same bit for bit on every run. idx_cap <= max_pages (VSA_ERR_UNSUPPORTED).
+ * workspace: vsa_paged_weigh_workspace_size bytes; it serves the plain calls too. */
+size_t vsa_paged_weigh_workspace_size(const vsa_paged_desc *desc);
+vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
+                                const void *v_cache, const float *k_scale, const float *v_scale, const int32_t *page_idx,
+                                const int32_t *page_cnt, int idx_cap, void *out, float *lse, const float *page_weight,
+                                float *weight_out, float decay, void *workspace, size_t workspace_bytes,
+                                vsa_stream_t stream);
+
+/* Cuts every sequence of more than `keep` pages down to `keep`: its first
+ * keep_first (>= 0) and last keep_last (>= 1) pages stay (keep >= keep_first +
+ * keep_last), and of the others those with the largest weight, the lower page among equals. A
+ * page's weight is the sum of page_weight[b, :, j] over the heads, added in fp64
+ * and rounded once to fp32; NaN counts as -inf. The entries of the pages that go are
+ * taken out of the sequence's rows of the table and of page_weight; those behind
+ * them (also the ones past the sequence's end) move up in order, and the places that come
+ * free at the end of a row get -1 and 0. freed [B, max(1, max_pages - keep)]
+ * receives the ids of the pages that went, ascending in their old places, then -1;
+ * freed_cnt [B] their number; lens_out the lengths without their tokens.
+ * Sequences of no more pages keep their rows. Tokens stay
+ * where they are in the pool, rotated as they were; later appends need positions of
+ * their own. table_out [B, max_pages], lens_out [B] and weight_out
+ * [B, Hkv, max_pages] may be desc->page_table, desc->seq_lens and page_weight
+ * themselves; otherwise none of the outputs overlaps another tensor.
+ * workspace: vsa_paged_workspace_size bytes. Errors as for vsa_page_select. */
+vsa_status vsa_page_evict(const vsa_paged_desc *desc, const float *page_weight, int keep, int keep_first, int keep_last,
+                          int32_t *table_out, int32_t *lens_out, float *weight_out, int32_t *freed, int32_t *freed_cnt,
+                          void *workspace, size_t workspace_bytes, vsa_stream_t stream);
+
 /* --------------------------------------------- rotary positions, several axes
  * Queries and keys of image and video tokens, rotated by the token's position
  * along several axes (frame, row, column) before the attention calls above, the
