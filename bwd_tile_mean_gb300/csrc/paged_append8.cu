@@ -53,11 +53,12 @@ __device__ __forceinline__ void rotate8(const AppendArgs &a, uint4 x, const Angl
     }
 }
 
-// What dtype holds: entries from `kInf` on are infinite in it, and fp16 has no value beyond 65,504 for a byte to stand for.
+// What dtype holds: entries that are infinite in it do not fit, and no byte may stand for more than its largest value: 256
+// times the largest scale would (65,536, and 2^128).
 template <typename T> struct Range;
 template <> struct Range<__nv_bfloat16> {
     static __device__ __forceinline__ bool fits(float x) { return fabsf(x) < INFINITY; }
-    static __device__ __forceinline__ float most(float) { return 448.f; }
+    static __device__ __forceinline__ float most(float scale) { return scale == 0x1p120f ? 240.f : 448.f; }
 };
 template <> struct Range<__half> {
     static __device__ __forceinline__ bool fits(float x) { return fabsf(x) < 65520.f; }

@@ -604,8 +604,8 @@ vsa_status vsa_paged_attn(const vsa_paged_desc *desc, const void *q, int64_t q_s
  * divided by the growth and rounded again, which only changes what falls below
  * 2^-6 of the scale. So scales do not depend on how the tokens were cut
  * into calls, bytes only there, and a call made again gives the same result.
- * Infinities become NaN and, like NaN, do not count for the scale; fp16 entries
- * never round beyond 65504. k_mean: of the stored values, in the order of
+ * Infinities become NaN and, like NaN, do not count for the scale; entries
+ * never round beyond dtype's largest value. k_mean: of the stored values, in the order of
  * vsa_paged_append. */
 vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const void *k, int64_t k_stride, const void *v,
                              int64_t v_stride, const void *q, int64_t q_stride, void *q_out,

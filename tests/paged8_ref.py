@@ -23,7 +23,7 @@ def as_bytes(x, scale, dtype):
     """x fp32 (any shape) as e4m3 values of this scale, held in fp32."""
     x = x.float()
     fits = x.abs() < (math.inf if dtype == torch.bfloat16 else 65520.0)
-    most = 240.0 if dtype == torch.float16 and scale == 256.0 else 448.0
+    most = 240.0 if scale == (256.0 if dtype == torch.float16 else 2.0 ** 120) else 448.0
     y = (torch.where(fits, x, 0.0) / scale).clamp(-most, most).to(E4M3).float()  # a power of two: exact
     return torch.where(fits, y, math.nan)
 

@@ -112,7 +112,7 @@ def test_append_in_pieces(page):
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_append_of_extremes(dtype):
     """Zeros, the smallest and the largest entries, infinities and NaN."""
-    pool = Pool8("bshd", dtype, 1, 2, 16, 3, 2, [32], seed=1)
+    pool = Pool8("bshd", dtype, 2, 2, 16, 3, 2, [32], seed=1)
     k, v = torch.zeros(32, 2, D, dtype=dtype), torch.zeros(32, 2, D, dtype=dtype)
     big = torch.finfo(dtype).max
     k[3, 0, :4] = torch.tensor([big, -big, 1.0, torch.finfo(dtype).tiny / 4]).to(dtype)
@@ -128,8 +128,9 @@ def test_append_of_extremes(dtype):
     assert torch.isfinite(rk.cpu()[fine]).all() and torch.isnan(rk.cpu()[~fine]).all()
     top = k.float().abs()
     scale = pool.real(torch.ones(3, 16, 2, 1), pool.ks)[pool.table[0]].reshape(32, 2, 1)
-    # half a step of e4m3 (2^-4 relative, 2^-10 of the scale absolute), and what fp16's end cuts off
-    bound = top * 2.0 ** -4 + scale * 2.0 ** -10 + (4096.0 if dtype == HF else 0.0) * (top > 61440) + 2.0 ** -25
+    # half a step of e4m3 (2^-4 relative, 2^-10 of the scale absolute), and what lies beyond the last byte of dtype
+    most = 240.0 * (2.0 ** 8 if dtype == HF else 2.0 ** 120)
+    bound = top * 2.0 ** -4 + scale * 2.0 ** -10 + (top - most).clamp(min=0.0) + 2.0 ** -25
     assert ((rk.cpu().float() - k.float()).abs() <= bound)[fine].all()
 
 
@@ -466,12 +467,11 @@ def test_decoding_within_a_budget():
         assert torch.equal(res["q"].cpu(), q)
         equal_bytes(pool, cache)
         want = ref8.attend(pool, q, weight=mass)
-        ref.check_attend((res["out"], res["lse"]), want, f"step {i}")
+        ref.check_attend((res["out"], res["lse"]), want[:4], f"step {i}")
         # what the device holds decides (two pages may weigh the same to rounding): it is near the reference's, and the
         # eviction is right for it
         mass, slack = want[4], slack + want[5]
         counts = [-(-n // page) for n in pool.lens]
-        given = res.get("given")
         tables, new_lens = cache.page_table.tolist(), cache.seq_lens.tolist()
         for b in range(B):
             gone = int(res["cnt"][b])
@@ -496,7 +496,6 @@ def test_decoding_within_a_budget():
             cache.page_table[b, P - gone:] = i32(out_ids)
         assert new_lens == pool.lens
         assert ((weight.double().cpu() - mass).abs() <= slack).all()
-        del given
     assert evicted > 4
 
 
@@ -539,7 +538,7 @@ def test_selected_pages_of_an_8_bit_cache():
     wd = w.cuda()
     got = cache.attend(qq.cuda(), pages, page_weight=wd)
     full = ref8.attend(pool, qq, want, weight=w)
-    ref.check_attend(got, full)
+    ref.check_attend(got, full[:4])
     check_weights(pool, wd, full, w)
 
 
