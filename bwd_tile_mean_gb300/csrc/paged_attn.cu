@@ -30,8 +30,8 @@ vsa_status attn16(const AttnCall &c, cudaStream_t s) {
     AttnArgs a{};
     const vsa_status st = attn_args(c, false, &a);
     if (st != VSA_OK) return st;
-    if (c.weigh) return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 16, true>(a, s) : launch_attn<__half, 16, true>(a, s);
-    return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 16, false>(a, s) : launch_attn<__half, 16, false>(a, s);
+    if (c.weigh) return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 0, true>(a, s) : launch_attn<__half, 0, true>(a, s);
+    return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 0, false>(a, s) : launch_attn<__half, 0, false>(a, s);
 }
 
 }  // namespace vsa

@@ -427,36 +427,47 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 // for powers of two until a weight falls below 2^-24 (2^-38 of the largest
 // weight's at the largest scale's). The sum W of the rounded weights is taken
 // before, so that the weights that O is made with sum to one as above.
-// A row of 128 bytes is 8 chunks of 16, stored at chunk ^ (row % 8). As a B
-// fragment of K thread (g, t) reads bytes 32 t .. 32 t + 31 of key g, two
-// chunks, and takes word j for k-step j: the order of the dims among the k-steps
-// is free as long as Q's fragments have the same. V comes through transposing
-// 16-bit loads: a word holds dims 2 g, 2 g + 1 of keys 2 t, 2 t + 1; one byte
-// permutation and two conversions make it the fragments of two tiles, one of the
-// even and one of the odd dims, so a thread ends with dims 16 c + 4 t .. + 3.
-// Half the bytes of the 16-bit cache, twice the steps per byte.
+//
+// At half the bytes per key the instructions count: keys and dims are the rows
+// of the products here, the query heads their columns, NT tiles of 8. Up to 8
+// heads (NT = 1) that is half of the 16-bit walk's products, exponentials and
+// accumulators: 34 products, 128 conversions and 8 exponentials per thread and
+// step of 32 keys.
+//   S^T (keys x heads) = K (16 keys x 16 dims) Q^T, O^T (dims x heads) = V^T (16 dims x 16 keys) P^T
+// A row of 128 bytes is 8 chunks of 16, stored at chunk ^ (row % 8). Thread (g, t)
+// reads bytes 32 t .. 32 t + 31 of keys g and g + 8 of a block and takes word j for
+// k-step j: the order of the dims among the k-steps is free as long as Q's
+// fragments have the same. V comes through transposing 16-bit loads: a word holds
+// dims 2 g, 2 g + 1 of keys 2 t, 2 t + 1; a byte permutation and two conversions
+// make it rows g and g + 8 of a tile, which so are the dims 2 g and 2 g + 1 of its
+// 16. P^T is turned by movmatrix.
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
 
-// Q as A fragments in fp16: row g (and g + 8), k-step j at dims 32 t + 4 j .. + 3; qs the rows' powers of two.
-template <typename T>
-__device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, uint32_t (&qa)[8][4], float (&qs)[2]) {
+// Q as B fragments in fp16: head 8 n + g, k-step j at dims 32 t + 4 j .. + 3; qs: the powers of two of heads 8 n + 2 t + e.
+template <typename T, int NT>
+__device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, uint32_t (&qb)[NT][8][2], float (&qs)[2 * NT]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const T *qb = static_cast<const T *>(a.q) + (long long)sg.b * a.qs + (sg.hq0 - (long long)sg.b * a.p.Hq) * kD;
+    const T *from = static_cast<const T *>(a.q) + (long long)sg.b * a.qs + (sg.hq0 - (long long)sg.b * a.p.Hq) * kD;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int row = g + 8 * e;
+    for (int n = 0; n < NT; ++n) {
+        const int row = 8 * n + g;
         uint4 x[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            x[c] = row < sg.rows ? reinterpret_cast<const uint4 *>(qb + (long long)row * kD + 32 * t)[c] : make_uint4(0, 0, 0, 0);
+            x[c] = row < sg.rows ? reinterpret_cast<const uint4 *>(from + (long long)row * kD + 32 * t)[c] : make_uint4(0, 0, 0, 0);
         uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
-        qs[e] = 1.f;
+        float down = 1.f;
         if constexpr (!std::is_same<T, __half>::value) {
             float top = 0.f;
 #pragma unroll
@@ -466,10 +477,10 @@ __device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, ui
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // top = 1.m 2^n: to 2^14; an infinite top keeps its products infinite
-            const int n = top == 0.f ? 14 : clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 127);
-            const float up = power_of(14 - n);
-            qs[e] = power_of(n - 14);
+            // top = 1.m 2^e: to 2^14; an infinite top keeps its products infinite
+            const int e = top == 0.f ? 14 : clampi((int)(__float_as_uint(top) >> 23) - 127, -100, 127);
+            const float up = power_of(14 - e);
+            down = power_of(e - 14);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
                 const float2 v = unpack2<T>(w[i]);
@@ -477,25 +488,54 @@ __device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, ui
             }
         }
 #pragma unroll
+        for (int e = 0; e < 2; ++e) qs[2 * n + e] = __shfl_sync(0xffffffffu, down, 4 * (2 * t + e));
+#pragma unroll
         for (int j = 0; j < 8; ++j) {
-            qa[j][e] = w[2 * j];
-            qa[j][2 + e] = w[2 * j + 1];
+            qb[n][j][0] = w[2 * j];
+            qb[n][j][1] = w[2 * j + 1];
         }
     }
 }
 
-// stream_blocks for 8 bits. The outputs come back finished: divided by w, and scaled.
-template <bool kWeigh>
-__device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment &sg, const uint32_t (&qa)[8][4],
-                                               const float (&qs)[2], int len, int blk0, int nblk, uint32_t ring,
-                                               float (&m_run)[2], float (&l_run)[2], float (&w_run)[2], float (&acc)[16][4]) {
+// store_weights for the turned scores: sc[block][8 n + ..] has keys g, g + 8 by heads 2 t, 2 t + 1. The eight lanes of a
+// head add up; four of them end with one (block, head) each.
+template <int NT>
+__device__ __forceinline__ void store_weights8(const AttnArgs &a, const Segment &sg, int blk, int end, const float (&sc)[2][NT][4],
+                                               const float (&ref)[2 * NT]) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, e = g & 1, h = (g >> 1) & 1;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float s[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float v0 = sc[i][n][0] + sc[i][n][2], v1 = sc[i][n][1] + sc[i][n][3];
+            s[i] = (e ? v1 : v0) + __shfl_xor_sync(0xffffffffu, e ? v0 : v1, 4);
+        }
+        float sum = (h ? s[1] : s[0]) + __shfl_xor_sync(0xffffffffu, h ? s[0] : s[1], 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = 8 * n + 2 * t + e;
+        if (g < 4 && row < sg.rows && blk + h < end)
+            a.bw[(sg.id * a.blocks + blk + h) * a.rows + row] = make_float2(sum, e ? ref[2 * n + 1] : ref[2 * n]);
+    }
+}
+
+// stream_blocks for 8 bits: m_run, l_run, w_run of heads 8 n + 2 t + e at 2 n + e, their outputs' dims 16 j + 2 g and + 1 in
+// acc[8 n + j][e] and [2 + e], finished: divided by w, and scaled.
+template <int NT, bool kWeigh>
+__device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment &sg, const uint32_t (&qb)[NT][8][2],
+                                               const float (&qs)[2 * NT], int len, int blk0, int nblk, uint32_t ring,
+                                               float (&m_run)[2 * NT], float (&l_run)[2 * NT], float (&w_run)[2 * NT],
+                                               float (&acc)[8 * NT][4]) {
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, b = sg.b, bh = sg.bh;
     const unsigned char *K = static_cast<const unsigned char *>(a.k), *V = static_cast<const unsigned char *>(a.v);
     // q of 2^14 and more with the largest softmax scales: still a finite multiple of differences that may be 0
-    const float sl2[2] = {fminf(p.scale * kLog2e * qs[0], FLT_MAX), fminf(p.scale * kLog2e * qs[1], FLT_MAX)};
+    float sl2[2 * NT];
+#pragma unroll
+    for (int e = 0; e < 2 * NT; ++e) sl2[e] = fminf(p.scale * kLog2e * qs[e], FLT_MAX);
     constexpr float kLift = 14.f, kDrop = 0x1p-14f;
     constexpr int kStage8 = stage_bytes<8>;
+    constexpr uint32_t kOnes[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
     const int key0 = blk0 * kBlk;
     // Window of up to 32 blocks, one per lane: page (or -1), slot, valid slots and scales.
     int w_id = -1, w_slot = 0, w_valid = 0, w_base = -32;
@@ -572,11 +612,15 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         scales(0);
     }
 
-    m_run[0] = m_run[1] = -INFINITY;
-    l_run[0] = l_run[1] = 0.f;
-    float wsum[4] = {0.f, 0.f, 0.f, 0.f}, vrun = 0x1p-126f;
+    float wsum[NT][4], vrun = 0x1p-126f;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int e = 0; e < 2 * NT; ++e) m_run[e] = -INFINITY, l_run[e] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) wsum[n][e] = 0.f;
+#pragma unroll
+    for (int j = 0; j < 8 * NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
     for (int i = 0; i < steps; ++i) {
@@ -588,12 +632,13 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
             copy(K, free_slot);
         }
         cp_commit();
-        float sc[4][4];  // keys 8 u + 2 t, + 1 of rows g, g + 8
+        float sc[2][NT][4];  // block h: keys g, g, g + 8, g + 8 by heads 8 n + 2 t, + 1, ..
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][e] = 0.f;
-        }
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[h][n][e] = 0.f;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {  // bytes 32 t + 16 half ..
             uint4 kw[4];
@@ -602,9 +647,13 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const uint32_t w = j == 0 ? kw[u].x : j == 1 ? kw[u].y : j == 2 ? kw[u].z : kw[u].w;
-                    mma16816<__half>(sc[u], qa[4 * half + j], half2_of(w), half2_of(w >> 16));
+                for (int h = 0; h < 2; ++h) {
+                    const uint4 &x = kw[2 * h], &y = kw[2 * h + 1];
+                    const uint32_t lo = j == 0 ? x.x : j == 1 ? x.y : j == 2 ? x.z : x.w;
+                    const uint32_t hi = j == 0 ? y.x : j == 1 ? y.y : j == 2 ? y.z : y.w;
+                    const uint32_t ka[4] = {half2_of(lo), half2_of(hi), half2_of(lo >> 16), half2_of(hi >> 16)};
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma16816<__half>(sc[h][n], ka, qb[n][4 * half + j][0], qb[n][4 * half + j][1]);
                 }
         }
         cp_wait<1>();
@@ -617,93 +666,108 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         for (int f = 0; f < 8; ++f)  // f = 4 h + j: dims 32 j .. of block h
             ldsm4t(vb[f], v_slot + ((f >> 2) * kBlk + vrow) * 128 + (((2 * (f & 3) + vc0) ^ (vrow & 7)) << 4));
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[u][e] *= ksc[u >> 1];
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[h][n][e] *= ksc[h];
         if (live[0] + live[1] < 2 * kBlk) {
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (8 * (u & 1) + 2 * t + (e & 1) >= live[u >> 1]) sc[u][e] = -INFINITY;
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (g + 8 * (e >> 1) >= live[h]) sc[h][n][e] = -INFINITY;
         }
         // vrun: the power of two at or below the largest scale so far; a block's ratio to it is below 2
-        float ratio[2] = {1.f, 1.f}, vcorr = 1.f;
+        float ratio[2], vcorr = 1.f;
         {
             const float top = fmaxf(vsc[0], vsc[1]);
             const float to = fmaxf(vrun, __uint_as_float(__float_as_uint(top) & 0x7f800000u));
             if (to != vrun) vcorr = vrun / to, vrun = to;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) ratio[h] = vsc[h] / vrun;
+            for (int h = 0; h < 2; ++h) ratio[h] = vsc[h] == vrun ? 1.f : vsc[h] / vrun;
         }
-        float corr[2];
+        float corr[2 * NT];
         bool moved = vcorr != 1.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            float mx = ptx::fmax3(sc[0][2 * e], sc[0][2 * e + 1], sc[1][2 * e]);
-            mx = ptx::fmax3(mx, sc[1][2 * e + 1], sc[2][2 * e]);
-            mx = ptx::fmax3(mx, sc[2][2 * e + 1], sc[3][2 * e]);
-            mx = fmaxf(mx, sc[3][2 * e + 1]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = ptx::fmax3(m_run[e], mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            moved = moved || mx != m_run[e];
-            const float ref = mx == -INFINITY ? 0.f : mx;
-            corr[e] = ptx::ex2((m_run[e] - ref) * sl2[e]);
-            m_run[e] = mx;
-            float sum = 0.f;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * n + e;
+                float mx = fmaxf(ptx::fmax3(sc[0][n][e], sc[0][n][2 + e], sc[1][n][e]), sc[1][n][2 + e]);
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                mx = ptx::fmax3(m_run[r], mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                moved = moved || mx != m_run[r];
+                const float ref = mx == -INFINITY ? 0.f : mx;  // a row without keys so far
+                corr[r] = ptx::ex2((m_run[r] - ref) * sl2[r]);
+                m_run[r] = mx;
+                float sum = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const float pr = ptx::ex2(fmaf(sc[u][2 * e + c] - ref, sl2[e], kLift));
-                    sc[u][2 * e + c] = pr;
-                    sum += pr;
-                }
-            l_run[e] = fmaf(l_run[e], corr[e], sum);
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const float pr = ptx::ex2(fmaf(sc[h][n][2 * c + e] - ref, sl2[r], kLift));
+                        sc[h][n][2 * c + e] = pr;
+                        sum += pr;
+                    }
+                l_run[r] = fmaf(l_run[r], corr[r], sum);  // this lane's keys; the eight of a head are joined at the end
+            }
+        if constexpr (kWeigh) {
+            float ref[2 * NT];
+#pragma unroll
+            for (int r = 0; r < 2 * NT; ++r) ref[r] = m_run[r] * sl2[r];
+            store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, ref);
         }
-        if constexpr (kWeigh) store_weights(a, sg, blk0 + 2 * i, blk0 + nblk, sc, m_run[0] * sl2[0], m_run[1] * sl2[1]);
         if (__any_sync(0xffffffffu, moved)) {
-            wsum[0] *= corr[0], wsum[1] *= corr[0], wsum[2] *= corr[1], wsum[3] *= corr[1];
-            const float c0 = corr[0] * vcorr, c1 = corr[1] * vcorr;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                acc[j][0] *= c0;
-                acc[j][1] *= c0;
-                acc[j][2] *= c1;
-                acc[j][3] *= c1;
+            for (int n = 0; n < NT; ++n) {
+                wsum[n][0] *= corr[2 * n], wsum[n][1] *= corr[2 * n + 1];
+                const float c0 = corr[2 * n] * vcorr, c1 = corr[2 * n + 1] * vcorr;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[8 * n + j][0] *= c0;
+                    acc[8 * n + j][1] *= c1;
+                    acc[8 * n + j][2] *= c0;
+                    acc[8 * n + j][3] *= c1;
+                }
             }
         }
-        uint32_t pa[2][4];
+        uint32_t pb[2][NT][2];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                pa[h][2 * u] = pack2<__half>(sc[2 * h + u][0], sc[2 * h + u][1]);
-                pa[h][2 * u + 1] = pack2<__half>(sc[2 * h + u][2], sc[2 * h + u][3]);
+            for (int n = 0; n < NT; ++n) {
+                pb[h][n][0] = turn8x8(pack2<__half>(sc[h][n][0], sc[h][n][1]));
+                pb[h][n][1] = turn8x8(pack2<__half>(sc[h][n][2], sc[h][n][3]));
+                mma16816<__half>(wsum[n], kOnes, pb[h][n][0], pb[h][n][1]);
             }
-        mma16816<__half>(wsum, pa[0], 0x3C003C00u, 0x3C003C00u);
-        mma16816<__half>(wsum, pa[1], 0x3C003C00u, 0x3C003C00u);
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (ratio[h] != 1.f) {  // the same for the whole warp; in two factors that fp16 holds in full
                 const float hi = fmaxf(ratio[h], 0x1p-14f), lo = ratio[h] / hi;
                 const __half2 r1 = __float2half2_rn(hi), r2 = __float2half2_rn(lo);
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    __half2 x = *reinterpret_cast<__half2 *>(&pa[h][u]);
-                    x = __hmul2(x, r1);
-                    if (lo != 1.f) x = __hmul2(x, r2);
-                    pa[h][u] = *reinterpret_cast<uint32_t *>(&x);
-                }
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        __half2 x = *reinterpret_cast<__half2 *>(&pb[h][n][u]);
+                        x = __hmul2(x, r1);
+                        if (lo != 1.f) x = __hmul2(x, r2);
+                        pb[h][n][u] = *reinterpret_cast<uint32_t *>(&x);
+                    }
             }
 #pragma unroll
         for (int f = 0; f < 8; ++f)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const uint32_t lo = __byte_perm(vb[f][2 * c], 0, 0x3120), hi = __byte_perm(vb[f][2 * c + 1], 0, 0x3120);
-                const int j = 4 * (f & 3) + 2 * c;
-                mma16816<__half>(acc[j], pa[f >> 2], half2_of(lo), half2_of(hi));
-                mma16816<__half>(acc[j + 1], pa[f >> 2], half2_of(lo >> 16), half2_of(hi >> 16));
+                const uint32_t va[4] = {half2_of(lo), half2_of(lo >> 16), half2_of(hi), half2_of(hi >> 16)};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816<__half>(acc[8 * n + 2 * (f & 3) + c], va, pb[f >> 2][n][0], pb[f >> 2][n][1]);
             }
         const uint32_t was_k = k_slot;
         k_slot = free_slot;
@@ -714,49 +778,62 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
     cp_wait<0>();
     __syncwarp();  // the warp's ring is free
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
-        l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
-        l_run[e] *= kDrop;
-        m_run[e] *= sl2[e];  // log2 units from here on
-        w_run[e] = wsum[2 * e];
-        const float inv = w_run[e] == 0.f ? 0.f : 1.f / w_run[e];
+    for (int r = 0; r < 2 * NT; ++r) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            acc[j][2 * e] = acc[j][2 * e] * inv * vrun;
-            acc[j][2 * e + 1] = acc[j][2 * e + 1] * inv * vrun;
+        for (int off = 4; off < 32; off <<= 1) l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], off);
+        l_run[r] *= kDrop;
+        m_run[r] *= sl2[r];  // log2 units from here on
+        w_run[r] = wsum[r >> 1][r & 1];
+        const float inv = w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float &x = acc[8 * (r >> 1) + j][2 * c + (r & 1)];
+                x = x * inv * vrun;
+            }
+    }
+}
+
+// Where a warp's results of a segment are: NT = 0 is the 16-bit walk, 1 and 2 the 8-bit one's tiles of heads.
+template <int NT> struct Frag {
+    static constexpr bool k8 = NT > 0;
+    static constexpr int kv = k8 ? 8 : 16, R = k8 ? 2 * NT : 2, A = k8 ? 8 * NT : 16;
+    static __device__ __forceinline__ int row(int r) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        return k8 ? 8 * (r >> 1) + 2 * t + (r & 1) : g + 8 * r;
+    }
+    // one of the lanes that hold row(r)'s sums
+    static __device__ __forceinline__ bool tells() { return k8 ? (threadIdx.x & 31) < 4 : (threadIdx.x & 3) == 0; }
+    // f(d, x) for a thread's parts x of row(r), at dims d and d + 1
+    template <typename F> static __device__ __forceinline__ void each(const float (&acc)[A][4], int r, F f) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        if constexpr (k8) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f(16 * j + 2 * g, make_float2(acc[8 * (r >> 1) + j][r & 1], acc[8 * (r >> 1) + j][2 + (r & 1)]));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f(8 * j + 2 * t, make_float2(acc[j][2 * r], acc[j][2 * r + 1]));
         }
     }
-}
-
-template <typename T, int KV>
-__device__ __forceinline__ void load_queries(const AttnArgs &a, const Segment &sg, uint32_t (&qa)[8][4], float (&qs)[2]) {
-    if constexpr (KV == 8)
-        load_q8<T>(a, sg, qa, qs);
-    else
-        load_q<T>(a, sg, qa);
-}
-template <typename T, int KV, bool kWeigh>
-__device__ __forceinline__ void stream(const AttnArgs &a, const Segment &sg, const uint32_t (&qa)[8][4], const float (&qs)[2],
-                                       int len, int blk0, int nblk, uint32_t ring, float (&m_run)[2], float (&l_run)[2],
-                                       float (&w_run)[2], float (&acc)[16][4]) {
-    if constexpr (KV == 8)
-        stream_blocks8<kWeigh>(a, sg, qa, qs, len, blk0, nblk, ring, m_run, l_run, w_run, acc);
-    else
-        stream_blocks<T, kWeigh>(a, sg, qa, len, blk0, nblk, ring, m_run, l_run, w_run, acc);
-}
-
-// f(d, x) for a thread's parts x of row g + 8 e of acc, at dims d..
-template <int KV, typename F> __device__ __forceinline__ void each_part(const float (&acc)[16][4], int e, int t, F f) {
-    if constexpr (KV == 8) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 2)
-            f(8 * j + 4 * t, make_float4(acc[j][2 * e], acc[j + 1][2 * e], acc[j][2 * e + 1], acc[j + 1][2 * e + 1]));
+};
+// The queries, and the walk with them.
+template <typename T, int NT, bool kWeigh>
+__device__ __forceinline__ void attend_blocks(const AttnArgs &a, const Segment &sg, int len, int blk0, int nblk, uint32_t ring,
+                                              float (&m_run)[Frag<NT>::R], float (&l_run)[Frag<NT>::R],
+                                              float (&w_run)[Frag<NT>::R], float (&acc)[Frag<NT>::A][4]) {
+    if constexpr (NT > 0) {
+        uint32_t qb[NT][8][2];
+        float qs[2 * NT];
+        load_q8<T, NT>(a, sg, qb, qs);
+        stream_blocks8<NT, kWeigh>(a, sg, qb, qs, len, blk0, nblk, ring, m_run, l_run, w_run, acc);
     } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f(8 * j + 2 * t, make_float2(acc[j][2 * e], acc[j][2 * e + 1]));
+        uint32_t qa[8][4];
+        load_q<T>(a, sg, qa);
+        stream_blocks<T, kWeigh>(a, sg, qa, len, blk0, nblk, ring, m_run, l_run, w_run, acc);
     }
 }
+
 // What a piece's output counts for in a join beyond its maximum: unnormalised
 // outputs hold their weights, finished ones (8 bits) do not.
 template <int KV> __device__ __forceinline__ float own_weight(float w) { return KV == 8 ? w : 1.f; }
@@ -768,22 +845,24 @@ template <int KV> __device__ __forceinline__ float own_weight(float w) { return 
 // The rows' weights come first, side by side: one after another, with the
 // division and the logarithm of each, 16 rows took 2.4 us more than 5.
 // The warps' rings hold the outputs meanwhile.
-template <int KV, typename S, typename F>
-__device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const float (&m_run)[2], const float (&l_run)[2],
-                                           const float (&w_run)[2], const float (&acc)[16][4], bool done, S stat, F out) {
+template <int NT, typename S, typename F>
+__device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const float (&m_run)[Frag<NT>::R],
+                                           const float (&l_run)[Frag<NT>::R], const float (&w_run)[Frag<NT>::R],
+                                           const float (&acc)[Frag<NT>::A][4], bool done, S stat, F out) {
+    constexpr int KV = Frag<NT>::kv;
     __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows], s_w[kWarps][kRows], s_f[kWarps][kRows];
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     float *so = reinterpret_cast<float *>(smem + wid * kStages * stage_bytes<KV>);
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        const int row = g + 8 * e;
-        if (t == 0) {
-            s_m[wid][row] = m_run[e];
-            s_l[wid][row] = l_run[e];
-            s_w[wid][row] = w_run[e];
+    for (int r = 0; r < Frag<NT>::R; ++r) {
+        const int row = Frag<NT>::row(r);
+        if (Frag<NT>::tells()) {
+            s_m[wid][row] = m_run[r];
+            s_l[wid][row] = l_run[r];
+            s_w[wid][row] = w_run[r];
         }
         if (row < rows)
-            each_part<KV>(acc, e, t, [&](int d, auto x) { *reinterpret_cast<decltype(x) *>(so + row * kPitch + d) = x; });
+            Frag<NT>::each(acc, r, [&](int d, float2 x) { *reinterpret_cast<float2 *>(so + row * kPitch + d) = x; });
     }
     __syncthreads();
     if (tid < kWarps * kRows) {  // the warps' weights
@@ -832,7 +911,8 @@ __device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -I
 // half the products too: the four warps' copies and fragment loads are 128 KB
 // a step through the SM's shared memory, 1,000 cycles. So few segments want
 // many CTAs.
-template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
+template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_cluster(AttnArgs a) {
+    constexpr int KV = Frag<NT>::kv;
     extern __shared__ __align__(128) unsigned char smem[];
     // [cluster][rows of this CTA]: a power of two times ceil(rows / it), 16 at most
     __shared__ __align__(16) float s_part[kRows][kD];
@@ -846,18 +926,15 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
     const int bh = segment / a.rc;
     const Segment sg = segment_of(a, bh, segment % a.rc);
     const int len = paged_len(a.p, sg.b), nb = seg_blocks(a, a.idx ? bh : sg.b);
-    uint32_t qa[8][4];
-    float qs[2];
-    load_queries<T, KV>(a, sg, qa, qs);
     const int per = (nb + CS * kWarps - 1) / (CS * kWarps);
     const int blk0 = min((rank * kWarps + wid) * per, nb), nblk = min(per, nb - blk0);
-    float m_run[2], l_run[2], w_run[2], acc[16][4];
-    stream<T, KV, kWeigh>(a, sg, qa, qs, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * stage_bytes<KV>, m_run,
-                          l_run, w_run, acc);
+    float m_run[Frag<NT>::R], l_run[Frag<NT>::R], w_run[Frag<NT>::R], acc[Frag<NT>::A][4];
+    attend_blocks<T, NT, kWeigh>(a, sg, len, blk0, nblk, ptx::smem_addr(smem) + wid * kStages * stage_bytes<KV>, m_run, l_run,
+                                 w_run, acc);
     grid_go();
     T *out = static_cast<T *>(a.out);
     if (CS == 1) {
-        join_warps<KV>(
+        join_warps<NT>(
             smem, sg.rows, m_run, l_run, w_run, acc, true,
             [&](int row, float4 s) { a.lse[sg.hq0 + row] = lse_of(s.x, s.y); },
             [&](int row, float4 o) {
@@ -869,7 +946,7 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");  // every CTA of the cluster runs
     const auto part = [&](int row) { return rank * own + (row >> lg); };
     const auto to = [&](int row) { return (uint32_t)(row & (CS - 1)); };
-    join_warps<KV>(
+    join_warps<NT>(
         smem, sg.rows, m_run, l_run, w_run, acc, false,
         [&](int row, float4 s) { st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), s); },
         [&](int row, float4 o) {
@@ -905,10 +982,11 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
 // (504 MB): 82 to 84 us with the join, 88 to 90% of the measured copy rate (99% at
 // four times the bytes); of the rest 3.5 us are the start of a CTA (scan, length,
 // page id, first keys) and 4 the join.
-template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
+template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
+    constexpr int KV = Frag<NT>::kv;
     extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     grid_wait();
     const int N = a.idx ? p.B * p.Hkv : p.B;       // list entries
     const int mult = a.idx ? a.rc : p.Hkv * a.rc;  // segments per entry
@@ -945,15 +1023,12 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
             off += skip - kLead;
             take -= skip;
         }
-        const int r = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
-        const Segment sg = segment_of(a, bh, r);
+        const int chunk = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
+        const Segment sg = segment_of(a, bh, chunk);
         const int len = paged_len(p, sg.b);
-        uint32_t qa[8][4];
-        float qs[2];
-        load_queries<T, KV>(a, sg, qa, qs);
-        float m_run[2], l_run[2], w_run[2], acc[16][4];
-        stream<T, KV, kWeigh>(a, sg, qa, qs, len, off, take, ptx::smem_addr(smem) + wid * kStages * stage_bytes<KV>, m_run,
-                              l_run, w_run, acc);
+        float m_run[Frag<NT>::R], l_run[Frag<NT>::R], w_run[Frag<NT>::R], acc[Frag<NT>::A][4];
+        attend_blocks<T, NT, kWeigh>(a, sg, len, off, take, ptx::smem_addr(smem) + wid * kStages * stage_bytes<KV>, m_run,
+                                     l_run, w_run, acc);
         if (x >= x_end) grid_go();
 
         // A piece of the segment that begins it describes all of its pieces.
@@ -969,11 +1044,11 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
                 d.z = cb - ca;
                 d.w = d.y + d.z + max(0, w_last + 1 - cb * kWarps);
             }
-            a.seg[(long long)bh * a.rc + r] = d;
+            a.seg[(long long)bh * a.rc + chunk] = d;
         }
         if (joined) {
             const bool whole = first && last;
-            join_warps<KV>(
+            join_warps<NT>(
                 smem, sg.rows, m_run, l_run, w_run, acc, whole,
                 [&](int row, float4 s) {
                     if (whole)
@@ -990,23 +1065,20 @@ template <typename T, int KV, bool kWeigh> __global__ void __launch_bounds__(kWa
             return;
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int row = g + 8 * e;
+        for (int r = 0; r < Frag<NT>::R; ++r) {
+            const int row = Frag<NT>::row(r);
             if (row >= sg.rows) continue;
             if (first && last) {
+                const float inv = KV == 8 ? 1.f : w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
                 T *dst = out + (sg.hq0 + row) * kD;
-                const float inv = w_run[e] == 0.f ? 0.f : 1.f / w_run[e];
-                each_part<KV>(acc, e, t, [&](int d, auto x) {
-                    if constexpr (KV == 8)
-                        *reinterpret_cast<uint2 *>(dst + d) = pack4<T>(x);
-                    else
-                        *reinterpret_cast<uint32_t *>(dst + d) = pack2<T>(x.x * inv, x.y * inv);
+                Frag<NT>::each(acc, r, [&](int d, float2 x) {
+                    *reinterpret_cast<uint32_t *>(dst + d) = pack2<T>(x.x * inv, x.y * inv);
                 });
-                if (t == 0) a.lse[sg.hq0 + row] = lse_of(m_run[e], l_run[e]);
+                if (Frag<NT>::tells()) a.lse[sg.hq0 + row] = lse_of(m_run[r], l_run[r]);
             } else {
                 float *dst = a.o + (slot * a.rows + row) * kD;
-                each_part<KV>(acc, e, t, [&](int d, auto x) { *reinterpret_cast<decltype(x) *>(dst + d) = x; });
-                if (t == 0) a.ml[slot * a.rows + row] = make_float4(m_run[e], l_run[e], w_run[e], 0.f);
+                Frag<NT>::each(acc, r, [&](int d, float2 x) { *reinterpret_cast<float2 *>(dst + d) = x; });
+                if (Frag<NT>::tells()) a.ml[slot * a.rows + row] = make_float4(m_run[r], l_run[r], w_run[r], 0.f);
             }
         }
     }
@@ -1135,10 +1207,11 @@ inline bool grows(int c, long long segments, long long keys) {
     return c == 4 ? segments <= 32 && keys > 768 : segments <= 14 && keys > 1024;
 }
 
-template <typename T, int KV, bool kWeigh> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
-    constexpr int smem = smem_bytes<KV>;
+// NT: the tiles of heads of an 8-bit cache's walk, 0: 16 bits.
+template <typename T, int NT, bool kWeigh> vsa_status launch_attn(const AttnArgs &a, cudaStream_t s) {
+    constexpr int KV = Frag<NT>::kv, smem = smem_bytes<KV>;
     if (a.cluster) {
-        const auto kernel = k_paged_attn_cluster<T, KV, kWeigh>;
+        const auto kernel = k_paged_attn_cluster<T, NT, kWeigh>;
         cudaError_t e = ensure_smem_limit((const void *)kernel, smem);
         if (e == cudaSuccess && a.cluster > 8) e = ensure_wide_clusters((const void *)kernel);
         if (e != cudaSuccess) return status_from_cuda(e);
@@ -1148,7 +1221,7 @@ template <typename T, int KV, bool kWeigh> vsa_status launch_attn(const AttnArgs
         prof_end(s);
         return status_from_cuda(e);
     }
-    const auto kernel = k_paged_attn_runs<T, KV, kWeigh>;
+    const auto kernel = k_paged_attn_runs<T, NT, kWeigh>;
     cudaError_t e = ensure_smem_limit((const void *)kernel, smem);
     if (e != cudaSuccess) return status_from_cuda(e);
     prof_begin(KV == 8 ? "paged8_attn" : "paged_attn", s);

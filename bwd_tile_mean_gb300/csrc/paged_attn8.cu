@@ -4,12 +4,18 @@
 
 namespace vsa {
 
+namespace {
+template <typename T> vsa_status launch8(const AttnArgs &a, bool weigh, cudaStream_t s) {
+    if (a.rows <= 8) return weigh ? launch_attn<T, 1, true>(a, s) : launch_attn<T, 1, false>(a, s);
+    return weigh ? launch_attn<T, 2, true>(a, s) : launch_attn<T, 2, false>(a, s);
+}
+}  // namespace
+
 vsa_status attn8(const AttnCall &c, cudaStream_t s) {
     AttnArgs a{};
     const vsa_status st = attn_args(c, true, &a);
     if (st != VSA_OK) return st;
-    if (c.weigh) return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 8, true>(a, s) : launch_attn<__half, 8, true>(a, s);
-    return a.p.dtype == T_BF16 ? launch_attn<__nv_bfloat16, 8, false>(a, s) : launch_attn<__half, 8, false>(a, s);
+    return a.p.dtype == T_BF16 ? launch8<__nv_bfloat16>(a, c.weigh, s) : launch8<__half>(a, c.weigh, s);
 }
 
 }  // namespace vsa
