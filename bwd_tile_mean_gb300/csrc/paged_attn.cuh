@@ -62,7 +62,12 @@ constexpr int kBlk = 16;        // keys per block; a warp takes two per step
 constexpr int kRows = 16;       // query heads per segment at most
 constexpr int kLead = 4;        // blocks a segment counts for beyond its own (its start-up time): 0, 1, 2, 3, 4
                                 // measured 102, 92, 87, 85.1, 84.8 us on 64 sequences of 37 to 16,000 keys
+// The same of an 8-bit cache, whose blocks stream in half the time: 4, 8, 12, 16 measured 81, 74.9, 75.5, 74.8 us on the
+// same lengths.
+constexpr int kLead8 = 8;
 constexpr int kAlignedKeys = 1280;  // keys per CTA up to which segments of unknown lengths get a cluster each
+constexpr int kAlignedKeys8 = 800;  // of an 8-bit cache: 8 heads of 16,000 keys in clusters of 16 14.0 us, 12.5 in runs; 3 of
+                                    // 8,000 7.6, 8.7
 constexpr int kFewCtas = 912;       // and CTAs in all, three at each place: 1,192 segments of 17 keys 11.6 us, 7.6 in runs;
                                     // 800 of 64 11.9, 14.2
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe
@@ -983,7 +988,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
 // four times the bytes); of the rest 3.5 us are the start of a CTA (scan, length,
 // page id, first keys) and 4 the join.
 template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
-    constexpr int KV = Frag<NT>::kv;
+    constexpr int KV = Frag<NT>::kv, kFront = KV == 8 ? kLead8 : kLead;
     extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -992,7 +997,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
     const int mult = a.idx ? a.rc : p.Hkv * a.rc;  // segments per entry
     auto weight = [&](int n) {
         const int nb = seg_blocks(a, n);
-        return nb > 0 ? nb + kLead : 0;
+        return nb > 0 ? nb + kFront : 0;
     };
     const Run run = find_run<kWarps>(
         N, [&](int n) -> long long { return (long long)weight(n) * mult; }, kCtas * kWarps, 1, kWarps);
@@ -1019,8 +1024,8 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
         const bool last = joined ? run.x1 == seg0 + nb : off + take == nb;
         x += take;
         {   // the piece's own blocks: those behind the lead
-            const int skip = clampi(kLead - off, 0, take);
-            off += skip - kLead;
+            const int skip = clampi(kFront - off, 0, take);
+            off += skip - kFront;
             take -= skip;
         }
         const int chunk = sub % a.rc, bh = a.idx ? n : n * p.Hkv + sub / a.rc;
@@ -1276,8 +1281,10 @@ inline vsa_status attn_args(const AttnCall &c, bool eight, AttnArgs *args) {
     const long long segments = (long long)a.p.B * a.p.Hkv * a.rc;
     int cluster = 1;
     while (cluster < kMaxCluster && grows(cluster, segments, most)) cluster *= 2;
-    const bool even = c.idx || a.p.B == 1;
-    const bool few = most <= (long long)kAlignedKeys * cluster && segments * cluster <= kFewCtas;
+    // An 8-bit cache's runs keep more warps on each SM than a cluster's place on it leaves: 24 heads of 4,000, 16,000,
+    // 122,880 keys 8.9 / 10.9, 25.2 / 19.7, 145 / 117.
+    const bool even = !eight && (c.idx || a.p.B == 1);
+    const bool few = most <= (long long)(eight ? kAlignedKeys8 : kAlignedKeys) * cluster && segments * cluster <= kFewCtas;
     a.cluster = few || (even && segments * cluster >= kAlignedCtas) ? cluster : 0;
     char *w = static_cast<char *>(c.ws);
     a.seg = reinterpret_cast<int4 *>(w + ws.seg);

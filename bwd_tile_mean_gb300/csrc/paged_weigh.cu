@@ -26,47 +26,61 @@ struct WeighArgs {
     const float *in;       // [B, Hkv, max_pages]
     float *out;
     float decay, drop;     // drop: the attention's lift of P, undone
+    int lanes;             // per page: as many as it has records, up to 32
 };
-constexpr int kWeighThreads = 128;
+constexpr int kWeighThreads = 256;
+constexpr int kWeighDeep = 4;  // pages per group of lanes
 
-// Sum of P over `n` blocks from entry block `blk` of list row bh, all of its query heads.
-__device__ __forceinline__ float mass_of(const WeighArgs &a, long long bh, int blk, int n) {
+// Sum of P over `n` blocks from entry block `blk` of list row bh, all of its query heads: by the L lanes (a power of two
+// up to 32) of a group; `me` is a lane's place in it. The records of a page lie side by side: a group reads them together.
+__device__ __forceinline__ float mass_of(const WeighArgs &a, long long bh, int blk, int n, int me) {
     const Paged &p = a.p;
-    const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv);
+    const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
     const float *lse = a.lse + (long long)b * p.Hq + h * p.G;
     float mass = 0.f;
     for (int r = 0; r < a.rc; ++r) {
         const int rows = min(a.rows, p.G - r * a.rows);
         const float2 *w = a.bw + ((bh * a.rc + r) * a.blocks + blk) * a.rows;
-        for (int i = 0; i < rows; ++i) {
-            const float ref = lse[r * a.rows + i] * kLog2e;
-            for (int k = 0; k < n; ++k) {
-                const float2 x = w[k * a.rows + i];
-                if (x.x != 0.f) mass += x.x * ptx::ex2(x.y - ref);
-            }
+        for (int k = me; k < n * a.rows; k += a.lanes) {
+            const int i = k % a.rows;
+            if (i >= rows) continue;  // the last chunk of a group may have fewer heads
+            const float2 x = w[k];
+            if (x.x != 0.f) mass += x.x * ptx::ex2(x.y - lse[r * a.rows + i] * kLog2e);
         }
     }
-    return mass * a.drop;
+    return mass;
 }
-__device__ __forceinline__ float aged(const WeighArgs &a, long long at) { return a.decay == 0.f ? 0.f : a.decay * a.in[at]; }
+// ... over the group, in every lane of it; whole warp.
+__device__ __forceinline__ float group_sum(const WeighArgs &a, float x) {
+    for (int off = 1; off < a.lanes; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    return x * a.drop;
+}
 
-// All pages: one thread per page.
+// All pages: kWeighDeep pages per group of lanes. 64 sequences of up to 16,000 keys x 8 heads with 4 queries each, 94,000
+// blocks: 14 us with a thread per page, which reads its records one after another.
 __global__ void __launch_bounds__(kWeighThreads) k_page_weigh(WeighArgs a) {
     const Paged &p = a.p;
-    const int chunks = (p.max_pages + kWeighThreads - 1) / kWeighThreads;
+    const int per = kWeighThreads / a.lanes, span = per * kWeighDeep, chunks = (p.max_pages + span - 1) / span;
     const long long bh = blockIdx.x / chunks;
-    const int j = (int)(blockIdx.x % chunks) * kWeighThreads + threadIdx.x;
+    const int me = threadIdx.x & (a.lanes - 1), j0 = (int)(blockIdx.x - bh * chunks) * span + threadIdx.x / a.lanes;
     grid_wait();
     grid_go();
-    if (j >= p.max_pages) return;
-    const int len = paged_len(p, (int)(bh / p.Hkv)), from = j << p.page_log2;
-    const long long at = bh * p.max_pages + j;
-    if (from < len) {
-        const int live = min(len - from, p.page);
-        const float mass = mass_of(a, bh, from / 16, (live + 15) / 16);
-        a.out[at] = a.decay == 0.f ? mass : fmaf(a.decay, a.in[at], mass);
-    } else if (a.out != a.in) {
-        a.out[at] = a.in[at];
+    const int len = paged_len(p, (int)(bh / p.Hkv));
+    float mass[kWeighDeep], old[kWeighDeep];
+#pragma unroll
+    for (int d = 0; d < kWeighDeep; ++d) {
+        const int j = j0 + d * per;
+        const long long from = (long long)j << p.page_log2, at = bh * p.max_pages + j;
+        const bool live = from < len;
+        mass[d] = live ? mass_of(a, bh, (int)(from / 16), (int)((min(len - from, (long long)p.page) + 15) / 16), me) : 0.f;
+        old[d] = j < p.max_pages && me == 0 && !(live && a.decay == 0.f) ? a.in[at] : 0.f;
+    }
+#pragma unroll
+    for (int d = 0; d < kWeighDeep; ++d) {
+        const int j = j0 + d * per;
+        const bool live = (long long)j << p.page_log2 < len;
+        const float sum = group_sum(a, mass[d]);
+        if (me == 0 && j < p.max_pages) a.out[bh * p.max_pages + j] = live ? fmaf(a.decay, old[d], sum) : old[d];
     }
 }
 
@@ -85,7 +99,7 @@ __global__ void __launch_bounds__(kWeighThreads) k_page_weigh_listed(WeighArgs a
     for (int j = tid; j < p.max_pages; j += kWeighThreads) {
         const long long at = bh * p.max_pages + j;
         if ((long long)j << p.page_log2 < len) {
-            if (a.decay != 1.f || a.out != a.in) a.out[at] = aged(a, at);
+            if (a.decay != 1.f || a.out != a.in) a.out[at] = a.decay == 0.f ? 0.f : a.decay * a.in[at];
         } else if (a.out != a.in) {
             a.out[at] = a.in[at];
         }
@@ -93,18 +107,18 @@ __global__ void __launch_bounds__(kWeighThreads) k_page_weigh_listed(WeighArgs a
     bool ascending = true;
     for (int n = tid + 1; n < cnt; n += kWeighThreads) ascending = ascending && idx[n - 1] < idx[n];
     ascending = __syncthreads_and(ascending);
-    const int blocks = p.page / 16;
-    for (int n0 = 0; n0 < cnt; n0 += kWeighThreads) {
-        const int n = n0 + tid, j = n < cnt ? idx[n] : -1;
+    const int blocks = p.page / 16, per = kWeighThreads / a.lanes, me = tid & (a.lanes - 1);
+    for (int n0 = 0; n0 < cnt; n0 += per) {
+        const int n = n0 + tid / a.lanes, j = n < cnt ? idx[n] : -1;
         const bool on = j >= 0 && j < p.max_pages && (long long)j << p.page_log2 < len;
-        const float mass = on ? mass_of(a, bh, n * blocks, blocks) : 0.f;
+        const float mass = group_sum(a, on ? mass_of(a, bh, n * blocks, blocks, me) : 0.f);
         if (ascending) {
-            if (on) out[j] += mass;
+            if (on && me == 0) out[j] += mass;
         } else {
-            s_mass[tid] = mass;
+            if (me == 0) s_mass[tid / a.lanes] = mass;
             __syncthreads();
             if (tid == 0)
-                for (int i = 0; i < kWeighThreads && n0 + i < cnt; ++i) {
+                for (int i = 0; i < per && n0 + i < cnt; ++i) {
                     const int at = idx[n0 + i];
                     if (at >= 0 && at < p.max_pages && (long long)at << p.page_log2 < len) out[at] += s_mass[i];
                 }
@@ -125,7 +139,8 @@ struct EvictArgs {
     uint32_t *keys;  // [B, max_pages] order-preserving keys of the pages' weights
     int *len;        // [B] the lengths: lens_out may be the lengths themselves
 };
-constexpr int kSumThreads = 256, kMoveThreads = 512, kMoveWarps = kMoveThreads / 32;
+constexpr int kSumThreads = 256;
+constexpr long long kOneCta = 16384;  // weights of a sequence that one CTA takes
 
 // A float's order as an unsigned's; NaN with -inf, -0 with 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -134,7 +149,16 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Weights over the heads, as keys. The heads are added in fp64: the sum, rounded once to fp32, does not depend on an order.
+// A page's weight over the heads, as a key. The heads are added in fp64: the sum, rounded once to fp32, does not depend on
+// an order.
+__device__ __forceinline__ uint32_t page_key(const EvictArgs &a, int b, int j) {
+    const Paged &p = a.p;
+    const float *w = a.weight + (long long)b * p.Hkv * p.max_pages + j;
+    double sum = 0.0;
+#pragma unroll 8
+    for (int h = 0; h < p.Hkv; ++h) sum += (double)w[(long long)h * p.max_pages];
+    return order_key((float)sum);
+}
 __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
     const Paged &p = a.p;
     const int chunks = (p.max_pages + kSumThreads - 1) / kSumThreads;
@@ -144,62 +168,65 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
     const int raw = p.lens[b], len = clampi(raw, 0, p.max_len);
     if (j == 0) a.len[b] = raw;
     if (j >= p.max_pages || (long long)j << p.page_log2 >= len) return;
-    const float *w = a.weight + (long long)b * p.Hkv * p.max_pages + j;
-    double sum = 0.0;
-#pragma unroll 8
-    for (int h = 0; h < p.Hkv; ++h) sum += (double)w[(long long)h * p.max_pages];
-    a.keys[(long long)b * p.max_pages + j] = order_key((float)sum);
+    a.keys[(long long)b * p.max_pages + j] = page_key(a, b, j);
 }
 
-// One CTA per row: sequence b's table (row 0 of Hkv + 1) or a head's weights. Each finds the last key to stay by itself,
-// 8 bits at a time, then moves its row in ascending chunks: an entry moves to a place at or before its own, and a chunk
-// is read before any of it is written, so the row may be moved in place.
-__global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs a) {
+// The CTA's rows of sequence b (row -1: the table, 0 .. Hkv - 1: a head's weights), N threads with E neighbouring
+// entries each. It finds the last key to stay, 8 bits at a time from the top (the lanes of a warp that add to one bin do
+// so together: weights share their upper bits, and 7,680 single additions to a few bins took 8 us), then places its
+// entries by one scan per N E of them, and moves its rows: an entry moves to a place at or before its own, and a chunk is
+// read before any of it is written, so a row may be moved in place. kSums: the CTA has all rows, and makes the keys itself;
+// all of them are in registers.
+template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
+    constexpr int W = N / 32, kChunk = N * E;
     __shared__ int s_hist[256];
-    __shared__ int s_bin, s_left, s_warp[kMoveWarps];
+    __shared__ int s_bin, s_left, s_warp[W];
     const Paged &p = a.p;
-    const int b = (int)(blockIdx.x / (p.Hkv + 1)), row = (int)(blockIdx.x % (p.Hkv + 1)) - 1;
+    const int rows = kSums ? 1 : p.Hkv + 1;  // CTAs per sequence
+    const int b = (int)(blockIdx.x / rows), row0 = (int)(blockIdx.x - (unsigned)b * rows) - 1;
+    const int row1 = kSums ? p.Hkv : row0 + 1;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, P = p.max_pages;
     grid_wait();
     grid_go();
-    const int raw = a.len[b], len = clampi(raw, 0, p.max_len), n = (len + p.page - 1) >> p.page_log2;
-    const long long at = row < 0 ? (long long)b * P : ((long long)b * p.Hkv + row) * P;
+    const int raw = kSums ? p.lens[b] : a.len[b], len = clampi(raw, 0, p.max_len), n = (len + p.page - 1) >> p.page_log2;
     const int gone = n > a.keep ? n - a.keep : 0;
-    if (row < 0) {
-        for (int i = gone + tid; i < a.freed_cap; i += kMoveThreads) a.freed[(long long)b * a.freed_cap + i] = -1;
-        if (tid == 0) {
-            a.cnt[b] = gone;
-            a.lens_out[b] = gone ? len - gone * p.page : raw;
-        }
-    }
-    const int *ti = p.table + at;
-    int *to = a.table_out + at;
-    const float *wi = a.weight + at;
-    float *wo = a.weight_out + at;
-    if (gone == 0) {
-        if (row < 0 ? to != ti : wo != wi)
-            for (int j = tid; j < P; j += kMoveThreads) {
-                if (row < 0)
-                    to[j] = ti[j];
-                else
-                    wo[j] = wi[j];
-            }
-        return;
-    }
-    // among the competing pages [first, n - last) the (keep - first - last)-th largest key, and how many of its equals stay
-    const uint32_t *keys = a.keys + (long long)b * P;
+    auto from = [&](int row) -> const int * {
+        return row < 0 ? p.table + (long long)b * P
+                       : reinterpret_cast<const int *>(a.weight) + ((long long)b * p.Hkv + row) * P;
+    };
+    auto to = [&](int row) -> int * {
+        return row < 0 ? a.table_out + (long long)b * P
+                       : reinterpret_cast<int *>(a.weight_out) + ((long long)b * p.Hkv + row) * P;
+    };
+    // among the competing pages [c0, c1) the (keep - first - last)-th largest key, and how many of its equals stay
     const int c0 = a.first, c1 = n - a.last;
     int left = a.keep - a.first - a.last;
-    uint32_t last_key = 0xffffffffu;
-    if (left > 0) {
+    uint32_t last_key = 0xffffffffu, key[E];  // of the first chunk
+    auto key_at = [&](int j) { return a.keys[(long long)b * P + j]; };
+    if (gone && left > 0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = tid * E + e;
+            key[e] = j < c0 || j >= c1 ? 0 : kSums ? page_key(a, b, j) : key_at(j);
+        }
         uint32_t found = 0;
         for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kMoveThreads) s_hist[i] = 0;
+            for (int i = tid; i < 256; i += N) s_hist[i] = 0;
             __syncthreads();
-            for (int j = c0 + tid; j < c1; j += kMoveThreads) {
-                const uint32_t k = keys[j];
-                if (shift == 24 || (k >> (shift + 8)) == (found >> (shift + 8))) atomicAdd(&s_hist[(k >> shift) & 255], 1);
-            }
+            auto count = [&](int j, uint32_t k) {
+                const bool in = j >= c0 && j < c1 && (shift == 24 || (k >> (shift + 8)) == (found >> (shift + 8)));
+                const uint32_t bin = in ? (k >> shift) & 255 : 256;
+                const unsigned peers = __match_any_sync(0xffffffffu, bin);
+                if (in && lane == __ffs(peers) - 1) atomicAdd(&s_hist[bin], __popc(peers));
+            };
+            if ((wid * 32) * E < c1)
+#pragma unroll
+                for (int e = 0; e < E; ++e) count(tid * E + e, key[e]);
+            if constexpr (!kSums)
+                for (int j0 = kChunk; j0 < c1; j0 += N) {
+                    const int j = j0 + tid;
+                    count(j, j >= c0 && j < c1 ? key_at(j) : 0);
+                }
             __syncthreads();
             if (wid == 0) {  // bins from the top: lane l has bins 255 - 8 l .. 248 - 8 l
                 int mine = 0;
@@ -224,17 +251,34 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs a) {
         }
         last_key = found;
     }
+    if (row0 < 0) {
+        for (int i = gone + tid; i < a.freed_cap; i += N) a.freed[(long long)b * a.freed_cap + i] = -1;
+        if (tid == 0) a.cnt[b] = gone;
+    }
+    if (gone == 0) {
+        if (row0 < 0 && tid == 0) a.lens_out[b] = raw;
+        for (int row = row0; row < row1; ++row)
+            if (to(row) != from(row))
+                for (int j = tid; j < P; j += N) to(row)[j] = from(row)[j];
+        return;
+    }
     // a page stays that competes with a larger key, that is kept or lies behind the end, or that is among the first
     // `left` of last_key
     int above = 0, equal = 0;  // before this chunk
-    for (int j0 = 0; j0 < P; j0 += kMoveThreads) {
-        const int j = j0 + tid;
-        const bool in = j < P, competes = in && j >= c0 && j < c1;
-        const uint32_t k = competes ? keys[j] : 0;
-        const bool gt = in && (!competes || k > last_key), eq = competes && left > 0 && k == last_key;
-        const int t = in && row < 0 ? ti[j] : 0;
-        const float w = in && row >= 0 ? wi[j] : 0.f;
-        int inc = (gt ? 1 : 0) | (eq ? 1 << 16 : 0);
+    for (int j0 = 0; j0 < P; j0 += kChunk) {
+        int place[E], gt = 0, eq = 0;  // ~j of the freed one where it goes
+        bool is_gt[E], is_eq[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = j0 + tid * E + e;
+            const bool competes = j >= c0 && j < c1;
+            const uint32_t k = !competes || left == 0 ? 0 : j0 == 0 ? key[e] : key_at(j);
+            is_gt[e] = j < P && (!competes || (left > 0 && k > last_key));
+            is_eq[e] = competes && left > 0 && k == last_key;
+            gt += is_gt[e];
+            eq += is_eq[e];
+        }
+        int inc = gt | eq << 16;  // kChunk < 2^15
         const int mine = inc;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -242,32 +286,53 @@ __global__ void __launch_bounds__(kMoveThreads) k_evict_move(EvictArgs a) {
             if (lane >= off) inc += y;
         }
         if (lane == 31) s_warp[wid] = inc;
-        __syncthreads();  // the chunk was read
+        __syncthreads();
         int all = 0;
 #pragma unroll
-        for (int v = 0; v < kMoveWarps; ++v) {
+        for (int v = 0; v < W; ++v) {
             if (v == wid) inc += all;
             all += s_warp[v];
         }
-        const int eq_before = equal + ((inc - mine) >> 16), place = above + ((inc - mine) & 0xffff) + min(eq_before, left);
-        if (in && (gt || (eq && eq_before < left))) {
-            if (row < 0)
-                to[place] = t;
-            else
-                wo[place] = w;
-        } else if (in && row < 0) {
-            a.freed[(long long)b * a.freed_cap + (j - place)] = t;
+        int g = above + ((inc - mine) & 0xffff), q = equal + ((inc - mine) >> 16);
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int j = j0 + tid * E + e, at = g + min(q, left);
+            place[e] = is_gt[e] || (is_eq[e] && q < left) ? at : ~(j - at);
+            g += is_gt[e];
+            q += is_eq[e];
         }
         above += all & 0xffff;
         equal += all >> 16;
-        __syncthreads();  // s_warp was read
+        for (int row = row0; row < row1; ++row) {
+            const int *src = from(row);
+            int *dst = to(row), x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = j0 + tid * E + e < P ? src[j0 + tid * E + e] : 0;
+            __syncthreads();  // the chunk of this row was read (and s_warp)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (j0 + tid * E + e >= P) continue;
+                if (place[e] >= 0)
+                    dst[place[e]] = x[e];
+                else if (row < 0)
+                    a.freed[(long long)b * a.freed_cap + ~place[e]] = x[e];
+            }
+        }
     }
-    for (int j = P - gone + tid; j < P; j += kMoveThreads) {
-        if (row < 0)
-            to[j] = -1;
-        else
-            wo[j] = 0.f;
-    }
+    __syncthreads();
+    if (row0 < 0 && tid == 0) a.lens_out[b] = len - gone * p.page;  // which may be where every thread read raw
+    for (int row = row0; row < row1; ++row)
+        for (int j = P - gone + tid; j < P; j += N) to(row)[j] = row < 0 ? -1 : 0;  // 0.f
+}
+
+// One CTA per sequence where its pages fit its registers and there is little to move, otherwise one per row, with the keys
+// made by a launch before.
+template <int N, int E> cudaError_t launch_evict(const EvictArgs &a, bool one, cudaStream_t s) {
+    prof_begin("evict_move", s);
+    const cudaError_t e = one ? launch_paged(k_evict_move<N, E, true>, dim3(a.p.B), N, 0, 1, a, s)
+                              : launch_paged(k_evict_move<N, E, false>, dim3((unsigned)(a.p.B * (a.p.Hkv + 1))), N, 0, 1, a, s);
+    prof_end(s);
+    return e;
 }
 
 }  // namespace
@@ -288,7 +353,11 @@ extern "C" vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const voi
     if (!(decay >= 0.f && decay <= 1.f)) return VSA_ERR_SHAPE;
     if (page_idx && idx_cap > a.p.max_pages) return VSA_ERR_UNSUPPORTED;  // records are kept per page of the table
     const bool eight = k_scale != nullptr;
-    const long long chunks = (a.p.max_pages + kWeighThreads - 1) / kWeighThreads;
+    a.rows = rows_of(a.p.G);
+    a.lanes = 1;
+    while (a.lanes < 32 && a.lanes < a.rows * (a.p.page / 16)) a.lanes *= 2;
+    const int span = kWeighThreads / a.lanes * kWeighDeep;
+    const long long chunks = (a.p.max_pages + span - 1) / span;
     const long long ctas = (long long)a.p.B * a.p.Hkv * (page_idx ? 1 : chunks);
     if (ctas > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -302,7 +371,6 @@ extern "C" vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const voi
     a.lse = lse;
     a.bw = reinterpret_cast<const float2 *>(static_cast<char *>(workspace) + paged_ws(a.p).total);
     a.blocks = a.p.max_len / 16;
-    a.rows = rows_of(a.p.G);
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     a.in = page_weight;
     a.out = weight_out;
@@ -345,12 +413,14 @@ extern "C" vsa_status vsa_page_evict(const vsa_paged_desc *desc, const float *pa
     a.keys = reinterpret_cast<uint32_t *>(w + ws.keys);
     a.len = reinterpret_cast<int *>(w + ws.seg);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    prof_begin("evict_sums", s);
-    cudaError_t e = launch_paged(k_evict_sums, dim3((unsigned)sums), kSumThreads, 0, 1, a, s);
-    prof_end(s);
-    if (e != cudaSuccess) return status_from_cuda(e);
-    prof_begin("evict_move", s);
-    e = launch_paged(k_evict_move, dim3((unsigned)moves), kMoveThreads, 0, 1, a, s);
-    prof_end(s);
-    return status_from_cuda(e);
+    const int P = a.p.max_pages;
+    const bool one = P <= 8192 && (long long)P * a.p.Hkv <= kOneCta;
+    if (!one) {
+        prof_begin("evict_sums", s);
+        const cudaError_t e = launch_paged(k_evict_sums, dim3((unsigned)sums), kSumThreads, 0, 1, a, s);
+        prof_end(s);
+        if (e != cudaSuccess) return status_from_cuda(e);
+    }
+    return status_from_cuda(P <= 512 ? launch_evict<128, 4>(a, one, s)
+                            : P <= 2048 ? launch_evict<512, 4>(a, one, s) : launch_evict<1024, 8>(a, one, s));
 }
