@@ -10,6 +10,8 @@
 // of 16 keys, the sum of the block's exponentials and the maximum that they are
 // relative to: 8 bytes per row and block against the block's 4 to 8 KB of keys
 // and values. k_page_weigh puts them over the rows' LSE, per page.
+#include <algorithm>
+
 #include "paged.cuh"
 #include "sm103_ptx.cuh"
 
@@ -26,61 +28,63 @@ struct WeighArgs {
     const float *in;       // [B, Hkv, max_pages]
     float *out;
     float decay, drop;     // drop: the attention's lift of P, undone
-    int lanes;             // per page: as many as it has records, up to 32
+    int lanes, row_lanes;  // log2 of the lanes per page (as many as it has records, up to 32), and of those per block
+    unsigned chunks;       // CTAs per list row
 };
 constexpr int kWeighThreads = 256;
 constexpr int kWeighDeep = 4;  // pages per group of lanes
 
-// Sum of P over `n` blocks from entry block `blk` of list row bh, all of its query heads: by the L lanes (a power of two
-// up to 32) of a group; `me` is a lane's place in it. The records of a page lie side by side: a group reads them together.
-__device__ __forceinline__ float mass_of(const WeighArgs &a, long long bh, int blk, int n, int me) {
+// Sum of P over `n` blocks from entry block `blk` of key/value head h of sequence b (list row bh), all of its query heads: by
+// the 2^lanes lanes of a group, `me` a lane's place in it. The records of a page lie side by side: a group reads them
+// together, a lane those of one row (of `row_lanes` bits; a chunk with fewer rows leaves lanes idle).
+__device__ __forceinline__ float mass_of(const WeighArgs &a, int b, int h, int bh, int blk, int n, int me) {
     const Paged &p = a.p;
-    const int b = (int)(bh / p.Hkv), h = (int)(bh - (long long)b * p.Hkv);
-    const float *lse = a.lse + (long long)b * p.Hq + h * p.G;
+    const int i = me & ((1 << a.row_lanes) - 1);
     float mass = 0.f;
     for (int r = 0; r < a.rc; ++r) {
-        const int rows = min(a.rows, p.G - r * a.rows);
-        const float2 *w = a.bw + ((bh * a.rc + r) * a.blocks + blk) * a.rows;
-        for (int k = me; k < n * a.rows; k += a.lanes) {
-            const int i = k % a.rows;
-            if (i >= rows) continue;  // the last chunk of a group may have fewer heads
-            const float2 x = w[k];
-            if (x.x != 0.f) mass += x.x * ptx::ex2(x.y - lse[r * a.rows + i] * kLog2e);
+        if (i >= min(a.rows, p.G - r * a.rows)) break;
+        const float ref = a.lse[(long long)b * p.Hq + h * p.G + r * a.rows + i] * kLog2e;
+        const float2 *w = a.bw + (((long long)bh * a.rc + r) * a.blocks + blk) * a.rows + i;
+        for (int k = me >> a.row_lanes; k < n; k += 1 << (a.lanes - a.row_lanes)) {
+            const float2 x = w[k * a.rows];
+            if (x.x != 0.f) mass += x.x * ptx::ex2(x.y - ref);
         }
     }
     return mass;
 }
 // ... over the group, in every lane of it; whole warp.
 __device__ __forceinline__ float group_sum(const WeighArgs &a, float x) {
-    for (int off = 1; off < a.lanes; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+    for (int off = 1; off < 1 << a.lanes; off <<= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
     return x * a.drop;
 }
 
 // All pages: kWeighDeep pages per group of lanes. 64 sequences of up to 16,000 keys x 8 heads with 4 queries each, 94,000
-// blocks: 14 us with a thread per page, which reads its records one after another.
+// blocks: 14 us with a thread per page, which reads its records one after another; 16 by groups of lanes with divisions for
+// each page.
 __global__ void __launch_bounds__(kWeighThreads) k_page_weigh(WeighArgs a) {
     const Paged &p = a.p;
-    const int per = kWeighThreads / a.lanes, span = per * kWeighDeep, chunks = (p.max_pages + span - 1) / span;
-    const long long bh = blockIdx.x / chunks;
-    const int me = threadIdx.x & (a.lanes - 1), j0 = (int)(blockIdx.x - bh * chunks) * span + threadIdx.x / a.lanes;
+    const int per = kWeighThreads >> a.lanes;
+    const unsigned bh = blockIdx.x / a.chunks, b = bh / (unsigned)p.Hkv, h = bh - b * p.Hkv;
+    const int me = threadIdx.x & ((1 << a.lanes) - 1);
+    const int j0 = (int)(blockIdx.x - bh * a.chunks) * per * kWeighDeep + (threadIdx.x >> a.lanes);
     grid_wait();
     grid_go();
-    const int len = paged_len(p, (int)(bh / p.Hkv));
+    const int len = paged_len(p, (int)b);
     float mass[kWeighDeep], old[kWeighDeep];
 #pragma unroll
     for (int d = 0; d < kWeighDeep; ++d) {
         const int j = j0 + d * per;
-        const long long from = (long long)j << p.page_log2, at = bh * p.max_pages + j;
-        const bool live = from < len;
-        mass[d] = live ? mass_of(a, bh, (int)(from / 16), (int)((min(len - from, (long long)p.page) + 15) / 16), me) : 0.f;
-        old[d] = j < p.max_pages && me == 0 && !(live && a.decay == 0.f) ? a.in[at] : 0.f;
+        const bool live = j < p.max_pages && j << p.page_log2 < len;
+        const int from = live ? j << p.page_log2 : 0;
+        old[d] = j < p.max_pages && me == 0 && !(live && a.decay == 0.f) ? a.in[(long long)bh * p.max_pages + j] : 0.f;
+        mass[d] = live ? mass_of(a, (int)b, (int)h, (int)bh, from >> 4, (min(len - from, p.page) + 15) >> 4, me) : 0.f;
     }
 #pragma unroll
     for (int d = 0; d < kWeighDeep; ++d) {
         const int j = j0 + d * per;
-        const bool live = (long long)j << p.page_log2 < len;
         const float sum = group_sum(a, mass[d]);
-        if (me == 0 && j < p.max_pages) a.out[bh * p.max_pages + j] = live ? fmaf(a.decay, old[d], sum) : old[d];
+        if (me == 0 && j < p.max_pages)
+            a.out[(long long)bh * p.max_pages + j] = j << p.page_log2 < len ? fmaf(a.decay, old[d], sum) : old[d];
     }
 }
 
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(kWeighThreads) k_page_weigh_listed(WeighArgs a
     const int tid = threadIdx.x;
     grid_wait();
     grid_go();
-    const int len = paged_len(p, (int)(bh / p.Hkv)), cnt = clampi(a.cnt[bh], 0, a.cap);
+    const int b = (int)(bh / p.Hkv), h = (int)(bh % p.Hkv), len = paged_len(p, b), cnt = clampi(a.cnt[bh], 0, a.cap);
     const int *idx = a.idx + bh * a.cap;
     float *out = a.out + bh * p.max_pages;
     for (int j = tid; j < p.max_pages; j += kWeighThreads) {
@@ -107,15 +111,15 @@ __global__ void __launch_bounds__(kWeighThreads) k_page_weigh_listed(WeighArgs a
     bool ascending = true;
     for (int n = tid + 1; n < cnt; n += kWeighThreads) ascending = ascending && idx[n - 1] < idx[n];
     ascending = __syncthreads_and(ascending);
-    const int blocks = p.page / 16, per = kWeighThreads / a.lanes, me = tid & (a.lanes - 1);
+    const int blocks = p.page / 16, per = kWeighThreads >> a.lanes, me = tid & ((1 << a.lanes) - 1), slot = tid >> a.lanes;
     for (int n0 = 0; n0 < cnt; n0 += per) {
-        const int n = n0 + tid / a.lanes, j = n < cnt ? idx[n] : -1;
+        const int n = n0 + slot, j = n < cnt ? idx[n] : -1;
         const bool on = j >= 0 && j < p.max_pages && (long long)j << p.page_log2 < len;
-        const float mass = group_sum(a, on ? mass_of(a, bh, n * blocks, blocks, me) : 0.f);
+        const float mass = group_sum(a, on ? mass_of(a, b, h, (int)bh, n * blocks, blocks, me) : 0.f);
         if (ascending) {
             if (on && me == 0) out[j] += mass;
         } else {
-            if (me == 0) s_mass[tid / a.lanes] = mass;
+            if (me == 0) s_mass[slot] = mass;
             __syncthreads();
             if (tid == 0)
                 for (int i = 0; i < per && n0 + i < cnt; ++i) {
@@ -140,7 +144,7 @@ struct EvictArgs {
     int *len;        // [B] the lengths: lens_out may be the lengths themselves
 };
 constexpr int kSumThreads = 256;
-constexpr long long kOneCta = 16384;  // weights of a sequence that one CTA takes
+constexpr int kOneHeads = 32;  // heads up to which a CTA takes a whole sequence (of up to 1,024 pages)
 
 // A float's order as an unsigned's; NaN with -inf, -0 with 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -171,25 +175,25 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
     a.keys[(long long)b * p.max_pages + j] = page_key(a, b, j);
 }
 
-// The CTA's rows of sequence b (row -1: the table, 0 .. Hkv - 1: a head's weights), N threads with E neighbouring
-// entries each. It finds the last key to stay, 8 bits at a time from the top (the lanes of a warp that add to one bin do
-// so together: weights share their upper bits, and 7,680 single additions to a few bins took 8 us), then places its
-// entries by one scan per N E of them, and moves its rows: an entry moves to a place at or before its own, and a chunk is
-// read before any of it is written, so a row may be moved in place. kSums: the CTA has all rows, and makes the keys itself;
-// all of them are in registers.
-template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
-    constexpr int W = N / 32, kChunk = N * E;
-    __shared__ int s_hist[256];
-    __shared__ int s_bin, s_left, s_warp[W];
+// Places the pages of sequence b and moves rows of it (row -1: the table, 0 .. Hkv - 1: a head's weights), N threads with E
+// neighbouring entries each. One: the CTA has all rows and makes the keys itself, each thread one page; otherwise it has
+// one row, with the keys made before.
+//
+// The last key to stay: 11 bits at a time from the top (2,048 bins: weights share their exponents, and one bin of few
+// takes the additions of a warp one after another), until a bin stays as a whole or its keys are all equal. Then one scan
+// per N E entries places them. An entry moves to a place at or before its own, and a chunk is read before any of it is
+// written, so a row may be moved in place. What will be moved is loaded first of all.
+constexpr int kBins = 2048, kRowsAhead = 8;
+template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
+    constexpr int W = N / 32, kChunk = N * E, R = kOne ? kRowsAhead : 1;
+    static_assert(!kOne || E == 1, "one page per thread");
+    __shared__ int s_hist[kBins];
+    __shared__ int s_bin, s_left, s_in, s_warp[W];
     const Paged &p = a.p;
-    const int rows = kSums ? 1 : p.Hkv + 1;  // CTAs per sequence
+    const int rows = kOne ? 1 : p.Hkv + 1;  // CTAs per sequence
     const int b = (int)(blockIdx.x / rows), row0 = (int)(blockIdx.x - (unsigned)b * rows) - 1;
-    const int row1 = kSums ? p.Hkv : row0 + 1;
+    const int row1 = kOne ? p.Hkv : row0 + 1;
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5, P = p.max_pages;
-    grid_wait();
-    grid_go();
-    const int raw = kSums ? p.lens[b] : a.len[b], len = clampi(raw, 0, p.max_len), n = (len + p.page - 1) >> p.page_log2;
-    const int gone = n > a.keep ? n - a.keep : 0;
     auto from = [&](int row) -> const int * {
         return row < 0 ? p.table + (long long)b * P
                        : reinterpret_cast<const int *>(a.weight) + ((long long)b * p.Hkv + row) * P;
@@ -198,58 +202,28 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
         return row < 0 ? a.table_out + (long long)b * P
                        : reinterpret_cast<int *>(a.weight_out) + ((long long)b * p.Hkv + row) * P;
     };
-    // among the competing pages [c0, c1) the (keep - first - last)-th largest key, and how many of its equals stay
-    const int c0 = a.first, c1 = n - a.last;
-    int left = a.keep - a.first - a.last;
-    uint32_t last_key = 0xffffffffu, key[E];  // of the first chunk
+    grid_wait();
+    grid_go();
+    int x[R][E];  // the first chunk of the first rows
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[r][e] = row0 + r < row1 && tid * E + e < P ? from(row0 + r)[tid * E + e] : 0;
+    const int raw = kOne ? p.lens[b] : a.len[b], len = clampi(raw, 0, p.max_len), n = (len + p.page - 1) >> p.page_log2;
+    const int gone = n > a.keep ? n - a.keep : 0;
+    const int c0 = a.first, c1 = n - a.last;  // the pages that compete
     auto key_at = [&](int j) { return a.keys[(long long)b * P + j]; };
-    if (gone && left > 0) {
+    uint32_t key[E];
+    if constexpr (kOne) {
+        double sum = 0.0;
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int j = tid * E + e;
-            key[e] = j < c0 || j >= c1 ? 0 : kSums ? page_key(a, b, j) : key_at(j);
-        }
-        uint32_t found = 0;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += N) s_hist[i] = 0;
-            __syncthreads();
-            auto count = [&](int j, uint32_t k) {
-                const bool in = j >= c0 && j < c1 && (shift == 24 || (k >> (shift + 8)) == (found >> (shift + 8)));
-                const uint32_t bin = in ? (k >> shift) & 255 : 256;
-                const unsigned peers = __match_any_sync(0xffffffffu, bin);
-                if (in && lane == __ffs(peers) - 1) atomicAdd(&s_hist[bin], __popc(peers));
-            };
-            if ((wid * 32) * E < c1)
+        for (int r = 1; r < R; ++r) sum += row0 + r < row1 ? (double)__int_as_float(x[r][0]) : 0.0;
+#pragma unroll 8
+        for (int row = row0 + R; row < row1; ++row) sum += tid < P ? (double)__int_as_float(from(row)[tid]) : 0.0;
+        key[0] = order_key((float)sum);
+    } else if (gone) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) count(tid * E + e, key[e]);
-            if constexpr (!kSums)
-                for (int j0 = kChunk; j0 < c1; j0 += N) {
-                    const int j = j0 + tid;
-                    count(j, j >= c0 && j < c1 ? key_at(j) : 0);
-                }
-            __syncthreads();
-            if (wid == 0) {  // bins from the top: lane l has bins 255 - 8 l .. 248 - 8 l
-                int mine = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) mine += s_hist[255 - 8 * lane - e];
-                int inc = mine;
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1) {
-                    const int y = __shfl_up_sync(0xffffffffu, inc, off);
-                    if (lane >= off) inc += y;
-                }
-                if (inc - mine < left && left <= inc) {  // one lane
-                    int before = inc - mine, e = 0;
-                    while (before + s_hist[255 - 8 * lane - e] < left) before += s_hist[255 - 8 * lane - e++];
-                    s_bin = 255 - 8 * lane - e;
-                    s_left = left - before;
-                }
-            }
-            __syncthreads();
-            found |= (uint32_t)s_bin << shift;
-            left = s_left;
-        }
-        last_key = found;
+        for (int e = 0; e < E; ++e) key[e] = tid * E + e >= c0 && tid * E + e < c1 ? key_at(tid * E + e) : 0;
     }
     if (row0 < 0) {
         for (int i = gone + tid; i < a.freed_cap; i += N) a.freed[(long long)b * a.freed_cap + i] = -1;
@@ -262,8 +236,66 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
                 for (int j = tid; j < P; j += N) to(row)[j] = from(row)[j];
         return;
     }
-    // a page stays that competes with a larger key, that is kept or lies behind the end, or that is among the first
-    // `left` of last_key
+    // a page that competes stays with a key above `last_key`, or as one of the first `left` equal to it
+    int left = a.keep - a.first - a.last;
+    uint32_t last_key = 0xffffffffu;
+    if (left > 0) {
+        uint32_t found = 0;
+        int shift = 21, known = 32;  // the digit's place; `known`: bits below it and its own
+        for (;;) {
+            const int bits = known - shift, bins = 1 << bits;
+            for (int i = tid; i < kBins; i += N) s_hist[i] = 0;
+            __syncthreads();
+            auto count = [&](int j, uint32_t k) {
+                if (j >= c0 && j < c1 && (known == 32 || k >> known == found >> known)) atomicAdd(&s_hist[k >> shift & (bins - 1)], 1);
+            };
+#pragma unroll
+            for (int e = 0; e < E; ++e) count(tid * E + e, key[e]);
+            if constexpr (!kOne)
+                for (int j = kChunk + tid; j < c1; j += N) count(j, j >= c0 ? key_at(j) : 0);
+            __syncthreads();
+            // bins from the top, kBins / N or so to a thread: their sums before it, and the thread that holds the last one
+            constexpr int kPer = kBins / N > 0 ? kBins / N : 1;
+            int mine = 0;
+            if (tid * kPer < kBins)
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) mine += s_hist[kBins - 1 - tid * kPer - e];
+            int inc = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += y;
+            }
+            if (lane == 31) s_warp[wid] = inc;
+            __syncthreads();
+            int below = 0;
+#pragma unroll
+            for (int v = 0; v < W; ++v)
+                if (v < wid) below += s_warp[v];
+            inc += below;
+            if (inc - mine < left && left <= inc) {  // one thread
+                int before = inc - mine, at = kBins - 1 - tid * kPer;
+                while (before + s_hist[at] < left) before += s_hist[at--];
+                s_bin = at;
+                s_left = left - before;
+                s_in = s_hist[at];
+            }
+            __syncthreads();
+            found |= (uint32_t)s_bin << shift;
+            left = s_left;
+            if (s_in == left && found) {  // the bin stays as a whole
+                last_key = found - 1;
+                left = 0;
+                break;
+            }
+            if (shift == 0) {
+                last_key = found;
+                break;
+            }
+            known = shift;
+            shift = shift > 11 ? shift - 11 : 0;
+        }
+    }
     int above = 0, equal = 0;  // before this chunk
     for (int j0 = 0; j0 < P; j0 += kChunk) {
         int place[E], gt = 0, eq = 0;  // ~j of the freed one where it goes
@@ -272,8 +304,8 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
         for (int e = 0; e < E; ++e) {
             const int j = j0 + tid * E + e;
             const bool competes = j >= c0 && j < c1;
-            const uint32_t k = !competes || left == 0 ? 0 : j0 == 0 ? key[e] : key_at(j);
-            is_gt[e] = j < P && (!competes || (left > 0 && k > last_key));
+            const uint32_t k = !competes ? 0 : j0 == 0 ? key[e] : kOne ? 0 : key_at(j);
+            is_gt[e] = j < P && (!competes || k > last_key);
             is_eq[e] = competes && left > 0 && k == last_key;
             gt += is_gt[e];
             eq += is_eq[e];
@@ -285,6 +317,7 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
             const int y = __shfl_up_sync(0xffffffffu, inc, off);
             if (lane >= off) inc += y;
         }
+        __syncthreads();  // s_warp was read
         if (lane == 31) s_warp[wid] = inc;
         __syncthreads();
         int all = 0;
@@ -303,20 +336,25 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
         }
         above += all & 0xffff;
         equal += all >> 16;
-        for (int row = row0; row < row1; ++row) {
-            const int *src = from(row);
-            int *dst = to(row), x[E];
+        for (int row = row0; row < row1; row += R) {
+            if (j0 > 0 || row > row0) {
 #pragma unroll
-            for (int e = 0; e < E; ++e) x[e] = j0 + tid * E + e < P ? src[j0 + tid * E + e] : 0;
-            __syncthreads();  // the chunk of this row was read (and s_warp)
+                for (int r = 0; r < R; ++r)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                if (j0 + tid * E + e >= P) continue;
-                if (place[e] >= 0)
-                    dst[place[e]] = x[e];
-                else if (row < 0)
-                    a.freed[(long long)b * a.freed_cap + ~place[e]] = x[e];
+                    for (int e = 0; e < E; ++e)
+                        x[r][e] = row + r < row1 && j0 + tid * E + e < P ? from(row + r)[j0 + tid * E + e] : 0;
             }
+            __syncthreads();  // the chunk of these rows was read
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    if (row + r >= row1 || j0 + tid * E + e >= P) continue;
+                    if (place[e] >= 0)
+                        to(row + r)[place[e]] = x[r][e];
+                    else if (row + r < 0)
+                        a.freed[(long long)b * a.freed_cap + ~place[e]] = x[r][e];
+                }
         }
     }
     __syncthreads();
@@ -325,12 +363,10 @@ template <int N, int E, bool kSums> __global__ void __launch_bounds__(N) k_evict
         for (int j = P - gone + tid; j < P; j += N) to(row)[j] = row < 0 ? -1 : 0;  // 0.f
 }
 
-// One CTA per sequence where its pages fit its registers and there is little to move, otherwise one per row, with the keys
-// made by a launch before.
-template <int N, int E> cudaError_t launch_evict(const EvictArgs &a, bool one, cudaStream_t s) {
+template <int N, int E, bool kOne> cudaError_t launch_evict(const EvictArgs &a, cudaStream_t s) {
     prof_begin("evict_move", s);
-    const cudaError_t e = one ? launch_paged(k_evict_move<N, E, true>, dim3(a.p.B), N, 0, 1, a, s)
-                              : launch_paged(k_evict_move<N, E, false>, dim3((unsigned)(a.p.B * (a.p.Hkv + 1))), N, 0, 1, a, s);
+    const cudaError_t e = launch_paged(k_evict_move<N, E, kOne>, dim3((unsigned)(kOne ? a.p.B : a.p.B * (a.p.Hkv + 1))), N, 0, 1,
+                                       a, s);
     prof_end(s);
     return e;
 }
@@ -354,10 +390,10 @@ extern "C" vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const voi
     if (page_idx && idx_cap > a.p.max_pages) return VSA_ERR_UNSUPPORTED;  // records are kept per page of the table
     const bool eight = k_scale != nullptr;
     a.rows = rows_of(a.p.G);
-    a.lanes = 1;
-    while (a.lanes < 32 && a.lanes < a.rows * (a.p.page / 16)) a.lanes *= 2;
-    const int span = kWeighThreads / a.lanes * kWeighDeep;
-    const long long chunks = (a.p.max_pages + span - 1) / span;
+    while (1 << a.row_lanes < a.rows) ++a.row_lanes;
+    a.lanes = std::min(a.row_lanes + a.p.page_log2 - 4, 5);
+    const int span = (kWeighThreads >> a.lanes) * kWeighDeep;
+    const long long chunks = a.chunks = (unsigned)((a.p.max_pages + span - 1) / span);
     const long long ctas = (long long)a.p.B * a.p.Hkv * (page_idx ? 1 : chunks);
     if (ctas > 0x7fffffffLL) return VSA_ERR_UNSUPPORTED;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -414,13 +450,13 @@ extern "C" vsa_status vsa_page_evict(const vsa_paged_desc *desc, const float *pa
     a.len = reinterpret_cast<int *>(w + ws.seg);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int P = a.p.max_pages;
-    const bool one = P <= 8192 && (long long)P * a.p.Hkv <= kOneCta;
-    if (!one) {
-        prof_begin("evict_sums", s);
-        const cudaError_t e = launch_paged(k_evict_sums, dim3((unsigned)sums), kSumThreads, 0, 1, a, s);
-        prof_end(s);
-        if (e != cudaSuccess) return status_from_cuda(e);
-    }
-    return status_from_cuda(P <= 512 ? launch_evict<128, 4>(a, one, s)
-                            : P <= 2048 ? launch_evict<512, 4>(a, one, s) : launch_evict<1024, 8>(a, one, s));
+    if (P <= 1024 && a.p.Hkv <= kOneHeads)
+        return status_from_cuda(P <= 256 ? launch_evict<256, 1, true>(a, s)
+                                : P <= 512 ? launch_evict<512, 1, true>(a, s) : launch_evict<1024, 1, true>(a, s));
+    prof_begin("evict_sums", s);
+    const cudaError_t e = launch_paged(k_evict_sums, dim3((unsigned)sums), kSumThreads, 0, 1, a, s);
+    prof_end(s);
+    if (e != cudaSuccess) return status_from_cuda(e);
+    return status_from_cuda(P <= 1024 ? launch_evict<1024, 1, false>(a, s)
+                            : P <= 4096 ? launch_evict<1024, 4, false>(a, s) : launch_evict<1024, 8, false>(a, s));
 }
