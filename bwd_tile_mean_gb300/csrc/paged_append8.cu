@@ -17,6 +17,8 @@
 // a warp per token row, 8 dims per lane, all of the block's rotated keys in
 // registers in fp32 (they are rounded once, to e4m3) until its largest entry is
 // known.
+#include <type_traits>
+
 #include "e4m3.cuh"
 #include "paged_rows.cuh"
 #include "sm103_ptx.cuh"
@@ -24,32 +26,25 @@
 namespace vsa {
 namespace {
 
-// The lane's 8 dims of a key, rotated, in fp32; whole warp.
-template <typename T>
-__device__ __forceinline__ void rotate8(const AppendArgs &a, uint4 x, const Angles &w, int i, float (&y)[8]) {
+// The lane's 8 dims of a key, rotated, in fp32; whole warp. peer: the lane with the other dims of its pairs.
+template <typename T, bool kInter>
+__device__ __forceinline__ void rotate8(uint4 x, const Angles &w, bool on, bool lower, int peer, float (&y)[8]) {
     const uint32_t r[4] = {x.x, x.y, x.z, x.w};
-    const int hop = a.rot >> 4;
-    const bool on = 8 * i < a.rot, lower = i < hop;
-    const int peer = (threadIdx.x & 16) | (on ? (lower ? i + hop : i - hop) : i);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 e = unpack2<T>(r[j]);
-        y[2 * j] = e.x;
-        y[2 * j + 1] = e.y;
-        if (a.rot == 0) continue;
-        if (a.inter) {
-            if (on) {
-                y[2 * j] = __fsub_rn(__fmul_rn(e.x, w.c[j]), __fmul_rn(e.y, w.s[j]));
-                y[2 * j + 1] = __fadd_rn(__fmul_rn(e.y, w.c[j]), __fmul_rn(e.x, w.s[j]));
-            }
+        float u, v;
+        if constexpr (kInter) {
+            u = __fsub_rn(__fmul_rn(e.x, w.c[j]), __fmul_rn(e.y, w.s[j]));
+            v = __fadd_rn(__fmul_rn(e.y, w.c[j]), __fmul_rn(e.x, w.s[j]));
         } else {
             const float2 f = unpack2<T>(__shfl_sync(0xffffffffu, r[j], peer));
-            if (on) {
-                const float sx = lower ? -w.s[2 * j] : w.s[2 * j], sy = lower ? -w.s[2 * j + 1] : w.s[2 * j + 1];
-                y[2 * j] = __fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx));
-                y[2 * j + 1] = __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy));
-            }
+            const float sx = lower ? -w.s[2 * j] : w.s[2 * j], sy = lower ? -w.s[2 * j + 1] : w.s[2 * j + 1];
+            u = __fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx));
+            v = __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy));
         }
+        y[2 * j] = on ? u : e.x;
+        y[2 * j + 1] = on ? v : e.y;
     }
 }
 
@@ -57,16 +52,21 @@ __device__ __forceinline__ void rotate8(const AppendArgs &a, uint4 x, const Angl
 // times the largest scale would (65,536, and 2^128).
 template <typename T> struct Range;
 template <> struct Range<__nv_bfloat16> {
-    static __device__ __forceinline__ bool fits(float x) { return fabsf(x) < INFINITY; }
-    static __device__ __forceinline__ float most(float scale) { return scale == 0x1p120f ? 240.f : 448.f; }
+    static constexpr float kInf = INFINITY, kTop = 0x1p120f;
 };
 template <> struct Range<__half> {
-    static __device__ __forceinline__ bool fits(float x) { return fabsf(x) < 65520.f; }
-    static __device__ __forceinline__ float most(float scale) { return scale == 256.f ? 240.f : 448.f; }
+    static constexpr float kInf = 65520.f, kTop = 256.f;
 };
-template <typename T> __device__ __forceinline__ float top_of(const float (&x)[8], float top) {
+// Largest magnitude of 8 entries and `top`; NaN does not count.
+__device__ __forceinline__ float top_of(const float (&x)[8], float top) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = fmaxf(top, Range<T>::fits(x[e]) ? fabsf(x[e]) : 0.f);
+    for (int e = 0; e < 8; e += 2) top = ptx::fmax3(top, fabsf(x[e]), fabsf(x[e + 1]));
+    return top;
+}
+// ... of those that fit.
+template <typename T> __device__ __forceinline__ float top_fitting(const float (&x)[8], float top) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]) < Range<T>::kInf ? fabsf(x[e]) : 0.f);
     return top;
 }
 __device__ __forceinline__ float warp_top(float x) {
@@ -74,19 +74,25 @@ __device__ __forceinline__ float warp_top(float x) {
     for (int off = 16; off; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
     return x;
 }
-// 8 entries as bytes of this scale (inv: its inverse); infinities as NaN.
-template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)[8], float scale, float inv) {
-    const float most = Range<T>::most(scale);
+// 8 entries as bytes of this scale (inv: its inverse). `plain`: all fit, and the scale is not the largest; otherwise
+// infinities become NaN.
+template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)[8], float scale, float inv, bool plain) {
     uint32_t r[4];
+    if (plain) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        float y[2];
+        for (int j = 0; j < 4; ++j) r[j] = e4m3x2_of(x[2 * j] * inv, x[2 * j + 1] * inv);
+    } else {
+        const float most = scale == Range<T>::kTop ? 240.f : 448.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float v = x[2 * j + e];
-            y[e] = Range<T>::fits(v) ? fminf(fmaxf(v * inv, -most), most) : __int_as_float(0x7fffffff);
+        for (int j = 0; j < 4; ++j) {
+            float y[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float v = x[2 * j + e];
+                y[e] = fabsf(v) < Range<T>::kInf ? fminf(fmaxf(v * inv, -most), most) : __int_as_float(0x7fffffff);
+            }
+            r[j] = e4m3x2_of(y[0], y[1]);
         }
-        r[j] = e4m3x2_of(y[0], y[1]);
     }
     return make_uint2(r[0] | r[1] << 16, r[2] | r[3] << 16);
 }
@@ -116,18 +122,41 @@ template <typename T> __device__ __forceinline__ void unpack8(uint4 x, float (&y
 }
 
 constexpr int kPairs = kGroup / 2;  // pairs of slots of a block: one of each for every half of the warp
+constexpr int kRawBytes = kPairs * 512;  // a block's keys, or values, as they come
 
-// HC, PB: the queries' heads (2 HC) and pairs of slots at once; a.hc key/value heads per chunk.
-template <typename T, int HC, int PB> __global__ void __launch_bounds__(256) k_paged8_append(AppendArgs a) {
-    extern __shared__ __align__(16) float ssum[];  // [units of the CTA][groups][hc][128] group sums
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 own16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Largest magnitudes of two packed rows of 8 entries, NaN apart.
+template <typename T> __device__ __forceinline__ uint32_t top2(uint4 x, uint32_t top) {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+    const uint32_t r[4] = {x.x, x.y, x.z, x.w};
+    T2 t = *reinterpret_cast<const T2 *>(&top);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) t = __hmax2(t, __habs2(*reinterpret_cast<const T2 *>(&r[j])));
+    return *reinterpret_cast<const uint32_t *>(&t);
+}
+
+// HC, PB: the queries' heads (2 HC) and pairs of slots at once; a.hc key/value heads per chunk. A warp's next block comes
+// into its part of shared memory (values, keys; a lane reads back what it copied itself) while it works on one, and is
+// walked twice: for the largest entry, and to be rounded. Rotating twice takes fewer instructions than it takes registers to
+// keep 64 rotated entries per lane.
+template <typename T, bool kInter, int HC, int PB> __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
+    extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][kRawBytes], [units of the CTA][groups][hc][128] sums
     const Paged &p = a.p;
-    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
-    const int groups = p.page / kGroup, per_cta = (int)(blockDim.x >> 5) / a.team;
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15, warps = (int)(blockDim.x >> 5);
+    float *ssum = reinterpret_cast<float *>(smem + warps * 2 * kRawBytes);
+    const uint32_t raw_v = ptx::smem_addr(smem) + wid * 2 * kRawBytes + lane * 16, raw_k = raw_v + kRawBytes;
+    const int groups = p.page / kGroup, per_cta = warps / a.team;
     const int chunk = (int)(blockIdx.x % a.chunks);
     const int unit = wid / a.team, first_grp = wid % a.team;
     const long long u = (long long)(blockIdx.x / a.chunks) * per_cta + unit;
-    const T *k = static_cast<const T *>(a.k), *v = static_cast<const T *>(a.v);
-    unsigned char *kc = static_cast<unsigned char *>(a.kc), *vc = static_cast<unsigned char *>(a.vc);
     grid_wait();
 
     const Unit of = find_unit(a, u, lane);
@@ -139,107 +168,173 @@ template <typename T, int HC, int PB> __global__ void __launch_bounds__(256) k_p
     }
     const int id = s1 > s0 ? paged_id(p, of.b, of.pg) : -1;
     const bool mean = a.mean && s1 == p.page && id >= 0;  // the page fills up in this call
-    const long long page_at = (long long)max(id, 0) * p.page_stride + 8 * i;
     const int h0 = chunk * a.hc, hn = min(a.hc, p.Hkv - h0);
-    for (int grp = first_grp; grp < groups && id >= 0; grp += a.team) {
-        const int g0 = grp * kGroup;
-        const bool fresh = g0 < s1 && g0 + kGroup > s0, begun = g0 < s0;
-        if (!fresh && !(mean && begun)) continue;
-        for (int hh = 0; hh < hn; ++hh) {
-            const int h = h0 + hh;
-            const long long at = page_at + h * p.head_stride, sc = ((long long)id * p.Hkv + h) * groups + grp;
-            const float k_old = begun ? a.kscale[sc] : 0.f, v_old = begun && fresh ? a.vscale[sc] : 0.f;
-            float ks = k_old, vs = v_old;
-            float key[kPairs][8];
-            uint4 xv[kPairs];
-            if (fresh) {
-                uint4 xk[kPairs];
+    const long long page_at = (long long)max(id, 0) * p.page_stride + half * p.tok_stride + 8 * i;
+    const int hop = a.rot >> 4;  // half style: lanes from a dim to the other of its pair
+    const bool on = 8 * i < a.rot, lower = i < hop;
+    const int peer = (threadIdx.x & 16) | (on ? (lower ? i + hop : i - hop) : i);
+    const int first_row = of.pg << p.page_log2;
+    // a lane has slot g0 + 2 c + half of block grp at pair c: the new ones are copied
+    auto copy = [&](const void *base, long long stride, uint32_t dst, int grp, int hh) {
+        const int s = grp * kGroup + half;
+        const T *from = static_cast<const T *>(base) + ((long long)of.t_of + s) * stride + (h0 + hh) * kD + 8 * i;
 #pragma unroll
-                for (int c = 0; c < kPairs; ++c) {
-                    const int s = g0 + 2 * c + half;
-                    xk[c] = xv[c] = make_uint4(0, 0, 0, 0);
-                    if (s >= s0 && s < s1) {
-                        const long long tok = of.t_of + s;
-                        xk[c] = *reinterpret_cast<const uint4 *>(k + tok * a.ks + h * kD + 8 * i);
-                        xv[c] = *reinterpret_cast<const uint4 *>(v + tok * a.vs + h * kD + 8 * i);
-                    }
-                }
-                float k_top = 0.f, v_top = 0.f;
-#pragma unroll
-                for (int c = 0; c < kPairs; ++c) {
-                    if (g0 + 2 * c + 1 < s0 || g0 + 2 * c >= s1) continue;
-                    const int s = g0 + 2 * c + half;
-                    Angles w;
-                    if (8 * i < a.rot && s >= s0 && s < s1) {
-                        const int row = a.pos ? a.pos[of.t_of + s] : (of.pg << p.page_log2) + s;
-                        load_angles(a, clampi(row, 0, a.rows - 1), i, w);
-                    }
-                    rotate8<T>(a, xk[c], w, i, key[c]);
-                    float val[8];
-                    unpack8<T>(xv[c], val);
-                    if (s >= s0 && s < s1) {
-                        k_top = top_of<T>(key[c], k_top);
-                        v_top = top_of<T>(val, v_top);
-                    }
-                }
-                ks = fmaxf(scale_of(warp_top(k_top)), k_old);
-                vs = fmaxf(scale_of(warp_top(v_top)), v_old);
+        for (int c = 0; c < kPairs; ++c)
+            if (s + 2 * c >= s0 && s + 2 * c < s1) copy16(dst + c * 512, from + 2 * c * stride);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    auto no_copy = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
+    auto has_new = [&](int grp) { return grp < groups && grp * kGroup < s1 && grp * kGroup + kGroup > s0; };
+    auto skip = [&](int grp) { return grp < groups && !has_new(grp) && !(mean && grp * kGroup < s0); };
+    int grp = first_grp;
+    if (id >= 0) {
+        while (skip(grp)) grp += a.team;
+        if (has_new(grp)) {
+            copy(a.v, a.vs, raw_v, grp, 0);
+            copy(a.k, a.ks, raw_k, grp, 0);
+        }
+    }
+    for (int hh = 0; id >= 0 && grp < groups;) {
+        const int g0 = grp * kGroup, h = h0 + hh, mine = g0 + half;
+        const bool fresh = has_new(grp), begun = g0 < s0;
+        int grp1 = grp, hh1 = hh + 1;  // the next block
+        if (hh1 == hn) {
+            hh1 = 0;
+            do grp1 += a.team;
+            while (skip(grp1));
+        }
+        const bool more = has_new(grp1);
+        const long long sc = ((long long)id * p.Hkv + h) * groups + grp;
+        unsigned char *kc = static_cast<unsigned char *>(a.kc) + page_at + h * p.head_stride + g0 * p.tok_stride;
+        unsigned char *vc = static_cast<unsigned char *>(a.vc) + page_at + h * p.head_stride + g0 * p.tok_stride;
+        const float k_old = begun ? a.kscale[sc] : 0.f, v_old = begun && fresh ? a.vscale[sc] : 0.f;
+        float ks = k_old;
+        const int c0 = max(s0 - g0, 0) >> 1, c1 = (min(s1 - g0, kGroup) + 1) >> 1;  // pairs with new slots
+        auto is_new = [&](int c) { return mine + 2 * c >= s0 && mine + 2 * c < s1; };
+        // earlier tokens of the block, `by` times what they are
+        auto shrink = [&](unsigned char *at, float by) {
+#pragma unroll 2
+            for (int c = 0; c < kPairs; ++c) {
+                if (mine + 2 * c >= s0) break;
+                uint2 *to = reinterpret_cast<uint2 *>(at + 2 * c * p.tok_stride);
+                float y[8];
+                floats_of(*to, by, y);
+                *to = make_uint2(e4m3x2_of(y[0], y[1]) | e4m3x2_of(y[2], y[3]) << 16,
+                                 e4m3x2_of(y[4], y[5]) | e4m3x2_of(y[6], y[7]) << 16);
             }
-            float acc[8];
+        };
+        float acc[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-            const bool k_grown = begun && ks != k_old, v_grown = begun && fresh && vs != v_old;
-            if (begun && (mean || k_grown || v_grown)) {  // the block's earlier tokens
-                const float k_by = k_old / ks, v_by = v_grown ? v_old / vs : 1.f;
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        auto old_keys = [&] {  // of a page that fills up, at their final scale
+#pragma unroll 4
+            for (int c = 0; c < kPairs; ++c) {
+                if (mine + 2 * c >= s0) break;
+                add8(acc, *reinterpret_cast<const uint2 *>(kc + 2 * c * p.tok_stride), ks);
+            }
+        };
+        if (fresh) {
+            {   // values
+                asm volatile("cp.async.wait_group 1;" ::: "memory");
+                uint4 x[kPairs];
+                uint32_t t2 = 0;
 #pragma unroll
                 for (int c = 0; c < kPairs; ++c) {
-                    const int s = g0 + 2 * c + half;
-                    if (s >= s0) continue;
-                    unsigned char *ka = kc + at + s * p.tok_stride, *va = vc + at + s * p.tok_stride;
-                    if (k_grown || mean) {
-                        uint2 b = *reinterpret_cast<const uint2 *>(ka);
-                        if (k_grown) {
-                            float y[8];
-                            floats_of(b, k_by, y);
-                            b = make_uint2(e4m3x2_of(y[0], y[1]) | e4m3x2_of(y[2], y[3]) << 16,
-                                           e4m3x2_of(y[4], y[5]) | e4m3x2_of(y[6], y[7]) << 16);
-                            *reinterpret_cast<uint2 *>(ka) = b;
-                        }
-                        if (mean) add8(acc, b, ks);
-                    }
-                    if (v_grown) {
+                    x[c] = is_new(c) ? own16(raw_v + c * 512) : make_uint4(0, 0, 0, 0);
+                    t2 = top2<T>(x[c], t2);
+                }
+                if (more)
+                    copy(a.v, a.vs, raw_v, grp1, hh1);
+                else
+                    no_copy();
+                float2 t = unpack2<T>(t2);
+                float top = warp_top(fmaxf(t.x, t.y));
+                bool plain = top < Range<T>::kInf;
+                if (!plain) {
+                    top = 0.f;
+#pragma unroll
+                    for (int c = 0; c < kPairs; ++c) {
                         float y[8];
-                        floats_of(*reinterpret_cast<const uint2 *>(va), v_by, y);
-                        *reinterpret_cast<uint2 *>(va) = make_uint2(e4m3x2_of(y[0], y[1]) | e4m3x2_of(y[2], y[3]) << 16,
-                                                                    e4m3x2_of(y[4], y[5]) | e4m3x2_of(y[6], y[7]) << 16);
+                        unpack8<T>(x[c], y);
+                        top = top_fitting<T>(y, top);
                     }
+                    top = warp_top(top);
                 }
-            }
-            if (fresh) {
-                const float k_inv = 1.f / ks, v_inv = 1.f / vs;
+                const float vs = fmaxf(scale_of(top), v_old), inv = 1.f / vs;
+                plain = plain && vs != Range<T>::kTop;
+                if (begun && vs != v_old) shrink(vc, v_old / vs);
 #pragma unroll
                 for (int c = 0; c < kPairs; ++c) {
-                    const int s = g0 + 2 * c + half;
-                    if (s < s0 || s >= s1) continue;
-                    float val[8];
-                    unpack8<T>(xv[c], val);
-                    const uint2 b = bytes_of<T>(key[c], ks, k_inv);
-                    *reinterpret_cast<uint2 *>(kc + at + s * p.tok_stride) = b;
-                    *reinterpret_cast<uint2 *>(vc + at + s * p.tok_stride) = bytes_of<T>(val, vs, v_inv);
+                    float y[8];
+                    unpack8<T>(x[c], y);
+                    if (is_new(c)) *reinterpret_cast<uint2 *>(vc + 2 * c * p.tok_stride) = bytes_of<T>(y, vs, inv, plain);
+                }
+                if (lane == 0) a.vscale[sc] = vs;
+            }
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            auto key = [&](int c, float (&y)[8]) {
+                const bool in = is_new(c);
+                Angles w;
+                if (on) {
+                    const int s = mine + 2 * c, row = !in ? 0 : a.pos ? a.pos[of.t_of + s] : first_row + s;
+                    load_angles(a, clampi(row, 0, a.rows - 1), i, w);
+                }
+                rotate8<T, kInter>(in ? own16(raw_k + c * 512) : make_uint4(0, 0, 0, 0), w, on, lower, peer, y);
+            };
+            float top = 0.f;
+#pragma unroll 2
+            for (int c = c0; c < c1; ++c) {
+                float y[8];
+                key(c, y);
+                top = top_of(y, top);
+            }
+            top = warp_top(top);
+            bool plain = top < Range<T>::kInf;
+            if (!plain) {
+                top = 0.f;
+#pragma unroll 1
+                for (int c = c0; c < c1; ++c) {
+                    float y[8];
+                    key(c, y);
+                    top = top_fitting<T>(y, top);
+                }
+                top = warp_top(top);
+            }
+            ks = fmaxf(scale_of(top), k_old);
+            plain = plain && ks != Range<T>::kTop;
+            const float inv = 1.f / ks;
+            if (begun && ks != k_old) shrink(kc, k_old / ks);
+            if (mean && begun) old_keys();
+#pragma unroll 2
+            for (int c = c0; c < c1; ++c) {
+                float y[8];
+                key(c, y);
+                const uint2 b = bytes_of<T>(y, ks, inv, plain);
+                if (is_new(c)) {
+                    *reinterpret_cast<uint2 *>(kc + 2 * c * p.tok_stride) = b;
                     if (mean) add8(acc, b, ks);
                 }
-                if (lane == 0) {
-                    a.kscale[sc] = ks;
-                    a.vscale[sc] = vs;
-                }
             }
-            if (mean)  // even + odd slots of the group
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float odd = __shfl_down_sync(0xffffffffu, acc[e], 16);
-                    if (half == 0) ssum[((unit * groups + grp) * a.hc + hh) * kD + 8 * i + e] = __fadd_rn(acc[e], odd);
-                }
+            if (more)
+                copy(a.k, a.ks, raw_k, grp1, hh1);
+            else
+                no_copy();
+            if (lane == 0) a.kscale[sc] = ks;
+        } else {
+            old_keys();
+            if (more) {  // a block of earlier tokens alone is followed by one with new ones
+                copy(a.v, a.vs, raw_v, grp1, hh1);
+                copy(a.k, a.ks, raw_k, grp1, hh1);
+            }
         }
+        if (mean)  // even + odd slots of the group
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float odd = __shfl_down_sync(0xffffffffu, acc[e], 16);
+                if (half == 0) ssum[((unit * groups + grp) * a.hc + hh) * kD + 8 * i + e] = __fadd_rn(acc[e], odd);
+            }
+        grp = grp1;
+        hh = hh1;
     }
     grid_go();
     if (!mean) return;
@@ -262,16 +357,19 @@ template <typename T, int HC, int PB> __global__ void __launch_bounds__(256) k_p
 }
 
 template <typename T, int HC, int PB> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {
+    const auto kernel = a.inter ? k_paged8_append<T, true, HC, PB> : k_paged8_append<T, false, HC, PB>;
     const int groups = a.p.page / kGroup;
     a.team = std::min(team_of(a), 8);
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
-    a.hc = HC;
+    a.hc = std::min(HC, 2);
     a.kv_chunks = (a.p.Hkv + a.hc - 1) / a.hc;
     a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
     const long long ctas = (a.units + per_cta - 1) / per_cta * a.chunks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-    const size_t smem = a.mean ? sizeof(float) * per_cta * groups * a.hc * kD : 0;
-    return launch_paged(k_paged8_append<T, HC, PB>, dim3((unsigned)ctas), 32 * warps, smem, 1, a, s);
+    const size_t smem = (size_t)warps * 2 * kRawBytes + (a.mean ? sizeof(float) * per_cta * groups * a.hc * kD : 0);
+    const cudaError_t e = ensure_smem_limit((const void *)kernel, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_paged(kernel, dim3((unsigned)ctas), 32 * warps, smem, 1, a, s);
 }
 
 struct ReadArgs {
@@ -285,7 +383,7 @@ struct ReadArgs {
 };
 
 // The stored values of tokens, as dtype: a warp has one token and a chunk of its heads, half of it keys, the other half
-// values; 8 dims per lane.
+// values.
 template <typename T, int KV> __global__ void __launch_bounds__(256) k_paged_read(ReadArgs a) {
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, half = lane >> 4, i = lane & 15;
@@ -314,23 +412,34 @@ template <typename T, int KV> __global__ void __launch_bounds__(256) k_paged_rea
     }
     const int id = pos >= 0 && pos < p.max_len ? paged_id(p, b, (int)(pos >> p.page_log2)) : -1;
     const int slot = (int)(pos & (p.page - 1));
-    T *to = static_cast<T *>(half ? a.v : a.k) + (long long)t * p.Hkv * kD + 8 * i;
-    const long long from = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + 8 * i;
+    const long long page_at = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride;
+    if constexpr (KV == 8) {  // 16 dims per lane: the keys and the values of two heads at once
+        const int d = 16 * (lane & 7), values = half, odd = (lane >> 3) & 1;
+        const unsigned char *from = static_cast<const unsigned char *>(values ? a.vc : a.kc) + page_at + d;
+        const float *scale = (values ? a.vs : a.ks) + (long long)max(id, 0) * p.Hkv * (p.page / kGroup) + slot / kGroup;
+        T *to = static_cast<T *>(values ? a.v : a.k) + (long long)t * p.Hkv * kD + d;
 #pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (id >= 0) {
-            if constexpr (KV == 8) {
-                const unsigned char *c = static_cast<const unsigned char *>(half ? a.vc : a.kc);
-                const uint2 w = *reinterpret_cast<const uint2 *>(c + from + h * p.head_stride);
-                float y[8];
-                floats_of(w, (half ? a.vs : a.ks)[((long long)id * p.Hkv + h) * (p.page / kGroup) + slot / kGroup], y);
-                x = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
-            } else {
-                x = *reinterpret_cast<const uint4 *>(static_cast<const T *>(half ? a.vc : a.kc) + from + h * p.head_stride);
+        for (int h = h0 + odd; h < h1; h += 2) {
+            uint4 w = make_uint4(0, 0, 0, 0);
+            float by = 0.f;
+            if (id >= 0) {
+                w = *reinterpret_cast<const uint4 *>(from + h * p.head_stride);
+                by = scale[(long long)h * (p.page / kGroup)];
             }
+            float y[8];
+            uint4 *out = reinterpret_cast<uint4 *>(to + (long long)h * kD);
+            floats_of(make_uint2(w.x, w.y), by, y);
+            out[0] = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
+            floats_of(make_uint2(w.z, w.w), by, y);
+            out[1] = make_uint4(pack2<T>(y[0], y[1]), pack2<T>(y[2], y[3]), pack2<T>(y[4], y[5]), pack2<T>(y[6], y[7]));
         }
-        *reinterpret_cast<uint4 *>(to + (long long)h * kD) = x;
+    } else {  // 8 dims per lane: a head's key and value at once
+        const T *from = static_cast<const T *>(half ? a.vc : a.kc) + page_at + 8 * i;
+        T *to = static_cast<T *>(half ? a.v : a.k) + (long long)t * p.Hkv * kD + 8 * i;
+#pragma unroll 4
+        for (int h = h0; h < h1; ++h)
+            *reinterpret_cast<uint4 *>(to + (long long)h * kD) =
+                id >= 0 ? *reinterpret_cast<const uint4 *>(from + h * p.head_stride) : make_uint4(0, 0, 0, 0);
     }
     grid_go();
 }
