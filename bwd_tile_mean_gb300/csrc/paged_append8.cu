@@ -27,7 +27,7 @@ namespace vsa {
 namespace {
 
 // The lane's 8 dims of a key, rotated, in fp32; whole warp. peer: the lane with the other dims of its pairs.
-template <typename T, bool kInter>
+template <typename T, bool kInter, bool kAll>
 __device__ __forceinline__ void rotate8(uint4 x, const Angles &w, bool on, bool lower, int peer, float (&y)[8]) {
     const uint32_t r[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -43,8 +43,8 @@ __device__ __forceinline__ void rotate8(uint4 x, const Angles &w, bool on, bool 
             u = __fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx));
             v = __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy));
         }
-        y[2 * j] = on ? u : e.x;
-        y[2 * j + 1] = on ? v : e.y;
+        y[2 * j] = kAll || on ? u : e.x;
+        y[2 * j + 1] = kAll || on ? v : e.y;
     }
 }
 
@@ -105,11 +105,15 @@ __device__ __forceinline__ void floats_of(uint2 b, float scale, float (&y)[8]) {
         y[2 * j + 1] = v.y * scale;
     }
 }
-__device__ __forceinline__ void add8(float (&acc)[8], uint2 b, float scale) {
-    float y[8];
-    floats_of(b, scale, y);
+// Adds what the bytes stand for over their scale, a power of two: the sums have the bits of those of the values.
+__device__ __forceinline__ void add8(float (&acc)[8], uint2 b) {
+    const uint32_t r[4] = {b.x, b.x >> 16, b.y, b.y >> 16};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = __fadd_rn(acc[e], y[e]);
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = float2_of(r[j]);
+        acc[2 * j] = __fadd_rn(acc[2 * j], v.x);
+        acc[2 * j + 1] = __fadd_rn(acc[2 * j + 1], v.y);
+    }
 }
 template <typename T> __device__ __forceinline__ void unpack8(uint4 x, float (&y)[8]) {
     const uint32_t r[4] = {x.x, x.y, x.z, x.w};
@@ -146,8 +150,10 @@ template <typename T> __device__ __forceinline__ uint32_t top2(uint4 x, uint32_t
 // HC, PB: the queries' heads (2 HC) and pairs of slots at once; a.hc key/value heads per chunk. A warp's next block comes
 // into its part of shared memory (values, keys; a lane reads back what it copied itself) while it works on one, and is
 // walked twice: for the largest entry, and to be rounded. Rotating twice takes fewer instructions than it takes registers to
-// keep 64 rotated entries per lane.
-template <typename T, bool kInter, int HC, int PB> __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
+// keep 64 rotated entries per lane. kAll: all dims are rotated, by the tokens' positions themselves. kFew: for calls
+// of few tokens, whose time is their code's way into the instruction caches.
+template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
+    constexpr int kUnroll = kFew ? 1 : 4;
     extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][kRawBytes], [units of the CTA][groups][hc][128] sums
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15, warps = (int)(blockDim.x >> 5);
@@ -162,17 +168,18 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
     const Unit of = find_unit(a, u, lane);
     const int s0 = of.s0, s1 = of.s1;
     if (chunk >= a.kv_chunks) {
-        append_queries<T, HC, PB>(a, of, (chunk - a.kv_chunks) * 2 * HC, first_grp);
+        const int part = chunk - a.kv_chunks;
+        append_queries<T, HC, PB>(a, of, (a.single ? part * a.team + first_grp : part) * 2 * HC, a.single ? s0 / kGroup : first_grp);
         grid_go();
         return;
     }
     const int id = s1 > s0 ? paged_id(p, of.b, of.pg) : -1;
-    const bool mean = a.mean && s1 == p.page && id >= 0;  // the page fills up in this call
+    const bool mean = a.mean && s1 == p.page;  // the page fills up in this call
     const int h0 = chunk * a.hc, hn = min(a.hc, p.Hkv - h0);
     const long long page_at = (long long)max(id, 0) * p.page_stride + half * p.tok_stride + 8 * i;
     const int hop = a.rot >> 4;  // half style: lanes from a dim to the other of its pair
-    const bool on = 8 * i < a.rot, lower = i < hop;
-    const int peer = (threadIdx.x & 16) | (on ? (lower ? i + hop : i - hop) : i);
+    const bool on = kAll || 8 * i < a.rot, lower = i < hop;
+    const int peer = kAll ? lane ^ 8 : (threadIdx.x & 16) | (on ? (lower ? i + hop : i - hop) : i);
     const int first_row = of.pg << p.page_log2;
     // a lane has slot g0 + 2 c + half of block grp at pair c: the new ones are copied
     auto copy = [&](const void *base, long long stride, uint32_t dst, int grp, int hh) {
@@ -186,15 +193,13 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
     auto no_copy = [] { asm volatile("cp.async.commit_group;" ::: "memory"); };
     auto has_new = [&](int grp) { return grp < groups && grp * kGroup < s1 && grp * kGroup + kGroup > s0; };
     auto skip = [&](int grp) { return grp < groups && !has_new(grp) && !(mean && grp * kGroup < s0); };
-    int grp = first_grp;
-    if (id >= 0) {
-        while (skip(grp)) grp += a.team;
-        if (has_new(grp)) {
-            copy(a.v, a.vs, raw_v, grp, 0);
-            copy(a.k, a.ks, raw_k, grp, 0);
-        }
+    int grp = first_grp, hh = 0;
+    while (skip(grp)) grp += a.team;
+    if (has_new(grp)) {
+        copy(a.v, a.vs, raw_v, grp, hh);
+        copy(a.k, a.ks, raw_k, grp, hh);
     }
-    for (int hh = 0; id >= 0 && grp < groups;) {
+    while (id >= 0 && grp < groups) {
         const int g0 = grp * kGroup, h = h0 + hh, mine = g0 + half;
         const bool fresh = has_new(grp), begun = g0 < s0;
         int grp1 = grp, hh1 = hh + 1;  // the next block
@@ -213,7 +218,7 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
         auto is_new = [&](int c) { return mine + 2 * c >= s0 && mine + 2 * c < s1; };
         // earlier tokens of the block, `by` times what they are
         auto shrink = [&](unsigned char *at, float by) {
-#pragma unroll 2
+#pragma unroll 1
             for (int c = 0; c < kPairs; ++c) {
                 if (mine + 2 * c >= s0) break;
                 uint2 *to = reinterpret_cast<uint2 *>(at + 2 * c * p.tok_stride);
@@ -230,32 +235,25 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
 #pragma unroll 4
             for (int c = 0; c < kPairs; ++c) {
                 if (mine + 2 * c >= s0) break;
-                add8(acc, *reinterpret_cast<const uint2 *>(kc + 2 * c * p.tok_stride), ks);
+                add8(acc, *reinterpret_cast<const uint2 *>(kc + 2 * c * p.tok_stride));
             }
         };
         if (fresh) {
             {   // values
                 asm volatile("cp.async.wait_group 1;" ::: "memory");
-                uint4 x[kPairs];
+                auto value = [&](int c) { return is_new(c) ? own16(raw_v + c * 512) : make_uint4(0, 0, 0, 0); };
                 uint32_t t2 = 0;
-#pragma unroll
-                for (int c = 0; c < kPairs; ++c) {
-                    x[c] = is_new(c) ? own16(raw_v + c * 512) : make_uint4(0, 0, 0, 0);
-                    t2 = top2<T>(x[c], t2);
-                }
-                if (more)
-                    copy(a.v, a.vs, raw_v, grp1, hh1);
-                else
-                    no_copy();
-                float2 t = unpack2<T>(t2);
+#pragma unroll kUnroll
+                for (int c = c0; c < c1; ++c) t2 = top2<T>(value(c), t2);
+                const float2 t = unpack2<T>(t2);
                 float top = warp_top(fmaxf(t.x, t.y));
                 bool plain = top < Range<T>::kInf;
                 if (!plain) {
                     top = 0.f;
-#pragma unroll
-                    for (int c = 0; c < kPairs; ++c) {
+#pragma unroll 1
+                    for (int c = c0; c < c1; ++c) {
                         float y[8];
-                        unpack8<T>(x[c], y);
+                        unpack8<T>(value(c), y);
                         top = top_fitting<T>(y, top);
                     }
                     top = warp_top(top);
@@ -263,26 +261,38 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
                 const float vs = fmaxf(scale_of(top), v_old), inv = 1.f / vs;
                 plain = plain && vs != Range<T>::kTop;
                 if (begun && vs != v_old) shrink(vc, v_old / vs);
-#pragma unroll
-                for (int c = 0; c < kPairs; ++c) {
+#pragma unroll kUnroll
+                for (int c = c0; c < c1; ++c) {
                     float y[8];
-                    unpack8<T>(x[c], y);
+                    unpack8<T>(value(c), y);
                     if (is_new(c)) *reinterpret_cast<uint2 *>(vc + 2 * c * p.tok_stride) = bytes_of<T>(y, vs, inv, plain);
                 }
                 if (lane == 0) a.vscale[sc] = vs;
+                if (more)
+                    copy(a.v, a.vs, raw_v, grp1, hh1);
+                else
+                    no_copy();
             }
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             auto key = [&](int c, float (&y)[8]) {
                 const bool in = is_new(c);
                 Angles w;
-                if (on) {
+                if constexpr (kAll) {  // of slots that are not new too: times 0
+                    const long long at = (long long)min(first_row + mine + 2 * c, a.rows - 1) * 64 + (kInter ? 4 * i : 8 * (i & 7));
+                    load4(w.c, a.cos + at);
+                    load4(w.s, a.sin + at);
+                    if constexpr (!kInter) {
+                        load4(w.c + 4, a.cos + at + 4);
+                        load4(w.s + 4, a.sin + at + 4);
+                    }
+                } else if (on) {
                     const int s = mine + 2 * c, row = !in ? 0 : a.pos ? a.pos[of.t_of + s] : first_row + s;
                     load_angles(a, clampi(row, 0, a.rows - 1), i, w);
                 }
-                rotate8<T, kInter>(in ? own16(raw_k + c * 512) : make_uint4(0, 0, 0, 0), w, on, lower, peer, y);
+                rotate8<T, kInter, kAll>(in ? own16(raw_k + c * 512) : make_uint4(0, 0, 0, 0), w, on, lower, peer, y);
             };
             float top = 0.f;
-#pragma unroll 2
+#pragma unroll kUnroll
             for (int c = c0; c < c1; ++c) {
                 float y[8];
                 key(c, y);
@@ -305,14 +315,14 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
             const float inv = 1.f / ks;
             if (begun && ks != k_old) shrink(kc, k_old / ks);
             if (mean && begun) old_keys();
-#pragma unroll 2
+#pragma unroll kUnroll
             for (int c = c0; c < c1; ++c) {
                 float y[8];
                 key(c, y);
                 const uint2 b = bytes_of<T>(y, ks, inv, plain);
                 if (is_new(c)) {
                     *reinterpret_cast<uint2 *>(kc + 2 * c * p.tok_stride) = b;
-                    if (mean) add8(acc, b, ks);
+                    if (mean) add8(acc, b);
                 }
             }
             if (more)
@@ -331,13 +341,13 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float odd = __shfl_down_sync(0xffffffffu, acc[e], 16);
-                if (half == 0) ssum[((unit * groups + grp) * a.hc + hh) * kD + 8 * i + e] = __fadd_rn(acc[e], odd);
+                if (half == 0) ssum[((unit * groups + grp) * a.hc + hh) * kD + 8 * i + e] = __fadd_rn(acc[e], odd) * ks;
             }
         grp = grp1;
         hh = hh1;
     }
     grid_go();
-    if (!mean) return;
+    if (!mean || id < 0) return;
     ptx::named_sync(1 + unit, 32 * a.team);  // the unit's warps alone: others may have left
     if (first_grp == 0) {  // the groups in order
         const float inv = 1.f / (float)p.page;  // a power of two: exact
@@ -356,14 +366,17 @@ template <typename T, bool kInter, int HC, int PB> __global__ void __launch_boun
     }
 }
 
-template <typename T, int HC, int PB> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {
-    const auto kernel = a.inter ? k_paged8_append<T, true, HC, PB> : k_paged8_append<T, false, HC, PB>;
+template <typename T, int HC, int PB, bool kFew> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {
+    const bool all = a.rot == kD && !a.pos;
+    const auto kernel = a.inter ? (all ? k_paged8_append<T, true, true, HC, PB, kFew> : k_paged8_append<T, true, false, HC, PB, kFew>)
+                                : (all ? k_paged8_append<T, false, true, HC, PB, kFew> : k_paged8_append<T, false, false, HC, PB, kFew>);
     const int groups = a.p.page / kGroup;
     a.team = std::min(team_of(a), 8);
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
-    a.hc = std::min(HC, 2);
+    const int at_once = 2 * HC * (a.single ? a.team : 1);  // query heads per chunk
+    a.hc = a.single ? 1 : std::min(HC, 2);
     a.kv_chunks = (a.p.Hkv + a.hc - 1) / a.hc;
-    a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + 2 * HC - 1) / (2 * HC) : 0);
+    a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + at_once - 1) / at_once : 0);
     const long long ctas = (a.units + per_cta - 1) / per_cta * a.chunks;
     if (ctas > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
     const size_t smem = (size_t)warps * 2 * kRawBytes + (a.mean ? sizeof(float) * per_cta * groups * a.hc * kD : 0);
@@ -468,8 +481,10 @@ extern "C" vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const
     prof_begin("paged8_append", s);
     const bool bf = a.p.dtype == T_BF16;
     const long long chunks = (a.p.Hkv + 3) / 4 + (q ? (a.p.Hq + 7) / 8 : 0), full = T / kGroup * chunks;
-    const cudaError_t e = full > 1216 ? (bf ? launch_append8<__nv_bfloat16, 4, 1>(a, s) : launch_append8<__half, 4, 1>(a, s))
-                                      : (bf ? launch_append8<__nv_bfloat16, 1, 2>(a, s) : launch_append8<__half, 1, 2>(a, s));
+    a.single = !cu_seqlens;
+    const cudaError_t e = a.single      ? (bf ? launch_append8<__nv_bfloat16, 2, 1, true>(a, s) : launch_append8<__half, 2, 1, true>(a, s))
+                          : full > 1216 ? (bf ? launch_append8<__nv_bfloat16, 4, 1, false>(a, s) : launch_append8<__half, 4, 1, false>(a, s))
+                                        : (bf ? launch_append8<__nv_bfloat16, 1, 2, true>(a, s) : launch_append8<__half, 1, 2, true>(a, s));
     prof_end(s);
     return status_from_cuda(e);
 }

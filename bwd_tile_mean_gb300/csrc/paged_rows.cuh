@@ -30,6 +30,7 @@ struct AppendArgs {
     int kv_chunks, chunks;  // chunks of key/value heads, and with the queries'
     int team;               // warps per unit
     int hc;                 // 8 bits: key/value heads per chunk
+    int single;             // 8 bits: one token per sequence
 };
 
 constexpr int kGroup = 16;  // slots per warp, and tokens that share a scale
