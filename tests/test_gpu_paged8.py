@@ -47,7 +47,8 @@ APPEND = [  # layout, dtype, Hq, Hkv, page, rot, interleaved, lengths, new token
 
 
 @pytest.mark.parametrize("case", APPEND, ids=lambda c: f"{c[0]}-{c[2]}x{c[3]}-p{c[4]}-r{c[5]}-{'i' if c[6] else 'h'}")
-def test_append(case):
+@pytest.mark.parametrize("rows", ["own-rows", "given-rows", "short-table"])
+def test_append(case, rows):
     layout, dtype, Hq, Hkv, page, rot, inter, lens, new = case
     need = sum(-(-n // page) for n in lens)
     pool = Pool8(layout, dtype, Hq, Hkv, page, need + 2, max(-(-n // page) for n in lens) + 1, lens, seed=len(lens))
@@ -55,15 +56,17 @@ def test_append(case):
     qkv, q, k, v = new_tokens(pool, T)
     qkv[:, Hq:] *= torch.exp2(torch.randint(-6, 7, (T, 1, 1)).to(dtype))  # some blocks' scales grow, some stay
     cu = [0] + list(itertools.accumulate(new))
-    cos, sin = angles(max(lens) + 1, rot) if rot else (None, None)
+    # a table that ends before the last positions: those take its last row
+    cos, sin = angles(max(lens) + 1 if rows != "short-table" else max(1, max(lens) // 2), rot) if rot else (None, None)
+    pos = torch.randint(-2, max(lens) + 4, (T,), dtype=torch.int32) if rows == "given-rows" else None
     cache = pool.cache()
     q_out = torch.full((T, Hq, D), math.nan, dtype=dtype, device="cuda")
     gpu = qkv.cuda()
     parts = gpu[:, Hq:Hq + Hkv], gpu[:, Hq + Hkv:], gpu[:, :Hq]
     cud = lambda x: None if x is None else x.cuda()  # noqa: E731
-    kw = dict(cu_seqlens=i32(cu), cos=cud(cos), sin=cud(sin), interleaved=inter, q_out=q_out)
+    kw = dict(cu_seqlens=i32(cu), cos=cud(cos), sin=cud(sin), positions=cud(pos), interleaved=inter, q_out=q_out)
     assert cache.append(*parts, **kw) is q_out
-    want = ref8.append(pool, k, v, q, cu, cos, sin, None, inter)
+    want = ref8.append(pool, k, v, q, cu, cos, sin, pos, inter)
     equal_bytes(pool, cache)
     assert same(cache.k_mean, pool.mean), "means"
     assert torch.equal(torch.isnan(q_out).cpu(), torch.isnan(want)), "q rows written"
@@ -107,6 +110,31 @@ def test_append_in_pieces(page):
     for a, b in ((pieces.k, whole.k), (pieces.v, whole.v)):
         a, b = a.float(), b.float()
         assert ((a == b) | ((a - b).abs() <= 2.0 ** -9) & (b.abs() < 2.0 ** -6)).all()
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,page", [(300, 8, 2, 16), (70, 20, 5, 64), (5, 40, 40, 256)])
+def test_next_tokens_of_a_batch(B, Hq, Hkv, page):
+    """One token per sequence, some at a page's last slot, some at a block's
+    first, rows of length 0 among them; twice in a row."""
+    g = torch.Generator().manual_seed(B)
+    lens = torch.randint(0, 3 * page, (B,), generator=g).tolist()
+    lens[0], lens[1], lens[2], lens[3] = 0, page, 2 * page, 17
+    pool = Pool8("bhsd", BF, Hq, Hkv, page, 3 * B + 3, 4, [n + 1 if n else 0 for n in lens], seed=2)
+    pool.lens = list(lens)
+    cache = pool.cache()
+    cos, sin = angles(3 * page + 2, 128)
+    for step in range(2):
+        _, q, k, v = new_tokens(pool, B, seed=step)
+        k *= torch.exp2(torch.randint(-2, 5, (B, Hkv, 1), generator=g).to(BF))
+        q_out = cache.append(k.cuda(), v.cuda(), q.cuda(), cos=cos.cuda(), sin=sin.cuda(),
+                             q_out=torch.full_like(q, math.nan).cuda())
+        want = ref8.append(pool, k, v, q, list(range(B + 1)), cos, sin)
+        equal_bytes(pool, cache)
+        assert same(cache.k_mean, pool.mean)
+        fine = ~torch.isnan(want)
+        assert torch.equal(torch.isnan(q_out).cpu(), ~fine) and torch.equal(q_out.cpu()[fine], want[fine])
+        pool.lens = [n + 1 if n else 0 for n in pool.lens]
+        cache.seq_lens.copy_(i32(pool.lens))
 
 
 @pytest.mark.parametrize("dtype", [BF, HF])
@@ -245,6 +273,18 @@ def test_attend(case, wide):
             ref.check_attend(cache.attend(q.cuda(), (idx.cuda(), cnt.cuda())), ref8.attend(pool, q, (idx, cnt)), "lists")
 
 
+@pytest.mark.parametrize("eight", [True, False])
+def test_attend_with_a_scale_of_its_own(eight):
+    pool = pool_of(ATTEND[4], eight)
+    q, w = queries(pool), weights_of(pool)
+    wd = w.cuda()
+    cache = pool.cache(scale=0.02, weigh=True)
+    got = cache.attend(q.cuda(), page_weight=wd)
+    want = ref8.attend(pool, q, scale=0.02, weight=w)
+    ref.check_attend(got, want[:4])
+    check_weights(pool, wd, want, w)
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("size", [1e-4, 1e-2, 1.0, 30.0])
 def test_attend_with_queries_of_any_size(dtype, size):
@@ -362,6 +402,10 @@ EVICT = [  # Hkv, page, max_pages, lengths, keep, keep_first, keep_last
     (2, 16, 5000, [16 * 4800 + 3, 16 * 2000], 4000, 4, 8),
     (1, 256, 6, [256 * 6 + 100], 3, 0, 1),                     # a length past the table
     (2, 16, 50, [-5, 16 * 50], 60, 0, 1),                      # keeps more than the table holds
+    (24, 32, 300, [32 * 290, 32 * 150 + 1], 140, 2, 3),        # one CTA with rows in several turns
+    (40, 16, 700, [16 * 699 + 2], 300, 0, 1),                  # more heads than that
+    (3, 16, 20000, [16 * 19990, 16 * 9000], 8500, 100, 50),    # more pages than a CTA holds at once
+    (1, 16, 8300, [16 * 8300 - 1], 8299, 0, 1),
 ]
 
 

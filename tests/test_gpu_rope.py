@@ -262,3 +262,27 @@ def test_with_tiles_and_block_sparse_attention():
         # the rotation's inputs, outputs and gradients and the attention's P, dS and outputs each round to bf16 once
         rel = float((got - want).norm() / want.norm())
         assert rel <= 6 * U[dtype], (name, rel)
+
+
+def test_offsets_past_32_bits():
+    """Tokens 2^31 elements apart, and more heads than one unit takes."""
+    rope = vsa().AxialRope((44, 42, 42))
+    pos = torch.tensor([[3, 4, 5], [700, 8, 9], [11, 0, 77]], dtype=torch.int32).cuda()
+    apart = (1 << 31) + 512
+    buf = torch.empty(2 * apart + 128 * 24, dtype=torch.bfloat16, device="cuda")
+    x = buf.as_strided((1, 3, 24, D), (0, apart, D, 1))
+    x.copy_(torch.randn(1, 3, 24, D, generator=torch.Generator().manual_seed(1)))
+    want = rope.forward(x.contiguous(), positions=pos)
+    assert torch.equal(rope.forward(x, positions=pos), want)
+    rope.forward(x, positions=pos, q_out=x)
+    assert torch.equal(x, want)
+
+
+def test_tokens_without_heads_or_batch():
+    rope = vsa().AxialRope((64, 64))
+    pos = torch.zeros(3, 2, dtype=torch.int32).cuda()
+    x = torch.randn(1, 3, 2, D, device="cuda").bfloat16()
+    q, k = rope.forward(x, x[:, :, :0], positions=pos)
+    assert k.shape == (1, 3, 0, D) and torch.equal(q, x)  # position 0: no turn
+    assert rope.forward(x[:0], positions=pos).shape == (0, 3, 2, D)
+    assert rope.table(pos[:0])[0].shape == (0, 64)
