@@ -169,7 +169,7 @@ template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __globa
     const int s0 = of.s0, s1 = of.s1;
     if (chunk >= a.kv_chunks) {
         const int part = chunk - a.kv_chunks;
-        append_queries<T, HC, PB>(a, of, (a.single ? part * a.team + first_grp : part) * 2 * HC, a.single ? s0 / kGroup : first_grp);
+        append_queries<T, HC, PB, !kAll ? 0 : kInter ? 1 : 2>(a, of, (a.single ? part * a.team + first_grp : part) * 2 * HC, a.single ? s0 / kGroup : first_grp);
         grid_go();
         return;
     }

@@ -145,9 +145,29 @@ __device__ __forceinline__ uint4 rotate(const AppendArgs &a, uint4 x, const Angl
     return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
+// rotate() of a whole head (128 dims) in one style: the same bits.
+template <typename T, bool kInter> __device__ __forceinline__ uint4 rotate_all(uint4 x, const Angles &w, bool lower) {
+    uint32_t r[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 e = unpack2<T>(r[j]);
+        if constexpr (kInter) {
+            r[j] = pack2<T>(__fsub_rn(__fmul_rn(e.x, w.c[j]), __fmul_rn(e.y, w.s[j])),
+                            __fadd_rn(__fmul_rn(e.y, w.c[j]), __fmul_rn(e.x, w.s[j])));
+        } else {
+            const float2 f = unpack2<T>(__shfl_xor_sync(0xffffffffu, r[j], 8));
+            const float sx = lower ? -w.s[2 * j] : w.s[2 * j], sy = lower ? -w.s[2 * j + 1] : w.s[2 * j + 1];
+            r[j] = pack2<T>(__fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx)),
+                            __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy)));
+        }
+    }
+    return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
 // The rotated queries of a unit's tokens, heads h0 .. h0 + 2 HC - 1: a warp
-// takes the 16-slot groups first_grp, first_grp + team, ..
-template <typename T, int HC, int PB>
+// takes the 16-slot groups first_grp, first_grp + team, .. kStyle: 0 any
+// rotation; all dims, interleaved (1) or not (2), at the tokens' positions.
+template <typename T, int HC, int PB, int kStyle = 0>
 __device__ __forceinline__ void append_queries(const AppendArgs &a, const Unit &of, int h0, int first_grp) {
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, half = lane >> 4, i = lane & 15;
@@ -169,7 +189,15 @@ __device__ __forceinline__ void append_queries(const AppendArgs &a, const Unit &
                 x[c][h] = fresh && h < hn
                               ? *reinterpret_cast<const uint4 *>(q + tok * a.qs + (h0 + h) * kD + 8 * i)
                               : make_uint4(0, 0, 0, 0);
-            if (fresh && 8 * i < a.rot) {
+            if constexpr (kStyle != 0) {
+                const long long at = (long long)min((pg << p.page_log2) + s, a.rows - 1) * 64 + (kStyle == 1 ? 4 * i : 8 * (i & 7));
+                load4(w[c].c, a.cos + at);
+                load4(w[c].s, a.sin + at);
+                if constexpr (kStyle == 2) {
+                    load4(w[c].c + 4, a.cos + at + 4);
+                    load4(w[c].s + 4, a.sin + at + 4);
+                }
+            } else if (fresh && 8 * i < a.rot) {
                 const int row = a.pos ? a.pos[tok] : (pg << p.page_log2) + s;
                 load_angles(a, clampi(row, 0, a.rows - 1), i, w[c]);
             }
@@ -181,7 +209,10 @@ __device__ __forceinline__ void append_queries(const AppendArgs &a, const Unit &
             const long long tok = fresh ? t_of + s : 0;
 #pragma unroll
             for (int h = 0; h < 2 * HC; ++h) {
-                if (a.rot) x[c][h] = rotate<T>(a, x[c][h], w[c], i);
+                if constexpr (kStyle != 0)
+                    x[c][h] = rotate_all<T, kStyle == 1>(x[c][h], w[c], i < 8);
+                else if (a.rot)
+                    x[c][h] = rotate<T>(a, x[c][h], w[c], i);
                 if (fresh && h < hn)
                     *reinterpret_cast<uint4 *>(qo + (tok * p.Hq + h0 + h) * kD + 8 * i) = x[c][h];
             }
