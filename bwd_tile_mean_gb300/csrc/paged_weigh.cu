@@ -58,33 +58,44 @@ __device__ __forceinline__ float group_sum(const WeighArgs &a, float x) {
     return x * a.drop;
 }
 
-// All pages: kWeighDeep pages per group of lanes. 64 sequences of up to 16,000 keys x 8 heads with 4 queries each, 94,000
-// blocks: 14 us with a thread per page, which reads its records one after another; 16 by groups of lanes with divisions for
-// each page.
+// All pages: kWeighDeep pages per group of lanes, whose sums go through shared memory so that weights are read and written
+// side by side. 64 sequences of up to 16,000 keys x 8 heads with 4 queries each (94,000 blocks, 512 rows of 250 pages) add
+// 5 us to the attention's 74; a thread per page, which reads its records one after another, 14; a weight read and
+// written by each group 8.
 __global__ void __launch_bounds__(kWeighThreads) k_page_weigh(WeighArgs a) {
+    __shared__ float s_sum[kWeighThreads * kWeighDeep];
     const Paged &p = a.p;
-    const int per = kWeighThreads >> a.lanes;
+    const int per = kWeighThreads >> a.lanes, span = per * kWeighDeep, tid = threadIdx.x;
     const unsigned bh = blockIdx.x / a.chunks, b = bh / (unsigned)p.Hkv, h = bh - b * p.Hkv;
-    const int me = threadIdx.x & ((1 << a.lanes) - 1);
-    const int j0 = (int)(blockIdx.x - bh * a.chunks) * per * kWeighDeep + (threadIdx.x >> a.lanes);
+    const int me = tid & ((1 << a.lanes) - 1), slot = tid >> a.lanes, j0 = (int)(blockIdx.x - bh * a.chunks) * span;
+    const long long at = (long long)bh * p.max_pages + j0;
     grid_wait();
     grid_go();
-    const int len = paged_len(p, (int)b);
-    float mass[kWeighDeep], old[kWeighDeep];
+    const int len = paged_len(p, (int)b), mine = min(span, p.max_pages - j0);
+    if ((long long)j0 << p.page_log2 >= len) {  // behind the sequence's end
+        if (a.out != a.in)
+            for (int i = tid; i < mine; i += kWeighThreads) a.out[at + i] = a.in[at + i];
+        return;
+    }
+    const float old = tid < mine ? a.in[at + tid] : 0.f;
+    float mass[kWeighDeep];
 #pragma unroll
     for (int d = 0; d < kWeighDeep; ++d) {
-        const int j = j0 + d * per;
+        const int j = j0 + slot + d * per;
         const bool live = j < p.max_pages && j << p.page_log2 < len;
         const int from = live ? j << p.page_log2 : 0;
-        old[d] = j < p.max_pages && me == 0 && !(live && a.decay == 0.f) ? a.in[(long long)bh * p.max_pages + j] : 0.f;
         mass[d] = live ? mass_of(a, (int)b, (int)h, (int)bh, from >> 4, (min(len - from, p.page) + 15) >> 4, me) : 0.f;
     }
 #pragma unroll
     for (int d = 0; d < kWeighDeep; ++d) {
-        const int j = j0 + d * per;
         const float sum = group_sum(a, mass[d]);
-        if (me == 0 && j < p.max_pages)
-            a.out[(long long)bh * p.max_pages + j] = j << p.page_log2 < len ? fmaf(a.decay, old[d], sum) : old[d];
+        if (me == 0) s_sum[slot + d * per] = sum;
+    }
+    __syncthreads();
+    for (int i = tid; i < mine; i += kWeighThreads) {
+        const float was = i == tid ? old : a.in[at + i];
+        const bool live = (j0 + i) << p.page_log2 < len;
+        a.out[at + i] = !live ? was : a.decay == 0.f ? s_sum[i] : fmaf(a.decay, was, s_sum[i]);
     }
 }
 
@@ -183,7 +194,11 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
 // takes the additions of a warp one after another), until a bin stays as a whole or its keys are all equal. Then one scan
 // per N E entries places them. An entry moves to a place at or before its own, and a chunk is read before any of it is
 // written, so a row may be moved in place. What will be moved is loaded first of all.
-constexpr int kBins = 2048, kRowsAhead = 8;
+//
+// Chains of loads and barriers bound it: 64 sequences of up to 250 pages x 8 heads 6.9 us in one launch (7.9 with the keys
+// before each counted instead of the digits); one of 7,680 pages x 24 heads 15.9, 4 of them the sums. With 8-bit digits and
+// 512 entries placed at a time the latter took 18.9, and 25 where a warp's lanes matched their bins first.
+constexpr int kBins = 2048, kRowsAhead = 10;  // rows: 8, 10, 16 took 7.0, 6.9, 7.8 us on the 64 sequences
 template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
     constexpr int W = N / 32, kChunk = N * E, R = kOne ? kRowsAhead : 1;
     static_assert(!kOne || E == 1, "one page per thread");
@@ -268,11 +283,7 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
             }
             if (lane == 31) s_warp[wid] = inc;
             __syncthreads();
-            int below = 0;
-#pragma unroll
-            for (int v = 0; v < W; ++v)
-                if (v < wid) below += s_warp[v];
-            inc += below;
+            inc += __reduce_add_sync(0xffffffffu, lane < wid ? s_warp[lane] : 0);
             if (inc - mine < left && left <= inc) {  // one thread
                 int before = inc - mine, at = kBins - 1 - tid * kPer;
                 while (before + s_hist[at] < left) before += s_hist[at--];
@@ -320,12 +331,8 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
         __syncthreads();  // s_warp was read
         if (lane == 31) s_warp[wid] = inc;
         __syncthreads();
-        int all = 0;
-#pragma unroll
-        for (int v = 0; v < W; ++v) {
-            if (v == wid) inc += all;
-            all += s_warp[v];
-        }
+        const int of_warp = lane < W ? s_warp[lane] : 0, all = __reduce_add_sync(0xffffffffu, of_warp);
+        inc += __reduce_add_sync(0xffffffffu, lane < wid ? of_warp : 0);
         int g = above + ((inc - mine) & 0xffff), q = equal + ((inc - mine) >> 16);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
