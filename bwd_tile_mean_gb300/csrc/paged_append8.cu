@@ -47,10 +47,11 @@ __device__ __forceinline__ void rotate8(uint4 x, const Angles &w, bool on, bool 
             u = __fsub_rn(__fmul_rn(e.x, w.c[j]), __fmul_rn(e.y, w.s[j]));
             v = __fadd_rn(__fmul_rn(e.y, w.c[j]), __fmul_rn(e.x, w.s[j]));
         } else {
-            const float2 f = unpack2<T>(__shfl_sync(0xffffffffu, r[j], peer));
-            const float sx = lower ? -w.s[2 * j] : w.s[2 * j], sy = lower ? -w.s[2 * j + 1] : w.s[2 * j + 1];
-            u = __fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, sx));
-            v = __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, sy));
+            // lower dims: x1 c + (-x2) s, the same bits as x1 c - x2 s. (Paired multiplications and additions become fused
+            // ones, which round once.)
+            const float2 f = unpack2<T>(__shfl_sync(0xffffffffu, r[j], peer) ^ (lower ? 0x80008000u : 0u));
+            u = __fadd_rn(__fmul_rn(e.x, w.c[2 * j]), __fmul_rn(f.x, w.s[2 * j]));
+            v = __fadd_rn(__fmul_rn(e.y, w.c[2 * j + 1]), __fmul_rn(f.y, w.s[2 * j + 1]));
         }
         y[2 * j] = kAll || on ? u : e.x;
         y[2 * j + 1] = kAll || on ? v : e.y;
@@ -89,7 +90,10 @@ template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)
     uint32_t r[4];
     if (plain) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) r[j] = e4m3x2_of(x[2 * j] * inv, x[2 * j + 1] * inv);
+        for (int j = 0; j < 4; ++j) {
+            const float2 y = ptx::f32x2_split(ptx::fmul_x2(ptx::f32x2(x[2 * j], x[2 * j + 1]), ptx::f32x2(inv, inv)));
+            r[j] = e4m3x2_of(y.x, y.y);
+        }
     } else {
         const float most = scale == Range<T>::kTop ? 240.f : 448.f;
 #pragma unroll
@@ -120,8 +124,9 @@ __device__ __forceinline__ void add8(float (&acc)[8], uint2 b) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const float2 v = float2_of(r[j]);
-        acc[2 * j] = __fadd_rn(acc[2 * j], v.x);
-        acc[2 * j + 1] = __fadd_rn(acc[2 * j + 1], v.y);
+        const float2 sum = ptx::f32x2_split(ptx::fadd_x2(ptx::f32x2(acc[2 * j], acc[2 * j + 1]), ptx::f32x2(v.x, v.y)));
+        acc[2 * j] = sum.x;
+        acc[2 * j + 1] = sum.y;
     }
 }
 template <typename T> __device__ __forceinline__ void unpack8(uint4 x, float (&y)[8]) {
@@ -375,6 +380,10 @@ template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __globa
     }
 }
 
+// Groups of tokens, counted once for every four key and every eight query heads, from which a warp has two key heads, whose
+// angles it reads once from memory: 30,000 tokens of 24 heads 208 us, with one 233, with four 219; 6,000 70, 66, 77.
+constexpr long long kTwoHeads = 8192;
+
 template <typename T, int HC, int PB, bool kFew> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {
     const bool all = a.rot == kD && !a.pos;
     const auto kernel = a.inter ? (all ? k_paged8_append<T, true, true, HC, PB, kFew> : k_paged8_append<T, true, false, HC, PB, kFew>)
@@ -383,7 +392,6 @@ template <typename T, int HC, int PB, bool kFew> cudaError_t launch_append8(Appe
     a.team = std::min(team_of(a), 8);
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
     const int at_once = 2 * HC * (a.single ? a.team : 1);  // query heads per chunk
-    a.hc = a.single ? 1 : std::min(HC, 2);
     a.kv_chunks = (a.p.Hkv + a.hc - 1) / a.hc;
     a.chunks = a.kv_chunks + (a.q ? (a.p.Hq + at_once - 1) / at_once : 0);
     const long long ctas = (a.units + per_cta - 1) / per_cta * a.chunks;
@@ -491,8 +499,14 @@ extern "C" vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const
     const bool bf = a.p.dtype == T_BF16;
     const long long chunks = (a.p.Hkv + 3) / 4 + (q ? (a.p.Hq + 7) / 8 : 0), full = T / kGroup * chunks;
     a.single = !cu_seqlens;
+    a.hc = full > kTwoHeads ? 2 : 1;
+    // Loops unrolled four deep, and eight query heads per warp, where pages are short or the tokens many; rolled ones, with two
+    // heads and four rows, for units of many groups, whose warps are many as it is (us, unrolled / rolled): 1,000 tokens of 8
+    // key heads in 64-token pages 10.0 / 10.5, 3,000 16.0 / 19.2, 8 x 1,000 of 2 16.5 / 20.8; 13 x 190 of 3 in 128-token pages
+    // 13.7 / 12.2, 4 x 500 of 24 in 256-token ones 26.6 / 22.7, 2 x 3,000 66.5 / 63.5.
+    const bool deep = a.p.page <= 64 || full > kTwoHeads;
     const cudaError_t e = a.single      ? (bf ? launch_append8<__nv_bfloat16, 2, 1, true>(a, s) : launch_append8<__half, 2, 1, true>(a, s))
-                          : full > 1216 ? (bf ? launch_append8<__nv_bfloat16, 4, 1, false>(a, s) : launch_append8<__half, 4, 1, false>(a, s))
+                          : deep     ? (bf ? launch_append8<__nv_bfloat16, 4, 1, false>(a, s) : launch_append8<__half, 4, 1, false>(a, s))
                                         : (bf ? launch_append8<__nv_bfloat16, 1, 2, true>(a, s) : launch_append8<__half, 1, 2, true>(a, s));
     prof_end(s);
     return status_from_cuda(e);
