@@ -17,8 +17,8 @@
 // a warp per token row, 8 dims per lane.
 //
 // Bound by instructions for long prompts: 30,000 tokens of 24 heads (0.92 GB) take
-// 208 us, 65% of the measured copy rate, with 54% of the issue slots and 58% of
-// DRAM's peak busy; the blocks are rotated, searched and rounded in fp32. Measured
+// 204 us, 66% of the measured copy rate, with 54% of the issue slots and 58% of
+// DRAM's peak busy (half style, whose pairs lie in two lanes, a fifth more); the blocks are rotated, searched and rounded in fp32. Measured
 // on the way there (us): rotated keys kept in registers, 8 warps per SM 360; with
 // 128 registers and spills 377; walked twice from shared memory 266, two heads per
 // warp 248 (one 272, four 266), with angles by position 207, loops unrolled four deep
