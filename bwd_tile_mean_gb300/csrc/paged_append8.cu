@@ -18,8 +18,8 @@
 //
 // Bound by instructions for long prompts: 30,000 tokens of 24 heads (0.92 GB) take
 // 204 us, 66% of the measured copy rate, with 54% of the issue slots and 58% of
-// DRAM's peak busy (half style, whose pairs lie in two lanes, a fifth more); the blocks are rotated, searched and rounded in fp32. Measured
-// on the way there (us): rotated keys kept in registers, 8 warps per SM 360; with
+// DRAM's peak busy (half style, whose pairs lie in two lanes, a fifth more); the
+// blocks are rotated, searched and rounded in fp32. Measured on the way there (us): rotated keys kept in registers, 8 warps per SM 360; with
 // 128 registers and spills 377; walked twice from shared memory 266, two heads per
 // warp 248 (one 272, four 266), with angles by position 207, loops unrolled four deep
 // 203 (two 207, one 221); a head instead of a group per warp, which share their
@@ -166,7 +166,8 @@ template <typename T> __device__ __forceinline__ uint32_t top2(uint4 x, uint32_t
 // walked twice: for the largest entry, and to be rounded. Rotating twice takes fewer instructions than it takes registers to
 // keep 64 rotated entries per lane. kAll: all dims are rotated, by the tokens' positions themselves. kFew: for calls
 // of few tokens, whose time is their code's way into the instruction caches.
-template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
+template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew>
+__global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
     constexpr int kUnroll = kFew ? 1 : 4;
     extern __shared__ __align__(16) unsigned char smem[];  // [warps][2][kRawBytes], [units of the CTA][groups][hc][128] sums
     const Paged &p = a.p;
@@ -183,7 +184,8 @@ template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __globa
     const int s0 = of.s0, s1 = of.s1;
     if (chunk >= a.kv_chunks) {
         const int part = chunk - a.kv_chunks;
-        append_queries<T, HC, PB, !kAll ? 0 : kInter ? 1 : 2>(a, of, (a.single ? part * a.team + first_grp : part) * 2 * HC, a.single ? s0 / kGroup : first_grp);
+        append_queries<T, HC, PB, !kAll ? 0 : kInter ? 1 : 2>(a, of, (a.single ? part * a.team + first_grp : part) * 2 * HC,
+                                                              a.single ? s0 / kGroup : first_grp);
         grid_go();
         return;
     }
@@ -212,6 +214,7 @@ template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __globa
     if (has_new(grp)) {
         copy(a.v, a.vs, raw_v, grp, hh);
         copy(a.k, a.ks, raw_k, grp, hh);
+        if (id < 0) asm volatile("cp.async.wait_group 0;" ::: "memory");  // nothing to store: the copies do not outlive the warp
     }
     while (id >= 0 && grp < groups) {
         const int g0 = grp * kGroup, h = h0 + hh, mine = g0 + half;
@@ -292,7 +295,8 @@ template <typename T, bool kInter, bool kAll, int HC, int PB, bool kFew> __globa
                 const bool in = is_new(c);
                 Angles w;
                 if constexpr (kAll) {  // of slots that are not new too: times 0
-                    const long long at = (long long)min(first_row + mine + 2 * c, a.rows - 1) * 64 + (kInter ? 4 * i : 8 * (i & 7));
+                    const int row = min(first_row + mine + 2 * c, a.rows - 1);
+                    const long long at = (long long)row * 64 + (kInter ? 4 * i : 8 * (i & 7));
                     load4(w.c, a.cos + at);
                     load4(w.s, a.sin + at);
                     if constexpr (!kInter) {
@@ -386,8 +390,10 @@ constexpr long long kTwoHeads = 8192;
 
 template <typename T, int HC, int PB, bool kFew> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {
     const bool all = a.rot == kD && !a.pos;
-    const auto kernel = a.inter ? (all ? k_paged8_append<T, true, true, HC, PB, kFew> : k_paged8_append<T, true, false, HC, PB, kFew>)
-                                : (all ? k_paged8_append<T, false, true, HC, PB, kFew> : k_paged8_append<T, false, false, HC, PB, kFew>);
+    const auto kernel = a.inter ? (all ? k_paged8_append<T, true, true, HC, PB, kFew>
+                                       : k_paged8_append<T, true, false, HC, PB, kFew>)
+                                : (all ? k_paged8_append<T, false, true, HC, PB, kFew>
+                                       : k_paged8_append<T, false, false, HC, PB, kFew>);
     const int groups = a.p.page / kGroup;
     a.team = std::min(team_of(a), 8);
     const int warps = a.team > 4 ? a.team : 4, per_cta = warps / a.team;
@@ -505,9 +511,13 @@ extern "C" vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const
     // key heads in 64-token pages 10.0 / 10.5, 3,000 16.0 / 19.2, 8 x 1,000 of 2 16.5 / 20.8; 13 x 190 of 3 in 128-token pages
     // 13.7 / 12.2, 4 x 500 of 24 in 256-token ones 26.6 / 22.7, 2 x 3,000 66.5 / 63.5.
     const bool deep = a.p.page <= 64 || full > kTwoHeads;
-    const cudaError_t e = a.single      ? (bf ? launch_append8<__nv_bfloat16, 2, 1, true>(a, s) : launch_append8<__half, 2, 1, true>(a, s))
-                          : deep     ? (bf ? launch_append8<__nv_bfloat16, 4, 1, false>(a, s) : launch_append8<__half, 4, 1, false>(a, s))
-                                        : (bf ? launch_append8<__nv_bfloat16, 1, 2, true>(a, s) : launch_append8<__half, 1, 2, true>(a, s));
+    cudaError_t e;
+    if (a.single)
+        e = bf ? launch_append8<__nv_bfloat16, 2, 1, true>(a, s) : launch_append8<__half, 2, 1, true>(a, s);
+    else if (deep)
+        e = bf ? launch_append8<__nv_bfloat16, 4, 1, false>(a, s) : launch_append8<__half, 4, 1, false>(a, s);
+    else
+        e = bf ? launch_append8<__nv_bfloat16, 1, 2, true>(a, s) : launch_append8<__half, 1, 2, true>(a, s);
     prof_end(s);
     return status_from_cuda(e);
 }

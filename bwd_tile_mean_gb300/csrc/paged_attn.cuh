@@ -456,7 +456,10 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 
 __device__ __forceinline__ uint4 lds16(uint32_t addr) {
     uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint32_t turn8x8(uint32_t x) {
@@ -476,7 +479,8 @@ __device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, ui
         uint4 x[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-            x[c] = row < sg.rows ? reinterpret_cast<const uint4 *>(from + (long long)row * kD + 32 * t)[c] : make_uint4(0, 0, 0, 0);
+            x[c] = row < sg.rows ? reinterpret_cast<const uint4 *>(from + (long long)row * kD + 32 * t)[c]
+                                 : make_uint4(0, 0, 0, 0);
         uint32_t w[16] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w,
                           x[2].x, x[2].y, x[2].z, x[2].w, x[3].x, x[3].y, x[3].z, x[3].w};
         float down = 1.f;
@@ -512,8 +516,8 @@ __device__ __forceinline__ void load_q8(const AttnArgs &a, const Segment &sg, ui
 // store_weights for the turned scores: sc[block][8 n + ..] has keys g, g + 8 by heads 2 t, 2 t + 1. The eight lanes of a
 // head add up; four of them end with one (block, head) each.
 template <int NT>
-__device__ __forceinline__ void store_weights8(const AttnArgs &a, const Segment &sg, int blk, int end, const float (&sc)[2][NT][4],
-                                               const float (&ref)[2 * NT]) {
+__device__ __forceinline__ void store_weights8(const AttnArgs &a, const Segment &sg, int blk, int end,
+                                               const float (&sc)[2][NT][4], const float (&ref)[2 * NT]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, e = g & 1, h = (g >> 1) & 1;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -604,7 +608,8 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
             const unsigned char *src = from + at[h];
             if (ok[h] == kBlk) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) cp16((dst + h * kBlk * 128 + e * 512) ^ ((e & 1) << 6), src + (uint64_t)e * four_rows);
+                for (int e = 0; e < 4; ++e)
+                    cp16((dst + h * kBlk * 128 + e * 512) ^ ((e & 1) << 6), src + (uint64_t)e * four_rows);
             } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -822,7 +827,8 @@ template <int NT> struct Frag {
         const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
         if constexpr (k8) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) f(16 * j + 2 * g, make_float2(acc[8 * (r >> 1) + j][r & 1], acc[8 * (r >> 1) + j][2 + (r & 1)]));
+            for (int j = 0; j < 8; ++j)
+                f(16 * j + 2 * g, make_float2(acc[8 * (r >> 1) + j][r & 1], acc[8 * (r >> 1) + j][2 + (r & 1)]));
         } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j) f(8 * j + 2 * t, make_float2(acc[j][2 * r], acc[j][2 * r + 1]));

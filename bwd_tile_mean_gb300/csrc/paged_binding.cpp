@@ -343,6 +343,7 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         apart(po, {pl, pt, pp});
         apart(pl, {pt, pp});
         if (pw && pt.at != pp.at) apart(pt, {pp});
+        apart(cache_ws(c, pw != nullptr), {pp});
         at::Tensor out = go ? *go : output(c, {c.d.B, c.d.Hq, c.d.D}, c.dtype());
         at::Tensor lse = gl ? *gl : output(c, {c.d.B, c.d.Hq}, at::kFloat);
         const int cap = idx ? (int)idx->size(2) : 0;
@@ -427,6 +428,7 @@ PyObject *calls_evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                 if (i != j || outs[i].at != in[j].at) apart(outs[i], {in[j]});
             for (int j = 0; j < i; ++j) apart(outs[i], {outs[j]});
         }
+        apart(cache_ws(c), {in[2]});
         at::Tensor freed = gf ? *gf : output(c, {c.d.B, cap}, at::kInt);
         at::Tensor count = gc ? *gc : output(c, {c.d.B}, at::kInt);
         run(c, "vsa_page_evict", [&](vsa_stream_t s) {
@@ -631,7 +633,8 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             const char *name = i ? "k_out" : "q_out";
             if (given[i]) {
                 same_device(q, name, *given[i], dtype);
-                if (given[i]->sizes() != in[i]->sizes()) refuse(name, ": expected ", in[i]->sizes(), ", got ", given[i]->sizes());
+                if (given[i]->sizes() != in[i]->sizes())
+                    refuse(name, ": expected ", in[i]->sizes(), ", got ", given[i]->sizes());
                 out[i] = *given[i];
             } else {
                 out[i] = at::empty(in[i]->sizes(), in[i]->options().memory_format(c10::nullopt));
@@ -640,7 +643,8 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             if (!given[i]) continue;
             if (!empty(y[i]) && !rows_apart(y[i])) refuse(name, ": its rows share memory");
             for (int j = 0; j < count; ++j)
-                if (!(i == j && same_place(y[i], x[j])) && !are_apart(y[i], x[j])) refuse(name, ": shares memory with ", x[j].name);
+                if (!(i == j && same_place(y[i], x[j])) && !are_apart(y[i], x[j]))
+                    refuse(name, ": shares memory with ", x[j].name);
             const char *first = y[i].at, *end = first + (empty(y[i]) ? 0 : y[i].last());
             const Tokens m = as_tokens(pos, "positions");
             if (!empty(m) && !empty(y[i]) && m.at < end && first < m.at + m.n[1]) refuse(name, ": shares memory with positions");

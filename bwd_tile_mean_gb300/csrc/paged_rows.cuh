@@ -1,8 +1,8 @@
 // paged_rows.cuh -- what the appends to a 16-bit and to an 8-bit cache share:
 // their arguments and checks, and which warp has which tokens. Internal.
 //
-// A unit is one page of one sequence that receives tokens. Units are found without a scan of the lengths: sequence b with tokens
-// [cu[b], cu[b+1]) touches at most (cu[b+1] - cu[b]) / page + 2 pages, so
+// A unit is one page of one sequence that receives tokens. Units are found
+// without a scan of the lengths: sequence b with tokens [cu[b], cu[b+1]) touches at most (cu[b+1] - cu[b]) / page + 2 pages, so
 // numbering its units from cu[b] / page + 2 b leaves room for them, and a
 // warp finds its b with a 32-way search of that ascending sequence.
 #pragma once
@@ -190,7 +190,8 @@ __device__ __forceinline__ void append_queries(const AppendArgs &a, const Unit &
                               ? *reinterpret_cast<const uint4 *>(q + tok * a.qs + (h0 + h) * kD + 8 * i)
                               : make_uint4(0, 0, 0, 0);
             if constexpr (kStyle != 0) {
-                const long long at = (long long)min((pg << p.page_log2) + s, a.rows - 1) * 64 + (kStyle == 1 ? 4 * i : 8 * (i & 7));
+                const int row = min((pg << p.page_log2) + s, a.rows - 1);
+                const long long at = (long long)row * 64 + (kStyle == 1 ? 4 * i : 8 * (i & 7));
                 load4(w[c].c, a.cos + at);
                 load4(w[c].s, a.sin + at);
                 if constexpr (kStyle == 2) {

@@ -262,7 +262,8 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
             for (int i = tid; i < kBins; i += N) s_hist[i] = 0;
             __syncthreads();
             auto count = [&](int j, uint32_t k) {
-                if (j >= c0 && j < c1 && (known == 32 || k >> known == found >> known)) atomicAdd(&s_hist[k >> shift & (bins - 1)], 1);
+                if (j >= c0 && j < c1 && (known == 32 || k >> known == found >> known))
+                    atomicAdd(&s_hist[k >> shift & (bins - 1)], 1);
             };
 #pragma unroll
             for (int e = 0; e < E; ++e) count(tid * E + e, key[e]);

@@ -54,7 +54,8 @@ constexpr int kRopeDeep = 4;  // rows per half warp in flight
 // measured copy rate; 75,600 of 24 + 24 head-major (1.86 GB) 299 us, 92%. 3, 4,
 // 6, 8 rows per half warp in flight took 519, 476, 525, 497 us for the former;
 // half a warp per token, for tokens side by side, 306 for the latter.
-template <typename T, bool kInter> __global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeArgs a) {
+template <typename T, bool kInter>
+__global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeArgs a) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
     const int pairs = a.r.rot_dim >> 1;
     uint64_t turn[2];

@@ -189,10 +189,14 @@ def test_calls_refuse_bad_tensors(L, kv):
             ("shares memory", lambda: c.evict(w, 2, freed=c.page_table.view(-1)[1:3].view(2, 1))),
             ("shares memory", lambda: c.evict(w, 2, freed_cnt=c.seq_lens)),
             ("shares memory", lambda: c.evict(c.workspace[:48].view(torch.float32).view(2, 2, 3), 2)),
+            ("shares memory", lambda: c.evict(c.workspace[:48].view(torch.float32).view(2, 2, 3), 2, out=out)),
+            ("shares memory", lambda: c.attend(q, page_weight=c.workspace[-48:].view(torch.float32).view(2, 2, 3),
+                                               weight_out=w2)),
             ("gradient", lambda: c.evict(w.clone().requires_grad_(), 2))):
         with pytest.raises(ValueError, match=match):
             call()
-    for call in (lambda: c.append(k, k), lambda: c.select(q, 2), lambda: c.attend(q), lambda: c.attend(q, (idx, cnt), page_weight=w),
+    for call in (lambda: c.append(k, k), lambda: c.select(q, 2), lambda: c.attend(q),
+                 lambda: c.attend(q, (idx, cnt), page_weight=w),
                  lambda: c.attend(q, page_weight=w, weight_out=w2, decay=0.5), lambda: c.read(2), lambda: c.evict(w, 2),
                  lambda: c.evict(w, 5, out=out), lambda: cache(kv_dtype=kv, allocate=False).evict(w, 2)):
         with pytest.raises(ValueError, match="GPU only"):
@@ -220,7 +224,8 @@ def test_workspaces_of_a_size_serve_both(L):
 
 
 def test_reference_scales():
-    for top, want in ((448.0, 1.0), (448.1, 2.0), (1.0, 2.0 ** -8), (1.75, 2.0 ** -8), (1.7500001, 2.0 ** -7), (0.0, 2.0 ** -126),
+    for top, want in ((448.0, 1.0), (448.1, 2.0), (1.0, 2.0 ** -8), (1.75, 2.0 ** -8), (1.7500001, 2.0 ** -7),
+                      (0.0, 2.0 ** -126),
                       (1e-40, 2.0 ** -126), (3.3e38, 2.0 ** 120), (57344.0, 128.0), (65504.0, 256.0)):
         assert ref8.scale_of(top) == want, top
     x = torch.tensor([65504.0, -61440.0, 65520.0, math.inf, math.nan])
