@@ -187,23 +187,24 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
 }
 
 // Places the pages of sequence b and moves rows of it (row -1: the table, 0 .. Hkv - 1: a head's weights), N threads with E
-// neighbouring entries each. One: the CTA has all rows and makes the keys itself, each thread one page; otherwise it has
+// entries each, N apart. One: the CTA has all rows and makes the keys itself, each thread one page; otherwise it has
 // one row, with the keys made before.
 //
 // The last key to stay: 11 bits at a time from the top (2,048 bins: weights share their exponents, and one bin of few
-// takes the additions of a warp one after another), until a bin stays as a whole or its keys are all equal. Then one scan
-// per N E entries places them. An entry moves to a place at or before its own, and a chunk is read before any of it is
+// takes the additions of a warp one after another), until a bin stays as a whole or its keys are all equal. Then the
+// counts of all warps, N E entries at a time, place them. An entry moves to a place at or before its own, and a chunk is read before any of it is
 // written, so a row may be moved in place. What will be moved is loaded first of all.
 //
 // Chains of loads and barriers bound it: 64 sequences of up to 250 pages x 8 heads 6.9 us in one launch (7.9 with the keys
-// before each counted instead of the digits); one of 7,680 pages x 24 heads 15.9, 4 of them the sums. With 8-bit digits and
-// 512 entries placed at a time the latter took 18.9, and 25 where a warp's lanes matched their bins first.
+// before each counted instead of the digits); one of 7,680 pages x 24 heads 13.2, 4 of them the sums. With 8-bit digits and
+// 512 entries placed at a time the latter took 18.9, 25 where a warp's lanes matched their bins first, and 15.9 with a
+// thread's entries side by side, whose stores are not.
 constexpr int kBins = 2048, kRowsAhead = 10;  // rows: 8, 10, 16 took 7.0, 6.9, 7.8 us on the 64 sequences
 template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
     constexpr int W = N / 32, kChunk = N * E, R = kOne ? kRowsAhead : 1;
     static_assert(!kOne || E == 1, "one page per thread");
     __shared__ int s_hist[kBins];
-    __shared__ int s_bin, s_left, s_in, s_warp[W];
+    __shared__ int s_bin, s_left, s_in, s_warp[W], s_cnt[E * W], s_all;
     const Paged &p = a.p;
     const int rows = kOne ? 1 : p.Hkv + 1;  // CTAs per sequence
     const int b = (int)(blockIdx.x / rows), row0 = (int)(blockIdx.x - (unsigned)b * rows) - 1;
@@ -223,7 +224,7 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
 #pragma unroll
     for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[r][e] = row0 + r < row1 && tid * E + e < P ? from(row0 + r)[tid * E + e] : 0;
+        for (int e = 0; e < E; ++e) x[r][e] = row0 + r < row1 && e * N + tid < P ? from(row0 + r)[e * N + tid] : 0;
     const int raw = kOne ? p.lens[b] : a.len[b], len = clampi(raw, 0, p.max_len), n = (len + p.page - 1) >> p.page_log2;
     const int gone = n > a.keep ? n - a.keep : 0;
     const int c0 = a.first, c1 = n - a.last;  // the pages that compete
@@ -238,7 +239,7 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
         key[0] = order_key((float)sum);
     } else if (gone) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) key[e] = tid * E + e >= c0 && tid * E + e < c1 ? key_at(tid * E + e) : 0;
+        for (int e = 0; e < E; ++e) key[e] = e * N + tid >= c0 && e * N + tid < c1 ? key_at(e * N + tid) : 0;
     }
     if (row0 < 0) {
         for (int i = gone + tid; i < a.freed_cap; i += N) a.freed[(long long)b * a.freed_cap + i] = -1;
@@ -266,7 +267,7 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
                     atomicAdd(&s_hist[k >> shift & (bins - 1)], 1);
             };
 #pragma unroll
-            for (int e = 0; e < E; ++e) count(tid * E + e, key[e]);
+            for (int e = 0; e < E; ++e) count(e * N + tid, key[e]);
             if constexpr (!kOne)
                 for (int j = kChunk + tid; j < c1; j += N) count(j, j >= c0 ? key_at(j) : 0);
             __syncthreads();
@@ -310,54 +311,65 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
     }
     int above = 0, equal = 0;  // before this chunk
     for (int j0 = 0; j0 < P; j0 += kChunk) {
-        int place[E], gt = 0, eq = 0;  // ~j of the freed one where it goes
-        bool is_gt[E], is_eq[E];
+        int place[E];  // ~ its number among the freed ones where it goes
+        unsigned gt[E], eq[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int j = j0 + tid * E + e;
+            const int j = j0 + e * N + tid;
             const bool competes = j >= c0 && j < c1;
             const uint32_t k = !competes ? 0 : j0 == 0 ? key[e] : kOne ? 0 : key_at(j);
-            is_gt[e] = j < P && (!competes || k > last_key);
-            is_eq[e] = competes && left > 0 && k == last_key;
-            gt += is_gt[e];
-            eq += is_eq[e];
+            gt[e] = __ballot_sync(0xffffffffu, j < P && (!competes || k > last_key));
+            eq[e] = __ballot_sync(0xffffffffu, competes && left > 0 && k == last_key);
+            if (lane == 0) s_cnt[e * W + wid] = __popc(gt[e]) | __popc(eq[e]) << 16;  // in the order of j; kChunk < 2^15
         }
-        int inc = gt | eq << 16;  // kChunk < 2^15
-        const int mine = inc;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
-        }
-        __syncthreads();  // s_warp was read
-        if (lane == 31) s_warp[wid] = inc;
         __syncthreads();
-        const int of_warp = lane < W ? s_warp[lane] : 0, all = __reduce_add_sync(0xffffffffu, of_warp);
-        inc += __reduce_add_sync(0xffffffffu, lane < wid ? of_warp : 0);
-        int g = above + ((inc - mine) & 0xffff), q = equal + ((inc - mine) >> 16);
+        if (wid == 0) {  // the counts before each
+            constexpr int kPer = (E * W + 31) / 32;
+            int mine[kPer], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                mine[i] = lane * kPer + i < E * W ? s_cnt[lane * kPer + i] : 0;
+                sum += mine[i];
+            }
+            int inc = sum;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, inc, off);
+                if (lane >= off) inc += y;
+            }
+            if (lane == 31) s_all = inc;
+            inc -= sum;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                if (lane * kPer + i < E * W) s_cnt[lane * kPer + i] = inc;
+                inc += mine[i];
+            }
+        }
+        __syncthreads();
+        const unsigned before = (1u << lane) - 1;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int j = j0 + tid * E + e, at = g + min(q, left);
-            place[e] = is_gt[e] || (is_eq[e] && q < left) ? at : ~(j - at);
-            g += is_gt[e];
-            q += is_eq[e];
+            const int j = j0 + e * N + tid, cnt = s_cnt[e * W + wid];
+            const int g = above + (cnt & 0xffff) + __popc(gt[e] & before), q = equal + (cnt >> 16) + __popc(eq[e] & before);
+            const int at = g + min(q, left);
+            place[e] = (gt[e] >> lane & 1) || ((eq[e] >> lane & 1) && q < left) ? at : ~(j - at);
         }
-        above += all & 0xffff;
-        equal += all >> 16;
+        above += s_all & 0xffff;
+        equal += s_all >> 16;
         for (int row = row0; row < row1; row += R) {
             if (j0 > 0 || row > row0) {
 #pragma unroll
                 for (int r = 0; r < R; ++r)
 #pragma unroll
                     for (int e = 0; e < E; ++e)
-                        x[r][e] = row + r < row1 && j0 + tid * E + e < P ? from(row + r)[j0 + tid * E + e] : 0;
+                        x[r][e] = row + r < row1 && j0 + e * N + tid < P ? from(row + r)[j0 + e * N + tid] : 0;
             }
-            __syncthreads();  // the chunk of these rows was read
+            __syncthreads();  // the chunk of these rows was read (and the counts)
 #pragma unroll
             for (int r = 0; r < R; ++r)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    if (row + r >= row1 || j0 + tid * E + e >= P) continue;
+                    if (row + r >= row1 || j0 + e * N + tid >= P) continue;
                     if (place[e] >= 0)
                         to(row + r)[place[e]] = x[r][e];
                     else if (row + r < 0)
