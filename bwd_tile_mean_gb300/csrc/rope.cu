@@ -51,11 +51,13 @@ constexpr int kRopeDeep = 4;  // rows per half warp in flight
 // dims per lane. Lane l computes the angles of pairs 2 l and 2 l + 1, once for
 // all heads of the unit, and every lane gathers those of its own dims. Bound by
 // HBM: 76,800 tokens of 40 + 40 heads (3.15 GB) 476 us = 6.6 TB/s, 97% of the
-// measured copy rate; 75,600 of 24 + 24 head-major (1.86 GB) 299 us, 92%. 3, 4,
+// measured copy rate; 75,600 of 24 + 24 head-major (1.86 GB) 286 us, 96%. 3, 4,
 // 6, 8 rows per half warp in flight took 519, 476, 525, 497 us for the former;
-// half a warp per token, for tokens side by side, 306 for the latter.
-template <typename T, bool kInter>
-__global__ void __launch_bounds__(kRopeWarps * 32) k_rope(const __grid_constant__ RopeArgs a) {
+// half a warp per token, for tokens side by side, 306 for the latter (299 then).
+// kPerSm: CTAs per SM. Tokens whose heads lie side by side go best with three
+// (476 us, with four 499), heads whose tokens do with four (286, with three 298).
+template <typename T, bool kInter, int kPerSm>
+__global__ void __launch_bounds__(kRopeWarps * 32, kPerSm) k_rope(const __grid_constant__ RopeArgs a) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
     const int pairs = a.r.rot_dim >> 1;
     uint64_t turn[2];
@@ -272,13 +274,17 @@ extern "C" vsa_status vsa_rope_apply(const vsa_rope *rope, int dtype, int B, int
     a.chunk = (a.chunk + 1) & ~1;
     a.chunks = (int)((heads + a.chunk - 1) / a.chunk);
     a.units = tokens * a.chunks;
-    // three CTAs fit on an SM: 3, 4, 5, 6, 8, 32 per SM took 475, 548, 498, 476, 486, 487 us
-    const unsigned grid = (unsigned)std::min((a.units + kRopeWarps - 1) / kRopeWarps, 152LL * 6);
+    // twice the CTAs that fit: with three of them 3, 4, 5, 6, 8, 32 per SM took 475, 548, 498, 476, 486, 487 us
+    const bool head_major = S > 1 && t[0].x_token < t[0].x_head;
+    const unsigned grid = (unsigned)std::min((a.units + kRopeWarps - 1) / kRopeWarps, head_major ? 152LL * 8 : 152LL * 6);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("rope", s);
     const bool bf = dtype == VSA_DTYPE_BF16;
-    const auto kernel = a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true> : k_rope<__half, true>)
-                                        : (bf ? k_rope<__nv_bfloat16, false> : k_rope<__half, false>);
+    const auto kernel =
+        head_major ? (a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true, 4> : k_rope<__half, true, 4>)
+                                      : (bf ? k_rope<__nv_bfloat16, false, 4> : k_rope<__half, false, 4>))
+                   : (a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true, 3> : k_rope<__half, true, 3>)
+                                      : (bf ? k_rope<__nv_bfloat16, false, 3> : k_rope<__half, false, 3>));
     const cudaError_t e = launch_paged(kernel, dim3(grid), kRopeWarps * 32, 0, 1, a, s);
     prof_end(s);
     return status_from_cuda(e);
