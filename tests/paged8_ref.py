@@ -205,7 +205,10 @@ def attend(pool, q, pages=None, scale=None, weight=None, decay=1.0):
                 one.index_add_(1, torch.tensor(at), p)
                 off = 3 * ds + 2.0 ** -22 * (s.abs().amax(1) + lse[b, rows].abs()) + (16 + n / 16 + G) * 2.0 ** -23
                 mass[b, h] += one.sum(0)
-                wtol[b, h] += (one * off[:, None]).sum(0) * 1.01 + mass[b, h].abs() * 2.0 ** -23 + G * 2.0 ** -100
+                # and each time a page is listed its sum is added to its weight, rounding that by half a step
+                times = torch.bincount(torch.tensor([j for j in listed if 0 <= j < pool.max_pages]), minlength=pool.max_pages)
+                wtol[b, h] += (one * off[:, None]).sum(0) * 1.01 + G * 2.0 ** -100
+                wtol[b, h] += mass[b, h].abs() * (2.0 ** -23 + times * 2.0 ** -24)
     if mass is None:
         return out, lse, tol, ltol
     return out, lse, tol, ltol, mass, wtol
