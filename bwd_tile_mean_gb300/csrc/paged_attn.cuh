@@ -697,14 +697,17 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
                     for (int e = 0; e < 4; ++e)
                         if (g + 8 * (e >> 1) >= live[h]) sc[h][n][e] = -INFINITY;
         }
-        // vrun: the power of two at or below the largest scale so far; a block's ratio to it is below 2
-        float ratio[2], vcorr = 1.f;
+        // vrun: the power of two at or below the largest scale so far, 2^126 at most; a block's ratio to it is below 2 (of
+        // larger scales 4, and 2^14 times that is still in fp16)
+        float ratio[2], vcorr;
         {
-            const float top = fmaxf(vsc[0], vsc[1]);
+            const float top = fminf(fmaxf(vsc[0], vsc[1]), 0x1p126f);
             const float to = fmaxf(vrun, __uint_as_float(__float_as_uint(top) & 0x7f800000u));
-            if (to != vrun) vcorr = vrun / to, vrun = to;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) ratio[h] = vsc[h] == vrun ? 1.f : vsc[h] / vrun;
+            const float inv = __uint_as_float(0x7f000000u - __float_as_uint(to));  // of a power of two
+            vcorr = vrun * inv;
+            vrun = to;
+            ratio[0] = vsc[0] * inv;
+            ratio[1] = vsc[1] * inv;
         }
         float corr[2 * NT];
         bool moved = vcorr != 1.f;
@@ -764,7 +767,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (ratio[h] != 1.f) {  // the same for the whole warp; in two factors that fp16 holds in full
-                const float hi = fmaxf(ratio[h], 0x1p-14f), lo = ratio[h] / hi;
+                const float hi = fmaxf(ratio[h], 0x1p-14f), lo = ratio[h] < 0x1p-14f ? ratio[h] * 0x1p14f : 1.f;
                 const __half2 r1 = __float2half2_rn(hi), r2 = __float2half2_rn(lo);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
