@@ -439,12 +439,14 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 // accumulators: 34 products, 128 conversions and 8 exponentials per thread and
 // step of 32 keys. 24 heads of 122,880 keys (756 MB): 118 us, 94% of the measured
 // copy rate (heads as rows, as in the 16-bit walk, 172 us); 64 sequences of 37 to
-// 16,000 keys x 8 heads (385 MB) 74 us, 77%: the CTAs' start, a segment's first
-// loads and the join are 10 of the rest. A warp alone takes about 1,650 cycles per
-// step, the conversions (a quarter of its 600 instructions) and products one after
-// another, so a few long rows gain nothing over 16 bits (one head of 30,000 keys
-// 10.4 us; 16 heads on each of 2, 16 sequences of up to 9,000 keys 17.0, 14.6 in 16 bits,
-// NT = 2). Two accumulators per product left all of these as they are.
+// 16,000 keys x 8 heads (385 MB) 73 us, 77%: the CTAs' start, a segment's first
+// loads and the join are 10 of the rest. A warp alone takes about 1,480 cycles and 600
+// instructions per step, one chain from the copies' wait to the products: left out
+// one at a time, the copies are 18% of it, products, conversions, permutations and
+// shuffles under 5% each (two fp32 divisions were 10%), so a few long rows gain little
+// over 16 bits (one head of 30,000 keys 10.1 us; 16 heads on each of 2, 16 sequences
+// of up to 9,000 keys 16.1, 14.5 in 16 bits, NT = 2). Two accumulators per product
+// left all of these as they are, a third step in the ring made them 2 to 6% slower.
 //   S^T (keys x heads) = K (16 keys x 16 dims) Q^T, O^T (dims x heads) = V^T (16 dims x 16 keys) P^T
 // A row of 128 bytes is 8 chunks of 16, stored at chunk ^ (row % 8). Thread (g, t)
 // reads bytes 32 t .. 32 t + 31 of keys g and g + 8 of a block and takes word j for
