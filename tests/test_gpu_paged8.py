@@ -307,6 +307,10 @@ def test_attend_with_scales_far_apart():
     ref.check_attend(pool.cache().attend(q.cuda()), ref8.attend(pool, q))
     pool.ks[:] = torch.exp2(torch.randint(-9, -4, pool.ks.shape).float())
     ref.check_attend(pool.cache().attend(q.cuda()), ref8.attend(pool, q))
+    pool.v[:] = (pool.v / 448).to(E4M3).float()  # the largest scales there are, and none
+    pool.vs[:] = torch.exp2(torch.randint(118, 128, pool.vs.shape).float())
+    pool.vs[pool.table[0][2]] = 0.0
+    ref.check_attend(pool.cache().attend(q.cuda()), ref8.attend(pool, q))
 
 
 @pytest.mark.parametrize("dtype,value", [(BF, 1.0), (HF, 61440.0), (HF, 60.0), (BF, 3.0e38)])
