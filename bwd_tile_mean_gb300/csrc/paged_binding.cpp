@@ -18,7 +18,9 @@
 
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -109,9 +111,15 @@ int64_t row_stride(const Calls &c, const char *name, const at::Tensor &t, int64_
     if (t.stride(0) < heads * c.d.D) refuse(name, ": tokens must not share memory");  // 0 means dense further on
     return t.stride(0);
 }
-at::Tensor output(const Calls &c, at::IntArrayRef shape, at::ScalarType dtype) {
-    const at::Device device = c.device < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c.device);
+// A dense tensor, uninitialised: straight from the GPU's allocator where at::empty would come to that (two of them cost a
+// call 3.4 us through the dispatcher, more than its launch).
+at::Tensor dense(at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
+    if (device.is_cuda() && !c10::InferenceMode::is_enabled())
+        return at::Tensor(at::detail::empty_cuda(shape, dtype, device, std::nullopt));
     return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+}
+at::Tensor output(const Calls &c, at::IntArrayRef shape, at::ScalarType dtype) {
+    return dense(shape, dtype, c.device < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c.device));
 }
 PyObject *pair(at::Tensor a, at::Tensor b) {
     PyObject *t = PyTuple_New(2);
@@ -637,7 +645,7 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                     refuse(name, ": expected ", in[i]->sizes(), ", got ", given[i]->sizes());
                 out[i] = *given[i];
             } else {
-                out[i] = at::empty(in[i]->sizes(), in[i]->options().memory_format(c10::nullopt));
+                out[i] = dense(in[i]->sizes(), dtype, q.device());
             }
             y[i] = tokens(name, out[i], layout);
             if (!given[i]) continue;
@@ -686,7 +694,7 @@ PyObject *rope_table(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                     refuse(name, ": expected a contiguous [", T, ", ", pairs, "], got ", given[i]->sizes());
                 out[i] = *given[i];
             } else {
-                out[i] = at::empty({T, pairs}, pos.options().dtype(at::kFloat));
+                out[i] = dense({T, pairs}, at::kFloat, pos.device());
             }
         }
         const Tokens m = as_tokens(pos, "positions");
