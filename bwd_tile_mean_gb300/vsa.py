@@ -919,7 +919,9 @@ class PagedCache:
         last keep_last. The table, the lengths and page_weight change in place, or
         are left and written to out = (page_table, seq_lens, page_weight).
         Returns (freed int32 [B, max(1, max_pages - keep)], freed_cnt int32 [B]):
-        the pages that went."""
+        the pages that went. Layers that share a table evict once, by one
+        page_weight that each layer's attend was given (decay in the first one's
+        alone). Later appends give positions: lengths no longer are."""
         if stream is not None:
             with self._on(stream):
                 return self._calls.evict(page_weight, keep, keep_first, keep_last, freed, freed_cnt, out)
