@@ -427,11 +427,20 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 // brings its largest entry into [2^14, 2^15) (bf16's 8 significant bits fit fp16's
 // 11 down to 2^-29 of that entry, below that to 2^-40 of it), and the products run
 // on the fp16 instructions for both types. The k scales multiply the scores. The
-// v scales multiply the weights: acc is kept relative to the largest power of two
-// met (vrun), and a block's weights are multiplied by its scale over that, exact
-// for powers of two until a weight falls below 2^-24 (2^-38 of the largest
-// weight's at the largest scale's). The sum W of the rounded weights is taken
-// before, so that the weights that O is made with sum to one as above.
+// v scales multiply the weights: acc is kept relative to a power of two, and a
+// block's weights are multiplied by its scale over that, exact as long as the
+// product is a normal fp16 number, 2^-14 and more. The sum W of the rounded weights is
+// taken before, so that the weights that O is made with sum to one as above.
+// While all v scales of a warp's blocks lie within kSpan of each other the power of two is the
+// largest one met (vrun), for all rows: the key of the largest weight, 2^14 by
+// the lift, then has a product of 2^8 or more, and what the roundings of products
+// below 2^-14 leave is 2^-33 of that per key. Scales further apart (`far`, looked at
+// for 32 blocks at a time) would take that room away: a block of the largest
+// scale that is hardly attended left the other weights a few bits or none. From there
+// on each row has a power of two of its own, by its largest product of weight
+// and scale: two more maxima per row and step, and the weights multiplied in
+// fp32, in a loop apart, so that the common one has no branch for it (scales 2^20 apart:
+// the batch below 74.3 us, the long context 118.9, 16 heads on each of 2, 16 sequences 18.1).
 //
 // At half the bytes per key the instructions count: keys and dims are the rows
 // of the products here, the query heads their columns, NT tiles of 8. Up to 8
@@ -537,6 +546,16 @@ __device__ __forceinline__ void store_weights8(const AttnArgs &a, const Segment 
     }
 }
 
+// A score tile's weights in fp16, turned into the B operands of the products with V.
+__device__ __forceinline__ void turn_weights(const float (&sc)[4], uint32_t (&pb)[2]) {
+    pb[0] = turn8x8(pack2<__half>(sc[0], sc[1]));
+    pb[1] = turn8x8(pack2<__half>(sc[2], sc[3]));
+}
+// Largest over smallest v scale up to which a warp's outputs are relative to one power of two for all rows (stream_blocks8).
+constexpr float kSpan = 64.f;
+// e of a positive x in [2^e, 2^(e + 1)), -126 at least.
+__device__ __forceinline__ int exponent_of(float x) { return max((int)(__float_as_uint(x) >> 23), 1) - 127; }
+
 // stream_blocks for 8 bits: m_run, l_run, w_run of heads 8 n + 2 t + e at 2 n + e, their outputs' dims 16 j + 2 g and + 1 in
 // acc[8 n + j][e] and [2 + e], finished: divided by w, and scaled.
 template <int NT, bool kWeigh>
@@ -594,8 +613,21 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
             at[h] = (long long)max(id, 0) * p.page_stride + slot * p.tok_stride + lane_at;
         }
     };
+    // The outputs are relative to vrun, the largest power of two met and 2^126 at most (vnext: with the window's scales); once
+    // far, each row's to 2^at_exp, of which every lane keeps a copy for its rows.
+    __shared__ int s_exp[kWarps][2 * NT][32];
+    int(&at_exp)[2 * NT][32] = s_exp[threadIdx.x >> 5];
+    float vrun = 0x1p-126f, vnext = vrun, vlow = INFINITY;
+    bool far = false;
     float ksc[2], vsc[2];
     auto scales = [&](int step) {  // of the step located last
+        if (2 * step == w_base) {  // a window's first: all of its scales; those of 0 (no tokens) do not count
+            const uint32_t u = __float_as_uint(w_vs) & 0x7fffffffu;
+            const uint32_t top = min(__reduce_max_sync(0xffffffffu, u), 0x7e800000u);  // 2^126
+            vlow = fminf(vlow, __uint_as_float(__reduce_min_sync(0xffffffffu, u ? u : 0x7f800000u)));
+            vnext = fmaxf(vrun, __uint_as_float(top & 0x7f800000u));
+            far = far || vnext > kSpan * vlow;
+        }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int from = 2 * step + h - w_base;
@@ -631,7 +663,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         scales(0);
     }
 
-    float wsum[NT][4], vrun = 0x1p-126f;
+    float wsum[NT][4];
 #pragma unroll
     for (int e = 0; e < 2 * NT; ++e) m_run[e] = -INFINITY, l_run[e] = 0.f;
 #pragma unroll
@@ -642,7 +674,8 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
     for (int j = 0; j < 8 * NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    for (int i = 0; i < steps; ++i) {
+    auto step = [&](auto is_far, int i) {
+        constexpr bool kFar = decltype(is_far)::value;
         const int live[2] = {ok[0], ok[1]};
         cp_wait<1>();
         __syncwarp();  // every lane's K copies have landed, and V of the step before was read
@@ -699,15 +732,12 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
                     for (int e = 0; e < 4; ++e)
                         if (g + 8 * (e >> 1) >= live[h]) sc[h][n][e] = -INFINITY;
         }
-        // vrun: the power of two at or below the largest scale so far, 2^126 at most; a block's ratio to it is below 2 (of
-        // larger scales 4, and 2^14 times that is still in fp16)
-        float ratio[2], vcorr;
-        {
-            const float top = fminf(fmaxf(vsc[0], vsc[1]), 0x1p126f);
-            const float to = fmaxf(vrun, __uint_as_float(__float_as_uint(top) & 0x7f800000u));
-            const float inv = __uint_as_float(0x7f000000u - __float_as_uint(to));  // of a power of two
+        // A block's ratio to vrun is below 2 (of larger scales than 2^126 4, and 2^14 times that is still in fp16).
+        float ratio[2] = {1.f, 1.f}, vcorr = 1.f;
+        if constexpr (!kFar) {
+            const float inv = __uint_as_float(0x7f000000u - __float_as_uint(vnext));  // of a power of two
             vcorr = vrun * inv;
-            vrun = to;
+            vrun = vnext;
             ratio[0] = vsc[0] * inv;
             ratio[1] = vsc[1] * inv;
         }
@@ -743,7 +773,57 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
             for (int r = 0; r < 2 * NT; ++r) ref[r] = m_run[r] * sl2[r];
             store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, ref);
         }
-        if (__any_sync(0xffffffffu, moved)) {
+        if constexpr (kFar) {
+            // The sum of the weights as below; then the weights for the outputs: a row's largest product of weight and scale
+            // so far comes to [2^12, 2^14) (a scale of 2^127: a binade more), and the outputs with it
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                wsum[n][0] *= corr[2 * n], wsum[n][1] *= corr[2 * n + 1];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[2];
+                    turn_weights(sc[h][n], w);
+                    mma16816<__half>(wsum[n], kOnes, w[0], w[1]);
+                }
+            }
+            int lv[2];
+            float part[2];  // a scale is part 2^lv
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                lv[h] = min(exponent_of(vsc[h]), 126);
+                part[h] = vsc[h] * power_of(-lv[h]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2 * NT; ++r) {
+                constexpr int kNone = -1000;
+                const int n = r >> 1, e = r & 1, was = at_exp[r][lane];
+                int to = corr[r] > 0.f ? was + exponent_of(corr[r]) : kNone;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float top = fmaxf(sc[h][n][e], sc[h][n][2 + e]);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                    if (top > 0.f && vsc[h] > 0.f) to = max(to, exponent_of(top) + lv[h] - 12);
+                }
+                to = to == kNone ? was : clampi(to, -300, 300);
+                at_exp[r][lane] = to;
+                const float by = corr[r] * power_of(clampi(was - to, -126, 127));
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    acc[8 * n + j][e] *= by;
+                    acc[8 * n + j][2 + e] *= by;
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    // in two factors: a small weight's may be 2^138
+                    const int up = clampi(lv[h] - to, -252, 252), one = up >> 1;
+                    const float f1 = power_of(one), f2 = power_of(up - one) * part[h];
+                    sc[h][n][e] = sc[h][n][e] * f1 * f2;
+                    sc[h][n][2 + e] = sc[h][n][2 + e] * f1 * f2;
+                }
+            }
+        } else if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 wsum[n][0] *= corr[2 * n], wsum[n][1] *= corr[2 * n + 1];
@@ -762,23 +842,19 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                pb[h][n][0] = turn8x8(pack2<__half>(sc[h][n][0], sc[h][n][1]));
-                pb[h][n][1] = turn8x8(pack2<__half>(sc[h][n][2], sc[h][n][3]));
-                mma16816<__half>(wsum[n], kOnes, pb[h][n][0], pb[h][n][1]);
+                turn_weights(sc[h][n], pb[h][n]);
+                if constexpr (!kFar) mma16816<__half>(wsum[n], kOnes, pb[h][n][0], pb[h][n][1]);
             }
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            if (ratio[h] != 1.f) {  // the same for the whole warp; in two factors that fp16 holds in full
-                const float hi = fmaxf(ratio[h], 0x1p-14f), lo = ratio[h] < 0x1p-14f ? ratio[h] * 0x1p14f : 1.f;
-                const __half2 r1 = __float2half2_rn(hi), r2 = __float2half2_rn(lo);
+            if (!kFar && ratio[h] != 1.f) {  // the same for the whole warp
+                const __half2 by = __float2half2_rn(ratio[h]);
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        __half2 x = *reinterpret_cast<__half2 *>(&pb[h][n][u]);
-                        x = __hmul2(x, r1);
-                        if (lo != 1.f) x = __hmul2(x, r2);
-                        pb[h][n][u] = *reinterpret_cast<uint32_t *>(&x);
+                        const __half2 x = __hmul2(*reinterpret_cast<__half2 *>(&pb[h][n][u]), by);
+                        pb[h][n][u] = *reinterpret_cast<const uint32_t *>(&x);
                     }
             }
 #pragma unroll
@@ -796,6 +872,26 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         free_slot = v_slot;
         v_slot = was_k;
         if (i + 1 < steps) scales(i + 1);
+    };
+    int i = 0;
+    for (; i < steps && !far; ++i) step(std::false_type{}, i);
+    if (far) {
+#pragma unroll
+        for (int r = 0; r < 2 * NT; ++r) at_exp[r][lane] = exponent_of(vrun);
+        for (; i < steps; ++i) step(std::true_type{}, i);
+#pragma unroll
+        for (int r = 0; r < 2 * NT; ++r) {  // finished here: over w, times 2^e in three factors, -300 <= e <= 300
+            const float w = wsum[r >> 1][r & 1], inv = w == 0.f ? 0.f : 1.f / w;
+            const int e = at_exp[r][lane], e1 = e / 3, e2 = (e - e1) / 2;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float &x = acc[8 * (r >> 1) + j][2 * c + (r & 1)];
+                    x = x * inv * power_of(e1) * power_of(e2) * power_of(e - e1 - e2);
+                }
+        }
+        vrun = 1.f;
     }
     cp_wait<0>();
     __syncwarp();  // the warp's ring is free
@@ -806,7 +902,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         l_run[r] *= kDrop;
         m_run[r] *= sl2[r];  // log2 units from here on
         w_run[r] = wsum[r >> 1][r & 1];
-        const float inv = w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
+        const float inv = far ? 1.f : w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
@@ -1005,7 +1101,9 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
 // (504 MB): 82 to 84 us with the join, 88 to 90% of the measured copy rate (99% at
 // four times the bytes); of the rest 3.5 us are the start of a CTA (scan, length,
 // page id, first keys) and 4 the join.
-template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32) k_paged_attn_runs(AttnArgs a) {
+// Two CTAs per SM, as many as the grid has: unasked, the compiler took 168 registers and spills for three in the 8-bit walk (24
+// heads of 122,880 keys 118 -> 127 us).
+template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWarps * 32, 2) k_paged_attn_runs(AttnArgs a) {
     constexpr int KV = Frag<NT>::kv, kFront = KV == 8 ? kLead8 : kLead;
     extern __shared__ __align__(128) unsigned char smem[];
     const Paged &p = a.p;

@@ -616,8 +616,10 @@ vsa_status vsa_paged8_append(const vsa_paged_desc *desc, int T, const void *k, i
 /* vsa_paged_attn over an 8-bit cache: the same arguments, results and errors,
  * and the scales. The products run in fp16 with fp32 sums: q is brought there by
  * a power of two per row (bf16 entries keep their 8 bits down to 2^-29 of the
- * row's largest), e4m3 exactly, the weights are rounded to fp16. A value
- * counts down to 2^-38 of the largest (scale of the cache times weight). */
+ * row's largest), e4m3 exactly, the weights are rounded to fp16's 11 bits. A
+ * weight's product with its value's scale keeps them down to 2^-22 of the largest
+ * such product of its row and counts for nothing below 2^-33 of it; a weight
+ * below 2^-126 of its row's largest counts for nothing. */
 vsa_status vsa_paged8_attn(const vsa_paged_desc *desc, const void *q, int64_t q_stride, const void *k_cache,
                            const void *v_cache, const float *k_scale, const float *v_scale, const int32_t *page_idx,
                            const int32_t *page_cnt, int idx_cap, void *out, float *lse, void *workspace,

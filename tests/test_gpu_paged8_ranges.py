@@ -1,0 +1,122 @@
+"""The paged attention where numbers lie far apart: v scales of an 8-bit cache."""
+import pytest
+import torch
+
+from bwd_tile_mean_gb300 import vsa
+from tests import paged8_ref as ref8
+from tests.paged8_ref import D, E4M3, Pool8
+from tests.paged_ref import U
+from tests.test_gpu_paged import BF, HF
+from tests.test_gpu_paged8 import queries
+
+pytestmark = pytest.mark.gpu
+
+
+def share_pages(pool, B):
+    """The pool's one sequence, B times over the same pages."""
+    pool.table, pool.lens, pool.B = pool.table * B, pool.lens * B, B
+    return pool
+
+
+# ------------------------------------------------- v scales of 8 bits, far apart
+
+def tail(Hq, Hkv, dtype, apart, B, n=9001):
+    """Values of 1. Every 24 blocks: a strong key (score 0), then a block with
+    scores of -60, a v scale 2^apart times the others' and dim 0 full, then
+    a tail of equal keys (-7: together a third of the strong one)."""
+    pool = Pool8("bshd", dtype, Hq, Hkv, 64, -(-n // 64) + 1, -(-n // 64), [n], seed=1)
+    pool.k[:], pool.ks[:] = 0.0, 1.0
+    pool.k[..., 0] = -7.0
+    pool.v[:], pool.vs[:] = 64.0, 2.0 ** -6
+    for blk in range(1, n // 16, 24):
+        pool.k[pool.table[0][(blk - 1) // 4], 16 * ((blk - 1) % 4) + 5, :, 0] = 0.0
+        p, i = pool.table[0][blk // 4], blk % 4
+        at = slice(16 * i, 16 * i + 16)
+        pool.k[p, at, :, 0] = -60.0
+        pool.v[p, at] = 0.0
+        pool.v[p, at, :, 0] = 448.0
+        pool.vs[p, :, i] = 2.0 ** (apart - 6)
+    q = torch.zeros(B, Hq, D, dtype=dtype)
+    q[..., 0] = 1.0
+    return share_pages(pool, B), q
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 4), (24, 2)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("apart", [0, 6, 7, 16, 22, 25, 27, 29, 60])
+def test_a_block_of_no_weight_takes_nothing_from_the_others(Hq, Hkv, dtype, apart):
+    """A constant comes back as it is however large the scale of a block that
+    is hardly attended: all weights together are 1 (they round alike: fp32
+    sums, 2^-18, and e^-60 of the large block are what is left)."""
+    pool, q = tail(Hq, Hkv, dtype, apart, 24)
+    for wide in (0, 3000):
+        table = torch.nn.functional.pad(torch.tensor(pool.table, dtype=torch.int32), (0, wide), value=-1).cuda()
+        cache = pool.cache(scale=1.0) if not wide else vsa.PagedCache(
+            pool.layout, dtype, pool.B, Hq, Hkv, D, 64, pool.num_pages, pool.max_pages + wide, k=pool.view(pool.k).cuda(),
+            v=pool.view(pool.v).cuda(), k_scale=pool.ks.cuda(), v_scale=pool.vs.cuda(), page_table=table,
+            seq_lens=torch.tensor(pool.lens, dtype=torch.int32).cuda(), kv_dtype=E4M3, scale=1.0)
+        out = cache.attend(q.cuda())[0].double().cpu()
+        assert ((out[..., 1:] - 1).abs() <= U[dtype] + 2.0 ** -18).all(), float((out[..., 1:] - 1).abs().max())
+
+
+def by_products(pool, q, scale=None):
+    """(out, bound) in fp64, the bound on what is lost in weights' products
+    with the v scales relative to the largest product of a row: weights round
+    to 11 bits, and where the product lies below 2^-20 of the largest to 2^-32 of
+    that (2^-33 by rounding to nearest)."""
+    want = ref8.attend(pool, q, scale=scale)
+    out, tol = want[0], torch.zeros_like(want[0])
+    scale, G = scale or D ** -0.5, pool.Hq // pool.Hkv
+    for b in range(pool.B):
+        for h in range(pool.Hkv):
+            pages = [pool.table[b][j] for j in range(-(-pool.lens[b] // pool.page))]
+            of = torch.cat([pool.vs[p, h].repeat_interleave(16) for p in pages])[: pool.lens[b]].double()
+            k, v, _, _ = ref8.rows_of(pool, b, h, range(len(pages)))
+            rows = slice(h * G, (h + 1) * G)
+            qq = q[b, rows].double()
+            s = qq @ k.T * scale
+            p = torch.softmax(s, 1)
+            mags = qq.abs() @ k.abs().T + 2.0 ** -15 * qq.abs().amax(1, keepdim=True) * k.abs().sum(1)[None]
+            ds = 132 * 2.0 ** -24 * scale * mags.amax(1) + 2.0 ** -22 * s.abs().amax(1)
+            n = k.shape[0]
+            rel = 2.0 ** -11 + 2 * ds + (8 + n / 16) * 2.0 ** -23
+            tol[b, rows] = U[pool.dtype] * out[b, rows].abs() + rel[:, None] * (p @ v.abs()) * 1.01
+            top = (p * of[None]).amax(1)
+            units = (v / torch.where(of > 0, of, 1.0)[:, None]).abs().sum(0)  # e4m3 values
+            tol[b, rows] += 2.0 ** -33 * top[:, None] * units[None]
+    return out, tol
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (32, 2)])
+@pytest.mark.parametrize("size", [0.5, 4.0, 12.0])
+@pytest.mark.parametrize("lens", [[160], [5000, 77, 3000]])
+def test_attend_by_products(Hq, Hkv, size, lens):
+    """Scales up to 2^60 apart with weights as far apart, so that products of
+    the two decide."""
+    need = sum(-(-n // 16) for n in lens)
+    pool = Pool8("bhsd", BF, Hq, Hkv, 16, need + 1, -(-max(lens) // 16), lens, seed=3)
+    g = torch.Generator().manual_seed(4)
+    q = queries(pool, size=size)
+    for lo, hi in ((-30, 31), (-4, 5), (60, 120), (-120, -60)):
+        pool.vs[:] = torch.exp2(torch.randint(lo, hi, pool.vs.shape, generator=g).float())
+        out, tol = by_products(pool, q)
+        got = pool.cache().attend(q.cuda())[0].double().cpu()
+        assert torch.isfinite(got).all()
+        assert ((got - out).abs() <= tol).all(), (lo, float(((got - out).abs() / tol).max()))
+
+
+def test_weights_tiny_and_scales_huge():
+    """Weights of 2^-100 of the largest whose values' scale is 2^110 times the
+    others': their products are what the output is made of."""
+    pool = Pool8("bshd", BF, 8, 1, 16, 40, 40, [640], seed=5)
+    pool.k[:], pool.ks[:] = 0.0, 1.0
+    pool.k[..., 0] = -72.0                      # 2^-103.9
+    pool.k[pool.table[0][7], 3, 0, 0] = 0.0
+    pool.v[:] = (pool.v / 4).to(E4M3).float()
+    pool.vs[:] = 2.0 ** 110
+    pool.vs[pool.table[0][7]] = 1.0
+    q = torch.zeros(1, 8, D, dtype=BF)
+    q[..., 0] = 1.0
+    out, tol = by_products(pool, q, scale=1.0)
+    got = pool.cache(scale=1.0).attend(q.cuda())[0].double().cpu()
+    assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
