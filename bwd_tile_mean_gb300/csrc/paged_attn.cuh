@@ -48,7 +48,6 @@
 #pragma once
 
 #include <algorithm>
-#include <cfloat>
 #include <type_traits>
 
 #include "e4m3.cuh"
@@ -426,7 +425,10 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 // exponents from -9 to 8), q becomes fp16 beside a power of two per row that
 // brings its largest entry into [2^14, 2^15) (bf16's 8 significant bits fit fp16's
 // 11 down to 2^-29 of that entry, below that to 2^-40 of it), and the products run
-// on the fp16 instructions for both types. The k scales multiply the scores. The
+// on the fp16 instructions for both types. Their sums times the k scale and the row's
+// power of two are the scores, q.k in fp32 as in the 16-bit walk (the power taken into the
+// softmax scale instead, keys near 2^110 overflowed with queries as small, and rows near
+// 2^-100 under a small softmax scale became NaN). The
 // v scales multiply the weights: acc is kept relative to a power of two, and a
 // block's weights are multiplied by its scale over that, exact as long as the
 // product is a normal fp16 number, 2^-14 and more. The sum W of the rounded weights is
@@ -553,6 +555,12 @@ __device__ __forceinline__ void turn_weights(const float (&sc)[4], uint32_t (&pb
 }
 // Largest over smallest v scale up to which a warp's outputs are relative to one power of two for all rows (stream_blocks8).
 constexpr float kSpan = 64.f;
+// The smaller one, NaN if either is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+    return r;
+}
 // e of a positive x in [2^e, 2^(e + 1)), -126 at least.
 __device__ __forceinline__ int exponent_of(float x) { return max((int)(__float_as_uint(x) >> 23), 1) - 127; }
 
@@ -566,10 +574,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, b = sg.b, bh = sg.bh;
     const unsigned char *K = static_cast<const unsigned char *>(a.k), *V = static_cast<const unsigned char *>(a.v);
-    // q of 2^14 and more with the largest softmax scales: still a finite multiple of differences that may be 0
-    float sl2[2 * NT];
-#pragma unroll
-    for (int e = 0; e < 2 * NT; ++e) sl2[e] = fminf(p.scale * kLog2e * qs[e], FLT_MAX);
+    const float sl2 = p.scale * kLog2e;
     constexpr float kLift = 14.f, kDrop = 0x1p-14f;
     constexpr int kStage8 = stage_bytes<8>;
     constexpr uint32_t kOnes[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
@@ -722,7 +727,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sc[h][n][e] *= ksc[h];
+                for (int e = 0; e < 4; ++e) sc[h][n][e] *= min_nan(ksc[h] * qs[2 * n + (e & 1)], 0x1p127f);
         if (live[0] + live[1] < 2 * kBlk) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -754,14 +759,14 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
                 mx = ptx::fmax3(m_run[r], mx, __shfl_xor_sync(0xffffffffu, mx, 16));
                 moved = moved || mx != m_run[r];
                 const float ref = mx == -INFINITY ? 0.f : mx;  // a row without keys so far
-                corr[r] = ptx::ex2((m_run[r] - ref) * sl2[r]);
+                corr[r] = ptx::ex2((m_run[r] - ref) * sl2);
                 m_run[r] = mx;
                 float sum = 0.f;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const float pr = ptx::ex2(fmaf(sc[h][n][2 * c + e] - ref, sl2[r], kLift));
+                        const float pr = ptx::ex2(fmaf(sc[h][n][2 * c + e] - ref, sl2, kLift));
                         sc[h][n][2 * c + e] = pr;
                         sum += pr;
                     }
@@ -770,7 +775,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         if constexpr (kWeigh) {
             float ref[2 * NT];
 #pragma unroll
-            for (int r = 0; r < 2 * NT; ++r) ref[r] = m_run[r] * sl2[r];
+            for (int r = 0; r < 2 * NT; ++r) ref[r] = m_run[r] * sl2;
             store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, ref);
         }
         if constexpr (kFar) {
@@ -900,7 +905,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], off);
         l_run[r] *= kDrop;
-        m_run[r] *= sl2[r];  // log2 units from here on
+        m_run[r] *= sl2;  // log2 units from here on
         w_run[r] = wsum[r >> 1][r & 1];
         const float inv = far ? 1.f : w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
 #pragma unroll

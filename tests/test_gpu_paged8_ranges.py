@@ -1,13 +1,15 @@
-"""The paged attention where numbers lie far apart: v scales of an 8-bit cache."""
+"""The paged attention where numbers lie far apart: v scales of an 8-bit cache,
+queries and keys near the ends of bf16's range."""
 import pytest
 import torch
 
 from bwd_tile_mean_gb300 import vsa
 from tests import paged8_ref as ref8
+from tests import paged_ref as ref
 from tests.paged8_ref import D, E4M3, Pool8
 from tests.paged_ref import U
 from tests.test_gpu_paged import BF, HF
-from tests.test_gpu_paged8 import queries
+from tests.test_gpu_paged8 import pool_of, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -120,3 +122,35 @@ def test_weights_tiny_and_scales_huge():
     out, tol = by_products(pool, q, scale=1.0)
     got = pool.cache(scale=1.0).attend(q.cuda())[0].double().cpu()
     assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
+
+
+# --------------------------------------------- queries and keys near bf16's ends
+
+def scaled(pool, q, k_by=0, q_by=0):
+    pool.ks = pool.ks * 2.0 ** k_by
+    return (q.double() * 2.0 ** q_by).to(q.dtype)
+
+
+@pytest.mark.parametrize("heads", [(6, 3), (24, 2)])
+@pytest.mark.parametrize("k_by,q_by,scale", [
+    (0, -110, 2.0 ** -40), (0, -120, 2.0 ** -120), (0, -60, 1e-38),  # the softmax scale times q below fp32's least number
+    (105, -105, 0.0), (112, -110, 0.0), (118, -118, 0.0), (112, -98, 2.0 ** -20),  # keys of 2^112 and more
+    (-118, 118, 0.0), (-100, 60, 2.0 ** 40),
+])
+def test_attend_near_the_ends_of_the_range(heads, k_by, q_by, scale):
+    Hq, Hkv = heads
+    pool = pool_of(("bshd", BF, Hq, Hkv, 64, [900, 17], 1))
+    q = scaled(pool, queries(pool), k_by, q_by)
+    got = pool.cache(scale=scale).attend(q.cuda())
+    ref.check_attend(got, ref8.attend(pool, q, scale=scale or None))
+
+
+def test_zero_scores_of_large_queries_and_keys():
+    """q of 2^120 against zeros in blocks of a scale of 2^30: scores of 0."""
+    pool = Pool8("bshd", BF, 2, 1, 16, 3, 2, [32], seed=6)
+    pool.k[..., 0], pool.ks[:] = 0.0, 2.0 ** 30
+    q = torch.zeros(1, 2, D, dtype=BF)
+    q[..., 0] = 2.0 ** 120
+    out, lse = pool.cache().attend(q.cuda())
+    want = ref8.attend(pool, q)
+    ref.check_attend((out, lse), want)
