@@ -92,7 +92,7 @@ struct AttnArgs {
     int rc, rows;          // chunks of a group's heads, rows per chunk
     int cluster;           // CTAs per segment, one cluster; 0: equal runs of all segments' blocks
     int4 *seg;             // [segments] its pieces: first warp, warps before / CTAs joined / pieces in all
-    float4 *ml;            // [2 * kCtas * kWarps, rows] maximum (log2 units), sum of P, sum of W, 0
+    float4 *ml;            // [2 * kCtas * kWarps, rows] maximum (of q.k), sum of P, sum of W, 0
     float *o;              // [2 * kCtas * kWarps, rows, 128]
     const float *ks, *vs;  // 8 bits: scales [num_pages, Hkv, page / 16]
     float2 *bw;            // vsa_paged_attn_weigh: [segments, blocks, rows] sum of P and the maximum (log2 units) it is
@@ -154,6 +154,9 @@ __device__ __forceinline__ void mma16816<__half>(float (&c)[4], const uint32_t (
 
 __device__ __forceinline__ int seg_blocks(const AttnArgs &a, int n) { return (seg_keys(a, n) + kBlk - 1) / kBlk; }
 
+// P's exponent per unit of q.k, in log2 units.
+__device__ __forceinline__ float log2_scale(const AttnArgs &a) { return a.p.scale * kLog2e; }
+
 // Where a segment's queries, keys and outputs are.
 struct Segment {
     int bh, b, h;        // list row, sequence, key/value head
@@ -211,7 +214,7 @@ __device__ __forceinline__ void store_weights(const AttnArgs &a, const Segment &
 
 // One warp streams blocks [blk0, blk0 + nblk) of a segment, two at a time
 // (32 keys: two independent chains of products, one maximum and one rescaling
-// for both): the running maximum (log2 units), the sums of P and of W of rows
+// for both): the running maximum (of q.k), the sums of P and of W of rows
 // g and g + 8, and their unnormalised outputs at dims 8 j + 2 t, + 1. The ring's slots take the
 // K rows of a step, its V rows, the K rows of the next step and so on; two are
 // in flight while one is used. The ring is free again afterwards.
@@ -222,7 +225,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, t = lane & 3, b = sg.b, bh = sg.bh;
     const T *K = static_cast<const T *>(a.k), *V = static_cast<const T *>(a.v);
-    const float sl2 = p.scale * kLog2e;
+    const float sl2 = log2_scale(a);
     constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f, kDrop = kLift != 0.f ? 0x1p-15f : 1.f;
     constexpr uint32_t kOnes = std::is_same<T, __half>::value ? 0x3C003C00u : 0x3F803F80u;
     const int key0 = blk0 * kBlk;
@@ -414,7 +417,6 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 1);
         l_run[e] += __shfl_xor_sync(0xffffffffu, l_run[e], 2);
         l_run[e] *= kDrop;  // the outputs and the sum of W they are divided by stay lifted
-        m_run[e] *= sl2;    // log2 units from here on
         w_run[e] = wsum[2 * e];
     }
 }
@@ -574,7 +576,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
     const Paged &p = a.p;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3, b = sg.b, bh = sg.bh;
     const unsigned char *K = static_cast<const unsigned char *>(a.k), *V = static_cast<const unsigned char *>(a.v);
-    const float sl2 = p.scale * kLog2e;
+    const float sl2 = log2_scale(a);
     constexpr float kLift = 14.f, kDrop = 0x1p-14f;
     constexpr int kStage8 = stage_bytes<8>;
     constexpr uint32_t kOnes[4] = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
@@ -905,7 +907,6 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l_run[r] += __shfl_xor_sync(0xffffffffu, l_run[r], off);
         l_run[r] *= kDrop;
-        m_run[r] *= sl2;  // log2 units from here on
         w_run[r] = wsum[r >> 1][r & 1];
         const float inv = far ? 1.f : w_run[r] == 0.f ? 0.f : 1.f / w_run[r];
 #pragma unroll
@@ -958,19 +959,25 @@ __device__ __forceinline__ void attend_blocks(const AttnArgs &a, const Segment &
     }
 }
 
+// What a piece with maximum m weighs beside one with maximum `ref`. The
+// difference first, as within a piece: scaled maxima are rounded, by more than
+// what is between two large ones (of 8 million: up to a factor of two in the
+// weights), and with the largest softmax scales they are infinite.
+__device__ __forceinline__ float beside(float m, float ref, float sl2) { return ptx::ex2((m - ref) * sl2); }
+
 // What a piece's output counts for in a join beyond its maximum: unnormalised
 // outputs hold their weights, finished ones (8 bits) do not.
 template <int KV> __device__ __forceinline__ float own_weight(float w) { return KV == 8 ? w : 1.f; }
 
 // Joins the CTA's four warps: stat(row, {M, l, w, 0}) once per row, with the
-// maximum M (log2 units) and the sums l of P and w of W, then out(row, o) per
+// maximum M and the sums l of P and w of W, then out(row, o) per
 // row, in one warp, with a lane's dims 4 lane..: the unnormalised output, or
 // where `done`, and always of an 8-bit cache, the finished one (divided by w).
 // The rows' weights come first, side by side: one after another, with the
 // division and the logarithm of each, 16 rows took 2.4 us more than 5.
 // The warps' rings hold the outputs meanwhile.
 template <int NT, typename S, typename F>
-__device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const float (&m_run)[Frag<NT>::R],
+__device__ __forceinline__ void join_warps(unsigned char *smem, int rows, float sl2, const float (&m_run)[Frag<NT>::R],
                                            const float (&l_run)[Frag<NT>::R], const float (&w_run)[Frag<NT>::R],
                                            const float (&acc)[Frag<NT>::A][4], bool done, S stat, F out) {
     constexpr int KV = Frag<NT>::kv;
@@ -997,11 +1004,11 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
         const float ref = M == -INFINITY ? 0.f : M;
 #pragma unroll
         for (int v = 0; v < kWarps; ++v) {
-            const float f = ptx::ex2(s_m[v][row] - ref);
+            const float f = beside(s_m[v][row], ref, sl2);
             l += f * s_l[v][row];
             w += f * s_w[v][row];
         }
-        const float f = ptx::ex2(s_m[mine][row] - ref) * own_weight<KV>(s_w[mine][row]);
+        const float f = beside(s_m[mine][row], ref, sl2) * own_weight<KV>(s_w[mine][row]);
         s_f[mine][row] = !(done || KV == 8) ? f : w == 0.f ? 0.f : f / w;
         if (mine == 0 && row < rows) stat(row, make_float4(M, l, w, 0.f));
     }
@@ -1022,7 +1029,9 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, const 
 template <typename T> __device__ __forceinline__ uint2 pack4(float4 o) {
     return make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
 }
-__device__ __forceinline__ float lse_of(float M, float l) { return l == 0.f ? -INFINITY : kLn2 * (M + log2f(l)); }
+__device__ __forceinline__ float lse_of(float M, float l, float sl2) {
+    return l == 0.f ? -INFINITY : kLn2 * __fadd_rn(__fmul_rn(M, sl2), log2f(l));
+}
 
 // A cluster per segment (a.cluster CTAs of four warps, equal runs of its
 // blocks). Row r is finished by CTA r % cluster, which has a place for every
@@ -1057,10 +1066,11 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
                                  w_run, acc);
     grid_go();
     T *out = static_cast<T *>(a.out);
+    const float sl2 = log2_scale(a);
     if (CS == 1) {
         join_warps<NT>(
-            smem, sg.rows, m_run, l_run, w_run, acc, true,
-            [&](int row, float4 s) { a.lse[sg.hq0 + row] = lse_of(s.x, s.y); },
+            smem, sg.rows, sl2, m_run, l_run, w_run, acc, true,
+            [&](int row, float4 s) { a.lse[sg.hq0 + row] = lse_of(s.x, s.y, sl2); },
             [&](int row, float4 o) {
                 *reinterpret_cast<uint2 *>(out + (sg.hq0 + row) * kD + 4 * lane) = pack4<T>(o);
             });
@@ -1071,7 +1081,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
     const auto part = [&](int row) { return rank * own + (row >> lg); };
     const auto to = [&](int row) { return (uint32_t)(row & (CS - 1)); };
     join_warps<NT>(
-        smem, sg.rows, m_run, l_run, w_run, acc, false,
+        smem, sg.rows, sl2, m_run, l_run, w_run, acc, false,
         [&](int row, float4 s) { st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_pml[part(row)]), to(row)), s); },
         [&](int row, float4 o) {
             st_cluster4(ptx::cluster_addr(ptx::smem_addr(&s_part[part(row)][4 * lane]), to(row)), o);
@@ -1085,12 +1095,12 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
 #pragma unroll 4
         for (int c = 0; c < CS; ++c) {
             const float4 s = s_pml[c * own + at];
-            const float f = ptx::ex2(s.x - ref);
+            const float f = beside(s.x, ref, sl2);
             l += f * s.y;
             w += f * s.z;
         }
-        s_f[tid] = w == 0.f ? 0.f : ptx::ex2(s_pml[tid].x - ref) * own_weight<KV>(s_pml[tid].z) / w;
-        if (tid < own && row < sg.rows) a.lse[sg.hq0 + row] = lse_of(M, l);
+        s_f[tid] = w == 0.f ? 0.f : beside(s_pml[tid].x, ref, sl2) * own_weight<KV>(s_pml[tid].z) / w;
+        if (tid < own && row < sg.rows) a.lse[sg.hq0 + row] = lse_of(M, l, sl2);
     }
     __syncthreads();
     for (int at = 0, row = rank; row < sg.rows; ++at, row += CS) {
@@ -1131,6 +1141,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
     long long x = min(run.x0 + wid * run.per, run.x1);
     const long long x_end = min(x + run.per, run.x1);
     T *out = static_cast<T *>(a.out);
+    const float sl2 = log2_scale(a);
     while (joined || x < x_end) {  // a joined CTA's warp without blocks still brings its empty part
         if (!joined && x >= before + (long long)nb * mult) {  // also passes over entries without keys
             before += (long long)nb * mult;
@@ -1175,10 +1186,10 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
         if (joined) {
             const bool whole = first && last;
             join_warps<NT>(
-                smem, sg.rows, m_run, l_run, w_run, acc, whole,
+                smem, sg.rows, sl2, m_run, l_run, w_run, acc, whole,
                 [&](int row, float4 s) {
                     if (whole)
-                        a.lse[sg.hq0 + row] = lse_of(s.x, s.y);
+                        a.lse[sg.hq0 + row] = lse_of(s.x, s.y, sl2);
                     else
                         a.ml[slot * a.rows + row] = s;
                 },
@@ -1200,7 +1211,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
                 Frag<NT>::each(acc, r, [&](int d, float2 x) {
                     *reinterpret_cast<uint32_t *>(dst + d) = pack2<T>(x.x * inv, x.y * inv);
                 });
-                if (Frag<NT>::tells()) a.lse[sg.hq0 + row] = lse_of(m_run[r], l_run[r]);
+                if (Frag<NT>::tells()) a.lse[sg.hq0 + row] = lse_of(m_run[r], l_run[r], sl2);
             } else {
                 float *dst = a.o + (slot * a.rows + row) * kD;
                 Frag<NT>::each(acc, r, [&](int d, float2 x) { *reinterpret_cast<float2 *>(dst + d) = x; });
@@ -1248,6 +1259,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
                                                             : sg.x + i + sg.z * (kWarps - 1));
         return (2LL * clampi(w, 0, kCtas * kWarps - 1) + (i == 0 ? 1 : 0)) * a.rows + r;
     };
+    const float sl2 = log2_scale(a);
     float M = -INFINITY;
     for (int i = tid; i < pieces; i += W * 32) {
         s_f[i] = a.ml[place(i)].x;
@@ -1264,7 +1276,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
     const float ref = M == -INFINITY ? 0.f : M;
     float l = 0.f, w = 0.f;
     for (int i = tid; i < pieces; i += W * 32) {  // the thread's own entries again
-        const float e = ptx::ex2(s_f[i] - ref);
+        const float e = beside(s_f[i], ref, sl2);
         const float4 s = a.ml[place(i)];
         s_f[i] = e * own_weight<KV>(s.z);
         l += e * s.y;
@@ -1300,7 +1312,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
     if (W == 1) {
         const float inv = w == 0.f ? 0.f : 1.f / w;
         *reinterpret_cast<uint2 *>(out + 4 * lane) = pack4<T>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (lane == 0) a.lse[row] = lse_of(M, l);
+        if (lane == 0) a.lse[row] = lse_of(M, l, sl2);
         return;
     }
     *reinterpret_cast<float4 *>(&s_o[wid][4 * lane]) = o;
@@ -1315,7 +1327,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
         val += s_o[c][tid];
     }
     out[tid] = from_f<T>(w == 0.f ? 0.f : val / w);
-    if (tid == 0) a.lse[row] = lse_of(M, l);
+    if (tid == 0) a.lse[row] = lse_of(M, l, sl2);
 }
 
 // Whether clusters of 2 c CTAs take segments of up to `keys` keys better than

@@ -1,5 +1,6 @@
 """The paged attention where numbers lie far apart: v scales of an 8-bit cache,
-queries and keys near the ends of bf16's range."""
+scores past the last bit of an exponent, queries and keys near the ends of
+bf16's range."""
 import pytest
 import torch
 
@@ -7,7 +8,7 @@ from bwd_tile_mean_gb300 import vsa
 from tests import paged8_ref as ref8
 from tests import paged_ref as ref
 from tests.paged8_ref import D, E4M3, Pool8
-from tests.paged_ref import U
+from tests.paged_ref import Pool, U
 from tests.test_gpu_paged import BF, HF
 from tests.test_gpu_paged8 import pool_of, queries
 
@@ -122,6 +123,65 @@ def test_weights_tiny_and_scales_huge():
     out, tol = by_products(pool, q, scale=1.0)
     got = pool.cache(scale=1.0).attend(q.cuda())[0].double().cpu()
     assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
+
+
+# ------------------------------------------------------------- large scores
+
+def plain_row(eight, n, seed=3, heads=2):
+    """A cache of one head per query head whose keys are zero but for dims 0
+    and 1, which q takes by 2^15 and 1: scores are whole numbers, exact in fp32."""
+    kind = Pool8 if eight else Pool
+    pool = kind("bshd", BF, heads, heads, 64, -(-n // 64) + 1, -(-n // 64), [n], seed=seed)
+    pool.k[:] = 0.0
+    if eight:
+        pool.ks[:] = 1.0
+    q = torch.zeros(1, heads, D, dtype=BF)
+    q[..., 0], q[..., 1] = 2.0 ** 15, 1.0
+    return pool, q
+
+
+@pytest.mark.parametrize("eight", [True, False], ids=["8", "16"])
+@pytest.mark.parametrize("wide", [0, 3000], ids=["", "wide-table"])
+def test_pieces_are_joined_by_exact_differences(eight, wide):
+    """Two keys in different pieces of a row whose scores, 8,388,609 and
+    8,388,610 and so on, differ by 1 and 2: by less than what their products
+    with log2(e) are rounded by."""
+    pool, q = plain_row(eight, 9001)
+    at = lambda pos: (pool.table[0][pos // 64], pos % 64)  # noqa: E731
+    for step, (near, far) in enumerate([(1, 2), (3, 5), (2, 1), (6, 7), (9, 8)]):
+        pool.k[:] = 0.0
+        for pos, x in ((70, near), (8100, far)):
+            pool.k[at(pos)][:, 0], pool.k[at(pos)][:, 1] = 256.0, float(x)
+        if eight:
+            cache = vsa.PagedCache("bshd", BF, 1, 2, 2, D, 64, pool.num_pages, pool.max_pages + wide,
+                                   k=pool.view(pool.k).cuda(), v=pool.view(pool.v).cuda(), k_scale=pool.ks.cuda(),
+                                   v_scale=pool.vs.cuda(), kv_dtype=E4M3, scale=1.0)
+        else:
+            cache = vsa.PagedCache("bshd", BF, 1, 2, 2, D, 64, pool.num_pages, pool.max_pages + wide,
+                                   k=pool.view(pool.k).cuda(), v=pool.view(pool.v).cuda(), scale=1.0)
+        cache.page_table[:, : pool.max_pages] = torch.tensor(pool.table, dtype=torch.int32)
+        cache.seq_lens.fill_(9001)
+        out = cache.attend(q.cuda())[0][0].double().cpu()
+        p = torch.softmax(torch.tensor([near, far], dtype=torch.float64), 0)
+        v = [(pool.v[at(x)] * (pool.vs[at(x)[0], :, at(x)[1] // 16, None] if eight else 1.0)).double() for x in (70, 8100)]
+        want = p[0] * v[0] + p[1] * v[1]
+        # the weights' rounding to 16 bits, the output's, and fp32
+        tol = (U[BF] + 2.0 ** -18) * (p[0] * v[0].abs() + p[1] * v[1].abs()) + U[BF] * want.abs()
+        assert ((out - want).abs() <= tol).all(), (step, float(((out - want).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("eight", [True, False], ids=["8", "16"])
+@pytest.mark.parametrize("n", [40, 9001])
+def test_the_largest_softmax_scale(eight, n):
+    """A scale whose product with a score is beyond fp32 takes the largest
+    score's value, whichever piece holds it."""
+    pool, q = plain_row(eight, n)
+    best = n // 3
+    p, slot = pool.table[0][best // 64], best % 64
+    pool.k[p, slot, :, 1] = 64.0
+    out = pool.cache(scale=2.2e38).attend(q.cuda())[0][0].cpu()
+    v = pool.v[p, slot].float() * (pool.vs[p, :, slot // 16, None] if eight else 1.0)
+    assert torch.equal(out, v.to(BF))
 
 
 # --------------------------------------------- queries and keys near bf16's ends
