@@ -202,6 +202,7 @@ struct PagedWs {
     size_t seg;         // [segments] int4: where a segment's pieces are
     size_t ml;          // [slots, rows] float4: maximum of q.k, sum of weights, of rounded weights, 0
     size_t o;           // [slots, rows, 128] fp32 unnormalised partial outputs
+    size_t stat;        // [B, Hq] float2, where pages are weighed: a row's maximum of q.k and 1 / sum of weights
     size_t total;
 };
 PagedWs paged_ws(const Paged &p);

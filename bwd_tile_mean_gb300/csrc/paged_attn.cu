@@ -17,6 +17,7 @@ PagedWs paged_ws(const Paged &p) {
     w.seg = take(sizeof(int4) * p.B * (size_t)p.Hkv * rc);
     w.ml = take(sizeof(float4) * 2 * kCtas * kWarps * rows);
     w.o = take(sizeof(float) * 2 * kCtas * kWarps * rows * kD);
+    w.stat = take(sizeof(float2) * p.B * (size_t)p.Hq);
     w.total = at;
     return w;
 }

@@ -95,8 +95,9 @@ struct AttnArgs {
     float4 *ml;            // [2 * kCtas * kWarps, rows] maximum (of q.k), sum of P, sum of W, 0
     float *o;              // [2 * kCtas * kWarps, rows, 128]
     const float *ks, *vs;  // 8 bits: scales [num_pages, Hkv, page / 16]
-    float2 *bw;            // vsa_paged_attn_weigh: [segments, blocks, rows] sum of P and the maximum (log2 units) it is
-    int blocks;            // relative to; blocks a segment has room for
+    float2 *bw;            // vsa_paged_attn_weigh: [segments, blocks, rows] sum of P and the maximum of q.k it is relative
+    int blocks;            // to; blocks a segment has room for
+    float2 *stat;          // [B, Hq] a row's maximum of q.k and 1 / sum of P
 };
 
 // Keys of segment list entry n ((b) without page lists, (b, h) with): the
@@ -193,8 +194,8 @@ template <typename T> __device__ __forceinline__ void load_q(const AttnArgs &a, 
 }
 
 // vsa_paged_attn_weigh: the sums of P (as lifted) over blocks blk and blk + 1 of
-// a segment (those before `end`), each row's beside the maximum (log2 units)
-// that it is relative to. The four lanes of a row add up: each ends with one
+// a segment (those before `end`), each row's beside the maximum of q.k that it
+// is relative to. The four lanes of a row add up: each ends with one
 // (block, row) of the four.
 __device__ __forceinline__ void store_weights(const AttnArgs &a, const Segment &sg, int blk, int end, const float (&sc)[4][4],
                                               float ref0, float ref1) {
@@ -375,7 +376,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
                 }
             l_run[e] = fmaf(l_run[e], corr[e], sum);  // this lane's keys; quads are joined at the end
         }
-        if constexpr (kWeigh) store_weights(a, sg, blk0 + 2 * i, blk0 + nblk, sc, m_run[0] * sl2, m_run[1] * sl2);
+        if constexpr (kWeigh) store_weights(a, sg, blk0 + 2 * i, blk0 + nblk, sc, m_run[0], m_run[1]);
         if (__any_sync(0xffffffffu, moved)) {
             wsum[0] *= corr[0], wsum[1] *= corr[0], wsum[2] *= corr[1], wsum[3] *= corr[1];
 #pragma unroll
@@ -774,12 +775,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
                     }
                 l_run[r] = fmaf(l_run[r], corr[r], sum);  // this lane's keys; the eight of a head are joined at the end
             }
-        if constexpr (kWeigh) {
-            float ref[2 * NT];
-#pragma unroll
-            for (int r = 0; r < 2 * NT; ++r) ref[r] = m_run[r] * sl2;
-            store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, ref);
-        }
+        if constexpr (kWeigh) store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, m_run);
         if constexpr (kFar) {
             // The sum of the weights as below; then the weights for the outputs: a row's largest product of weight and scale
             // so far comes to [2^12, 2^14) (a scale of 2^127: a binade more), and the outputs with it
@@ -1029,8 +1025,11 @@ __device__ __forceinline__ void join_warps(unsigned char *smem, int rows, float 
 template <typename T> __device__ __forceinline__ uint2 pack4(float4 o) {
     return make_uint2(pack2<T>(o.x, o.y), pack2<T>(o.z, o.w));
 }
-__device__ __forceinline__ float lse_of(float M, float l, float sl2) {
-    return l == 0.f ? -INFINITY : kLn2 * __fadd_rn(__fmul_rn(M, sl2), log2f(l));
+// A finished row's LSE; where pages are weighed also its maximum and sum, which the LSE is too short for (rounded, it is off
+// by 2^-24 of itself, and weights by a factor of e to that: a hundredth for scores of 100,000, anything for 1e9).
+__device__ __forceinline__ void store_row(const AttnArgs &a, long long row, float M, float l, float sl2) {
+    a.lse[row] = l == 0.f ? -INFINITY : kLn2 * __fadd_rn(__fmul_rn(M, sl2), log2f(l));
+    if (a.stat) a.stat[row] = make_float2(M, 1.f / l);
 }
 
 // A cluster per segment (a.cluster CTAs of four warps, equal runs of its
@@ -1070,7 +1069,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
     if (CS == 1) {
         join_warps<NT>(
             smem, sg.rows, sl2, m_run, l_run, w_run, acc, true,
-            [&](int row, float4 s) { a.lse[sg.hq0 + row] = lse_of(s.x, s.y, sl2); },
+            [&](int row, float4 s) { store_row(a, sg.hq0 + row, s.x, s.y, sl2); },
             [&](int row, float4 o) {
                 *reinterpret_cast<uint2 *>(out + (sg.hq0 + row) * kD + 4 * lane) = pack4<T>(o);
             });
@@ -1100,7 +1099,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
             w += f * s.z;
         }
         s_f[tid] = w == 0.f ? 0.f : beside(s_pml[tid].x, ref, sl2) * own_weight<KV>(s_pml[tid].z) / w;
-        if (tid < own && row < sg.rows) a.lse[sg.hq0 + row] = lse_of(M, l, sl2);
+        if (tid < own && row < sg.rows) store_row(a, sg.hq0 + row, M, l, sl2);
     }
     __syncthreads();
     for (int at = 0, row = rank; row < sg.rows; ++at, row += CS) {
@@ -1189,7 +1188,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
                 smem, sg.rows, sl2, m_run, l_run, w_run, acc, whole,
                 [&](int row, float4 s) {
                     if (whole)
-                        a.lse[sg.hq0 + row] = lse_of(s.x, s.y, sl2);
+                        store_row(a, sg.hq0 + row, s.x, s.y, sl2);
                     else
                         a.ml[slot * a.rows + row] = s;
                 },
@@ -1211,7 +1210,7 @@ template <typename T, int NT, bool kWeigh> __global__ void __launch_bounds__(kWa
                 Frag<NT>::each(acc, r, [&](int d, float2 x) {
                     *reinterpret_cast<uint32_t *>(dst + d) = pack2<T>(x.x * inv, x.y * inv);
                 });
-                if (Frag<NT>::tells()) a.lse[sg.hq0 + row] = lse_of(m_run[r], l_run[r], sl2);
+                if (Frag<NT>::tells()) store_row(a, sg.hq0 + row, m_run[r], l_run[r], sl2);
             } else {
                 float *dst = a.o + (slot * a.rows + row) * kD;
                 Frag<NT>::each(acc, r, [&](int d, float2 x) { *reinterpret_cast<float2 *>(dst + d) = x; });
@@ -1312,7 +1311,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
     if (W == 1) {
         const float inv = w == 0.f ? 0.f : 1.f / w;
         *reinterpret_cast<uint2 *>(out + 4 * lane) = pack4<T>(make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (lane == 0) a.lse[row] = lse_of(M, l, sl2);
+        if (lane == 0) store_row(a, row, M, l, sl2);
         return;
     }
     *reinterpret_cast<float4 *>(&s_o[wid][4 * lane]) = o;
@@ -1327,7 +1326,7 @@ template <typename T, int KV, int W, int R> __global__ void __launch_bounds__(W 
         val += s_o[c][tid];
     }
     out[tid] = from_f<T>(w == 0.f ? 0.f : val / w);
-    if (tid == 0) a.lse[row] = lse_of(M, l, sl2);
+    if (tid == 0) store_row(a, row, M, l, sl2);
 }
 
 // Whether clusters of 2 c CTAs take segments of up to `keys` keys better than
@@ -1424,6 +1423,7 @@ inline vsa_status attn_args(const AttnCall &c, bool eight, AttnArgs *args) {
     a.ml = reinterpret_cast<float4 *>(w + ws.ml);
     a.o = reinterpret_cast<float *>(w + ws.o);
     if (c.weigh) {
+        a.stat = reinterpret_cast<float2 *>(w + ws.stat);
         a.bw = reinterpret_cast<float2 *>(w + ws.total);
         a.blocks = a.p.max_len / kBlk;
     }

@@ -9,7 +9,9 @@
 // a key's P is known only when its row is finished. It leaves, per row and block
 // of 16 keys, the sum of the block's exponentials and the maximum that they are
 // relative to: 8 bytes per row and block against the block's 4 to 8 KB of keys
-// and values. k_page_weigh puts them over the rows' LSE, per page.
+// and values. k_page_weigh puts them over the rows' sums, per page, by the
+// difference of the maxima before its scaling: a row's weights are one together
+// at any score.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -22,12 +24,13 @@ struct WeighArgs {
     Paged p;
     const int *idx, *cnt;
     int cap;
-    const float *lse;
+    const float2 *stat;    // [B, Hq] the rows' maxima of q.k, and 1 / their sums of P
     const float2 *bw;      // [segments, blocks, rows]
     int blocks, rows, rc;
     const float *in;       // [B, Hkv, max_pages]
     float *out;
     float decay, drop;     // drop: the attention's lift of P, undone
+    float sl2;             // P's exponent per unit of q.k, in log2 units
     int lanes, row_lanes;  // log2 of the lanes per page (as many as it has records, up to 32), and of those per block
     unsigned chunks;       // CTAs per list row
 };
@@ -43,11 +46,11 @@ __device__ __forceinline__ float mass_of(const WeighArgs &a, int b, int h, int b
     float mass = 0.f;
     for (int r = 0; r < a.rc; ++r) {
         if (i >= min(a.rows, p.G - r * a.rows)) break;
-        const float ref = a.lse[(long long)b * p.Hq + h * p.G + r * a.rows + i] * kLog2e;
+        const float2 row = a.stat[(long long)b * p.Hq + h * p.G + r * a.rows + i];
         const float2 *w = a.bw + (((long long)bh * a.rc + r) * a.blocks + blk) * a.rows + i;
         for (int k = me >> a.row_lanes; k < n; k += 1 << (a.lanes - a.row_lanes)) {
             const float2 x = w[k * a.rows];
-            if (x.x != 0.f) mass += x.x * ptx::ex2(x.y - ref);
+            if (x.x != 0.f) mass += x.x * (ptx::ex2((x.y - row.x) * a.sl2) * row.y);
         }
     }
     return mass;
@@ -424,8 +427,10 @@ extern "C" vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const voi
     a.idx = page_idx;
     a.cnt = page_cnt;
     a.cap = idx_cap;
-    a.lse = lse;
-    a.bw = reinterpret_cast<const float2 *>(static_cast<char *>(workspace) + paged_ws(a.p).total);
+    const PagedWs ws = paged_ws(a.p);
+    a.stat = reinterpret_cast<const float2 *>(static_cast<char *>(workspace) + ws.stat);
+    a.bw = reinterpret_cast<const float2 *>(static_cast<char *>(workspace) + ws.total);
+    a.sl2 = a.p.scale * kLog2e;
     a.blocks = a.p.max_len / 16;
     a.rc = (a.p.G + a.rows - 1) / a.rows;
     a.in = page_weight;

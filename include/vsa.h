@@ -645,7 +645,7 @@ vsa_status vsa_paged_read(const vsa_paged_desc *desc, int T, const int32_t *cu_s
  *   weight_out[b, h, j] = decay * page_weight[b, h, j] + sum P
  * over the page's tokens and the query heads of key/value head h, P = exp(scale
  * q.k - LSE); a listed page that is listed twice counts twice, one that is not listed
- * adds 0. The other entries are copied. page_weight, weight_out [B, Hkv,
+ * adds 0. A row's weights are 1 together at any score, as in O. The other entries are copied. page_weight, weight_out [B, Hkv,
  * max_pages] fp32, one buffer or two that do not overlap; decay in [0, 1] (0: what page_weight
  * holds for the sequence's pages does not count, NaN included). out and lse are those of the plain call bit for bit, and the
  * sums are the same bit for bit on every run. idx_cap <= max_pages (VSA_ERR_UNSUPPORTED).

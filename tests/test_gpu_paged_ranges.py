@@ -9,7 +9,7 @@ from tests import paged8_ref as ref8
 from tests import paged_ref as ref
 from tests.paged8_ref import D, E4M3, Pool8
 from tests.paged_ref import Pool, U
-from tests.test_gpu_paged import BF, HF
+from tests.test_gpu_paged import BF, HF, attend_pool, widened
 from tests.test_gpu_paged8 import pool_of, queries
 
 pytestmark = pytest.mark.gpu
@@ -182,6 +182,59 @@ def test_the_largest_softmax_scale(eight, n):
     out = pool.cache(scale=2.2e38).attend(q.cuda())[0][0].cpu()
     v = pool.v[p, slot].float() * (pool.vs[p, :, slot // 16, None] if eight else 1.0)
     assert torch.equal(out, v.to(BF))
+
+
+def sums_of(weight):
+    return weight.double().sum(-1).cpu()
+
+
+@pytest.mark.parametrize("lens", [[40], [9001], [9001, 33, 5000]])
+@pytest.mark.parametrize("eight", [True, False], ids=["8", "16"])
+def test_page_weights_of_the_largest_scores(lens, eight):
+    """Scores of 1e13 and more: every row's weights are still 1 together, all
+    of it on the page of its largest score."""
+    if eight:
+        pool = pool_of(("bhsd", BF, 4, 2, 64, lens, 0), garbage=False)
+        q = (queries(pool).float().abs() + 1).to(BF) * 1e6
+        pool.k, pool.ks[:] = pool.k.abs().clamp(max=120), 2.0 ** 13
+        big, apart = 448.0, 1.0
+    else:
+        pool, q = attend_pool(("bhsd", BF, 4, 2, 64, lens), seed=45)
+        q = (q.float().abs() + 1).to(BF) * 1e6
+        pool.k.copy_((pool.k.float().abs() * 1e5).to(BF))
+        big = 3e6
+    best = [n // 3 for n in lens]
+    for b, pos in enumerate(best):
+        pool.k[pool.table[b][pos // 64], pos % 64] = big
+    caches = [pool.cache(weigh=True)]
+    if not eight:
+        wide = widened(pool, 1000)
+        caches.append(vsa.PagedCache("bhsd", BF, pool.B, 4, 2, D, 64, pool.num_pages, pool.max_pages + 1000, k=wide.k, v=wide.v,
+                                     page_table=wide.page_table, seq_lens=wide.seq_lens, weigh=True))
+    for cache in caches:
+        every = torch.arange(cache.max_pages, dtype=torch.int32).expand(pool.B, 2, -1).contiguous().cuda()
+        count = torch.tensor([[-(-n // 64)] * 2 for n in lens], dtype=torch.int32).cuda()
+        for pages in (None, (every, count)):
+            w = torch.zeros(pool.B, 2, cache.max_pages, device="cuda")
+            cache.attend(q.cuda(), pages, page_weight=w)
+            assert ((sums_of(w) - 2).abs() <= 2 * 2.0 ** -14).all()
+            for b, pos in enumerate(best):
+                assert ((w[b, :, pos // 64].cpu() - 2).abs() <= 2 * 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("eight", [True, False], ids=["8", "16"])
+@pytest.mark.parametrize("size", [30.0, 3e3, 3e5, 3e7])
+@pytest.mark.parametrize("Hq,Hkv,lens", [(6, 3, [37, 4000]), (24, 2, [9001]), (8, 8, [3000, 0, 100])])
+def test_weights_of_a_row_are_one(Hq, Hkv, lens, eight, size):
+    """Random scores of any size: whatever their fp32 errors are, a row's
+    weights are what its output is made with, 1 together."""
+    pool = pool_of(("bshd", BF, Hq, Hkv, 32, lens, 1), eight, garbage=eight)
+    q = queries(pool, size=size)
+    cache = pool.cache(weigh=True)
+    w = torch.zeros(pool.B, Hkv, cache.max_pages, device="cuda")
+    cache.attend(q.cuda(), page_weight=w)
+    want = torch.tensor([Hq / Hkv if n else 0.0 for n in lens], dtype=torch.float64)[:, None]
+    assert ((sums_of(w) - want).abs() <= want * 2.0 ** -14).all(), float((sums_of(w) - want).abs().max())
 
 
 # --------------------------------------------- queries and keys near bf16's ends
