@@ -16,11 +16,14 @@
 // vsa_rope_table; calls run on the device of their tensors.
 #include <Python.h>
 
+#include <ATen/Context.h>
 #include <ATen/core/Tensor.h>
 #include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <ATen/record_function.h>
 #include <c10/core/InferenceMode.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -111,16 +114,26 @@ int64_t row_stride(const Calls &c, const char *name, const at::Tensor &t, int64_
     if (t.stride(0) < heads * c.d.D) refuse(name, ": tokens must not share memory");  // 0 means dense further on
     return t.stride(0);
 }
-// A dense tensor, uninitialised: straight from the GPU's allocator where at::empty would come to that (two of them cost a
-// call 3.4 us through the dispatcher, more than its launch).
-at::Tensor dense(at::IntArrayRef shape, at::ScalarType dtype, at::Device device) {
-    if (device.is_cuda() && !c10::InferenceMode::is_enabled())
-        return at::Tensor(at::detail::empty_cuda(shape, dtype, device, std::nullopt));
-    return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+// Whether at::empty does more than allocate: inference tensors, torch.use_deterministic_algorithms' NaN in uninitialised
+// memory, dispatch modes and the profiler that are to see it.
+bool empty_is_more() {
+    const at::Context &torch = at::globalContext();
+    return c10::InferenceMode::is_enabled() ||
+           (torch.deterministicAlgorithms() && torch.deterministicFillUninitializedMemory()) ||
+           c10::impl::dispatch_mode_enabled() || at::hasCallbacks();
 }
-at::Tensor output(const Calls &c, at::IntArrayRef shape, at::ScalarType dtype) {
-    return dense(shape, dtype, c.device < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c.device));
-}
+// Dense tensors for a call's outputs, uninitialised: straight from the GPU's allocator where at::empty would come to that (two
+// of them cost a call 3.4 us through the dispatcher, more than its launch; the question costs some 0.1).
+struct Outputs {
+    const bool more = empty_is_more();
+    at::Tensor dense(at::IntArrayRef shape, at::ScalarType dtype, at::Device device) const {
+        if (device.is_cuda() && !more) return at::Tensor(at::detail::empty_cuda(shape, dtype, device, std::nullopt));
+        return at::empty(shape, at::TensorOptions().dtype(dtype).device(device));
+    }
+    at::Tensor dense(at::IntArrayRef shape, at::ScalarType dtype, const Calls &c) const {
+        return dense(shape, dtype, c.device < 0 ? at::Device(at::kCPU) : at::Device(at::kCUDA, c.device));
+    }
+};
 PyObject *pair(at::Tensor a, at::Tensor b) {
     PyObject *t = PyTuple_New(2);
     if (!t) throw Raised();
@@ -243,6 +256,7 @@ PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             check_dense(c, "sin", *sin, at::kFloat, cos->sizes());
         }
         if (pos) check_dense(c, "positions", *pos, at::kInt, {T});
+        const Outputs made;
         at::Tensor q_out;
         if (given) {
             if (!q) refuse("q_out without q");
@@ -254,7 +268,7 @@ PyObject *calls_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                    cache_mean(c), cache_table(c), cache_lens(c)});
             q_out = *given;
         } else if (q) {
-            q_out = output(c, {T, c.d.Hq, c.d.D}, c.dtype());
+            q_out = made.dense({T, c.d.Hq, c.d.D}, c.dtype(), c);
         }
         for (const Pieces &written : {cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_mean(c)})
             apart(written, {pieces("k", k), pieces("v", v), opt("q", q), opt("cu_seqlens", cu), opt("cos", cos),
@@ -298,8 +312,9 @@ PyObject *calls_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         for (const Pieces &written : {pi, pc})
             apart(written, {pieces("q", q), cache_mean(c), cache_table(c), cache_lens(c), cache_ws(c)});
         apart(pi, {pc});
-        at::Tensor idx = gi ? *gi : output(c, {c.d.B, c.d.Hkv, topk}, at::kInt);
-        at::Tensor cnt = gc ? *gc : output(c, {c.d.B, c.d.Hkv}, at::kInt);
+        const Outputs made;
+        at::Tensor idx = gi ? *gi : made.dense({c.d.B, c.d.Hkv, topk}, at::kInt, c);
+        at::Tensor cnt = gc ? *gc : made.dense({c.d.B, c.d.Hkv}, at::kInt, c);
         run(c, "vsa_page_select", [&](vsa_stream_t s) {
             return c.select(&c.d, q.data_ptr(), qs, static_cast<float *>(c.mean), (int)topk, (int)first, (int)last,
                             ptr<int32_t>(&idx), ptr<int32_t>(&cnt), c.ws, c.ws_bytes, s);
@@ -352,8 +367,9 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         apart(pl, {pt, pp});
         if (pw && pt.at != pp.at) apart(pt, {pp});
         apart(cache_ws(c, pw != nullptr), {pp});
-        at::Tensor out = go ? *go : output(c, {c.d.B, c.d.Hq, c.d.D}, c.dtype());
-        at::Tensor lse = gl ? *gl : output(c, {c.d.B, c.d.Hq}, at::kFloat);
+        const Outputs made;
+        at::Tensor out = go ? *go : made.dense({c.d.B, c.d.Hq, c.d.D}, c.dtype(), c);
+        at::Tensor lse = gl ? *gl : made.dense({c.d.B, c.d.Hq}, at::kFloat, c);
         const int cap = idx ? (int)idx->size(2) : 0;
         run(c, pw ? "vsa_paged_attn_weigh" : c.eight ? "vsa_paged8_attn" : "vsa_paged_attn", [&](vsa_stream_t s) {
             if (pw)
@@ -388,8 +404,9 @@ PyObject *calls_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             apart(written, {opt("cu_seqlens", cu), cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_table(c),
                             cache_lens(c)});
         apart(pk, {pv});
-        at::Tensor k = gk ? *gk : output(c, {T, c.d.Hkv, c.d.D}, c.dtype());
-        at::Tensor v = gv ? *gv : output(c, {T, c.d.Hkv, c.d.D}, c.dtype());
+        const Outputs made;
+        at::Tensor k = gk ? *gk : made.dense({T, c.d.Hkv, c.d.D}, c.dtype(), c);
+        at::Tensor v = gv ? *gv : made.dense({T, c.d.Hkv, c.d.D}, c.dtype(), c);
         if (T > 0 || c.device < 0)
             run(c, "vsa_paged_read", [&](vsa_stream_t s) {
                 return c.read(&c.d, (int)T, ptr<int32_t>(cu), c.k, c.v, c.kscale, c.vscale, k.data_ptr(), v.data_ptr(), s);
@@ -437,8 +454,9 @@ PyObject *calls_evict(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             for (int j = 0; j < i; ++j) apart(outs[i], {outs[j]});
         }
         apart(cache_ws(c), {in[2]});
-        at::Tensor freed = gf ? *gf : output(c, {c.d.B, cap}, at::kInt);
-        at::Tensor count = gc ? *gc : output(c, {c.d.B}, at::kInt);
+        const Outputs made;
+        at::Tensor freed = gf ? *gf : made.dense({c.d.B, cap}, at::kInt, c);
+        at::Tensor count = gc ? *gc : made.dense({c.d.B}, at::kInt, c);
         run(c, "vsa_page_evict", [&](vsa_stream_t s) {
             return c.evict(&c.d, ptr<float>(&w), (int)keep, (int)first, (int)last, static_cast<int32_t *>(table),
                            static_cast<int32_t *>(lens), static_cast<float *>(to), ptr<int32_t>(&freed), ptr<int32_t>(&count),
@@ -634,6 +652,7 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
             if (B > INT32_MAX || S > INT32_MAX || x[i].n[2] > INT32_MAX) refuse(x[i].name, ": too large");
         const Positions p = positions_of(r, pos, B, S, layout != kTnd);
         const int count = k ? 2 : 1;
+        const Outputs made;
         at::Tensor out[2];
         Tokens y[2];
         const at::Tensor *in[2] = {&q, k}, *given[2] = {qo, ko};
@@ -645,7 +664,7 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                     refuse(name, ": expected ", in[i]->sizes(), ", got ", given[i]->sizes());
                 out[i] = *given[i];
             } else {
-                out[i] = dense(in[i]->sizes(), dtype, q.device());
+                out[i] = made.dense(in[i]->sizes(), dtype, q.device());
             }
             y[i] = tokens(name, out[i], layout);
             if (!given[i]) continue;
@@ -684,6 +703,7 @@ PyObject *rope_table(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int64_t T = pos.dim() == 2 ? pos.size(0) : 0, pairs = r.r.rot_dim / 2;
         const Positions p = positions_of(r, pos, 1, T, false);
         if (T > INT32_MAX) refuse("positions: too many tokens");
+        const Outputs made;
         at::Tensor out[2];
         const at::Tensor *given[2] = {gc, gs};
         for (int i = 0; i < 2; ++i) {
@@ -694,7 +714,7 @@ PyObject *rope_table(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                     refuse(name, ": expected a contiguous [", T, ", ", pairs, "], got ", given[i]->sizes());
                 out[i] = *given[i];
             } else {
-                out[i] = dense({T, pairs}, at::kFloat, pos.device());
+                out[i] = made.dense({T, pairs}, at::kFloat, pos.device());
             }
         }
         const Tokens m = as_tokens(pos, "positions");
