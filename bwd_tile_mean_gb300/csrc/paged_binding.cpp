@@ -366,7 +366,9 @@ PyObject *calls_attend(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         apart(po, {pl, pt, pp});
         apart(pl, {pt, pp});
         if (pw && pt.at != pp.at) apart(pt, {pp});
-        apart(cache_ws(c, pw != nullptr), {pp});
+        if (pw)  // the part behind the plain calls' may be a tensor of the cache, as long as pages are not weighed
+            apart(cache_ws(c, true), {pp, cache_k(c), cache_v(c), cache_ks(c), cache_vs(c), cache_mean(c), cache_table(c),
+                                      cache_lens(c)});
         const Outputs made;
         at::Tensor out = go ? *go : made.dense({c.d.B, c.d.Hq, c.d.D}, c.dtype(), c);
         at::Tensor lse = gl ? *gl : made.dense({c.d.B, c.d.Hq}, at::kFloat, c);
