@@ -84,9 +84,10 @@ __device__ __forceinline__ float warp_top(float x) {
     for (int off = 16; off; off >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
     return x;
 }
-// 8 entries as bytes of this scale (inv: its inverse). `plain`: all fit, and the scale is not the largest; otherwise
-// infinities become NaN.
-template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)[8], float scale, float inv, bool plain) {
+// 8 entries as bytes of a scale, by its inverse. `plain`: all fit, and the scale is below the largest; otherwise infinities
+// become NaN, and others the largest value that the scale brings within dtype: 240 (1.875 2^7) for the largest scale that is
+// made here, less in steps of 2^-9 at the end for a larger one that the cache came with.
+template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)[8], float inv, bool plain) {
     uint32_t r[4];
     if (plain) {
 #pragma unroll
@@ -95,7 +96,8 @@ template <typename T> __device__ __forceinline__ uint2 bytes_of(const float (&x)
             r[j] = e4m3x2_of(y.x, y.y);
         }
     } else {
-        const float most = scale == Range<T>::kTop ? 240.f : 448.f;
+        const float top = 240.f * (Range<T>::kTop * inv);
+        const float most = top > 240.f ? 448.f : top < 0x1p-6f ? floorf(top * 0x1p9f) * 0x1p-9f : top;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             float y[2];
@@ -276,13 +278,13 @@ __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
                     top = warp_top(top);
                 }
                 const float vs = fmaxf(scale_of(top), v_old), inv = 1.f / vs;
-                plain = plain && vs != Range<T>::kTop;
+                plain = plain && vs < Range<T>::kTop;
                 if (begun && vs != v_old) shrink(vc, v_old / vs);
 #pragma unroll kUnroll
                 for (int c = c0; c < c1; ++c) {
                     float y[8];
                     unpack8<T>(value(c), y);
-                    if (is_new(c)) *reinterpret_cast<uint2 *>(vc + 2 * c * p.tok_stride) = bytes_of<T>(y, vs, inv, plain);
+                    if (is_new(c)) *reinterpret_cast<uint2 *>(vc + 2 * c * p.tok_stride) = bytes_of<T>(y, inv, plain);
                 }
                 if (lane == 0) a.vscale[sc] = vs;
                 if (more)
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
                 top = warp_top(top);
             }
             ks = fmaxf(scale_of(top), k_old);
-            plain = plain && ks != Range<T>::kTop;
+            plain = plain && ks < Range<T>::kTop;
             const float inv = 1.f / ks;
             if (begun && ks != k_old) shrink(kc, k_old / ks);
             if (mean && begun) old_keys();
@@ -337,7 +339,7 @@ __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
             for (int c = c0; c < c1; ++c) {
                 float y[8];
                 key(c, y);
-                const uint2 b = bytes_of<T>(y, ks, inv, plain);
+                const uint2 b = bytes_of<T>(y, inv, plain);
                 if (is_new(c)) {
                     *reinterpret_cast<uint2 *>(kc + 2 * c * p.tok_stride) = b;
                     if (mean) add8(acc, b);

@@ -1,6 +1,6 @@
 """The paged attention where numbers lie far apart: v scales of an 8-bit cache,
 scores past the last bit of an exponent, queries and keys near the ends of
-bf16's range."""
+bf16's range, the largest entries under the largest scales."""
 import pytest
 import torch
 
@@ -235,6 +235,35 @@ def test_weights_of_a_row_are_one(Hq, Hkv, lens, eight, size):
     cache.attend(q.cuda(), page_weight=w)
     want = torch.tensor([Hq / Hkv if n else 0.0 for n in lens], dtype=torch.float64)[:, None]
     assert ((sums_of(w) - want).abs() <= want * 2.0 ** -14).all(), float((sums_of(w) - want).abs().max())
+
+
+# --------------------------------------------------- appends under large scales
+
+@pytest.mark.parametrize("dtype,top", [(HF, 8), (BF, 120)])
+@pytest.mark.parametrize("more", [0, 1, 6, 13, 14, 16, 17, 20])
+def test_append_under_a_scale_larger_than_any_of_its_own(dtype, top, more):
+    """A begun block whose scale (given with the cache) is 2^more times the
+    largest that an append makes: the type's largest entry still reads back
+    finite, as the nearest byte that stays within it."""
+    if top + more > 127:
+        pytest.skip("no such scale in fp32")
+    scale, big = 2.0 ** (top + more), torch.finfo(dtype).max
+    cache = vsa.PagedCache("bshd", dtype, 1, 2, 2, D, 16, 2, 2, kv_dtype=E4M3)
+    cache.k_scale.fill_(scale), cache.v_scale.fill_(scale)
+    cache.page_table.copy_(torch.tensor([[1, 0]], dtype=torch.int32))
+    cache.seq_lens.fill_(6)
+    x = torch.zeros(1, 2, D, dtype=dtype, device="cuda")
+    x[..., 0], x[..., 1], x[..., 2] = big, -big, big / 2
+    cache.append(x, x)
+    assert (cache.k_scale[1] == scale).all() and (cache.v_scale[1] == scale).all()
+    e4m3 = torch.arange(127, dtype=torch.uint8).view(E4M3).double() * scale
+    e4m3 = e4m3[e4m3 <= big]
+    for got in cache.read(1):
+        got = got.double().cpu()[0]
+        for d, want in ((0, big), (1, -big), (2, big / 2)):
+            nearest = (e4m3 - abs(want)).abs().min()
+            assert ((got[:, d].abs() - abs(want)).abs() == nearest).all() and torch.isfinite(got).all()
+            assert (got[:, d] * want >= 0).all()
 
 
 # --------------------------------------------- queries and keys near bf16's ends
