@@ -158,7 +158,16 @@ struct EvictArgs {
     int *len;        // [B] the lengths: lens_out may be the lengths themselves
 };
 constexpr int kSumThreads = 256;
-constexpr int kOneHeads = 32;  // heads up to which a CTA takes a whole sequence (of up to 1,024 pages)
+// Whether one CTA takes a whole sequence (of up to 1,024 pages) in one launch, which costs it half a microsecond or more per
+// head, instead of a launch for the sums and then a CTA per row, which does where there are many more rows than SMs. Measured
+// (us, one launch / two): 1 sequence of 250 pages x 4, 8, 16, 32 heads 5.8 / 6.1, 6.9 / 6.3, 10.5 / 7.9, 18.7 / 10.3; of 1,000
+// pages x 1, 8, 32 heads 9.9 / 5.7, 11.4 / 6.7, 35.4 / 10.6; 16 of 250 x 8, 32 7.1 / 7.9, 19.6 / 20.0; 24 of 250 x 8, 16, 32 7.0 /
+// 9.9, 12.0 / 14.6, 19.7 / 26.5, of 1,000 12.4 / 11.6, 19.8 / 17.5, 36.1 / 32.7; 64 of 250 x 1, 8, 32 5.6 / 6.6, 7.7 / 17.9, 19.6 /
+// 66.2, of 1,000 x 1, 4, 32 10.5 / 7.5, 11.3 / 14.6, 36.2 / 79.3.
+inline bool one_launch(const Paged &p) {
+    if (p.max_pages > 1024) return false;
+    return (p.Hkv <= 4 && p.max_pages <= 512) || (p.B > 20 && (long long)p.B * (p.Hkv + 1) > 152);
+}
 
 // A float's order as an unsigned's; NaN with -inf, -0 with 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -202,7 +211,9 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
 // before each counted instead of the digits); one of 7,680 pages x 24 heads 13.2, 4 of them the sums. With 8-bit digits and
 // 512 entries placed at a time the latter took 18.9, 25 where a warp's lanes matched their bins first, and 15.9 with a
 // thread's entries side by side, whose stores are not.
-constexpr int kBins = 2048, kRowsAhead = 10;  // rows: 8, 10, 16 took 7.0, 6.9, 7.8 us on the 64 sequences
+// Rows of a sequence loaded at once: 8, 10, 16 took 6.0, 6.9, 7.3 us for 64 sequences of 250 pages x 4 heads, 7.9, 7.0, 8.2 for 8
+// (nine rows, all at once with ten), 12.0, 12.1, 11.2 for 16, 19.5, 19.8, 19.2 for 32.
+constexpr int kBins = 2048, kRowsAhead = 10;
 template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
     constexpr int W = N / 32, kChunk = N * E, R = kOne ? kRowsAhead : 1;
     static_assert(!kOne || E == 1, "one page per thread");
@@ -475,7 +486,7 @@ extern "C" vsa_status vsa_page_evict(const vsa_paged_desc *desc, const float *pa
     a.len = reinterpret_cast<int *>(w + ws.seg);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int P = a.p.max_pages;
-    if (P <= 1024 && a.p.Hkv <= kOneHeads)
+    if (one_launch(a.p))
         return status_from_cuda(P <= 256 ? launch_evict<256, 1, true>(a, s)
                                 : P <= 512 ? launch_evict<512, 1, true>(a, s) : launch_evict<1024, 1, true>(a, s));
     prof_begin("evict_sums", s);
