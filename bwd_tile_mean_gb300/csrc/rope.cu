@@ -20,14 +20,13 @@ namespace {
 
 struct RopeArgs {
     vsa_rope r;
-    int n;                        // tensors
     int heads0, heads;            // heads of the first tensor, of both
     const void *x[2];
     void *y[2];
     long long xb[2], xt[2], xh[2], yb[2], yt[2], yh[2];
     const int *pos;
     long long pb, pt;
-    int B, S, inverse;
+    int S, inverse;
     int chunk, chunks;            // heads per unit, units per token
     long long units;
 };
@@ -55,7 +54,10 @@ constexpr int kRopeDeep = 4;  // rows per half warp in flight
 // 6, 8 rows per half warp in flight took 519, 476, 525, 497 us for the former;
 // half a warp per token, for tokens side by side, 306 for the latter (299 then).
 // kPerSm: CTAs per SM. Tokens whose heads lie side by side go best with three
-// (476 us, with four 499), heads whose tokens do with four (286, with three 298).
+// (476 us, with four 499), heads whose tokens do with four where pairs are
+// interleaved (75,600 tokens of 24 + 24 heads 286, with three 298; 20,000 86, 86;
+// 5,000 30, 30). The half style, whose angles take twice the registers, spills
+// with four: 325, with three 320; 97, 91; 35, 32.
 template <typename T, bool kInter, int kPerSm>
 __global__ void __launch_bounds__(kRopeWarps * 32, kPerSm) k_rope(const __grid_constant__ RopeArgs a) {
     const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, half = lane >> 4, i = lane & 15;
@@ -257,13 +259,11 @@ extern "C" vsa_status vsa_rope_apply(const vsa_rope *rope, int dtype, int B, int
     if (none) return VSA_OK;
     if (!positions) return VSA_ERR_NULL;
     a.r = *rope;
-    a.n = n;
     a.heads0 = t[0].heads;
     a.heads = (int)heads;
     a.pos = positions;
     a.pb = pos_batch;
     a.pt = pos_token;
-    a.B = B;
     a.S = S;
     a.inverse = inverse != 0;
     const long long tokens = (long long)B * S, places = 152 * 64;
@@ -275,16 +275,15 @@ extern "C" vsa_status vsa_rope_apply(const vsa_rope *rope, int dtype, int B, int
     a.chunks = (int)((heads + a.chunk - 1) / a.chunk);
     a.units = tokens * a.chunks;
     // twice the CTAs that fit: with three of them 3, 4, 5, 6, 8, 32 per SM took 475, 548, 498, 476, 486, 487 us
-    const bool head_major = S > 1 && t[0].x_token < t[0].x_head;
-    const unsigned grid = (unsigned)std::min((a.units + kRopeWarps - 1) / kRopeWarps, head_major ? 152LL * 8 : 152LL * 6);
+    const bool four = a.r.interleaved && S > 1 && t[0].x_token < t[0].x_head;
+    const unsigned grid = (unsigned)std::min((a.units + kRopeWarps - 1) / kRopeWarps, four ? 152LL * 8 : 152LL * 6);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     prof_begin("rope", s);
     const bool bf = dtype == VSA_DTYPE_BF16;
     const auto kernel =
-        head_major ? (a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true, 4> : k_rope<__half, true, 4>)
-                                      : (bf ? k_rope<__nv_bfloat16, false, 4> : k_rope<__half, false, 4>))
-                   : (a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true, 3> : k_rope<__half, true, 3>)
-                                      : (bf ? k_rope<__nv_bfloat16, false, 3> : k_rope<__half, false, 3>));
+        four ? (bf ? k_rope<__nv_bfloat16, true, 4> : k_rope<__half, true, 4>)
+             : (a.r.interleaved ? (bf ? k_rope<__nv_bfloat16, true, 3> : k_rope<__half, true, 3>)
+                                : (bf ? k_rope<__nv_bfloat16, false, 3> : k_rope<__half, false, 3>));
     const cudaError_t e = launch_paged(kernel, dim3(grid), kRopeWarps * 32, 0, 1, a, s);
     prof_end(s);
     return status_from_cuda(e);
