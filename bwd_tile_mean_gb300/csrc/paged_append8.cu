@@ -19,7 +19,8 @@
 // Bound by instructions for long prompts: 30,000 tokens of 24 heads (0.92 GB) take
 // 204 us, 66% of the measured copy rate, with 54% of the issue slots and 58% of
 // DRAM's peak busy (half style, whose pairs lie in two lanes, a fifth more); the
-// blocks are rotated, searched and rounded in fp32. Measured on the way there (us): rotated keys kept in registers, 8 warps per SM 360; with
+// blocks are rotated, searched and rounded in fp32. Measured on the way there, each
+// with what was built then (us): rotated keys kept in registers, 8 warps per SM 360; with
 // 128 registers and spills 377; walked twice from shared memory 266, two heads per
 // warp 248 (one 272, four 266), with angles by position 207, loops unrolled four deep
 // 203 (two 207, one 221); a head instead of a group per warp, which share their
@@ -387,7 +388,7 @@ __global__ void __launch_bounds__(256, 2) k_paged8_append(AppendArgs a) {
 }
 
 // Groups of tokens, counted once for every four key and every eight query heads, from which a warp has two key heads, whose
-// angles it reads once from memory: 30,000 tokens of 24 heads 208 us, with one 233, with four 219; 6,000 70, 66, 77.
+// angles it reads once from memory: 30,000 tokens of 24 heads 208 us (204 since), with one 233, with four 219; 6,000 70, 66, 77.
 constexpr long long kTwoHeads = 8192;
 
 template <typename T, int HC, int PB, bool kFew> cudaError_t launch_append8(AppendArgs &a, cudaStream_t s) {

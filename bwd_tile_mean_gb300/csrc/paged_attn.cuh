@@ -65,8 +65,11 @@ constexpr int kLead = 4;        // blocks a segment counts for beyond its own (i
 // same lengths.
 constexpr int kLead8 = 8;
 constexpr int kAlignedKeys = 1280;  // keys per CTA up to which segments of unknown lengths get a cluster each
-constexpr int kAlignedKeys8 = 800;  // of an 8-bit cache: 8 heads of 16,000 keys in clusters of 16 14.0 us, 12.5 in runs; 3 of
-                                    // 8,000 7.6, 8.7
+// Of an 8-bit cache. Equal lengths, 4 heads per key head (us, clusters / runs), up to 800 keys per CTA: 1 head of 12,000
+// keys 9.0 / 10.3, 8 of 8,000 8.9 / 10.3, 24 of 1,000 5.8 / 10.1, 64 of 2,400 11.6 / 13.6; more: 24 of 12,000 19.3 / 17.5,
+// 8 of 16,000 13.7 / 12.8, 32 of 12,000 20.9 / 20.5, 64 of 8,000 28.1 / 31.1, 256 of 800 12.4 / 16.2 (unequal lengths would lose
+// that: a cluster's longest decides). 16 heads per key head: 32 of 4,000 15.9 / 16.6, of 6,400 22.4 / 18.9, of 8,000 24.0 / 20.4.
+constexpr int kAlignedKeys8 = 800;
 constexpr int kFewCtas = 912;       // and CTAs in all, three at each place: 1,192 segments of 17 keys 11.6 us, 7.6 in runs;
                                     // 800 of 64 11.9, 14.2
 constexpr int kAlignedCtas = 96;    // CTAs that nearly fill the memory pipe

@@ -2,7 +2,7 @@
 // a call, allocates its outputs and passes their pointers on to the C entry
 // points, for the decode step whose kernels take a few microseconds. The same
 // in Python (checks, two torch.empty, a ctypes call) took 12.7 us for
-// vsa_paged_attn on a GB300's CPU; here 4.7 us, most of it the launch.
+// vsa_paged_attn on a GB300's CPU; here 4.0 to 4.5 us, most of it the launch.
 //
 // Module paged_binding, type Calls(desc, device, eight, k, v, k_scale, v_scale, k_mean, workspace,
 // workspace_bytes, weigh_bytes, functions, fail), the cache's tensors apart: desc is the address of a vsa_paged_desc

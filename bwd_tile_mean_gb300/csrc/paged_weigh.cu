@@ -102,8 +102,13 @@ __global__ void __launch_bounds__(kWeighThreads) k_page_weigh(WeighArgs a) {
     }
 }
 
-// Listed pages: one CTA per list. A list that is not ascending may name a page
-// twice: its entries are then added one after another.
+// Listed pages: one CTA per list, a few entries per turn. A list that is not ascending may name a page
+// twice: its entries are then added one after another. On top of the attention's
+// time (us, ascending / any order): 64 sequences x 8 heads, 64 of 250 pages of 64
+// tokens, 10 / 26 on 104; 8 x 8 heads with 16 queries each, 500 of 1,000 of 16 tokens,
+// 37 / 116 on 37; one sequence, 4,000 of 8,000 of 16 tokens, 1 head 55 / 585 on 12, 8 heads
+// 72 / 668 on 32. Chains of loads bound it, in any order one thread's additions; a list
+// in parts is not built.
 __global__ void __launch_bounds__(kWeighThreads) k_page_weigh_listed(WeighArgs a) {
     __shared__ float s_mass[kWeighThreads];
     const Paged &p = a.p;
@@ -158,12 +163,14 @@ struct EvictArgs {
     int *len;        // [B] the lengths: lens_out may be the lengths themselves
 };
 constexpr int kSumThreads = 256;
-// Whether one CTA takes a whole sequence (of up to 1,024 pages) in one launch, which costs it half a microsecond or more per
-// head, instead of a launch for the sums and then a CTA per row, which does where there are many more rows than SMs. Measured
-// (us, one launch / two): 1 sequence of 250 pages x 4, 8, 16, 32 heads 5.8 / 6.1, 6.9 / 6.3, 10.5 / 7.9, 18.7 / 10.3; of 1,000
-// pages x 1, 8, 32 heads 9.9 / 5.7, 11.4 / 6.7, 35.4 / 10.6; 16 of 250 x 8, 32 7.1 / 7.9, 19.6 / 20.0; 24 of 250 x 8, 16, 32 7.0 /
-// 9.9, 12.0 / 14.6, 19.7 / 26.5, of 1,000 12.4 / 11.6, 19.8 / 17.5, 36.1 / 32.7; 64 of 250 x 1, 8, 32 5.6 / 6.6, 7.7 / 17.9, 19.6 /
-// 66.2, of 1,000 x 1, 4, 32 10.5 / 7.5, 11.3 / 14.6, 36.2 / 79.3.
+// Whether one CTA takes a whole sequence (of up to 1,024 pages) in one launch,
+// which costs it half a microsecond or more per head, instead of a launch for the
+// sums and then a CTA per row, which does where there are many more rows than SMs.
+// Measured (us, one launch / two), 250 pages: 1 sequence x 4, 8, 16, 32 heads 5.8 / 6.1,
+// 6.9 / 6.3, 10.5 / 7.9, 18.7 / 10.3; 16 x 8, 32 7.1 / 7.9, 19.6 / 20.0; 24 x 8, 16, 32 7.0 / 9.9,
+// 12.0 / 14.6, 19.7 / 26.5; 64 x 1, 8, 32 5.6 / 6.6, 7.7 / 17.9, 19.6 / 66.2. 1,000 pages: 1 x
+// 1, 8, 32 9.9 / 5.7, 11.4 / 6.7, 35.4 / 10.6; 24 x 8, 16, 32 12.4 / 11.6, 19.8 / 17.5, 36.1 / 32.7;
+// 64 x 1, 4, 32 10.5 / 7.5, 11.3 / 14.6, 36.2 / 79.3.
 inline bool one_launch(const Paged &p) {
     if (p.max_pages > 1024) return false;
     return (p.Hkv <= 4 && p.max_pages <= 512) || (p.B > 20 && (long long)p.B * (p.Hkv + 1) > 152);
@@ -176,8 +183,8 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// A page's weight over the heads, as a key. The heads are added in fp64: the sum, rounded once to fp32, does not depend on
-// an order.
+// A page's weight over the heads, as a key: added in fp64 in ascending order (k_evict_move adds in the same one where it does
+// so itself), rounded once to fp32.
 __device__ __forceinline__ uint32_t page_key(const EvictArgs &a, int b, int j) {
     const Paged &p = a.p;
     const float *w = a.weight + (long long)b * p.Hkv * p.max_pages + j;
@@ -211,8 +218,8 @@ __global__ void __launch_bounds__(kSumThreads) k_evict_sums(EvictArgs a) {
 // before each counted instead of the digits); one of 7,680 pages x 24 heads 13.2, 4 of them the sums. With 8-bit digits and
 // 512 entries placed at a time the latter took 18.9, 25 where a warp's lanes matched their bins first, and 15.9 with a
 // thread's entries side by side, whose stores are not.
-// Rows of a sequence loaded at once: 8, 10, 16 took 6.0, 6.9, 7.3 us for 64 sequences of 250 pages x 4 heads, 7.9, 7.0, 8.2 for 8
-// (nine rows, all at once with ten), 12.0, 12.1, 11.2 for 16, 19.5, 19.8, 19.2 for 32.
+// Rows of a sequence loaded at once: 8, 10, 16 took 6.0, 6.9, 7.3 us for 64 sequences of 250 pages x 4 heads, 7.9, 7.0, 8.2
+// for 8 heads (nine rows: all at once with ten), 12.0, 12.1, 11.2 for 16, 19.5, 19.8, 19.2 for 32.
 constexpr int kBins = 2048, kRowsAhead = 10;
 template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_move(EvictArgs a) {
     constexpr int W = N / 32, kChunk = N * E, R = kOne ? kRowsAhead : 1;
@@ -245,7 +252,7 @@ template <int N, int E, bool kOne> __global__ void __launch_bounds__(N) k_evict_
     auto key_at = [&](int j) { return a.keys[(long long)b * P + j]; };
     uint32_t key[E];
     if constexpr (kOne) {
-        double sum = 0.0;
+        double sum = 0.0;  // page_key's order
 #pragma unroll
         for (int r = 1; r < R; ++r) sum += row0 + r < row1 ? (double)__int_as_float(x[r][0]) : 0.0;
 #pragma unroll 8

@@ -134,6 +134,8 @@ __global__ void __launch_bounds__(kRopeWarps * 32, kPerSm) k_rope(const __grid_c
     grid_go();
 }
 
+// Bound by its instructions, a 64-bit division among them: 100, 6,000, 76,800
+// tokens of 64 pairs 1.9, 4.2, 20.4 us, where the bytes of the last take 5.8.
 struct TableArgs {
     vsa_rope r;
     const int *pos;

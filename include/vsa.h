@@ -660,8 +660,8 @@ vsa_status vsa_paged_attn_weigh(const vsa_paged_desc *desc, const void *q, int64
 /* Cuts every sequence of more than `keep` pages down to `keep`: its first
  * keep_first (>= 0) and last keep_last (>= 1) pages stay (keep >= keep_first +
  * keep_last), and of the others those with the largest weight, the lower page among equals. A
- * page's weight is the sum of page_weight[b, :, j] over the heads, added in fp64
- * and rounded once to fp32; NaN counts as -inf. The entries of the pages that go are
+ * page's weight is the sum of page_weight[b, :, j] over the heads, added in fp64 in
+ * ascending order and rounded once to fp32; NaN counts as -inf. The entries of the pages that go are
  * taken out of the sequence's rows of the table and of page_weight; those behind
  * them (also the ones past the sequence's end) move up in order, and the places that come
  * free at the end of a row get -1 and 0. freed [B, max(1, max_pages - keep)]
