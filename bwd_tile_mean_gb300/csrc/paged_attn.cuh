@@ -567,8 +567,8 @@ __device__ __forceinline__ float min_nan(float x, float y) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
     return r;
 }
-// e of a positive x in [2^e, 2^(e + 1)), -126 at least.
-__device__ __forceinline__ int exponent_of(float x) { return max((int)(__float_as_uint(x) >> 23), 1) - 127; }
+// e of an x with |x| in [2^e, 2^(e + 1)), -126 at least.
+__device__ __forceinline__ int exponent_of(float x) { return max((int)(__float_as_uint(x) >> 23 & 255), 1) - 127; }
 
 // stream_blocks for 8 bits: m_run, l_run, w_run of heads 8 n + 2 t + e at 2 n + e, their outputs' dims 16 j + 2 g and + 1 in
 // acc[8 n + j][e] and [2 + e], finished: divided by w, and scaled.
@@ -810,7 +810,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    if (top > 0.f && vsc[h] > 0.f) to = max(to, exponent_of(top) + lv[h] - 12);
+                    if (top > 0.f && vsc[h] != 0.f) to = max(to, exponent_of(top) + lv[h] - 12);
                 }
                 to = to == kNone ? was : clampi(to, -300, 300);
                 at_exp[r][lane] = to;

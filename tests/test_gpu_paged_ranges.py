@@ -125,6 +125,21 @@ def test_weights_tiny_and_scales_huge():
     assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(4, 2), (32, 2)])
+@pytest.mark.parametrize("apart", [2, 12])
+def test_negative_scales_are_used_as_they_are(Hq, Hkv, apart):
+    """Not what an append makes, but what a caller may give: the sign in the
+    scale is the sign in the values, bit for bit."""
+    pool = Pool8("bshd", BF, Hq, Hkv, 32, 60, 30, [900, 700], seed=7, spread=apart)
+    q = queries(pool, size=3.0)
+    want = pool.cache().attend(q.cuda())
+    sign = torch.randint(0, 2, pool.vs.shape) * 2.0 - 1
+    pool.vs = pool.vs * sign
+    pool.v = pool.real(pool.v, sign)
+    got = pool.cache().attend(q.cuda())
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 # ------------------------------------------------------------- large scores
 
 def plain_row(eight, n, seed=3, heads=2):
