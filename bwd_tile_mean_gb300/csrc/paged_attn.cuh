@@ -448,7 +448,7 @@ __device__ __forceinline__ void stream_blocks(const AttnArgs &a, const Segment &
 // on each row has a power of two of its own, by its largest product of weight
 // and scale: two more maxima per row and step, and the weights multiplied in
 // fp32, in a loop apart, so that the common one has no branch for it (scales 2^20 apart:
-// the batch below 74.3 us, the long context 118.9, 16 heads on each of 2, 16 sequences 18.1).
+// the batch below 75.0 us, the long context 119.7, 16 heads on each of 2, 16 sequences 19.3).
 //
 // At half the bytes per key the instructions count: keys and dims are the rows
 // of the products here, the query heads their columns, NT tiles of 8. Up to 8
@@ -625,9 +625,11 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         }
     };
     // The outputs are relative to vrun, the largest power of two met and 2^126 at most (vnext: with the window's scales); once
-    // far, each row's to 2^at_exp, of which every lane keeps a copy for its rows.
-    __shared__ int s_exp[kWarps][2 * NT][32];
-    int(&at_exp)[2 * NT][32] = s_exp[threadIdx.x >> 5];
+    // far, each row's to 2^exp_of(peak): its largest product of (lifted) weight and scale so far as a logarithm, not rounded,
+    // since it falls with the weights by less than a binade per step. Every lane keeps a copy for its rows.
+    __shared__ float s_peak[kWarps][2 * NT][32];
+    float(&peak)[2 * NT][32] = s_peak[threadIdx.x >> 5];
+    auto exp_of = [](float x) { return clampi((int)floorf(x) - 12, -300, 300); };
     float vrun = 0x1p-126f, vnext = vrun, vlow = INFINITY;
     bool far = false;
     float ksc[2], vsc[2];
@@ -781,7 +783,7 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
         if constexpr (kWeigh) store_weights8<NT>(a, sg, blk0 + 2 * i, blk0 + nblk, sc, m_run);
         if constexpr (kFar) {
             // The sum of the weights as below; then the weights for the outputs: a row's largest product of weight and scale
-            // so far comes to [2^12, 2^14) (a scale of 2^127: a binade more), and the outputs with it
+            // so far comes to [2^12, 2^14) (a scale of 2^127: a binade more), and the outputs with it.
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 wsum[n][0] *= corr[2 * n], wsum[n][1] *= corr[2 * n + 1];
@@ -801,20 +803,21 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
             }
 #pragma unroll
             for (int r = 0; r < 2 * NT; ++r) {
-                constexpr int kNone = -1000;
-                const int n = r >> 1, e = r & 1, was = at_exp[r][lane];
-                int to = corr[r] > 0.f ? was + exponent_of(corr[r]) : kNone;
+                const int n = r >> 1, e = r & 1;
+                const float before = peak[r][lane];
+                float now = corr[r] > 0.f ? before + __log2f(corr[r]) : -INFINITY;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float top = fmaxf(sc[h][n][e], sc[h][n][2 + e]);
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-                    if (top > 0.f && vsc[h] != 0.f) to = max(to, exponent_of(top) + lv[h] - 12);
+                    if (top > 0.f && vsc[h] != 0.f) now = fmaxf(now, (float)(exponent_of(top) + lv[h]));
                 }
-                to = to == kNone ? was : clampi(to, -300, 300);
-                at_exp[r][lane] = to;
-                const float by = corr[r] * power_of(clampi(was - to, -126, 127));
+                if (now == -INFINITY) now = before;
+                peak[r][lane] = now;
+                const int to = exp_of(now);
+                const float by = corr[r] * power_of(clampi(exp_of(before) - to, -126, 127));
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
                     acc[8 * n + j][e] *= by;
@@ -883,12 +886,12 @@ __device__ __forceinline__ void stream_blocks8(const AttnArgs &a, const Segment 
     for (; i < steps && !far; ++i) step(std::false_type{}, i);
     if (far) {
 #pragma unroll
-        for (int r = 0; r < 2 * NT; ++r) at_exp[r][lane] = exponent_of(vrun);
+        for (int r = 0; r < 2 * NT; ++r) peak[r][lane] = (float)(exponent_of(vrun) + 12);
         for (; i < steps; ++i) step(std::true_type{}, i);
 #pragma unroll
         for (int r = 0; r < 2 * NT; ++r) {  // finished here: over w, times 2^e in three factors, -300 <= e <= 300
             const float w = wsum[r >> 1][r & 1], inv = w == 0.f ? 0.f : 1.f / w;
-            const int e = at_exp[r][lane], e1 = e / 3, e2 = (e - e1) / 2;
+            const int e = exp_of(peak[r][lane]), e1 = e / 3, e2 = (e - e1) / 2;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
 #pragma unroll

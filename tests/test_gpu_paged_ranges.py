@@ -125,6 +125,32 @@ def test_weights_tiny_and_scales_huge():
     assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
 
 
+@pytest.mark.parametrize("Hq,small", [(1, -60), (1, -20), (12, -60)])
+def test_scores_that_creep_up_behind_a_large_scale(Hq, small):
+    """16,384 keys of scores that rise by 1/64 from block to block; every 330
+    blocks one with a v scale of 2^100, the others with a small one: what the
+    large ones add stays what outputs are relative to, for hundreds of steps
+    whose maximum moves a little."""
+    n, B = 16384, 400
+    pool = Pool8("bshd", BF, Hq, 1, 64, n // 64, n // 64, [n], seed=2)
+    g = torch.Generator().manual_seed(9)
+    pool.k[:], pool.ks[:] = 0.0, 1.0
+    pool.v[:] = (torch.randint(1, 16, pool.v.shape, generator=g) * 1.0)
+    pool.vs[:] = 2.0 ** small
+    for blk in range(n // 16):
+        p, at = pool.table[0][blk // 4], slice(16 * (blk % 4), 16 * (blk % 4) + 16)
+        pool.k[p, at, 0, 0], pool.k[p, at, 0, 1], pool.k[p, at, 0, 2] = blk // 64, blk // 4 % 16, blk % 4
+        if blk % 330 == 5:
+            pool.vs[p, 0, blk % 4] = 2.0 ** 100
+    q = torch.zeros(1, Hq, D, dtype=BF)
+    q[..., 0], q[..., 1], q[..., 2] = 1.0, 2.0 ** -4, 2.0 ** -6
+    out, tol = by_products(pool, q, scale=1.0)
+    share_pages(pool, B)
+    got = pool.cache(scale=1.0).attend(q.expand(B, -1, -1).contiguous().cuda())[0].double().cpu()
+    assert torch.isfinite(got).all()
+    assert ((got - out).abs() <= tol).all(), float(((got - out).abs() / tol).max())
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(4, 2), (32, 2)])
 @pytest.mark.parametrize("apart", [2, 12])
 def test_negative_scales_are_used_as_they_are(Hq, Hkv, apart):
